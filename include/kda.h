@@ -474,6 +474,152 @@ KDA_API int kda_prefill_noalloc(const void* q, const void* k, const void* v, con
  */
 KDA_API int kda_prefill_noalloc_status(void* stream);
 
+/*
+ * Decayed linear attention: one scalar decay per head and no delta rule, the
+ * layer that hybrid stacks put beside KDA.  With a_h = e^{log_decay[h]}, per
+ * sequence and head,
+ *
+ *     S_t = a_h S_{t-1} + k_t v_t^T          o_t = scale * S_t^T q_t
+ *
+ * The conventions above hold: packed token-major tensors, fp32 states
+ * [n][H][d_k][d_v] (the same pools, slots and kda_state_io serve them), d_k and
+ * d_v in {32, 64, 128}, fp32 or bf16.  log_decay [H] is fp32 and a constant
+ * of the layer (no gradient); it is normally negative, 0 keeps everything and
+ * -infinity drops the state at every token.  q and k are taken as they are.
+ *
+ * kda_lin_prefill -- the recurrence over N packed sequences, in chunks.
+ *
+ *  q, k           [total_T, H, d_k] dt;  v [total_T, H, d_v] dt
+ *  log_decay      [H] fp32
+ *  initial_state, cu_seqlens, cu_seqlens_host, N, total_T, scale: as
+ *                 kda_prefill
+ *  flags          0 or KDA_FLAG_RECURRENT (the CUDA-core form even where the
+ *                 tensor-core one applies)
+ *  o              [total_T, H, d_v] dt
+ *  final_state    [N, H, d_k, d_v] fp32 or NULL; may be initial_state itself
+ *  workspace      kda_lin_prefill_workspace_bytes(...) bytes, 256-byte
+ *                 aligned, no initialisation needed
+ * A sequence of length zero hands its initial state (or zeros) on.
+ * Errors (nothing is launched): as kda_prefill, and KDA_ERR_INVALID_ARG for an
+ * output or the workspace on top of another buffer.
+ */
+KDA_API int kda_lin_prefill(const void* q, const void* k, const void* v,
+                            const float* log_decay, const float* initial_state,
+                            const int32_t* cu_seqlens, const int32_t* cu_seqlens_host,
+                            int32_t N, int32_t total_T, int32_t H, int32_t d_k, int32_t d_v,
+                            kda_dtype dt, float scale, uint32_t flags, void* o,
+                            float* final_state, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* kda_lin_prefill_workspace_bytes -- the workspace kda_lin_prefill needs on the
+ * current device: a status word and, where few (sequence, head) pairs leave
+ * SMs idle and the sequences are cut into segments, a state per segment and
+ * head and a copy of the initial states (0 for invalid sizes). */
+KDA_API size_t kda_lin_prefill_workspace_bytes(int32_t N, int32_t total_T, int32_t H,
+                                               int32_t d_k, int32_t d_v, kda_dtype dt);
+
+/*
+ * kda_lin_decode_step -- one token for each of B sequences; the state pool is
+ * updated in place, as kda_decode_step does it (slots, bad slots, NULL slots).
+ *
+ *  q, k [B, H, d_k] dt;  v [B, H, d_v] dt;  log_decay [H] fp32
+ *  state [pool_size, H, d_k, d_v] fp32;  slots [B] int32 or NULL, distinct
+ *  o [B, H, d_v] dt, overlapping none of the others
+ */
+KDA_API int kda_lin_decode_step(const void* q, const void* k, const void* v,
+                                const float* log_decay, float* state, const int32_t* slots,
+                                int32_t pool_size, int32_t B, int32_t H, int32_t d_k,
+                                int32_t d_v, kda_dtype dt, float scale, void* o, void* stream);
+
+/*
+ * kda_lin_backward -- gradients of kda_lin_prefill: with G_T = dS_final +
+ * scale q_T dO_T^T and G_t = scale q_t dO_t^T + a_h G_{t+1},
+ *
+ *     dq_t = scale S_t dO_t    dk_t = G_t v_t    dv_t = G_t^T k_t    dS0 = a_h G_1
+ *
+ * Each is a decayed linear attention itself (dk and dv in reverse time).
+ *
+ *  the forward's inputs as kda_lin_prefill takes them
+ *  dO             [total_T, H, d_v] dt;  dS_final [N, H, d_k, d_v] fp32 or
+ *                 NULL (zero)
+ *  dq, dk         [total_T, H, d_k] dt;  dv [total_T, H, d_v] dt;  dS0
+ *                 [N, H, d_k, d_v] fp32 or NULL; written, not accumulated; no
+ *                 output may overlap another buffer
+ *  workspace      kda_lin_backward_workspace_bytes(...) bytes, 256-byte aligned
+ * The result is the same bits on every call (no atomics in any sum).
+ */
+KDA_API int kda_lin_backward(const void* q, const void* k, const void* v,
+                             const float* log_decay, const float* initial_state,
+                             const int32_t* cu_seqlens, const int32_t* cu_seqlens_host,
+                             int32_t N, int32_t total_T, int32_t H, int32_t d_k, int32_t d_v,
+                             kda_dtype dt, float scale, uint32_t flags, const void* dO,
+                             const float* dS_final, void* dq, void* dk, void* dv, float* dS0,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+KDA_API size_t kda_lin_backward_workspace_bytes(int32_t N, int32_t total_T, int32_t H,
+                                                int32_t d_k, int32_t d_v, kda_dtype dt);
+
+enum { KDA_GATE_SIGMOID = 0, KDA_GATE_SILU = 1 };
+
+/*
+ * kda_block_norm -- what stands between the output of a block and the input
+ * of the next, in one pass over the rows:
+ *
+ *     n     = y / sqrt(mean(y^2) + eps) * w_post     over each group of channels
+ *     u     = n * act(gate)                          act: sigmoid, or t * sigmoid(t)
+ *     x_out = x + res_scale * u
+ *     h     = x_out / sqrt(mean(x_out^2) + eps) * w_pre
+ *
+ * With group = d_v, a gate and nothing else it is the output norm of an
+ * attention layer over heads (D = H d_v); with group = D, x and w_pre it joins
+ * a block's post norm, the residual and the next block's pre norm.
+ *
+ *  y        [rows, D] dt
+ *  w_post   [group] fp32
+ *  gate     [rows, D] dt, or NULL (u = n)
+ *  x        [rows, D] dt, or NULL (x_out = res_scale * u)
+ *  res_scale [D] fp32, or NULL (1)
+ *  w_pre    [D] fp32, or NULL (no h)
+ *  D        a multiple of 8, at most 16384;  group: D, or one of 32, 64, 128
+ *           that divides D (KDA_ERR_UNSUPPORTED otherwise)
+ *  gate_act KDA_GATE_SIGMOID or KDA_GATE_SILU;  eps > 0
+ *  x_out    [rows, D] dt;  h [rows, D] dt with w_pre, else NULL.  Each may be
+ *           y, gate or x itself (in place), and overlap nothing otherwise.
+ * All pointers 16-byte aligned.  h is formed from x_out before its rounding to
+ * dt; statistics, products and sums are fp32.
+ */
+KDA_API int kda_block_norm(const void* y, const float* w_post, const void* gate, const void* x,
+                           const float* res_scale, const float* w_pre, int64_t rows, int32_t D,
+                           int32_t group, kda_dtype dt, int32_t gate_act, float eps,
+                           void* x_out, void* h, void* stream);
+
+/*
+ * kda_block_norm_backward -- gradients of kda_block_norm, given dx_out and dh
+ * (those of x_out and h).  x_out is read as the forward stored it.
+ *
+ *  y, w_post, gate, res_scale, w_pre, rows, D, group, dt, gate_act, eps: the
+ *           forward's;  x_out [rows, D] dt, needed with w_pre
+ *  dx_out   [rows, D] dt, or NULL (zero; then w_pre and dh are given);
+ *  dh       [rows, D] dt with w_pre, else NULL
+ *  dy       [rows, D] dt;  dgate [rows, D] dt with a gate, else NULL;
+ *  dx       [rows, D] dt, or NULL (not wanted)
+ *  dw_post  [group] fp32;  dres_scale [D] fp32 with res_scale, else NULL;
+ *  dw_pre   [D] fp32 with w_pre, else NULL
+ *  workspace  kda_block_norm_backward_workspace_bytes(rows, D, group) bytes,
+ *           16-byte aligned, no initialisation needed
+ * Outputs are written, not accumulated, and overlap no other buffer.  Sums over
+ * rows are added in a fixed order: the same bits on every call.
+ */
+KDA_API int kda_block_norm_backward(const void* y, const float* w_post, const void* gate,
+                                    const void* x_out, const float* res_scale,
+                                    const float* w_pre, const void* dx_out, const void* dh,
+                                    int64_t rows, int32_t D, int32_t group, kda_dtype dt,
+                                    int32_t gate_act, float eps, void* dy, void* dgate,
+                                    void* dx, float* dw_post, float* dres_scale, float* dw_pre,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+KDA_API size_t kda_block_norm_backward_workspace_bytes(int64_t rows, int32_t D, int32_t group);
+
 /* Human-readable name of a kda_status value (static storage). */
 KDA_API const char* kda_status_string(int status);
 

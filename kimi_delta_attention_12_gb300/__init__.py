@@ -9,6 +9,9 @@ Entry points (same names as the C ABI):
   kda_prefill(q, k, v, z, beta, A, ...)      chunked prefill over packed sequences
   kda_decode_step(q, k, v, z, beta, A, state, ...)  one token per sequence, state in place
   kda_state_io(op, dst, src, ...)            zero / copy / gather / scatter of states
+  kda_lin_prefill, kda_lin_decode_step, kda_lin_backward
+                                             linear attention with one decay per head
+  kda_block_norm, kda_block_norm_backward    norms, gate and residual between two blocks
 """
 from __future__ import annotations
 
@@ -52,7 +55,14 @@ EXPORTED_SYMBOLS = (
     "kda_short_conv", "kda_decode_step_conv", "kda_decode_conv_workspace_bytes",
     "kda_backward", "kda_backward_workspace_bytes", "kda_prefill_noalloc_status",
     "kda_prefill_conv", "kda_prefill_conv_workspace_bytes",
+    "kda_lin_prefill", "kda_lin_prefill_workspace_bytes", "kda_lin_decode_step",
+    "kda_lin_backward", "kda_lin_backward_workspace_bytes",
+    "kda_block_norm", "kda_block_norm_backward", "kda_block_norm_backward_workspace_bytes",
 )
+
+KDA_GATE_SIGMOID = 0
+KDA_GATE_SILU = 1
+_GATE_ACTS = {"sigmoid": KDA_GATE_SIGMOID, "silu": KDA_GATE_SILU}
 
 _lock = threading.Lock()
 _lib = None
@@ -128,6 +138,28 @@ def lib() -> ctypes.CDLL:
                                                            ctypes.c_int]
             L.kda_checkpoint_count.restype = ctypes.c_int64
             L.kda_checkpoint_count.argtypes = [vp, i32, i32, i32]
+            i64, dt = ctypes.c_int64, ctypes.c_int
+            L.kda_lin_prefill.restype = ctypes.c_int
+            L.kda_lin_prefill.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, dt,
+                                          f32, u32, vp, vp, vp, sz, vp]
+            L.kda_lin_decode_step.restype = ctypes.c_int
+            L.kda_lin_decode_step.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, dt,
+                                              f32, vp, vp]
+            L.kda_lin_backward.restype = ctypes.c_int
+            L.kda_lin_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, dt,
+                                           f32, u32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+            for f in (L.kda_lin_prefill_workspace_bytes, L.kda_lin_backward_workspace_bytes):
+                f.restype = sz
+                f.argtypes = [i32, i32, i32, i32, i32, dt]
+            L.kda_block_norm.restype = ctypes.c_int
+            L.kda_block_norm.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i32, dt, i32, f32,
+                                         vp, vp, vp]
+            L.kda_block_norm_backward.restype = ctypes.c_int
+            L.kda_block_norm_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i32, i32,
+                                                  dt, i32, f32, vp, vp, vp, vp, vp, vp, vp, sz,
+                                                  vp]
+            L.kda_block_norm_backward_workspace_bytes.restype = sz
+            L.kda_block_norm_backward_workspace_bytes.argtypes = [i64, i32, i32]
             _lib = L
     return _lib
 
@@ -612,3 +644,305 @@ def kda_state_io(op: int, dst: torch.Tensor, src: Optional[torch.Tensor] = None,
                             H, d_k, d_v, _stream_ptr(stream))
     if st != KDA_OK:
         raise KDAError(st, "kda_state_io")
+
+
+# ---------------------------------------------------- decayed linear attention
+class _Launch:
+    """Where a call allocates and launches: the tensors' device, and the given
+    stream or that device's current one.  Memory allocated for the call
+    belongs to that stream, so that its reuse waits for the call's kernels."""
+
+    def __init__(self, stream: Optional[torch.cuda.Stream], first: torch.Tensor, *others):
+        if not first.is_cuda:
+            raise ValueError("KDA tensors must live on a CUDA device")
+        for t in others:
+            if t is not None and t.device != first.device:
+                raise ValueError("KDA tensors must live on one CUDA device")
+        self._device = None
+        if first.device.index != torch.cuda.current_device():
+            self._device = torch.cuda.device(first.device)
+        self._stream = stream
+
+    def __enter__(self):
+        if self._device is not None:
+            self._device.__enter__()
+        if self._stream is not None:
+            self._context = torch.cuda.stream(self._stream)
+            self._context.__enter__()
+            return self._stream.cuda_stream
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self._stream is not None:
+            self._context.__exit__(*exc)
+        if self._device is not None:
+            self._device.__exit__(*exc)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def lin_prefill_workspace_bytes(N: int, total_T: int, H: int, d_k: int, d_v: int,
+                                dtype: torch.dtype) -> int:
+    return int(lib().kda_lin_prefill_workspace_bytes(N, total_T, H, d_k, d_v, _dtype_code(dtype)))
+
+
+def lin_backward_workspace_bytes(N: int, total_T: int, H: int, d_k: int, d_v: int,
+                                 dtype: torch.dtype) -> int:
+    return int(lib().kda_lin_backward_workspace_bytes(N, total_T, H, d_k, d_v,
+                                                      _dtype_code(dtype)))
+
+
+def _lin_sizes(q, k, v, log_decay, cu_seqlens):
+    """(N, total_T, H, d_k, d_v) of packed inputs, their shapes checked."""
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must have shape [total_T, H, d]")
+    total_T, H, d_k = q.shape
+    d_v = v.shape[2]
+    if k.shape != q.shape:
+        raise ValueError(f"k must have shape {tuple(q.shape)}, got {tuple(k.shape)}")
+    if v.shape[0] != total_T or v.shape[1] != H:
+        raise ValueError(f"v must have shape {(total_T, H, d_v)}, got {tuple(v.shape)}")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k and v must share one dtype")
+    _expect(log_decay, (H,), "log_decay", torch.float32)
+    N = 1
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.dtype != torch.int32 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be a 1-D int32 tensor of N + 1 starts")
+        N = cu_seqlens.numel() - 1
+    return N, total_T, H, d_k, d_v
+
+
+def _host_seqlens(cu_seqlens_host, N: int):
+    """The host mirror as contiguous int32 (kept alive by the caller)."""
+    if cu_seqlens_host is None:
+        return None
+    if cu_seqlens_host.is_cuda or cu_seqlens_host.numel() != N + 1:
+        raise ValueError(f"cu_seqlens_host must be a host tensor of {N + 1} starts")
+    return cu_seqlens_host.to(torch.int32).contiguous()
+
+
+def _workspace(workspace, nbytes: int, device):
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _check_cuda(workspace)
+    return workspace
+
+
+def kda_lin_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                    initial_state: Optional[torch.Tensor] = None,
+                    cu_seqlens: Optional[torch.Tensor] = None,
+                    cu_seqlens_host: Optional[torch.Tensor] = None, scale: float = 1.0,
+                    recurrent: bool = False, output_final_state: bool = True,
+                    o: Optional[torch.Tensor] = None,
+                    final_state: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None
+                    ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Decayed linear attention over packed sequences (kda_lin_prefill in
+    include/kda.h): q, k [total_T, H, d_k], v [total_T, H, d_v], log_decay [H]
+    fp32; a 4-D [B, T, H, d] batch is accepted and treated as B sequences of
+    length T.  recurrent=True runs the fp32 CUDA-core form everywhere.
+    Returns (o, final_state)."""
+    batch = None
+    if q.dim() == 4:
+        batch = q.shape[:2]
+        q, k, v = (t.reshape(-1, *t.shape[2:]) for t in (q, k, v))
+    _check_cuda(q, k, v, log_decay, initial_state, cu_seqlens, o, final_state)
+    N, total_T, H, d_k, d_v = _lin_sizes(q, k, v, log_decay, cu_seqlens)
+    if batch is not None:
+        if cu_seqlens is not None:
+            raise ValueError("a 4-D batch takes no cu_seqlens")
+        N = batch[0]
+    dt = q.dtype
+    code = _dtype_code(dt)
+    _expect(initial_state, (N, H, d_k, d_v), "initial_state", torch.float32)
+    _expect(final_state, (N, H, d_k, d_v), "final_state", torch.float32)
+    host_cu = _host_seqlens(cu_seqlens_host, N)
+    if o is not None and batch is not None:
+        _expect(o, (*batch, H, d_v), "o", dt)
+        o = o.view(total_T, H, d_v)
+    _expect(o, (total_T, H, d_v), "o", dt)
+    with _Launch(stream, q, k, v, log_decay, initial_state, cu_seqlens, o, final_state,
+                 workspace) as s:
+        if o is None:
+            o = torch.empty((total_T, H, d_v), dtype=dt, device=q.device)
+        if final_state is None and output_final_state:
+            final_state = torch.empty((N, H, d_k, d_v), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = _workspace(None, lin_prefill_workspace_bytes(N, total_T, H, d_k, d_v, dt),
+                                   q.device)
+        st = lib().kda_lin_prefill(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _addr(initial_state),
+            _addr(cu_seqlens), _addr(host_cu), N, total_T, H, d_k, d_v, code, scale,
+            KDA_FLAG_RECURRENT if recurrent else 0, o.data_ptr(), _addr(final_state),
+            workspace.data_ptr(), _nbytes(workspace), s)
+    if st != KDA_OK:
+        raise KDAError(st, "kda_lin_prefill")
+    return (o if batch is None else o.view(*batch, H, d_v)), final_state
+
+
+def kda_lin_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                        log_decay: torch.Tensor, state: torch.Tensor,
+                        slots: Optional[torch.Tensor] = None, scale: float = 1.0,
+                        o: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """One decode token of the decayed linear attention per sequence: q, k
+    [B, H, d_k], v [B, H, d_v]; `state` [pool, H, d_k, d_v] fp32 is updated in
+    place at rows `slots` (default 0..B-1).  Returns o [B, H, d_v]."""
+    _check_cuda(q, k, v, log_decay, state, slots, o)
+    _, B, H, d_k, d_v = _lin_sizes(q, k, v, log_decay, None)
+    dt = q.dtype
+    code = _dtype_code(dt)
+    if state.dim() != 4:
+        raise ValueError("state must have shape [pool, H, d_k, d_v]")
+    _expect(state, (state.shape[0], H, d_k, d_v), "state", torch.float32)
+    _expect(slots, (B,), "slots", torch.int32)
+    _expect(o, (B, H, d_v), "o", dt)
+    with _Launch(stream, q, k, v, log_decay, state, slots, o) as s:
+        if o is None:
+            o = torch.empty((B, H, d_v), dtype=dt, device=q.device)
+        st = lib().kda_lin_decode_step(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state.data_ptr(),
+            _addr(slots), state.shape[0], B, H, d_k, d_v, code, scale, o.data_ptr(), s)
+    if st != KDA_OK:
+        raise KDAError(st, "kda_lin_decode_step")
+    return o
+
+
+def kda_lin_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                     dO: torch.Tensor, initial_state: Optional[torch.Tensor] = None,
+                     cu_seqlens: Optional[torch.Tensor] = None,
+                     cu_seqlens_host: Optional[torch.Tensor] = None,
+                     dS_final: Optional[torch.Tensor] = None, scale: float = 1.0,
+                     recurrent: bool = False, workspace: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """Gradients of kda_lin_prefill (kda_lin_backward in include/kda.h) for
+    packed inputs; dO [total_T, H, d_v] in the inputs' dtype, dS_final
+    [N, H, d_k, d_v] fp32 or None.  Returns a dict: dq, dk [total_T, H, d_k] and
+    dv [total_T, H, d_v] in the inputs' dtype, dS0 [N, H, d_k, d_v] fp32."""
+    _check_cuda(q, k, v, log_decay, dO, initial_state, cu_seqlens, dS_final)
+    N, total_T, H, d_k, d_v = _lin_sizes(q, k, v, log_decay, cu_seqlens)
+    dt = q.dtype
+    code = _dtype_code(dt)
+    _expect(dO, (total_T, H, d_v), "dO", dt)
+    _expect(initial_state, (N, H, d_k, d_v), "initial_state", torch.float32)
+    _expect(dS_final, (N, H, d_k, d_v), "dS_final", torch.float32)
+    host_cu = _host_seqlens(cu_seqlens_host, N)
+    with _Launch(stream, q, k, v, log_decay, dO, initial_state, cu_seqlens, dS_final,
+                 workspace) as s:
+        dev = q.device
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        dS0 = torch.empty((N, H, d_k, d_v), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = _workspace(None,
+                                   lin_backward_workspace_bytes(N, total_T, H, d_k, d_v, dt), dev)
+        st = lib().kda_lin_backward(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _addr(initial_state),
+            _addr(cu_seqlens), _addr(host_cu), N, total_T, H, d_k, d_v, code, scale,
+            KDA_FLAG_RECURRENT if recurrent else 0, dO.data_ptr(), _addr(dS_final),
+            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dS0.data_ptr(), workspace.data_ptr(),
+            _nbytes(workspace), s)
+    if st != KDA_OK:
+        raise KDAError(st, "kda_lin_backward")
+    return dict(dq=dq, dk=dk, dv=dv, dS0=dS0)
+
+
+# ----------------------------------------------------------------- block norms
+def _norm_sizes(y, w_post, gate, x, res_scale, w_pre, gate_act):
+    """(rows, D, group, gate code) of a block norm, shapes and types checked;
+    the leading dimensions of y are rows."""
+    if y.dim() < 1 or w_post.dim() != 1:
+        raise ValueError("y must have shape [..., D] and w_post [group]")
+    D, group = y.shape[-1], w_post.shape[0]
+    for name, t in (("gate", gate), ("x", x)):
+        if t is not None and (t.shape != y.shape or t.dtype != y.dtype):
+            raise ValueError(f"{name} must be a {y.dtype} tensor of shape {tuple(y.shape)}, "
+                             f"got {t.dtype} {tuple(t.shape)}")
+    _expect(w_post, (group,), "w_post", torch.float32)
+    _expect(res_scale, (D,), "res_scale", torch.float32)
+    _expect(w_pre, (D,), "w_pre", torch.float32)
+    if gate is None:
+        act = KDA_GATE_SIGMOID
+    elif gate_act in _GATE_ACTS:
+        act = _GATE_ACTS[gate_act]
+    else:
+        raise ValueError(f"gate_act must be one of {sorted(_GATE_ACTS)}, got {gate_act!r}")
+    return (y.numel() // D if D else 0), D, group, act
+
+
+def kda_block_norm(y: torch.Tensor, w_post: torch.Tensor, gate: Optional[torch.Tensor] = None,
+                   x: Optional[torch.Tensor] = None, res_scale: Optional[torch.Tensor] = None,
+                   w_pre: Optional[torch.Tensor] = None, gate_act: str = "sigmoid",
+                   eps: float = 1e-6, x_out: Optional[torch.Tensor] = None,
+                   h: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None
+                   ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The norms around a block (kda_block_norm in include/kda.h):
+    x_out = x + res_scale * RMSNorm(y; w_post) * act(gate), h = RMSNorm(x_out;
+    w_pre).  y, gate, x [..., D]; w_post [group] (group: D, or a head of 32, 64
+    or 128 channels that divides D); res_scale, w_pre [D] fp32; every part but
+    y and w_post optional.  gate_act: "sigmoid" or "silu" (unused without a
+    gate).  Returns (x_out, h), h None without w_pre."""
+    _check_cuda(y, w_post, gate, x, res_scale, w_pre, x_out, h)
+    rows, D, group, act = _norm_sizes(y, w_post, gate, x, res_scale, w_pre, gate_act)
+    code = _dtype_code(y.dtype)
+    _expect(x_out, tuple(y.shape), "x_out", y.dtype)
+    _expect(h, tuple(y.shape), "h", y.dtype)
+    with _Launch(stream, y, w_post, gate, x, res_scale, w_pre, x_out, h) as s:
+        if x_out is None:
+            x_out = torch.empty_like(y)
+        if h is None and w_pre is not None:
+            h = torch.empty_like(y)
+        st = lib().kda_block_norm(
+            y.data_ptr(), w_post.data_ptr(), _addr(gate), _addr(x), _addr(res_scale),
+            _addr(w_pre), rows, D, group, code, act, eps, x_out.data_ptr(), _addr(h), s)
+    if st != KDA_OK:
+        raise KDAError(st, "kda_block_norm")
+    return x_out, h
+
+
+def block_norm_backward_workspace_bytes(rows: int, D: int, group: int) -> int:
+    return int(lib().kda_block_norm_backward_workspace_bytes(rows, D, group))
+
+
+def kda_block_norm_backward(y: torch.Tensor, w_post: torch.Tensor,
+                            dx_out: Optional[torch.Tensor],
+                            gate: Optional[torch.Tensor] = None,
+                            x_out: Optional[torch.Tensor] = None,
+                            res_scale: Optional[torch.Tensor] = None,
+                            w_pre: Optional[torch.Tensor] = None,
+                            dh: Optional[torch.Tensor] = None, gate_act: str = "sigmoid",
+                            eps: float = 1e-6, residual: bool = True,
+                            workspace: Optional[torch.Tensor] = None,
+                            stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """Gradients of kda_block_norm (kda_block_norm_backward in include/kda.h),
+    given dx_out (or None) and, with w_pre, dh; x_out as the forward returned
+    it (needed with w_pre).  residual=False leaves dx out.  Returns a dict of
+    dy, dgate, dx in y's dtype and dw_post, dres_scale, dw_pre fp32, None where
+    the forward had no such input."""
+    _check_cuda(y, w_post, dx_out, gate, x_out, res_scale, w_pre, dh)
+    rows, D, group, act = _norm_sizes(y, w_post, gate, x_out, res_scale, w_pre, gate_act)
+    code = _dtype_code(y.dtype)
+    for name, t in (("dx_out", dx_out), ("dh", dh)):
+        _expect(t, tuple(y.shape), name, y.dtype)
+    with _Launch(stream, y, w_post, dx_out, gate, x_out, res_scale, w_pre, dh, workspace) as s:
+        dev = y.device
+        dy = torch.empty_like(y)
+        dgate = None if gate is None else torch.empty_like(y)
+        dx = torch.empty_like(y) if residual else None
+        dw_post = torch.empty(group, dtype=torch.float32, device=dev)
+        dres = None if res_scale is None else torch.empty_like(res_scale)
+        dw_pre = None if w_pre is None else torch.empty_like(w_pre)
+        if workspace is None:
+            workspace = _workspace(None, block_norm_backward_workspace_bytes(rows, D, group), dev)
+        st = lib().kda_block_norm_backward(
+            y.data_ptr(), w_post.data_ptr(), _addr(gate), _addr(x_out), _addr(res_scale),
+            _addr(w_pre), _addr(dx_out), _addr(dh), rows, D, group, code, act, eps,
+            dy.data_ptr(), _addr(dgate), _addr(dx), dw_post.data_ptr(), _addr(dres),
+            _addr(dw_pre), workspace.data_ptr(), _nbytes(workspace), s)
+    if st != KDA_OK:
+        raise KDAError(st, "kda_block_norm_backward")
+    return dict(dy=dy, dgate=dgate, dx=dx, dw_post=dw_post, dres_scale=dres, dw_pre=dw_pre)

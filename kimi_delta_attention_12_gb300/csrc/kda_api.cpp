@@ -8,17 +8,16 @@
 #include <stdint.h>
 #include <string.h>
 
+#include "kda_checks.h"
 #include "kda_internal.h"
 
 namespace {
 
-inline bool aligned(const void* p, uintptr_t a) {
-    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
-}
-
-inline bool supported_dim(int32_t d) { return d == 32 || d == 64 || d == 128; }
-
-inline size_t elem_bytes(kda_dtype dt) { return dt == KDA_F32 ? 4 : 2; }
+using kda::aligned;
+using kda::elem_bytes;
+using kda::overlaps;
+using kda::round_up;
+using kda::supported_dim;
 
 constexpr uint32_t kKnownFlags = KDA_FLAG_L2NORM_QK | KDA_FLAG_RECURRENT |
                                  KDA_FLAG_SOFTPLUS_GATE | KDA_FLAG_SHORT_PEER_WAITS;
@@ -30,15 +29,6 @@ constexpr int32_t kCheckpointGrain = 64;  // checkpoints fall on chunk boundarie
 
 // status word + work counter, then the optional schedule (one int per unit)
 constexpr size_t kWsHeader = 256;
-
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-// Whether the byte ranges [a, a + na) and [b, b + nb) share a byte.
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-    if (!a || !b || na == 0 || nb == 0) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
 
 constexpr int32_t kMaxConvWidth = 4;
 

@@ -1,0 +1,100 @@
+// kda_lin.cuh -- device helpers of the decayed linear attention: powers of
+// the decay and the cut of packed sequences into segments.
+#pragma once
+
+#include <stdint.h>
+
+#include "kda_seqlens.cuh"
+
+namespace kda {
+namespace lin {
+
+// e^{g n}, n >= 0.  The product's rounding error is carried into the factor
+// (e^{p + err} = e^p (1 + err)), so a long distance costs no digits; n = 0 is
+// 1 whatever g is (an infinite g means a state that is dropped every token).
+__device__ __forceinline__ float decay_pow(float g, int64_t n) {
+    if (n == 0) return 1.0f;
+    const float fn = (float)n, p = g * fn;
+    if (p < -200.0f) return 0.0f;
+    const float err = fmaf(g, fn, -p);
+    return fabsf(err) < 1.0f ? expf(p) * (1.0f + err) : expf(p);
+}
+
+// A segment of a sequence in the order of the pass.
+struct Segment {
+    int n;            // sequence, or -1: no such segment
+    int j;            // position among the sequence's segments, in pass order
+    int count;        // the sequence's segments
+    int64_t bos, eos; // its sequence's tokens
+    int64_t t0, t1;   // its own tokens
+    int64_t u;        // row of seg_states of the sequence's segment 0
+};
+
+__device__ __forceinline__ int seg_count(int64_t len, int64_t seg_len) {
+    return len <= seg_len ? 1 : (int)((len + seg_len - 1) / seg_len);
+}
+
+// Token range of the sequence's segment i in pass order.
+__device__ __forceinline__ void seg_tokens(const Segment& s, int i, int64_t seg_len, int reverse,
+                                           int64_t& t0, int64_t& t1) {
+    const int k = reverse ? s.count - 1 - i : i;
+    t0 = s.bos + (int64_t)k * seg_len;
+    t1 = t0 + seg_len < s.eos ? t0 + seg_len : s.eos;
+}
+
+// Rows of seg_states: each sequence keeps the states of all its segments but
+// the last one, at most floor(length / seg_len) of them.
+__device__ __forceinline__ int64_t seg_rows(int64_t total_T, int64_t seg_len) {
+    return total_T / seg_len;
+}
+
+// Segment number `index` over all sequences (sequence by sequence; an empty
+// sequence has one empty segment).  Every warp calls it whole.
+__device__ __forceinline__ Segment find_segment(const int32_t* cu, int N, int64_t total_T,
+                                                int64_t seg_len, int reverse, int64_t index) {
+    Segment s;
+    s.n = -1;
+    s.j = s.count = 0;
+    s.bos = s.eos = s.t0 = s.t1 = s.u = 0;
+    if (!cu) {
+        const int64_t len = total_T / N;
+        s.count = seg_count(len, seg_len);
+        if (index >= (int64_t)N * s.count) return s;
+        s.n = (int)(index / s.count);
+        s.j = (int)(index % s.count);
+        s.u = (int64_t)s.n * (s.count - 1);
+        s.bos = s.n * len;
+        s.eos = s.bos + len;
+    } else {
+        const int lane = threadIdx.x & 31;
+        int64_t before = 0;   // segments of the sequences before this round's
+        for (int base = 0; base < N; base += 32) {
+            const int n = base + lane;
+            const int c = n < N ? seg_count(clamped_len(cu, n, N, total_T), seg_len) : 0;
+            int sum = c;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += o;
+            }
+            const int64_t first = before + sum - c;
+            const unsigned hit = __ballot_sync(0xffffffffu, index >= first && index < first + c);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                const int64_t f = before + __shfl_sync(0xffffffffu, sum - c, src);
+                s.n = base + src;
+                s.j = (int)(index - f);
+                s.count = __shfl_sync(0xffffffffu, c, src);
+                s.u = f - s.n;   // every sequence before it keeps all segments but one
+                clamped_seq(cu, s.n, N, total_T, s.bos, s.eos);
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        if (s.n < 0) return s;
+    }
+    seg_tokens(s, s.j, seg_len, reverse, s.t0, s.t1);
+    return s;
+}
+
+}  // namespace lin
+}  // namespace kda

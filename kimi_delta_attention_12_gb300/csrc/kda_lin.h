@@ -1,0 +1,72 @@
+// kda_lin.h -- declarations of the decayed linear attention, shared by its
+// C-ABI layer (kda_lin_api.cpp) and its kernels.  Not part of the public
+// interface.
+//
+// Forward and backward are one kind of pass.  With a = e^{g_h},
+//     out_t = out_scale * ( sum_{s <= t} kv_scale a^{t-s} (x_t . y_s) z_s
+//                           + a^{(tokens before t) + 1} S_in^T x_t )
+// over rows x, y of width dx and z, out of width dz:
+//   o  : x, y, z = q, k, v      S_in = S_0
+//   dq : x, y, z = dO, v, k     S_in = S_0^T
+//   dk : x, y, z = v, dO, q     S_in = dS_T^T, time reversed
+//   dv : x, y, z = k, q, dO     S_in = dS_T,   time reversed; S_out = dS_0
+// In a reversed pass t and s run from each sequence's end and the carried
+// state is already decayed when it is handed on: the token that meets S_in
+// first weights it with a^0, and S_out ends with one factor a more.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace kda {
+
+struct LinPass {
+    const void* x;              // [total_T, H, dx]
+    const void* y;              // [total_T, H, dx]
+    const void* z;              // [total_T, H, dz]
+    void* out;                  // [total_T, H, dz]
+    const float* log_decay;     // [H]
+    const float* state_in;      // [N, H, dx, dz] (or [N, H, dz, dx]), or null
+    float* state_out;           // [N, H, dx, dz], or null
+    float* seg_states;          // workspace [total_T / seg_len][H][dx][dz]
+    const int32_t* cu_seqlens;  // device [N + 1], or null (equal lengths)
+    int32_t* status;            // workspace status word (tensor-core form)
+    int32_t N;
+    int32_t total_T;
+    int32_t H;
+    int32_t dx;
+    int32_t dz;
+    int32_t seg_len;            // tokens per segment, a multiple of 128
+    int32_t state_in_turned;    // state_in holds [dz, dx]
+    int32_t reverse;
+    float out_scale;
+    float kv_scale;
+};
+
+// Tokens per segment for these sizes: every sequence is cut into segments of
+// this length so that a few long sequences still fill `sms` SMs.
+// `ctas_per_pair`: CTAs that work on one (sequence, head) pair without a cut.
+int32_t lin_segment_tokens(int32_t N, int32_t total_T, int32_t H, int ctas_per_pair, int sms);
+
+// The pass on the CUDA cores, fp32 arithmetic: dx, dz in {32, 64, 128}, dtype
+// 0 = fp32, 1 = bf16.
+cudaError_t launch_lin_pass(const LinPass& p, int dtype, cudaStream_t stream);
+
+// One decode token per row, the state pool updated in place.
+struct LinDecode {
+    const void* q;              // [B, H, d_k]
+    const void* k;
+    const void* v;              // [B, H, d_v]
+    const float* log_decay;     // [H]
+    float* state;               // [pool_size, H, d_k, d_v]
+    const int32_t* slots;       // [B] or null
+    void* o;                    // [B, H, d_v]
+    int32_t pool_size;
+    int32_t B;
+    int32_t H;
+    float scale;
+};
+cudaError_t launch_lin_decode(const LinDecode& p, int d_k, int d_v, int dtype,
+                              cudaStream_t stream);
+
+}  // namespace kda

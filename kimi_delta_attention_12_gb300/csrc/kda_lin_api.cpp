@@ -1,0 +1,251 @@
+// kda_lin_api.cpp -- the C ABI of the decayed linear attention declared in
+// include/kda.h: argument validation, workspace layout and launches on the
+// caller's stream.  No allocation, no exceptions across the boundary.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <string.h>
+
+#include "kda_checks.h"
+#include "kda_lin.h"
+
+namespace {
+
+using kda::aligned;
+using kda::elem_bytes;
+using kda::overlaps;
+using kda::round_up;
+using kda::supported_dim;
+
+constexpr size_t kHeader = 256;   // status word
+constexpr uint32_t kLinFlags = KDA_FLAG_RECURRENT;
+
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return sms;
+}
+
+// Both forms cut the sequences alike where they can, so that a workspace
+// serves either; dz is the width whose columns the CUDA-core form spreads.
+int32_t segment_tokens(int32_t N, int32_t total_T, int32_t H, int32_t dz) {
+    return kda::lin_segment_tokens(N, total_T, H, dz / 32, sm_count());
+}
+
+size_t seg_state_bytes(int32_t total_T, int32_t H, int32_t dx, int32_t dz, int32_t seg_len) {
+    return round_up((size_t)(total_T / seg_len) * H * dx * dz * sizeof(float), 256);
+}
+
+size_t state_bytes(int32_t N, int32_t H, int32_t d_k, int32_t d_v) {
+    return (size_t)N * H * d_k * d_v * sizeof(float);
+}
+
+bool bad_sizes(int32_t N, int32_t total_T, int32_t H) { return N < 1 || H < 1 || total_T < 0; }
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_lin_prefill_workspace_bytes(int32_t N, int32_t total_T, int32_t H, int32_t d_k,
+                                       int32_t d_v, kda_dtype dt) {
+    if (bad_sizes(N, total_T, H) || !supported_dim(d_k) || !supported_dim(d_v) ||
+        (dt != KDA_F32 && dt != KDA_BF16)) {
+        return 0;
+    }
+    const int32_t seg = segment_tokens(N, total_T, H, d_v);
+    // the states of the segments, and a copy of the initial states for a call
+    // that updates them in place
+    size_t b = kHeader + seg_state_bytes(total_T, H, d_k, d_v, seg);
+    if (total_T / seg > 0) b += round_up(state_bytes(N, H, d_k, d_v), 256);
+    return b;
+}
+
+int kda_lin_prefill(const void* q, const void* k, const void* v, const float* log_decay,
+                    const float* initial_state, const int32_t* cu_seqlens,
+                    const int32_t* cu_seqlens_host, int32_t N, int32_t total_T, int32_t H,
+                    int32_t d_k, int32_t d_v, kda_dtype dt, float scale, uint32_t flags, void* o,
+                    float* final_state, void* workspace, size_t workspace_bytes, void* stream) {
+    if (dt != KDA_F32 && dt != KDA_BF16) return KDA_ERR_UNSUPPORTED;
+    if (!supported_dim(d_k) || !supported_dim(d_v)) return KDA_ERR_UNSUPPORTED;
+    if (bad_sizes(N, total_T, H)) return KDA_ERR_INVALID_ARG;
+    if ((flags & ~kLinFlags) != 0 || !isfinite(scale) || !log_decay) return KDA_ERR_INVALID_ARG;
+    if (total_T > 0 && (!q || !k || !v || !o)) return KDA_ERR_INVALID_ARG;
+    if (!cu_seqlens && total_T % N != 0) return KDA_ERR_INVALID_ARG;
+    if (cu_seqlens_host && !kda::valid_host_seqlens(cu_seqlens_host, N, total_T)) {
+        return KDA_ERR_INVALID_ARG;
+    }
+    const size_t need = kda_lin_prefill_workspace_bytes(N, total_T, H, d_k, d_v, dt);
+    if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;
+    const size_t eb = elem_bytes(dt), nst = state_bytes(N, H, d_k, d_v);
+    const size_t nqk = (size_t)total_T * H * d_k * eb, nv = (size_t)total_T * H * d_v * eb;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) ||
+        !aligned(log_decay, 4) || !aligned(initial_state, 16) || !aligned(final_state, 16) ||
+        !aligned(cu_seqlens, 4) || !aligned(workspace, 256)) {
+        return KDA_ERR_ALIGNMENT;
+    }
+    // o may not overlap an input; final_state only the initial one, whole
+    const void* ins[4] = {q, k, v, initial_state};
+    const size_t nin[4] = {nqk, nqk, nv, nst};
+    const size_t used = need;
+    for (int i = 0; i < 4; ++i) {
+        if (overlaps(o, nv, ins[i], nin[i]) || overlaps(workspace, used, ins[i], nin[i])) {
+            return KDA_ERR_INVALID_ARG;
+        }
+        if (overlaps(final_state, nst, ins[i], nin[i]) && final_state != initial_state) {
+            return KDA_ERR_INVALID_ARG;
+        }
+    }
+    if (overlaps(o, nv, final_state, nst) || overlaps(workspace, used, o, nv) ||
+        overlaps(workspace, used, final_state, nst)) {
+        return KDA_ERR_INVALID_ARG;
+    }
+    if (total_T == 0 && !final_state) return KDA_OK;
+
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    if (cudaMemsetAsync(ws, 0, sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
+    kda::LinPass p;
+    memset(&p, 0, sizeof(p));
+    p.x = q; p.y = k; p.z = v; p.out = o;
+    p.log_decay = log_decay;
+    p.state_in = initial_state; p.state_out = final_state;
+    p.cu_seqlens = cu_seqlens;
+    p.status = reinterpret_cast<int32_t*>(ws);
+    p.N = N; p.total_T = total_T; p.H = H; p.dx = d_k; p.dz = d_v;
+    p.seg_len = segment_tokens(N, total_T, H, d_v);
+    p.seg_states = reinterpret_cast<float*>(ws + kHeader);
+    p.out_scale = scale; p.kv_scale = 1.0f;
+    if (initial_state && initial_state == final_state && total_T / p.seg_len > 0) {
+        // the last segment may write its state before the first has read it
+        float* copy = reinterpret_cast<float*>(
+            ws + kHeader + seg_state_bytes(total_T, H, d_k, d_v, p.seg_len));
+        if (cudaMemcpyAsync(copy, initial_state, nst, cudaMemcpyDeviceToDevice, s) !=
+            cudaSuccess) {
+            return KDA_ERR_CUDA;
+        }
+        p.state_in = copy;
+    }
+    return kda::launch_lin_pass(p, dt == KDA_F32 ? 0 : 1, s) == cudaSuccess ? KDA_OK
+                                                                            : KDA_ERR_CUDA;
+}
+
+int kda_lin_decode_step(const void* q, const void* k, const void* v, const float* log_decay,
+                        float* state, const int32_t* slots, int32_t pool_size, int32_t B,
+                        int32_t H, int32_t d_k, int32_t d_v, kda_dtype dt, float scale, void* o,
+                        void* stream) {
+    if (dt != KDA_F32 && dt != KDA_BF16) return KDA_ERR_UNSUPPORTED;
+    if (!supported_dim(d_k) || !supported_dim(d_v)) return KDA_ERR_UNSUPPORTED;
+    if (B < 0 || H < 1 || pool_size < 0 || !isfinite(scale)) return KDA_ERR_INVALID_ARG;
+    if (B == 0) return KDA_OK;
+    if (!q || !k || !v || !log_decay || !state || !o) return KDA_ERR_INVALID_ARG;
+    if (!slots && pool_size < B) return KDA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) ||
+        !aligned(state, 16) || !aligned(log_decay, 4) || !aligned(slots, 4)) {
+        return KDA_ERR_ALIGNMENT;
+    }
+    const size_t eb = elem_bytes(dt), nqk = (size_t)B * H * d_k * eb,
+                 nv = (size_t)B * H * d_v * eb, nst = state_bytes(pool_size, H, d_k, d_v);
+    const void* ins[3] = {q, k, v};
+    const size_t nin[3] = {nqk, nqk, nv};
+    for (int i = 0; i < 3; ++i) {
+        if (overlaps(o, nv, ins[i], nin[i]) || overlaps(state, nst, ins[i], nin[i])) {
+            return KDA_ERR_INVALID_ARG;
+        }
+    }
+    if (overlaps(o, nv, state, nst)) return KDA_ERR_INVALID_ARG;
+    kda::LinDecode p;
+    p.q = q; p.k = k; p.v = v; p.log_decay = log_decay; p.state = state; p.slots = slots; p.o = o;
+    p.pool_size = pool_size; p.B = B; p.H = H; p.scale = scale;
+    return kda::launch_lin_decode(p, d_k, d_v, dt == KDA_F32 ? 0 : 1,
+                                  static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KDA_OK
+               : KDA_ERR_CUDA;
+}
+
+// The three passes run one after another on the stream and share the segment
+// states' room, sized for the pass that needs most.
+size_t kda_lin_backward_workspace_bytes(int32_t N, int32_t total_T, int32_t H, int32_t d_k,
+                                        int32_t d_v, kda_dtype dt) {
+    if (bad_sizes(N, total_T, H) || !supported_dim(d_k) || !supported_dim(d_v) ||
+        (dt != KDA_F32 && dt != KDA_BF16)) {
+        return 0;
+    }
+    const size_t a = seg_state_bytes(total_T, H, d_k, d_v, segment_tokens(N, total_T, H, d_v));
+    const size_t b = seg_state_bytes(total_T, H, d_k, d_v, segment_tokens(N, total_T, H, d_k));
+    return kHeader + (a > b ? a : b);
+}
+
+int kda_lin_backward(const void* q, const void* k, const void* v, const float* log_decay,
+                     const float* initial_state, const int32_t* cu_seqlens,
+                     const int32_t* cu_seqlens_host, int32_t N, int32_t total_T, int32_t H,
+                     int32_t d_k, int32_t d_v, kda_dtype dt, float scale, uint32_t flags,
+                     const void* dO, const float* dS_final, void* dq, void* dk, void* dv,
+                     float* dS0, void* workspace, size_t workspace_bytes, void* stream) {
+    if (dt != KDA_F32 && dt != KDA_BF16) return KDA_ERR_UNSUPPORTED;
+    if (!supported_dim(d_k) || !supported_dim(d_v)) return KDA_ERR_UNSUPPORTED;
+    if (bad_sizes(N, total_T, H)) return KDA_ERR_INVALID_ARG;
+    if ((flags & ~kLinFlags) != 0 || !isfinite(scale) || !log_decay) return KDA_ERR_INVALID_ARG;
+    if (total_T > 0 && (!q || !k || !v || !dO || !dq || !dk || !dv)) return KDA_ERR_INVALID_ARG;
+    if (!cu_seqlens && total_T % N != 0) return KDA_ERR_INVALID_ARG;
+    if (cu_seqlens_host && !kda::valid_host_seqlens(cu_seqlens_host, N, total_T)) {
+        return KDA_ERR_INVALID_ARG;
+    }
+    const size_t need = kda_lin_backward_workspace_bytes(N, total_T, H, d_k, d_v, dt);
+    if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;
+    const void* bufs[12] = {q, k, v, dO, initial_state, dS_final, dq, dk, dv, dS0, workspace,
+                            nullptr};
+    for (int i = 0; i < 10; ++i) {
+        if (!aligned(bufs[i], 16)) return KDA_ERR_ALIGNMENT;
+    }
+    if (!aligned(log_decay, 4) || !aligned(cu_seqlens, 4) || !aligned(workspace, 256)) {
+        return KDA_ERR_ALIGNMENT;
+    }
+    const size_t eb = elem_bytes(dt), nst = state_bytes(N, H, d_k, d_v);
+    const size_t nqk = (size_t)total_T * H * d_k * eb, nv = (size_t)total_T * H * d_v * eb;
+    const size_t size[11] = {nqk, nqk, nv, nv, nst, nst, nqk, nqk, nv, nst, need};
+    for (int i = 6; i < 11; ++i) {      // no output, nor the workspace, on another buffer
+        for (int j = 0; j < i; ++j) {
+            if (overlaps(bufs[i], size[i], bufs[j], size[j])) return KDA_ERR_INVALID_ARG;
+        }
+    }
+    if (total_T == 0 && !dS0) return KDA_OK;
+
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    if (cudaMemsetAsync(ws, 0, sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
+    const int dtype = dt == KDA_F32 ? 0 : 1;
+    kda::LinPass p;
+    memset(&p, 0, sizeof(p));
+    p.log_decay = log_decay;
+    p.cu_seqlens = cu_seqlens;
+    p.status = reinterpret_cast<int32_t*>(ws);
+    p.seg_states = reinterpret_cast<float*>(ws + kHeader);
+    p.N = N; p.total_T = total_T; p.H = H;
+    cudaError_t err = cudaSuccess;
+    if (total_T > 0) {
+        // dq_t = scale S_t dO_t: forward in time with the turned state
+        p.x = dO; p.y = v; p.z = k; p.out = dq; p.dx = d_v; p.dz = d_k;
+        p.state_in = initial_state; p.state_in_turned = 1; p.state_out = nullptr;
+        p.reverse = 0; p.out_scale = scale; p.kv_scale = 1.0f;
+        p.seg_len = segment_tokens(N, total_T, H, d_k);
+        err = kda::launch_lin_pass(p, dtype, s);
+        if (err != cudaSuccess) return KDA_ERR_CUDA;
+        // dk_t = G_t v_t, G_t = scale q_t dO_t^T + a G_{t+1}: from the ends
+        p.x = v; p.y = dO; p.z = q; p.out = dk;
+        p.state_in = dS_final; p.reverse = 1; p.out_scale = 1.0f; p.kv_scale = scale;
+        err = kda::launch_lin_pass(p, dtype, s);
+        if (err != cudaSuccess) return KDA_ERR_CUDA;
+    }
+    // dv_t = G_t^T k_t; the state it ends with is dS_0
+    p.x = k; p.y = q; p.z = dO; p.out = dv; p.dx = d_k; p.dz = d_v;
+    p.state_in = dS_final; p.state_in_turned = 0; p.state_out = dS0;
+    p.reverse = 1; p.out_scale = 1.0f; p.kv_scale = scale;
+    p.seg_len = segment_tokens(N, total_T, H, d_v);
+    err = kda::launch_lin_pass(p, dtype, s);
+    return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,382 @@
+// kda_lin_attn.cu -- decayed linear attention on the CUDA cores (fp32
+// arithmetic) for every type and head size, and its decode step.
+//
+// A pass walks a segment of a sequence in chunks of C = 32 tokens with the
+// state in shared memory.  With a = e^g, rows i, j of a chunk of c tokens and
+// the state S before it (forward in time):
+//     out_i = sum_{j <= i} a^{i-j} (x_i . y_j) z_j + a^{i+1} S^T x_i
+//     S'    = a^c S + sum_j a^{c-1-j} y_j z_j^T
+// A CTA owns 32 of the dz columns of one (segment, head): state columns do
+// not mix, only the products x_i . y_j are formed again in each slice.
+// A sequence that is cut into segments is walked twice: once for the state
+// that each segment adds, and, after that, for the outputs, where a segment
+// first joins the states of the segments before it.
+#include "kda_lin.h"
+
+#include <cuda_bf16.h>
+#include <limits.h>
+
+#include "kda_lin.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int C = 32;        // tokens per chunk
+constexpr int SLICE = 32;    // state columns per CTA
+constexpr int THREADS = 256;
+
+__device__ __forceinline__ float4 load4(const float* p) {
+    return *reinterpret_cast<const float4*>(p);
+}
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+    const uint2 r = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u),
+                       __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) {
+    *reinterpret_cast<float4*>(p) = v;
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    uint2 r;
+    r.x = *reinterpret_cast<const uint32_t*>(&a);
+    r.y = *reinterpret_cast<const uint32_t*>(&b);
+    *reinterpret_cast<uint2*>(p) = r;
+}
+
+template <int DX>
+constexpr size_t pass_smem_bytes() {
+    return sizeof(float) * (2 * C * (DX + 4) + C * SLICE + C * (C + 1) + DX * SLICE + C + 1);
+}
+
+// S[d][0..31] of one (sequence, head) slice, in a turned or plain state.
+__device__ __forceinline__ float4 state_at(const float* st, int d, int c, int dx, int dz,
+                                           int turned) {
+    if (!turned) return load4(st + (size_t)d * dz + c);
+    return make_float4(st[(size_t)c * dx + d], st[(size_t)(c + 1) * dx + d],
+                       st[(size_t)(c + 2) * dx + d], st[(size_t)(c + 3) * dx + d]);
+}
+
+// STATES: only the state that the segment adds, into seg_states.
+template <typename T, int DX, bool STATES>
+__global__ void __launch_bounds__(THREADS) lin_pass_kernel(LinPass p) {
+    constexpr int LD = DX + 4, ROWS = DX / 32;
+    extern __shared__ float4 smem4[];
+    float* X = reinterpret_cast<float*>(smem4);
+    float* Y = X + C * LD;
+    float* Z = Y + C * LD;
+    float* P = Z + C * SLICE;         // [C][C + 1]
+    float* S = P + C * (C + 1);
+    float* lam = S + DX * SLICE;      // a^0 .. a^C
+
+    const int tid = threadIdx.x, dz = p.dz, slices = dz / SLICE;
+    const int col0 = (blockIdx.x % slices) * SLICE;
+    const int64_t rest = blockIdx.x / slices;
+    const int h = (int)(rest % p.H);
+    const lin::Segment sg = lin::find_segment(p.cu_seqlens, p.N, p.total_T, p.seg_len, p.reverse,
+                                              rest / p.H);
+    if (sg.n < 0 || (STATES && sg.j + 1 >= sg.count)) return;
+    const float g = p.log_decay[h];
+    if (tid <= C) lam[tid] = lin::decay_pow(g, tid);
+
+    const size_t state_floats = (size_t)DX * dz;
+    const int64_t rows = lin::seg_rows(p.total_T, p.seg_len);
+    const int c4 = (tid & 7) * 4;     // 4 columns of the slice, and rows (tid / 8) + 32 i
+    {
+        float4 st[ROWS];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) st[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!STATES) {
+            if (p.state_in) {
+                const float* s0 = p.state_in + ((size_t)sg.n * p.H + h) * state_floats;
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i)
+                    st[i] = state_at(s0, tid / 8 + 32 * i, col0 + c4, DX, dz, p.state_in_turned);
+            }
+            for (int i = 0; i < sg.j; ++i) {   // join the segments before this one
+                int64_t a, b;
+                lin::seg_tokens(sg, i, p.seg_len, p.reverse, a, b);
+                const float f = lin::decay_pow(g, b - a);
+                if (sg.u + i >= rows) break;   // only a malformed cu_seqlens
+                const float* u = p.seg_states + ((sg.u + i) * (int64_t)p.H + h) * state_floats;
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r) {
+                    const float4 v = load4(u + (size_t)(tid / 8 + 32 * r) * dz + col0 + c4);
+                    st[r].x = f * st[r].x + v.x;
+                    st[r].y = f * st[r].y + v.y;
+                    st[r].z = f * st[r].z + v.z;
+                    st[r].w = f * st[r].w + v.w;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) store4(S + (tid / 8 + 32 * i) * SLICE + c4, st[i]);
+    }
+    __syncthreads();
+
+    const T* x = static_cast<const T*>(p.x);
+    const T* y = static_cast<const T*>(p.y);
+    const T* z = static_cast<const T*>(p.z);
+    T* out = static_cast<T*>(p.out);
+    const int64_t chunks = (sg.t1 - sg.t0 + C - 1) / C;
+    for (int64_t ci = 0; ci < chunks; ++ci) {
+        const int64_t c0 = sg.t0 + (p.reverse ? chunks - 1 - ci : ci) * C;
+        const int len = (int)(sg.t1 - c0 < C ? sg.t1 - c0 : C);
+        for (int i = tid; i < C * DX / 4; i += THREADS) {
+            const int r = i / (DX / 4), d = (i % (DX / 4)) * 4;
+            float4 vx = make_float4(0.f, 0.f, 0.f, 0.f), vy = vx;
+            if (r < len) {
+                const size_t at = ((size_t)(c0 + r) * p.H + h) * DX + d;
+                if (!STATES) vx = load4(x + at);
+                vy = load4(y + at);
+            }
+            if (!STATES) store4(X + r * LD + d, vx);
+            store4(Y + r * LD + d, vy);
+        }
+        {
+            const int r = tid / 8;
+            float4 vz = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < len) vz = load4(z + ((size_t)(c0 + r) * p.H + h) * dz + col0 + c4);
+            store4(Z + r * SLICE + c4, vz);
+        }
+        __syncthreads();
+        if (!STATES) {
+            const int r0 = (tid / 16) * 2, q0 = tid % 16;   // rows r0, r0 + 1; columns q0, q0 + 16
+            float acc[2][2] = {};
+#pragma unroll 4
+            for (int d = 0; d < DX; d += 4) {
+                float4 a[2], b[2];
+                a[0] = load4(X + r0 * LD + d);
+                a[1] = load4(X + (r0 + 1) * LD + d);
+                b[0] = load4(Y + q0 * LD + d);
+                b[1] = load4(Y + (q0 + 16) * LD + d);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[i][j] += a[i].x * b[j].x + a[i].y * b[j].y + a[i].z * b[j].z +
+                                     a[i].w * b[j].w;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int t = r0 + i, s = q0 + 16 * j, dist = p.reverse ? s - t : t - s;
+                    P[t * (C + 1) + s] =
+                        dist >= 0 && s < len ? acc[i][j] * lam[dist] * p.kv_scale : 0.0f;
+                }
+            __syncthreads();
+            const int t = tid / 8;
+            float4 intra = make_float4(0.f, 0.f, 0.f, 0.f), inter = intra;
+            // no token that is masked for this row is touched, not even times zero
+            const int s0 = p.reverse ? t : 0, s1 = p.reverse ? len : t + 1;
+#pragma unroll 4
+            for (int s = s0; s < s1; ++s) {
+                const float w = P[t * (C + 1) + s];
+                const float4 v = load4(Z + s * SLICE + c4);
+                intra.x += w * v.x; intra.y += w * v.y; intra.z += w * v.z; intra.w += w * v.w;
+            }
+#pragma unroll 8
+            for (int d = 0; d < DX; ++d) {
+                const float w = X[t * LD + d];
+                const float4 v = load4(S + d * SLICE + c4);
+                inter.x += w * v.x; inter.y += w * v.y; inter.z += w * v.z; inter.w += w * v.w;
+            }
+            if (t < len) {
+                const float f = lam[p.reverse ? len - 1 - t : t + 1], m = p.out_scale;
+                store4(out + ((size_t)(c0 + t) * p.H + h) * dz + col0 + c4,
+                       make_float4(m * (intra.x + f * inter.x), m * (intra.y + f * inter.y),
+                                   m * (intra.z + f * inter.z), m * (intra.w + f * inter.w)));
+            }
+            __syncthreads();   // S and the operands are read before S moves on
+        }
+        {
+            const float f = lam[len];
+            float4 st[ROWS];
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                st[i] = load4(S + (tid / 8 + 32 * i) * SLICE + c4);
+                st[i].x *= f; st[i].y *= f; st[i].z *= f; st[i].w *= f;
+            }
+            for (int s = 0; s < len; ++s) {
+                const float w = lam[p.reverse ? s + 1 : len - 1 - s] * p.kv_scale;
+                float4 v = load4(Z + s * SLICE + c4);
+                v.x *= w; v.y *= w; v.z *= w; v.w *= w;
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i) {
+                    const float k = Y[s * LD + tid / 8 + 32 * i];
+                    st[i].x += k * v.x; st[i].y += k * v.y; st[i].z += k * v.z; st[i].w += k * v.w;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) store4(S + (tid / 8 + 32 * i) * SLICE + c4, st[i]);
+        }
+        __syncthreads();
+    }
+
+    float* dst = nullptr;
+    if (STATES) {
+        if (sg.u + sg.j < rows)
+            dst = p.seg_states + ((sg.u + sg.j) * (int64_t)p.H + h) * state_floats;
+    } else if (p.state_out && sg.j + 1 == sg.count) {
+        dst = p.state_out + ((size_t)sg.n * p.H + h) * state_floats;
+    }
+    if (dst) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const int d = tid / 8 + 32 * i;
+            store4(dst + (size_t)d * dz + col0 + c4, load4(S + d * SLICE + c4));
+        }
+    }
+}
+
+template <typename T, int DX>
+cudaError_t launch_pass(const LinPass& p, cudaStream_t stream) {
+    constexpr int smem = (int)pass_smem_bytes<DX>();
+    const int64_t most = (int64_t)p.total_T / p.seg_len;   // segments that are not a last one
+    const int64_t grid = (most + p.N) * p.H * (p.dz / SLICE);
+    if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
+    cudaError_t err;
+    if (most > 0) {
+        auto* k1 = lin_pass_kernel<T, DX, true>;
+        err = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (err != cudaSuccess) return err;
+        k1<<<(unsigned)grid, THREADS, smem, stream>>>(p);
+    }
+    auto* k2 = lin_pass_kernel<T, DX, false>;
+    err = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+    k2<<<(unsigned)grid, THREADS, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ decode
+// S = a S + k v^T, o = scale S^T q: the state is read and written once, so the
+// step is bound by 8 d_k d_v bytes per (row, head).  A CTA takes 32 columns:
+// 8 lanes cover a 128-byte piece of a state row, so that every warp request is
+// four full lines, and each thread has its d_k / 16 rows in flight at once.
+constexpr int DEC_THREADS = 128;
+
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(DEC_THREADS) lin_decode_kernel(LinDecode p) {
+    constexpr int STEP = DEC_THREADS / 8, ROWS = DK / STEP, slices = DV / 32;
+    __shared__ float sq[DK], sk[DK];
+    __shared__ float4 part[DEC_THREADS / 32][8];
+    const int tid = threadIdx.x, c = (blockIdx.x % slices) * 32 + (tid & 7) * 4;
+    const int64_t bh = blockIdx.x / slices;
+    const int h = (int)(bh % p.H);
+    const int64_t b = bh / p.H;
+    const int64_t slot = p.slots ? p.slots[b] : b;
+    T* o = static_cast<T*>(p.o) + bh * DV;
+    if (slot < 0 || slot >= p.pool_size) {
+        if (tid < 8) {
+            const float nan = __int_as_float(0x7fffffff);
+            store4(o + c, make_float4(nan, nan, nan, nan));
+        }
+        return;
+    }
+    float* st = p.state + (slot * p.H + h) * (int64_t)(DK * DV) + c;
+    float4 s[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+        s[i] = __ldcs(reinterpret_cast<const float4*>(st + (tid / 8 + STEP * i) * DV));
+    const float4 v = load4(static_cast<const T*>(p.v) + bh * DV + c);
+    if (tid < DK / 4) store4(sq + 4 * tid, load4(static_cast<const T*>(p.q) + bh * DK + 4 * tid));
+    else if (tid >= 64 && tid < 64 + DK / 4)
+        store4(sk + 4 * (tid - 64), load4(static_cast<const T*>(p.k) + bh * DK + 4 * (tid - 64)));
+    const float a = lin::decay_pow(p.log_decay[h], 1);
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int d = tid / 8 + STEP * i;
+        const float k = sk[d], q = sq[d];
+        s[i].x = a * s[i].x + k * v.x;
+        s[i].y = a * s[i].y + k * v.y;
+        s[i].z = a * s[i].z + k * v.z;
+        s[i].w = a * s[i].w + k * v.w;
+        __stcs(reinterpret_cast<float4*>(st + d * DV), s[i]);
+        acc.x += q * s[i].x; acc.y += q * s[i].y; acc.z += q * s[i].z; acc.w += q * s[i].w;
+    }
+#pragma unroll
+    for (int m = 8; m < 32; m <<= 1) {
+        acc.x += __shfl_xor_sync(0xffffffffu, acc.x, m);
+        acc.y += __shfl_xor_sync(0xffffffffu, acc.y, m);
+        acc.z += __shfl_xor_sync(0xffffffffu, acc.z, m);
+        acc.w += __shfl_xor_sync(0xffffffffu, acc.w, m);
+    }
+    if ((tid & 31) < 8) part[tid / 32][tid & 7] = acc;
+    __syncthreads();
+    if (tid < 8) {
+        float4 r = part[0][tid];
+#pragma unroll
+        for (int w = 1; w < DEC_THREADS / 32; ++w) {
+            r.x += part[w][tid].x; r.y += part[w][tid].y;
+            r.z += part[w][tid].z; r.w += part[w][tid].w;
+        }
+        store4(o + c, make_float4(p.scale * r.x, p.scale * r.y, p.scale * r.z, p.scale * r.w));
+    }
+}
+
+template <typename T, int DK, int DV>
+cudaError_t launch_decode(const LinDecode& p, cudaStream_t stream) {
+    const int64_t grid = (int64_t)p.B * p.H * (DV / 32);
+    if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
+    lin_decode_kernel<T, DK, DV><<<(unsigned)grid, DEC_THREADS, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T, int DK>
+cudaError_t decode_dv(const LinDecode& p, int d_v, cudaStream_t stream) {
+    switch (d_v) {
+        case 32: return launch_decode<T, DK, 32>(p, stream);
+        case 64: return launch_decode<T, DK, 64>(p, stream);
+        case 128: return launch_decode<T, DK, 128>(p, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+template <typename T>
+cudaError_t decode_dk(const LinDecode& p, int d_k, int d_v, cudaStream_t stream) {
+    switch (d_k) {
+        case 32: return decode_dv<T, 32>(p, d_v, stream);
+        case 64: return decode_dv<T, 64>(p, d_v, stream);
+        case 128: return decode_dv<T, 128>(p, d_v, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+template <typename T>
+cudaError_t pass_dx(const LinPass& p, cudaStream_t stream) {
+    switch (p.dx) {
+        case 32: return launch_pass<T, 32>(p, stream);
+        case 64: return launch_pass<T, 64>(p, stream);
+        case 128: return launch_pass<T, 128>(p, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+int32_t lin_segment_tokens(int32_t N, int32_t total_T, int32_t H, int ctas_per_pair, int sms) {
+    constexpr int64_t grain = 128;
+    if (sms <= 0) sms = 152;   // no device to ask: sizes for a whole GB300
+    const int64_t pairs = (int64_t)N * H * ctas_per_pair;
+    const int64_t cuts = sms / pairs;
+    if (cuts < 2) return INT32_MAX / grain * grain;
+    const int64_t len = ((int64_t)total_T + N * cuts - 1) / (N * cuts);
+    const int64_t seg = (len + grain - 1) / grain * grain;
+    return (int32_t)(seg < grain ? grain : seg);
+}
+
+cudaError_t launch_lin_pass(const LinPass& p, int dtype, cudaStream_t stream) {
+    return dtype == 0 ? pass_dx<float>(p, stream) : pass_dx<__nv_bfloat16>(p, stream);
+}
+
+cudaError_t launch_lin_decode(const LinDecode& p, int d_k, int d_v, int dtype,
+                              cudaStream_t stream) {
+    return dtype == 0 ? decode_dk<float>(p, d_k, d_v, stream)
+                      : decode_dk<__nv_bfloat16>(p, d_k, d_v, stream);
+}
+
+}  // namespace kda

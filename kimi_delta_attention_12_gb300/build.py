@@ -24,7 +24,8 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
 SOURCES = ["kda_api.cpp", "kda_recurrent.cu", "kda_state_io.cu", "kda_prefill_sm103.cu",
            "kda_noalloc.cu", "kda_short_conv.cu",
            "kda_backward.cu", "kda_bwd_chunked.cu",
-           "kda_lin_api.cpp", "kda_lin_attn.cu", "kda_norm_api.cpp", "kda_block_norm.cu"]
+           "kda_lin_api.cpp", "kda_lin_attn.cu", "kda_lin_sm103.cu",
+           "kda_norm_api.cpp", "kda_block_norm.cu"]
 
 
 def _nvcc() -> str:

@@ -51,6 +51,9 @@ int32_t lin_segment_tokens(int32_t N, int32_t total_T, int32_t H, int ctas_per_p
 // The pass on the CUDA cores, fp32 arithmetic: dx, dz in {32, 64, 128}, dtype
 // 0 = fp32, 1 = bf16.
 cudaError_t launch_lin_pass(const LinPass& p, int dtype, cudaStream_t stream);
+// The pass on the tensor cores: bf16, dx = dz = 128, total_T > 0.  A wait that
+// ran out leaves a nonzero status word.
+cudaError_t launch_lin_pass_tc(const LinPass& p, cudaStream_t stream);
 
 // One decode token per row, the state pool updated in place.
 struct LinDecode {

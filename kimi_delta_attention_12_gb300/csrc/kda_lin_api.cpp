@@ -29,10 +29,23 @@ int sm_count() {
     return sms;
 }
 
-// Both forms cut the sequences alike where they can, so that a workspace
-// serves either; dz is the width whose columns the CUDA-core form spreads.
-int32_t segment_tokens(int32_t N, int32_t total_T, int32_t H, int32_t dz) {
-    return kda::lin_segment_tokens(N, total_T, H, dz / 32, sm_count());
+// Whether a pass runs on the tensor cores.
+bool on_tensor_cores(int32_t d_k, int32_t d_v, kda_dtype dt, uint32_t flags, int32_t total_T) {
+    return dt == KDA_BF16 && d_k == 128 && d_v == 128 && !(flags & KDA_FLAG_RECURRENT) &&
+           total_T > 0;
+}
+
+// The tensor-core form works on a (sequence, head) pair with one CTA, the
+// CUDA-core form with one for each 32 columns of dz.
+int32_t segment_tokens(int32_t N, int32_t total_T, int32_t H, int32_t dz, bool tc) {
+    return kda::lin_segment_tokens(N, total_T, H, tc ? 1 : dz / 32, sm_count());
+}
+
+// The segment of the form that cuts finer, whose states need most room.
+int32_t finest_segment(int32_t N, int32_t total_T, int32_t H, int32_t d_k, int32_t d_v,
+                       kda_dtype dt) {
+    const int32_t dz = d_k < d_v ? d_k : d_v;
+    return segment_tokens(N, total_T, H, dz, on_tensor_cores(d_k, d_v, dt, 0, total_T));
 }
 
 size_t seg_state_bytes(int32_t total_T, int32_t H, int32_t dx, int32_t dz, int32_t seg_len) {
@@ -41,6 +54,11 @@ size_t seg_state_bytes(int32_t total_T, int32_t H, int32_t dx, int32_t dz, int32
 
 size_t state_bytes(int32_t N, int32_t H, int32_t d_k, int32_t d_v) {
     return (size_t)N * H * d_k * d_v * sizeof(float);
+}
+
+cudaError_t run(const kda::LinPass& p, bool tc, kda_dtype dt, cudaStream_t s) {
+    return tc ? kda::launch_lin_pass_tc(p, s)
+              : kda::launch_lin_pass(p, dt == KDA_F32 ? 0 : 1, s);
 }
 
 bool bad_sizes(int32_t N, int32_t total_T, int32_t H) { return N < 1 || H < 1 || total_T < 0; }
@@ -55,7 +73,7 @@ size_t kda_lin_prefill_workspace_bytes(int32_t N, int32_t total_T, int32_t H, in
         (dt != KDA_F32 && dt != KDA_BF16)) {
         return 0;
     }
-    const int32_t seg = segment_tokens(N, total_T, H, d_v);
+    const int32_t seg = finest_segment(N, total_T, H, d_k, d_v, dt);
     // the states of the segments, and a copy of the initial states for a call
     // that updates them in place
     size_t b = kHeader + seg_state_bytes(total_T, H, d_k, d_v, seg);
@@ -106,6 +124,7 @@ int kda_lin_prefill(const void* q, const void* k, const void* v, const float* lo
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
+    const bool tc = on_tensor_cores(d_k, d_v, dt, flags, total_T);
     if (cudaMemsetAsync(ws, 0, sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
     kda::LinPass p;
     memset(&p, 0, sizeof(p));
@@ -115,21 +134,21 @@ int kda_lin_prefill(const void* q, const void* k, const void* v, const float* lo
     p.cu_seqlens = cu_seqlens;
     p.status = reinterpret_cast<int32_t*>(ws);
     p.N = N; p.total_T = total_T; p.H = H; p.dx = d_k; p.dz = d_v;
-    p.seg_len = segment_tokens(N, total_T, H, d_v);
+    p.seg_len = segment_tokens(N, total_T, H, d_v, tc);
     p.seg_states = reinterpret_cast<float*>(ws + kHeader);
     p.out_scale = scale; p.kv_scale = 1.0f;
     if (initial_state && initial_state == final_state && total_T / p.seg_len > 0) {
         // the last segment may write its state before the first has read it
         float* copy = reinterpret_cast<float*>(
-            ws + kHeader + seg_state_bytes(total_T, H, d_k, d_v, p.seg_len));
+            ws + kHeader + seg_state_bytes(total_T, H, d_k, d_v,
+                                           finest_segment(N, total_T, H, d_k, d_v, dt)));
         if (cudaMemcpyAsync(copy, initial_state, nst, cudaMemcpyDeviceToDevice, s) !=
             cudaSuccess) {
             return KDA_ERR_CUDA;
         }
         p.state_in = copy;
     }
-    return kda::launch_lin_pass(p, dt == KDA_F32 ? 0 : 1, s) == cudaSuccess ? KDA_OK
-                                                                            : KDA_ERR_CUDA;
+    return run(p, tc, dt, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 int kda_lin_decode_step(const void* q, const void* k, const void* v, const float* log_decay,
@@ -173,9 +192,8 @@ size_t kda_lin_backward_workspace_bytes(int32_t N, int32_t total_T, int32_t H, i
         (dt != KDA_F32 && dt != KDA_BF16)) {
         return 0;
     }
-    const size_t a = seg_state_bytes(total_T, H, d_k, d_v, segment_tokens(N, total_T, H, d_v));
-    const size_t b = seg_state_bytes(total_T, H, d_k, d_v, segment_tokens(N, total_T, H, d_k));
-    return kHeader + (a > b ? a : b);
+    return kHeader + seg_state_bytes(total_T, H, d_k, d_v,
+                                     finest_segment(N, total_T, H, d_k, d_v, dt));
 }
 
 int kda_lin_backward(const void* q, const void* k, const void* v, const float* log_decay,
@@ -216,7 +234,7 @@ int kda_lin_backward(const void* q, const void* k, const void* v, const float* l
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     if (cudaMemsetAsync(ws, 0, sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
-    const int dtype = dt == KDA_F32 ? 0 : 1;
+    const bool tc = on_tensor_cores(d_k, d_v, dt, flags, total_T);
     kda::LinPass p;
     memset(&p, 0, sizeof(p));
     p.log_decay = log_decay;
@@ -230,21 +248,21 @@ int kda_lin_backward(const void* q, const void* k, const void* v, const float* l
         p.x = dO; p.y = v; p.z = k; p.out = dq; p.dx = d_v; p.dz = d_k;
         p.state_in = initial_state; p.state_in_turned = 1; p.state_out = nullptr;
         p.reverse = 0; p.out_scale = scale; p.kv_scale = 1.0f;
-        p.seg_len = segment_tokens(N, total_T, H, d_k);
-        err = kda::launch_lin_pass(p, dtype, s);
+        p.seg_len = segment_tokens(N, total_T, H, d_k, tc);
+        err = run(p, tc, dt, s);
         if (err != cudaSuccess) return KDA_ERR_CUDA;
         // dk_t = G_t v_t, G_t = scale q_t dO_t^T + a G_{t+1}: from the ends
         p.x = v; p.y = dO; p.z = q; p.out = dk;
         p.state_in = dS_final; p.reverse = 1; p.out_scale = 1.0f; p.kv_scale = scale;
-        err = kda::launch_lin_pass(p, dtype, s);
+        err = run(p, tc, dt, s);
         if (err != cudaSuccess) return KDA_ERR_CUDA;
     }
     // dv_t = G_t^T k_t; the state it ends with is dS_0
     p.x = k; p.y = q; p.z = dO; p.out = dv; p.dx = d_k; p.dz = d_v;
     p.state_in = dS_final; p.state_in_turned = 0; p.state_out = dS0;
     p.reverse = 1; p.out_scale = 1.0f; p.kv_scale = scale;
-    p.seg_len = segment_tokens(N, total_T, H, d_v);
-    err = kda::launch_lin_pass(p, dtype, s);
+    p.seg_len = segment_tokens(N, total_T, H, d_v, tc);
+    err = run(p, tc, dt, s);
     return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

@@ -12,9 +12,10 @@
 // bits), so that the state keeps fp32 sums of exact products: three products
 // on a tensor core that otherwise waits for memory.
 //
-// Roles: warps 0-3 turn P into P' and write the outputs (thread = token);
-// warps 4-7 split w Y and carry the state (thread = row of S); warp 8 issues
-// the TMA loads, warp 9 the products.
+// Roles (20 warps): 0-7 turn P into P' and write the outputs (thread = token;
+// each half takes half of the columns), 8-15 carry the state (thread = row of
+// S; half of the columns each) and split w Y (half of the tokens each), 16
+// issues the TMA loads, 17 the products, 18 the TMA stores.
 #include "kda_lin.h"
 
 #include <cuda.h>
@@ -33,7 +34,13 @@ using namespace sm103;
 
 constexpr int C = 128;                   // tokens per chunk = rows of a tile
 constexpr int D = 128;                   // dx = dz
-constexpr int THREADS = 320;
+constexpr int THREADS = 640;             // the pass
+constexpr int STATE_THREADS = 320;       // the segment states: 8 warps, and 8 and 9 to issue
+// Registers: 640 threads start with 96 each.  The warps that issue give theirs
+// above 56, the 8 that hold the state in registers take 112:
+// 128 (96 + 96 + 112 + 112 + 56) is below 640 x 96.
+constexpr int REGS_ISSUE = 56, REGS_STATE = 112;
+static_assert(128 * (2 * 96 + 2 * REGS_STATE + REGS_ISSUE) <= THREADS * 96, "register split");
 constexpr uint32_t HALF = C * 128;       // a tile's 64 columns: 128 rows of 128 bytes
 constexpr uint32_t TILE = 2 * HALF;
 constexpr int STAGES = 2;                // the pass: X, Y, Z per stage
@@ -44,21 +51,23 @@ static_assert(SM_S >= STATE_STAGES * 2 * TILE, "the states' stages end before th
 constexpr uint32_t SMEM = SM_TAB + 2048 + 1024;          // tables, alignment
 static_assert(SMEM <= 232448, "more shared memory than a CTA may have");
 
-// TMEM columns of the pass
-constexpr uint32_t TC_P = 0;             // P; P' (bf16 pairs) in its first 64 columns
-constexpr uint32_t TC_O = 128;           // P' Z
-constexpr uint32_t TC_U = 256;           // X S, then (w Y)^T Z
-constexpr uint32_t TC_W = 384;           // w Y: tokens 0-63 in three parts of 32 columns,
-                                         // tokens 64-127: first part, the others ...
-constexpr uint32_t TC_W2 = 64;           // ... where P was
+// TMEM columns of the pass.  P': 16 columns of bf16 pairs where each 32 columns
+// of P were; the 16 that this frees take parts of w Y.
+constexpr uint32_t TC_P = 0;
+constexpr uint32_t TC_O = 128;           // X S, scaled in place, then + P' Z
+constexpr uint32_t TC_U = 256;           // (w Y)^T Z
+constexpr uint32_t TC_W = 384;           // tokens 0-63: three parts of 32 columns
+constexpr uint32_t TC_W1 = 480;          // tokens 64-127: the first part,
+constexpr uint32_t TC_W2 = 16;           // the second (free columns of P's first half),
+constexpr uint32_t TC_W3 = 80;           // the third (of its second half)
 // and of the segment states
 constexpr uint32_t TS_U = 0;
 constexpr uint32_t TS_W = 128;           // two buffers of three parts of 64 columns
 
-static_assert((132 + 132) * 4 + 256 <= 2048, "tables and barriers");
+static_assert((132 + 132 + 128) * 4 + 256 <= 2048, "tables and barriers");
 
 struct Args {
-    CUtensorMap x, y, z;
+    CUtensorMap x, y, z, out;
     LinPass p;
 };
 
@@ -66,7 +75,9 @@ struct Bars {
     uint64_t full[STATE_STAGES];   // tiles of a stage are there
     uint64_t empty[STATE_STAGES];  // products on a stage are done
     uint64_t qk, o1, o2, u;        // P / X S / P' Z / (w Y)^T Z done
-    uint64_t p, s, o1r, wa, wb;    // P' / S copy / X S read / w Y first and second half written
+    uint64_t p, s, o1s, od;        // P' / S copy / X S scaled / outputs written
+    uint64_t xfree[2];             // the outputs have left the stage's X tile
+    uint64_t wa, wb;               // w Y first and second half written
     uint64_t w[2], wfree[2];       // segment states: w Y of a buffer written, read
     uint64_t fin;
     uint32_t tmem;
@@ -74,6 +85,26 @@ struct Bars {
 };
 
 static_assert(sizeof(Bars) <= 256, "barriers");
+
+// Bounded wait that sleeps in the barrier (up to ~1 ms at a time) instead of
+// polling: polls would take issue slots from the warps that work.  False on a
+// timeout or when the CTA gives up.
+__device__ __forceinline__ bool sleep_wait(Bars* b, uint64_t* bar, uint32_t parity) {
+    const uint32_t at = smem_u32(bar);
+    for (uint32_t i = 0; i < kSpinLimit; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(at), "r"(parity), "r"(1000000u)
+            : "memory");
+        if (ok) return true;
+        if (b->abort) return false;
+    }
+    return false;
+}
 
 __device__ __forceinline__ void give_up(const LinPass& p, Bars* b, int site) {
     atomicCAS(p.status, 0, site);
@@ -83,7 +114,7 @@ __device__ __forceinline__ void give_up(const LinPass& p, Bars* b, int site) {
 // One thread's bounded wait; on a timeout every role of the CTA leaves its loop.
 __device__ __forceinline__ bool wait1(Bars* b, uint64_t* bar, uint32_t parity, const LinPass& p,
                                       int site) {
-    if (mbar_wait(bar, parity, &b->abort)) return true;
+    if (sleep_wait(b, bar, parity)) return true;
     give_up(p, b, site);
     return false;
 }
@@ -91,7 +122,7 @@ __device__ __forceinline__ bool wait1(Bars* b, uint64_t* bar, uint32_t parity, c
 // The same for a whole warp: all lanes go on, or none.
 __device__ __forceinline__ bool wait_warp(Bars* b, uint64_t* bar, uint32_t parity,
                                           const LinPass& p, int site) {
-    const bool ok = mbar_wait(bar, parity, &b->abort);
+    const bool ok = sleep_wait(b, bar, parity);
     if (__all_sync(0xffffffffu, ok)) return true;
     give_up(p, b, site);
     return false;
@@ -104,53 +135,126 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// K-major operand: rows of 64 channels; k-step kk covers 16 channels.
-__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int kk) {
-    return smem_desc(tile + (kk >> 2) * HALF + (kk & 3) * 32, 16, 1024);
-}
-// MN-major operand: rows are the summed index; k-step kk covers 16 rows.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int kk) {
-    return smem_desc(tile + kk * 2048, HALF, 1024);
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// w Y of one row of S for 64 tokens, split into three bf16 parts: column pairs
-// of tokens to TMEM.  w: the weight of token 0, those of the others up (REV) or
-// down from there.  Rows past the chunk's end (another sequence's, maybe not
-// finite) count as zero; their weights are read from the table below.
-template <bool REV>
-__device__ __forceinline__ void split_w(const uint8_t* y, int r, int tok0, const float* w, float f,
+// The upper halves of a and b.
+__device__ __forceinline__ uint32_t cut(float a, float b) {
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+
+// Low words of the shared-memory descriptors of an operand tile; the steps of a
+// product add to the address in them.  One thread issues every product, so each
+// is kept to a few instructions.  The high word (128-byte swizzle, 1024 bytes
+// between groups of 8 rows) is the same for all.
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+// K-major: rows of 64 channels; k-step kk covers 16 channels.
+__device__ __forceinline__ uint32_t tile_k(uint32_t tile) { return tile >> 4 | 1u << 16; }
+__device__ __forceinline__ constexpr uint32_t step_k(int kk) {
+    return ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+}
+// MN-major: rows are the summed index; k-step kk covers 16 rows.
+__device__ __forceinline__ uint32_t tile_mn(uint32_t tile) { return tile >> 4 | (HALF >> 4) << 16; }
+__device__ __forceinline__ constexpr uint32_t step_mn(int kk) { return kk * 2048 >> 4; }
+
+// D (+)= A B of 128 x 128 x 16: A in shared memory, or in TMEM.
+template <bool ADD>
+__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint32_t b, uint32_t id) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %4};\n\t"
+        "mov.b64 b, {%2, %4};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(DESC_HI), "n"(ADD ? 1 : 0)
+        : "memory");
+}
+template <bool ADD>
+__device__ __forceinline__ void product_ta(uint32_t d, uint32_t a, uint32_t b, uint32_t id) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %4};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(DESC_HI), "n"(ADD ? 1 : 0)
+        : "memory");
+}
+
+// 16 TMEM lanes x 16 columns: register j of lane l holds row l / 4 + 8 (j & 1),
+// column 4 (j / 2) + l % 4.
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
+}
+
+// Four 8 x 8 matrices, transposed: register k of lane l holds rows 2 (l % 4)
+// and + 1, column l / 4 of matrix k, whose row i lane 8 k + i points to.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// w Y of this warp's 32 rows of S (TMEM lanes) for 32 tokens, split into three
+// bf16 parts: bits cut off twice, the rest rounded, so that the parts add up
+// to the fp32 product within 2^-24.  The tile is read transposed, 8 x 8 values
+// at a time, into the layout that TMEM takes 16 lanes at a time.  w: the weight
+// of token 0 of the chunk; rows past its end (another sequence's, maybe not
+// finite) count as zero, and their weights are read from the tables behind.
+__device__ __forceinline__ void split_w(uint32_t y, int quad, int tok0, const float* w, float f,
                                         int len, uint32_t hi, uint32_t mid, uint32_t lo) {
-    const uint8_t* col = y + (r >> 6) * HALF;
-    const uint32_t at = (r & 63) * 2;
+    const int lane = threadIdx.x & 31, row = lane & 7, mat = lane >> 3;
+    const int t0 = tok0 + 2 * (lane & 3);
+    float ws[4][2];
+    if (len == C) {
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
+        for (int j = 0; j < 4; ++j) {
+            const float2 v = *reinterpret_cast<const float2*>(w + t0 + 8 * j);
+            ws[j][0] = v.x * f;
+            ws[j][1] = v.y * f;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            ws[j][0] = w[t0 + 8 * j] * f;
+            ws[j][1] = w[t0 + 8 * j + 1] * f;
+        }
+    }
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+        const int chunk = (quad & 1) * 4 + 2 * half + (mat & 1);
+        const uint32_t at = y + (quad >> 1) * HALF + (tok0 + 8 * (mat >> 1) + row) * 128 +
+                            ((chunk ^ row) << 4);
         uint32_t h[8], m[8], l[8];
+        ldmatrix_x4_trans(at, h);
+        ldmatrix_x4_trans(at + 16 * 128, h + 4);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int s = tok0 + 16 * b + 2 * j;
-            const float w0 = w[REV ? s : -s], w1 = w[REV ? s + 1 : -s - 1];
-            const uint32_t k0 = *reinterpret_cast<const uint16_t*>(col + sw128(s, at));
-            const uint32_t k1 = *reinterpret_cast<const uint16_t*>(col + sw128(s + 1, at));
-            float x0 = __uint_as_float(k0 << 16) * (w0 * f);
-            float x1 = __uint_as_float(k1 << 16) * (w1 * f);
-            if (s >= len) x0 = 0.0f;
-            if (s + 1 >= len) x1 = 0.0f;
-            h[j] = pack(x0, x1);
+            float x0 = low(h[j]) * ws[j >> 1][0], x1 = high(h[j]) * ws[j >> 1][1];
+            if (len < C) {
+                if (t0 + 8 * (j >> 1) >= len) x0 = 0.0f;
+                if (t0 + 8 * (j >> 1) + 1 >= len) x1 = 0.0f;
+            }
+            h[j] = cut(x0, x1);
             x0 -= low(h[j]);
             x1 -= high(h[j]);
-            m[j] = pack(x0, x1);
+            m[j] = cut(x0, x1);
             l[j] = pack(x0 - low(m[j]), x1 - high(m[j]));
         }
-        tmem_st8(hi + 8 * b, h);
-        tmem_st8(mid + 8 * b, m);
-        tmem_st8(lo + 8 * b, l);
+        const uint32_t lanes = (uint32_t)half << 20;   // lane 16 of the warp's 32
+        tmem_st_16x128b_x4(hi + lanes, h);
+        tmem_st_16x128b_x4(mid + lanes, m);
+        tmem_st_16x128b_x4(lo + lanes, l);
     }
 }
 
 // Rows len .. 127 of a Z tile to zero: they meet zeros of P' and w Y, and may
 // hold another sequence's values, which need not be finite.
 __device__ __forceinline__ void zero_rows(uint8_t* z, int len, int tid) {
-    for (int i = tid; i < (C - len) * 16; i += 128) {
+    for (int i = tid; i < (C - len) * 16; i += 256) {
         const int row = len + (i >> 4), part = i & 15;
         *reinterpret_cast<uint4*>(z + (part >> 3) * HALF + row * 128 + (part & 7) * 16) =
             make_uint4(0, 0, 0, 0);
@@ -169,7 +273,8 @@ struct Cta {
     uint8_t* sm;
     Bars* b;
     float* lam;     // a^0 .. a^128
-    float* lamk;    // the same times kv_scale (behind lam: see split_w)
+    float* lamk;    // the same times kv_scale
+    float* wtab;    // weights of a whole chunk's tokens in the state
     lin::Segment sg;
     int h, chunks;
     float g;
@@ -182,14 +287,16 @@ __device__ __forceinline__ bool start(const Args& args, Cta& c) {
                                       ~(uintptr_t)1023);
     c.lam = reinterpret_cast<float*>(c.sm + SM_TAB);
     c.lamk = c.lam + 132;
-    c.b = reinterpret_cast<Bars*>(c.lamk + 132);
+    c.wtab = c.lamk + 132;
+    c.b = reinterpret_cast<Bars*>(c.wtab + 128);
     c.h = blockIdx.x % p.H;
     c.sg = lin::find_segment(p.cu_seqlens, p.N, p.total_T, p.seg_len, p.reverse,
                              blockIdx.x / p.H);
     return c.sg.n >= 0;
 }
 
-__device__ __forceinline__ void set_up(const Args& args, Cta& c) {
+// `issue`: the first of the two issuing warps.
+__device__ __forceinline__ void set_up(const Args& args, Cta& c, int issue) {
     const LinPass& p = args.p;
     const int tid = threadIdx.x;
     c.chunks = (int)((c.sg.t1 - c.sg.t0 + C - 1) / C);
@@ -198,21 +305,22 @@ __device__ __forceinline__ void set_up(const Args& args, Cta& c) {
         const float a = lin::decay_pow(c.g, tid);
         c.lam[tid] = a;
         c.lamk[tid] = a * p.kv_scale;
+        if (p.reverse ? tid > 0 : tid < C) c.wtab[p.reverse ? tid - 1 : C - 1 - tid] = a * p.kv_scale;
     }
-    if (tid == 288) {
+    if (tid == 32 * issue + 32) {
         Bars* b = c.b;
         for (int i = 0; i < STATE_STAGES; ++i) {
             mbar_init(&b->full[i], 1);
             mbar_init(&b->empty[i], 1);
         }
-        uint64_t* one[] = {&b->qk, &b->o1, &b->o2, &b->u, &b->wfree[0], &b->wfree[1], &b->fin};
-        uint64_t* all[] = {&b->p, &b->s, &b->o1r, &b->wa, &b->wb, &b->w[0], &b->w[1]};
+        uint64_t* one[] = {&b->xfree[0], &b->xfree[1], &b->qk, &b->o1, &b->o2, &b->u, &b->wfree[0], &b->wfree[1], &b->fin};
+        uint64_t* all[] = {&b->p, &b->s, &b->o1s, &b->od, &b->wa, &b->wb, &b->w[0], &b->w[1]};
         for (uint64_t* x : one) mbar_init(x, 1);
-        for (uint64_t* x : all) mbar_init(x, 128);
+        for (uint64_t* x : all) mbar_init(x, 256);
         b->abort = 0;
         fence_mbar_init();
     }
-    if (tid >> 5 == 8) {
+    if (tid >> 5 == issue) {
         tmem_alloc(&c.b->tmem, 512);
         tmem_relinquish();
         if ((tid & 31) == 0) {
@@ -226,12 +334,12 @@ __device__ __forceinline__ void set_up(const Args& args, Cta& c) {
     tc_fence_after();
 }
 
-__device__ __forceinline__ void finish(const Cta& c, uint32_t tmem) {
+__device__ __forceinline__ void finish(uint32_t tmem, int issue) {
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (threadIdx.x >> 5 == 8) tmem_dealloc(tmem, 512);
+    if (threadIdx.x >> 5 == issue) tmem_dealloc(tmem, 512);
 }
 
 // Token range of the pass's step i.
@@ -243,256 +351,370 @@ __device__ __forceinline__ int chunk_len(const Cta& c, int64_t tok) {
 }
 
 // ------------------------------------------------------------------ the pass
+template <int N>
+__device__ __forceinline__ void take_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void give_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <bool REV>
+__device__ __forceinline__ void issue_loads(const Args& args, const Cta& c) {
+    const LinPass& p = args.p;
+    Bars* b = c.b;
+    int issued = 0;
+    for (int i = 0; i < c.chunks; ++i) {
+        const int s = i & 1;
+        if (i >= STAGES && !wait1(b, &b->empty[s], ((i >> 1) - 1) & 1, p, 301)) break;
+        uint8_t* st = c.sm + s * 3 * TILE;
+        const int tok = (int)chunk_start(c, REV, i);
+        mbar_arrive_expect_tx(&b->full[s], 3 * TILE);
+        load_tile(&args.y, st + TILE, c.h, tok, &b->full[s]);
+        load_tile(&args.z, st + 2 * TILE, c.h, tok, &b->full[s]);
+        // (the expected bytes are all announced, so a give-up here still loads X)
+        if (i >= STAGES) wait1(b, &b->xfree[s], ((i >> 1) - 1) & 1, p, 315);
+        load_tile(&args.x, st, c.h, tok, &b->full[s]);
+        issued = i + 1;
+    }
+    for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
+        mbar_wait(&b->full[i & 1], (i >> 1) & 1, nullptr);   // no copy outlives the CTA
+}
+
+// The outputs of whole chunks, from the X tiles to memory.
+template <bool REV>
+__device__ __forceinline__ void issue_stores(const Args& args, const Cta& c) {
+    const LinPass& p = args.p;
+    Bars* b = c.b;
+    for (int i = 0; i < c.chunks; ++i) {
+        if (!wait1(b, &b->od, i & 1, p, 316)) break;
+        const int64_t tok = chunk_start(c, REV, i);
+        if (chunk_len(c, tok) == C) {
+            const uint8_t* tile = c.sm + (i & 1) * 3 * TILE;
+            tma_store_3d(&args.out, tile, 0, c.h, (int)tok);
+            tma_store_3d(&args.out, tile + HALF, 64, c.h, (int)tok);
+            bulk_commit();
+            bulk_wait<true>();
+        }
+        mbar_arrive(&b->xfree[i & 1]);
+    }
+    bulk_wait<false>();
+}
+
+// The products of all chunks.  The tensor core runs them in this order; what
+// may overwrite an operand waits for `u`, which follows every product before.
+__device__ __forceinline__ void issue_products(const LinPass& p, const Cta& c, uint32_t tmem) {
+    Bars* b = c.b;
+    constexpr uint32_t id_kk = idesc_bf16(D, D, 0, 0), id_km = idesc_bf16(D, D, 0, 1);
+    const uint32_t base = smem_u32(c.sm), state = tile_mn(base + SM_S);
+    const int n = c.chunks;
+    // steps whose chunk ends early: the last one in time
+    const int shorter = chunk_len(c, chunk_start(c, p.reverse, p.reverse ? 0 : n - 1)) < C
+                            ? (p.reverse ? 0 : n - 1)
+                            : -1;
+    for (int i = 0; i < n; ++i) {
+        const uint32_t ph = i & 1, tile = base + (i & 1) * 3 * TILE;
+        const uint32_t x = tile_k(tile), y = tile_k(tile + TILE), z = tile_mn(tile + 2 * TILE);
+        if (!wait1(b, &b->full[i & 1], (i >> 1) & 1, p, 302)) break;
+        if (i > 0 && !wait1(b, &b->u, (i - 1) & 1, p, 303)) break;
+        tc_fence_after();
+        product<false>(tmem + TC_P, x, y, id_kk);
+#pragma unroll
+        for (int kk = 1; kk < 8; ++kk)
+            product<true>(tmem + TC_P, x + step_k(kk), y + step_k(kk), id_kk);
+        mma_commit(&b->qk);
+        if (!wait1(b, &b->s, ph, p, 304)) break;
+        if (i > 0 && !wait1(b, &b->od, (i - 1) & 1, p, 314)) break;
+        tc_fence_after();
+        product<false>(tmem + TC_O, x, state, id_km);
+#pragma unroll
+        for (int kk = 1; kk < 8; ++kk)
+            product<true>(tmem + TC_O, x + step_k(kk), state + step_mn(kk), id_km);
+        mma_commit(&b->o1);
+        if (!wait1(b, &b->wa, ph, p, 305)) break;
+        // a short chunk's z rows past its end are zeroed before P' is handed over
+        if (i == shorter && !wait1(b, &b->p, ph, p, 306)) break;
+        tc_fence_after();
+        product_ta<false>(tmem + TC_U, tmem + TC_W + 64, z, id_km);
+        product_ta<true>(tmem + TC_U, tmem + TC_W + 32, z, id_km);
+        product_ta<true>(tmem + TC_U, tmem + TC_W, z, id_km);
+#pragma unroll
+        for (int kk = 1; kk < 4; ++kk)
+#pragma unroll
+            for (int w = 2; w >= 0; --w)
+                product_ta<true>(tmem + TC_U, tmem + TC_W + 32 * w + 8 * kk, z + step_mn(kk),
+                                 id_km);
+        if (!wait1(b, &b->p, ph, p, 307) || !wait1(b, &b->o1s, ph, p, 308)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+            product_ta<true>(tmem + TC_O, tmem + TC_P + 32 * (kk >> 1) + 8 * (kk & 1),
+                             z + step_mn(kk), id_km);
+        mma_commit(&b->o2);
+        if (!wait1(b, &b->wb, ph, p, 309)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            const uint32_t hole = 32 * (kk >> 1) + 8 * (kk & 1), zk = z + step_mn(kk + 4);
+            product_ta<true>(tmem + TC_U, tmem + TC_W3 + hole, zk, id_km);
+            product_ta<true>(tmem + TC_U, tmem + TC_W2 + hole, zk, id_km);
+            product_ta<true>(tmem + TC_U, tmem + TC_W1 + 8 * kk, zk, id_km);
+        }
+        mma_commit(&b->u);
+        mma_commit(&b->empty[i & 1]);
+    }
+    mma_commit(&b->fin);
+    mbar_wait(&b->fin, 0, nullptr);   // no product outlives the CTA
+}
+
+// 32 columns of P from column 32 q on, weighted by a^{|t - s|} kv_scale, as
+// bf16 pairs.  The weights are formed on the spot, 2^{g2 |t - s|}: their error
+// (2^-22 and that of the product, under |g2 (t - s)| 2^-24) is far below the
+// rounding to bf16 that follows, and a table in shared memory would wait for
+// the products' own reads of it.  MASKED: the block of the diagonal, and chunks
+// that end early.
+template <bool REV, bool MASKED>
+__device__ __forceinline__ void weigh(uint32_t col, int t, int q, int len, float g2, float kv) {
+    uint32_t r[2][16], w[16];
+    tmem_ld16(col, r[0]);
+    tmem_ld16(col + 16, r[1]);
+    tmem_wait_ld();
+    const float dt = (float)(t - 32 * q);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        float v[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int s = 2 * j + e;
+            const float d = REV ? (float)s - dt : dt - (float)s;
+            v[e] = __uint_as_float(r[j >> 3][s & 15]) * (exp2_approx(g2 * d) * kv);
+            if (MASKED) v[e] = d >= 0.0f && 32 * q + s < len ? v[e] : 0.0f;
+        }
+        w[j] = pack(v[0], v[1]);
+    }
+    tmem_st16(col, w);
+}
+
+// Warps 0-7: P' (columns 32 q with q even or odd) and the outputs (columns 64 grp on).
+template <bool REV>
+__device__ __forceinline__ void outputs(const LinPass& p, const Cta& c, uint32_t lanes) {
+    Bars* b = c.b;
+    const int t = threadIdx.x & 127, quad = (threadIdx.x >> 5) & 3, grp = threadIdx.x >> 7;
+    // log2 a, finite, so that a distance of 0 weighs 1 under every decay
+    const float g2 = c.g < -1e30f ? -1e30f : c.g * 1.44269504f;
+    for (int i = 0; i < c.chunks; ++i) {
+        const uint32_t ph = i & 1;
+        const int64_t tok = chunk_start(c, REV, i);
+        const int len = chunk_len(c, tok);
+        if (len < C) {
+            if (!wait_warp(b, &b->full[i & 1], (i >> 1) & 1, p, 310)) break;
+            zero_rows(c.sm + (i & 1) * 3 * TILE + 2 * TILE, len, threadIdx.x);
+        }
+        if (!wait_warp(b, &b->qk, ph, p, 311)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+            const int q = 2 * k + grp;
+            const uint32_t col = lanes + TC_P + 32 * q;
+            if ((REV ? q > quad : q < quad) && len == C) {
+                weigh<REV, false>(col, t, q, len, g2, p.kv_scale);
+            } else if (REV ? q >= quad : q <= quad) {
+                weigh<REV, true>(col, t, q, len, g2, p.kv_scale);
+            } else {
+                const uint32_t zero[16] = {};
+                tmem_st16(col, zero);
+            }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&b->p);
+
+        const float f = t < len ? c.lam[REV ? len - 1 - t : t + 1] : 0.0f;
+        const uint32_t o = lanes + TC_O + 64 * grp;
+        if (!wait_warp(b, &b->o1, ph, p, 312)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int q = 0; q < 4; q += 2) {
+            uint32_t r[2][16];
+            tmem_ld16(o + 16 * q, r[0]);
+            tmem_ld16(o + 16 * q + 16, r[1]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                r[j >> 4][j & 15] = __float_as_uint(f * __uint_as_float(r[j >> 4][j & 15]));
+            tmem_st16(o + 16 * q, r[0]);
+            tmem_st16(o + 16 * q + 16, r[1]);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&b->o1s);
+
+        // The outputs of a whole chunk leave through the X tile, which both
+        // products that read it are done with, as one TMA store: a row per thread
+        // written straight to memory would send 32 pieces of lines per warp store.
+        uint8_t* tile = c.sm + (i & 1) * 3 * TILE + grp * HALF;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
+                             ((size_t)(tok + t) * p.H + c.h) * D + 64 * grp;
+        const float m = p.out_scale;
+        if (!wait_warp(b, &b->o2, ph, p, 313)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int q = 0; q < 4; q += 2) {
+            uint32_t r[2][16];
+            tmem_ld16(o + 16 * q, r[0]);
+            tmem_ld16(o + 16 * q + 16, r[1]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = 8 * e + 2 * j;
+                    w[j] = pack(m * __uint_as_float(r[k >> 4][k & 15]),
+                                m * __uint_as_float(r[k >> 4][(k & 15) + 1]));
+                }
+                const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+                if (len == C) {
+                    *reinterpret_cast<uint4*>(tile + sw128(t, 16 * (2 * q + e))) = v;
+                } else if (t < len) {
+                    reinterpret_cast<uint4*>(out + 16 * q)[e] = v;
+                }
+            }
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        mbar_arrive(&b->od);
+    }
+}
+
+// Warps 8-15: the state (row r, columns 64 grp on) and w Y.
+template <bool REV>
+__device__ __forceinline__ void states(const LinPass& p, const Cta& c, uint32_t lanes) {
+    Bars* b = c.b;
+    constexpr int W = D / 2;
+    const int r = threadIdx.x & 127, quad = (threadIdx.x >> 5) & 3, grp = (threadIdx.x >> 7) & 1;
+    const size_t state_floats = (size_t)D * D;
+    float S[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) S[j] = 0.0f;
+    if (p.state_in) {
+        const float* s0 = p.state_in + ((size_t)c.sg.n * p.H + c.h) * state_floats;
+        if (p.state_in_turned) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) S[j] = s0[(size_t)(W * grp + j) * D + r];
+        } else {
+#pragma unroll
+            for (int j = 0; j < W; j += 4) {
+                const float4 v =
+                    *reinterpret_cast<const float4*>(s0 + (size_t)r * D + W * grp + j);
+                S[j] = v.x; S[j + 1] = v.y; S[j + 2] = v.z; S[j + 3] = v.w;
+            }
+        }
+    }
+    const int64_t rows = lin::seg_rows(p.total_T, p.seg_len);
+    for (int k = 0; k < c.sg.j && c.sg.u + k < rows; ++k) {   // join the segments before
+        int64_t a, e;
+        lin::seg_tokens(c.sg, k, p.seg_len, REV, a, e);
+        const float f = lin::decay_pow(c.g, e - a);
+        const float* u = p.seg_states + ((c.sg.u + k) * (int64_t)p.H + c.h) * state_floats +
+                         (size_t)r * D + W * grp;
+#pragma unroll
+        for (int j = 0; j < W; j += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(u + j);
+            S[j] = f * S[j] + v.x;
+            S[j + 1] = f * S[j + 1] + v.y;
+            S[j + 2] = f * S[j + 2] + v.z;
+            S[j + 3] = f * S[j + 3] + v.w;
+        }
+    }
+    uint8_t* copy = c.sm + SM_S + grp * HALF;
+    bool ok = true;
+    for (int i = 0; i < c.chunks; ++i) {
+        const uint32_t ph = i & 1;
+        const int len = chunk_len(c, chunk_start(c, REV, i));
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            uint4 v;
+            v.x = pack(S[8 * q], S[8 * q + 1]);
+            v.y = pack(S[8 * q + 2], S[8 * q + 3]);
+            v.z = pack(S[8 * q + 4], S[8 * q + 5]);
+            v.w = pack(S[8 * q + 6], S[8 * q + 7]);
+            *reinterpret_cast<uint4*>(copy + sw128(r, q * 16)) = v;
+        }
+        fence_proxy_async();
+        mbar_arrive(&b->s);
+        if (!(ok = wait_warp(b, &b->full[i & 1], (i >> 1) & 1, p, 320))) break;
+        const uint32_t y = smem_u32(c.sm) + (i & 1) * 3 * TILE + TILE;
+        const float* w = c.wtab + (REV ? 0 : C - len);
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+            if (k && !(ok = wait_warp(b, &b->p, ph, p, 321))) break;   // P has been read
+            tc_fence_after();
+            const uint32_t w1 = k ? TC_W1 + 16 * grp : TC_W + 16 * grp;
+            const uint32_t w2 = k ? TC_W2 + 32 * grp : TC_W + 32 + 16 * grp;
+            const uint32_t w3 = k ? TC_W3 + 32 * grp : TC_W + 64 + 16 * grp;
+            split_w(y, quad, 64 * k + 32 * grp, w, 1.0f, len, lanes + w1, lanes + w2, lanes + w3);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(k ? &b->wb : &b->wa);
+        }
+        if (!ok) break;
+        if (!(ok = wait_warp(b, &b->u, ph, p, 322))) break;
+        tc_fence_after();
+        const float f = c.lam[len];
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+            uint32_t v[2][16];
+            tmem_ld16(lanes + TC_U + 64 * grp + 16 * q, v[0]);
+            tmem_ld16(lanes + TC_U + 64 * grp + 16 * q + 16, v[1]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                S[16 * q + j] = f * S[16 * q + j] + __uint_as_float(v[j >> 4][j & 15]);
+        }
+        tc_fence_before();
+    }
+    if (ok && p.state_out && c.sg.j + 1 == c.sg.count) {
+        float* dst = p.state_out + ((size_t)c.sg.n * p.H + c.h) * state_floats + (size_t)r * D +
+                     W * grp;
+#pragma unroll
+        for (int j = 0; j < W; j += 4)
+            *reinterpret_cast<float4*>(dst + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+    }
+}
+
 template <bool REV>
 __global__ void __launch_bounds__(THREADS, 1) lin_pass_tc_kernel(const __grid_constant__ Args args) {
     const LinPass& p = args.p;
     Cta c;
     if (!start(args, c)) return;
-    set_up(args, c);
-    Bars* b = c.b;
-    const uint32_t tmem = b->tmem;
-    const int tid = threadIdx.x, warp = tid >> 5, n = c.chunks;
+    set_up(args, c, 16);
+    const uint32_t tmem = c.b->tmem;
+    const int warp = threadIdx.x >> 5;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // this warp's 32 TMEM lanes
-
-    if (warp == 8) {
-        if ((tid & 31) == 0) {
-            int issued = 0;
-            for (int i = 0; i < n; ++i) {
-                const int s = i & 1;
-                if (i >= STAGES && !wait1(b, &b->empty[s], ((i >> 1) - 1) & 1, p, 301)) break;
-                uint8_t* st = c.sm + s * 3 * TILE;
-                const int tok = (int)chunk_start(c, REV, i);
-                mbar_arrive_expect_tx(&b->full[s], 3 * TILE);
-                load_tile(&args.x, st, c.h, tok, &b->full[s]);
-                load_tile(&args.y, st + TILE, c.h, tok, &b->full[s]);
-                load_tile(&args.z, st + 2 * TILE, c.h, tok, &b->full[s]);
-                issued = i + 1;
-            }
-            for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
-                mbar_wait(&b->full[i & 1], (i >> 1) & 1, nullptr);   // no copy outlives the CTA
+    if (warp >= 16) {
+        give_registers<REGS_ISSUE>();
+        if ((threadIdx.x & 31) == 0) {
+            if (warp == 16) issue_loads<REV>(args, c);
+            if (warp == 17) issue_products(p, c, tmem);
+            if (warp == 18) issue_stores<REV>(args, c);
         }
-    } else if (warp == 9) {
-        if ((tid & 31) == 0) {
-            const uint32_t id_kk = idesc_bf16(D, D, 0, 0), id_km = idesc_bf16(D, D, 0, 1);
-            const uint32_t base = smem_u32(c.sm), sb = base + SM_S;
-            for (int i = 0; i < n; ++i) {
-                const uint32_t ph = i & 1, x = base + (i & 1) * 3 * TILE, y = x + TILE,
-                               z = y + TILE;
-                if (!wait1(b, &b->full[i & 1], (i >> 1) & 1, p, 302)) break;
-                if (i > 0 && !wait1(b, &b->u, (i - 1) & 1, p, 303)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_bf16(tmem + TC_P, desc_k(x, kk), desc_k(y, kk), id_kk, kk > 0);
-                mma_commit(&b->qk);
-                if (!wait1(b, &b->s, ph, p, 304)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_bf16(tmem + TC_U, desc_k(x, kk), desc_mn(sb, kk), id_km, kk > 0);
-                mma_commit(&b->o1);
-                if (!wait1(b, &b->p, ph, p, 305)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_bf16_ta(tmem + TC_O, tmem + TC_P + 8 * kk, desc_mn(z, kk), id_km, kk > 0);
-                mma_commit(&b->o2);
-                if (!wait1(b, &b->o1r, ph, p, 306)) break;
-                if (!wait1(b, &b->wa, ph, p, 307)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-                    for (int part = 2; part >= 0; --part)
-                        mma_bf16_ta(tmem + TC_U, tmem + TC_W + 32 * part + 8 * kk, desc_mn(z, kk),
-                                    id_km, kk > 0 || part < 2);
-                if (!wait1(b, &b->wb, ph, p, 308)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    mma_bf16_ta(tmem + TC_U, tmem + TC_W2 + 32 + 8 * kk, desc_mn(z, kk + 4), id_km,
-                                1);
-                    mma_bf16_ta(tmem + TC_U, tmem + TC_W2 + 8 * kk, desc_mn(z, kk + 4), id_km, 1);
-                    mma_bf16_ta(tmem + TC_U, tmem + TC_W + 96 + 8 * kk, desc_mn(z, kk + 4), id_km,
-                                1);
-                }
-                mma_commit(&b->u);
-                mma_commit(&b->empty[i & 1]);
-            }
-            mma_commit(&b->fin);
-            mbar_wait(&b->fin, 0, nullptr);   // no product outlives the CTA
-        }
-    } else if (warp < 4) {
-        const int t = tid;
-        for (int i = 0; i < n; ++i) {
-            const uint32_t ph = i & 1;
-            const int64_t tok = chunk_start(c, REV, i);
-            const int len = chunk_len(c, tok);
-            if (len < C) {
-                if (!wait_warp(b, &b->full[i & 1], (i >> 1) & 1, p, 310)) break;
-                zero_rows(c.sm + (i & 1) * 3 * TILE + 2 * TILE, len, tid);
-            }
-            if (!wait_warp(b, &b->qk, ph, p, 311)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {     // 32 columns at a time, written where they were read
-                uint32_t w[16];
-                if (REV ? q >= warp : q <= warp) {
-                    uint32_t r[2][16];
-                    tmem_ld16(lanes + TC_P + 32 * q, r[0]);
-                    tmem_ld16(lanes + TC_P + 32 * q + 16, r[1]);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float v[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int s = 32 * q + 2 * j + e, d = REV ? s - t : t - s;
-                            const float f = c.lamk[d & 127];
-                            v[e] = d >= 0 && s < len
-                                       ? __uint_as_float(r[j >> 3][2 * (j & 7) + e]) * f
-                                       : 0.0f;
-                        }
-                        w[j] = pack(v[0], v[1]);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) w[j] = 0;
-                }
-                tmem_st16(lanes + TC_P + 16 * q, w);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&b->p);
-
-            if (!wait_warp(b, &b->o1, ph, p, 312)) break;
-            tc_fence_after();
-            uint32_t o1[8][16];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) tmem_ld16(lanes + TC_U + 16 * q, o1[q]);
-            tmem_wait_ld();
-            tc_fence_before();
-            mbar_arrive(&b->o1r);
-            const float m = p.out_scale;
-            const float f = t < len ? m * c.lam[REV ? len - 1 - t : t + 1] : 0.0f;
-            __nv_bfloat16* out =
-                static_cast<__nv_bfloat16*>(p.out) + ((size_t)(tok + t) * p.H + c.h) * D;
-            if (!wait_warp(b, &b->o2, ph, p, 313)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                uint32_t r[16], w[8];
-                tmem_ld16(lanes + TC_O + 16 * q, r);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    w[j] = pack(f * __uint_as_float(o1[q][2 * j]) + m * __uint_as_float(r[2 * j]),
-                                f * __uint_as_float(o1[q][2 * j + 1]) +
-                                    m * __uint_as_float(r[2 * j + 1]));
-                if (t < len) {
-                    uint4* dst = reinterpret_cast<uint4*>(out + 16 * q);
-                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                }
-            }
-            tc_fence_before();
-        }
+    } else if (warp < 8) {
+        outputs<REV>(p, c, lanes);
     } else {
-        const int r = tid - 128;      // row of the state
-        float S[D];
-        const size_t state_floats = (size_t)D * D;
-#pragma unroll
-        for (int j = 0; j < D; ++j) S[j] = 0.0f;
-        if (p.state_in) {
-            const float* s0 = p.state_in + ((size_t)c.sg.n * p.H + c.h) * state_floats;
-            if (p.state_in_turned) {
-#pragma unroll
-                for (int j = 0; j < D; ++j) S[j] = s0[(size_t)j * D + r];
-            } else {
-#pragma unroll
-                for (int j = 0; j < D; j += 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(s0 + (size_t)r * D + j);
-                    S[j] = v.x; S[j + 1] = v.y; S[j + 2] = v.z; S[j + 3] = v.w;
-                }
-            }
-        }
-        const int64_t rows = lin::seg_rows(p.total_T, p.seg_len);
-        for (int k = 0; k < c.sg.j && c.sg.u + k < rows; ++k) {   // join the segments before
-            int64_t a, e;
-            lin::seg_tokens(c.sg, k, p.seg_len, REV, a, e);
-            const float f = lin::decay_pow(c.g, e - a);
-            const float* u = p.seg_states + ((c.sg.u + k) * (int64_t)p.H + c.h) * state_floats +
-                             (size_t)r * D;
-#pragma unroll
-            for (int j = 0; j < D; j += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(u + j);
-                S[j] = f * S[j] + v.x;
-                S[j + 1] = f * S[j + 1] + v.y;
-                S[j + 2] = f * S[j + 2] + v.z;
-                S[j + 3] = f * S[j + 3] + v.w;
-            }
-        }
-        bool ok = true;
-        for (int i = 0; i < n; ++i) {
-            const uint32_t ph = i & 1;
-            const int len = chunk_len(c, chunk_start(c, REV, i));
-            uint8_t* sbuf = c.sm + SM_S;
-#pragma unroll
-            for (int q = 0; q < 16; ++q) {
-                uint4 v;
-                v.x = pack(S[8 * q], S[8 * q + 1]);
-                v.y = pack(S[8 * q + 2], S[8 * q + 3]);
-                v.z = pack(S[8 * q + 4], S[8 * q + 5]);
-                v.w = pack(S[8 * q + 6], S[8 * q + 7]);
-                *reinterpret_cast<uint4*>(sbuf + (q >> 3) * HALF + sw128(r, (q & 7) * 16)) = v;
-            }
-            fence_proxy_async();
-            mbar_arrive(&b->s);
-            if (!(ok = wait_warp(b, &b->full[i & 1], (i >> 1) & 1, p, 320))) break;
-            const uint8_t* y = c.sm + (i & 1) * 3 * TILE + TILE;
-            const float* w = c.lamk + (REV ? 1 : len - 1);
-            split_w<REV>(y, r, 0, w, 1.0f, len, lanes + TC_W, lanes + TC_W + 32, lanes + TC_W + 64);
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&b->wa);
-            if (!(ok = wait_warp(b, &b->p, ph, p, 321))) break;   // P has been read
-            tc_fence_after();
-            split_w<REV>(y, r, 64, w, 1.0f, len, lanes + TC_W + 96, lanes + TC_W2,
-                         lanes + TC_W2 + 32);
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&b->wb);
-            if (!(ok = wait_warp(b, &b->u, ph, p, 322))) break;
-            tc_fence_after();
-            const float f = c.lam[len];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                uint32_t v[16];
-                tmem_ld16(lanes + TC_U + 16 * q, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    S[16 * q + j] = f * S[16 * q + j] + __uint_as_float(v[j]);
-            }
-            tc_fence_before();
-        }
-        if (ok && p.state_out && c.sg.j + 1 == c.sg.count) {
-            float* dst = p.state_out + ((size_t)c.sg.n * p.H + c.h) * state_floats + (size_t)r * D;
-#pragma unroll
-            for (int j = 0; j < D; j += 4)
-                *reinterpret_cast<float4*>(dst + j) =
-                    make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
-        }
+        take_registers<REGS_STATE>();
+        states<REV>(p, c, lanes);
     }
-    finish(c, tmem);
+    finish(tmem, 16);
 }
 
 // ------------------------------------------------- the state a segment adds
 // sum_j a^{tokens from j to the segment's end} kv_scale y_j z_j^T, accumulated in TMEM
-// over the whole segment: the weights are taken to its end at once.  The two
-// groups of four warps split w Y of every other chunk.
+// over the whole segment: the weights are taken to its end at once.  Eight
+// warps split w Y into one of two buffers while the products read the other.
 template <bool REV>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(STATE_THREADS, 1)
 lin_states_tc_kernel(const __grid_constant__ Args args) {
     const LinPass& p = args.p;
     Cta c;
@@ -500,7 +722,7 @@ lin_states_tc_kernel(const __grid_constant__ Args args) {
         c.sg.u + c.sg.j >= lin::seg_rows(p.total_T, p.seg_len)) {
         return;
     }
-    set_up(args, c);
+    set_up(args, c, 8);
     Bars* b = c.b;
     const uint32_t tmem = b->tmem;
     const int tid = threadIdx.x, warp = tid >> 5, n = c.chunks;
@@ -523,20 +745,27 @@ lin_states_tc_kernel(const __grid_constant__ Args args) {
         }
     } else if (warp == 9) {
         if ((tid & 31) == 0) {
-            const uint32_t id = idesc_bf16(D, D, 0, 1);
+            constexpr uint32_t id = idesc_bf16(D, D, 0, 1);
             for (int i = 0; i < n; ++i) {
                 const int s = i % STATE_STAGES;
-                const uint32_t z = smem_u32(c.sm) + s * 2 * TILE + TILE;
+                const uint32_t z = tile_mn(smem_u32(c.sm) + s * 2 * TILE + TILE);
                 const uint32_t w = tmem + TS_W + 192 * (i & 1);
                 if (!wait1(b, &b->full[s], (i / STATE_STAGES) & 1, p, 332)) break;
                 if (!wait1(b, &b->w[i & 1], (i >> 1) & 1, p, 333)) break;
                 tc_fence_after();
+                if (i == 0) {
+                    product_ta<false>(tmem + TS_U, w + 128, z, id);
+                } else {
+                    product_ta<true>(tmem + TS_U, w + 128, z, id);
+                }
+                product_ta<true>(tmem + TS_U, w + 64, z, id);
+                product_ta<true>(tmem + TS_U, w, z, id);
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
+                for (int kk = 1; kk < 8; ++kk)
 #pragma unroll
                     for (int part = 2; part >= 0; --part)
-                        mma_bf16_ta(tmem + TS_U, w + 64 * part + 8 * kk, desc_mn(z, kk), id,
-                                    i > 0 || kk > 0 || part < 2);
+                        product_ta<true>(tmem + TS_U, w + 64 * part + 8 * kk, z + step_mn(kk),
+                                         id);
                 mma_commit(&b->wfree[i & 1]);
                 mma_commit(&b->empty[s]);
             }
@@ -545,34 +774,36 @@ lin_states_tc_kernel(const __grid_constant__ Args args) {
         }
     } else {
         const int r = tid & 127, grp = tid >> 7;
-        const uint32_t w = lanes + TS_W + 192 * grp;
         bool ok = true;
-        for (int i = grp; i < n; i += 2) {
-            const int s = i % STATE_STAGES;
+        for (int i = 0; i < n; ++i) {
+            const int s = i % STATE_STAGES, buf = i & 1;
             const int64_t tok = chunk_start(c, REV, i);
             const int len = chunk_len(c, tok);
             const float f = lin::decay_pow(c.g, REV ? tok - c.sg.t0 : c.sg.t1 - (tok + len));
             if (!(ok = wait_warp(b, &b->full[s], (i / STATE_STAGES) & 1, p, 334))) break;
-            if (i >= 2 && !(ok = wait_warp(b, &b->wfree[grp], ((i >> 1) - 1) & 1, p, 335))) break;
+            if (i >= 2 && !(ok = wait_warp(b, &b->wfree[buf], ((i >> 1) - 1) & 1, p, 335))) break;
             tc_fence_after();
             uint8_t* y = c.sm + s * 2 * TILE;
-            if (len < C) zero_rows(y + TILE, len, r);
-            const float* wt = c.lamk + (REV ? 1 : len - 1);
-            split_w<REV>(y, r, 0, wt, f, len, w, w + 64, w + 128);
-            split_w<REV>(y, r, 64, wt, f, len, w + 32, w + 96, w + 160);
+            if (len < C) zero_rows(y + TILE, len, tid);
+            const float* wt = c.wtab + (REV ? 0 : C - len);
+            const uint32_t w = lanes + TS_W + 192 * buf + 32 * grp;
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k)
+                split_w(smem_u32(y), warp & 3, 64 * grp + 32 * k, wt, f, len, w + 16 * k,
+                        w + 64 + 16 * k, w + 128 + 16 * k);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&b->w[grp]);
+            mbar_arrive(&b->w[buf]);
         }
-        if (grp == 1 && ok && wait_warp(b, &b->fin, 0, p, 336)) {
+        if (ok && wait_warp(b, &b->fin, 0, p, 336)) {
             tc_fence_after();
             float* dst = p.seg_states +
                          ((c.sg.u + c.sg.j) * (int64_t)p.H + c.h) * (int64_t)(D * D) +
-                         (size_t)r * D;
+                         (size_t)r * D + 64 * grp;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < 4; ++q) {
                 uint32_t v[16];
-                tmem_ld16(lanes + TS_U + 16 * q, v);
+                tmem_ld16(lanes + TS_U + 64 * grp + 16 * q, v);
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 16; j += 4)
@@ -581,7 +812,7 @@ lin_states_tc_kernel(const __grid_constant__ Args args) {
             }
         }
     }
-    finish(c, tmem);
+    finish(tmem, 8);
 }
 
 template <bool REV>
@@ -591,7 +822,7 @@ cudaError_t launch(const Args& args, unsigned grid, bool cut, cudaStream_t strea
         err = cudaFuncSetAttribute(lin_states_tc_kernel<REV>,
                                    cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
         if (err != cudaSuccess) return err;
-        lin_states_tc_kernel<REV><<<grid, THREADS, SMEM, stream>>>(args);
+        lin_states_tc_kernel<REV><<<grid, STATE_THREADS, SMEM, stream>>>(args);
     }
     err = cudaFuncSetAttribute(lin_pass_tc_kernel<REV>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
@@ -608,7 +839,8 @@ cudaError_t launch_lin_pass_tc(const LinPass& p, cudaStream_t stream) {
     args.p = p;
     if (!make_row_map(&args.x, p.x, p.total_T, p.H, C) ||
         !make_row_map(&args.y, p.y, p.total_T, p.H, C) ||
-        !make_row_map(&args.z, p.z, p.total_T, p.H, C)) {
+        !make_row_map(&args.z, p.z, p.total_T, p.H, C) ||
+        !make_row_map(&args.out, p.out, p.total_T, p.H, C)) {
         return cudaErrorInvalidValue;
     }
     const int64_t most = (int64_t)p.total_T / p.seg_len;

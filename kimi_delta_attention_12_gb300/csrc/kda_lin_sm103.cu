@@ -132,6 +132,45 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
+// Two fp32 values in one register pair and the packed operations on them.
+__device__ __forceinline__ uint64_t two(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void apart(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t two(uint32_t a, uint32_t b) {
+    return two(__uint_as_float(a), __uint_as_float(b));
+}
+__device__ __forceinline__ uint32_t pack(uint64_t v) {
+    float a, b;
+    apart(v, a, b);
+    return pack(a, b);
+}
+
+// One arrival for the calling warp, behind what all of its lanes did.
+__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
@@ -144,6 +183,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // The upper halves of a and b.
 __device__ __forceinline__ uint32_t cut(float a, float b) {
     return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+
+__device__ __forceinline__ float upper(float a) {
+    return __uint_as_float(__float_as_uint(a) & 0xffff0000u);
 }
 
 // Low words of the shared-memory descriptors of an operand tile; the steps of a
@@ -208,21 +251,10 @@ __device__ __forceinline__ void split_w(uint32_t y, int quad, int tok0, const fl
                                         int len, uint32_t hi, uint32_t mid, uint32_t lo) {
     const int lane = threadIdx.x & 31, row = lane & 7, mat = lane >> 3;
     const int t0 = tok0 + 2 * (lane & 3);
-    float ws[4][2];
-    if (len == C) {
+    uint64_t ws[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 v = *reinterpret_cast<const float2*>(w + t0 + 8 * j);
-            ws[j][0] = v.x * f;
-            ws[j][1] = v.y * f;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            ws[j][0] = w[t0 + 8 * j] * f;
-            ws[j][1] = w[t0 + 8 * j + 1] * f;
-        }
-    }
+    for (int j = 0; j < 4; ++j)   // (single loads: a short chunk's table starts anywhere)
+        ws[j] = mul2(two(w[t0 + 8 * j], w[t0 + 8 * j + 1]), two(f, f));
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
         const int chunk = (quad & 1) * 4 + 2 * half + (mat & 1);
@@ -233,16 +265,18 @@ __device__ __forceinline__ void split_w(uint32_t y, int quad, int tok0, const fl
         ldmatrix_x4_trans(at + 16 * 128, h + 4);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            float x0 = low(h[j]) * ws[j >> 1][0], x1 = high(h[j]) * ws[j >> 1][1];
+            uint64_t x = mul2(two(low(h[j]), high(h[j])), ws[j >> 1]);
+            float x0, x1;
+            apart(x, x0, x1);
             if (len < C) {
                 if (t0 + 8 * (j >> 1) >= len) x0 = 0.0f;
                 if (t0 + 8 * (j >> 1) + 1 >= len) x1 = 0.0f;
             }
             h[j] = cut(x0, x1);
-            x0 -= low(h[j]);
-            x1 -= high(h[j]);
+            x = sub2(two(x0, x1), two(upper(x0), upper(x1)));
+            apart(x, x0, x1);
             m[j] = cut(x0, x1);
-            l[j] = pack(x0 - low(m[j]), x1 - high(m[j]));
+            l[j] = pack(sub2(x, two(upper(x0), upper(x1))));
         }
         const uint32_t lanes = (uint32_t)half << 20;   // lane 16 of the warp's 32
         tmem_st_16x128b_x4(hi + lanes, h);
@@ -316,7 +350,7 @@ __device__ __forceinline__ void set_up(const Args& args, Cta& c, int issue) {
         uint64_t* one[] = {&b->xfree[0], &b->xfree[1], &b->qk, &b->o1, &b->o2, &b->u, &b->wfree[0], &b->wfree[1], &b->fin};
         uint64_t* all[] = {&b->p, &b->s, &b->o1s, &b->od, &b->wa, &b->wb, &b->w[0], &b->w[1]};
         for (uint64_t* x : one) mbar_init(x, 1);
-        for (uint64_t* x : all) mbar_init(x, 256);
+        for (uint64_t* x : all) mbar_init(x, 8);   // warps
         b->abort = 0;
         fence_mbar_init();
     }
@@ -468,30 +502,32 @@ __device__ __forceinline__ void issue_products(const LinPass& p, const Cta& c, u
     mbar_wait(&b->fin, 0, nullptr);   // no product outlives the CTA
 }
 
-// 32 columns of P from column 32 q on, weighted by a^{|t - s|} kv_scale, as
-// bf16 pairs.  The weights are formed on the spot, 2^{g2 |t - s|}: their error
-// (2^-22 and that of the product, under |g2 (t - s)| 2^-24) is far below the
-// rounding to bf16 that follows, and a table in shared memory would wait for
-// the products' own reads of it.  MASKED: the block of the diagonal, and chunks
-// that end early.
+// 32 columns of P, as bf16 pairs, column s weighted by 2^{g2 |t - s| + c}.  The
+// weights are formed on the spot, as 2^{base + slope s}: their error (2^-22 and
+// that of the exponent, at most 31 |g2| 2^-24) is far below the rounding to bf16
+// that follows, and a table in shared memory would wait for the products' own
+// reads of it.  MASKED: rows `t`, counted from the block's first column, take
+// columns up to (or from) their own and below `len`.
 template <bool REV, bool MASKED>
-__device__ __forceinline__ void weigh(uint32_t col, int t, int q, int len, float g2, float kv) {
+__device__ __forceinline__ void weigh(uint32_t col, float base, float slope, int t, int len) {
     uint32_t r[2][16], w[16];
     tmem_ld16(col, r[0]);
     tmem_ld16(col + 16, r[1]);
     tmem_wait_ld();
-    const float dt = (float)(t - 32 * q);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-        float v[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int s = 2 * j + e;
-            const float d = REV ? (float)s - dt : dt - (float)s;
-            v[e] = __uint_as_float(r[j >> 3][s & 15]) * (exp2_approx(g2 * d) * kv);
-            if (MASKED) v[e] = d >= 0.0f && 32 * q + s < len ? v[e] : 0.0f;
+        const int s = 2 * j;
+        uint64_t v = mul2(two(r[j >> 3][s & 15], r[j >> 3][(s & 15) + 1]),
+                          two(exp2_approx(fmaf(slope, (float)s, base)),
+                              exp2_approx(fmaf(slope, (float)(s + 1), base))));
+        if (MASKED) {
+            float v0, v1;
+            apart(v, v0, v1);
+            if ((REV ? s < t : s > t) || s >= len) v0 = 0.0f;
+            if ((REV ? s + 1 < t : s + 1 > t) || s + 1 >= len) v1 = 0.0f;
+            v = two(v0, v1);
         }
-        w[j] = pack(v[0], v[1]);
+        w[j] = pack(v);
     }
     tmem_st16(col, w);
 }
@@ -501,8 +537,15 @@ template <bool REV>
 __device__ __forceinline__ void outputs(const LinPass& p, const Cta& c, uint32_t lanes) {
     Bars* b = c.b;
     const int t = threadIdx.x & 127, quad = (threadIdx.x >> 5) & 3, grp = threadIdx.x >> 7;
-    // log2 a, finite, so that a distance of 0 weighs 1 under every decay
-    const float g2 = c.g < -1e30f ? -1e30f : c.g * 1.44269504f;
+    // The exponent of a weight: slope s + base.  log2 a is kept above -128, where a
+    // distance of one already weighs nothing (2^-128 is no fp32 of full precision),
+    // so that a distance of zero weighs 1 under every decay.  The pass's two scales
+    // go into the weights and, once more, into X S; their sign into the outputs.
+    const float g2 = c.g < -88.0f ? -128.0f : c.g * 1.44269504f, slope = REV ? g2 : -g2;
+    const float scale = p.out_scale * p.kv_scale;
+    const float c2 = log2f(fabsf(scale));
+    const uint32_t flip = scale < 0.0f ? 0x80008000u : 0u;
+    const float m = scale < 0.0f ? -p.out_scale : p.out_scale;
     for (int i = 0; i < c.chunks; ++i) {
         const uint32_t ph = i & 1;
         const int64_t tok = chunk_start(c, REV, i);
@@ -517,10 +560,12 @@ __device__ __forceinline__ void outputs(const LinPass& p, const Cta& c, uint32_t
         for (int k = 0; k < 2; ++k) {
             const int q = 2 * k + grp;
             const uint32_t col = lanes + TC_P + 32 * q;
+            const int tq = t - 32 * q;
+            const float base = fmaf(-slope, (float)tq, c2);
             if ((REV ? q > quad : q < quad) && len == C) {
-                weigh<REV, false>(col, t, q, len, g2, p.kv_scale);
+                weigh<REV, false>(col, base, slope, tq, C);
             } else if (REV ? q >= quad : q <= quad) {
-                weigh<REV, true>(col, t, q, len, g2, p.kv_scale);
+                weigh<REV, true>(col, base, slope, tq, len - 32 * q);
             } else {
                 const uint32_t zero[16] = {};
                 tmem_st16(col, zero);
@@ -528,9 +573,9 @@ __device__ __forceinline__ void outputs(const LinPass& p, const Cta& c, uint32_t
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&b->p);
+        arrive_warp(&b->p);
 
-        const float f = t < len ? c.lam[REV ? len - 1 - t : t + 1] : 0.0f;
+        const float f = t < len ? m * c.lam[REV ? len - 1 - t : t + 1] : 0.0f;
         const uint32_t o = lanes + TC_O + 64 * grp;
         if (!wait_warp(b, &b->o1, ph, p, 312)) break;
         tc_fence_after();
@@ -541,14 +586,18 @@ __device__ __forceinline__ void outputs(const LinPass& p, const Cta& c, uint32_t
             tmem_ld16(o + 16 * q + 16, r[1]);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                r[j >> 4][j & 15] = __float_as_uint(f * __uint_as_float(r[j >> 4][j & 15]));
+            for (int j = 0; j < 32; j += 2) {
+                float a, e;
+                apart(mul2(two(r[j >> 4][j & 15], r[j >> 4][(j & 15) + 1]), two(f, f)), a, e);
+                r[j >> 4][j & 15] = __float_as_uint(a);
+                r[j >> 4][(j & 15) + 1] = __float_as_uint(e);
+            }
             tmem_st16(o + 16 * q, r[0]);
             tmem_st16(o + 16 * q + 16, r[1]);
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&b->o1s);
+        arrive_warp(&b->o1s);
 
         // The outputs of a whole chunk leave through the X tile, which both
         // products that read it are done with, as one TMA store: a row per thread
@@ -556,7 +605,6 @@ __device__ __forceinline__ void outputs(const LinPass& p, const Cta& c, uint32_t
         uint8_t* tile = c.sm + (i & 1) * 3 * TILE + grp * HALF;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
                              ((size_t)(tok + t) * p.H + c.h) * D + 64 * grp;
-        const float m = p.out_scale;
         if (!wait_warp(b, &b->o2, ph, p, 313)) break;
         tc_fence_after();
 #pragma unroll 1
@@ -571,8 +619,8 @@ __device__ __forceinline__ void outputs(const LinPass& p, const Cta& c, uint32_t
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int k = 8 * e + 2 * j;
-                    w[j] = pack(m * __uint_as_float(r[k >> 4][k & 15]),
-                                m * __uint_as_float(r[k >> 4][(k & 15) + 1]));
+                    w[j] = pack(__uint_as_float(r[k >> 4][k & 15]),
+                                __uint_as_float(r[k >> 4][(k & 15) + 1])) ^ flip;
                 }
                 const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
                 if (len == C) {
@@ -584,7 +632,7 @@ __device__ __forceinline__ void outputs(const LinPass& p, const Cta& c, uint32_t
         }
         fence_proxy_async();
         tc_fence_before();
-        mbar_arrive(&b->od);
+        arrive_warp(&b->od);
     }
 }
 
@@ -643,7 +691,7 @@ __device__ __forceinline__ void states(const LinPass& p, const Cta& c, uint32_t 
             *reinterpret_cast<uint4*>(copy + sw128(r, q * 16)) = v;
         }
         fence_proxy_async();
-        mbar_arrive(&b->s);
+        arrive_warp(&b->s);
         if (!(ok = wait_warp(b, &b->full[i & 1], (i >> 1) & 1, p, 320))) break;
         const uint32_t y = smem_u32(c.sm) + (i & 1) * 3 * TILE + TILE;
         const float* w = c.wtab + (REV ? 0 : C - len);
@@ -657,7 +705,7 @@ __device__ __forceinline__ void states(const LinPass& p, const Cta& c, uint32_t 
             split_w(y, quad, 64 * k + 32 * grp, w, 1.0f, len, lanes + w1, lanes + w2, lanes + w3);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(k ? &b->wb : &b->wa);
+            arrive_warp(k ? &b->wb : &b->wa);
         }
         if (!ok) break;
         if (!(ok = wait_warp(b, &b->u, ph, p, 322))) break;
@@ -670,8 +718,10 @@ __device__ __forceinline__ void states(const LinPass& p, const Cta& c, uint32_t 
             tmem_ld16(lanes + TC_U + 64 * grp + 16 * q + 16, v[1]);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                S[16 * q + j] = f * S[16 * q + j] + __uint_as_float(v[j >> 4][j & 15]);
+            for (int j = 0; j < 32; j += 2)
+                apart(fma2(two(f, f), two(S[16 * q + j], S[16 * q + j + 1]),
+                           two(v[j >> 4][j & 15], v[j >> 4][(j & 15) + 1])),
+                      S[16 * q + j], S[16 * q + j + 1]);
         }
         tc_fence_before();
     }
@@ -793,7 +843,7 @@ lin_states_tc_kernel(const __grid_constant__ Args args) {
                         w + 64 + 16 * k, w + 128 + 16 * k);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&b->w[buf]);
+            arrive_warp(&b->w[buf]);
         }
         if (ok && wait_warp(b, &b->fin, 0, p, 336)) {
             tc_fence_after();

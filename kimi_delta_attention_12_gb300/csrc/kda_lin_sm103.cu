@@ -51,15 +51,12 @@ static_assert(SM_S >= STATE_STAGES * 2 * TILE, "the states' stages end before th
 constexpr uint32_t SMEM = SM_TAB + 2048 + 1024;          // tables, alignment
 static_assert(SMEM <= 232448, "more shared memory than a CTA may have");
 
-// TMEM columns of the pass.  P': 16 columns of bf16 pairs where each 32 columns
-// of P were; the 16 that this frees take parts of w Y.
+// TMEM columns of the pass.  P' (bf16 pairs) takes the first 16 of each 32
+// columns of P.
 constexpr uint32_t TC_P = 0;
 constexpr uint32_t TC_O = 128;           // X S, scaled in place, then + P' Z
 constexpr uint32_t TC_U = 256;           // (w Y)^T Z
-constexpr uint32_t TC_W = 384;           // tokens 0-63: three parts of 32 columns
-constexpr uint32_t TC_W1 = 480;          // tokens 64-127: the first part,
-constexpr uint32_t TC_W2 = 16;           // the second (free columns of P's first half),
-constexpr uint32_t TC_W3 = 80;           // the third (of its second half)
+constexpr uint32_t TC_W = 384;           // w Y of 32 tokens: two buffers of three parts of 16
 // and of the segment states
 constexpr uint32_t TS_U = 0;
 constexpr uint32_t TS_W = 128;           // two buffers of three parts of 64 columns
@@ -77,8 +74,7 @@ struct Bars {
     uint64_t qk, o1, o2, u;        // P / X S / P' Z / (w Y)^T Z done
     uint64_t p, s, o1s, od;        // P' / S copy / X S scaled / outputs written
     uint64_t xfree[2];             // the outputs have left the stage's X tile
-    uint64_t wa, wb;               // w Y first and second half written
-    uint64_t w[2], wfree[2];       // segment states: w Y of a buffer written, read
+    uint64_t w[2], wfree[2];       // w Y of a buffer written, read
     uint64_t fin;
     uint32_t tmem;
     volatile int abort;
@@ -203,23 +199,34 @@ __device__ __forceinline__ constexpr uint32_t step_k(int kk) {
 __device__ __forceinline__ uint32_t tile_mn(uint32_t tile) { return tile >> 4 | (HALF >> 4) << 16; }
 __device__ __forceinline__ constexpr uint32_t step_mn(int kk) { return kk * 2048 >> 4; }
 
-// D (+)= A B of 128 x 128 x 16: A in shared memory, or in TMEM.
+// D (+)= A B of 128 x 128 x 16: A in shared memory, or in TMEM.  The whole warp
+// calls it, so that the operands stay in uniform registers, and one lane (always
+// the same) issues.
 template <bool ADD>
 __device__ __forceinline__ void product(uint32_t d, uint32_t a, uint32_t b, uint32_t id) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %4};\n\t"
-        "mov.b64 b, {%2, %4};\n\tsetp.ne.b32 p, %5, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %4};\n\t"
+        "mov.b64 b, {%2, %4};\n\tsetp.ne.b32 p, %5, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
         "r"(a), "r"(b), "r"(id), "r"(DESC_HI), "n"(ADD ? 1 : 0)
         : "memory");
 }
 template <bool ADD>
 __device__ __forceinline__ void product_ta(uint32_t d, uint32_t a, uint32_t b, uint32_t id) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %4};\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %4};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
         "r"(a), "r"(b), "r"(id), "r"(DESC_HI), "n"(ADD ? 1 : 0)
+        : "memory");
+}
+
+// Arrives once every product issued so far is done (the same lane).
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::
+            "r"(smem_u32(bar))
         : "memory");
 }
 
@@ -329,8 +336,8 @@ __device__ __forceinline__ bool start(const Args& args, Cta& c) {
     return c.sg.n >= 0;
 }
 
-// `issue`: the first of the two issuing warps.
-__device__ __forceinline__ void set_up(const Args& args, Cta& c, int issue) {
+// `issue`: the first of the issuing warps; `w_warps`: those that fill a buffer of w Y.
+__device__ __forceinline__ void set_up(const Args& args, Cta& c, int issue, int w_warps) {
     const LinPass& p = args.p;
     const int tid = threadIdx.x;
     c.chunks = (int)((c.sg.t1 - c.sg.t0 + C - 1) / C);
@@ -348,9 +355,10 @@ __device__ __forceinline__ void set_up(const Args& args, Cta& c, int issue) {
             mbar_init(&b->empty[i], 1);
         }
         uint64_t* one[] = {&b->xfree[0], &b->xfree[1], &b->qk, &b->o1, &b->o2, &b->u, &b->wfree[0], &b->wfree[1], &b->fin};
-        uint64_t* all[] = {&b->p, &b->s, &b->o1s, &b->od, &b->wa, &b->wb, &b->w[0], &b->w[1]};
+        uint64_t* all[] = {&b->p, &b->s, &b->o1s, &b->od};
         for (uint64_t* x : one) mbar_init(x, 1);
         for (uint64_t* x : all) mbar_init(x, 8);   // warps
+        for (uint64_t& x : b->w) mbar_init(&x, w_warps);
         b->abort = 0;
         fence_mbar_init();
     }
@@ -436,69 +444,77 @@ __device__ __forceinline__ void issue_stores(const Args& args, const Cta& c) {
     bulk_wait<false>();
 }
 
-// The products of all chunks.  The tensor core runs them in this order; what
-// may overwrite an operand waits for `u`, which follows every product before.
+// The products of all chunks, in the order in which the tensor core runs them.
+// P of the next chunk comes last: it fills the time that the state takes.
+template <bool REV>
 __device__ __forceinline__ void issue_products(const LinPass& p, const Cta& c, uint32_t tmem) {
     Bars* b = c.b;
     constexpr uint32_t id_kk = idesc_bf16(D, D, 0, 0), id_km = idesc_bf16(D, D, 0, 1);
     const uint32_t base = smem_u32(c.sm), state = tile_mn(base + SM_S);
     const int n = c.chunks;
-    // steps whose chunk ends early: the last one in time
-    const int shorter = chunk_len(c, chunk_start(c, p.reverse, p.reverse ? 0 : n - 1)) < C
-                            ? (p.reverse ? 0 : n - 1)
-                            : -1;
-    for (int i = 0; i < n; ++i) {
-        const uint32_t ph = i & 1, tile = base + (i & 1) * 3 * TILE;
-        const uint32_t x = tile_k(tile), y = tile_k(tile + TILE), z = tile_mn(tile + 2 * TILE);
-        if (!wait1(b, &b->full[i & 1], (i >> 1) & 1, p, 302)) break;
-        if (i > 0 && !wait1(b, &b->u, (i - 1) & 1, p, 303)) break;
-        tc_fence_after();
-        product<false>(tmem + TC_P, x, y, id_kk);
+    for (int i = -1; i < n; ++i) {
+        const uint32_t ph = i & 1;
+        if (i >= 0) {
+            const uint32_t tile = base + ph * 3 * TILE, x = tile_k(tile);
+            const uint32_t z = tile_mn(tile + 2 * TILE);
+            if (!wait_warp(b, &b->s, ph, p, 304)) break;
+            if (i > 0 && !wait_warp(b, &b->od, ph ^ 1, p, 314)) break;
+            tc_fence_after();
+            product<false>(tmem + TC_O, x, state, id_km);
 #pragma unroll
-        for (int kk = 1; kk < 8; ++kk)
-            product<true>(tmem + TC_P, x + step_k(kk), y + step_k(kk), id_kk);
-        mma_commit(&b->qk);
-        if (!wait1(b, &b->s, ph, p, 304)) break;
-        if (i > 0 && !wait1(b, &b->od, (i - 1) & 1, p, 314)) break;
-        tc_fence_after();
-        product<false>(tmem + TC_O, x, state, id_km);
+            for (int kk = 1; kk < 8; ++kk)
+                product<true>(tmem + TC_O, x + step_k(kk), state + step_mn(kk), id_km);
+            commit(&b->o1);
+            // a short chunk's z rows past its end are zeroed before P' is handed over
+            if (chunk_len(c, chunk_start(c, REV, i)) < C && !wait_warp(b, &b->p, ph, p, 306)) break;
+            bool ok = true;
 #pragma unroll
-        for (int kk = 1; kk < 8; ++kk)
-            product<true>(tmem + TC_O, x + step_k(kk), state + step_mn(kk), id_km);
-        mma_commit(&b->o1);
-        if (!wait1(b, &b->wa, ph, p, 305)) break;
-        // a short chunk's z rows past its end are zeroed before P' is handed over
-        if (i == shorter && !wait1(b, &b->p, ph, p, 306)) break;
-        tc_fence_after();
-        product_ta<false>(tmem + TC_U, tmem + TC_W + 64, z, id_km);
-        product_ta<true>(tmem + TC_U, tmem + TC_W + 32, z, id_km);
-        product_ta<true>(tmem + TC_U, tmem + TC_W, z, id_km);
+            for (int g = 0; g < 4; ++g) {     // w Y of 32 tokens each
+                const int buf = g & 1;
+                if (g == 2) {
+                    ok = wait_warp(b, &b->p, ph, p, 307) && wait_warp(b, &b->o1s, ph, p, 308);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-        for (int kk = 1; kk < 4; ++kk)
+                    for (int kk = 0; kk < 8; ++kk)
+                        product_ta<true>(tmem + TC_O, tmem + TC_P + 32 * (kk >> 1) + 8 * (kk & 1),
+                                         z + step_mn(kk), id_km);
+                    commit(&b->o2);
+                }
+                if (!(ok = wait_warp(b, &b->w[buf], g >> 1, p, 305))) break;
+                tc_fence_after();
+                const uint32_t w = tmem + TC_W + 48 * buf;
 #pragma unroll
-            for (int w = 2; w >= 0; --w)
-                product_ta<true>(tmem + TC_U, tmem + TC_W + 32 * w + 8 * kk, z + step_mn(kk),
-                                 id_km);
-        if (!wait1(b, &b->p, ph, p, 307) || !wait1(b, &b->o1s, ph, p, 308)) break;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-            product_ta<true>(tmem + TC_O, tmem + TC_P + 32 * (kk >> 1) + 8 * (kk & 1),
-                             z + step_mn(kk), id_km);
-        mma_commit(&b->o2);
-        if (!wait1(b, &b->wb, ph, p, 309)) break;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            const uint32_t hole = 32 * (kk >> 1) + 8 * (kk & 1), zk = z + step_mn(kk + 4);
-            product_ta<true>(tmem + TC_U, tmem + TC_W3 + hole, zk, id_km);
-            product_ta<true>(tmem + TC_U, tmem + TC_W2 + hole, zk, id_km);
-            product_ta<true>(tmem + TC_U, tmem + TC_W1 + 8 * kk, zk, id_km);
+                for (int kk = 0; kk < 2; ++kk) {
+                    const uint32_t zk = z + step_mn(2 * g + kk);
+                    if (g == 0 && kk == 0) {
+                        product_ta<false>(tmem + TC_U, w + 32, zk, id_km);
+                    } else {
+                        product_ta<true>(tmem + TC_U, w + 32 + 8 * kk, zk, id_km);
+                    }
+                    product_ta<true>(tmem + TC_U, w + 16 + 8 * kk, zk, id_km);
+                    product_ta<true>(tmem + TC_U, w + 8 * kk, zk, id_km);
+                }
+                commit(&b->wfree[buf]);
+            }
+            if (!ok) break;
+            commit(&b->u);
+            commit(&b->empty[ph]);
         }
-        mma_commit(&b->u);
-        mma_commit(&b->empty[i & 1]);
+        if (i + 1 < n) {
+            const uint32_t next = base + (ph ^ 1) * 3 * TILE, x = tile_k(next);
+            const uint32_t y = tile_k(next + TILE);
+            if (!wait_warp(b, &b->full[ph ^ 1], ((i + 1) >> 1) & 1, p, 302)) break;
+            if (i >= 0 && !wait_warp(b, &b->o2, ph, p, 303)) break;   // P' has been read
+            tc_fence_after();
+            product<false>(tmem + TC_P, x, y, id_kk);
+#pragma unroll
+            for (int kk = 1; kk < 8; ++kk)
+                product<true>(tmem + TC_P, x + step_k(kk), y + step_k(kk), id_kk);
+            commit(&b->qk);
+        }
     }
-    mma_commit(&b->fin);
+    commit(&b->fin);
     mbar_wait(&b->fin, 0, nullptr);   // no product outlives the CTA
 }
 
@@ -676,54 +692,61 @@ __device__ __forceinline__ void states(const LinPass& p, const Cta& c, uint32_t 
             S[j + 3] = f * S[j + 3] + v.w;
         }
     }
+    // Step i: the state before chunk i to its copy, and w Y of the chunk's tokens
+    // 32 grp on and 64 + 32 grp on into the group's buffer.  The first of these
+    // waits for the products on the buffer before, those of the state for all;
+    // group 1, whose buffer is read last, starts with the state.
     uint8_t* copy = c.sm + SM_S + grp * HALF;
+    const uint32_t w = lanes + TC_W + 48 * grp;
     bool ok = true;
-    for (int i = 0; i < c.chunks; ++i) {
+    for (int i = 0; ok && i <= c.chunks; ++i) {
         const uint32_t ph = i & 1;
-        const int len = chunk_len(c, chunk_start(c, REV, i));
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            uint4 v;
-            v.x = pack(S[8 * q], S[8 * q + 1]);
-            v.y = pack(S[8 * q + 2], S[8 * q + 3]);
-            v.z = pack(S[8 * q + 4], S[8 * q + 5]);
-            v.w = pack(S[8 * q + 6], S[8 * q + 7]);
-            *reinterpret_cast<uint4*>(copy + sw128(r, q * 16)) = v;
-        }
-        fence_proxy_async();
-        arrive_warp(&b->s);
-        if (!(ok = wait_warp(b, &b->full[i & 1], (i >> 1) & 1, p, 320))) break;
-        const uint32_t y = smem_u32(c.sm) + (i & 1) * 3 * TILE + TILE;
-        const float* w = c.wtab + (REV ? 0 : C - len);
+        const int len = i < c.chunks ? chunk_len(c, chunk_start(c, REV, i)) : 0;
 #pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
-            if (k && !(ok = wait_warp(b, &b->p, ph, p, 321))) break;   // P has been read
-            tc_fence_after();
-            const uint32_t w1 = k ? TC_W1 + 16 * grp : TC_W + 16 * grp;
-            const uint32_t w2 = k ? TC_W2 + 32 * grp : TC_W + 32 + 16 * grp;
-            const uint32_t w3 = k ? TC_W3 + 32 * grp : TC_W + 64 + 16 * grp;
-            split_w(y, quad, 64 * k + 32 * grp, w, 1.0f, len, lanes + w1, lanes + w2, lanes + w3);
-            tmem_wait_st();
-            tc_fence_before();
-            arrive_warp(k ? &b->wb : &b->wa);
-        }
-        if (!ok) break;
-        if (!(ok = wait_warp(b, &b->u, ph, p, 322))) break;
-        tc_fence_after();
-        const float f = c.lam[len];
+        for (int k = 0; k < 3; ++k) {
+            if (k == (grp ^ 1)) {
+                if (i > 0) {
+                    if (!(ok = wait_warp(b, &b->u, ph ^ 1, p, 322))) break;
+                    tc_fence_after();
+                    const float f = c.lam[chunk_len(c, chunk_start(c, REV, i - 1))];
 #pragma unroll
-        for (int q = 0; q < 4; q += 2) {
-            uint32_t v[2][16];
-            tmem_ld16(lanes + TC_U + 64 * grp + 16 * q, v[0]);
-            tmem_ld16(lanes + TC_U + 64 * grp + 16 * q + 16, v[1]);
-            tmem_wait_ld();
+                    for (int q = 0; q < 4; q += 2) {
+                        uint32_t v[2][16];
+                        tmem_ld16(lanes + TC_U + 64 * grp + 16 * q, v[0]);
+                        tmem_ld16(lanes + TC_U + 64 * grp + 16 * q + 16, v[1]);
+                        tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; j += 2)
-                apart(fma2(two(f, f), two(S[16 * q + j], S[16 * q + j + 1]),
-                           two(v[j >> 4][j & 15], v[j >> 4][(j & 15) + 1])),
-                      S[16 * q + j], S[16 * q + j + 1]);
+                        for (int j = 0; j < 32; j += 2)
+                            apart(fma2(two(f, f), two(S[16 * q + j], S[16 * q + j + 1]),
+                                       two(v[j >> 4][j & 15], v[j >> 4][(j & 15) + 1])),
+                                  S[16 * q + j], S[16 * q + j + 1]);
+                    }
+                    tc_fence_before();
+                }
+                if (i == c.chunks) break;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    uint4 v;
+                    v.x = pack(S[8 * q], S[8 * q + 1]);
+                    v.y = pack(S[8 * q + 2], S[8 * q + 3]);
+                    v.z = pack(S[8 * q + 4], S[8 * q + 5]);
+                    v.w = pack(S[8 * q + 6], S[8 * q + 7]);
+                    *reinterpret_cast<uint4*>(copy + sw128(r, q * 16)) = v;
+                }
+                fence_proxy_async();
+                arrive_warp(&b->s);
+            } else if (i < c.chunks) {
+                const int half = k == 2;      // the group's second 32 tokens
+                if (!half && !(ok = wait_warp(b, &b->full[ph], (i >> 1) & 1, p, 320))) break;
+                if ((half || i > 0) && !(ok = wait_warp(b, &b->wfree[grp], half ^ 1, p, 321))) break;
+                tc_fence_after();
+                split_w(smem_u32(c.sm) + ph * 3 * TILE + TILE, quad, 64 * half + 32 * grp,
+                        c.wtab + (REV ? 0 : C - len), 1.0f, len, w, w + 16, w + 32);
+                tmem_wait_st();
+                tc_fence_before();
+                arrive_warp(&b->w[grp]);
+            }
         }
-        tc_fence_before();
     }
     if (ok && p.state_out && c.sg.j + 1 == c.sg.count) {
         float* dst = p.state_out + ((size_t)c.sg.n * p.H + c.h) * state_floats + (size_t)r * D +
@@ -739,15 +762,16 @@ __global__ void __launch_bounds__(THREADS, 1) lin_pass_tc_kernel(const __grid_co
     const LinPass& p = args.p;
     Cta c;
     if (!start(args, c)) return;
-    set_up(args, c, 16);
+    set_up(args, c, 16, 4);
     const uint32_t tmem = c.b->tmem;
     const int warp = threadIdx.x >> 5;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // this warp's 32 TMEM lanes
     if (warp >= 16) {
         give_registers<REGS_ISSUE>();
-        if ((threadIdx.x & 31) == 0) {
+        if (warp == 17) {
+            issue_products<REV>(p, c, tmem);
+        } else if ((threadIdx.x & 31) == 0) {
             if (warp == 16) issue_loads<REV>(args, c);
-            if (warp == 17) issue_products(p, c, tmem);
             if (warp == 18) issue_stores<REV>(args, c);
         }
     } else if (warp < 8) {
@@ -772,7 +796,7 @@ lin_states_tc_kernel(const __grid_constant__ Args args) {
         c.sg.u + c.sg.j >= lin::seg_rows(p.total_T, p.seg_len)) {
         return;
     }
-    set_up(args, c, 8);
+    set_up(args, c, 8, 8);
     Bars* b = c.b;
     const uint32_t tmem = b->tmem;
     const int tid = threadIdx.x, warp = tid >> 5, n = c.chunks;
@@ -794,34 +818,32 @@ lin_states_tc_kernel(const __grid_constant__ Args args) {
                 mbar_wait(&b->full[i % STATE_STAGES], (i / STATE_STAGES) & 1, nullptr);
         }
     } else if (warp == 9) {
-        if ((tid & 31) == 0) {
-            constexpr uint32_t id = idesc_bf16(D, D, 0, 1);
-            for (int i = 0; i < n; ++i) {
-                const int s = i % STATE_STAGES;
-                const uint32_t z = tile_mn(smem_u32(c.sm) + s * 2 * TILE + TILE);
-                const uint32_t w = tmem + TS_W + 192 * (i & 1);
-                if (!wait1(b, &b->full[s], (i / STATE_STAGES) & 1, p, 332)) break;
-                if (!wait1(b, &b->w[i & 1], (i >> 1) & 1, p, 333)) break;
-                tc_fence_after();
-                if (i == 0) {
-                    product_ta<false>(tmem + TS_U, w + 128, z, id);
-                } else {
-                    product_ta<true>(tmem + TS_U, w + 128, z, id);
-                }
-                product_ta<true>(tmem + TS_U, w + 64, z, id);
-                product_ta<true>(tmem + TS_U, w, z, id);
-#pragma unroll
-                for (int kk = 1; kk < 8; ++kk)
-#pragma unroll
-                    for (int part = 2; part >= 0; --part)
-                        product_ta<true>(tmem + TS_U, w + 64 * part + 8 * kk, z + step_mn(kk),
-                                         id);
-                mma_commit(&b->wfree[i & 1]);
-                mma_commit(&b->empty[s]);
+        constexpr uint32_t id = idesc_bf16(D, D, 0, 1);
+        for (int i = 0; i < n; ++i) {
+            const int s = i % STATE_STAGES;
+            const uint32_t z = tile_mn(smem_u32(c.sm) + s * 2 * TILE + TILE);
+            const uint32_t w = tmem + TS_W + 192 * (i & 1);
+            if (!wait_warp(b, &b->full[s], (i / STATE_STAGES) & 1, p, 332)) break;
+            if (!wait_warp(b, &b->w[i & 1], (i >> 1) & 1, p, 333)) break;
+            tc_fence_after();
+            if (i == 0) {
+                product_ta<false>(tmem + TS_U, w + 128, z, id);
+            } else {
+                product_ta<true>(tmem + TS_U, w + 128, z, id);
             }
-            mma_commit(&b->fin);
-            mbar_wait(&b->fin, 0, nullptr);
+            product_ta<true>(tmem + TS_U, w + 64, z, id);
+            product_ta<true>(tmem + TS_U, w, z, id);
+#pragma unroll
+            for (int kk = 1; kk < 8; ++kk)
+#pragma unroll
+                for (int part = 2; part >= 0; --part)
+                    product_ta<true>(tmem + TS_U, w + 64 * part + 8 * kk, z + step_mn(kk),
+                                     id);
+            commit(&b->wfree[i & 1]);
+            commit(&b->empty[s]);
         }
+        commit(&b->fin);
+        mbar_wait(&b->fin, 0, nullptr);
     } else {
         const int r = tid & 127, grp = tid >> 7;
         bool ok = true;

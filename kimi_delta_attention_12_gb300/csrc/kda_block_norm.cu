@@ -5,33 +5,65 @@
 //     h  = x' / rms(x') * w_pre
 // and its backward.  All of it is bound by the bytes of the rows: each tensor
 // is read or written once, the row stays in registers between the two norms,
-// statistics and sums are fp32.
+// statistics and sums are fp32.  What that takes is bytes in flight: a thread
+// has the loads of its next row (or of four vectors, where rows do not matter)
+// under way while it works.
 #include "kda_block_norm.h"
 
 #include <cuda_bf16.h>
+#include <limits.h>
+
+#include <type_traits>
+
+#include "kda_packed.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int V = 8;             // channels per vector: 16 bytes of bf16
 constexpr int MAX_THREADS = 512;
-constexpr int MAX_PARTS = 304;   // two CTAs on each of 152 SMs
 constexpr int MAX_ROWS = 4;      // rows that short-row blocks take at once
+constexpr int TILE = 2048;       // columns per block where rows do not couple them
 
-__device__ __forceinline__ void load(const float* p, float (&v)[V]) {
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    const float4 b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+// A vector as it was loaded.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+    float4 a, b;
+};
+template <>
+struct Raw<__nv_bfloat16> {
+    uint4 a;
+};
+
+__device__ __forceinline__ void fetch(const float* p, Raw<float>& r) {
+    r.a = *reinterpret_cast<const float4*>(p);
+    r.b = *reinterpret_cast<const float4*>(p + 4);
 }
-__device__ __forceinline__ void load(const __nv_bfloat16* p, float (&v)[V]) {
-    const uint4 r = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+__device__ __forceinline__ void fetch(const __nv_bfloat16* p, Raw<__nv_bfloat16>& r) {
+    r.a = *reinterpret_cast<const uint4*>(p);
+}
+__device__ __forceinline__ void clear(Raw<float>& r) {
+    r.a = r.b = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+__device__ __forceinline__ void clear(Raw<__nv_bfloat16>& r) { r.a = make_uint4(0, 0, 0, 0); }
+__device__ __forceinline__ void expand(const Raw<float>& r, float (&v)[V]) {
+    v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
+    v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
+}
+__device__ __forceinline__ void expand(const Raw<__nv_bfloat16>& r, float (&v)[V]) {
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         v[2 * i] = __uint_as_float(w[i] << 16);
         v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
+}
+__device__ __forceinline__ void load(const float* p, float (&v)[V]) {
+    Raw<float> r;
+    fetch(p, r);
+    expand(r, v);
 }
 __device__ __forceinline__ void store(float* p, const float (&v)[V]) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
@@ -47,7 +79,47 @@ __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[V]) {
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ float sigmoid(float t) { return 1.0f / (1.0f + expf(-t)); }
+// 1 / (1 + e^-t).  fp32: a few units in the last place.  bf16 rows: from the
+// approximate 2^x and reciprocal, relative error near 2^-22 (1 + |t|), which
+// the rounding of the gate itself (2^-9) hides, in 4 instructions instead of 14:
+// with the full expf the heads' forward took 885 us where it now takes 7xx.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float t);
+template <>
+__device__ __forceinline__ float sigmoid<float>(float t) {
+    return __fdividef(1.0f, 1.0f + expf(-t));
+}
+template <>
+__device__ __forceinline__ float sigmoid<__nv_bfloat16>(float t) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+
+// A vector as four pairs.
+__device__ __forceinline__ void expand2(const Raw<float>& r, uint64_t (&v)[V / 2]) {
+    v[0] = two(r.a.x, r.a.y); v[1] = two(r.a.z, r.a.w);
+    v[2] = two(r.b.x, r.b.y); v[3] = two(r.b.z, r.b.w);
+}
+__device__ __forceinline__ void expand2(const Raw<__nv_bfloat16>& r, uint64_t (&v)[V / 2]) {
+    v[0] = two(low(r.a.x), high(r.a.x)); v[1] = two(low(r.a.y), high(r.a.y));
+    v[2] = two(low(r.a.z), high(r.a.z)); v[3] = two(low(r.a.w), high(r.a.w));
+}
+__device__ __forceinline__ void load2(const float* p, uint64_t (&v)[V / 2]) {
+    Raw<float> r;
+    fetch(p, r);
+    expand2(r, v);
+}
+__device__ __forceinline__ void store2(float* p, const uint64_t (&v)[V / 2]) {
+    float f[V];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) apart(v[i], f[2 * i], f[2 * i + 1]);
+    store(p, f);
+}
+__device__ __forceinline__ void store2(__nv_bfloat16* p, const uint64_t (&v)[V / 2]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack(v[0]), pack(v[1]), pack(v[2]), pack(v[3]));
+}
 
 // Sums of M values over the `width` consecutive lanes (a power of two) of the
 // calling thread.
@@ -73,46 +145,125 @@ __device__ __forceinline__ void row_sum(float (&s)[M], float* buf, int warps, in
         for (int i = 0; i < M; ++i) b[w * 3 + i] = s[i];
     }
     __syncthreads();
+    // every warp adds the (up to 16) warps' sums itself, in each half of its lanes
+    const int lane = threadIdx.x & 15;
 #pragma unroll
-    for (int i = 0; i < M; ++i) s[i] = 0.0f;
-    for (int j = 0; j < warps; ++j) {
+    for (int i = 0; i < M; ++i) s[i] = lane < warps ? b[lane * 3 + i] : 0.0f;
+    lane_sum(s, 16);
+}
+
+// n act(gate) res_scale of one vector; y replaced by it.
+template <typename T>
+__device__ __forceinline__ void branch(float (&u)[V], const float (&g)[V], float r,
+                                       const float* w_post, const float* res, bool gate,
+                                       int silu) {
+    float w[V];
+    load(w_post, w);
 #pragma unroll
-        for (int i = 0; i < M; ++i) s[i] += b[j * 3 + i];
+    for (int e = 0; e < V; ++e) u[e] = u[e] * r * w[e];
+    if (gate) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float a = sigmoid<T>(g[e]);
+            u[e] *= silu ? g[e] * a : a;
+        }
+    }
+    if (res) {
+        load(res, w);
+#pragma unroll
+        for (int e = 0; e < V; ++e) u[e] *= w[e];
     }
 }
 
-// Block shape: threadIdx.x over the vectors of a row's tile (whole warps), VPT
-// vectors per thread, threadIdx.y over rows; blockIdx.y over the tiles, of
-// which there is only one where a sum runs over the whole row.
+// ------------------------------------------------------------ forward, heads
+// No sum runs over a row: the tensors are streams of vectors, a group's lanes
+// side by side.  Four vectors a thread, all loads first.
+template <typename T>
+__global__ void __launch_bounds__(256) block_norm_heads_kernel(BlockNorm p, int64_t vecs) {
+    constexpr int U = 4;
+    const int lanes = p.group / V;
+    const int64_t first = (int64_t)blockIdx.x * (256 * U) + threadIdx.x;
+    const T* y = static_cast<const T*>(p.y);
+    const T* gate = static_cast<const T*>(p.gate);
+    const T* x = static_cast<const T*>(p.x);
+    Raw<T> ry[U], rg[U], rx[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const int64_t vec = first + 256 * i;
+        clear(ry[i]);
+        clear(rg[i]);
+        clear(rx[i]);
+        if (vec < vecs) {
+            fetch(y + vec * V, ry[i]);
+            if (gate) fetch(gate + vec * V, rg[i]);
+            if (x) fetch(x + vec * V, rx[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const int64_t vec = first + 256 * i;
+        float u[V], g[V], xs[V], s[1] = {0.f};
+        expand(ry[i], u);
+        expand(rg[i], g);
+        expand(rx[i], xs);
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[0] += u[e] * u[e];
+        lane_sum(s, lanes);
+        if (vec >= vecs) continue;
+        const float* res =
+            p.res_scale ? p.res_scale + (vec % (p.D / V)) * V : nullptr;
+        branch<T>(u, g, rsqrtf(s[0] / (float)p.group + p.eps),
+               p.w_post + (int)(vec & (lanes - 1)) * V, res, gate != nullptr, p.silu);
+        if (x) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) u[e] += xs[e];
+        }
+        store(static_cast<T*>(p.x_out) + vec * V, u);
+    }
+}
+
+// ------------------------------------------------------------- forward, rows
+// Block shape: threadIdx.x over the vectors of a row (whole warps), VPT
+// vectors per thread, threadIdx.y over rows.
 template <typename T, int VPT>
-__global__ void __launch_bounds__(MAX_THREADS) block_norm_kernel(BlockNorm p, int tile) {
+__global__ void __launch_bounds__(MAX_THREADS) block_norm_kernel(BlockNorm p) {
     __shared__ float buf[2 * MAX_ROWS * 32 * 3];
-    const int warps = blockDim.x >> 5;
-    const int vec0 = blockIdx.y * tile / V + threadIdx.x;
-    const int vecs = min(p.D, ((int)blockIdx.y + 1) * tile) / V;
+    const int warps = blockDim.x >> 5, vecs = p.D / V;
     const bool whole = p.group == p.D;
     const int lanes = whole ? 32 : p.group / V;
     const T* y = static_cast<const T*>(p.y);
     const T* gate = static_cast<const T*>(p.gate);
     const T* x = static_cast<const T*>(p.x);
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
-    for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < p.rows; r0 += step) {
-        const int64_t row = r0 + threadIdx.y;
-        const bool live = row < p.rows;
-        float u[VPT][V], xs[VPT][V], gt[VPT][V];
+    Raw<T> ry[VPT], rg[VPT], rx[VPT];
+    auto fetch_row = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int vec = vec0 + i * blockDim.x;
-            const size_t at = (size_t)row * p.D + (size_t)vec * V;
-            const bool in = live && vec < vecs;
-#pragma unroll
-            for (int e = 0; e < V; ++e) { u[i][e] = 0.f; xs[i][e] = 0.f; gt[i][e] = 0.f; }
-            if (in) {
-                load(y + at, u[i]);
-                if (gate) load(gate + at, gt[i]);
-                if (x) load(x + at, xs[i]);
+            const int vec = threadIdx.x + i * blockDim.x;
+            clear(ry[i]);
+            clear(rg[i]);
+            clear(rx[i]);
+            if (row < p.rows && vec < vecs) {
+                const size_t at = (size_t)row * p.D + (size_t)vec * V;
+                fetch(y + at, ry[i]);
+                if (gate) fetch(gate + at, rg[i]);
+                if (x) fetch(x + at, rx[i]);
             }
         }
+    };
+    int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    fetch_row(row);
+    for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < p.rows; r0 += step, row += step) {
+        const bool live = row < p.rows;
+        float u[VPT][V];
+        Raw<T> cg[VPT], cx[VPT];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            expand(ry[i], u[i]);
+            cg[i] = rg[i];
+            cx[i] = rx[i];
+        }
+        fetch_row(row + step);
         float ss[VPT][1];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -134,28 +285,17 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_kernel(BlockNorm p, in
         float s2[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int vec = vec0 + i * blockDim.x;
+            const int vec = threadIdx.x + i * blockDim.x;
             if (!live || vec >= vecs) continue;
-            const float r = rsqrtf(ss[i][0] / (float)p.group + p.eps);
-            float w[V];
-            load(p.w_post + (vec * V) % p.group, w);
-#pragma unroll
-            for (int e = 0; e < V; ++e) u[i][e] = u[i][e] * r * w[e];
-            if (gate) {
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float a = sigmoid(gt[i][e]);
-                    u[i][e] *= p.silu ? gt[i][e] * a : a;
-                }
-            }
-            if (p.res_scale) {
-                load(p.res_scale + vec * V, w);
-#pragma unroll
-                for (int e = 0; e < V; ++e) u[i][e] *= w[e];
-            }
+            float g[V], xs[V];
+            expand(cg[i], g);
+            expand(cx[i], xs);
+            branch<T>(u[i], g, rsqrtf(ss[i][0] / (float)p.group + p.eps),
+                   p.w_post + (vec * V) % p.group,
+                   p.res_scale ? p.res_scale + vec * V : nullptr, gate != nullptr, p.silu);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                u[i][e] += xs[i][e];
+                if (x) u[i][e] += xs[e];
                 s2[0] += u[i][e] * u[i][e];
             }
             store(static_cast<T*>(p.x_out) + (size_t)row * p.D + (size_t)vec * V, u[i]);
@@ -165,7 +305,7 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_kernel(BlockNorm p, in
             const float r = rsqrtf(s2[0] / (float)p.D + p.eps);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int vec = vec0 + i * blockDim.x;
+                const int vec = threadIdx.x + i * blockDim.x;
                 if (!live || vec >= vecs) continue;
                 float w[V];
                 load(p.w_pre + vec * V, w);
@@ -179,6 +319,7 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_kernel(BlockNorm p, in
     }
 }
 
+// ------------------------------------------------------------------ backward
 // Per row, with r = 1 / rms and the upstream gradients dX of x' and dh of h:
 //     total  = dX + r (dh w_pre) - x' r^3 mean(dh w_pre x')        (= dx)
 //     dy     = r dn - y r^3 mean(dn y),   dn = total res_scale act(gate) w_post
@@ -186,140 +327,221 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_kernel(BlockNorm p, in
 // and over the rows: dw_pre += dh x' r, dres_scale += total u,
 // dw_post += total res_scale act(gate) y r.  The rows of a CTA add to
 // registers; each CTA leaves its sums apart and a second kernel adds them in
-// order, so that a repeated call gives the same bits.
-template <typename T, int VPT>
-__global__ void __launch_bounds__(MAX_THREADS) block_norm_backward_kernel(BlockNorm p, int tile) {
+// order, so that a repeated call gives the same bits.  blockIdx.y is the tile of
+// columns, of which there is one where a sum runs over the row.
+//
+// RING: rows arrive in shared memory by asynchronous copies, `stages` of them
+// under way or at work; a thread copies what it reads itself, so that its own
+// wait is enough.  The registers that rows in flight would take go to the
+// sums.  Rows too wide for that (stages = 0) are read into registers.
+enum { Y = 0, GATE = 1, DXO = 2, X = 3, DH = 4, TENSORS = 5 };
+
+__device__ __forceinline__ void copy16(void* smem, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(smem)),
+                 "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_done(int behind) {   // all but the last `behind` rows'
+    if (behind >= 2) {
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+    } else if (behind == 1) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+}
+
+enum { NO_GATE = 0, SIGMOID = 1, SILU = 2 };
+
+template <typename T, int VPT, int ACT, bool RING>
+__global__ void __launch_bounds__(MAX_THREADS)
+block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
     __shared__ float buf[2 * MAX_ROWS * 32 * 3];
     const int warps = blockDim.x >> 5;
     const int vec0 = blockIdx.y * tile / V + threadIdx.x;
     const int vecs = min(p.D, ((int)blockIdx.y + 1) * tile) / V;
     const bool whole = p.group == p.D;
     const int lanes = whole ? 32 : p.group / V;
-    const T* y = static_cast<const T*>(p.y);
-    const T* gate = static_cast<const T*>(p.gate);
-    const T* x = static_cast<const T*>(p.x);
-    const T* dxo = static_cast<const T*>(p.dx_out);
-    const T* dh = static_cast<const T*>(p.dh);
-    float a_post[VPT][V], a_res[VPT][V], a_pre[VPT][V];
+    const T* src[TENSORS] = {static_cast<const T*>(p.y), static_cast<const T*>(p.gate),
+                             static_cast<const T*>(p.dx_out),
+                             static_cast<const T*>(p.w_pre ? p.x : nullptr),
+                             static_cast<const T*>(p.w_pre ? p.dh : nullptr)};
+    extern __shared__ float4 dyn4[];
+    uint64_t a_post[VPT][V / 2], a_res[VPT][V / 2], a_pre[VPT][V / 2];   // pairs
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int e = 0; e < V; ++e) a_post[i][e] = a_res[i][e] = a_pre[i][e] = 0.f;
+        for (int e = 0; e < V / 2; ++e) a_post[i][e] = a_res[i][e] = a_pre[i][e] = 0;
 
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
-    for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < p.rows; r0 += step) {
-        const int64_t row = r0 + threadIdx.y;
-        const bool live = row < p.rows;
-        float yv[VPT][V], gt[VPT][V], tot[VPT][V], ry[VPT];
-        float s[3] = {0.f, 0.f, 0.f};   // x'^2, dh w_pre x', y^2
-        float xv[VPT][V], dn[VPT][V];
+    int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int all = blockDim.x * blockDim.y, flat = threadIdx.y * blockDim.x + threadIdx.x;
+    Raw<T>* ring = reinterpret_cast<Raw<T>*>(dyn4);   // [stages][TENSORS][VPT][all]
+    auto slot = [&](int stage, int k, int i) {
+        return ring + ((stage * TENSORS + k) * VPT + i) * all + flat;
+    };
+    auto copy_row = [&](int64_t r, int stage) {
+        if (r < p.rows) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int vec = vec0 + i * blockDim.x;
-            const size_t at = (size_t)row * p.D + (size_t)vec * V;
-            const bool in = live && vec < vecs;
+            for (int i = 0; i < VPT; ++i) {
+                const int vec = vec0 + i * blockDim.x;
+                if (vec >= vecs) continue;
+                const size_t at = (size_t)r * p.D + (size_t)vec * V;
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                yv[i][e] = gt[i][e] = tot[i][e] = xv[i][e] = dn[i][e] = 0.f;
-            }
-            if (in) {
-                load(y + at, yv[i]);
-                if (gate) load(gate + at, gt[i]);
-                if (dxo) load(dxo + at, tot[i]);
-                if (p.w_pre) {
-                    load(x + at, xv[i]);
-                    load(dh + at, dn[i]);
+                for (int k = 0; k < TENSORS; ++k) {
+                    if (!src[k]) continue;
+#pragma unroll
+                    for (int q = 0; q < (int)sizeof(Raw<T>) / 16; ++q)
+                        copy16(reinterpret_cast<uint4*>(slot(stage, k, i)) + q,
+                               reinterpret_cast<const uint4*>(src[k] + at) + q);
                 }
             }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");   // a group a row, empty or not
+    };
+    if (RING) {
+        for (int k = 0; k + 1 < stages; ++k) copy_row(row + k * step, k);
+    }
+    int stage = 0;
+    const float inv_row = 1.0f / (float)p.D, inv_group = 1.0f / (float)p.group;
+    for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < p.rows; r0 += step, row += step) {
+        const bool live = row < p.rows;
+        Raw<T> held[RING ? 1 : TENSORS][RING ? 1 : VPT];
+        if (RING) {
+            // the stage that the row before has left takes the next row to come
+            const int free = stage == 0 ? stages - 1 : stage - 1;
+            copy_row(row + (stages - 1) * step, free);
+            copies_done(stages - 1);
+        } else {
+#pragma unroll
+            for (int k = 0; k < (RING ? 0 : TENSORS); ++k)
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+                    const int vec = vec0 + i * blockDim.x;
+                    clear(held[k][i]);
+                    if (src[k] && live && vec < vecs)
+                        fetch(src[k] + (size_t)row * p.D + (size_t)vec * V, held[k][i]);
+                }
+        }
+        auto get = [&](int k, int i, uint64_t (&v)[V / 2]) {
+            const bool in = live && src[k] && vec0 + i * (int)blockDim.x < vecs;
+            if (RING) {
+                Raw<T> r;
+                clear(r);
+                if (in) r = *slot(stage, k, i);
+                expand2(r, v);
+            } else {
+                expand2(held[RING ? 0 : k][RING ? 0 : i], v);
+            }
+        };
+        float s[3] = {0.f, 0.f, 0.f};   // x'^2, dh w_pre x', y^2
+        float rr[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int vec = vec0 + i * blockDim.x;
-            float w[V], yy[1] = {0.f};
+            uint64_t a[V / 2], q0 = 0, q1 = 0, q2 = 0;
             if (p.w_pre && vec < vecs) {
-                load(p.w_pre + vec * V, w);
+                uint64_t w[V / 2], h[V / 2];
+                get(X, i, a);
+                get(DH, i, h);
+                load2(p.w_pre + vec * V, w);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    s[0] += xv[i][e] * xv[i][e];
-                    s[1] += dn[i][e] * w[e] * xv[i][e];
+                for (int e = 0; e < V / 2; ++e) {
+                    q0 = fma2(a[e], a[e], q0);
+                    q1 = fma2(mul2(h[e], w[e]), a[e], q1);
                 }
             }
+            get(Y, i, a);
 #pragma unroll
-            for (int e = 0; e < V; ++e) yy[0] += yv[i][e] * yv[i][e];
+            for (int e = 0; e < V / 2; ++e) q2 = fma2(a[e], a[e], q2);
+            s[0] += sum2(q0);
+            s[1] += sum2(q1);
             if (whole) {
-                s[2] += yy[0];
+                s[2] += sum2(q2);
             } else {
+                float yy[1] = {sum2(q2)};
                 lane_sum(yy, lanes);
-                ry[i] = rsqrtf(yy[0] / (float)p.group + p.eps);
+                rr[i] = rsqrtf(yy[0] * inv_group + p.eps);
             }
         }
         const bool sums = whole || p.w_pre;
         if (sums) row_sum(s, buf, warps, 0);
         if (whole) {
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) ry[i] = rsqrtf(s[2] / (float)p.D + p.eps);
+            for (int i = 0; i < VPT; ++i) rr[i] = rsqrtf(s[2] * inv_group + p.eps);
         }
+        const float rx = rsqrtf(s[0] * inv_row + p.eps);
+        const uint64_t rx2 = two(rx, rx);
+        const float cx = -s[1] * inv_row * rx * rx * rx;
+        const uint64_t cx2 = two(cx, cx);
         float s2[1] = {0.f};
-        float cy[VPT];
+        uint64_t tot[VPT][V / 2];
+        float cc[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int vec = vec0 + i * blockDim.x;
             const bool in = live && vec < vecs;
             const size_t at = (size_t)row * p.D + (size_t)vec * V;
-            float w[V];
+            uint64_t w[V / 2], part = 0;
+            get(DXO, i, tot[i]);
             if (in && p.w_pre) {
-                const float r = rsqrtf(s[0] / (float)p.D + p.eps);
-                const float c = s[1] / (float)p.D * r * r * r;
-                load(p.w_pre + vec * V, w);
+                uint64_t a[V / 2], h[V / 2];
+                get(X, i, a);
+                get(DH, i, h);
+                load2(p.w_pre + vec * V, w);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    a_pre[i][e] += dn[i][e] * xv[i][e] * r;
-                    tot[i][e] += r * dn[i][e] * w[e] - xv[i][e] * c;
+                for (int e = 0; e < V / 2; ++e) {
+                    h[e] = mul2(h[e], rx2);
+                    a_pre[i][e] = fma2(h[e], a[e], a_pre[i][e]);
+                    tot[i][e] = fma2(a[e], cx2, fma2(h[e], w[e], tot[i][e]));
                 }
             }
-            if (in && p.dx) store(static_cast<T*>(p.dx) + at, tot[i]);
-            float part[1] = {0.f};
+            if (in && p.dx) store2(static_cast<T*>(p.dx) + at, tot[i]);
             if (in) {
-                float act[V], slope[V];
+                uint64_t rs[V / 2], a[V / 2], g[V / 2];
+                const uint64_t one = two(1.f, 1.f), r2 = two(rr[i], rr[i]);
 #pragma unroll
-                for (int e = 0; e < V; ++e) { act[e] = 1.f; slope[e] = 0.f; }
-                if (gate) {
+                for (int e = 0; e < V / 2; ++e) rs[e] = one;
+                if (p.res_scale) load2(p.res_scale + vec * V, rs);
+                load2(p.w_post + (vec * V) % p.group, w);
+                get(Y, i, a);
+                if (ACT != NO_GATE) get(GATE, i, g);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        const float t = gt[i][e], a = sigmoid(t);
-                        act[e] = p.silu ? t * a : a;
-                        slope[e] = p.silu ? a * (1.f + t * (1.f - a)) : a * (1.f - a);
+                for (int e = 0; e < V / 2; ++e) {
+                    const uint64_t yn = mul2(a[e], r2), n = mul2(yn, w[e]);
+                    uint64_t da = tot[i][e];              // total act
+                    if (ACT != NO_GATE) {
+                        float t0, t1;
+                        apart(g[e], t0, t1);
+                        const uint64_t q = two(sigmoid<T>(t0), sigmoid<T>(t1));
+                        const uint64_t act = ACT == SILU ? mul2(g[e], q) : q;
+                        // act' = act (1 - q), for silu + q
+                        uint64_t slope = mul2(act, sub2(one, q));
+                        if (ACT == SILU) slope = add2(slope, q);
+                        g[e] = mul2(mul2(da, rs[e]), mul2(n, slope));
+                        da = mul2(da, act);
                     }
+                    a_res[i][e] = fma2(da, n, a_res[i][e]);
+                    da = mul2(da, rs[e]);
+                    a_post[i][e] = fma2(da, yn, a_post[i][e]);
+                    tot[i][e] = mul2(da, w[e]);           // dn from here on
+                    part = fma2(tot[i][e], a[e], part);
                 }
-                float rs[V];
-#pragma unroll
-                for (int e = 0; e < V; ++e) rs[e] = 1.f;
-                if (p.res_scale) load(p.res_scale + vec * V, rs);
-                load(p.w_post + (vec * V) % p.group, w);
-                float dg[V];
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float yn = yv[i][e] * ry[i], n = yn * w[e];
-                    a_res[i][e] += tot[i][e] * n * act[e];
-                    const float du = tot[i][e] * rs[e];
-                    dg[e] = du * n * slope[e];
-                    a_post[i][e] += du * act[e] * yn;
-                    tot[i][e] = du * act[e] * w[e];   // dn from here on
-                    part[0] += tot[i][e] * yv[i][e];
-                }
-                if (gate) store(static_cast<T*>(p.dgate) + at, dg);
+                if (ACT != NO_GATE) store2(static_cast<T*>(p.dgate) + at, g);
             }
             if (whole) {
-                s2[0] += part[0];
+                s2[0] += sum2(part);
             } else {
-                lane_sum(part, lanes);
-                cy[i] = part[0] / (float)p.group;
+                float pt[1] = {sum2(part)};
+                lane_sum(pt, lanes);
+                cc[i] = pt[0] * inv_group;
             }
         }
         if (whole) {
             row_sum(s2, buf, warps, 1);
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) cy[i] = s2[0] / (float)p.D;
+            for (int i = 0; i < VPT; ++i) cc[i] = s2[0] * inv_row;
         } else if (sums && warps > 1) {
             __syncthreads();   // the next row writes the sums this row has read
         }
@@ -327,65 +549,92 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_backward_kernel(BlockN
         for (int i = 0; i < VPT; ++i) {
             const int vec = vec0 + i * blockDim.x;
             if (!live || vec >= vecs) continue;
-            const float r = ry[i], c = cy[i] * r * r * r;
+            uint64_t a[V / 2];
+            get(Y, i, a);
+            const float c = -cc[i] * rr[i] * rr[i] * rr[i];
+            const uint64_t c2 = two(c, c), r2 = two(rr[i], rr[i]);
 #pragma unroll
-            for (int e = 0; e < V; ++e) tot[i][e] = r * tot[i][e] - yv[i][e] * c;
-            store(static_cast<T*>(p.dy) + (size_t)row * p.D + (size_t)vec * V, tot[i]);
+            for (int e = 0; e < V / 2; ++e) tot[i][e] = fma2(a[e], c2, mul2(r2, tot[i][e]));
+            store2(static_cast<T*>(p.dy) + (size_t)row * p.D + (size_t)vec * V, tot[i]);
         }
+        if (RING && ++stage == stages) stage = 0;
     }
+    if (RING) copies_done(0);
+    __syncthreads();   // the ring's room takes the sums
 
-    // sums of this block's rows: threadIdx.y groups in order, then one part per CTA
-    extern __shared__ float4 dyn4[];
-    float* dyn = reinterpret_cast<float*>(dyn4);   // [3][D] when blockDim.y > 1
+    // This block's sums: threadIdx.y groups in order, then one part per block.
+    // The part of dw_post holds one value per channel of a group: where a group
+    // is a head, its heads are added here, in order.
+    float* dyn = reinterpret_cast<float*>(dyn4);   // [tile]
+    const int col0 = blockIdx.y * tile, width = vecs * V - col0;
     float* mine = p.partial + (size_t)blockIdx.x * 3 * p.D;
-    float* sum = blockDim.y > 1 ? dyn : mine;
-    for (unsigned k = 0; k < blockDim.y; ++k) {
-        if (threadIdx.y == k) {
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                const int vec = vec0 + i * blockDim.x;
-                if (vec >= vecs) continue;
+    for (int which = 0; which < 3; ++which) {
+        if (which == 1 && !p.res_scale) continue;
+        if (which == 2 && !p.w_pre) continue;
+        for (unsigned k = 0; k < blockDim.y; ++k) {
+            if (threadIdx.y == k) {
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const int c = vec * V + e;
-                    sum[c] = (k ? sum[c] : 0.f) + a_post[i][e];
-                    sum[p.D + c] = (k ? sum[p.D + c] : 0.f) + a_res[i][e];
-                    sum[2 * p.D + c] = (k ? sum[2 * p.D + c] : 0.f) + a_pre[i][e];
+                for (int i = 0; i < VPT; ++i) {
+                    const int vec = vec0 + i * blockDim.x;
+                    if (vec >= vecs) continue;
+#pragma unroll
+                    for (int e = 0; e < V; e += 2) {
+                        float v0, v1;
+                        apart(which == 0   ? a_post[i][e / 2]
+                              : which == 1 ? a_res[i][e / 2]
+                                           : a_pre[i][e / 2],
+                              v0, v1);
+                        float* at = dyn + vec * V + e - col0;
+                        at[0] = k ? at[0] + v0 : v0;
+                        at[1] = k ? at[1] + v1 : v1;
+                    }
                 }
             }
+            __syncthreads();
         }
-        if (blockDim.y > 1) __syncthreads();
-    }
-    if (blockDim.y > 1) {
-        for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < 3 * p.D;
-             c += blockDim.x * blockDim.y)
-            mine[c] = dyn[c];
+        if (which == 0 && !whole) {
+            for (int c = flat; c < p.group; c += all) {
+                float v = dyn[c];
+                for (int at = c + p.group; at < width; at += p.group) v += dyn[at];
+                mine[blockIdx.y * p.group + c] = v;
+            }
+        } else {
+            for (int c = flat; c < width; c += all) mine[which * p.D + col0 + c] = dyn[c];
+        }
+        __syncthreads();
     }
 }
 
-// One CTA per 32 columns of one of the three sums: parts in order within each
-// of 8 rows of threads, then the rows in order.  dw_post of a head also adds
-// the heads.
-__global__ void block_norm_sums_kernel(BlockNorm p, int parts) {
-    __shared__ float buf[8][33];
+// One block per 128 columns of one of the three sums; 32 rows of threads take
+// the parts in turn, then the rows are added in order.  dw_post of heads has a
+// part per tile too.
+__global__ void __launch_bounds__(1024) block_norm_sums_kernel(BlockNorm p, int parts, int tiles) {
+    __shared__ float4 buf[32][32];
     const int which = blockIdx.y;
     float* dst = which == 0 ? p.dw_post : which == 1 ? p.dres_scale : p.dw_pre;
     const int width = which == 0 ? p.group : p.D;
-    if (!dst) return;
-    const int c = blockIdx.x * 32 + threadIdx.x;
-    if (blockIdx.x * 32 >= width) return;
-    float s = 0.f;
+    const int per = which == 0 && p.group != p.D ? tiles : 1;
+    if (!dst || blockIdx.x * 128 >= width) return;
+    const int c = blockIdx.x * 128 + threadIdx.x * 4, n = parts * per;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (c < width) {
-        for (int k = threadIdx.y; k < parts; k += 8) {
-            const float* part = p.partial + ((size_t)k * 3 + which) * p.D;
-            for (int at = c; at < p.D; at += width) s += part[at];
+#pragma unroll 8
+        for (int k = threadIdx.y; k < n; k += 32) {
+            const float4 v = *reinterpret_cast<const float4*>(
+                p.partial + ((size_t)(k / per) * 3 + which) * p.D + (k % per) * width + c);
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
         }
     }
     buf[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y == 0 && c < width) {
-        for (int k = 1; k < 8; ++k) s += buf[k][threadIdx.x];
-        dst[c] = s;
+#pragma unroll
+        for (int k = 1; k < 32; ++k) {
+            const float4 v = buf[k][threadIdx.x];
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        }
+        *reinterpret_cast<float4*>(dst + c) = s;
     }
 }
 
@@ -396,64 +645,99 @@ struct Shape {
     int tiles;
 };
 
-// Up to 512 threads on a row; short rows share a block of 128 threads.  Where
-// no sum runs over the row (heads, no pre norm) a wide one is cut into tiles of
-// 2048 columns, blocks of their own.
-Shape shape_of(int32_t D, bool coupled) {
+// Up to `most` threads on a row while two vectors a thread are enough, then 512;
+// short rows share a block of 128 threads.  Where no sum runs over the row
+// (heads, no pre norm) a wide one is cut into tiles, blocks of their own.
+Shape shape_of(int32_t D, bool coupled, int most) {
     Shape s;
-    s.tile = coupled || D <= 2048 ? D : 2048;
+    s.tile = coupled || D <= TILE ? D : TILE;
     s.tiles = (D + s.tile - 1) / s.tile;
     const int vecs = s.tile / V;
-    s.vpt = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4;
+    s.vpt = vecs <= most ? 1 : vecs <= 1024 ? 2 : 4;
     const int tx = ((vecs + s.vpt - 1) / s.vpt + 31) / 32 * 32;
     s.block = dim3(tx, tx >= 128 ? 1 : 128 / tx);
     return s;
 }
 
+constexpr int BACKWARD_THREADS = 256;
+constexpr size_t RING_HALF = 110 * 1024, RING_ALL = 220 * 1024;
+
 bool coupled(const BlockNorm& p) { return p.group == p.D || p.w_pre; }
 
 template <typename T>
 cudaError_t forward(const BlockNorm& p, cudaStream_t stream) {
-    const Shape s = shape_of(p.D, coupled(p));
-    const int64_t rows = (p.rows + s.block.y - 1) / s.block.y, most = 152 * 16 / s.tiles;
-    const dim3 grid((unsigned)(rows < most ? rows : most), s.tiles);
+    if (!coupled(p)) {
+        const int64_t vecs = p.rows * (p.D / V), blocks = (vecs + 1023) / 1024;
+        if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
+        block_norm_heads_kernel<T><<<(unsigned)blocks, 256, 0, stream>>>(p, vecs);
+        return cudaGetLastError();
+    }
+    const Shape s = shape_of(p.D, true, 512);
+    const int threads = s.block.x * s.block.y;
+    const int64_t rows = (p.rows + s.block.y - 1) / s.block.y, most = 152 * (1024 / threads);
+    const unsigned grid = (unsigned)(rows < most ? rows : most);
     switch (s.vpt) {
-        case 1: block_norm_kernel<T, 1><<<grid, s.block, 0, stream>>>(p, s.tile); break;
-        case 2: block_norm_kernel<T, 2><<<grid, s.block, 0, stream>>>(p, s.tile); break;
-        default: block_norm_kernel<T, 4><<<grid, s.block, 0, stream>>>(p, s.tile); break;
+        case 1: block_norm_kernel<T, 1><<<grid, s.block, 0, stream>>>(p); break;
+        case 2: block_norm_kernel<T, 2><<<grid, s.block, 0, stream>>>(p); break;
+        default: block_norm_kernel<T, 4><<<grid, s.block, 0, stream>>>(p); break;
     }
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t backward(const BlockNorm& p, cudaStream_t stream) {
-    const Shape s = shape_of(p.D, coupled(p));
+    const Shape s = shape_of(p.D, coupled(p), BACKWARD_THREADS);
     const int parts = block_norm_parts(p.rows, p.D);
     const dim3 grid(parts, s.tiles);
-    // rows that share a block add their sums in shared memory (one tile then)
-    const size_t smem = s.block.y > 1 ? (size_t)3 * p.D * sizeof(float) : 0;
-    switch (s.vpt) {
-        case 1:
-            block_norm_backward_kernel<T, 1><<<grid, s.block, smem, stream>>>(p, s.tile);
-            break;
-        case 2:
-            block_norm_backward_kernel<T, 2><<<grid, s.block, smem, stream>>>(p, s.tile);
-            break;
-        default:
-            block_norm_backward_kernel<T, 4><<<grid, s.block, smem, stream>>>(p, s.tile);
-            break;
+    // a ring of up to 3 rows in half of an SM's shared memory, of 2 in all of it
+    const size_t row = (size_t)TENSORS * s.vpt * s.block.x * s.block.y * V * sizeof(T);
+    const int stages = 3 * row <= RING_HALF ? 3 : 2 * row <= RING_ALL ? 2 : 0;
+    const size_t sums = (size_t)s.tile * sizeof(float), ring = stages * row;
+    const size_t smem = ring > sums ? ring : sums;
+    cudaError_t err = cudaSuccess;
+    auto launch = [&](auto kernel) {
+        if (smem > 48 * 1024) {
+            err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
+        }
+        if (err == cudaSuccess) kernel<<<grid, s.block, smem, stream>>>(p, s.tile, stages);
+    };
+    auto with_gate = [&](auto act) {
+        constexpr int ACT = decltype(act)::value;
+        if (stages == 0) {
+            launch(block_norm_backward_kernel<T, 4, ACT, false>);
+        } else if (s.vpt == 1) {
+            launch(block_norm_backward_kernel<T, 1, ACT, true>);
+        } else if (s.vpt == 2) {
+            launch(block_norm_backward_kernel<T, 2, ACT, true>);
+        } else {
+            launch(block_norm_backward_kernel<T, 4, ACT, true>);
+        }
+    };
+    if (!p.gate) {
+        with_gate(std::integral_constant<int, NO_GATE>());
+    } else if (p.silu) {
+        with_gate(std::integral_constant<int, SILU>());
+    } else {
+        with_gate(std::integral_constant<int, SIGMOID>());
     }
-    cudaError_t err = cudaGetLastError();
+    if (err == cudaSuccess) err = cudaGetLastError();
     if (err != cudaSuccess) return err;
-    block_norm_sums_kernel<<<dim3((p.D + 31) / 32, 3), dim3(32, 8), 0, stream>>>(p, parts);
+    block_norm_sums_kernel<<<dim3((p.D + 127) / 128, 3), dim3(32, 32), 0, stream>>>(p, parts,
+                                                                                    s.tiles);
     return cudaGetLastError();
 }
 
 }  // namespace
 
+// The backward's blocks along the rows: what keeps 152 SMs busy, fewer where
+// there are fewer rows.
 int block_norm_parts(int64_t rows, int32_t D) {
-    const int64_t y = shape_of(D, true).block.y, blocks = (rows + y - 1) / y;
-    return (int)(blocks < MAX_PARTS ? (blocks < 1 ? 1 : blocks) : MAX_PARTS);
+    const Shape s = shape_of(D, true, BACKWARD_THREADS);
+    const int threads = s.block.x * s.block.y;
+    const int most = 152 * (threads <= 128 ? 4 : threads <= 256 ? 2 : 1);
+    const int64_t blocks = (rows + s.block.y - 1) / s.block.y;
+    return (int)(blocks < most ? (blocks < 1 ? 1 : blocks) : most);
 }
 
 cudaError_t launch_block_norm(const BlockNorm& p, int dtype, cudaStream_t stream) {

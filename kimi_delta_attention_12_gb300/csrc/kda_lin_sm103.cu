@@ -25,6 +25,7 @@
 
 #include "kda_chunked.h"
 #include "kda_lin.cuh"
+#include "kda_packed.cuh"
 #include "sm103_ptx.cuh"
 
 namespace kda {
@@ -51,6 +52,8 @@ static_assert(SM_S >= STATE_STAGES * 2 * TILE, "the states' stages end before th
 constexpr uint32_t SMEM = SM_TAB + 2048 + 1024;          // tables, alignment
 static_assert(SMEM <= 232448, "more shared memory than a CTA may have");
 
+// All 512 columns of TMEM are allocated, so that their base is 0 and addresses
+// are constants.
 // TMEM columns of the pass.  P' (bf16 pairs) takes the first 16 of each 32
 // columns of P.
 constexpr uint32_t TC_P = 0;
@@ -124,51 +127,11 @@ __device__ __forceinline__ bool wait_warp(Bars* b, uint64_t* bar, uint32_t parit
     return false;
 }
 
-__device__ __forceinline__ uint32_t pack(float a, float b) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-// Two fp32 values in one register pair and the packed operations on them.
-__device__ __forceinline__ uint64_t two(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void apart(uint64_t v, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t two(uint32_t a, uint32_t b) {
-    return two(__uint_as_float(a), __uint_as_float(b));
-}
-__device__ __forceinline__ uint32_t pack(uint64_t v) {
-    float a, b;
-    apart(v, a, b);
-    return pack(a, b);
-}
-
 // One arrival for the calling warp, behind what all of its lanes did.
 __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
-
-__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
@@ -376,12 +339,12 @@ __device__ __forceinline__ void set_up(const Args& args, Cta& c, int issue, int 
     tc_fence_after();
 }
 
-__device__ __forceinline__ void finish(uint32_t tmem, int issue) {
+__device__ __forceinline__ void finish(const Cta& c, int issue) {
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (threadIdx.x >> 5 == issue) tmem_dealloc(tmem, 512);
+    if (threadIdx.x >> 5 == issue) tmem_dealloc(c.b->tmem, 512);
 }
 
 // Token range of the pass's step i.
@@ -447,7 +410,7 @@ __device__ __forceinline__ void issue_stores(const Args& args, const Cta& c) {
 // The products of all chunks, in the order in which the tensor core runs them.
 // P of the next chunk comes last: it fills the time that the state takes.
 template <bool REV>
-__device__ __forceinline__ void issue_products(const LinPass& p, const Cta& c, uint32_t tmem) {
+__device__ __forceinline__ void issue_products(const LinPass& p, const Cta& c) {
     Bars* b = c.b;
     constexpr uint32_t id_kk = idesc_bf16(D, D, 0, 0), id_km = idesc_bf16(D, D, 0, 1);
     const uint32_t base = smem_u32(c.sm), state = tile_mn(base + SM_S);
@@ -460,10 +423,10 @@ __device__ __forceinline__ void issue_products(const LinPass& p, const Cta& c, u
             if (!wait_warp(b, &b->s, ph, p, 304)) break;
             if (i > 0 && !wait_warp(b, &b->od, ph ^ 1, p, 314)) break;
             tc_fence_after();
-            product<false>(tmem + TC_O, x, state, id_km);
+            product<false>(TC_O, x, state, id_km);
 #pragma unroll
             for (int kk = 1; kk < 8; ++kk)
-                product<true>(tmem + TC_O, x + step_k(kk), state + step_mn(kk), id_km);
+                product<true>(TC_O, x + step_k(kk), state + step_mn(kk), id_km);
             commit(&b->o1);
             // a short chunk's z rows past its end are zeroed before P' is handed over
             if (chunk_len(c, chunk_start(c, REV, i)) < C && !wait_warp(b, &b->p, ph, p, 306)) break;
@@ -477,23 +440,23 @@ __device__ __forceinline__ void issue_products(const LinPass& p, const Cta& c, u
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        product_ta<true>(tmem + TC_O, tmem + TC_P + 32 * (kk >> 1) + 8 * (kk & 1),
+                        product_ta<true>(TC_O, TC_P + 32 * (kk >> 1) + 8 * (kk & 1),
                                          z + step_mn(kk), id_km);
                     commit(&b->o2);
                 }
                 if (!(ok = wait_warp(b, &b->w[buf], g >> 1, p, 305))) break;
                 tc_fence_after();
-                const uint32_t w = tmem + TC_W + 48 * buf;
+                const uint32_t w = TC_W + 48 * buf;
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
                     const uint32_t zk = z + step_mn(2 * g + kk);
                     if (g == 0 && kk == 0) {
-                        product_ta<false>(tmem + TC_U, w + 32, zk, id_km);
+                        product_ta<false>(TC_U, w + 32, zk, id_km);
                     } else {
-                        product_ta<true>(tmem + TC_U, w + 32 + 8 * kk, zk, id_km);
+                        product_ta<true>(TC_U, w + 32 + 8 * kk, zk, id_km);
                     }
-                    product_ta<true>(tmem + TC_U, w + 16 + 8 * kk, zk, id_km);
-                    product_ta<true>(tmem + TC_U, w + 8 * kk, zk, id_km);
+                    product_ta<true>(TC_U, w + 16 + 8 * kk, zk, id_km);
+                    product_ta<true>(TC_U, w + 8 * kk, zk, id_km);
                 }
                 commit(&b->wfree[buf]);
             }
@@ -507,10 +470,10 @@ __device__ __forceinline__ void issue_products(const LinPass& p, const Cta& c, u
             if (!wait_warp(b, &b->full[ph ^ 1], ((i + 1) >> 1) & 1, p, 302)) break;
             if (i >= 0 && !wait_warp(b, &b->o2, ph, p, 303)) break;   // P' has been read
             tc_fence_after();
-            product<false>(tmem + TC_P, x, y, id_kk);
+            product<false>(TC_P, x, y, id_kk);
 #pragma unroll
             for (int kk = 1; kk < 8; ++kk)
-                product<true>(tmem + TC_P, x + step_k(kk), y + step_k(kk), id_kk);
+                product<true>(TC_P, x + step_k(kk), y + step_k(kk), id_kk);
             commit(&b->qk);
         }
     }
@@ -763,13 +726,12 @@ __global__ void __launch_bounds__(THREADS, 1) lin_pass_tc_kernel(const __grid_co
     Cta c;
     if (!start(args, c)) return;
     set_up(args, c, 16, 4);
-    const uint32_t tmem = c.b->tmem;
     const int warp = threadIdx.x >> 5;
-    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // this warp's 32 TMEM lanes
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // this warp's 32 TMEM lanes
     if (warp >= 16) {
         give_registers<REGS_ISSUE>();
         if (warp == 17) {
-            issue_products<REV>(p, c, tmem);
+            issue_products<REV>(p, c);
         } else if ((threadIdx.x & 31) == 0) {
             if (warp == 16) issue_loads<REV>(args, c);
             if (warp == 18) issue_stores<REV>(args, c);
@@ -780,7 +742,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_pass_tc_kernel(const __grid_co
         take_registers<REGS_STATE>();
         states<REV>(p, c, lanes);
     }
-    finish(tmem, 16);
+    finish(c, 16);
 }
 
 // ------------------------------------------------- the state a segment adds
@@ -798,9 +760,8 @@ lin_states_tc_kernel(const __grid_constant__ Args args) {
     }
     set_up(args, c, 8, 8);
     Bars* b = c.b;
-    const uint32_t tmem = b->tmem;
     const int tid = threadIdx.x, warp = tid >> 5, n = c.chunks;
-    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     if (warp == 8) {
         if ((tid & 31) == 0) {
             int issued = 0;
@@ -822,22 +783,22 @@ lin_states_tc_kernel(const __grid_constant__ Args args) {
         for (int i = 0; i < n; ++i) {
             const int s = i % STATE_STAGES;
             const uint32_t z = tile_mn(smem_u32(c.sm) + s * 2 * TILE + TILE);
-            const uint32_t w = tmem + TS_W + 192 * (i & 1);
+            const uint32_t w = TS_W + 192 * (i & 1);
             if (!wait_warp(b, &b->full[s], (i / STATE_STAGES) & 1, p, 332)) break;
             if (!wait_warp(b, &b->w[i & 1], (i >> 1) & 1, p, 333)) break;
             tc_fence_after();
             if (i == 0) {
-                product_ta<false>(tmem + TS_U, w + 128, z, id);
+                product_ta<false>(TS_U, w + 128, z, id);
             } else {
-                product_ta<true>(tmem + TS_U, w + 128, z, id);
+                product_ta<true>(TS_U, w + 128, z, id);
             }
-            product_ta<true>(tmem + TS_U, w + 64, z, id);
-            product_ta<true>(tmem + TS_U, w, z, id);
+            product_ta<true>(TS_U, w + 64, z, id);
+            product_ta<true>(TS_U, w, z, id);
 #pragma unroll
             for (int kk = 1; kk < 8; ++kk)
 #pragma unroll
                 for (int part = 2; part >= 0; --part)
-                    product_ta<true>(tmem + TS_U, w + 64 * part + 8 * kk, z + step_mn(kk),
+                    product_ta<true>(TS_U, w + 64 * part + 8 * kk, z + step_mn(kk),
                                      id);
             commit(&b->wfree[i & 1]);
             commit(&b->empty[s]);
@@ -884,7 +845,7 @@ lin_states_tc_kernel(const __grid_constant__ Args args) {
             }
         }
     }
-    finish(tmem, 8);
+    finish(c, 8);
 }
 
 template <bool REV>

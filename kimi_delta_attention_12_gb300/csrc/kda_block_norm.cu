@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_kernel(BlockNorm p) {
             expand(cg[i], g);
             expand(cx[i], xs);
             branch<T>(u[i], g, rsqrtf(ss[i][0] / (float)p.group + p.eps),
-                   p.w_post + (vec * V) % p.group,
+                   p.w_post + (whole ? vec : vec & (lanes - 1)) * V,
                    p.res_scale ? p.res_scale + vec * V : nullptr, gate != nullptr, p.silu);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
@@ -334,6 +334,8 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_kernel(BlockNorm p) {
 // under way or at work; a thread copies what it reads itself, so that its own
 // wait is enough.  The registers that rows in flight would take go to the
 // sums.  Rows too wide for that (stages = 0) are read into registers.
+// FULL: a block takes one row at a time and its threads cover the columns
+// exactly, so that nothing needs a guard.
 enum { Y = 0, GATE = 1, DXO = 2, X = 3, DH = 4, TENSORS = 5 };
 
 __device__ __forceinline__ void copy16(void* smem, const void* src) {
@@ -354,7 +356,7 @@ __device__ __forceinline__ void copies_done(int behind) {   // all but the last 
 
 enum { NO_GATE = 0, SIGMOID = 1, SILU = 2 };
 
-template <typename T, int VPT, int ACT, bool RING>
+template <typename T, int VPT, int ACT, bool RING, bool FULL>
 __global__ void __launch_bounds__(MAX_THREADS)
 block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
     __shared__ float buf[2 * MAX_ROWS * 32 * 3];
@@ -386,7 +388,7 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int vec = vec0 + i * blockDim.x;
-                if (vec >= vecs) continue;
+                if (!FULL && vec >= vecs) continue;
                 const size_t at = (size_t)r * p.D + (size_t)vec * V;
 #pragma unroll
                 for (int k = 0; k < TENSORS; ++k) {
@@ -406,7 +408,7 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
     int stage = 0;
     const float inv_row = 1.0f / (float)p.D, inv_group = 1.0f / (float)p.group;
     for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < p.rows; r0 += step, row += step) {
-        const bool live = row < p.rows;
+        const bool live = FULL || row < p.rows;
         Raw<T> held[RING ? 1 : TENSORS][RING ? 1 : VPT];
         if (RING) {
             // the stage that the row before has left takes the next row to come
@@ -425,10 +427,10 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
                 }
         }
         auto get = [&](int k, int i, uint64_t (&v)[V / 2]) {
-            const bool in = live && src[k] && vec0 + i * (int)blockDim.x < vecs;
+            const bool in = FULL || (live && vec0 + i * (int)blockDim.x < vecs);
             if (RING) {
                 Raw<T> r;
-                clear(r);
+                if (!FULL) clear(r);
                 if (in) r = *slot(stage, k, i);
                 expand2(r, v);
             } else {
@@ -441,7 +443,7 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
         for (int i = 0; i < VPT; ++i) {
             const int vec = vec0 + i * blockDim.x;
             uint64_t a[V / 2], q0 = 0, q1 = 0, q2 = 0;
-            if (p.w_pre && vec < vecs) {
+            if (p.w_pre && (FULL || vec < vecs)) {
                 uint64_t w[V / 2], h[V / 2];
                 get(X, i, a);
                 get(DH, i, h);
@@ -481,10 +483,15 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int vec = vec0 + i * blockDim.x;
-            const bool in = live && vec < vecs;
+            const bool in = FULL || (live && vec < vecs);
             const size_t at = (size_t)row * p.D + (size_t)vec * V;
             uint64_t w[V / 2], part = 0;
-            get(DXO, i, tot[i]);
+            if (src[DXO]) {
+                get(DXO, i, tot[i]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e) tot[i][e] = 0;
+            }
             if (in && p.w_pre) {
                 uint64_t a[V / 2], h[V / 2];
                 get(X, i, a);
@@ -504,7 +511,7 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e) rs[e] = one;
                 if (p.res_scale) load2(p.res_scale + vec * V, rs);
-                load2(p.w_post + (vec * V) % p.group, w);
+                load2(p.w_post + (whole ? vec : vec & (lanes - 1)) * V, w);
                 get(Y, i, a);
                 if (ACT != NO_GATE) get(GATE, i, g);
 #pragma unroll
@@ -548,7 +555,7 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int vec = vec0 + i * blockDim.x;
-            if (!live || vec >= vecs) continue;
+            if (!FULL && (!live || vec >= vecs)) continue;
             uint64_t a[V / 2];
             get(Y, i, a);
             const float c = -cc[i] * rr[i] * rr[i] * rr[i];
@@ -702,16 +709,20 @@ cudaError_t backward(const BlockNorm& p, cudaStream_t stream) {
         }
         if (err == cudaSuccess) kernel<<<grid, s.block, smem, stream>>>(p, s.tile, stages);
     };
+    const bool full = s.block.y == 1 && p.D % s.tile == 0 &&
+                      s.tile == (int)s.block.x * s.vpt * V;
     auto with_gate = [&](auto act) {
         constexpr int ACT = decltype(act)::value;
         if (stages == 0) {
-            launch(block_norm_backward_kernel<T, 4, ACT, false>);
+            launch(block_norm_backward_kernel<T, 4, ACT, false, false>);
         } else if (s.vpt == 1) {
-            launch(block_norm_backward_kernel<T, 1, ACT, true>);
+            if (full) launch(block_norm_backward_kernel<T, 1, ACT, true, true>);
+            else launch(block_norm_backward_kernel<T, 1, ACT, true, false>);
         } else if (s.vpt == 2) {
-            launch(block_norm_backward_kernel<T, 2, ACT, true>);
+            if (full) launch(block_norm_backward_kernel<T, 2, ACT, true, true>);
+            else launch(block_norm_backward_kernel<T, 2, ACT, true, false>);
         } else {
-            launch(block_norm_backward_kernel<T, 4, ACT, true>);
+            launch(block_norm_backward_kernel<T, 4, ACT, true, false>);
         }
     };
     if (!p.gate) {

@@ -77,6 +77,8 @@ class KDAError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load libkda.so (built by ``__graft_entry__.build()``); raise if absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -647,36 +649,38 @@ def kda_state_io(op: int, dst: torch.Tensor, src: Optional[torch.Tensor] = None,
 
 
 # ---------------------------------------------------- decayed linear attention
-class _Launch:
-    """Where a call allocates and launches: the tensors' device, and the given
-    stream or that device's current one.  Memory allocated for the call
-    belongs to that stream, so that its reuse waits for the call's kernels."""
-
-    def __init__(self, stream: Optional[torch.cuda.Stream], first: torch.Tensor, *others):
-        if not first.is_cuda:
-            raise ValueError("KDA tensors must live on a CUDA device")
-        for t in others:
-            if t is not None and t.device != first.device:
+def _one_device(*ts) -> int:
+    """The device all given tensors live on; contiguity is checked on the way.
+    These calls take microseconds of GPU time, so their checks are kept to a
+    few attribute reads per tensor."""
+    dev = -1
+    for t in ts:
+        if t is not None:
+            d = t.get_device()
+            if d < 0:
+                raise ValueError("KDA tensors must live on a CUDA device")
+            if not t.is_contiguous():
+                raise ValueError("KDA tensors must be contiguous")
+            if dev < 0:
+                dev = d
+            elif d != dev:
                 raise ValueError("KDA tensors must live on one CUDA device")
-        self._device = None
-        if first.device.index != torch.cuda.current_device():
-            self._device = torch.cuda.device(first.device)
-        self._stream = stream
+    return dev
 
-    def __enter__(self):
-        if self._device is not None:
-            self._device.__enter__()
-        if self._stream is not None:
-            self._context = torch.cuda.stream(self._stream)
-            self._context.__enter__()
-            return self._stream.cuda_stream
-        return torch.cuda.current_stream().cuda_stream
 
-    def __exit__(self, *exc):
-        if self._stream is not None:
-            self._context.__exit__(*exc)
-        if self._device is not None:
-            self._device.__exit__(*exc)
+def _on(stream: Optional[torch.cuda.Stream], dev: int):
+    """The context a call allocates and launches in: its tensors' device, and the
+    given stream (memory allocated for the call then belongs to it, so that its
+    reuse waits for the call's kernels).  None where that is the present one."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if dev != torch.cuda.current_device():
+        return torch.cuda.device(dev)
+    return None
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _addr(t: Optional[torch.Tensor]):
@@ -706,12 +710,13 @@ def _lin_sizes(q, k, v, log_decay, cu_seqlens):
         raise ValueError(f"v must have shape {(total_T, H, d_v)}, got {tuple(v.shape)}")
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise TypeError("q, k and v must share one dtype")
-    _expect(log_decay, (H,), "log_decay", torch.float32)
+    if log_decay.shape != (H,) or log_decay.dtype != torch.float32:
+        _expect(log_decay, (H,), "log_decay", torch.float32)
     N = 1
     if cu_seqlens is not None:
         if cu_seqlens.dim() != 1 or cu_seqlens.dtype != torch.int32 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens must be a 1-D int32 tensor of N + 1 starts")
-        N = cu_seqlens.numel() - 1
+        N = cu_seqlens.shape[0] - 1
     return N, total_T, H, d_k, d_v
 
 
@@ -721,14 +726,13 @@ def _host_seqlens(cu_seqlens_host, N: int):
         return None
     if cu_seqlens_host.is_cuda or cu_seqlens_host.numel() != N + 1:
         raise ValueError(f"cu_seqlens_host must be a host tensor of {N + 1} starts")
+    if cu_seqlens_host.dtype == torch.int32 and cu_seqlens_host.is_contiguous():
+        return cu_seqlens_host
     return cu_seqlens_host.to(torch.int32).contiguous()
 
 
-def _workspace(workspace, nbytes: int, device):
-    if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    _check_cuda(workspace)
-    return workspace
+def _scratch(nbytes: int, device) -> torch.Tensor:
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def kda_lin_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
@@ -750,7 +754,7 @@ def kda_lin_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay
     if q.dim() == 4:
         batch = q.shape[:2]
         q, k, v = (t.reshape(-1, *t.shape[2:]) for t in (q, k, v))
-    _check_cuda(q, k, v, log_decay, initial_state, cu_seqlens, o, final_state)
+    dev = _one_device(q, k, v, log_decay, initial_state, cu_seqlens, o, final_state, workspace)
     N, total_T, H, d_k, d_v = _lin_sizes(q, k, v, log_decay, cu_seqlens)
     if batch is not None:
         if cu_seqlens is not None:
@@ -765,20 +769,25 @@ def kda_lin_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay
         _expect(o, (*batch, H, d_v), "o", dt)
         o = o.view(total_T, H, d_v)
     _expect(o, (total_T, H, d_v), "o", dt)
-    with _Launch(stream, q, k, v, log_decay, initial_state, cu_seqlens, o, final_state,
-                 workspace) as s:
+    on = _on(stream, dev)
+    if on is not None:
+        on.__enter__()
+    try:
         if o is None:
-            o = torch.empty((total_T, H, d_v), dtype=dt, device=q.device)
+            o = torch.empty_like(v)
         if final_state is None and output_final_state:
             final_state = torch.empty((N, H, d_k, d_v), dtype=torch.float32, device=q.device)
         if workspace is None:
-            workspace = _workspace(None, lin_prefill_workspace_bytes(N, total_T, H, d_k, d_v, dt),
-                                   q.device)
+            workspace = _scratch(lin_prefill_workspace_bytes(N, total_T, H, d_k, d_v, dt),
+                                 q.device)
         st = lib().kda_lin_prefill(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _addr(initial_state),
             _addr(cu_seqlens), _addr(host_cu), N, total_T, H, d_k, d_v, code, scale,
             KDA_FLAG_RECURRENT if recurrent else 0, o.data_ptr(), _addr(final_state),
-            workspace.data_ptr(), _nbytes(workspace), s)
+            workspace.data_ptr(), workspace.nbytes, _raw_stream(dev))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
     if st != KDA_OK:
         raise KDAError(st, "kda_lin_prefill")
     return (o if batch is None else o.view(*batch, H, d_v)), final_state
@@ -792,21 +801,27 @@ def kda_lin_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """One decode token of the decayed linear attention per sequence: q, k
     [B, H, d_k], v [B, H, d_v]; `state` [pool, H, d_k, d_v] fp32 is updated in
     place at rows `slots` (default 0..B-1).  Returns o [B, H, d_v]."""
-    _check_cuda(q, k, v, log_decay, state, slots, o)
+    dev = _one_device(q, k, v, log_decay, state, slots, o)
     _, B, H, d_k, d_v = _lin_sizes(q, k, v, log_decay, None)
     dt = q.dtype
     code = _dtype_code(dt)
-    if state.dim() != 4:
-        raise ValueError("state must have shape [pool, H, d_k, d_v]")
-    _expect(state, (state.shape[0], H, d_k, d_v), "state", torch.float32)
+    pool = state.shape[0]
+    if state.shape != (pool, H, d_k, d_v) or state.dtype != torch.float32:
+        raise ValueError(f"state must be a float32 [pool, {H}, {d_k}, {d_v}] tensor")
     _expect(slots, (B,), "slots", torch.int32)
     _expect(o, (B, H, d_v), "o", dt)
-    with _Launch(stream, q, k, v, log_decay, state, slots, o) as s:
+    on = _on(stream, dev)
+    if on is not None:
+        on.__enter__()
+    try:
         if o is None:
-            o = torch.empty((B, H, d_v), dtype=dt, device=q.device)
+            o = torch.empty_like(v)
         st = lib().kda_lin_decode_step(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state.data_ptr(),
-            _addr(slots), state.shape[0], B, H, d_k, d_v, code, scale, o.data_ptr(), s)
+            _addr(slots), pool, B, H, d_k, d_v, code, scale, o.data_ptr(), _raw_stream(dev))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
     if st != KDA_OK:
         raise KDAError(st, "kda_lin_decode_step")
     return o
@@ -823,28 +838,33 @@ def kda_lin_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     packed inputs; dO [total_T, H, d_v] in the inputs' dtype, dS_final
     [N, H, d_k, d_v] fp32 or None.  Returns a dict: dq, dk [total_T, H, d_k] and
     dv [total_T, H, d_v] in the inputs' dtype, dS0 [N, H, d_k, d_v] fp32."""
-    _check_cuda(q, k, v, log_decay, dO, initial_state, cu_seqlens, dS_final)
+    dev = _one_device(q, k, v, log_decay, dO, initial_state, cu_seqlens, dS_final, workspace)
     N, total_T, H, d_k, d_v = _lin_sizes(q, k, v, log_decay, cu_seqlens)
     dt = q.dtype
     code = _dtype_code(dt)
-    _expect(dO, (total_T, H, d_v), "dO", dt)
+    if dO.shape != v.shape or dO.dtype != dt:
+        _expect(dO, (total_T, H, d_v), "dO", dt)
     _expect(initial_state, (N, H, d_k, d_v), "initial_state", torch.float32)
     _expect(dS_final, (N, H, d_k, d_v), "dS_final", torch.float32)
     host_cu = _host_seqlens(cu_seqlens_host, N)
-    with _Launch(stream, q, k, v, log_decay, dO, initial_state, cu_seqlens, dS_final,
-                 workspace) as s:
-        dev = q.device
+    on = _on(stream, dev)
+    if on is not None:
+        on.__enter__()
+    try:
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        dS0 = torch.empty((N, H, d_k, d_v), dtype=torch.float32, device=dev)
+        dS0 = torch.empty((N, H, d_k, d_v), dtype=torch.float32, device=q.device)
         if workspace is None:
-            workspace = _workspace(None,
-                                   lin_backward_workspace_bytes(N, total_T, H, d_k, d_v, dt), dev)
+            workspace = _scratch(lin_backward_workspace_bytes(N, total_T, H, d_k, d_v, dt),
+                                 q.device)
         st = lib().kda_lin_backward(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _addr(initial_state),
             _addr(cu_seqlens), _addr(host_cu), N, total_T, H, d_k, d_v, code, scale,
             KDA_FLAG_RECURRENT if recurrent else 0, dO.data_ptr(), _addr(dS_final),
             dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dS0.data_ptr(), workspace.data_ptr(),
-            _nbytes(workspace), s)
+            workspace.nbytes, _raw_stream(dev))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
     if st != KDA_OK:
         raise KDAError(st, "kda_lin_backward")
     return dict(dq=dq, dk=dk, dv=dv, dS0=dS0)
@@ -854,23 +874,27 @@ def kda_lin_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
 def _norm_sizes(y, w_post, gate, x, res_scale, w_pre, gate_act):
     """(rows, D, group, gate code) of a block norm, shapes and types checked;
     the leading dimensions of y are rows."""
-    if y.dim() < 1 or w_post.dim() != 1:
+    shape, dt = y.shape, y.dtype
+    if not shape or w_post.dim() != 1:
         raise ValueError("y must have shape [..., D] and w_post [group]")
-    D, group = y.shape[-1], w_post.shape[0]
-    for name, t in (("gate", gate), ("x", x)):
-        if t is not None and (t.shape != y.shape or t.dtype != y.dtype):
-            raise ValueError(f"{name} must be a {y.dtype} tensor of shape {tuple(y.shape)}, "
-                             f"got {t.dtype} {tuple(t.shape)}")
-    _expect(w_post, (group,), "w_post", torch.float32)
-    _expect(res_scale, (D,), "res_scale", torch.float32)
-    _expect(w_pre, (D,), "w_pre", torch.float32)
+    D = shape[-1]
+    if (gate is not None and (gate.shape != shape or gate.dtype != dt)) or (
+            x is not None and (x.shape != shape or x.dtype != dt)):
+        raise ValueError(f"gate and x must be {dt} tensors of y's shape {tuple(shape)}")
+    for name, t, n in (("w_post", w_post, None), ("res_scale", res_scale, D),
+                       ("w_pre", w_pre, D)):
+        if t is not None:
+            if t.dtype != torch.float32:
+                raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
+            if n is not None and t.shape != (n,):
+                raise ValueError(f"{name} must have shape {(n,)}, got {tuple(t.shape)}")
     if gate is None:
         act = KDA_GATE_SIGMOID
     elif gate_act in _GATE_ACTS:
         act = _GATE_ACTS[gate_act]
     else:
         raise ValueError(f"gate_act must be one of {sorted(_GATE_ACTS)}, got {gate_act!r}")
-    return (y.numel() // D if D else 0), D, group, act
+    return (y.numel() // D if D else 0), D, w_post.shape[0], act
 
 
 def kda_block_norm(y: torch.Tensor, w_post: torch.Tensor, gate: Optional[torch.Tensor] = None,
@@ -886,19 +910,26 @@ def kda_block_norm(y: torch.Tensor, w_post: torch.Tensor, gate: Optional[torch.T
     or 128 channels that divides D); res_scale, w_pre [D] fp32; every part but
     y and w_post optional.  gate_act: "sigmoid" or "silu" (unused without a
     gate).  Returns (x_out, h), h None without w_pre."""
-    _check_cuda(y, w_post, gate, x, res_scale, w_pre, x_out, h)
+    dev = _one_device(y, w_post, gate, x, res_scale, w_pre, x_out, h)
     rows, D, group, act = _norm_sizes(y, w_post, gate, x, res_scale, w_pre, gate_act)
     code = _dtype_code(y.dtype)
-    _expect(x_out, tuple(y.shape), "x_out", y.dtype)
-    _expect(h, tuple(y.shape), "h", y.dtype)
-    with _Launch(stream, y, w_post, gate, x, res_scale, w_pre, x_out, h) as s:
+    _expect(x_out, y.shape, "x_out", y.dtype)
+    _expect(h, y.shape, "h", y.dtype)
+    on = _on(stream, dev)
+    if on is not None:
+        on.__enter__()
+    try:
         if x_out is None:
             x_out = torch.empty_like(y)
         if h is None and w_pre is not None:
             h = torch.empty_like(y)
         st = lib().kda_block_norm(
             y.data_ptr(), w_post.data_ptr(), _addr(gate), _addr(x), _addr(res_scale),
-            _addr(w_pre), rows, D, group, code, act, eps, x_out.data_ptr(), _addr(h), s)
+            _addr(w_pre), rows, D, group, code, act, eps, x_out.data_ptr(), _addr(h),
+            _raw_stream(dev))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
     if st != KDA_OK:
         raise KDAError(st, "kda_block_norm")
     return x_out, h
@@ -923,26 +954,33 @@ def kda_block_norm_backward(y: torch.Tensor, w_post: torch.Tensor,
     it (needed with w_pre).  residual=False leaves dx out.  Returns a dict of
     dy, dgate, dx in y's dtype and dw_post, dres_scale, dw_pre fp32, None where
     the forward had no such input."""
-    _check_cuda(y, w_post, dx_out, gate, x_out, res_scale, w_pre, dh)
+    dev = _one_device(y, w_post, dx_out, gate, x_out, res_scale, w_pre, dh, workspace)
     rows, D, group, act = _norm_sizes(y, w_post, gate, x_out, res_scale, w_pre, gate_act)
-    code = _dtype_code(y.dtype)
+    shape, dt = y.shape, y.dtype
+    code = _dtype_code(dt)
     for name, t in (("dx_out", dx_out), ("dh", dh)):
-        _expect(t, tuple(y.shape), name, y.dtype)
-    with _Launch(stream, y, w_post, dx_out, gate, x_out, res_scale, w_pre, dh, workspace) as s:
-        dev = y.device
+        if t is not None and (t.shape != shape or t.dtype != dt):
+            _expect(t, shape, name, dt)
+    on = _on(stream, dev)
+    if on is not None:
+        on.__enter__()
+    try:
         dy = torch.empty_like(y)
         dgate = None if gate is None else torch.empty_like(y)
         dx = torch.empty_like(y) if residual else None
-        dw_post = torch.empty(group, dtype=torch.float32, device=dev)
+        dw_post = torch.empty_like(w_post)
         dres = None if res_scale is None else torch.empty_like(res_scale)
         dw_pre = None if w_pre is None else torch.empty_like(w_pre)
         if workspace is None:
-            workspace = _workspace(None, block_norm_backward_workspace_bytes(rows, D, group), dev)
+            workspace = _scratch(block_norm_backward_workspace_bytes(rows, D, group), y.device)
         st = lib().kda_block_norm_backward(
             y.data_ptr(), w_post.data_ptr(), _addr(gate), _addr(x_out), _addr(res_scale),
             _addr(w_pre), _addr(dx_out), _addr(dh), rows, D, group, code, act, eps,
             dy.data_ptr(), _addr(dgate), _addr(dx), dw_post.data_ptr(), _addr(dres),
-            _addr(dw_pre), workspace.data_ptr(), _nbytes(workspace), s)
+            _addr(dw_pre), workspace.data_ptr(), workspace.nbytes, _raw_stream(dev))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
     if st != KDA_OK:
         raise KDAError(st, "kda_block_norm_backward")
     return dict(dy=dy, dgate=dgate, dx=dx, dw_post=dw_post, dres_scale=dres, dw_pre=dw_pre)

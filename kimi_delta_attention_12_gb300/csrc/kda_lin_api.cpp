@@ -38,14 +38,17 @@ bool on_tensor_cores(int32_t d_k, int32_t d_v, kda_dtype dt, uint32_t flags, int
 // The tensor-core form works on a (sequence, head) pair with one CTA, the
 // CUDA-core form with one for each 32 columns of dz.
 int32_t segment_tokens(int32_t N, int32_t total_T, int32_t H, int32_t dz, bool tc) {
-    return kda::lin_segment_tokens(N, total_T, H, tc ? 1 : dz / 32, sm_count());
+    return kda::lin_segment_tokens(N, total_T, H, tc ? 1 : dz / 32, tc ? 1 : 3, sm_count());
 }
 
-// The segment of the form that cuts finer, whose states need most room.
+// The segment of the form (and, in the backward, the direction) that cuts
+// finest, whose states need most room.
 int32_t finest_segment(int32_t N, int32_t total_T, int32_t H, int32_t d_k, int32_t d_v,
                        kda_dtype dt) {
-    const int32_t dz = d_k < d_v ? d_k : d_v;
-    return segment_tokens(N, total_T, H, dz, on_tensor_cores(d_k, d_v, dt, 0, total_T));
+    const int32_t a = segment_tokens(N, total_T, H, d_k < d_v ? d_k : d_v, false);
+    if (!on_tensor_cores(d_k, d_v, dt, 0, total_T)) return a;
+    const int32_t b = segment_tokens(N, total_T, H, 0, true);
+    return a < b ? a : b;
 }
 
 size_t seg_state_bytes(int32_t total_T, int32_t H, int32_t dx, int32_t dz, int32_t seg_len) {
@@ -125,7 +128,7 @@ int kda_lin_prefill(const void* q, const void* k, const void* v, const float* lo
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     const bool tc = on_tensor_cores(d_k, d_v, dt, flags, total_T);
-    if (cudaMemsetAsync(ws, 0, sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
+    if (tc && cudaMemsetAsync(ws, 0, sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
     kda::LinPass p;
     memset(&p, 0, sizeof(p));
     p.x = q; p.y = k; p.z = v; p.out = o;
@@ -233,8 +236,8 @@ int kda_lin_backward(const void* q, const void* k, const void* v, const float* l
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
-    if (cudaMemsetAsync(ws, 0, sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
     const bool tc = on_tensor_cores(d_k, d_v, dt, flags, total_T);
+    if (tc && cudaMemsetAsync(ws, 0, sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
     kda::LinPass p;
     memset(&p, 0, sizeof(p));
     p.log_decay = log_decay;

@@ -17,6 +17,7 @@
 #include <limits.h>
 
 #include "kda_lin.cuh"
+#include "kda_packed.cuh"
 
 namespace kda {
 namespace {
@@ -44,12 +45,15 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
     *reinterpret_cast<uint2*>(p) = r;
 }
 
+constexpr int PLD = C + 4;   // row of a 32 x 32 tile of products
+
 template <int DX>
 constexpr size_t pass_smem_bytes() {
-    return sizeof(float) * (2 * C * (DX + 4) + C * SLICE + C * (C + 1) + DX * SLICE + C + 1);
+    return sizeof(float) *
+           (2 * C * (DX + 4) + C * SLICE + 4 * C * PLD + DX * SLICE + (C + 4));
 }
 
-// S[d][0..31] of one (sequence, head) slice, in a turned or plain state.
+// 4 values at the thread's rows of a state: row d of [dx][dz], or of a turned one.
 __device__ __forceinline__ float4 state_at(const float* st, int d, int c, int dx, int dz,
                                            int turned) {
     if (!turned) return load4(st + (size_t)d * dz + c);
@@ -57,7 +61,39 @@ __device__ __forceinline__ float4 state_at(const float* st, int d, int c, int dx
                        st[(size_t)(c + 2) * dx + d], st[(size_t)(c + 3) * dx + d]);
 }
 
+__device__ __forceinline__ void add_scaled(float4& acc, float w, float4 v) {
+    acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
+}
+
+// acc[i][j] += a row of 4 values times b's: the products of 4 rows with 4 rows
+// over 4 summed values, in pairs.
+__device__ __forceinline__ void dot4(uint64_t (&acc)[4][4], const float4 (&a)[4],
+                                     const float4 (&b)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc[i][j] = fma2(two(a[i].z, a[i].w), two(b[j].z, b[j].w),
+                             fma2(two(a[i].x, a[i].y), two(b[j].x, b[j].y), acc[i][j]));
+}
+
+// acc[i] += sum over 4 rows k of a[i][k] b[k].
+__device__ __forceinline__ void mul4(float4 (&acc)[4], const float4 (&a)[4], const float4 (&b)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        add_scaled(acc[i], a[i].x, b[0]);
+        add_scaled(acc[i], a[i].y, b[1]);
+        add_scaled(acc[i], a[i].z, b[2]);
+        add_scaled(acc[i], a[i].w, b[3]);
+    }
+}
+
 // STATES: only the state that the segment adds, into seg_states.
+//
+// The two 32 x 32 products (x . y, and the outputs) are formed by four groups of
+// 64 threads, each over a quarter of the summed index in 4 x 4 tiles (16
+// multiply-adds for every two 16-byte reads of shared memory), and the quarters
+// added in order; the state's product has 4 columns and dx / 32 rows a thread.
 template <typename T, int DX, bool STATES>
 __global__ void __launch_bounds__(THREADS) lin_pass_kernel(LinPass p) {
     constexpr int LD = DX + 4, ROWS = DX / 32;
@@ -65,8 +101,8 @@ __global__ void __launch_bounds__(THREADS) lin_pass_kernel(LinPass p) {
     float* X = reinterpret_cast<float*>(smem4);
     float* Y = X + C * LD;
     float* Z = Y + C * LD;
-    float* P = Z + C * SLICE;         // [C][C + 1]
-    float* S = P + C * (C + 1);
+    float* P = Z + C * SLICE;         // [4][C][PLD]
+    float* S = P + 4 * C * PLD;       // [DX][SLICE]
     float* lam = S + DX * SLICE;      // a^0 .. a^C
 
     const int tid = threadIdx.x, dz = p.dz, slices = dz / SLICE;
@@ -81,137 +117,176 @@ __global__ void __launch_bounds__(THREADS) lin_pass_kernel(LinPass p) {
 
     const size_t state_floats = (size_t)DX * dz;
     const int64_t rows = lin::seg_rows(p.total_T, p.seg_len);
-    const int c4 = (tid & 7) * 4;     // 4 columns of the slice, and rows (tid / 8) + 32 i
-    {
-        float4 st[ROWS];
+    const int c4 = (tid & 7) * 4, d0 = (tid / 8) * ROWS;   // the thread's part of the state
+    float4 st[ROWS];
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) st[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (!STATES) {
-            if (p.state_in) {
-                const float* s0 = p.state_in + ((size_t)sg.n * p.H + h) * state_floats;
+    for (int i = 0; i < ROWS; ++i) st[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!STATES) {
+        if (p.state_in) {
+            const float* s0 = p.state_in + ((size_t)sg.n * p.H + h) * state_floats;
 #pragma unroll
-                for (int i = 0; i < ROWS; ++i)
-                    st[i] = state_at(s0, tid / 8 + 32 * i, col0 + c4, DX, dz, p.state_in_turned);
-            }
-            for (int i = 0; i < sg.j; ++i) {   // join the segments before this one
-                int64_t a, b;
-                lin::seg_tokens(sg, i, p.seg_len, p.reverse, a, b);
-                const float f = lin::decay_pow(g, b - a);
-                if (sg.u + i >= rows) break;   // only a malformed cu_seqlens
-                const float* u = p.seg_states + ((sg.u + i) * (int64_t)p.H + h) * state_floats;
+            for (int i = 0; i < ROWS; ++i)
+                st[i] = state_at(s0, d0 + i, col0 + c4, DX, dz, p.state_in_turned);
+        }
+#pragma unroll 4
+        for (int i = 0; i < sg.j; ++i) {   // join the segments before this one
+            int64_t a, b;
+            lin::seg_tokens(sg, i, p.seg_len, p.reverse, a, b);
+            const float f = lin::decay_pow(g, b - a);
+            if (sg.u + i >= rows) break;   // only a malformed cu_seqlens
+            const float* u = p.seg_states + ((sg.u + i) * (int64_t)p.H + h) * state_floats;
 #pragma unroll
-                for (int r = 0; r < ROWS; ++r) {
-                    const float4 v = load4(u + (size_t)(tid / 8 + 32 * r) * dz + col0 + c4);
-                    st[r].x = f * st[r].x + v.x;
-                    st[r].y = f * st[r].y + v.y;
-                    st[r].z = f * st[r].z + v.z;
-                    st[r].w = f * st[r].w + v.w;
-                }
+            for (int r = 0; r < ROWS; ++r) {
+                const float4 v = load4(u + (size_t)(d0 + r) * dz + col0 + c4);
+                st[r].x = f * st[r].x + v.x;
+                st[r].y = f * st[r].y + v.y;
+                st[r].z = f * st[r].z + v.z;
+                st[r].w = f * st[r].w + v.w;
             }
         }
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) store4(S + (tid / 8 + 32 * i) * SLICE + c4, st[i]);
     }
-    __syncthreads();
 
     const T* x = static_cast<const T*>(p.x);
     const T* y = static_cast<const T*>(p.y);
     const T* z = static_cast<const T*>(p.z);
     T* out = static_cast<T*>(p.out);
+    // group of the thread, and its tile's rows r + 8 i and columns q + 8 j (of
+    // x . y) or 4 q .. 4 q + 3 (of the outputs)
+    const int grp = tid / 64, r = (tid / 8) & 7, q = tid & 7;
     const int64_t chunks = (sg.t1 - sg.t0 + C - 1) / C;
     for (int64_t ci = 0; ci < chunks; ++ci) {
         const int64_t c0 = sg.t0 + (p.reverse ? chunks - 1 - ci : ci) * C;
         const int len = (int)(sg.t1 - c0 < C ? sg.t1 - c0 : C);
-        for (int i = tid; i < C * DX / 4; i += THREADS) {
-            const int r = i / (DX / 4), d = (i % (DX / 4)) * 4;
+#pragma unroll
+        for (int k = 0; k < C * DX / 4 / THREADS; ++k) {
+            const int i = tid + k * THREADS, row = i / (DX / 4), d = (i % (DX / 4)) * 4;
             float4 vx = make_float4(0.f, 0.f, 0.f, 0.f), vy = vx;
-            if (r < len) {
-                const size_t at = ((size_t)(c0 + r) * p.H + h) * DX + d;
+            if (row < len) {
+                const size_t at = ((size_t)(c0 + row) * p.H + h) * DX + d;
                 if (!STATES) vx = load4(x + at);
                 vy = load4(y + at);
             }
-            if (!STATES) store4(X + r * LD + d, vx);
-            store4(Y + r * LD + d, vy);
+            if (!STATES) store4(X + row * LD + d, vx);
+            store4(Y + row * LD + d, vy);
         }
         {
-            const int r = tid / 8;
+            const int row = tid / 8;
             float4 vz = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < len) vz = load4(z + ((size_t)(c0 + r) * p.H + h) * dz + col0 + c4);
-            store4(Z + r * SLICE + c4, vz);
+            if (row < len) vz = load4(z + ((size_t)(c0 + row) * p.H + h) * dz + col0 + c4);
+            store4(Z + row * SLICE + c4, vz);
+        }
+        if (!STATES) {
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) store4(S + (d0 + i) * SLICE + c4, st[i]);
         }
         __syncthreads();
         if (!STATES) {
-            const int r0 = (tid / 16) * 2, q0 = tid % 16;   // rows r0, r0 + 1; columns q0, q0 + 16
-            float acc[2][2] = {};
+            {
+                uint64_t acc[4][4] = {};
 #pragma unroll 4
-            for (int d = 0; d < DX; d += 4) {
-                float4 a[2], b[2];
-                a[0] = load4(X + r0 * LD + d);
-                a[1] = load4(X + (r0 + 1) * LD + d);
-                b[0] = load4(Y + q0 * LD + d);
-                b[1] = load4(Y + (q0 + 16) * LD + d);
+                for (int d = grp * (DX / 4); d < (grp + 1) * (DX / 4); d += 4) {
+                    float4 a[4], b[4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        acc[i][j] += a[i].x * b[j].x + a[i].y * b[j].y + a[i].z * b[j].z +
-                                     a[i].w * b[j].w;
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int t = r0 + i, s = q0 + 16 * j, dist = p.reverse ? s - t : t - s;
-                    P[t * (C + 1) + s] =
-                        dist >= 0 && s < len ? acc[i][j] * lam[dist] * p.kv_scale : 0.0f;
+                    for (int i = 0; i < 4; ++i) {
+                        a[i] = load4(X + (r + 8 * i) * LD + d);
+                        b[i] = load4(Y + (q + 8 * i) * LD + d);
+                    }
+                    dot4(acc, a, b);
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        P[(grp * C + r + 8 * i) * PLD + q + 8 * j] = sum2(acc[i][j]);
+            }
+            __syncthreads();
+            {
+                // the quarters together, masked and weighted
+                const int t = tid / 8;
+                float4 v = load4(P + t * PLD + c4);
+#pragma unroll
+                for (int k = 1; k < 4; ++k) {
+                    const float4 w = load4(P + (k * C + t) * PLD + c4);
+                    v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+                }
+                float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int s = c4 + j, dist = p.reverse ? s - t : t - s;
+                    e[j] = dist >= 0 && s < len ? e[j] * (lam[dist & (C - 1)] * p.kv_scale) : 0.0f;
+                }
+                store4(P + t * PLD + c4, make_float4(e[0], e[1], e[2], e[3]));
+            }
+            __syncthreads();
+            {
+                float4 intra[4], inter[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) intra[i] = inter[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int s = 8 * grp; s < 8 * grp + 8; s += 4) {
+                    float4 a[4], b[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        a[i] = load4(P + (r + 8 * i) * PLD + s);
+                        b[i] = load4(Z + (s + i) * SLICE + 4 * q);
+                    }
+                    mul4(intra, a, b);
+                }
+#pragma unroll 4
+                for (int d = grp * (DX / 4); d < (grp + 1) * (DX / 4); d += 4) {
+                    float4 a[4], b[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        a[i] = load4(X + (r + 8 * i) * LD + d);
+                        b[i] = load4(S + (d + i) * SLICE + 4 * q);
+                    }
+                    mul4(inter, a, b);
+                }
+                __syncthreads();   // P is read; its room takes the quarters of the outputs
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = r + 8 * i;
+                    const float f = t < len ? lam[p.reverse ? len - 1 - t : t + 1] : 0.0f;
+                    add_scaled(intra[i], f, inter[i]);
+                    store4(P + (grp * C + t) * PLD + 4 * q, intra[i]);
+                }
+            }
             __syncthreads();
             const int t = tid / 8;
-            float4 intra = make_float4(0.f, 0.f, 0.f, 0.f), inter = intra;
-            // no token that is masked for this row is touched, not even times zero
-            const int s0 = p.reverse ? t : 0, s1 = p.reverse ? len : t + 1;
-#pragma unroll 4
-            for (int s = s0; s < s1; ++s) {
-                const float w = P[t * (C + 1) + s];
-                const float4 v = load4(Z + s * SLICE + c4);
-                intra.x += w * v.x; intra.y += w * v.y; intra.z += w * v.z; intra.w += w * v.w;
-            }
-#pragma unroll 8
-            for (int d = 0; d < DX; ++d) {
-                const float w = X[t * LD + d];
-                const float4 v = load4(S + d * SLICE + c4);
-                inter.x += w * v.x; inter.y += w * v.y; inter.z += w * v.z; inter.w += w * v.w;
-            }
             if (t < len) {
-                const float f = lam[p.reverse ? len - 1 - t : t + 1], m = p.out_scale;
-                store4(out + ((size_t)(c0 + t) * p.H + h) * dz + col0 + c4,
-                       make_float4(m * (intra.x + f * inter.x), m * (intra.y + f * inter.y),
-                                   m * (intra.z + f * inter.z), m * (intra.w + f * inter.w)));
-            }
-            __syncthreads();   // S and the operands are read before S moves on
-        }
-        {
-            const float f = lam[len];
-            float4 st[ROWS];
+                float4 v = load4(P + t * PLD + c4);
 #pragma unroll
-            for (int i = 0; i < ROWS; ++i) {
-                st[i] = load4(S + (tid / 8 + 32 * i) * SLICE + c4);
-                st[i].x *= f; st[i].y *= f; st[i].z *= f; st[i].w *= f;
-            }
-            for (int s = 0; s < len; ++s) {
-                const float w = lam[p.reverse ? s + 1 : len - 1 - s] * p.kv_scale;
-                float4 v = load4(Z + s * SLICE + c4);
-                v.x *= w; v.y *= w; v.z *= w; v.w *= w;
-#pragma unroll
-                for (int i = 0; i < ROWS; ++i) {
-                    const float k = Y[s * LD + tid / 8 + 32 * i];
-                    st[i].x += k * v.x; st[i].y += k * v.y; st[i].z += k * v.z; st[i].w += k * v.w;
+                for (int k = 1; k < 4; ++k) {
+                    const float4 w = load4(P + (k * C + t) * PLD + c4);
+                    v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
                 }
+                const float m = p.out_scale;
+                store4(out + ((size_t)(c0 + t) * p.H + h) * dz + col0 + c4,
+                       make_float4(m * v.x, m * v.y, m * v.z, m * v.w));
+            }
+        }
+        const float f = lam[len];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            st[i].x *= f; st[i].y *= f; st[i].z *= f; st[i].w *= f;
+        }
+#pragma unroll 8
+        for (int s = 0; s < C; ++s) {     // rows past the end are zeros
+            const float w = lam[p.reverse ? s + 1 : (len - 1 - s) & (C - 1)] * p.kv_scale;
+            float4 v = load4(Z + s * SLICE + c4);
+            v.x *= w; v.y *= w; v.z *= w; v.w *= w;
+            float k[ROWS];
+            if (ROWS == 4) {
+                const float4 k4 = load4(Y + s * LD + d0);
+                k[0] = k4.x; k[1 % ROWS] = k4.y; k[2 % ROWS] = k4.z; k[3 % ROWS] = k4.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i) k[i] = Y[s * LD + d0 + i];
             }
 #pragma unroll
-            for (int i = 0; i < ROWS; ++i) store4(S + (tid / 8 + 32 * i) * SLICE + c4, st[i]);
+            for (int i = 0; i < ROWS; ++i) add_scaled(st[i], k[i], v);
         }
-        __syncthreads();
+        __syncthreads();   // the next chunk's rows overwrite this one's
     }
 
     float* dst = nullptr;
@@ -223,10 +298,7 @@ __global__ void __launch_bounds__(THREADS) lin_pass_kernel(LinPass p) {
     }
     if (dst) {
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            const int d = tid / 8 + 32 * i;
-            store4(dst + (size_t)d * dz + col0 + c4, load4(S + d * SLICE + c4));
-        }
+        for (int i = 0; i < ROWS; ++i) store4(dst + (size_t)(d0 + i) * dz + col0 + c4, st[i]);
     }
 }
 
@@ -358,11 +430,12 @@ cudaError_t pass_dx(const LinPass& p, cudaStream_t stream) {
 
 }  // namespace
 
-int32_t lin_segment_tokens(int32_t N, int32_t total_T, int32_t H, int ctas_per_pair, int sms) {
+int32_t lin_segment_tokens(int32_t N, int32_t total_T, int32_t H, int ctas_per_pair,
+                           int ctas_per_sm, int sms) {
     constexpr int64_t grain = 128;
     if (sms <= 0) sms = 152;   // no device to ask: sizes for a whole GB300
     const int64_t pairs = (int64_t)N * H * ctas_per_pair;
-    const int64_t cuts = sms / pairs;
+    const int64_t cuts = (int64_t)sms * ctas_per_sm / pairs;
     if (cuts < 2) return INT32_MAX / grain * grain;
     const int64_t len = ((int64_t)total_T + N * cuts - 1) / (N * cuts);
     const int64_t seg = (len + grain - 1) / grain * grain;

@@ -96,5 +96,27 @@ __device__ __forceinline__ Segment find_segment(const int32_t* cu, int N, int64_
     return s;
 }
 
+// The first segment of sequence n.  Every warp calls it whole.
+__device__ __forceinline__ Segment first_segment(const int32_t* cu, int N, int64_t total_T,
+                                                 int64_t seg_len, int reverse, int n) {
+    Segment s;
+    s.n = n;
+    s.j = 0;
+    s.u = 0;
+    clamped_seq(cu, n, N, total_T, s.bos, s.eos);
+    s.count = seg_count(s.eos - s.bos, seg_len);
+    if (!cu) {
+        s.u = (int64_t)n * (s.count - 1);
+    } else {
+        int64_t u = 0;
+        for (int m = threadIdx.x & 31; m < n; m += 32)
+            u += seg_count(clamped_len(cu, m, N, total_T), seg_len) - 1;
+        for (int d = 16; d > 0; d >>= 1) u += __shfl_xor_sync(0xffffffffu, u, d);
+        s.u = u;
+    }
+    seg_tokens(s, 0, seg_len, reverse, s.t0, s.t1);
+    return s;
+}
+
 }  // namespace lin
 }  // namespace kda

@@ -57,6 +57,11 @@ cudaError_t launch_lin_pass(const LinPass& p, int dtype, cudaStream_t stream);
 // ran out leaves a nonzero status word.
 cudaError_t launch_lin_pass_tc(const LinPass& p, cudaStream_t stream);
 
+// Turns the states that the segments add into the states before the segments:
+// row u + j of seg_states, the sum of segment j alone, becomes the state before
+// segment j + 1 (in pass order).
+cudaError_t launch_lin_scan(const LinPass& p, cudaStream_t stream);
+
 // One decode token per row, the state pool updated in place.
 struct LinDecode {
     const void* q;              // [B, H, d_k]

@@ -10,7 +10,7 @@
 // not mix, only the products x_i . y_j are formed again in each slice.
 // A sequence that is cut into segments is walked twice: once for the state
 // that each segment adds, and, after that, for the outputs, where a segment
-// first joins the states of the segments before it.
+// starts from the state that a scan over the segments left for it.
 #include "kda_lin.h"
 
 #include <cuda_bf16.h>
@@ -122,27 +122,20 @@ __global__ void __launch_bounds__(THREADS) lin_pass_kernel(LinPass p) {
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) st[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (!STATES) {
-        if (p.state_in) {
+        // the state before the segment: the initial one, or what the scan left
+        if (sg.j > 0) {
+            if (sg.u + sg.j - 1 < rows) {      // (else a malformed cu_seqlens)
+                const float* s0 =
+                    p.seg_states + ((sg.u + sg.j - 1) * (int64_t)p.H + h) * state_floats;
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i)
+                    st[i] = load4(s0 + (size_t)(d0 + i) * dz + col0 + c4);
+            }
+        } else if (p.state_in) {
             const float* s0 = p.state_in + ((size_t)sg.n * p.H + h) * state_floats;
 #pragma unroll
             for (int i = 0; i < ROWS; ++i)
                 st[i] = state_at(s0, d0 + i, col0 + c4, DX, dz, p.state_in_turned);
-        }
-#pragma unroll 4
-        for (int i = 0; i < sg.j; ++i) {   // join the segments before this one
-            int64_t a, b;
-            lin::seg_tokens(sg, i, p.seg_len, p.reverse, a, b);
-            const float f = lin::decay_pow(g, b - a);
-            if (sg.u + i >= rows) break;   // only a malformed cu_seqlens
-            const float* u = p.seg_states + ((sg.u + i) * (int64_t)p.H + h) * state_floats;
-#pragma unroll
-            for (int r = 0; r < ROWS; ++r) {
-                const float4 v = load4(u + (size_t)(d0 + r) * dz + col0 + c4);
-                st[r].x = f * st[r].x + v.x;
-                st[r].y = f * st[r].y + v.y;
-                st[r].z = f * st[r].z + v.z;
-                st[r].w = f * st[r].w + v.w;
-            }
         }
     }
 
@@ -314,12 +307,58 @@ cudaError_t launch_pass(const LinPass& p, cudaStream_t stream) {
         err = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (err != cudaSuccess) return err;
         k1<<<(unsigned)grid, THREADS, smem, stream>>>(p);
+        err = launch_lin_scan(p, stream);
+        if (err != cudaSuccess) return err;
     }
     auto* k2 = lin_pass_kernel<T, DX, false>;
     err = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     k2<<<(unsigned)grid, THREADS, smem, stream>>>(p);
     return cudaGetLastError();
+}
+
+// ------------------------------------------------------ states between segments
+// S_{j+1} = a^{tokens of segment j} S_j + (what segment j adds), one float4 of the
+// state per thread, the rows of four segments on their way at once.
+constexpr int SCAN_THREADS = 128;
+
+__global__ void __launch_bounds__(SCAN_THREADS) lin_scan_kernel(LinPass p) {
+    const int per = p.dx * p.dz / 4 / SCAN_THREADS;       // blocks of one state
+    const int64_t pair = blockIdx.x / per;
+    const int n = (int)(pair / p.H), h = (int)(pair % p.H);
+    const int at = (blockIdx.x % per) * SCAN_THREADS + threadIdx.x;
+    const lin::Segment sg = lin::first_segment(p.cu_seqlens, p.N, p.total_T, p.seg_len, p.reverse,
+                                               n);
+    if (sg.count < 2) return;
+    const float g = p.log_decay[h];
+    const int64_t rows = lin::seg_rows(p.total_T, p.seg_len);
+    const size_t state4 = (size_t)p.dx * p.dz / 4;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.state_in) {
+        const float* s0 = p.state_in + (size_t)pair * p.dx * p.dz;
+        const int d = at * 4 / p.dz, c = at * 4 % p.dz;
+        s = state_at(s0, d, c, p.dx, p.dz, p.state_in_turned);
+    }
+    float4* u = reinterpret_cast<float4*>(p.seg_states) + at;
+    const int last = (int)(rows - sg.u < sg.count - 1 ? rows - sg.u : sg.count - 1);
+    for (int j = 0; j < last; j += 4) {
+        float4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (j + k < last) v[k] = u[((sg.u + j + k) * (int64_t)p.H + h) * state4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (j + k >= last) break;
+            int64_t a, b;
+            lin::seg_tokens(sg, j + k, p.seg_len, p.reverse, a, b);
+            const float f = lin::decay_pow(g, b - a);
+            s.x = f * s.x + v[k].x;
+            s.y = f * s.y + v[k].y;
+            s.z = f * s.z + v[k].z;
+            s.w = f * s.w + v[k].w;
+            u[((sg.u + j + k) * (int64_t)p.H + h) * state4] = s;
+        }
+    }
 }
 
 // ------------------------------------------------------------------ decode
@@ -440,6 +479,13 @@ int32_t lin_segment_tokens(int32_t N, int32_t total_T, int32_t H, int ctas_per_p
     const int64_t len = ((int64_t)total_T + N * cuts - 1) / (N * cuts);
     const int64_t seg = (len + grain - 1) / grain * grain;
     return (int32_t)(seg < grain ? grain : seg);
+}
+
+cudaError_t launch_lin_scan(const LinPass& p, cudaStream_t stream) {
+    const int64_t grid = (int64_t)p.N * p.H * (p.dx * p.dz / 4 / SCAN_THREADS);
+    if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
+    lin_scan_kernel<<<(unsigned)grid, SCAN_THREADS, 0, stream>>>(p);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_lin_pass(const LinPass& p, int dtype, cudaStream_t stream) {

@@ -46,6 +46,7 @@ constexpr uint32_t HALF = C * 128;       // a tile's 64 columns: 128 rows of 128
 constexpr uint32_t TILE = 2 * HALF;
 constexpr int STAGES = 2;                // the pass: X, Y, Z per stage
 constexpr int STATE_STAGES = 3;          // the segment states: Y, Z per stage
+static_assert(D * D * 4 <= 3 * TILE, "the state before a segment fits stage 1");
 constexpr uint32_t SM_S = STAGES * 3 * TILE;             // bf16 copy of the state
 constexpr uint32_t SM_TAB = SM_S + TILE;
 static_assert(SM_S >= STATE_STAGES * 2 * TILE, "the states' stages end before the copy");
@@ -64,10 +65,11 @@ constexpr uint32_t TC_W = 384;           // w Y of 32 tokens: two buffers of thr
 constexpr uint32_t TS_U = 0;
 constexpr uint32_t TS_W = 128;           // two buffers of three parts of 64 columns
 
-static_assert((132 + 132 + 128) * 4 + 256 <= 2048, "tables and barriers");
+static_assert((132 + 132 + 128) * 4 + 288 <= 2048, "tables and barriers");
 
 struct Args {
     CUtensorMap x, y, z, out;
+    CUtensorMap init, segs;        // states: the initial ones, those between the segments
     LinPass p;
 };
 
@@ -78,12 +80,13 @@ struct Bars {
     uint64_t p, s, o1s, od;        // P' / S copy / X S scaled / outputs written
     uint64_t xfree[2];             // the outputs have left the stage's X tile
     uint64_t w[2], wfree[2];       // w Y of a buffer written, read
+    uint64_t init, begun;          // the state before the segment is there / taken over
     uint64_t fin;
     uint32_t tmem;
     volatile int abort;
 };
 
-static_assert(sizeof(Bars) <= 256, "barriers");
+static_assert(sizeof(Bars) <= 288, "barriers");
 
 // Bounded wait that sleeps in the barrier (up to ~1 ms at a time) instead of
 // polling: polls would take issue slots from the warps that work.  False on a
@@ -317,8 +320,8 @@ __device__ __forceinline__ void set_up(const Args& args, Cta& c, int issue, int 
             mbar_init(&b->full[i], 1);
             mbar_init(&b->empty[i], 1);
         }
-        uint64_t* one[] = {&b->xfree[0], &b->xfree[1], &b->qk, &b->o1, &b->o2, &b->u, &b->wfree[0], &b->wfree[1], &b->fin};
-        uint64_t* all[] = {&b->p, &b->s, &b->o1s, &b->od};
+        uint64_t* one[] = {&b->init, &b->xfree[0], &b->xfree[1], &b->qk, &b->o1, &b->o2, &b->u, &b->wfree[0], &b->wfree[1], &b->fin};
+        uint64_t* all[] = {&b->p, &b->s, &b->o1s, &b->od, &b->begun};
         for (uint64_t* x : one) mbar_init(x, 1);
         for (uint64_t* x : all) mbar_init(x, 8);   // warps
         for (uint64_t& x : b->w) mbar_init(&x, w_warps);
@@ -365,13 +368,36 @@ __device__ __forceinline__ void give_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// The state before the segment, or null (zeros): the initial one, or the one that
+// the scan left in the row of the segment before.
+__device__ __forceinline__ const float* start_state(const LinPass& p, const Cta& c) {
+    const int64_t rows = lin::seg_rows(p.total_T, p.seg_len);
+    if (c.sg.j > 0) {
+        if (c.sg.u + c.sg.j - 1 >= rows) return nullptr;   // only a malformed cu_seqlens
+        return p.seg_states + ((c.sg.u + c.sg.j - 1) * (int64_t)p.H + c.h) * (int64_t)(D * D);
+    }
+    return p.state_in ? p.state_in + ((size_t)c.sg.n * p.H + c.h) * (size_t)(D * D) : nullptr;
+}
+
 template <bool REV>
 __device__ __forceinline__ void issue_loads(const Args& args, const Cta& c) {
     const LinPass& p = args.p;
     Bars* b = c.b;
     int issued = 0;
+    const float* start = start_state(p, c);
+    const bool init = start && (c.sg.j > 0 || !p.state_in_turned);
+    if (init) {
+        mbar_arrive_expect_tx(&b->init, D * D * 4);
+        const CUtensorMap* map = c.sg.j > 0 ? &args.segs : &args.init;
+        const int state = (int)(c.sg.j > 0 ? (c.sg.u + c.sg.j - 1) * p.H + c.h
+                                           : (int64_t)c.sg.n * p.H + c.h);
+        for (int q = 0; q < D / 32; ++q)
+            tma_load_3d(c.sm + 3 * TILE + q * HALF, map, 32 * q, 0, state, &b->init);
+    }
     for (int i = 0; i < c.chunks; ++i) {
         const int s = i & 1;
+        // stage 1 holds the state first
+        if (i == 1 && !wait1(b, &b->begun, 0, p, 317)) break;
         if (i >= STAGES && !wait1(b, &b->empty[s], ((i >> 1) - 1) & 1, p, 301)) break;
         uint8_t* st = c.sm + s * 3 * TILE;
         const int tok = (int)chunk_start(c, REV, i);
@@ -383,8 +409,10 @@ __device__ __forceinline__ void issue_loads(const Args& args, const Cta& c) {
         load_tile(&args.x, st, c.h, tok, &b->full[s]);
         issued = i + 1;
     }
+    // no copy outlives the CTA
     for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
-        mbar_wait(&b->full[i & 1], (i >> 1) & 1, nullptr);   // no copy outlives the CTA
+        mbar_wait(&b->full[i & 1], (i >> 1) & 1, nullptr);
+    if (init) mbar_wait(&b->init, 0, nullptr);
 }
 
 // The outputs of whole chunks, from the X tiles to memory.
@@ -625,49 +653,34 @@ __device__ __forceinline__ void states(const LinPass& p, const Cta& c, uint32_t 
     float S[W];
 #pragma unroll
     for (int j = 0; j < W; ++j) S[j] = 0.0f;
-    if (p.state_in) {
-        const float* s0 = p.state_in + ((size_t)c.sg.n * p.H + c.h) * state_floats;
-        if (p.state_in_turned) {
-#pragma unroll
-            for (int j = 0; j < W; ++j) S[j] = s0[(size_t)(W * grp + j) * D + r];
-        } else {
-#pragma unroll
-            for (int j = 0; j < W; j += 4) {
-                const float4 v =
-                    *reinterpret_cast<const float4*>(s0 + (size_t)r * D + W * grp + j);
-                S[j] = v.x; S[j + 1] = v.y; S[j + 2] = v.z; S[j + 3] = v.w;
-            }
-        }
-    }
-    const int64_t rows = lin::seg_rows(p.total_T, p.seg_len);
-    for (int k = 0; k < c.sg.j && c.sg.u + k < rows; ++k) {   // join the segments before
-        int64_t a, e;
-        lin::seg_tokens(c.sg, k, p.seg_len, REV, a, e);
-        const float f = lin::decay_pow(c.g, e - a);
-        const float* u = p.seg_states + ((c.sg.u + k) * (int64_t)p.H + c.h) * state_floats +
-                         (size_t)r * D + W * grp;
+    bool ok = true;
+    const float* start = start_state(p, c);
+    if (start && (c.sg.j > 0 || !p.state_in_turned)) {
+        // it comes into stage 1, 32 columns a tile, swizzled as the operands are
+        ok = wait_warp(b, &b->init, 0, p, 323);
+        const uint8_t* tile = c.sm + 3 * TILE + 2 * grp * HALF;
 #pragma unroll
         for (int j = 0; j < W; j += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(u + j);
-            S[j] = f * S[j] + v.x;
-            S[j + 1] = f * S[j + 1] + v.y;
-            S[j + 2] = f * S[j + 2] + v.z;
-            S[j + 3] = f * S[j + 3] + v.w;
+            const float4 v = *reinterpret_cast<const float4*>(tile + (j >> 5) * HALF +
+                                                              sw128(r, (j & 31) * 4));
+            S[j] = v.x; S[j + 1] = v.y; S[j + 2] = v.z; S[j + 3] = v.w;
         }
+    } else if (start) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) S[j] = start[(size_t)(W * grp + j) * D + r];
     }
-    // Step i: the state before chunk i to its copy, and w Y of the chunk's tokens
-    // 32 grp on and 64 + 32 grp on into the group's buffer.  The first of these
-    // waits for the products on the buffer before, those of the state for all;
-    // group 1, whose buffer is read last, starts with the state.
+    arrive_warp(&b->begun);   // stage 1 is free
+    // Step i: the state before chunk i to its copy (which the products wait for
+    // most), then w Y of the chunk's tokens 32 grp on and 64 + 32 grp on into the
+    // group's buffer.
     uint8_t* copy = c.sm + SM_S + grp * HALF;
     const uint32_t w = lanes + TC_W + 48 * grp;
-    bool ok = true;
     for (int i = 0; ok && i <= c.chunks; ++i) {
         const uint32_t ph = i & 1;
         const int len = i < c.chunks ? chunk_len(c, chunk_start(c, REV, i)) : 0;
 #pragma unroll 1
         for (int k = 0; k < 3; ++k) {
-            if (k == (grp ^ 1)) {
+            if (k == 0) {
                 if (i > 0) {
                     if (!(ok = wait_warp(b, &b->u, ph ^ 1, p, 322))) break;
                     tc_fence_after();
@@ -856,6 +869,8 @@ cudaError_t launch(const Args& args, unsigned grid, bool cut, cudaStream_t strea
                                    cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
         if (err != cudaSuccess) return err;
         lin_states_tc_kernel<REV><<<grid, STATE_THREADS, SMEM, stream>>>(args);
+        err = launch_lin_scan(args.p, stream);
+        if (err != cudaSuccess) return err;
     }
     err = cudaFuncSetAttribute(lin_pass_tc_kernel<REV>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
@@ -873,7 +888,10 @@ cudaError_t launch_lin_pass_tc(const LinPass& p, cudaStream_t stream) {
     if (!make_row_map(&args.x, p.x, p.total_T, p.H, C) ||
         !make_row_map(&args.y, p.y, p.total_T, p.H, C) ||
         !make_row_map(&args.z, p.z, p.total_T, p.H, C) ||
-        !make_row_map(&args.out, p.out, p.total_T, p.H, C)) {
+        !make_row_map(&args.out, p.out, p.total_T, p.H, C) ||
+        (p.state_in && !make_state_map(&args.init, p.state_in, (int64_t)p.N * p.H)) ||
+        (p.total_T >= p.seg_len &&
+         !make_state_map(&args.segs, p.seg_states, (int64_t)(p.total_T / p.seg_len) * p.H))) {
         return cudaErrorInvalidValue;
     }
     const int64_t most = (int64_t)p.total_T / p.seg_len;

@@ -12,10 +12,10 @@
 // bits), so that the state keeps fp32 sums of exact products: three products
 // on a tensor core that otherwise waits for memory.
 //
-// Roles (20 warps): 0-7 turn P into P' and write the outputs (thread = token;
+// Roles (28 warps): 0-7 turn P into P' and write the outputs (thread = token;
 // each half takes half of the columns), 8-15 carry the state (thread = row of
-// S; half of the columns each) and split w Y (half of the tokens each), 16
-// issues the TMA loads, 17 the products, 18 the TMA stores.
+// S; half of the columns each), 16-23 split w Y (half of the tokens each), 24
+// issues the TMA loads, 25 the products, 26 the TMA stores.
 #include "kda_lin.h"
 
 #include <cuda.h>
@@ -35,13 +35,14 @@ using namespace sm103;
 
 constexpr int C = 128;                   // tokens per chunk = rows of a tile
 constexpr int D = 128;                   // dx = dz
-constexpr int THREADS = 640;             // the pass
+constexpr int THREADS = 896;             // the pass
 constexpr int STATE_THREADS = 320;       // the segment states: 8 warps, and 8 and 9 to issue
-// Registers: 640 threads start with 96 each.  The warps that issue give theirs
-// above 56, the 8 that hold the state in registers take 112:
-// 128 (96 + 96 + 112 + 112 + 56) is below 640 x 96.
-constexpr int REGS_ISSUE = 56, REGS_STATE = 112;
-static_assert(128 * (2 * 96 + 2 * REGS_STATE + REGS_ISSUE) <= THREADS * 96, "register split");
+// Registers: 896 threads start with 72 each.  The warps that issue and those
+// that split give some up for the 8 that hold the state:
+// 128 (72 + 72 + 96 + 96 + 64 + 64 + 40) = 896 x 72.
+constexpr int REGS = 72, REGS_STATE = 96, REGS_SPLIT = 64, REGS_ISSUE = 40;
+static_assert(128 * (2 * REGS + 2 * REGS_STATE + 2 * REGS_SPLIT + REGS_ISSUE) <= THREADS * REGS,
+              "register split");
 constexpr uint32_t HALF = C * 128;       // a tile's 64 columns: 128 rows of 128 bytes
 constexpr uint32_t TILE = 2 * HALF;
 constexpr int STAGES = 2;                // the pass: X, Y, Z per stage
@@ -643,12 +644,37 @@ __device__ __forceinline__ void outputs(const LinPass& p, const Cta& c, uint32_t
     }
 }
 
-// Warps 8-15: the state (row r, columns 64 grp on) and w Y.
+// Warps 16-23: w Y of the chunks' tokens 32 grp on and 64 + 32 grp on, into the
+// group's buffer.
+template <bool REV>
+__device__ __forceinline__ void weights(const LinPass& p, const Cta& c, uint32_t lanes) {
+    Bars* b = c.b;
+    const int quad = (threadIdx.x >> 5) & 3, grp = (threadIdx.x >> 7) & 1;
+    const uint32_t w = lanes + TC_W + 48 * grp;
+    bool ok = true;
+    for (int i = 0; ok && i < c.chunks; ++i) {
+        const uint32_t ph = i & 1;
+        const int len = chunk_len(c, chunk_start(c, REV, i));
+        if (!wait_warp(b, &b->full[ph], (i >> 1) & 1, p, 320)) break;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+            if ((half || i > 0) && !(ok = wait_warp(b, &b->wfree[grp], half ^ 1, p, 321))) break;
+            tc_fence_after();
+            split_w(smem_u32(c.sm) + ph * 3 * TILE + TILE, quad, 64 * half + 32 * grp,
+                    c.wtab + (REV ? 0 : C - len), 1.0f, len, w, w + 16, w + 32);
+            tmem_wait_st();
+            tc_fence_before();
+            arrive_warp(&b->w[grp]);
+        }
+    }
+}
+
+// Warps 8-15: the state (row r, columns 64 grp on).
 template <bool REV>
 __device__ __forceinline__ void states(const LinPass& p, const Cta& c, uint32_t lanes) {
     Bars* b = c.b;
     constexpr int W = D / 2;
-    const int r = threadIdx.x & 127, quad = (threadIdx.x >> 5) & 3, grp = (threadIdx.x >> 7) & 1;
+    const int r = threadIdx.x & 127, grp = (threadIdx.x >> 7) & 1;
     const size_t state_floats = (size_t)D * D;
     float S[W];
 #pragma unroll
@@ -670,59 +696,38 @@ __device__ __forceinline__ void states(const LinPass& p, const Cta& c, uint32_t 
         for (int j = 0; j < W; ++j) S[j] = start[(size_t)(W * grp + j) * D + r];
     }
     arrive_warp(&b->begun);   // stage 1 is free
-    // Step i: the state before chunk i to its copy (which the products wait for
-    // most), then w Y of the chunk's tokens 32 grp on and 64 + 32 grp on into the
-    // group's buffer.
     uint8_t* copy = c.sm + SM_S + grp * HALF;
-    const uint32_t w = lanes + TC_W + 48 * grp;
     for (int i = 0; ok && i <= c.chunks; ++i) {
-        const uint32_t ph = i & 1;
-        const int len = i < c.chunks ? chunk_len(c, chunk_start(c, REV, i)) : 0;
-#pragma unroll 1
-        for (int k = 0; k < 3; ++k) {
-            if (k == 0) {
-                if (i > 0) {
-                    if (!(ok = wait_warp(b, &b->u, ph ^ 1, p, 322))) break;
-                    tc_fence_after();
-                    const float f = c.lam[chunk_len(c, chunk_start(c, REV, i - 1))];
+        if (i > 0) {
+            if (!(ok = wait_warp(b, &b->u, (i - 1) & 1, p, 322))) break;
+            tc_fence_after();
+            const float f = c.lam[chunk_len(c, chunk_start(c, REV, i - 1))];
 #pragma unroll
-                    for (int q = 0; q < 4; q += 2) {
-                        uint32_t v[2][16];
-                        tmem_ld16(lanes + TC_U + 64 * grp + 16 * q, v[0]);
-                        tmem_ld16(lanes + TC_U + 64 * grp + 16 * q + 16, v[1]);
-                        tmem_wait_ld();
+            for (int q = 0; q < 4; q += 2) {
+                uint32_t v[2][16];
+                tmem_ld16(lanes + TC_U + 64 * grp + 16 * q, v[0]);
+                tmem_ld16(lanes + TC_U + 64 * grp + 16 * q + 16, v[1]);
+                tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2)
-                            apart(fma2(two(f, f), two(S[16 * q + j], S[16 * q + j + 1]),
-                                       two(v[j >> 4][j & 15], v[j >> 4][(j & 15) + 1])),
-                                  S[16 * q + j], S[16 * q + j + 1]);
-                    }
-                    tc_fence_before();
-                }
-                if (i == c.chunks) break;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    uint4 v;
-                    v.x = pack(S[8 * q], S[8 * q + 1]);
-                    v.y = pack(S[8 * q + 2], S[8 * q + 3]);
-                    v.z = pack(S[8 * q + 4], S[8 * q + 5]);
-                    v.w = pack(S[8 * q + 6], S[8 * q + 7]);
-                    *reinterpret_cast<uint4*>(copy + sw128(r, q * 16)) = v;
-                }
-                fence_proxy_async();
-                arrive_warp(&b->s);
-            } else if (i < c.chunks) {
-                const int half = k == 2;      // the group's second 32 tokens
-                if (!half && !(ok = wait_warp(b, &b->full[ph], (i >> 1) & 1, p, 320))) break;
-                if ((half || i > 0) && !(ok = wait_warp(b, &b->wfree[grp], half ^ 1, p, 321))) break;
-                tc_fence_after();
-                split_w(smem_u32(c.sm) + ph * 3 * TILE + TILE, quad, 64 * half + 32 * grp,
-                        c.wtab + (REV ? 0 : C - len), 1.0f, len, w, w + 16, w + 32);
-                tmem_wait_st();
-                tc_fence_before();
-                arrive_warp(&b->w[grp]);
+                for (int j = 0; j < 32; j += 2)
+                    apart(fma2(two(f, f), two(S[16 * q + j], S[16 * q + j + 1]),
+                               two(v[j >> 4][j & 15], v[j >> 4][(j & 15) + 1])),
+                          S[16 * q + j], S[16 * q + j + 1]);
             }
+            tc_fence_before();
         }
+        if (i == c.chunks) break;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            uint4 v;
+            v.x = pack(S[8 * q], S[8 * q + 1]);
+            v.y = pack(S[8 * q + 2], S[8 * q + 3]);
+            v.z = pack(S[8 * q + 4], S[8 * q + 5]);
+            v.w = pack(S[8 * q + 6], S[8 * q + 7]);
+            *reinterpret_cast<uint4*>(copy + sw128(r, q * 16)) = v;
+        }
+        fence_proxy_async();
+        arrive_warp(&b->s);
     }
     if (ok && p.state_out && c.sg.j + 1 == c.sg.count) {
         float* dst = p.state_out + ((size_t)c.sg.n * p.H + c.h) * state_floats + (size_t)r * D +
@@ -738,24 +743,27 @@ __global__ void __launch_bounds__(THREADS, 1) lin_pass_tc_kernel(const __grid_co
     const LinPass& p = args.p;
     Cta c;
     if (!start(args, c)) return;
-    set_up(args, c, 16, 4);
+    set_up(args, c, 24, 4);
     const int warp = threadIdx.x >> 5;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // this warp's 32 TMEM lanes
-    if (warp >= 16) {
-        give_registers<REGS_ISSUE>();
-        if (warp == 17) {
-            issue_products<REV>(p, c);
-        } else if ((threadIdx.x & 31) == 0) {
-            if (warp == 16) issue_loads<REV>(args, c);
-            if (warp == 18) issue_stores<REV>(args, c);
-        }
-    } else if (warp < 8) {
+    if (warp < 8) {
         outputs<REV>(p, c, lanes);
-    } else {
+    } else if (warp < 16) {
         take_registers<REGS_STATE>();
         states<REV>(p, c, lanes);
+    } else if (warp < 24) {
+        give_registers<REGS_SPLIT>();
+        weights<REV>(p, c, lanes);
+    } else {
+        give_registers<REGS_ISSUE>();
+        if (warp == 25) {
+            issue_products<REV>(p, c);
+        } else if ((threadIdx.x & 31) == 0) {
+            if (warp == 24) issue_loads<REV>(args, c);
+            if (warp == 26) issue_stores<REV>(args, c);
+        }
     }
-    finish(c, 16);
+    finish(c, 24);
 }
 
 // ------------------------------------------------- the state a segment adds

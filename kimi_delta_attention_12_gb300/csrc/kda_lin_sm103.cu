@@ -259,6 +259,11 @@ __device__ __forceinline__ void split_w(uint32_t y, int quad, int tok0, const fl
     }
 }
 
+// What ordinary stores write to shared memory is made visible to TMA and the
+// tensor core by a proxy fence of the warp that issues those, behind the barrier
+// that the writers arrived on: in every writer, where it waits for the writer's
+// own stores, the fence took some 900 cycles of each hand-over.
+
 // Rows len .. 127 of a Z tile to zero: they meet zeros of P' and w Y, and may
 // hold another sequence's values, which need not be finite.
 __device__ __forceinline__ void zero_rows(uint8_t* z, int len, int tid) {
@@ -267,7 +272,6 @@ __device__ __forceinline__ void zero_rows(uint8_t* z, int len, int tid) {
         *reinterpret_cast<uint4*>(z + (part >> 3) * HALF + row * 128 + (part & 7) * 16) =
             make_uint4(0, 0, 0, 0);
     }
-    fence_proxy_async();
 }
 
 __device__ __forceinline__ void load_tile(const CUtensorMap* map, uint8_t* dst, int h, int tok,
@@ -426,6 +430,7 @@ __device__ __forceinline__ void issue_stores(const Args& args, const Cta& c) {
         const int64_t tok = chunk_start(c, REV, i);
         if (chunk_len(c, tok) == C) {
             const uint8_t* tile = c.sm + (i & 1) * 3 * TILE;
+            fence_proxy_async();
             tma_store_3d(&args.out, tile, 0, c.h, (int)tok);
             tma_store_3d(&args.out, tile + HALF, 64, c.h, (int)tok);
             bulk_commit();
@@ -451,6 +456,7 @@ __device__ __forceinline__ void issue_products(const LinPass& p, const Cta& c) {
             const uint32_t z = tile_mn(tile + 2 * TILE);
             if (!wait_warp(b, &b->s, ph, p, 304)) break;
             if (i > 0 && !wait_warp(b, &b->od, ph ^ 1, p, 314)) break;
+            fence_proxy_async();   // the state's copy
             tc_fence_after();
             product<false>(TC_O, x, state, id_km);
 #pragma unroll
@@ -458,7 +464,10 @@ __device__ __forceinline__ void issue_products(const LinPass& p, const Cta& c) {
                 product<true>(TC_O, x + step_k(kk), state + step_mn(kk), id_km);
             commit(&b->o1);
             // a short chunk's z rows past its end are zeroed before P' is handed over
-            if (chunk_len(c, chunk_start(c, REV, i)) < C && !wait_warp(b, &b->p, ph, p, 306)) break;
+            if (chunk_len(c, chunk_start(c, REV, i)) < C) {
+                if (!wait_warp(b, &b->p, ph, p, 306)) break;
+                fence_proxy_async();
+            }
             bool ok = true;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {     // w Y of 32 tokens each
@@ -638,7 +647,6 @@ __device__ __forceinline__ void outputs(const LinPass& p, const Cta& c, uint32_t
                 }
             }
         }
-        fence_proxy_async();
         tc_fence_before();
         arrive_warp(&b->od);
     }
@@ -726,7 +734,6 @@ __device__ __forceinline__ void states(const LinPass& p, const Cta& c, uint32_t 
             v.w = pack(S[8 * q + 6], S[8 * q + 7]);
             *reinterpret_cast<uint4*>(copy + sw128(r, q * 16)) = v;
         }
-        fence_proxy_async();
         arrive_warp(&b->s);
     }
     if (ok && p.state_out && c.sg.j + 1 == c.sg.count) {
@@ -807,6 +814,7 @@ lin_states_tc_kernel(const __grid_constant__ Args args) {
             const uint32_t w = TS_W + 192 * (i & 1);
             if (!wait_warp(b, &b->full[s], (i / STATE_STAGES) & 1, p, 332)) break;
             if (!wait_warp(b, &b->w[i & 1], (i >> 1) & 1, p, 333)) break;
+            fence_proxy_async();   // rows of z that were zeroed
             tc_fence_after();
             if (i == 0) {
                 product_ta<false>(TS_U, w + 128, z, id);

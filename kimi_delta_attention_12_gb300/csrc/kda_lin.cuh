@@ -96,6 +96,25 @@ __device__ __forceinline__ Segment find_segment(const int32_t* cu, int N, int64_
     return s;
 }
 
+// The sequence of rank k by length, longest first (equal ones in order), of up to
+// RANKED sequences; N past them.  Every warp calls it whole.
+constexpr int RANKED = 64;
+__device__ __forceinline__ int nth_longest(const int32_t* cu, int N, int64_t total_T, int k) {
+    if (k >= N) return N;
+    const int lane = threadIdx.x & 31;
+    const int64_t a = lane < N ? clamped_len(cu, lane, N, total_T) : -1;
+    const int64_t b = lane + 32 < N ? clamped_len(cu, lane + 32, N, total_T) : -1;
+    int ra = 0, rb = 0;
+    for (int j = 0; j < N; ++j) {
+        const int64_t l = __shfl_sync(0xffffffffu, j < 32 ? a : b, j & 31);
+        ra += l > a || (l == a && j < lane);
+        rb += l > b || (l == b && j < lane + 32);
+    }
+    const unsigned ha = __ballot_sync(0xffffffffu, lane < N && ra == k);
+    const unsigned hb = __ballot_sync(0xffffffffu, lane + 32 < N && rb == k);
+    return ha ? __ffs(ha) - 1 : 31 + __ffs(hb);
+}
+
 // The first segment of sequence n.  Every warp calls it whole.
 __device__ __forceinline__ Segment first_segment(const int32_t* cu, int N, int64_t total_T,
                                                  int64_t seg_len, int reverse, int n) {

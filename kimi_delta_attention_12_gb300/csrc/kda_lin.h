@@ -55,12 +55,13 @@ int32_t lin_segment_tokens(int32_t N, int32_t total_T, int32_t H, int ctas_per_p
 cudaError_t launch_lin_pass(const LinPass& p, int dtype, cudaStream_t stream);
 // The pass on the tensor cores: bf16, dx = dz = 128, total_T > 0.  A wait that
 // ran out leaves a nonzero status word.
-cudaError_t launch_lin_pass_tc(const LinPass& p, cudaStream_t stream);
+// Up to three passes of the same sizes and sequences run as one.
+cudaError_t launch_lin_pass_tc(const LinPass* passes, int n, cudaStream_t stream);
 
 // Turns the states that the segments add into the states before the segments:
 // row u + j of seg_states, the sum of segment j alone, becomes the state before
 // segment j + 1 (in pass order).
-cudaError_t launch_lin_scan(const LinPass& p, cudaStream_t stream);
+cudaError_t launch_lin_scan(const LinPass* passes, int n, cudaStream_t stream);
 
 // One decode token per row, the state pool updated in place.
 struct LinDecode {

@@ -35,20 +35,12 @@ bool on_tensor_cores(int32_t d_k, int32_t d_v, kda_dtype dt, uint32_t flags, int
            total_T > 0;
 }
 
-// The tensor-core form works on a (sequence, head) pair with one CTA, the
-// CUDA-core form with one for each 32 columns of dz.
-int32_t segment_tokens(int32_t N, int32_t total_T, int32_t H, int32_t dz, bool tc) {
-    return kda::lin_segment_tokens(N, total_T, H, tc ? 1 : dz / 32, tc ? 1 : 3, sm_count());
-}
-
-// The segment of the form (and, in the backward, the direction) that cuts
-// finest, whose states need most room.
-int32_t finest_segment(int32_t N, int32_t total_T, int32_t H, int32_t d_k, int32_t d_v,
-                       kda_dtype dt) {
-    const int32_t a = segment_tokens(N, total_T, H, d_k < d_v ? d_k : d_v, false);
-    if (!on_tensor_cores(d_k, d_v, dt, 0, total_T)) return a;
-    const int32_t b = segment_tokens(N, total_T, H, 0, true);
-    return a < b ? a : b;
+// The tensor-core form works on a (sequence, head) pair of each of the `passes` it
+// runs at once with one CTA an SM; the CUDA-core form with one CTA for each 32
+// columns of dz, of which an SM takes three.
+int32_t segment_tokens(int32_t N, int32_t total_T, int32_t H, int32_t dz, int tc_passes) {
+    return tc_passes > 0 ? kda::lin_segment_tokens(N, total_T, H, tc_passes, 1, sm_count())
+                         : kda::lin_segment_tokens(N, total_T, H, dz / 32, 3, sm_count());
 }
 
 size_t seg_state_bytes(int32_t total_T, int32_t H, int32_t dx, int32_t dz, int32_t seg_len) {
@@ -59,9 +51,17 @@ size_t state_bytes(int32_t N, int32_t H, int32_t d_k, int32_t d_v) {
     return (size_t)N * H * d_k * d_v * sizeof(float);
 }
 
-cudaError_t run(const kda::LinPass& p, bool tc, kda_dtype dt, cudaStream_t s) {
-    return tc ? kda::launch_lin_pass_tc(p, s)
-              : kda::launch_lin_pass(p, dt == KDA_F32 ? 0 : 1, s);
+// Room for the segments' states of `passes` passes that run at once, whichever
+// form a call's flags choose.
+size_t segment_room(int32_t N, int32_t total_T, int32_t H, int32_t d_k, int32_t d_v, kda_dtype dt,
+                    int passes) {
+    const int32_t dz = d_k < d_v ? d_k : d_v;
+    const size_t a =
+        seg_state_bytes(total_T, H, d_k, d_v, segment_tokens(N, total_T, H, dz, 0));
+    if (!on_tensor_cores(d_k, d_v, dt, 0, total_T)) return a;
+    const size_t b = passes * seg_state_bytes(total_T, H, d_k, d_v,
+                                              segment_tokens(N, total_T, H, dz, passes));
+    return a > b ? a : b;
 }
 
 bool bad_sizes(int32_t N, int32_t total_T, int32_t H) { return N < 1 || H < 1 || total_T < 0; }
@@ -76,12 +76,10 @@ size_t kda_lin_prefill_workspace_bytes(int32_t N, int32_t total_T, int32_t H, in
         (dt != KDA_F32 && dt != KDA_BF16)) {
         return 0;
     }
-    const int32_t seg = finest_segment(N, total_T, H, d_k, d_v, dt);
     // the states of the segments, and a copy of the initial states for a call
     // that updates them in place
-    size_t b = kHeader + seg_state_bytes(total_T, H, d_k, d_v, seg);
-    if (total_T / seg > 0) b += round_up(state_bytes(N, H, d_k, d_v), 256);
-    return b;
+    const size_t room = segment_room(N, total_T, H, d_k, d_v, dt, 1);
+    return kHeader + room + (room > 0 ? round_up(state_bytes(N, H, d_k, d_v), 256) : 0);
 }
 
 int kda_lin_prefill(const void* q, const void* k, const void* v, const float* log_decay,
@@ -137,21 +135,22 @@ int kda_lin_prefill(const void* q, const void* k, const void* v, const float* lo
     p.cu_seqlens = cu_seqlens;
     p.status = reinterpret_cast<int32_t*>(ws);
     p.N = N; p.total_T = total_T; p.H = H; p.dx = d_k; p.dz = d_v;
-    p.seg_len = segment_tokens(N, total_T, H, d_v, tc);
+    p.seg_len = segment_tokens(N, total_T, H, d_v, tc ? 1 : 0);
     p.seg_states = reinterpret_cast<float*>(ws + kHeader);
     p.out_scale = scale; p.kv_scale = 1.0f;
     if (initial_state && initial_state == final_state && total_T / p.seg_len > 0) {
         // the last segment may write its state before the first has read it
         float* copy = reinterpret_cast<float*>(
-            ws + kHeader + seg_state_bytes(total_T, H, d_k, d_v,
-                                           finest_segment(N, total_T, H, d_k, d_v, dt)));
+            ws + kHeader + segment_room(N, total_T, H, d_k, d_v, dt, 1));
         if (cudaMemcpyAsync(copy, initial_state, nst, cudaMemcpyDeviceToDevice, s) !=
             cudaSuccess) {
             return KDA_ERR_CUDA;
         }
         p.state_in = copy;
     }
-    return run(p, tc, dt, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    const cudaError_t err = tc ? kda::launch_lin_pass_tc(&p, 1, s)
+                               : kda::launch_lin_pass(p, dt == KDA_F32 ? 0 : 1, s);
+    return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 int kda_lin_decode_step(const void* q, const void* k, const void* v, const float* log_decay,
@@ -187,16 +186,15 @@ int kda_lin_decode_step(const void* q, const void* k, const void* v, const float
                : KDA_ERR_CUDA;
 }
 
-// The three passes run one after another on the stream and share the segment
-// states' room, sized for the pass that needs most.
+// On the tensor cores the three passes run at once, each with states of its own;
+// on the CUDA cores one after another in the same room.
 size_t kda_lin_backward_workspace_bytes(int32_t N, int32_t total_T, int32_t H, int32_t d_k,
                                         int32_t d_v, kda_dtype dt) {
     if (bad_sizes(N, total_T, H) || !supported_dim(d_k) || !supported_dim(d_v) ||
         (dt != KDA_F32 && dt != KDA_BF16)) {
         return 0;
     }
-    return kHeader + seg_state_bytes(total_T, H, d_k, d_v,
-                                     finest_segment(N, total_T, H, d_k, d_v, dt));
+    return kHeader + segment_room(N, total_T, H, d_k, d_v, dt, 3);
 }
 
 int kda_lin_backward(const void* q, const void* k, const void* v, const float* log_decay,
@@ -238,35 +236,46 @@ int kda_lin_backward(const void* q, const void* k, const void* v, const float* l
     char* ws = static_cast<char*>(workspace);
     const bool tc = on_tensor_cores(d_k, d_v, dt, flags, total_T);
     if (tc && cudaMemsetAsync(ws, 0, sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
-    kda::LinPass p;
-    memset(&p, 0, sizeof(p));
-    p.log_decay = log_decay;
-    p.cu_seqlens = cu_seqlens;
-    p.status = reinterpret_cast<int32_t*>(ws);
-    p.seg_states = reinterpret_cast<float*>(ws + kHeader);
-    p.N = N; p.total_T = total_T; p.H = H;
-    cudaError_t err = cudaSuccess;
-    if (total_T > 0) {
-        // dq_t = scale S_t dO_t: forward in time with the turned state
-        p.x = dO; p.y = v; p.z = k; p.out = dq; p.dx = d_v; p.dz = d_k;
-        p.state_in = initial_state; p.state_in_turned = 1; p.state_out = nullptr;
-        p.reverse = 0; p.out_scale = scale; p.kv_scale = 1.0f;
-        p.seg_len = segment_tokens(N, total_T, H, d_k, tc);
-        err = run(p, tc, dt, s);
-        if (err != cudaSuccess) return KDA_ERR_CUDA;
-        // dk_t = G_t v_t, G_t = scale q_t dO_t^T + a G_{t+1}: from the ends
-        p.x = v; p.y = dO; p.z = q; p.out = dk;
-        p.state_in = dS_final; p.reverse = 1; p.out_scale = 1.0f; p.kv_scale = scale;
-        err = run(p, tc, dt, s);
-        if (err != cudaSuccess) return KDA_ERR_CUDA;
+    kda::LinPass pass[3];
+    memset(pass, 0, sizeof(pass));
+    for (kda::LinPass& p : pass) {
+        p.log_decay = log_decay;
+        p.cu_seqlens = cu_seqlens;
+        p.status = reinterpret_cast<int32_t*>(ws);
+        p.N = N; p.total_T = total_T; p.H = H;
     }
+    // dq_t = scale S_t dO_t: forward in time with the turned state
+    kda::LinPass& a = pass[0];
+    a.x = dO; a.y = v; a.z = k; a.out = dq; a.dx = d_v; a.dz = d_k;
+    a.state_in = initial_state; a.state_in_turned = 1;
+    a.out_scale = scale; a.kv_scale = 1.0f;
+    // dk_t = G_t v_t, G_t = scale q_t dO_t^T + a G_{t+1}: from the ends
+    kda::LinPass& b = pass[1];
+    b.x = v; b.y = dO; b.z = q; b.out = dk; b.dx = d_v; b.dz = d_k;
+    b.state_in = dS_final; b.state_in_turned = 1;
+    b.reverse = 1; b.out_scale = 1.0f; b.kv_scale = scale;
     // dv_t = G_t^T k_t; the state it ends with is dS_0
-    p.x = k; p.y = q; p.z = dO; p.out = dv; p.dx = d_k; p.dz = d_v;
-    p.state_in = dS_final; p.state_in_turned = 0; p.state_out = dS0;
-    p.reverse = 1; p.out_scale = 1.0f; p.kv_scale = scale;
-    p.seg_len = segment_tokens(N, total_T, H, d_v, tc);
-    err = run(p, tc, dt, s);
-    return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    kda::LinPass& c = pass[2];
+    c.x = k; c.y = q; c.z = dO; c.out = dv; c.dx = d_k; c.dz = d_v;
+    c.state_in = dS_final; c.state_out = dS0;
+    c.reverse = 1; c.out_scale = 1.0f; c.kv_scale = scale;
+    float* states = reinterpret_cast<float*>(ws + kHeader);
+    if (tc) {
+        const int32_t seg = segment_tokens(N, total_T, H, d_v, 3);
+        for (int i = 0; i < 3; ++i) {
+            pass[i].seg_len = seg;
+            pass[i].seg_states =
+                states + i * (seg_state_bytes(total_T, H, d_k, d_v, seg) / sizeof(float));
+        }
+        return kda::launch_lin_pass_tc(pass, 3, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    }
+    for (kda::LinPass& p : pass) {
+        if (total_T == 0 && &p != &c) continue;   // only the state is handed on
+        p.seg_len = segment_tokens(N, total_T, H, p.dz, 0);
+        p.seg_states = states;
+        if (kda::launch_lin_pass(p, dt == KDA_F32 ? 0 : 1, s) != cudaSuccess) return KDA_ERR_CUDA;
+    }
+    return KDA_OK;
 }
 
 }  // extern "C"

@@ -307,7 +307,7 @@ cudaError_t launch_pass(const LinPass& p, cudaStream_t stream) {
         err = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (err != cudaSuccess) return err;
         k1<<<(unsigned)grid, THREADS, smem, stream>>>(p);
-        err = launch_lin_scan(p, stream);
+        err = launch_lin_scan(&p, 1, stream);
         if (err != cudaSuccess) return err;
     }
     auto* k2 = lin_pass_kernel<T, DX, false>;
@@ -322,7 +322,12 @@ cudaError_t launch_pass(const LinPass& p, cudaStream_t stream) {
 // state per thread, the rows of four segments on their way at once.
 constexpr int SCAN_THREADS = 128;
 
-__global__ void __launch_bounds__(SCAN_THREADS) lin_scan_kernel(LinPass p) {
+struct Scan {
+    LinPass p[3];
+};
+
+__global__ void __launch_bounds__(SCAN_THREADS) lin_scan_kernel(const __grid_constant__ Scan scan) {
+    const LinPass& p = scan.p[blockIdx.y];
     const int per = p.dx * p.dz / 4 / SCAN_THREADS;       // blocks of one state
     const int64_t pair = blockIdx.x / per;
     const int n = (int)(pair / p.H), h = (int)(pair % p.H);
@@ -481,10 +486,13 @@ int32_t lin_segment_tokens(int32_t N, int32_t total_T, int32_t H, int ctas_per_p
     return (int32_t)(seg < grain ? grain : seg);
 }
 
-cudaError_t launch_lin_scan(const LinPass& p, cudaStream_t stream) {
+cudaError_t launch_lin_scan(const LinPass* passes, int n, cudaStream_t stream) {
+    Scan scan;
+    for (int i = 0; i < n; ++i) scan.p[i] = passes[i];
+    const LinPass& p = passes[0];
     const int64_t grid = (int64_t)p.N * p.H * (p.dx * p.dz / 4 / SCAN_THREADS);
     if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-    lin_scan_kernel<<<(unsigned)grid, SCAN_THREADS, 0, stream>>>(p);
+    lin_scan_kernel<<<dim3((unsigned)grid, n), SCAN_THREADS, 0, stream>>>(scan);
     return cudaGetLastError();
 }
 

@@ -66,12 +66,19 @@ constexpr uint32_t TC_W = 384;           // w Y of 32 tokens: two buffers of thr
 constexpr uint32_t TS_U = 0;
 constexpr uint32_t TS_W = 128;           // two buffers of three parts of 64 columns
 
-static_assert((132 + 132 + 128) * 4 + 288 <= 2048, "tables and barriers");
+static_assert((132 + 132 + 128) * 4 + 320 <= 2048, "tables and barriers");
 
 struct Args {
     CUtensorMap x, y, z, out;
-    CUtensorMap init, segs;        // states: the initial ones, those between the segments
+    CUtensorMap init, segs, last;  // states: the initial, between the segments, the final ones
     LinPass p;
+};
+
+// Up to three passes of the same sizes in one launch: the gradients of q, k and v
+// need nothing of each other.
+struct Jobs {
+    Args a[3];
+    int n;
 };
 
 struct Bars {
@@ -81,13 +88,13 @@ struct Bars {
     uint64_t p, s, o1s, od;        // P' / S copy / X S scaled / outputs written
     uint64_t xfree[2];             // the outputs have left the stage's X tile
     uint64_t w[2], wfree[2];       // w Y of a buffer written, read
-    uint64_t init, begun;          // the state before the segment is there / taken over
+    uint64_t init, begun, end;     // the state before the segment there / taken over; after it written
     uint64_t fin;
     uint32_t tmem;
     volatile int abort;
 };
 
-static_assert(sizeof(Bars) <= 288, "barriers");
+static_assert(sizeof(Bars) <= 320, "barriers");
 
 // Bounded wait that sleeps in the barrier (up to ~1 ms at a time) instead of
 // polling: polls would take issue slots from the warps that work.  False on a
@@ -289,22 +296,30 @@ struct Cta {
     float* wtab;    // weights of a whole chunk's tokens in the state
     lin::Segment sg;
     int h, chunks;
+    bool rev;
     float g;
 };
 
-__device__ __forceinline__ bool start(const Args& args, Cta& c) {
+// The pass and the segment of this CTA (heads fastest, then the passes, then the
+// segments).  Whole sequences come longest first, so that none starts late.
+__device__ __forceinline__ const Args* start(const Jobs& jobs, Cta& c) {
     extern __shared__ uint8_t smem_raw[];
-    const LinPass& p = args.p;
+    const int H = jobs.a[0].p.H, unit = blockIdx.x / H;
+    const Args* args = &jobs.a[unit % jobs.n];
+    const LinPass& p = args->p;
     c.sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                       ~(uintptr_t)1023);
     c.lam = reinterpret_cast<float*>(c.sm + SM_TAB);
     c.lamk = c.lam + 132;
     c.wtab = c.lamk + 132;
     c.b = reinterpret_cast<Bars*>(c.wtab + 128);
-    c.h = blockIdx.x % p.H;
-    c.sg = lin::find_segment(p.cu_seqlens, p.N, p.total_T, p.seg_len, p.reverse,
-                             blockIdx.x / p.H);
-    return c.sg.n >= 0;
+    c.h = blockIdx.x % H;
+    c.rev = p.reverse != 0;
+    int index = unit / jobs.n;
+    if (p.cu_seqlens && p.N <= lin::RANKED && p.total_T < p.seg_len)
+        index = lin::nth_longest(p.cu_seqlens, p.N, p.total_T, index);
+    c.sg = lin::find_segment(p.cu_seqlens, p.N, p.total_T, p.seg_len, p.reverse, index);
+    return c.sg.n >= 0 ? args : nullptr;
 }
 
 // `issue`: the first of the issuing warps; `w_warps`: those that fill a buffer of w Y.
@@ -326,7 +341,7 @@ __device__ __forceinline__ void set_up(const Args& args, Cta& c, int issue, int 
             mbar_init(&b->empty[i], 1);
         }
         uint64_t* one[] = {&b->init, &b->xfree[0], &b->xfree[1], &b->qk, &b->o1, &b->o2, &b->u, &b->wfree[0], &b->wfree[1], &b->fin};
-        uint64_t* all[] = {&b->p, &b->s, &b->o1s, &b->od, &b->begun};
+        uint64_t* all[] = {&b->p, &b->s, &b->o1s, &b->od, &b->begun, &b->end};
         for (uint64_t* x : one) mbar_init(x, 1);
         for (uint64_t* x : all) mbar_init(x, 8);   // warps
         for (uint64_t& x : b->w) mbar_init(&x, w_warps);
@@ -356,8 +371,8 @@ __device__ __forceinline__ void finish(const Cta& c, int issue) {
 }
 
 // Token range of the pass's step i.
-__device__ __forceinline__ int64_t chunk_start(const Cta& c, int reverse, int i) {
-    return c.sg.t0 + (int64_t)(reverse ? c.chunks - 1 - i : i) * C;
+__device__ __forceinline__ int64_t chunk_start(const Cta& c, int i) {
+    return c.sg.t0 + (int64_t)(c.rev ? c.chunks - 1 - i : i) * C;
 }
 __device__ __forceinline__ int chunk_len(const Cta& c, int64_t tok) {
     return (int)(c.sg.t1 - tok < C ? c.sg.t1 - tok : C);
@@ -384,7 +399,6 @@ __device__ __forceinline__ const float* start_state(const LinPass& p, const Cta&
     return p.state_in ? p.state_in + ((size_t)c.sg.n * p.H + c.h) * (size_t)(D * D) : nullptr;
 }
 
-template <bool REV>
 __device__ __forceinline__ void issue_loads(const Args& args, const Cta& c) {
     const LinPass& p = args.p;
     Bars* b = c.b;
@@ -405,7 +419,7 @@ __device__ __forceinline__ void issue_loads(const Args& args, const Cta& c) {
         if (i == 1 && !wait1(b, &b->begun, 0, p, 317)) break;
         if (i >= STAGES && !wait1(b, &b->empty[s], ((i >> 1) - 1) & 1, p, 301)) break;
         uint8_t* st = c.sm + s * 3 * TILE;
-        const int tok = (int)chunk_start(c, REV, i);
+        const int tok = (int)chunk_start(c, i);
         mbar_arrive_expect_tx(&b->full[s], 3 * TILE);
         load_tile(&args.y, st + TILE, c.h, tok, &b->full[s]);
         load_tile(&args.z, st + 2 * TILE, c.h, tok, &b->full[s]);
@@ -420,14 +434,30 @@ __device__ __forceinline__ void issue_loads(const Args& args, const Cta& c) {
     if (init) mbar_wait(&b->init, 0, nullptr);
 }
 
-// The outputs of whole chunks, from the X tiles to memory.
-template <bool REV>
+// Whether the CTA writes a final state.
+__device__ __forceinline__ bool hands_on(const LinPass& p, const Cta& c) {
+    return p.state_out && c.sg.j + 1 == c.sg.count;
+}
+
+// Four values of row r of a state to where store_states takes them from.
+__device__ __forceinline__ void store_state(uint8_t* tiles, int r, int col, const float* v) {
+    *reinterpret_cast<float4*>(tiles + (col >> 5) * HALF + sw128(r, (col & 31) * 4)) =
+        make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store_states(const CUtensorMap* map, const uint8_t* tiles,
+                                             int state) {
+    fence_proxy_async();
+    for (int q = 0; q < D / 32; ++q) tma_store_3d(map, tiles + q * HALF, 32 * q, 0, state);
+    bulk_commit();
+}
+
+// The outputs of whole chunks, from the X tiles to memory, and the final state.
 __device__ __forceinline__ void issue_stores(const Args& args, const Cta& c) {
     const LinPass& p = args.p;
     Bars* b = c.b;
     for (int i = 0; i < c.chunks; ++i) {
         if (!wait1(b, &b->od, i & 1, p, 316)) break;
-        const int64_t tok = chunk_start(c, REV, i);
+        const int64_t tok = chunk_start(c, i);
         if (chunk_len(c, tok) == C) {
             const uint8_t* tile = c.sm + (i & 1) * 3 * TILE;
             fence_proxy_async();
@@ -438,12 +468,13 @@ __device__ __forceinline__ void issue_stores(const Args& args, const Cta& c) {
         }
         mbar_arrive(&b->xfree[i & 1]);
     }
+    if (hands_on(p, c) && !b->abort && wait1(b, &b->end, 0, p, 318))
+        store_states(&args.last, c.sm + TILE, c.sg.n * p.H + c.h);
     bulk_wait<false>();
 }
 
 // The products of all chunks, in the order in which the tensor core runs them.
 // P of the next chunk comes last: it fills the time that the state takes.
-template <bool REV>
 __device__ __forceinline__ void issue_products(const LinPass& p, const Cta& c) {
     Bars* b = c.b;
     constexpr uint32_t id_kk = idesc_bf16(D, D, 0, 0), id_km = idesc_bf16(D, D, 0, 1);
@@ -464,7 +495,7 @@ __device__ __forceinline__ void issue_products(const LinPass& p, const Cta& c) {
                 product<true>(TC_O, x + step_k(kk), state + step_mn(kk), id_km);
             commit(&b->o1);
             // a short chunk's z rows past its end are zeroed before P' is handed over
-            if (chunk_len(c, chunk_start(c, REV, i)) < C) {
+            if (chunk_len(c, chunk_start(c, i)) < C) {
                 if (!wait_warp(b, &b->p, ph, p, 306)) break;
                 fence_proxy_async();
             }
@@ -523,14 +554,15 @@ __device__ __forceinline__ void issue_products(const LinPass& p, const Cta& c) {
 // weights are formed on the spot, as 2^{base + slope s}: their error (2^-22 and
 // that of the exponent, at most 31 |g2| 2^-24) is far below the rounding to bf16
 // that follows, and a table in shared memory would wait for the products' own
-// reads of it.  MASKED: rows `t`, counted from the block's first column, take
-// columns up to (or from) their own and below `len`.
-template <bool REV, bool MASKED>
-__device__ __forceinline__ void weigh(uint32_t col, float base, float slope, int t, int len) {
+// reads of it.  MASKED: only columns first .. last of the block count.
+template <bool MASKED>
+__device__ __forceinline__ void weigh(uint32_t col, float base, float slope, int first, int last) {
     uint32_t r[2][16], w[16];
     tmem_ld16(col, r[0]);
     tmem_ld16(col + 16, r[1]);
     tmem_wait_ld();
+    const bool none = last < first;
+    const uint32_t from = none ? 64 : first, span = none ? 0 : last - first;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
         const int s = 2 * j;
@@ -540,8 +572,8 @@ __device__ __forceinline__ void weigh(uint32_t col, float base, float slope, int
         if (MASKED) {
             float v0, v1;
             apart(v, v0, v1);
-            if ((REV ? s < t : s > t) || s >= len) v0 = 0.0f;
-            if ((REV ? s + 1 < t : s + 1 > t) || s + 1 >= len) v1 = 0.0f;
+            if (s - from > span) v0 = 0.0f;
+            if (s + 1 - from > span) v1 = 0.0f;
             v = two(v0, v1);
         }
         w[j] = pack(v);
@@ -550,7 +582,6 @@ __device__ __forceinline__ void weigh(uint32_t col, float base, float slope, int
 }
 
 // Warps 0-7: P' (columns 32 q with q even or odd) and the outputs (columns 64 grp on).
-template <bool REV>
 __device__ __forceinline__ void outputs(const LinPass& p, const Cta& c, uint32_t lanes) {
     Bars* b = c.b;
     const int t = threadIdx.x & 127, quad = (threadIdx.x >> 5) & 3, grp = threadIdx.x >> 7;
@@ -558,14 +589,14 @@ __device__ __forceinline__ void outputs(const LinPass& p, const Cta& c, uint32_t
     // distance of one already weighs nothing (2^-128 is no fp32 of full precision),
     // so that a distance of zero weighs 1 under every decay.  The pass's two scales
     // go into the weights and, once more, into X S; their sign into the outputs.
-    const float g2 = c.g < -88.0f ? -128.0f : c.g * 1.44269504f, slope = REV ? g2 : -g2;
+    const float g2 = c.g < -88.0f ? -128.0f : c.g * 1.44269504f, slope = c.rev ? g2 : -g2;
     const float scale = p.out_scale * p.kv_scale;
     const float c2 = log2f(fabsf(scale));
     const uint32_t flip = scale < 0.0f ? 0x80008000u : 0u;
     const float m = scale < 0.0f ? -p.out_scale : p.out_scale;
     for (int i = 0; i < c.chunks; ++i) {
         const uint32_t ph = i & 1;
-        const int64_t tok = chunk_start(c, REV, i);
+        const int64_t tok = chunk_start(c, i);
         const int len = chunk_len(c, tok);
         if (len < C) {
             if (!wait_warp(b, &b->full[i & 1], (i >> 1) & 1, p, 310)) break;
@@ -579,10 +610,11 @@ __device__ __forceinline__ void outputs(const LinPass& p, const Cta& c, uint32_t
             const uint32_t col = lanes + TC_P + 32 * q;
             const int tq = t - 32 * q;
             const float base = fmaf(-slope, (float)tq, c2);
-            if ((REV ? q > quad : q < quad) && len == C) {
-                weigh<REV, false>(col, base, slope, tq, C);
-            } else if (REV ? q >= quad : q <= quad) {
-                weigh<REV, true>(col, base, slope, tq, len - 32 * q);
+            if ((c.rev ? q > quad : q < quad) && len == C) {
+                weigh<false>(col, base, slope, 0, 31);
+            } else if (c.rev ? q >= quad : q <= quad) {
+                const int end = len - 32 * q - 1;
+                weigh<true>(col, base, slope, c.rev ? max(tq, 0) : 0, c.rev ? end : min(tq, end));
             } else {
                 const uint32_t zero[16] = {};
                 tmem_st16(col, zero);
@@ -592,7 +624,7 @@ __device__ __forceinline__ void outputs(const LinPass& p, const Cta& c, uint32_t
         tc_fence_before();
         arrive_warp(&b->p);
 
-        const float f = t < len ? m * c.lam[REV ? len - 1 - t : t + 1] : 0.0f;
+        const float f = t < len ? m * c.lam[c.rev ? len - 1 - t : t + 1] : 0.0f;
         const uint32_t o = lanes + TC_O + 64 * grp;
         if (!wait_warp(b, &b->o1, ph, p, 312)) break;
         tc_fence_after();
@@ -654,7 +686,6 @@ __device__ __forceinline__ void outputs(const LinPass& p, const Cta& c, uint32_t
 
 // Warps 16-23: w Y of the chunks' tokens 32 grp on and 64 + 32 grp on, into the
 // group's buffer.
-template <bool REV>
 __device__ __forceinline__ void weights(const LinPass& p, const Cta& c, uint32_t lanes) {
     Bars* b = c.b;
     const int quad = (threadIdx.x >> 5) & 3, grp = (threadIdx.x >> 7) & 1;
@@ -662,14 +693,14 @@ __device__ __forceinline__ void weights(const LinPass& p, const Cta& c, uint32_t
     bool ok = true;
     for (int i = 0; ok && i < c.chunks; ++i) {
         const uint32_t ph = i & 1;
-        const int len = chunk_len(c, chunk_start(c, REV, i));
+        const int len = chunk_len(c, chunk_start(c, i));
         if (!wait_warp(b, &b->full[ph], (i >> 1) & 1, p, 320)) break;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
             if ((half || i > 0) && !(ok = wait_warp(b, &b->wfree[grp], half ^ 1, p, 321))) break;
             tc_fence_after();
             split_w(smem_u32(c.sm) + ph * 3 * TILE + TILE, quad, 64 * half + 32 * grp,
-                    c.wtab + (REV ? 0 : C - len), 1.0f, len, w, w + 16, w + 32);
+                    c.wtab + (c.rev ? 0 : C - len), 1.0f, len, w, w + 16, w + 32);
             tmem_wait_st();
             tc_fence_before();
             arrive_warp(&b->w[grp]);
@@ -678,12 +709,10 @@ __device__ __forceinline__ void weights(const LinPass& p, const Cta& c, uint32_t
 }
 
 // Warps 8-15: the state (row r, columns 64 grp on).
-template <bool REV>
 __device__ __forceinline__ void states(const LinPass& p, const Cta& c, uint32_t lanes) {
     Bars* b = c.b;
     constexpr int W = D / 2;
     const int r = threadIdx.x & 127, grp = (threadIdx.x >> 7) & 1;
-    const size_t state_floats = (size_t)D * D;
     float S[W];
 #pragma unroll
     for (int j = 0; j < W; ++j) S[j] = 0.0f;
@@ -709,7 +738,7 @@ __device__ __forceinline__ void states(const LinPass& p, const Cta& c, uint32_t 
         if (i > 0) {
             if (!(ok = wait_warp(b, &b->u, (i - 1) & 1, p, 322))) break;
             tc_fence_after();
-            const float f = c.lam[chunk_len(c, chunk_start(c, REV, i - 1))];
+            const float f = c.lam[chunk_len(c, chunk_start(c, i - 1))];
 #pragma unroll
             for (int q = 0; q < 4; q += 2) {
                 uint32_t v[2][16];
@@ -736,38 +765,39 @@ __device__ __forceinline__ void states(const LinPass& p, const Cta& c, uint32_t 
         }
         arrive_warp(&b->s);
     }
-    if (ok && p.state_out && c.sg.j + 1 == c.sg.count) {
-        float* dst = p.state_out + ((size_t)c.sg.n * p.H + c.h) * state_floats + (size_t)r * D +
-                     W * grp;
+    if (ok && hands_on(p, c)) {
+        // through the Y and Z tiles of stage 0, which nothing reads any more
 #pragma unroll
-        for (int j = 0; j < W; j += 4)
-            *reinterpret_cast<float4*>(dst + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+        for (int j = 0; j < W; j += 4) store_state(c.sm + TILE, r, W * grp + j, &S[j]);
+        arrive_warp(&b->end);
     }
 }
 
-template <bool REV>
-__global__ void __launch_bounds__(THREADS, 1) lin_pass_tc_kernel(const __grid_constant__ Args args) {
-    const LinPass& p = args.p;
+__global__ void __launch_bounds__(THREADS, 1)
+lin_pass_tc_kernel(const __grid_constant__ Jobs jobs) {
     Cta c;
-    if (!start(args, c)) return;
+    const Args* job = start(jobs, c);
+    if (!job) return;
+    const Args& args = *job;
+    const LinPass& p = args.p;
     set_up(args, c, 24, 4);
     const int warp = threadIdx.x >> 5;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // this warp's 32 TMEM lanes
     if (warp < 8) {
-        outputs<REV>(p, c, lanes);
+        outputs(p, c, lanes);
     } else if (warp < 16) {
         take_registers<REGS_STATE>();
-        states<REV>(p, c, lanes);
+        states(p, c, lanes);
     } else if (warp < 24) {
         give_registers<REGS_SPLIT>();
-        weights<REV>(p, c, lanes);
+        weights(p, c, lanes);
     } else {
         give_registers<REGS_ISSUE>();
         if (warp == 25) {
-            issue_products<REV>(p, c);
+            issue_products(p, c);
         } else if ((threadIdx.x & 31) == 0) {
-            if (warp == 24) issue_loads<REV>(args, c);
-            if (warp == 26) issue_stores<REV>(args, c);
+            if (warp == 24) issue_loads(args, c);
+            if (warp == 26) issue_stores(args, c);
         }
     }
     finish(c, 24);
@@ -777,15 +807,14 @@ __global__ void __launch_bounds__(THREADS, 1) lin_pass_tc_kernel(const __grid_co
 // sum_j a^{tokens from j to the segment's end} kv_scale y_j z_j^T, accumulated in TMEM
 // over the whole segment: the weights are taken to its end at once.  Eight
 // warps split w Y into one of two buffers while the products read the other.
-template <bool REV>
 __global__ void __launch_bounds__(STATE_THREADS, 1)
-lin_states_tc_kernel(const __grid_constant__ Args args) {
-    const LinPass& p = args.p;
+lin_states_tc_kernel(const __grid_constant__ Jobs jobs) {
     Cta c;
-    if (!start(args, c) || c.sg.j + 1 >= c.sg.count ||
-        c.sg.u + c.sg.j >= lin::seg_rows(p.total_T, p.seg_len)) {
-        return;
-    }
+    const Args* job = start(jobs, c);
+    if (!job) return;
+    const Args& args = *job;
+    const LinPass& p = args.p;
+    if (c.sg.j + 1 >= c.sg.count || c.sg.u + c.sg.j >= lin::seg_rows(p.total_T, p.seg_len)) return;
     set_up(args, c, 8, 8);
     Bars* b = c.b;
     const int tid = threadIdx.x, warp = tid >> 5, n = c.chunks;
@@ -797,7 +826,7 @@ lin_states_tc_kernel(const __grid_constant__ Args args) {
                 const int s = i % STATE_STAGES, use = i / STATE_STAGES;
                 if (use > 0 && !wait1(b, &b->empty[s], (use - 1) & 1, p, 331)) break;
                 uint8_t* st = c.sm + s * 2 * TILE;
-                const int tok = (int)chunk_start(c, REV, i);
+                const int tok = (int)chunk_start(c, i);
                 mbar_arrive_expect_tx(&b->full[s], 2 * TILE);
                 load_tile(&args.y, st, c.h, tok, &b->full[s]);
                 load_tile(&args.z, st + TILE, c.h, tok, &b->full[s]);
@@ -805,6 +834,10 @@ lin_states_tc_kernel(const __grid_constant__ Args args) {
             }
             for (int i = issued > STATE_STAGES ? issued - STATE_STAGES : 0; i < issued; ++i)
                 mbar_wait(&b->full[i % STATE_STAGES], (i / STATE_STAGES) & 1, nullptr);
+            if (!b->abort && wait1(b, &b->end, 0, p, 337)) {
+                store_states(&args.segs, c.sm, (int)((c.sg.u + c.sg.j) * p.H + c.h));
+                bulk_wait<false>();
+            }
         }
     } else if (warp == 9) {
         constexpr uint32_t id = idesc_bf16(D, D, 0, 1);
@@ -839,15 +872,15 @@ lin_states_tc_kernel(const __grid_constant__ Args args) {
         bool ok = true;
         for (int i = 0; i < n; ++i) {
             const int s = i % STATE_STAGES, buf = i & 1;
-            const int64_t tok = chunk_start(c, REV, i);
+            const int64_t tok = chunk_start(c, i);
             const int len = chunk_len(c, tok);
-            const float f = lin::decay_pow(c.g, REV ? tok - c.sg.t0 : c.sg.t1 - (tok + len));
+            const float f = lin::decay_pow(c.g, c.rev ? tok - c.sg.t0 : c.sg.t1 - (tok + len));
             if (!(ok = wait_warp(b, &b->full[s], (i / STATE_STAGES) & 1, p, 334))) break;
             if (i >= 2 && !(ok = wait_warp(b, &b->wfree[buf], ((i >> 1) - 1) & 1, p, 335))) break;
             tc_fence_after();
             uint8_t* y = c.sm + s * 2 * TILE;
             if (len < C) zero_rows(y + TILE, len, tid);
-            const float* wt = c.wtab + (REV ? 0 : C - len);
+            const float* wt = c.wtab + (c.rev ? 0 : C - len);
             const uint32_t w = lanes + TS_W + 192 * buf + 32 * grp;
 #pragma unroll 1
             for (int k = 0; k < 2; ++k)
@@ -859,62 +892,63 @@ lin_states_tc_kernel(const __grid_constant__ Args args) {
         }
         if (ok && wait_warp(b, &b->fin, 0, p, 336)) {
             tc_fence_after();
-            float* dst = p.seg_states +
-                         ((c.sg.u + c.sg.j) * (int64_t)p.H + c.h) * (int64_t)(D * D) +
-                         (size_t)r * D + 64 * grp;
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < 4; ++q) {
                 uint32_t v[16];
                 tmem_ld16(lanes + TS_U + 64 * grp + 16 * q, v);
                 tmem_wait_ld();
+                float f[16];
 #pragma unroll
-                for (int j = 0; j < 16; j += 4)
-                    *reinterpret_cast<uint4*>(dst + 16 * q + j) =
-                        make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
+#pragma unroll
+                for (int j = 0; j < 16; j += 4)   // (the stages are read)
+                    store_state(c.sm, r, 64 * grp + 16 * q + j, f + j);
             }
+            arrive_warp(&b->end);
         }
     }
     finish(c, 8);
 }
 
-template <bool REV>
-cudaError_t launch(const Args& args, unsigned grid, bool cut, cudaStream_t stream) {
-    cudaError_t err;
-    if (cut) {
-        err = cudaFuncSetAttribute(lin_states_tc_kernel<REV>,
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-        if (err != cudaSuccess) return err;
-        lin_states_tc_kernel<REV><<<grid, STATE_THREADS, SMEM, stream>>>(args);
-        err = launch_lin_scan(args.p, stream);
-        if (err != cudaSuccess) return err;
-    }
-    err = cudaFuncSetAttribute(lin_pass_tc_kernel<REV>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-    if (err != cudaSuccess) return err;
-    lin_pass_tc_kernel<REV><<<grid, THREADS, SMEM, stream>>>(args);
-    return cudaGetLastError();
+bool make_args(Args* a, const LinPass& p) {
+    a->p = p;
+    return make_row_map(&a->x, p.x, p.total_T, p.H, C) &&
+           make_row_map(&a->y, p.y, p.total_T, p.H, C) &&
+           make_row_map(&a->z, p.z, p.total_T, p.H, C) &&
+           make_row_map(&a->out, p.out, p.total_T, p.H, C) &&
+           (!p.state_in || make_state_map(&a->init, p.state_in, (int64_t)p.N * p.H)) &&
+           (!p.state_out || make_state_map(&a->last, p.state_out, (int64_t)p.N * p.H)) &&
+           (p.total_T < p.seg_len ||
+            make_state_map(&a->segs, p.seg_states, (int64_t)(p.total_T / p.seg_len) * p.H));
 }
 
 }  // namespace
 
-cudaError_t launch_lin_pass_tc(const LinPass& p, cudaStream_t stream) {
-    Args args;
-    memset(&args, 0, sizeof(args));
-    args.p = p;
-    if (!make_row_map(&args.x, p.x, p.total_T, p.H, C) ||
-        !make_row_map(&args.y, p.y, p.total_T, p.H, C) ||
-        !make_row_map(&args.z, p.z, p.total_T, p.H, C) ||
-        !make_row_map(&args.out, p.out, p.total_T, p.H, C) ||
-        (p.state_in && !make_state_map(&args.init, p.state_in, (int64_t)p.N * p.H)) ||
-        (p.total_T >= p.seg_len &&
-         !make_state_map(&args.segs, p.seg_states, (int64_t)(p.total_T / p.seg_len) * p.H))) {
-        return cudaErrorInvalidValue;
+cudaError_t launch_lin_pass_tc(const LinPass* passes, int n, cudaStream_t stream) {
+    Jobs jobs;
+    memset(&jobs, 0, sizeof(jobs));
+    jobs.n = n;
+    for (int i = 0; i < n; ++i) {
+        if (!make_args(&jobs.a[i], passes[i])) return cudaErrorInvalidValue;
     }
-    const int64_t most = (int64_t)p.total_T / p.seg_len;
-    const int64_t grid = (most + p.N) * p.H;
+    const LinPass& p = passes[0];
+    const int64_t most = (int64_t)p.total_T / p.seg_len;   // segments that are not a last one
+    const int64_t grid = (most + p.N) * p.H * n;
     if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-    return p.reverse ? launch<true>(args, (unsigned)grid, most > 0, stream)
-                     : launch<false>(args, (unsigned)grid, most > 0, stream);
+    cudaError_t err;
+    if (most > 0) {
+        err = cudaFuncSetAttribute(lin_states_tc_kernel,
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        if (err != cudaSuccess) return err;
+        lin_states_tc_kernel<<<(unsigned)grid, STATE_THREADS, SMEM, stream>>>(jobs);
+        err = launch_lin_scan(passes, n, stream);
+        if (err != cudaSuccess) return err;
+    }
+    err = cudaFuncSetAttribute(lin_pass_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               SMEM);
+    if (err != cudaSuccess) return err;
+    lin_pass_tc_kernel<<<(unsigned)grid, THREADS, SMEM, stream>>>(jobs);
+    return cudaGetLastError();
 }
 
 }  // namespace kda

@@ -613,36 +613,45 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
     }
 }
 
-// One block per 128 columns of one of the three sums; 32 rows of threads take
-// the parts in turn, then the rows are added in order.  dw_post of heads has a
-// part per tile too.
+// One block per 32 columns of one of the three sums: 128 rows of 8 threads take
+// the parts in turn, four columns a thread; rows are added in the order of a
+// fixed tree.  dw_post of heads has a part per tile too.
 __global__ void __launch_bounds__(1024) block_norm_sums_kernel(BlockNorm p, int parts, int tiles) {
-    __shared__ float4 buf[32][32];
+    __shared__ float4 buf[32][8];
     const int which = blockIdx.y;
     float* dst = which == 0 ? p.dw_post : which == 1 ? p.dres_scale : p.dw_pre;
     const int width = which == 0 ? p.group : p.D;
     const int per = which == 0 && p.group != p.D ? tiles : 1;
-    if (!dst || blockIdx.x * 128 >= width) return;
-    const int c = blockIdx.x * 128 + threadIdx.x * 4, n = parts * per;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!dst || blockIdx.x * 32 >= width) return;
+    const int c = blockIdx.x * 32 + (threadIdx.x & 7) * 4, n = parts * per;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
     if (c < width) {
 #pragma unroll 8
-        for (int k = threadIdx.y; k < n; k += 32) {
+        for (int k = threadIdx.x >> 3; k < n; k += 128) {
             const float4 v = *reinterpret_cast<const float4*>(
                 p.partial + ((size_t)(k / per) * 3 + which) * p.D + (k % per) * width + c);
-            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+            s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
         }
     }
-    buf[threadIdx.y][threadIdx.x] = s;
-    __syncthreads();
-    if (threadIdx.y == 0 && c < width) {
+    auto add_rows = [&]() {      // the four rows of a warp
 #pragma unroll
-        for (int k = 1; k < 32; ++k) {
-            const float4 v = buf[k][threadIdx.x];
-            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-        }
-        *reinterpret_cast<float4*>(dst + c) = s;
+        for (int m = 8; m < 32; m <<= 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], m);
+    };
+    add_rows();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane < 8) buf[warp][lane] = make_float4(s[0], s[1], s[2], s[3]);
+    __syncthreads();
+    if (warp > 0) return;
+    s[0] = s[1] = s[2] = s[3] = 0.f;
+#pragma unroll
+    for (int k = lane >> 3; k < 32; k += 4) {
+        const float4 v = buf[k][lane & 7];
+        s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
     }
+    add_rows();
+    if (lane < 8 && c < width) *reinterpret_cast<float4*>(dst + c) = make_float4(s[0], s[1], s[2], s[3]);
 }
 
 struct Shape {
@@ -734,8 +743,7 @@ cudaError_t backward(const BlockNorm& p, cudaStream_t stream) {
     }
     if (err == cudaSuccess) err = cudaGetLastError();
     if (err != cudaSuccess) return err;
-    block_norm_sums_kernel<<<dim3((p.D + 127) / 128, 3), dim3(32, 32), 0, stream>>>(p, parts,
-                                                                                    s.tiles);
+    block_norm_sums_kernel<<<dim3((p.D + 31) / 32, 3), 1024, 0, stream>>>(p, parts, s.tiles);
     return cudaGetLastError();
 }
 

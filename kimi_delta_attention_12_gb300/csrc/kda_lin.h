@@ -46,7 +46,7 @@ struct LinPass {
 // Tokens per segment for these sizes: every sequence is cut into segments of
 // this length so that a few long sequences still fill `sms` SMs.
 // `ctas_per_pair`: CTAs that work on one (sequence, head) pair without a cut;
-// `ctas_per_sm`: how many an SM takes at once.
+// `ctas_per_sm`: how many an SM is to get.
 int32_t lin_segment_tokens(int32_t N, int32_t total_T, int32_t H, int ctas_per_pair,
                            int ctas_per_sm, int sms);
 

@@ -37,10 +37,11 @@ bool on_tensor_cores(int32_t d_k, int32_t d_v, kda_dtype dt, uint32_t flags, int
 
 // The tensor-core form works on a (sequence, head) pair of each of the `passes` it
 // runs at once with one CTA an SM; the CUDA-core form with one CTA for each 32
-// columns of dz, of which an SM takes three.
+// columns of dz, of which an SM takes two, and a few rounds of them even out
+// ragged lengths (a ragged fp32 backward took 368 us with one round and a half).
 int32_t segment_tokens(int32_t N, int32_t total_T, int32_t H, int32_t dz, int tc_passes) {
     return tc_passes > 0 ? kda::lin_segment_tokens(N, total_T, H, tc_passes, 1, sm_count())
-                         : kda::lin_segment_tokens(N, total_T, H, dz / 32, 3, sm_count());
+                         : kda::lin_segment_tokens(N, total_T, H, dz / 32, 8, sm_count());
 }
 
 size_t seg_state_bytes(int32_t total_T, int32_t H, int32_t dx, int32_t dz, int32_t seg_len) {

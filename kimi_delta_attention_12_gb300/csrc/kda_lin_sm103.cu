@@ -36,7 +36,7 @@ using namespace sm103;
 constexpr int C = 128;                   // tokens per chunk = rows of a tile
 constexpr int D = 128;                   // dx = dz
 constexpr int THREADS = 896;             // the pass
-constexpr int STATE_THREADS = 320;       // the segment states: 8 warps, and 8 and 9 to issue
+constexpr int STATE_THREADS = 576;       // the segment states: 16 warps, and 16 and 17 to issue
 // Registers: 896 threads start with 72 each.  The warps that issue and those
 // that split give some up for the 8 that hold the state:
 // 128 (72 + 72 + 96 + 96 + 64 + 64 + 40) = 896 x 72.
@@ -273,8 +273,8 @@ __device__ __forceinline__ void split_w(uint32_t y, int quad, int tok0, const fl
 
 // Rows len .. 127 of a Z tile to zero: they meet zeros of P' and w Y, and may
 // hold another sequence's values, which need not be finite.
-__device__ __forceinline__ void zero_rows(uint8_t* z, int len, int tid) {
-    for (int i = tid; i < (C - len) * 16; i += 256) {
+__device__ __forceinline__ void zero_rows(uint8_t* z, int len, int tid, int threads) {
+    for (int i = tid; i < (C - len) * 16; i += threads) {
         const int row = len + (i >> 4), part = i & 15;
         *reinterpret_cast<uint4*>(z + (part >> 3) * HALF + row * 128 + (part & 7) * 16) =
             make_uint4(0, 0, 0, 0);
@@ -341,10 +341,11 @@ __device__ __forceinline__ void set_up(const Args& args, Cta& c, int issue, int 
             mbar_init(&b->empty[i], 1);
         }
         uint64_t* one[] = {&b->init, &b->xfree[0], &b->xfree[1], &b->qk, &b->o1, &b->o2, &b->u, &b->wfree[0], &b->wfree[1], &b->fin};
-        uint64_t* all[] = {&b->p, &b->s, &b->o1s, &b->od, &b->begun, &b->end};
+        uint64_t* all[] = {&b->p, &b->s, &b->o1s, &b->od, &b->begun};
         for (uint64_t* x : one) mbar_init(x, 1);
         for (uint64_t* x : all) mbar_init(x, 8);   // warps
         for (uint64_t& x : b->w) mbar_init(&x, w_warps);
+        mbar_init(&b->end, w_warps == 4 ? 8 : w_warps);   // the warps that hold a state
         b->abort = 0;
         fence_mbar_init();
     }
@@ -600,7 +601,7 @@ __device__ __forceinline__ void outputs(const LinPass& p, const Cta& c, uint32_t
         const int len = chunk_len(c, tok);
         if (len < C) {
             if (!wait_warp(b, &b->full[i & 1], (i >> 1) & 1, p, 310)) break;
-            zero_rows(c.sm + (i & 1) * 3 * TILE + 2 * TILE, len, threadIdx.x);
+            zero_rows(c.sm + (i & 1) * 3 * TILE + 2 * TILE, len, threadIdx.x, 256);
         }
         if (!wait_warp(b, &b->qk, ph, p, 311)) break;
         tc_fence_after();
@@ -805,7 +806,7 @@ lin_pass_tc_kernel(const __grid_constant__ Jobs jobs) {
 
 // ------------------------------------------------- the state a segment adds
 // sum_j a^{tokens from j to the segment's end} kv_scale y_j z_j^T, accumulated in TMEM
-// over the whole segment: the weights are taken to its end at once.  Eight
+// over the whole segment: the weights are taken to its end at once.  Sixteen
 // warps split w Y into one of two buffers while the products read the other.
 __global__ void __launch_bounds__(STATE_THREADS, 1)
 lin_states_tc_kernel(const __grid_constant__ Jobs jobs) {
@@ -815,11 +816,11 @@ lin_states_tc_kernel(const __grid_constant__ Jobs jobs) {
     const Args& args = *job;
     const LinPass& p = args.p;
     if (c.sg.j + 1 >= c.sg.count || c.sg.u + c.sg.j >= lin::seg_rows(p.total_T, p.seg_len)) return;
-    set_up(args, c, 8, 8);
+    set_up(args, c, 16, 16);
     Bars* b = c.b;
     const int tid = threadIdx.x, warp = tid >> 5, n = c.chunks;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    if (warp == 8) {
+    if (warp == 16) {
         if ((tid & 31) == 0) {
             int issued = 0;
             for (int i = 0; i < n; ++i) {
@@ -839,7 +840,7 @@ lin_states_tc_kernel(const __grid_constant__ Jobs jobs) {
                 bulk_wait<false>();
             }
         }
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         constexpr uint32_t id = idesc_bf16(D, D, 0, 1);
         for (int i = 0; i < n; ++i) {
             const int s = i % STATE_STAGES;
@@ -879,13 +880,10 @@ lin_states_tc_kernel(const __grid_constant__ Jobs jobs) {
             if (i >= 2 && !(ok = wait_warp(b, &b->wfree[buf], ((i >> 1) - 1) & 1, p, 335))) break;
             tc_fence_after();
             uint8_t* y = c.sm + s * 2 * TILE;
-            if (len < C) zero_rows(y + TILE, len, tid);
+            if (len < C) zero_rows(y + TILE, len, tid, 512);
             const float* wt = c.wtab + (c.rev ? 0 : C - len);
-            const uint32_t w = lanes + TS_W + 192 * buf + 32 * grp;
-#pragma unroll 1
-            for (int k = 0; k < 2; ++k)
-                split_w(smem_u32(y), warp & 3, 64 * grp + 32 * k, wt, f, len, w + 16 * k,
-                        w + 64 + 16 * k, w + 128 + 16 * k);
+            const uint32_t w = lanes + TS_W + 192 * buf + 16 * grp;
+            split_w(smem_u32(y), warp & 3, 32 * grp, wt, f, len, w, w + 64, w + 128);
             tmem_wait_st();
             tc_fence_before();
             arrive_warp(&b->w[buf]);
@@ -893,21 +891,21 @@ lin_states_tc_kernel(const __grid_constant__ Jobs jobs) {
         if (ok && wait_warp(b, &b->fin, 0, p, 336)) {
             tc_fence_after();
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
                 uint32_t v[16];
-                tmem_ld16(lanes + TS_U + 64 * grp + 16 * q, v);
+                tmem_ld16(lanes + TS_U + 32 * grp + 16 * q, v);
                 tmem_wait_ld();
                 float f[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
 #pragma unroll
                 for (int j = 0; j < 16; j += 4)   // (the stages are read)
-                    store_state(c.sm, r, 64 * grp + 16 * q + j, f + j);
+                    store_state(c.sm, r, 32 * grp + 16 * q + j, f + j);
             }
             arrive_warp(&b->end);
         }
     }
-    finish(c, 8);
+    finish(c, 16);
 }
 
 bool make_args(Args* a, const LinPass& p) {

@@ -498,8 +498,16 @@ KDA_API int kda_prefill_noalloc_status(void* stream);
  *  o              [total_T, H, d_v] dt
  *  final_state    [N, H, d_k, d_v] fp32 or NULL; may be initial_state itself
  *  workspace      kda_lin_prefill_workspace_bytes(...) bytes, 256-byte
- *                 aligned, no initialisation needed
+ *                 aligned, no initialisation needed; it begins with a status
+ *                 word that kda_workspace_status reads
  * A sequence of length zero hands its initial state (or zeros) on.
+ *
+ * bf16 with d_k = d_v = 128 runs on the tensor cores in chunks of 128 tokens;
+ * o carries the rounding to bf16 of the products q.k and of the carried state
+ * where they are multiplied (2^-9 each), the states keep fp32 sums.  Every other
+ * size and type runs in fp32 arithmetic on the CUDA cores, in chunks of 32.  A
+ * value that is not finite may reach the outputs of all tokens of its own chunk,
+ * earlier ones among them; it never reaches another sequence.
  * Errors (nothing is launched): as kda_prefill, and KDA_ERR_INVALID_ARG for an
  * output or the workspace on top of another buffer.
  */
@@ -545,7 +553,8 @@ KDA_API int kda_lin_decode_step(const void* q, const void* k, const void* v,
  *  dq, dk         [total_T, H, d_k] dt;  dv [total_T, H, d_v] dt;  dS0
  *                 [N, H, d_k, d_v] fp32 or NULL; written, not accumulated; no
  *                 output may overlap another buffer
- *  workspace      kda_lin_backward_workspace_bytes(...) bytes, 256-byte aligned
+ *  workspace      kda_lin_backward_workspace_bytes(...) bytes, 256-byte aligned,
+ *                 beginning with a status word as kda_lin_prefill's
  * The result is the same bits on every call (no atomics in any sum).
  */
 KDA_API int kda_lin_backward(const void* q, const void* k, const void* v,

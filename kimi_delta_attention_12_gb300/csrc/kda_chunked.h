@@ -139,11 +139,6 @@ void split_bind(const SplitPlan& plan, void* workspace, ChunkedParams* p);
 // by 128 channels (no swizzle: one 16 KB row-major tile) or, swizzled, 64
 // channels (128-byte swizzle: one 8 KB operand half per load).
 bool make_token_map(CUtensorMap* map, const void* base, int total_T, int H, bool swizzled);
-// The same tensor with boxes of `rows` tokens by 64 channels, 128-byte swizzled.
-bool make_row_map(CUtensorMap* map, const void* base, int total_T, int H, int rows);
-// TMA map of `count` fp32 states [128][128] with boxes of all rows by 32 columns,
-// 128-byte swizzled.
-bool make_state_map(CUtensorMap* map, const float* base, int64_t count);
 cudaError_t launch_chunked_prefill(const ChunkedParams& p, cudaStream_t stream);
 cudaError_t launch_split_prefill(const ChunkedParams& p, int num_sms, cudaStream_t stream);
 

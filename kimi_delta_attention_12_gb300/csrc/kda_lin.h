@@ -30,7 +30,7 @@ struct LinPass {
     float* state_out;           // [N, H, dx, dz], or null
     float* seg_states;          // workspace [total_T / seg_len][H][dx][dz]
     const int32_t* cu_seqlens;  // device [N + 1], or null (equal lengths)
-    int32_t* status;            // workspace status word (tensor-core form)
+    int32_t* status;            // workspace status word
     int32_t N;
     int32_t total_T;
     int32_t H;

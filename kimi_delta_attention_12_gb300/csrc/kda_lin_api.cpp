@@ -127,7 +127,6 @@ int kda_lin_prefill(const void* q, const void* k, const void* v, const float* lo
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     const bool tc = on_tensor_cores(d_k, d_v, dt, flags, total_T);
-    if (tc && cudaMemsetAsync(ws, 0, sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
     kda::LinPass p;
     memset(&p, 0, sizeof(p));
     p.x = q; p.y = k; p.z = v; p.out = o;
@@ -236,7 +235,6 @@ int kda_lin_backward(const void* q, const void* k, const void* v, const float* l
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     const bool tc = on_tensor_cores(d_k, d_v, dt, flags, total_T);
-    if (tc && cudaMemsetAsync(ws, 0, sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
     kda::LinPass pass[3];
     memset(pass, 0, sizeof(pass));
     for (kda::LinPass& p : pass) {

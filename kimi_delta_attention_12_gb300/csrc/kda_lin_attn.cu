@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(THREADS) lin_pass_kernel(LinPass p) {
     float* S = P + 4 * C * PLD;       // [DX][SLICE]
     float* lam = S + DX * SLICE;      // a^0 .. a^C
 
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;   // no wait here can run out
     const int tid = threadIdx.x, dz = p.dz, slices = dz / SLICE;
     const int col0 = (blockIdx.x % slices) * SLICE;
     const int64_t rest = blockIdx.x / slices;

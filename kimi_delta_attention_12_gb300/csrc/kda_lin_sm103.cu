@@ -19,11 +19,11 @@
 #include "kda_lin.h"
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <limits.h>
 #include <string.h>
 
-#include "kda_chunked.h"
 #include "kda_lin.cuh"
 #include "kda_packed.cuh"
 #include "sm103_ptx.cuh"
@@ -79,6 +79,7 @@ struct Args {
 struct Jobs {
     Args a[3];
     int n;
+    int first;                     // the call's first kernel: it clears the status word
 };
 
 struct Bars {
@@ -96,19 +97,44 @@ struct Bars {
 
 static_assert(sizeof(Bars) <= 320, "barriers");
 
-// Bounded wait that sleeps in the barrier (up to ~1 ms at a time) instead of
-// polling: polls would take issue slots from the warps that work.  False on a
-// timeout or when the CTA gives up.
+// 3-D tiled store of one box from shared memory, in this thread's bulk group.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src, int c0,
+                                             int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], "
+                 "[%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(smem_src)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Until the bulk stores of this thread have read their shared memory (READ), or
+// are done.
+template <bool READ>
+__device__ __forceinline__ void bulk_wait() {
+    if (READ) {
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    } else {
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+}
+
+// Bounded wait that sleeps in the barrier, up to 20 us at a time, instead of
+// polling: polls would take issue slots from the warps that work.  False when
+// the CTA gives up, or after WAIT_TRIES (some 10 s if every one sleeps its time
+// out; a wait of these kernels is over in microseconds).
+constexpr uint32_t WAIT_TRIES = 1u << 19;
+
 __device__ __forceinline__ bool sleep_wait(Bars* b, uint64_t* bar, uint32_t parity) {
     const uint32_t at = smem_u32(bar);
-    for (uint32_t i = 0; i < kSpinLimit; ++i) {
+    for (uint32_t i = 0; i < WAIT_TRIES; ++i) {
         uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
             "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(ok)
-            : "r"(at), "r"(parity), "r"(1000000u)
+            : "r"(at), "r"(parity), "r"(20000u)
             : "memory");
         if (ok) return true;
         if (b->abort) return false;
@@ -307,6 +333,8 @@ __device__ __forceinline__ const Args* start(const Jobs& jobs, Cta& c) {
     const int H = jobs.a[0].p.H, unit = blockIdx.x / H;
     const Args* args = &jobs.a[unit % jobs.n];
     const LinPass& p = args->p;
+    // (the earliest any CTA can report a wait is seconds away)
+    if (jobs.first && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
     c.sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                       ~(uintptr_t)1023);
     c.lam = reinterpret_cast<float*>(c.sm + SM_TAB);
@@ -908,12 +936,44 @@ lin_states_tc_kernel(const __grid_constant__ Jobs jobs) {
     finish(c, 16);
 }
 
+// A tensor [n2][n1][128] cut into boxes of b2 x b1 rows of 128 bytes, swizzled as the
+// tensor core's operands are.
+bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t n1, int64_t n2,
+              uint32_t b1, uint32_t b2) {
+    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                                         cudaEnableDefault, &found) == cudaSuccess &&
+                        found == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f) : nullptr;
+    }();
+    if (!encode || n1 > INT_MAX || n2 > INT_MAX) return false;
+    const cuuint64_t eb = type == CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 ? 2 : 4;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)n1, (cuuint64_t)n2};
+    const cuuint64_t strides[2] = {D * eb, D * eb * (cuuint64_t)n1};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / eb), b1, b2}, one[3] = {1, 1, 1};
+    return encode(map, type, 3, const_cast<void*>(base), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [total_T][H][128] bf16 in boxes of 128 tokens by 64 channels of one head.
+bool make_row_map(CUtensorMap* map, const void* base, const LinPass& p) {
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, p.H, p.total_T, 1, C);
+}
+// `count` fp32 states [128][128] in boxes of all rows by 32 columns.
+bool make_state_map(CUtensorMap* map, const float* base, int64_t count) {
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, D, count, D, 1);
+}
+
 bool make_args(Args* a, const LinPass& p) {
     a->p = p;
-    return make_row_map(&a->x, p.x, p.total_T, p.H, C) &&
-           make_row_map(&a->y, p.y, p.total_T, p.H, C) &&
-           make_row_map(&a->z, p.z, p.total_T, p.H, C) &&
-           make_row_map(&a->out, p.out, p.total_T, p.H, C) &&
+    return make_row_map(&a->x, p.x, p) &&
+           make_row_map(&a->y, p.y, p) &&
+           make_row_map(&a->z, p.z, p) &&
+           make_row_map(&a->out, p.out, p) &&
            (!p.state_in || make_state_map(&a->init, p.state_in, (int64_t)p.N * p.H)) &&
            (!p.state_out || make_state_map(&a->last, p.state_out, (int64_t)p.N * p.H)) &&
            (p.total_T < p.seg_len ||
@@ -926,6 +986,7 @@ cudaError_t launch_lin_pass_tc(const LinPass* passes, int n, cudaStream_t stream
     Jobs jobs;
     memset(&jobs, 0, sizeof(jobs));
     jobs.n = n;
+    jobs.first = 1;
     for (int i = 0; i < n; ++i) {
         if (!make_args(&jobs.a[i], passes[i])) return cudaErrorInvalidValue;
     }
@@ -939,6 +1000,7 @@ cudaError_t launch_lin_pass_tc(const LinPass* passes, int n, cudaStream_t stream
                                    cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
         if (err != cudaSuccess) return err;
         lin_states_tc_kernel<<<(unsigned)grid, STATE_THREADS, SMEM, stream>>>(jobs);
+        jobs.first = 0;
         err = launch_lin_scan(passes, n, stream);
         if (err != cudaSuccess) return err;
     }

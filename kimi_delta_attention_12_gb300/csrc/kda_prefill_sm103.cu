@@ -1232,14 +1232,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 bool make_map_impl(CUtensorMap* map, const void* base, int total_T, int H, int box_c,
-                   CUtensorMapSwizzle swz, int box_t = C) {
+                   CUtensorMapSwizzle swz) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
     if (!fn) {
         return false;
     }
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)total_T};
     cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
-    cuuint32_t box[3] = {(cuuint32_t)box_c, 1, (cuuint32_t)box_t};
+    cuuint32_t box[3] = {(cuuint32_t)box_c, 1, (cuuint32_t)C};
     cuuint32_t es[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
               box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1251,25 +1251,6 @@ bool make_map_impl(CUtensorMap* map, const void* base, int total_T, int H, int b
 bool make_token_map(CUtensorMap* map, const void* base, int total_T, int H, bool swizzled) {
     return make_map_impl(map, base, total_T, H, swizzled ? 64 : 128,
                          swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
-}
-
-bool make_row_map(CUtensorMap* map, const void* base, int total_T, int H, int rows) {
-    return make_map_impl(map, base, total_T, H, 64, CU_TENSOR_MAP_SWIZZLE_128B, rows);
-}
-
-bool make_state_map(CUtensorMap* map, const float* base, int64_t count) {
-    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
-    if (!fn || count > INT32_MAX) {
-        return false;
-    }
-    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)D, (cuuint64_t)count};
-    cuuint64_t strides[2] = {(cuuint64_t)D * 4, (cuuint64_t)D * D * 4};
-    cuuint32_t box[3] = {32, (cuuint32_t)D, 1};
-    cuuint32_t es[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(base), dims, strides,
-              box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-           CUDA_SUCCESS;
 }
 
 namespace {

@@ -84,30 +84,6 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
         : "memory");
 }
 
-// 3-D tiled store of one box from shared memory (its own bulk group member).
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src, int c0,
-                                             int c1, int c2) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], "
-                 "[%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
-                 "r"(smem_u32(smem_src)), "r"(c0), "r"(c1), "r"(c2)
-                 : "memory");
-}
-
-__device__ __forceinline__ void bulk_commit() {
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-
-// Until the bulk stores committed by this thread have read their shared memory
-// (READ), or are done.
-template <bool READ>
-__device__ __forceinline__ void bulk_wait() {
-    if (READ) {
-        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-    } else {
-        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    }
-}
-
 // Plain bulk copy of `bytes` (a multiple of 16, both addresses 16-byte
 // aligned) from global into shared memory, completing on `bar`.
 __device__ __forceinline__ void bulk_load(void* smem_dst, const void* gsrc, uint32_t bytes,

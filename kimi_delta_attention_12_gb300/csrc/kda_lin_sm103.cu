@@ -329,12 +329,12 @@ struct Cta {
 // The pass and the segment of this CTA (heads fastest, then the passes, then the
 // segments).  Whole sequences come longest first, so that none starts late.
 __device__ __forceinline__ const Args* start(const Jobs& jobs, Cta& c) {
+    // (the earliest any CTA can report a wait is seconds away)
+    if (jobs.first && blockIdx.x == 0 && threadIdx.x == 0) *jobs.a[0].p.status = 0;
     extern __shared__ uint8_t smem_raw[];
     const int H = jobs.a[0].p.H, unit = blockIdx.x / H;
     const Args* args = &jobs.a[unit % jobs.n];
     const LinPass& p = args->p;
-    // (the earliest any CTA can report a wait is seconds away)
-    if (jobs.first && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
     c.sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                       ~(uintptr_t)1023);
     c.lam = reinterpret_cast<float*>(c.sm + SM_TAB);

@@ -328,3 +328,55 @@ def test_binding_refusals():
         kda.kda_lin_prefill(*a, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(kda.KDAError):
         kda.kda_lin_prefill(*a, o=x["v"])                   # onto an input
+
+
+def test_many_ragged_sequences_in_any_order():
+    """More (sequence, head) pairs than SMs: whole sequences, taken longest first."""
+    lens = [5, 300, 0, 129, 128, 1, 257, 40] * 5          # 40 sequences, ties among them
+    x = R.make(lens, 4, 128, 128, BF, seed=12, state=True)
+    v = R.dev(x)
+    for n in (40, 70):                                     # ranked, and past the ranked range
+        cu = torch.cat([x["cu"], x["cu"][-1:].repeat(n - 40)])
+        S0 = torch.cat([v["S0"], v["S0"][:n - 40]])
+        o, S = kda.kda_lin_prefill(v["q"], v["k"], v["v"], v["log_decay"], S0, cu.cuda(), cu)
+        assert torch.equal(S[40:], S0[40:])                # empty ones hand theirs on
+        check_forward(x, o, S[:40], 1.0, 128, BF, True)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.75, 2.5])
+def test_scales(scale):
+    for dtype, d in ((F, 32), (BF, 128)):
+        x = R.make([150, 20], 2, d, d, dtype, seed=13, state=True)
+        v = R.dev(x)
+        o, S = kda.kda_lin_prefill(v["q"], v["k"], v["v"], v["log_decay"], v["S0"], v["cu"],
+                                   x["cu"], scale=scale)
+        check_forward(x, o, S, scale, d, dtype, dtype == BF)
+        g = kda.kda_lin_backward(v["q"], v["k"], v["v"], v["log_decay"], v["dO"], v["S0"],
+                                 v["cu"], x["cu"], v["dS"], scale=scale)
+        a = {n: R.f64(t) for n, t in x.items() if isinstance(t, torch.Tensor)}
+        want = R.lin_backward(a["q"], a["k"], a["v"], a["log_decay"], x["lens"], a["dO"],
+                              a["S0"], a["dS"], scale)
+        for n in want:
+            assert R.rel_fro(g[n], want[n]) <= (R.U16 if g[n].dtype == BF else 2e-6), n
+
+
+def test_growing_decay():
+    """log_decay above zero: the formula as it stands."""
+    for dtype, d in ((F, 64), (BF, 128)):
+        x = R.make([200], 2, d, d, dtype, seed=14, state=True, g=[0.02, 0.005])
+        v = R.dev(x)
+        o, S = kda.kda_lin_prefill(v["q"], v["k"], v["v"], v["log_decay"], v["S0"])
+        check_forward(x, o, S, 1.0, d, dtype, dtype == BF)
+
+
+@pytest.mark.parametrize("dtype,d", [(F, 32), (BF, 128)])
+def test_status_word(dtype, d):
+    x = R.make([200], 1, d, d, dtype)
+    v = R.dev(x)
+    args = (v["q"], v["k"], v["v"], v["log_decay"])
+    for size, call in ((kda.lin_prefill_workspace_bytes, lambda w: kda.kda_lin_prefill(
+            *args, workspace=w)), (kda.lin_backward_workspace_bytes,
+                                   lambda w: kda.kda_lin_backward(*args, v["dO"], workspace=w))):
+        w = torch.full((size(1, 200, 1, d, d, dtype),), 255, dtype=torch.uint8, device="cuda")
+        call(w)
+        assert kda.workspace_status(w) == kda.KDA_OK

@@ -47,10 +47,28 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
 
 constexpr int PLD = C + 4;   // row of a 32 x 32 tile of products
 
+// fp32 rows come by asynchronous copies, a chunk ahead; bf16 ones are converted on
+// their way through registers and have one stage.
+template <typename T>
+constexpr int STAGES = sizeof(T) == 4 ? 2 : 1;
 template <int DX>
+constexpr int STAGE_FLOATS = 2 * C * (DX + 4) + C * SLICE;   // X, Y, Z
+
+template <typename T, int DX>
 constexpr size_t pass_smem_bytes() {
     return sizeof(float) *
-           (2 * C * (DX + 4) + C * SLICE + 4 * C * PLD + DX * SLICE + (C + 4));
+           (STAGES<T> * STAGE_FLOATS<DX> + 4 * C * PLD + DX * SLICE + (C + 4));
+}
+
+// Four values to shared memory, zeros instead unless `live`.
+__device__ __forceinline__ void copy4(float* dst, const float* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(dst)),
+                 "l"(src), "r"(live ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy4(float* dst, const __nv_bfloat16* src, bool live) {
+    store4(dst, live ? load4(src) : make_float4(0.f, 0.f, 0.f, 0.f));
 }
 
 // 4 values at the thread's rows of a state: row d of [dx][dz], or of a turned one.
@@ -98,10 +116,8 @@ template <typename T, int DX, bool STATES>
 __global__ void __launch_bounds__(THREADS) lin_pass_kernel(LinPass p) {
     constexpr int LD = DX + 4, ROWS = DX / 32;
     extern __shared__ float4 smem4[];
-    float* X = reinterpret_cast<float*>(smem4);
-    float* Y = X + C * LD;
-    float* Z = Y + C * LD;
-    float* P = Z + C * SLICE;         // [4][C][PLD]
+    float* stages = reinterpret_cast<float*>(smem4);
+    float* P = stages + STAGES<T> * STAGE_FLOATS<DX>;   // [4][C][PLD]
     float* S = P + 4 * C * PLD;       // [DX][SLICE]
     float* lam = S + DX * SLICE;      // a^0 .. a^C
 
@@ -148,26 +164,39 @@ __global__ void __launch_bounds__(THREADS) lin_pass_kernel(LinPass p) {
     // x . y) or 4 q .. 4 q + 3 (of the outputs)
     const int grp = tid / 64, r = (tid / 8) & 7, q = tid & 7;
     const int64_t chunks = (sg.t1 - sg.t0 + C - 1) / C;
-    for (int64_t ci = 0; ci < chunks; ++ci) {
-        const int64_t c0 = sg.t0 + (p.reverse ? chunks - 1 - ci : ci) * C;
+    auto first = [&](int64_t ci) { return sg.t0 + (p.reverse ? chunks - 1 - ci : ci) * C; };
+    auto load_chunk = [&](int64_t ci) {
+        float* X = stages + (ci % STAGES<T>) * STAGE_FLOATS<DX>;
+        float *Y = X + C * LD, *Z = Y + C * LD;
+        const int64_t c0 = first(ci);
         const int len = (int)(sg.t1 - c0 < C ? sg.t1 - c0 : C);
 #pragma unroll
         for (int k = 0; k < C * DX / 4 / THREADS; ++k) {
             const int i = tid + k * THREADS, row = i / (DX / 4), d = (i % (DX / 4)) * 4;
-            float4 vx = make_float4(0.f, 0.f, 0.f, 0.f), vy = vx;
-            if (row < len) {
-                const size_t at = ((size_t)(c0 + row) * p.H + h) * DX + d;
-                if (!STATES) vx = load4(x + at);
-                vy = load4(y + at);
-            }
-            if (!STATES) store4(X + row * LD + d, vx);
-            store4(Y + row * LD + d, vy);
+            const bool live = row < len;
+            const size_t at = ((size_t)(c0 + (live ? row : 0)) * p.H + h) * DX + d;
+            if (!STATES) copy4(X + row * LD + d, x + at, live);
+            copy4(Y + row * LD + d, y + at, live);
         }
-        {
-            const int row = tid / 8;
-            float4 vz = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (row < len) vz = load4(z + ((size_t)(c0 + row) * p.H + h) * dz + col0 + c4);
-            store4(Z + row * SLICE + c4, vz);
+        const int row = tid / 8;
+        const bool live = row < len;
+        copy4(Z + row * SLICE + c4,
+              z + ((size_t)(c0 + (live ? row : 0)) * p.H + h) * dz + col0 + c4, live);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (STAGES<T> == 2 && chunks > 0) load_chunk(0);
+    for (int64_t ci = 0; ci < chunks; ++ci) {
+        const int64_t c0 = first(ci);
+        const int len = (int)(sg.t1 - c0 < C ? sg.t1 - c0 : C);
+        const float* X = stages + (ci % STAGES<T>) * STAGE_FLOATS<DX>;
+        const float *Y = X + C * LD, *Z = Y + C * LD;
+        if (STAGES<T> == 1) {
+            load_chunk(ci);
+        } else if (ci + 1 < chunks) {
+            load_chunk(ci + 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
         if (!STATES) {
 #pragma unroll
@@ -296,23 +325,30 @@ __global__ void __launch_bounds__(THREADS) lin_pass_kernel(LinPass p) {
     }
 }
 
+// Beyond 48 KB a kernel has to be allowed its shared memory.
+cudaError_t allow(const void* kernel, int smem) {
+    return smem <= 48 * 1024 ? cudaSuccess
+                             : cudaFuncSetAttribute(
+                                   kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
+
 template <typename T, int DX>
 cudaError_t launch_pass(const LinPass& p, cudaStream_t stream) {
-    constexpr int smem = (int)pass_smem_bytes<DX>();
+    constexpr int smem = (int)pass_smem_bytes<T, DX>();
     const int64_t most = (int64_t)p.total_T / p.seg_len;   // segments that are not a last one
     const int64_t grid = (most + p.N) * p.H * (p.dz / SLICE);
     if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
     cudaError_t err;
     if (most > 0) {
         auto* k1 = lin_pass_kernel<T, DX, true>;
-        err = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        err = allow(reinterpret_cast<const void*>(k1), smem);
         if (err != cudaSuccess) return err;
         k1<<<(unsigned)grid, THREADS, smem, stream>>>(p);
         err = launch_lin_scan(&p, 1, stream);
         if (err != cudaSuccess) return err;
     }
     auto* k2 = lin_pass_kernel<T, DX, false>;
-    err = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    err = allow(reinterpret_cast<const void*>(k2), smem);
     if (err != cudaSuccess) return err;
     k2<<<(unsigned)grid, THREADS, smem, stream>>>(p);
     return cudaGetLastError();

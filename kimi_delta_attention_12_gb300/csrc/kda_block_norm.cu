@@ -82,7 +82,7 @@ __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[V]) {
 // 1 / (1 + e^-t).  fp32: a few units in the last place.  bf16 rows: from the
 // approximate 2^x and reciprocal, relative error near 2^-22 (1 + |t|), which
 // the rounding of the gate itself (2^-9) hides, in 4 instructions instead of 14:
-// with the full expf the heads' forward took 885 us where it now takes 7xx.
+// with the full expf 65,536 rows of 96 heads took 885 us where they take 780.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float t);
 template <>
@@ -131,9 +131,19 @@ __device__ __forceinline__ void lane_sum(float (&s)[M], int width) {
     }
 }
 
-// Sums over the warps of a row (all threads of the block call it; threadIdx.y
-// is the row).  `turn` alternates between two halves of the buffer, so that
-// one barrier per sum is enough.
+// The threads of one row wait for one another (threadIdx.y is the row; a block
+// has two rows of several warps at most).
+__device__ __forceinline__ void row_wait() {
+    if (threadIdx.y == 0) {
+        asm volatile("bar.sync 1, %0;" ::"r"(blockDim.x) : "memory");
+    } else {
+        asm volatile("bar.sync 2, %0;" ::"r"(blockDim.x) : "memory");
+    }
+}
+
+// Sums over the warps of a row (all threads of the row call it).  `turn`
+// alternates between two halves of the buffer, so that one barrier per sum is
+// enough.
 template <int M>
 __device__ __forceinline__ void row_sum(float (&s)[M], float* buf, int warps, int turn) {
     lane_sum(s, 32);
@@ -144,7 +154,7 @@ __device__ __forceinline__ void row_sum(float (&s)[M], float* buf, int warps, in
 #pragma unroll
         for (int i = 0; i < M; ++i) b[w * 3 + i] = s[i];
     }
-    __syncthreads();
+    row_wait();
     // every warp adds the (up to 16) warps' sums itself, in each half of its lanes
     const int lane = threadIdx.x & 15;
 #pragma unroll
@@ -253,8 +263,7 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_kernel(BlockNorm p) {
     };
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     fetch_row(row);
-    for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < p.rows; r0 += step, row += step) {
-        const bool live = row < p.rows;
+    for (; row < p.rows; row += step) {
         float u[VPT][V];
         Raw<T> cg[VPT], cx[VPT];
 #pragma unroll
@@ -286,7 +295,7 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_kernel(BlockNorm p) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int vec = threadIdx.x + i * blockDim.x;
-            if (!live || vec >= vecs) continue;
+            if (vec >= vecs) continue;
             float g[V], xs[V];
             expand(cg[i], g);
             expand(cx[i], xs);
@@ -306,7 +315,7 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_kernel(BlockNorm p) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int vec = threadIdx.x + i * blockDim.x;
-                if (!live || vec >= vecs) continue;
+                if (vec >= vecs) continue;
                 float w[V];
                 load(p.w_pre + vec * V, w);
 #pragma unroll
@@ -314,7 +323,7 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_kernel(BlockNorm p) {
                 store(static_cast<T*>(p.h) + (size_t)row * p.D + (size_t)vec * V, u[i]);
             }
         }
-        if (warps > 1 && (whole != (p.w_pre != nullptr))) __syncthreads();   // one sum a row: the
+        if (warps > 1 && (whole != (p.w_pre != nullptr))) row_wait();   // one sum a row: the
         // next row writes the half that this row still reads
     }
 }
@@ -334,8 +343,13 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_kernel(BlockNorm p) {
 // under way or at work; a thread copies what it reads itself, so that its own
 // wait is enough.  The registers that rows in flight would take go to the
 // sums.  Rows too wide for that (stages = 0) are read into registers.
-// FULL: a block takes one row at a time and its threads cover the columns
-// exactly, so that nothing needs a guard.
+// FULL: a row's threads cover the columns exactly, so that nothing needs a guard.
+// KEEP: the three weights are in shared memory too, for the block's rows.  Beside
+// two blocks' rings of wide rows L1 is too small for them, and each row would
+// wait for L2: 4,096 rows of 4,096 in bf16 took 69 us without it and take 59
+// (4.6 TB/s, 68 % of a plain copy's).  What is left is the chain of a row: two sums
+// over it, each a barrier, with 16 warps on an SM (128 registers a thread); the
+// instructions alone would take 28 us.  64 registers and twice the warps: 79 us.
 enum { Y = 0, GATE = 1, DXO = 2, X = 3, DH = 4, TENSORS = 5 };
 
 __device__ __forceinline__ void copy16(void* smem, const void* src) {
@@ -356,7 +370,7 @@ __device__ __forceinline__ void copies_done(int behind) {   // all but the last 
 
 enum { NO_GATE = 0, SIGMOID = 1, SILU = 2 };
 
-template <typename T, int VPT, int ACT, bool RING, bool FULL>
+template <typename T, int VPT, int ACT, bool RING, bool FULL, bool KEEP = false>
 __global__ void __launch_bounds__(MAX_THREADS)
 block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
     __shared__ float buf[2 * MAX_ROWS * 32 * 3];
@@ -380,6 +394,18 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int all = blockDim.x * blockDim.y, flat = threadIdx.y * blockDim.x + threadIdx.x;
     Raw<T>* ring = reinterpret_cast<Raw<T>*>(dyn4);   // [stages][TENSORS][VPT][all]
+    float* kept = reinterpret_cast<float*>(ring + stages * TENSORS * VPT * all);   // [3][tile]
+    if (KEEP) {
+        for (int c = flat; c < tile; c += all) {
+            if (c < p.group) kept[c] = p.w_post[c];
+            if (p.res_scale) kept[tile + c] = p.res_scale[c];
+            if (p.w_pre) kept[2 * tile + c] = p.w_pre[c];
+        }
+        __syncthreads();
+    }
+    const float* w_post = KEEP ? kept : p.w_post;
+    const float* res_scale = KEEP ? kept + tile : p.res_scale;
+    const float* w_pre = KEEP ? kept + 2 * tile : p.w_pre;
     auto slot = [&](int stage, int k, int i) {
         return ring + ((stage * TENSORS + k) * VPT + i) * all + flat;
     };
@@ -407,8 +433,7 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
     }
     int stage = 0;
     const float inv_row = 1.0f / (float)p.D, inv_group = 1.0f / (float)p.group;
-    for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < p.rows; r0 += step, row += step) {
-        const bool live = FULL || row < p.rows;
+    for (; row < p.rows; row += step) {
         Raw<T> held[RING ? 1 : TENSORS][RING ? 1 : VPT];
         if (RING) {
             // the stage that the row before has left takes the next row to come
@@ -422,12 +447,12 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
                 for (int i = 0; i < VPT; ++i) {
                     const int vec = vec0 + i * blockDim.x;
                     clear(held[k][i]);
-                    if (src[k] && live && vec < vecs)
+                    if (src[k] && vec < vecs)
                         fetch(src[k] + (size_t)row * p.D + (size_t)vec * V, held[k][i]);
                 }
         }
         auto get = [&](int k, int i, uint64_t (&v)[V / 2]) {
-            const bool in = FULL || (live && vec0 + i * (int)blockDim.x < vecs);
+            const bool in = FULL || vec0 + i * (int)blockDim.x < vecs;
             if (RING) {
                 Raw<T> r;
                 if (!FULL) clear(r);
@@ -447,7 +472,7 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
                 uint64_t w[V / 2], h[V / 2];
                 get(X, i, a);
                 get(DH, i, h);
-                load2(p.w_pre + vec * V, w);
+                load2(w_pre + vec * V, w);
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e) {
                     q0 = fma2(a[e], a[e], q0);
@@ -483,7 +508,7 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int vec = vec0 + i * blockDim.x;
-            const bool in = FULL || (live && vec < vecs);
+            const bool in = FULL || vec < vecs;
             const size_t at = (size_t)row * p.D + (size_t)vec * V;
             uint64_t w[V / 2], part = 0;
             if (src[DXO]) {
@@ -496,7 +521,7 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
                 uint64_t a[V / 2], h[V / 2];
                 get(X, i, a);
                 get(DH, i, h);
-                load2(p.w_pre + vec * V, w);
+                load2(w_pre + vec * V, w);
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e) {
                     h[e] = mul2(h[e], rx2);
@@ -510,8 +535,8 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
                 const uint64_t one = two(1.f, 1.f), r2 = two(rr[i], rr[i]);
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e) rs[e] = one;
-                if (p.res_scale) load2(p.res_scale + vec * V, rs);
-                load2(p.w_post + (whole ? vec : vec & (lanes - 1)) * V, w);
+                if (p.res_scale) load2(res_scale + vec * V, rs);
+                load2(w_post + (whole ? vec : vec & (lanes - 1)) * V, w);
                 get(Y, i, a);
                 if (ACT != NO_GATE) get(GATE, i, g);
 #pragma unroll
@@ -550,12 +575,12 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) cc[i] = s2[0] * inv_row;
         } else if (sums && warps > 1) {
-            __syncthreads();   // the next row writes the sums this row has read
+            row_wait();   // the next row writes the sums this row has read
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int vec = vec0 + i * blockDim.x;
-            if (!FULL && (!live || vec >= vecs)) continue;
+            if (!FULL && vec >= vecs) continue;
             uint64_t a[V / 2];
             get(Y, i, a);
             const float c = -cc[i] * rr[i] * rr[i] * rr[i];
@@ -678,6 +703,34 @@ Shape shape_of(int32_t D, bool coupled, int most) {
 constexpr int BACKWARD_THREADS = 256;
 constexpr size_t RING_HALF = 110 * 1024, RING_ALL = 220 * 1024;
 
+// The backward's shape.  A ring of up to 3 rows in half of an SM's shared memory,
+// of 2 in all of it.  Two rows of 256 threads, each with its ring of 2, share a
+// block where that lets the weights stay beside them (4,096 columns of bf16).
+struct BackwardShape {
+    Shape s;
+    int stages;
+    bool full, keep;
+    size_t smem;
+};
+
+BackwardShape backward_shape(int32_t D, bool coupled, int bytes) {
+    BackwardShape b;
+    b.s = shape_of(D, coupled, BACKWARD_THREADS);
+    Shape& s = b.s;
+    const size_t row = (size_t)TENSORS * s.vpt * s.block.x * s.block.y * V * bytes;
+    const size_t sums = (size_t)s.tile * sizeof(float);
+    b.stages = 3 * row <= RING_HALF ? 3 : 2 * row <= RING_ALL ? 2 : 0;
+    b.full = s.tiles * s.tile == D && s.tile == (int)s.block.x * s.vpt * V;
+    b.keep = b.full && s.tiles == 1 && s.vpt == 2 && s.block.x == 256 && b.stages == 2 &&
+             4 * row + 3 * sums <= RING_ALL;
+    b.smem = b.stages * row > sums ? b.stages * row : sums;
+    if (b.keep) {
+        s.block.y = 2;
+        b.smem = 4 * row + 3 * sums;
+    }
+    return b;
+}
+
 bool coupled(const BlockNorm& p) { return p.group == p.D || p.w_pre; }
 
 template <typename T>
@@ -700,35 +753,39 @@ cudaError_t forward(const BlockNorm& p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
+// The backward's blocks along the rows: what keeps 152 SMs busy, fewer where
+// there are fewer rows.
+int parts_of(const Shape& s, int64_t rows) {
+    const int threads = s.block.x * s.block.y;
+    const int most = 152 * (threads <= 128 ? 4 : threads <= 256 ? 2 : 1);
+    const int64_t blocks = (rows + s.block.y - 1) / s.block.y;
+    return (int)(blocks < most ? (blocks < 1 ? 1 : blocks) : most);
+}
+
 template <typename T>
 cudaError_t backward(const BlockNorm& p, cudaStream_t stream) {
-    const Shape s = shape_of(p.D, coupled(p), BACKWARD_THREADS);
-    const int parts = block_norm_parts(p.rows, p.D);
+    const BackwardShape b = backward_shape(p.D, coupled(p), sizeof(T));
+    const Shape& s = b.s;
+    const int parts = b.keep ? parts_of(s, p.rows) : block_norm_parts(p.rows, p.D);
     const dim3 grid(parts, s.tiles);
-    // a ring of up to 3 rows in half of an SM's shared memory, of 2 in all of it
-    const size_t row = (size_t)TENSORS * s.vpt * s.block.x * s.block.y * V * sizeof(T);
-    const int stages = 3 * row <= RING_HALF ? 3 : 2 * row <= RING_ALL ? 2 : 0;
-    const size_t sums = (size_t)s.tile * sizeof(float), ring = stages * row;
-    const size_t smem = ring > sums ? ring : sums;
     cudaError_t err = cudaSuccess;
     auto launch = [&](auto kernel) {
-        if (smem > 48 * 1024) {
+        if (b.smem > 48 * 1024) {
             err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+                                       (int)b.smem);
         }
-        if (err == cudaSuccess) kernel<<<grid, s.block, smem, stream>>>(p, s.tile, stages);
+        if (err == cudaSuccess) kernel<<<grid, s.block, b.smem, stream>>>(p, s.tile, b.stages);
     };
-    const bool full = s.block.y == 1 && p.D % s.tile == 0 &&
-                      s.tile == (int)s.block.x * s.vpt * V;
     auto with_gate = [&](auto act) {
         constexpr int ACT = decltype(act)::value;
-        if (stages == 0) {
+        if (b.stages == 0) {
             launch(block_norm_backward_kernel<T, 4, ACT, false, false>);
         } else if (s.vpt == 1) {
-            if (full) launch(block_norm_backward_kernel<T, 1, ACT, true, true>);
+            if (b.full) launch(block_norm_backward_kernel<T, 1, ACT, true, true>);
             else launch(block_norm_backward_kernel<T, 1, ACT, true, false>);
         } else if (s.vpt == 2) {
-            if (full) launch(block_norm_backward_kernel<T, 2, ACT, true, true>);
+            if (b.keep) launch(block_norm_backward_kernel<T, 2, ACT, true, true, true>);
+            else if (b.full) launch(block_norm_backward_kernel<T, 2, ACT, true, true>);
             else launch(block_norm_backward_kernel<T, 2, ACT, true, false>);
         } else {
             launch(block_norm_backward_kernel<T, 4, ACT, true, false>);
@@ -749,14 +806,9 @@ cudaError_t backward(const BlockNorm& p, cudaStream_t stream) {
 
 }  // namespace
 
-// The backward's blocks along the rows: what keeps 152 SMs busy, fewer where
-// there are fewer rows.
+// Room for the sums of the most blocks that any type takes.
 int block_norm_parts(int64_t rows, int32_t D) {
-    const Shape s = shape_of(D, true, BACKWARD_THREADS);
-    const int threads = s.block.x * s.block.y;
-    const int most = 152 * (threads <= 128 ? 4 : threads <= 256 ? 2 : 1);
-    const int64_t blocks = (rows + s.block.y - 1) / s.block.y;
-    return (int)(blocks < most ? (blocks < 1 ? 1 : blocks) : most);
+    return parts_of(shape_of(D, true, BACKWARD_THREADS), rows);
 }
 
 cudaError_t launch_block_norm(const BlockNorm& p, int dtype, cudaStream_t stream) {

@@ -27,6 +27,9 @@ CASES = [
     (700, 1024, 128, "sigmoid", False, True, False, BF),
     (401, 2304, 0, "sigmoid", True, True, True, BF),
     (4, 4096, 0, "sigmoid", True, False, True, BF),
+    (333, 4096, 0, "sigmoid", True, True, True, BF),
+    (607, 4096, 128, "silu", False, True, True, BF),
+    (5, 4096, 0, "none", False, True, False, BF),
     (3, 4104, 0, "silu", True, True, True, F),
     (5, 7168, 64, "silu", False, False, True, BF),
     (2, 8200, 0, "sigmoid", True, True, True, BF),

@@ -137,5 +137,34 @@ __device__ __forceinline__ Segment first_segment(const int32_t* cu, int N, int64
     return s;
 }
 
+// Sequence n cut in two, a head of `lead` segments and a tail (n < 0: no such
+// part).  The state before the tail is the one after segment lead - 1; a
+// sequence of no more than `lead` segments is all head.
+__device__ __forceinline__ Segment half_segment(const int32_t* cu, int N, int64_t total_T,
+                                                int64_t seg_len, int reverse, int lead, int n,
+                                                bool tail) {
+    Segment s = first_segment(cu, N, total_T, seg_len, reverse, n);
+    const bool two = s.count > lead;
+    if (tail && !two) s.n = -1;
+    const int64_t at = reverse ? s.bos + (s.count - lead) * seg_len : s.bos + lead * seg_len;
+    s.t0 = s.bos;
+    s.t1 = s.eos;
+    if (two) (tail != (reverse != 0) ? s.t0 : s.t1) = at;
+    s.j = tail ? lead : 0;
+    s.count = two ? lead + 1 : 1;
+    return s;
+}
+
+// Segment j of the head of sequence n, where there is a tail behind it.
+__device__ __forceinline__ Segment lead_segment(const int32_t* cu, int N, int64_t total_T,
+                                                int64_t seg_len, int reverse, int lead, int n,
+                                                int j) {
+    Segment s = first_segment(cu, N, total_T, seg_len, reverse, n);
+    if (s.count <= lead) s.n = -1;
+    s.j = j;
+    seg_tokens(s, j, seg_len, reverse, s.t0, s.t1);
+    return s;
+}
+
 }  // namespace lin
 }  // namespace kda

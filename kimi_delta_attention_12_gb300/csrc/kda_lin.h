@@ -37,18 +37,28 @@ struct LinPass {
     int32_t dx;
     int32_t dz;
     int32_t seg_len;            // tokens per segment, a multiple of 128
+    int32_t lead;               // segments of a sequence's head where it is cut in two, else 0
     int32_t state_in_turned;    // state_in holds [dz, dx]
     int32_t reverse;
     float out_scale;
     float kv_scale;
 };
 
-// Tokens per segment for these sizes: every sequence is cut into segments of
-// this length so that a few long sequences still fill `sms` SMs.
+// The cut of the sequences for these sizes: every one is cut into segments of
+// seg_len tokens so that a few long sequences still fill `sms` SMs.
 // `ctas_per_pair`: CTAs that work on one (sequence, head) pair without a cut;
 // `ctas_per_sm`: how many an SM is to get.
-int32_t lin_segment_tokens(int32_t N, int32_t total_T, int32_t H, int ctas_per_pair,
-                           int ctas_per_sm, int sms);
+struct LinCut {
+    int32_t seg_len;
+    int32_t lead;
+};
+LinCut lin_cut(int32_t N, int32_t total_T, int32_t H, int ctas_per_pair, int ctas_per_sm, int sms);
+// The cut for the pass on the tensor cores (one CTA an SM).  Where the pairs fill
+// more than half of the SMs but not all, each sequence is cut in two: a head of
+// `lead` segments, and a tail.  The idle SMs work on heads, k of them one after
+// another while a tail, k times as long, runs; the states before the tails come
+// first, from the heads' segments over all SMs.
+LinCut lin_cut_tc(int32_t N, int32_t total_T, int32_t H, int passes, int sms);
 
 // The pass on the CUDA cores, fp32 arithmetic: dx, dz in {32, 64, 128}, dtype
 // 0 = fp32, 1 = bf16.

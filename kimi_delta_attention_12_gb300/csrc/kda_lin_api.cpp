@@ -39,9 +39,9 @@ bool on_tensor_cores(int32_t d_k, int32_t d_v, kda_dtype dt, uint32_t flags, int
 // runs at once with one CTA an SM; the CUDA-core form with one CTA for each 32
 // columns of dz, of which an SM takes two, and a few rounds of them even out
 // ragged lengths (a ragged fp32 backward took 368 us with one round and a half).
-int32_t segment_tokens(int32_t N, int32_t total_T, int32_t H, int32_t dz, int tc_passes) {
-    return tc_passes > 0 ? kda::lin_segment_tokens(N, total_T, H, tc_passes, 1, sm_count())
-                         : kda::lin_segment_tokens(N, total_T, H, dz / 32, 8, sm_count());
+kda::LinCut cut_of(int32_t N, int32_t total_T, int32_t H, int32_t dz, int tc_passes) {
+    return tc_passes > 0 ? kda::lin_cut_tc(N, total_T, H, tc_passes, sm_count())
+                         : kda::lin_cut(N, total_T, H, dz / 32, 8, sm_count());
 }
 
 size_t seg_state_bytes(int32_t total_T, int32_t H, int32_t dx, int32_t dz, int32_t seg_len) {
@@ -58,10 +58,10 @@ size_t segment_room(int32_t N, int32_t total_T, int32_t H, int32_t d_k, int32_t 
                     int passes) {
     const int32_t dz = d_k < d_v ? d_k : d_v;
     const size_t a =
-        seg_state_bytes(total_T, H, d_k, d_v, segment_tokens(N, total_T, H, dz, 0));
+        seg_state_bytes(total_T, H, d_k, d_v, cut_of(N, total_T, H, dz, 0).seg_len);
     if (!on_tensor_cores(d_k, d_v, dt, 0, total_T)) return a;
     const size_t b = passes * seg_state_bytes(total_T, H, d_k, d_v,
-                                              segment_tokens(N, total_T, H, dz, passes));
+                                              cut_of(N, total_T, H, dz, passes).seg_len);
     return a > b ? a : b;
 }
 
@@ -135,7 +135,9 @@ int kda_lin_prefill(const void* q, const void* k, const void* v, const float* lo
     p.cu_seqlens = cu_seqlens;
     p.status = reinterpret_cast<int32_t*>(ws);
     p.N = N; p.total_T = total_T; p.H = H; p.dx = d_k; p.dz = d_v;
-    p.seg_len = segment_tokens(N, total_T, H, d_v, tc ? 1 : 0);
+    const kda::LinCut cut = cut_of(N, total_T, H, d_v, tc ? 1 : 0);
+    p.seg_len = cut.seg_len;
+    p.lead = cut.lead;
     p.seg_states = reinterpret_cast<float*>(ws + kHeader);
     p.out_scale = scale; p.kv_scale = 1.0f;
     if (initial_state && initial_state == final_state && total_T / p.seg_len > 0) {
@@ -260,17 +262,18 @@ int kda_lin_backward(const void* q, const void* k, const void* v, const float* l
     c.reverse = 1; c.out_scale = 1.0f; c.kv_scale = scale;
     float* states = reinterpret_cast<float*>(ws + kHeader);
     if (tc) {
-        const int32_t seg = segment_tokens(N, total_T, H, d_v, 3);
+        const kda::LinCut cut = cut_of(N, total_T, H, d_v, 3);
         for (int i = 0; i < 3; ++i) {
-            pass[i].seg_len = seg;
+            pass[i].seg_len = cut.seg_len;
+            pass[i].lead = cut.lead;
             pass[i].seg_states =
-                states + i * (seg_state_bytes(total_T, H, d_k, d_v, seg) / sizeof(float));
+                states + i * (seg_state_bytes(total_T, H, d_k, d_v, cut.seg_len) / sizeof(float));
         }
         return kda::launch_lin_pass_tc(pass, 3, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     }
     for (kda::LinPass& p : pass) {
         if (total_T == 0 && &p != &c) continue;   // only the state is handed on
-        p.seg_len = segment_tokens(N, total_T, H, p.dz, 0);
+        p.seg_len = cut_of(N, total_T, H, p.dz, 0).seg_len;
         p.seg_states = states;
         if (kda::launch_lin_pass(p, dt == KDA_F32 ? 0 : 1, s) != cudaSuccess) return KDA_ERR_CUDA;
     }

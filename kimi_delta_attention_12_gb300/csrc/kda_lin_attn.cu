@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) lin_scan_kernel(const __grid_con
     const int at = (blockIdx.x % per) * SCAN_THREADS + threadIdx.x;
     const lin::Segment sg = lin::first_segment(p.cu_seqlens, p.N, p.total_T, p.seg_len, p.reverse,
                                                n);
-    if (sg.count < 2) return;
+    if (sg.count < 2 || (p.lead > 0 && sg.count <= p.lead)) return;
     const float g = p.log_decay[h];
     const int64_t rows = lin::seg_rows(p.total_T, p.seg_len);
     const size_t state4 = (size_t)p.dx * p.dz / 4;
@@ -382,7 +382,8 @@ __global__ void __launch_bounds__(SCAN_THREADS) lin_scan_kernel(const __grid_con
         s = state_at(s0, d, c, p.dx, p.dz, p.state_in_turned);
     }
     float4* u = reinterpret_cast<float4*>(p.seg_states) + at;
-    const int last = (int)(rows - sg.u < sg.count - 1 ? rows - sg.u : sg.count - 1);
+    const int used = p.lead > 0 ? p.lead : sg.count - 1;
+    const int last = (int)(rows - sg.u < used ? rows - sg.u : used);
     for (int j = 0; j < last; j += 4) {
         float4 v[4];
 #pragma unroll
@@ -511,16 +512,38 @@ cudaError_t pass_dx(const LinPass& p, cudaStream_t stream) {
 
 }  // namespace
 
-int32_t lin_segment_tokens(int32_t N, int32_t total_T, int32_t H, int ctas_per_pair,
-                           int ctas_per_sm, int sms) {
+LinCut lin_cut(int32_t N, int32_t total_T, int32_t H, int ctas_per_pair, int ctas_per_sm, int sms) {
     constexpr int64_t grain = 128;
     if (sms <= 0) sms = 152;   // no device to ask: sizes for a whole GB300
     const int64_t pairs = (int64_t)N * H * ctas_per_pair;
     const int64_t cuts = (int64_t)sms * ctas_per_sm / pairs;
-    if (cuts < 2) return INT32_MAX / grain * grain;
+    if (cuts < 2) return {INT32_MAX / grain * grain, 0};
     const int64_t len = ((int64_t)total_T + N * cuts - 1) / (N * cuts);
     const int64_t seg = (len + grain - 1) / grain * grain;
-    return (int32_t)(seg < grain ? grain : seg);
+    return {(int32_t)(seg < grain ? grain : seg), 0};
+}
+
+LinCut lin_cut_tc(int32_t N, int32_t total_T, int32_t H, int passes, int sms) {
+    if (sms <= 0) sms = 152;
+    const LinCut whole = lin_cut(N, total_T, H, passes, 1, sms);
+    const int64_t pairs = (int64_t)N * H * passes, chunks = total_T / (128 * (int64_t)N);
+    if (whole.seg_len <= total_T || pairs >= sms) return whole;
+    const int64_t k = (pairs + sms - pairs - 1) / (sms - pairs), head = chunks / (k + 1);
+    // A cut saves the heads' time, but their states come first (a chunk of them takes
+    // about half of a chunk's time), and 152 busy SMs share the memory.  96 heads:
+    // 8K tokens 203 -> 209 us, 16K 393 -> 366, 64K 1,528 -> 1,291; 112 heads: 8K 207 ->
+    // 227, 32K 786 -> 748; the backward of 32 heads: 8K 205 -> 221, 16K 396 -> 393, 32K
+    // 779 -> 675.
+    if (k > 3 || chunks < 64 * k) return whole;
+    int64_t lead = 1, best = 0;
+    for (int64_t n = 1; n <= 8; ++n) {     // segments that share the SMs best; 3 chunks' start
+        const int64_t time = (pairs * n + sms - 1) / sms * ((head + n - 1) / n + 3);
+        if (best == 0 || time < best) {
+            best = time;
+            lead = n;
+        }
+    }
+    return {(int32_t)((head + lead - 1) / lead * 128), (int32_t)lead};
 }
 
 cudaError_t launch_lin_scan(const LinPass* passes, int n, cudaStream_t stream) {

@@ -327,7 +327,9 @@ struct Cta {
 };
 
 // The pass and the segment of this CTA (heads fastest, then the passes, then the
-// segments).  Whole sequences come longest first, so that none starts late.
+// segments).  Whole sequences come longest first, so that none starts late; of
+// sequences cut in two the tails, and then the heads.
+template <bool STATES>
 __device__ __forceinline__ const Args* start(const Jobs& jobs, Cta& c) {
     // (the earliest any CTA can report a wait is seconds away)
     if (jobs.first && blockIdx.x == 0 && threadIdx.x == 0) *jobs.a[0].p.status = 0;
@@ -344,9 +346,19 @@ __device__ __forceinline__ const Args* start(const Jobs& jobs, Cta& c) {
     c.h = blockIdx.x % H;
     c.rev = p.reverse != 0;
     int index = unit / jobs.n;
-    if (p.cu_seqlens && p.N <= lin::RANKED && p.total_T < p.seg_len)
+    if (p.lead > 0 && STATES) {
+        c.sg = lin::lead_segment(p.cu_seqlens, p.N, p.total_T, p.seg_len, p.reverse, p.lead,
+                                 index % p.N, index / p.N);
+        return c.sg.n >= 0 ? args : nullptr;
+    }
+    const bool tail = p.lead > 0 && index < p.N;
+    if (p.lead > 0 && !tail) index -= p.N;
+    if (p.cu_seqlens && p.N <= lin::RANKED && (p.lead > 0 || p.total_T < p.seg_len))
         index = lin::nth_longest(p.cu_seqlens, p.N, p.total_T, index);
-    c.sg = lin::find_segment(p.cu_seqlens, p.N, p.total_T, p.seg_len, p.reverse, index);
+    c.sg = p.lead > 0 ? lin::half_segment(p.cu_seqlens, p.N, p.total_T, p.seg_len, p.reverse,
+                                          p.lead, index, tail)
+                      : lin::find_segment(p.cu_seqlens, p.N, p.total_T, p.seg_len, p.reverse,
+                                          index);
     return c.sg.n >= 0 ? args : nullptr;
 }
 
@@ -805,7 +817,7 @@ __device__ __forceinline__ void states(const LinPass& p, const Cta& c, uint32_t 
 __global__ void __launch_bounds__(THREADS, 1)
 lin_pass_tc_kernel(const __grid_constant__ Jobs jobs) {
     Cta c;
-    const Args* job = start(jobs, c);
+    const Args* job = start<false>(jobs, c);
     if (!job) return;
     const Args& args = *job;
     const LinPass& p = args.p;
@@ -839,7 +851,7 @@ lin_pass_tc_kernel(const __grid_constant__ Jobs jobs) {
 __global__ void __launch_bounds__(STATE_THREADS, 1)
 lin_states_tc_kernel(const __grid_constant__ Jobs jobs) {
     Cta c;
-    const Args* job = start(jobs, c);
+    const Args* job = start<true>(jobs, c);
     if (!job) return;
     const Args& args = *job;
     const LinPass& p = args.p;
@@ -992,14 +1004,16 @@ cudaError_t launch_lin_pass_tc(const LinPass* passes, int n, cudaStream_t stream
     }
     const LinPass& p = passes[0];
     const int64_t most = (int64_t)p.total_T / p.seg_len;   // segments that are not a last one
-    const int64_t grid = (most + p.N) * p.H * n;
-    if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
+    const int64_t units = (int64_t)p.H * n;
+    const int64_t grid = (p.lead > 0 ? 2 * (int64_t)p.N : most + p.N) * units;
+    const int64_t state_grid = p.lead > 0 ? (int64_t)p.N * p.lead * units : grid;
+    if (grid > INT_MAX || state_grid > INT_MAX) return cudaErrorInvalidConfiguration;
     cudaError_t err;
     if (most > 0) {
         err = cudaFuncSetAttribute(lin_states_tc_kernel,
                                    cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
         if (err != cudaSuccess) return err;
-        lin_states_tc_kernel<<<(unsigned)grid, STATE_THREADS, SMEM, stream>>>(jobs);
+        lin_states_tc_kernel<<<(unsigned)state_grid, STATE_THREADS, SMEM, stream>>>(jobs);
         jobs.first = 0;
         err = launch_lin_scan(passes, n, stream);
         if (err != cudaSuccess) return err;

@@ -271,6 +271,27 @@ def test_malformed_device_seqlens_stay_inside(dtype, d):
         assert bool((wbuf[:256] == 9).all()) and bool((wbuf[256 + need:] == 9).all())
 
 
+def test_malformed_device_seqlens_of_sequences_cut_in_two():
+    T, H, pad = 33000, 40, 64
+    x = R.make([T], H, 128, 128, BF, seed=3)
+    v = R.dev(x)
+    for cu in ([0, T, 0], [-5, T + 3, 7], [T, 1, 10 ** 9]):
+        N = len(cu) - 1
+        buf = torch.full((T + 2 * pad, H, 128), 3.0, dtype=BF, device="cuda")
+        sbuf = torch.full((N + 2, H, 128, 128), 3.0, device="cuda")
+        need = kda.lin_prefill_workspace_bytes(N, T, H, 128, 128, BF)
+        wbuf = torch.full((need + 512,), 9, dtype=torch.uint8, device="cuda")
+        kda.kda_lin_prefill(v["q"], v["k"], v["v"], v["log_decay"], None,
+                            torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                            o=buf[pad:pad + T], final_state=sbuf[1:N + 1],
+                            workspace=wbuf[256:256 + need])
+        torch.cuda.synchronize()
+        assert int(wbuf[256:260].view(torch.int32)) == 0
+        assert bool((buf[:pad] == 3.0).all()) and bool((buf[pad + T:] == 3.0).all())
+        assert bool((sbuf[[0, N + 1]] == 3.0).all())
+        assert bool((wbuf[:256] == 9).all()) and bool((wbuf[256 + need:] == 9).all())
+
+
 def test_offsets_past_32_bits():
     """2.2e9 elements per tensor: the last tokens, whose decay forgets what came before."""
     T, H, d = 136000, 128, 128
@@ -341,6 +362,54 @@ def test_many_ragged_sequences_in_any_order():
         o, S = kda.kda_lin_prefill(v["q"], v["k"], v["v"], v["log_decay"], S0, cu.cuda(), cu)
         assert torch.equal(S[40:], S0[40:])                # empty ones hand theirs on
         check_forward(x, o, S[:40], 1.0, 128, BF, True)
+
+
+def heads(x, keep):
+    """The same sequences with some of the heads: what heads do is independent."""
+    axis = {"q": 1, "k": 1, "v": 1, "dO": 1, "log_decay": 0, "S0": 1, "dS": 1}
+    return {n: t.index_select(axis[n], torch.tensor(keep)) if n in axis and t is not None else t
+            for n, t in x.items()}
+
+
+# Pairs of sequences and heads that fill more than half of the SMs but not all:
+# the sequences are cut into a head of a few segments and a tail.
+CUT_IN_TWO = [([16509], 96, True), ([31000, 1850], 39, True), ([12000, 24000, 0, 30500], 20, False),
+              ([16400] * 2, 40, False)]
+
+
+@pytest.mark.parametrize("lens,H,state", CUT_IN_TWO, ids=["1x96", "2x39", "4x20", "2x40"])
+def test_prefill_of_sequences_cut_in_two(lens, H, state):
+    x = R.make(lens, H, 128, 128, BF, seed=H, state=state, g=[-0.3 * h / H for h in range(H)])
+    d = R.dev(x)
+    cu = (None, None) if len(set(lens)) == 1 and len(lens) > 1 else (d["cu"], x["cu"])
+    S0 = None if x["S0"] is None else d["S0"].clone()
+    shape = (len(lens), -1, H, 128) if cu[0] is None else (-1, H, 128)
+    o, S = kda.kda_lin_prefill(d["q"].reshape(shape), d["k"].reshape(shape),
+                               d["v"].reshape(shape), d["log_decay"], S0, *cu, scale=0.75,
+                               final_state=S0)      # in place, where there is one
+    keep = [0, H // 2, H - 1]
+    o = o.reshape(-1, H, 128)
+    check_forward(heads(x, keep), o[:, keep], S[:, keep], 0.75, 128, BF, True)
+
+
+@pytest.mark.parametrize("lens,H", [([16509], 26), ([31000, 1850], 13)], ids=["1x26", "2x13"])
+def test_backward_of_sequences_cut_in_two(lens, H):
+    x = R.make(lens, H, 128, 128, BF, seed=H, state=True, g=[-0.3 * h / H for h in range(H)])
+    d = R.dev(x)
+    g = kda.kda_lin_backward(d["q"], d["k"], d["v"], d["log_decay"], d["dO"], d["S0"], d["cu"],
+                             x["cu"], d["dS"], scale=0.75)
+    keep = [0, H - 1]
+    x = heads(x, keep)
+    a = {n: R.f64(t) for n, t in x.items() if isinstance(t, torch.Tensor)}
+    want = R.lin_backward(a["q"], a["k"], a["v"], a["log_decay"], lens, a["dO"], a["S0"], a["dS"],
+                          0.75)
+    mag = R.lin_backward(*R.absolute(a["q"], a["k"], a["v"]), a["log_decay"], lens,
+                         np.abs(a["dO"]), *R.absolute(a["S0"], a["dS"]), 0.75)
+    terms = R.fp32_terms(lens, 128)
+    for n in ("dq", "dk", "dv"):
+        R.check(n, g[n][:, keep], want[n], mag[n], terms, True, 1)
+        assert R.rel_fro(g[n][:, keep], want[n]) <= R.U16
+    R.check("dS0", g["dS0"][:, keep], want["dS0"], mag["dS0"], terms)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.75, 2.5])

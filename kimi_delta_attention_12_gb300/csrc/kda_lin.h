@@ -60,9 +60,10 @@ LinCut lin_cut(int32_t N, int32_t total_T, int32_t H, int ctas_per_pair, int cta
 // first, from the heads' segments over all SMs.
 LinCut lin_cut_tc(int32_t N, int32_t total_T, int32_t H, int passes, int sms);
 
-// The pass on the CUDA cores, fp32 arithmetic: dx, dz in {32, 64, 128}, dtype
-// 0 = fp32, 1 = bf16.
-cudaError_t launch_lin_pass(const LinPass& p, int dtype, cudaStream_t stream);
+// Up to three passes on the CUDA cores, fp32 arithmetic: dx, dz in {32, 64, 128},
+// dtype 0 = fp32, 1 = bf16.  Same sequences, heads and dx dz; sizes of segments and
+// their states each their own.
+cudaError_t launch_lin_pass(const LinPass* passes, int n, int dtype, cudaStream_t stream);
 // The pass on the tensor cores: bf16, dx = dz = 128, total_T > 0.  A wait that
 // ran out leaves a nonzero status word.
 // Up to three passes of the same sizes and sequences run as one.

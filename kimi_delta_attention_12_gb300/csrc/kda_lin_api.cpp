@@ -38,10 +38,12 @@ bool on_tensor_cores(int32_t d_k, int32_t d_v, kda_dtype dt, uint32_t flags, int
 // The tensor-core form works on a (sequence, head) pair of each of the `passes` it
 // runs at once with one CTA an SM; the CUDA-core form with one CTA for each 32
 // columns of dz, of which an SM takes two, and a few rounds of them even out
-// ragged lengths (a ragged fp32 backward took 368 us with one round and a half).
-kda::LinCut cut_of(int32_t N, int32_t total_T, int32_t H, int32_t dz, int tc_passes) {
-    return tc_passes > 0 ? kda::lin_cut_tc(N, total_T, H, tc_passes, sm_count())
-                         : kda::lin_cut(N, total_T, H, dz / 32, 8, sm_count());
+// ragged lengths (with one round and a half a ragged fp32 backward took 368 us for
+// 329).  The three passes of a backward make three rounds of segments three times
+// as long: 253 us, 259 with eight.
+kda::LinCut cut_of(int32_t N, int32_t total_T, int32_t H, int32_t dz, int passes, bool tc) {
+    return tc ? kda::lin_cut_tc(N, total_T, H, passes, sm_count())
+              : kda::lin_cut(N, total_T, H, dz / 32, passes > 1 ? 3 : 8, sm_count());
 }
 
 size_t seg_state_bytes(int32_t total_T, int32_t H, int32_t dx, int32_t dz, int32_t seg_len) {
@@ -58,10 +60,10 @@ size_t segment_room(int32_t N, int32_t total_T, int32_t H, int32_t d_k, int32_t 
                     int passes) {
     const int32_t dz = d_k < d_v ? d_k : d_v;
     const size_t a =
-        seg_state_bytes(total_T, H, d_k, d_v, cut_of(N, total_T, H, dz, 0).seg_len);
+        passes * seg_state_bytes(total_T, H, d_k, d_v, cut_of(N, total_T, H, dz, passes, false).seg_len);
     if (!on_tensor_cores(d_k, d_v, dt, 0, total_T)) return a;
     const size_t b = passes * seg_state_bytes(total_T, H, d_k, d_v,
-                                              cut_of(N, total_T, H, dz, passes).seg_len);
+                                              cut_of(N, total_T, H, dz, passes, true).seg_len);
     return a > b ? a : b;
 }
 
@@ -135,7 +137,7 @@ int kda_lin_prefill(const void* q, const void* k, const void* v, const float* lo
     p.cu_seqlens = cu_seqlens;
     p.status = reinterpret_cast<int32_t*>(ws);
     p.N = N; p.total_T = total_T; p.H = H; p.dx = d_k; p.dz = d_v;
-    const kda::LinCut cut = cut_of(N, total_T, H, d_v, tc ? 1 : 0);
+    const kda::LinCut cut = cut_of(N, total_T, H, d_v, 1, tc);
     p.seg_len = cut.seg_len;
     p.lead = cut.lead;
     p.seg_states = reinterpret_cast<float*>(ws + kHeader);
@@ -151,7 +153,7 @@ int kda_lin_prefill(const void* q, const void* k, const void* v, const float* lo
         p.state_in = copy;
     }
     const cudaError_t err = tc ? kda::launch_lin_pass_tc(&p, 1, s)
-                               : kda::launch_lin_pass(p, dt == KDA_F32 ? 0 : 1, s);
+                               : kda::launch_lin_pass(&p, 1, dt == KDA_F32 ? 0 : 1, s);
     return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -188,8 +190,7 @@ int kda_lin_decode_step(const void* q, const void* k, const void* v, const float
                : KDA_ERR_CUDA;
 }
 
-// On the tensor cores the three passes run at once, each with states of its own;
-// on the CUDA cores one after another in the same room.
+// The three passes run at once, each with segments' states of its own.
 size_t kda_lin_backward_workspace_bytes(int32_t N, int32_t total_T, int32_t H, int32_t d_k,
                                         int32_t d_v, kda_dtype dt) {
     if (bad_sizes(N, total_T, H) || !supported_dim(d_k) || !supported_dim(d_v) ||
@@ -262,7 +263,7 @@ int kda_lin_backward(const void* q, const void* k, const void* v, const float* l
     c.reverse = 1; c.out_scale = 1.0f; c.kv_scale = scale;
     float* states = reinterpret_cast<float*>(ws + kHeader);
     if (tc) {
-        const kda::LinCut cut = cut_of(N, total_T, H, d_v, 3);
+        const kda::LinCut cut = cut_of(N, total_T, H, d_v, 3, true);
         for (int i = 0; i < 3; ++i) {
             pass[i].seg_len = cut.seg_len;
             pass[i].lead = cut.lead;
@@ -272,12 +273,14 @@ int kda_lin_backward(const void* q, const void* k, const void* v, const float* l
         return kda::launch_lin_pass_tc(pass, 3, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     }
     for (kda::LinPass& p : pass) {
-        if (total_T == 0 && &p != &c) continue;   // only the state is handed on
-        p.seg_len = cut_of(N, total_T, H, p.dz, 0).seg_len;
+        p.seg_len = cut_of(N, total_T, H, p.dz, 3, false).seg_len;
         p.seg_states = states;
-        if (kda::launch_lin_pass(p, dt == KDA_F32 ? 0 : 1, s) != cudaSuccess) return KDA_ERR_CUDA;
+        states += seg_state_bytes(total_T, H, d_k, d_v, p.seg_len) / sizeof(float);
     }
-    return KDA_OK;
+    // (without tokens only the state is handed on)
+    const cudaError_t err = total_T > 0 ? kda::launch_lin_pass(pass, 3, dt == KDA_F32 ? 0 : 1, s)
+                                        : kda::launch_lin_pass(&c, 1, dt == KDA_F32 ? 0 : 1, s);
+    return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 }  // extern "C"

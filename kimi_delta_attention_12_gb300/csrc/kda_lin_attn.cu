@@ -15,6 +15,7 @@
 
 #include <cuda_bf16.h>
 #include <limits.h>
+#include <string.h>
 
 #include "kda_lin.cuh"
 #include "kda_packed.cuh"
@@ -113,7 +114,7 @@ __device__ __forceinline__ void mul4(float4 (&acc)[4], const float4 (&a)[4], con
 // multiply-adds for every two 16-byte reads of shared memory), and the quarters
 // added in order; the state's product has 4 columns and dx / 32 rows a thread.
 template <typename T, int DX, bool STATES>
-__global__ void __launch_bounds__(THREADS) lin_pass_kernel(LinPass p) {
+__device__ __forceinline__ void pass(const LinPass& p, uint32_t block) {
     constexpr int LD = DX + 4, ROWS = DX / 32;
     extern __shared__ float4 smem4[];
     float* stages = reinterpret_cast<float*>(smem4);
@@ -121,10 +122,9 @@ __global__ void __launch_bounds__(THREADS) lin_pass_kernel(LinPass p) {
     float* S = P + 4 * C * PLD;       // [DX][SLICE]
     float* lam = S + DX * SLICE;      // a^0 .. a^C
 
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;   // no wait here can run out
     const int tid = threadIdx.x, dz = p.dz, slices = dz / SLICE;
-    const int col0 = (blockIdx.x % slices) * SLICE;
-    const int64_t rest = blockIdx.x / slices;
+    const int col0 = (int)(block % slices) * SLICE;
+    const int64_t rest = block / slices;
     const int h = (int)(rest % p.H);
     const lin::Segment sg = lin::find_segment(p.cu_seqlens, p.N, p.total_T, p.seg_len, p.reverse,
                                               rest / p.H);
@@ -325,33 +325,73 @@ __global__ void __launch_bounds__(THREADS) lin_pass_kernel(LinPass p) {
     }
 }
 
-// Beyond 48 KB a kernel has to be allowed its shared memory.
-cudaError_t allow(const void* kernel, int smem) {
-    return smem <= 48 * 1024 ? cudaSuccess
-                             : cudaFuncSetAttribute(
-                                   kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// Up to three passes of one call, one after another in the grid: the blocks of the
+// next fill the SMs that the last round of the one before leaves idle.
+struct Passes {
+    LinPass p[3];
+    uint32_t end[3];   // blocks of the passes up to this one
+};
+
+template <typename T, bool STATES>
+__global__ void __launch_bounds__(THREADS, 2)
+lin_passes_kernel(const __grid_constant__ Passes jobs) {
+    const int k = blockIdx.x < jobs.end[0] ? 0 : blockIdx.x < jobs.end[1] ? 1 : 2;
+    const LinPass& p = jobs.p[k];
+    const uint32_t block = blockIdx.x - (k > 0 ? jobs.end[k - 1] : 0);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;   // no wait here can run out
+    if (p.dx == 32) pass<T, 32, STATES>(p, block);
+    else if (p.dx == 64) pass<T, 64, STATES>(p, block);
+    else pass<T, 128, STATES>(p, block);
 }
 
-template <typename T, int DX>
-cudaError_t launch_pass(const LinPass& p, cudaStream_t stream) {
-    constexpr int smem = (int)pass_smem_bytes<T, DX>();
-    const int64_t most = (int64_t)p.total_T / p.seg_len;   // segments that are not a last one
-    const int64_t grid = (most + p.N) * p.H * (p.dz / SLICE);
-    if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-    cudaError_t err;
-    if (most > 0) {
-        auto* k1 = lin_pass_kernel<T, DX, true>;
-        err = allow(reinterpret_cast<const void*>(k1), smem);
-        if (err != cudaSuccess) return err;
-        k1<<<(unsigned)grid, THREADS, smem, stream>>>(p);
-        err = launch_lin_scan(&p, 1, stream);
-        if (err != cudaSuccess) return err;
+template <typename T>
+size_t pass_smem(int dx) {
+    return dx == 32   ? pass_smem_bytes<T, 32>()
+           : dx == 64 ? pass_smem_bytes<T, 64>()
+                      : pass_smem_bytes<T, 128>();
+}
+
+template <typename T, bool STATES>
+cudaError_t launch_passes(const LinPass* passes, int n, cudaStream_t stream) {
+    Passes jobs;
+    memset(&jobs, 0, sizeof(jobs));
+    int64_t grid = 0;
+    size_t smem = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (i < n) {
+            const LinPass& p = jobs.p[i] = passes[i];
+            const int64_t most = (int64_t)p.total_T / p.seg_len;   // segments that are not a last one
+            if (!STATES || most > 0) grid += (most + p.N) * p.H * (p.dz / SLICE);
+            const size_t need = pass_smem<T>(p.dx);
+            if (need > smem) smem = need;
+        }
+        if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
+        jobs.end[i] = (uint32_t)grid;
     }
-    auto* k2 = lin_pass_kernel<T, DX, false>;
-    err = allow(reinterpret_cast<const void*>(k2), smem);
+    if (grid == 0) return cudaSuccess;
+    auto* kernel = lin_passes_kernel<T, STATES>;
+    const cudaError_t err =
+        smem <= 48 * 1024
+            ? cudaSuccess
+            : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
-    k2<<<(unsigned)grid, THREADS, smem, stream>>>(p);
+    kernel<<<(unsigned)grid, THREADS, smem, stream>>>(jobs);
     return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t run_passes(const LinPass* passes, int n, cudaStream_t stream) {
+    bool cut = false;
+    for (int i = 0; i < n; ++i) {
+        const int32_t dx = passes[i].dx;
+        if (dx != 32 && dx != 64 && dx != 128) return cudaErrorInvalidValue;
+        cut = cut || passes[i].total_T >= passes[i].seg_len;
+    }
+    cudaError_t err = cudaSuccess;
+    if (cut) err = launch_passes<T, true>(passes, n, stream);
+    if (cut && err == cudaSuccess) err = launch_lin_scan(passes, n, stream);
+    if (err == cudaSuccess) err = launch_passes<T, false>(passes, n, stream);
+    return err;
 }
 
 // ------------------------------------------------------ states between segments
@@ -500,16 +540,6 @@ cudaError_t decode_dk(const LinDecode& p, int d_k, int d_v, cudaStream_t stream)
     }
 }
 
-template <typename T>
-cudaError_t pass_dx(const LinPass& p, cudaStream_t stream) {
-    switch (p.dx) {
-        case 32: return launch_pass<T, 32>(p, stream);
-        case 64: return launch_pass<T, 64>(p, stream);
-        case 128: return launch_pass<T, 128>(p, stream);
-        default: return cudaErrorInvalidValue;
-    }
-}
-
 }  // namespace
 
 LinCut lin_cut(int32_t N, int32_t total_T, int32_t H, int ctas_per_pair, int ctas_per_sm, int sms) {
@@ -556,8 +586,9 @@ cudaError_t launch_lin_scan(const LinPass* passes, int n, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_lin_pass(const LinPass& p, int dtype, cudaStream_t stream) {
-    return dtype == 0 ? pass_dx<float>(p, stream) : pass_dx<__nv_bfloat16>(p, stream);
+cudaError_t launch_lin_pass(const LinPass* passes, int n, int dtype, cudaStream_t stream) {
+    return dtype == 0 ? run_passes<float>(passes, n, stream)
+                      : run_passes<__nv_bfloat16>(passes, n, stream);
 }
 
 cudaError_t launch_lin_decode(const LinDecode& p, int d_k, int d_v, int dtype,

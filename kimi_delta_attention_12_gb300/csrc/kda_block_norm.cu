@@ -157,11 +157,15 @@ __device__ __forceinline__ void row_sum(float (&s)[M], float* buf, int warps, in
         for (int i = 0; i < M; ++i) b[w * 3 + i] = s[i];
     }
     row_wait();
-    // every warp adds the (up to 16) warps' sums itself, in each half of its lanes
-    const int lane = threadIdx.x & 15;
+    // every warp adds the (up to 16) warps' sums itself, in each half or quarter of its lanes
+    const int lane = threadIdx.x & (warps <= 8 ? 7 : 15);
 #pragma unroll
     for (int i = 0; i < M; ++i) s[i] = lane < warps ? b[lane * 3 + i] : 0.0f;
-    lane_sum(s, 16);
+    if (warps <= 8) {
+        lane_sum(s, 8);
+    } else {
+        lane_sum(s, 16);
+    }
 }
 
 // n act(gate) res_scale of one vector; y replaced by it.
@@ -346,12 +350,14 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_kernel(BlockNorm p) {
 // wait is enough.  The registers that rows in flight would take go to the
 // sums.  Rows too wide for that (stages = 0) are read into registers.
 // FULL: a row's threads cover the columns exactly, so that nothing needs a guard.
-// KEEP: the three weights are in shared memory too, for the block's rows.  Beside
+// KEEP: every part is there (the norm over the row, both upstream gradients, dx), and
+// the three weights are in shared memory too, for the block's rows.  Beside
 // two blocks' rings of wide rows L1 is too small for them, and each row would
-// wait for L2: 4,096 rows of 4,096 in bf16 took 69 us without it and take 59
-// (4.6 TB/s, 68 % of a plain copy's).  What is left is the chain of a row: two sums
-// over it, each a barrier, with 16 warps on an SM (128 registers a thread); the
-// instructions alone would take 28 us.  64 registers and twice the warps: 79 us.
+// wait for L2: 4,096 rows of 4,096 in bf16 took 69 us without it, 59 with it, and 55
+// (4.9 TB/s, 72 % of a plain copy's) without the branches that absent parts need.
+// What is left is the chain of a row: two sums over it, each a barrier, with 16 warps
+// on an SM (128 registers a thread); the instructions alone would take 20 us.  64
+// registers and twice the warps spill, and take 74.
 enum { Y = 0, GATE = 1, DXO = 2, X = 3, DH = 4, TENSORS = 5 };
 
 __device__ __forceinline__ void copy16(void* smem, const void* src) {
@@ -371,20 +377,25 @@ __device__ __forceinline__ void copies_done(int behind) {   // all but the last 
 }
 
 enum { NO_GATE = 0, SIGMOID = 1, SILU = 2 };
+constexpr int KEEP_THREADS = 256, KEEP_ROWS = 2;   // of a block that keeps the weights
 
 template <typename T, int VPT, int ACT, bool RING, bool FULL, bool KEEP = false>
 __global__ void __launch_bounds__(MAX_THREADS)
 block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
     __shared__ float buf[2 * MAX_ROWS * 32 * 3];
-    const int warps = blockDim.x >> 5;
-    const int vec0 = blockIdx.y * tile / V + threadIdx.x;
-    const int vecs = min(p.D, ((int)blockIdx.y + 1) * tile) / V;
-    const bool whole = p.group == p.D;
+    // what the shape of a block that keeps the weights is
+    const int width = KEEP ? KEEP_THREADS : (int)blockDim.x, rows = KEEP ? KEEP_ROWS : (int)blockDim.y;
+    const int D = KEEP ? KEEP_THREADS * VPT * V : p.D, cols = KEEP ? D : tile;
+    const int depth = KEEP ? 2 : stages, warps = width >> 5;
+    const int vec0 = KEEP ? (int)threadIdx.x : (int)(blockIdx.y * cols / V + threadIdx.x);
+    const int vecs = KEEP ? D / V : min(D, ((int)blockIdx.y + 1) * cols) / V;
+    const bool whole = KEEP || p.group == D, pre = KEEP || p.w_pre, pass_on = KEEP || p.dx;
     const int lanes = whole ? 32 : p.group / V;
     const T* src[TENSORS] = {static_cast<const T*>(p.y), static_cast<const T*>(p.gate),
                              static_cast<const T*>(p.dx_out),
-                             static_cast<const T*>(p.w_pre ? p.x : nullptr),
-                             static_cast<const T*>(p.w_pre ? p.dh : nullptr)};
+                             static_cast<const T*>(pre ? p.x : nullptr),
+                             static_cast<const T*>(pre ? p.dh : nullptr)};
+    auto has = [&](int t) { return t == GATE ? ACT != NO_GATE : KEEP || src[t]; };
     extern __shared__ float4 dyn4[];
     uint64_t a_post[VPT][V / 2], a_res[VPT][V / 2], a_pre[VPT][V / 2];   // pairs
 #pragma unroll
@@ -392,22 +403,22 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
 #pragma unroll
         for (int e = 0; e < V / 2; ++e) a_post[i][e] = a_res[i][e] = a_pre[i][e] = 0;
 
-    const int64_t step = (int64_t)gridDim.x * blockDim.y;
-    int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const int all = blockDim.x * blockDim.y, flat = threadIdx.y * blockDim.x + threadIdx.x;
-    Raw<T>* ring = reinterpret_cast<Raw<T>*>(dyn4);   // [stages][TENSORS][VPT][all]
-    float* kept = reinterpret_cast<float*>(ring + stages * TENSORS * VPT * all);   // [3][tile]
+    const int64_t step = (int64_t)gridDim.x * rows;
+    int64_t row = (int64_t)blockIdx.x * rows + threadIdx.y;
+    const int all = width * rows, flat = threadIdx.y * width + threadIdx.x;
+    Raw<T>* ring = reinterpret_cast<Raw<T>*>(dyn4);   // [depth][TENSORS][VPT][all]
+    float* kept = reinterpret_cast<float*>(ring + depth * TENSORS * VPT * all);   // [3][tile]
     if (KEEP) {
-        for (int c = flat; c < tile; c += all) {
-            if (c < p.group) kept[c] = p.w_post[c];
-            if (p.res_scale) kept[tile + c] = p.res_scale[c];
-            if (p.w_pre) kept[2 * tile + c] = p.w_pre[c];
+        for (int c = flat; c < cols; c += all) {
+            kept[c] = p.w_post[c];
+            kept[cols + c] = p.res_scale ? p.res_scale[c] : 1.0f;
+            kept[2 * cols + c] = p.w_pre[c];
         }
         __syncthreads();
     }
     const float* w_post = KEEP ? kept : p.w_post;
-    const float* res_scale = KEEP ? kept + tile : p.res_scale;
-    const float* w_pre = KEEP ? kept + 2 * tile : p.w_pre;
+    const float* res_scale = KEEP ? kept + cols : p.res_scale;
+    const float* w_pre = KEEP ? kept + 2 * cols : p.w_pre;
     auto slot = [&](int stage, int k, int i) {
         return ring + ((stage * TENSORS + k) * VPT + i) * all + flat;
     };
@@ -415,12 +426,12 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
         if (r < p.rows) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int vec = vec0 + i * blockDim.x;
+                const int vec = vec0 + i * width;
                 if (!FULL && vec >= vecs) continue;
-                const size_t at = (size_t)r * p.D + (size_t)vec * V;
+                const size_t at = (size_t)r * D + (size_t)vec * V;
 #pragma unroll
                 for (int k = 0; k < TENSORS; ++k) {
-                    if (!src[k]) continue;
+                    if (!has(k)) continue;
 #pragma unroll
                     for (int q = 0; q < (int)sizeof(Raw<T>) / 16; ++q)
                         copy16(reinterpret_cast<uint4*>(slot(stage, k, i)) + q,
@@ -431,30 +442,30 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
         asm volatile("cp.async.commit_group;" ::: "memory");   // a group a row, empty or not
     };
     if (RING) {
-        for (int k = 0; k + 1 < stages; ++k) copy_row(row + k * step, k);
+        for (int k = 0; k + 1 < depth; ++k) copy_row(row + k * step, k);
     }
     int stage = 0;
-    const float inv_row = 1.0f / (float)p.D, inv_group = 1.0f / (float)p.group;
+    const float inv_row = 1.0f / (float)D, inv_group = 1.0f / (float)p.group;
     for (; row < p.rows; row += step) {
         Raw<T> held[RING ? 1 : TENSORS][RING ? 1 : VPT];
         if (RING) {
             // the stage that the row before has left takes the next row to come
-            const int free = stage == 0 ? stages - 1 : stage - 1;
-            copy_row(row + (stages - 1) * step, free);
-            copies_done(stages - 1);
+            const int free = stage == 0 ? depth - 1 : stage - 1;
+            copy_row(row + (depth - 1) * step, free);
+            copies_done(depth - 1);
         } else {
 #pragma unroll
             for (int k = 0; k < (RING ? 0 : TENSORS); ++k)
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) {
-                    const int vec = vec0 + i * blockDim.x;
+                    const int vec = vec0 + i * width;
                     clear(held[k][i]);
-                    if (src[k] && vec < vecs)
-                        fetch(src[k] + (size_t)row * p.D + (size_t)vec * V, held[k][i]);
+                    if (has(k) && vec < vecs)
+                        fetch(src[k] + (size_t)row * D + (size_t)vec * V, held[k][i]);
                 }
         }
         auto get = [&](int k, int i, uint64_t (&v)[V / 2]) {
-            const bool in = FULL || vec0 + i * (int)blockDim.x < vecs;
+            const bool in = FULL || vec0 + i * width < vecs;
             if (RING) {
                 Raw<T> r;
                 if (!FULL) clear(r);
@@ -468,9 +479,9 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
         float rr[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int vec = vec0 + i * blockDim.x;
+            const int vec = vec0 + i * width;
             uint64_t a[V / 2], q0 = 0, q1 = 0, q2 = 0;
-            if (p.w_pre && (FULL || vec < vecs)) {
+            if (pre && (FULL || vec < vecs)) {
                 uint64_t w[V / 2], h[V / 2];
                 get(X, i, a);
                 get(DH, i, h);
@@ -494,7 +505,7 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
                 rr[i] = rsqrtf(yy[0] * inv_group + p.eps);
             }
         }
-        const bool sums = whole || p.w_pre;
+        const bool sums = whole || pre;
         if (sums) row_sum(s, buf, warps, 0);
         if (whole) {
 #pragma unroll
@@ -509,17 +520,18 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
         float cc[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int vec = vec0 + i * blockDim.x;
+            const int vec = vec0 + i * width;
             const bool in = FULL || vec < vecs;
-            const size_t at = (size_t)row * p.D + (size_t)vec * V;
+            const size_t at = (size_t)row * D + (size_t)vec * V;
             uint64_t w[V / 2], part = 0;
-            if (src[DXO]) {
+            if (KEEP) asm volatile("" ::: "memory");   // (loads ahead of their turn would spill)
+            if (has(DXO)) {
                 get(DXO, i, tot[i]);
             } else {
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e) tot[i][e] = 0;
             }
-            if (in && p.w_pre) {
+            if (in && pre) {
                 uint64_t a[V / 2], h[V / 2];
                 get(X, i, a);
                 get(DH, i, h);
@@ -531,13 +543,13 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
                     tot[i][e] = fma2(a[e], cx2, fma2(h[e], w[e], tot[i][e]));
                 }
             }
-            if (in && p.dx) store2(static_cast<T*>(p.dx) + at, tot[i]);
+            if (in && pass_on) store2(static_cast<T*>(p.dx) + at, tot[i]);
             if (in) {
                 uint64_t rs[V / 2], a[V / 2], g[V / 2];
                 const uint64_t one = two(1.f, 1.f), r2 = two(rr[i], rr[i]);
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e) rs[e] = one;
-                if (p.res_scale) load2(res_scale + vec * V, rs);
+                if (KEEP || p.res_scale) load2(res_scale + vec * V, rs);
                 load2(w_post + (whole ? vec : vec & (lanes - 1)) * V, w);
                 get(Y, i, a);
                 if (ACT != NO_GATE) get(GATE, i, g);
@@ -581,7 +593,7 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int vec = vec0 + i * blockDim.x;
+            const int vec = vec0 + i * width;
             if (!FULL && vec >= vecs) continue;
             uint64_t a[V / 2];
             get(Y, i, a);
@@ -589,9 +601,9 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
             const uint64_t c2 = two(c, c), r2 = two(rr[i], rr[i]);
 #pragma unroll
             for (int e = 0; e < V / 2; ++e) tot[i][e] = fma2(a[e], c2, mul2(r2, tot[i][e]));
-            store2(static_cast<T*>(p.dy) + (size_t)row * p.D + (size_t)vec * V, tot[i]);
+            store2(static_cast<T*>(p.dy) + (size_t)row * D + (size_t)vec * V, tot[i]);
         }
-        if (RING && ++stage == stages) stage = 0;
+        if (RING && ++stage == depth) stage = 0;
     }
     if (RING) copies_done(0);
     __syncthreads();   // the ring's room takes the sums
@@ -600,7 +612,7 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
     // The part of dw_post holds one value per channel of a group: where a group
     // is a head, its heads are added here, in order.
     float* dyn = reinterpret_cast<float*>(dyn4);   // [tile]
-    const int col0 = blockIdx.y * tile, width = vecs * V - col0;
+    const int col0 = blockIdx.y * tile, count = vecs * V - col0;
     float* mine = p.partial + (size_t)blockIdx.x * 3 * p.D;
 #pragma unroll
     for (int which = 0; which < 3; ++which) {
@@ -610,7 +622,7 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
             if (threadIdx.y == k) {
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) {
-                    const int vec = vec0 + i * blockDim.x;
+                    const int vec = vec0 + i * width;
                     if (vec >= vecs) continue;
 #pragma unroll
                     for (int e = 0; e < V; e += 2) {
@@ -630,11 +642,11 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
         if (which == 0 && !whole) {
             for (int c = flat; c < p.group; c += all) {
                 float v = dyn[c];
-                for (int at = c + p.group; at < width; at += p.group) v += dyn[at];
+                for (int at = c + p.group; at < count; at += p.group) v += dyn[at];
                 mine[blockIdx.y * p.group + c] = v;
             }
         } else {
-            for (int c = flat; c < width; c += all) mine[which * p.D + col0 + c] = dyn[c];
+            for (int c = flat; c < count; c += all) mine[which * p.D + col0 + c] = dyn[c];
         }
         __syncthreads();
     }
@@ -715,7 +727,7 @@ struct BackwardShape {
     size_t smem;
 };
 
-BackwardShape backward_shape(int32_t D, bool coupled, int bytes) {
+BackwardShape backward_shape(int32_t D, bool coupled, bool all, int bytes) {
     BackwardShape b;
     b.s = shape_of(D, coupled, BACKWARD_THREADS);
     Shape& s = b.s;
@@ -723,11 +735,11 @@ BackwardShape backward_shape(int32_t D, bool coupled, int bytes) {
     const size_t sums = (size_t)s.tile * sizeof(float);
     b.stages = 3 * row <= RING_HALF ? 3 : 2 * row <= RING_ALL ? 2 : 0;
     b.full = s.tiles * s.tile == D && s.tile == (int)s.block.x * s.vpt * V;
-    b.keep = b.full && s.tiles == 1 && s.vpt == 2 && s.block.x == 256 && b.stages == 2 &&
+    b.keep = all && bytes == 2 && b.full && s.tiles == 1 && s.vpt == 2 && s.block.x == KEEP_THREADS && b.stages == 2 &&
              4 * row + 3 * sums <= RING_ALL;
     b.smem = b.stages * row > sums ? b.stages * row : sums;
     if (b.keep) {
-        s.block.y = 2;
+        s.block.y = KEEP_ROWS;
         b.smem = 4 * row + 3 * sums;
     }
     return b;
@@ -766,7 +778,8 @@ int parts_of(const Shape& s, int64_t rows) {
 
 template <typename T>
 cudaError_t backward(const BlockNorm& p, cudaStream_t stream) {
-    const BackwardShape b = backward_shape(p.D, coupled(p), sizeof(T));
+    const BackwardShape b = backward_shape(
+        p.D, coupled(p), p.group == p.D && p.w_pre && p.dx_out && p.dx, sizeof(T));
     const Shape& s = b.s;
     const int parts = b.keep ? parts_of(s, p.rows) : block_norm_parts(p.rows, p.D);
     const dim3 grid(parts, s.tiles);
@@ -780,14 +793,16 @@ cudaError_t backward(const BlockNorm& p, cudaStream_t stream) {
     };
     auto with_gate = [&](auto act) {
         constexpr int ACT = decltype(act)::value;
+        if constexpr (sizeof(T) == 2) {   // (fp32 rows that wide fill shared memory)
+            if (b.keep) return launch(block_norm_backward_kernel<T, 2, ACT, true, true, true>);
+        }
         if (b.stages == 0) {
             launch(block_norm_backward_kernel<T, 4, ACT, false, false>);
         } else if (s.vpt == 1) {
             if (b.full) launch(block_norm_backward_kernel<T, 1, ACT, true, true>);
             else launch(block_norm_backward_kernel<T, 1, ACT, true, false>);
         } else if (s.vpt == 2) {
-            if (b.keep) launch(block_norm_backward_kernel<T, 2, ACT, true, true, true>);
-            else if (b.full) launch(block_norm_backward_kernel<T, 2, ACT, true, true>);
+            if (b.full) launch(block_norm_backward_kernel<T, 2, ACT, true, true>);
             else launch(block_norm_backward_kernel<T, 2, ACT, true, false>);
         } else {
             launch(block_norm_backward_kernel<T, 4, ACT, true, false>);

@@ -376,19 +376,24 @@ __device__ __forceinline__ const Args* start(const Jobs& jobs, Cta& c) {
     return c.sg.n >= 0 ? args : nullptr;
 }
 
-// `issue`: the first of the issuing warps; `w_warps`: those that fill a buffer of w Y.
-__device__ __forceinline__ void set_up(const Args& args, Cta& c, int issue, int w_warps) {
+// Token range of the pass's step i.
+__device__ __forceinline__ int64_t chunk_start(const Cta& c, int i) {
+    return c.sg.t0 + (int64_t)(c.rev ? c.chunks - 1 - i : i) * C;
+}
+__device__ __forceinline__ int chunk_len(const Cta& c, int64_t tok) {
+    return (int)(c.sg.t1 - tok < C ? c.sg.t1 - tok : C);
+}
+
+// `issue`: the first of the issuing warps; `w_warps`: those that fill a buffer of w Y;
+// `first`: the first loads, which one thread issues as soon as the barriers are there,
+// under the tables and the allocation.
+template <typename First>
+__device__ __forceinline__ void set_up(const Args& args, Cta& c, int issue, int w_warps,
+                                       First first) {
     const LinPass& p = args.p;
     const int tid = threadIdx.x;
     c.chunks = (int)((c.sg.t1 - c.sg.t0 + C - 1) / C);
-    c.g = p.log_decay[c.h];
-    if (tid <= C) {
-        const float a = lin::decay_pow(c.g, tid);
-        c.lam[tid] = a;
-        c.lamk[tid] = a * p.kv_scale;
-        if (p.reverse ? tid > 0 : tid < C) c.wtab[p.reverse ? tid - 1 : C - 1 - tid] = a * p.kv_scale;
-    }
-    if (tid == 32 * issue + 32) {
+    if (tid == 32 * issue) {
         Bars* b = c.b;
         for (int i = 0; i < STATE_STAGES; ++i) {
             mbar_init(&b->full[i], 1);
@@ -402,16 +407,21 @@ __device__ __forceinline__ void set_up(const Args& args, Cta& c, int issue, int 
         mbar_init(&b->end, w_warps == 4 ? 8 : w_warps);   // the warps that hold a state
         b->abort = 0;
         fence_mbar_init();
+        fence_proxy_async();
+        first();
     }
-    if (tid >> 5 == issue) {
+    if (tid >> 5 == issue + 1) {
         tmem_alloc(&c.b->tmem, 512);
         tmem_relinquish();
-        if ((tid & 31) == 0) {
-            prefetch_tmap(&args.x);
-            prefetch_tmap(&args.y);
-            prefetch_tmap(&args.z);
-        }
     }
+    c.g = p.log_decay[c.h];
+    if (tid <= C) {
+        const float a = lin::decay_pow(c.g, tid);
+        c.lam[tid] = a;
+        c.lamk[tid] = a * p.kv_scale;
+        if (p.reverse ? tid > 0 : tid < C) c.wtab[p.reverse ? tid - 1 : C - 1 - tid] = a * p.kv_scale;
+    }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -422,15 +432,7 @@ __device__ __forceinline__ void finish(const Cta& c, int issue) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (threadIdx.x >> 5 == issue) tmem_dealloc(c.b->tmem, 512);
-}
-
-// Token range of the pass's step i.
-__device__ __forceinline__ int64_t chunk_start(const Cta& c, int i) {
-    return c.sg.t0 + (int64_t)(c.rev ? c.chunks - 1 - i : i) * C;
-}
-__device__ __forceinline__ int chunk_len(const Cta& c, int64_t tok) {
-    return (int)(c.sg.t1 - tok < C ? c.sg.t1 - tok : C);
+    if (threadIdx.x >> 5 == issue + 1) tmem_dealloc(c.b->tmem, 512);
 }
 
 // ------------------------------------------------------------------ the pass
@@ -454,13 +456,22 @@ __device__ __forceinline__ const float* start_state(const LinPass& p, const Cta&
     return p.state_in ? p.state_in + ((size_t)c.sg.n * p.H + c.h) * (size_t)(D * D) : nullptr;
 }
 
-__device__ __forceinline__ void issue_loads(const Args& args, const Cta& c) {
+// The state before the segment, where TMA brings it, and the first chunk.
+__device__ __forceinline__ bool tma_start(const LinPass& p, const Cta& c) {
+    return (c.sg.j > 0 || !p.state_in_turned) && start_state(p, c);
+}
+
+__device__ __forceinline__ void first_loads(const Args& args, const Cta& c) {
     const LinPass& p = args.p;
     Bars* b = c.b;
-    int issued = 0;
-    const float* start = start_state(p, c);
-    const bool init = start && (c.sg.j > 0 || !p.state_in_turned);
-    if (init) {
+    if (c.chunks > 0) {
+        const int tok = (int)chunk_start(c, 0);
+        mbar_arrive_expect_tx(&b->full[0], 3 * TILE);
+        load_tile(&args.y, c.sm + TILE, c.h, tok, &b->full[0]);
+        load_tile(&args.x, c.sm, c.h, tok, &b->full[0]);
+        load_tile(&args.z, c.sm + 2 * TILE, c.h, tok, &b->full[0]);
+    }
+    if (tma_start(p, c)) {
         mbar_arrive_expect_tx(&b->init, D * D * 4);
         const CUtensorMap* map = c.sg.j > 0 ? &args.segs : &args.init;
         const int state = (int)(c.sg.j > 0 ? (c.sg.u + c.sg.j - 1) * p.H + c.h
@@ -468,7 +479,13 @@ __device__ __forceinline__ void issue_loads(const Args& args, const Cta& c) {
         for (int q = 0; q < D / 32; ++q)
             tma_load_3d(c.sm + 3 * TILE + q * HALF, map, 32 * q, 0, state, &b->init);
     }
-    for (int i = 0; i < c.chunks; ++i) {
+}
+
+__device__ __forceinline__ void issue_loads(const Args& args, const Cta& c) {
+    const LinPass& p = args.p;
+    Bars* b = c.b;
+    int issued = c.chunks > 0;
+    for (int i = 1; i < c.chunks; ++i) {
         const int s = i & 1;
         // stage 1 holds the state first
         if (i == 1 && !wait1(b, &b->begun, 0, p, 317)) break;
@@ -486,7 +503,7 @@ __device__ __forceinline__ void issue_loads(const Args& args, const Cta& c) {
     // no copy outlives the CTA
     for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
         mbar_wait(&b->full[i & 1], (i >> 1) & 1, nullptr);
-    if (init) mbar_wait(&b->init, 0, nullptr);
+    if (tma_start(p, c)) mbar_wait(&b->init, 0, nullptr);
 }
 
 // Whether the CTA writes a final state.
@@ -835,7 +852,7 @@ lin_pass_tc_kernel(const __grid_constant__ Jobs jobs) {
     if (!job) return;
     const Args& args = *job;
     const LinPass& p = args.p;
-    set_up(args, c, 24, 4);
+    set_up(args, c, 24, 4, [&] { first_loads(args, c); });
     const int warp = threadIdx.x >> 5;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // this warp's 32 TMEM lanes
     if (warp < 8) {
@@ -870,21 +887,27 @@ lin_states_tc_kernel(const __grid_constant__ Jobs jobs) {
     const Args& args = *job;
     const LinPass& p = args.p;
     if (c.sg.j + 1 >= c.sg.count || c.sg.u + c.sg.j >= lin::seg_rows(p.total_T, p.seg_len)) return;
-    set_up(args, c, 16, 16);
+    auto load = [&](int i) {
+        uint8_t* st = c.sm + i % STATE_STAGES * 2 * TILE;
+        uint64_t* full = &c.b->full[i % STATE_STAGES];
+        const int tok = (int)chunk_start(c, i);
+        mbar_arrive_expect_tx(full, 2 * TILE);
+        load_tile(&args.y, st, c.h, tok, full);
+        load_tile(&args.z, st + TILE, c.h, tok, full);
+    };
+    set_up(args, c, 16, 16, [&] {
+        for (int i = 0; i < c.chunks && i < STATE_STAGES; ++i) load(i);
+    });
     Bars* b = c.b;
     const int tid = threadIdx.x, warp = tid >> 5, n = c.chunks;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     if (warp == 16) {
         if ((tid & 31) == 0) {
-            int issued = 0;
-            for (int i = 0; i < n; ++i) {
-                const int s = i % STATE_STAGES, use = i / STATE_STAGES;
-                if (use > 0 && !wait1(b, &b->empty[s], (use - 1) & 1, p, 331)) break;
-                uint8_t* st = c.sm + s * 2 * TILE;
-                const int tok = (int)chunk_start(c, i);
-                mbar_arrive_expect_tx(&b->full[s], 2 * TILE);
-                load_tile(&args.y, st, c.h, tok, &b->full[s]);
-                load_tile(&args.z, st + TILE, c.h, tok, &b->full[s]);
+            int issued = n < STATE_STAGES ? n : STATE_STAGES;
+            for (int i = issued; i < n; ++i) {
+                if (!wait1(b, &b->empty[i % STATE_STAGES], (i / STATE_STAGES - 1) & 1, p, 331))
+                    break;
+                load(i);
                 issued = i + 1;
             }
             for (int i = issued > STATE_STAGES ? issued - STATE_STAGES : 0; i < issued; ++i)

@@ -17,6 +17,7 @@
 
 #include <type_traits>
 
+#include "kda_follow.cuh"
 #include "kda_packed.cuh"
 
 namespace kda {
@@ -605,6 +606,7 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
         }
         if (RING && ++stage == depth) stage = 0;
     }
+    let_follow();
     if (RING) copies_done(0);
     __syncthreads();   // the ring's room takes the sums
 
@@ -657,6 +659,7 @@ block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
 // fixed tree.  dw_post of heads has a part per tile too.
 __global__ void __launch_bounds__(1024) block_norm_sums_kernel(BlockNorm p, int parts, int tiles) {
     __shared__ float4 buf[32][8];
+    wait_before();
     const int which = blockIdx.y;
     float* dst = which == 0 ? p.dw_post : which == 1 ? p.dres_scale : p.dw_pre;
     const int width = which == 0 ? p.group : p.D;
@@ -817,8 +820,8 @@ cudaError_t backward(const BlockNorm& p, cudaStream_t stream) {
     }
     if (err == cudaSuccess) err = cudaGetLastError();
     if (err != cudaSuccess) return err;
-    block_norm_sums_kernel<<<dim3((p.D + 31) / 32, 3), 1024, 0, stream>>>(p, parts, s.tiles);
-    return cudaGetLastError();
+    return launch_follower(block_norm_sums_kernel, dim3((p.D + 31) / 32, 3), 1024, 0, stream, p,
+                           parts, s.tiles);
 }
 
 }  // namespace

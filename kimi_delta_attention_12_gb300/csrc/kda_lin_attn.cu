@@ -26,6 +26,7 @@
 #include <limits.h>
 #include <string.h>
 
+#include "kda_follow.cuh"
 #include "kda_lin.cuh"
 #include "kda_packed.cuh"
 
@@ -347,6 +348,8 @@ lin_passes_kernel(const __grid_constant__ Passes jobs) {
     const int k = blockIdx.x < jobs.end[0] ? 0 : blockIdx.x < jobs.end[1] ? 1 : 2;
     const LinPass& p = jobs.p[k];
     const uint32_t block = blockIdx.x - (k > 0 ? jobs.end[k - 1] : 0);
+    if (STATES) let_follow();
+    else wait_before();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;   // no wait here can run out
     if (p.dx == 32) pass<T, 32, STATES>(p, block);
     else if (p.dx == 64) pass<T, 64, STATES>(p, block);
@@ -361,7 +364,7 @@ size_t pass_smem(int dx) {
 }
 
 template <typename T, bool STATES>
-cudaError_t launch_passes(const LinPass* passes, int n, cudaStream_t stream) {
+cudaError_t launch_passes(const LinPass* passes, int n, bool follows, cudaStream_t stream) {
     Passes jobs;
     memset(&jobs, 0, sizeof(jobs));
     int64_t grid = 0;
@@ -384,6 +387,7 @@ cudaError_t launch_passes(const LinPass* passes, int n, cudaStream_t stream) {
             ? cudaSuccess
             : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
+    if (follows) return launch_follower(kernel, (unsigned)grid, THREADS, smem, stream, jobs);
     kernel<<<(unsigned)grid, THREADS, smem, stream>>>(jobs);
     return cudaGetLastError();
 }
@@ -397,9 +401,9 @@ cudaError_t run_passes(const LinPass* passes, int n, cudaStream_t stream) {
         cut = cut || passes[i].total_T >= passes[i].seg_len;
     }
     cudaError_t err = cudaSuccess;
-    if (cut) err = launch_passes<T, true>(passes, n, stream);
+    if (cut) err = launch_passes<T, true>(passes, n, false, stream);
     if (cut && err == cudaSuccess) err = launch_lin_scan(passes, n, stream);
-    if (err == cudaSuccess) err = launch_passes<T, false>(passes, n, stream);
+    if (err == cudaSuccess) err = launch_passes<T, false>(passes, n, cut, stream);
     return err;
 }
 
@@ -413,6 +417,8 @@ struct Scan {
 };
 
 __global__ void __launch_bounds__(SCAN_THREADS) lin_scan_kernel(const __grid_constant__ Scan scan) {
+    let_follow();
+    wait_before();
     const LinPass& p = scan.p[blockIdx.y];
     const int per = p.dx * p.dz / 4 / SCAN_THREADS;       // blocks of one state
     const int64_t pair = blockIdx.x / per;
@@ -593,8 +599,7 @@ cudaError_t launch_lin_scan(const LinPass* passes, int n, cudaStream_t stream) {
     const LinPass& p = passes[0];
     const int64_t grid = (int64_t)p.N * p.H * (p.dx * p.dz / 4 / SCAN_THREADS);
     if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-    lin_scan_kernel<<<dim3((unsigned)grid, n), SCAN_THREADS, 0, stream>>>(scan);
-    return cudaGetLastError();
+    return launch_follower(lin_scan_kernel, dim3((unsigned)grid, n), SCAN_THREADS, 0, stream, scan);
 }
 
 cudaError_t launch_lin_pass(const LinPass* passes, int n, int dtype, cudaStream_t stream) {

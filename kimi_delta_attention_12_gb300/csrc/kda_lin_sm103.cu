@@ -24,7 +24,8 @@
 // segments: one kernel forms the state that each segment adds (Y and Z alone, the
 // sums in TMEM from the first token to the last: 1.6 us a chunk), a scan carries them
 // on, and the pass starts each segment from its state.  One sequence of 4,096 tokens,
-// 32 heads: 68 us (22 states, 6 scan, 36 pass) where whole sequences took 108.
+// 32 heads: 64 us (about 21 states, 6 scan, 35 pass; each kernel is brought on
+// while the one before ends) where whole sequences took 108.
 //
 // Roles (28 warps): 0-7 turn P into P' and write the outputs (thread = token;
 // each half takes half of the columns), 8-15 carry the state (thread = row of
@@ -38,6 +39,7 @@
 #include <limits.h>
 #include <string.h>
 
+#include "kda_follow.cuh"
 #include "kda_lin.cuh"
 #include "kda_packed.cuh"
 #include "sm103_ptx.cuh"
@@ -471,6 +473,8 @@ __device__ __forceinline__ void first_loads(const Args& args, const Cta& c) {
         load_tile(&args.x, c.sm, c.h, tok, &b->full[0]);
         load_tile(&args.z, c.sm + 2 * TILE, c.h, tok, &b->full[0]);
     }
+    wait_before();             // the segments' states
+    fence_proxy_async();
     if (tma_start(p, c)) {
         mbar_arrive_expect_tx(&b->init, D * D * 4);
         const CUtensorMap* map = c.sg.j > 0 ? &args.segs : &args.init;
@@ -882,6 +886,7 @@ lin_pass_tc_kernel(const __grid_constant__ Jobs jobs) {
 __global__ void __launch_bounds__(STATE_THREADS, 1)
 lin_states_tc_kernel(const __grid_constant__ Jobs jobs) {
     Cta c;
+    let_follow();
     const Args* job = start<true>(jobs, c);
     if (!job) return;
     const Args& args = *job;
@@ -1058,6 +1063,7 @@ cudaError_t launch_lin_pass_tc(const LinPass* passes, int n, cudaStream_t stream
     err = cudaFuncSetAttribute(lin_pass_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                SMEM);
     if (err != cudaSuccess) return err;
+    if (most > 0) return launch_follower(lin_pass_tc_kernel, (unsigned)grid, THREADS, SMEM, stream, jobs);
     lin_pass_tc_kernel<<<(unsigned)grid, THREADS, SMEM, stream>>>(jobs);
     return cudaGetLastError();
 }

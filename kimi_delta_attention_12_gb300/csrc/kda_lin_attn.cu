@@ -195,11 +195,21 @@ __device__ __forceinline__ void pass(const LinPass& p, uint32_t block) {
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     if (STAGES<T> == 2 && chunks > 0) load_chunk(0);
+    if (STATES) __syncthreads();   // lam
     for (int64_t ci = 0; ci < chunks; ++ci) {
         const int64_t c0 = first(ci);
         const int len = (int)(sg.t1 - c0 < C ? sg.t1 - c0 : C);
         const float* X = stages + (ci % STAGES<T>) * STAGE_FLOATS<DX>;
-        const float *Y = X + C * LD, *Z = Y + C * LD;
+        const float* Y = X + C * LD;
+        float* Z = stages + (ci % STAGES<T>) * STAGE_FLOATS<DX> + 2 * C * LD;
+        // the thread's four values of Z, which it has copied, get their weight in the state
+        auto weigh = [&] {
+            const int s = tid / 8;
+            const float w = lam[p.reverse ? s + 1 : (len - 1 - s) & (C - 1)] * p.kv_scale;
+            float4 v = load4(Z + s * SLICE + c4);
+            v.x *= w; v.y *= w; v.z *= w; v.w *= w;
+            store4(Z + s * SLICE + c4, v);
+        };
         if (STAGES<T> == 1) {
             load_chunk(ci);
         } else if (ci + 1 < chunks) {
@@ -211,6 +221,8 @@ __device__ __forceinline__ void pass(const LinPass& p, uint32_t block) {
         if (!STATES) {
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) store4(S + (d0 + i) * SLICE + c4, st[i]);
+        } else {
+            weigh();
         }
         __syncthreads();
         if (!STATES) {
@@ -276,6 +288,7 @@ __device__ __forceinline__ void pass(const LinPass& p, uint32_t block) {
                     mul4(inter, a, b);
                 }
                 __syncthreads();   // P is read; its room takes the quarters of the outputs
+                weigh();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int t = r + 8 * i;
@@ -305,9 +318,7 @@ __device__ __forceinline__ void pass(const LinPass& p, uint32_t block) {
         }
 #pragma unroll 8
         for (int s = 0; s < C; ++s) {     // rows past the end are zeros
-            const float w = lam[p.reverse ? s + 1 : (len - 1 - s) & (C - 1)] * p.kv_scale;
-            float4 v = load4(Z + s * SLICE + c4);
-            v.x *= w; v.y *= w; v.z *= w; v.w *= w;
+            const float4 v = load4(Z + s * SLICE + c4);
             float k[ROWS];
             if (ROWS == 4) {
                 const float4 k4 = load4(Y + s * LD + d0);

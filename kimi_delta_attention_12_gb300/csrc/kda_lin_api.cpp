@@ -40,7 +40,7 @@ bool on_tensor_cores(int32_t d_k, int32_t d_v, kda_dtype dt, uint32_t flags, int
 // columns of dz, of which an SM takes two, and a few rounds of them even out
 // ragged lengths (with one round and a half a ragged fp32 backward took 368 us for
 // 329).  The three passes of a backward make three rounds of segments three times
-// as long: 253 us, 259 with eight.
+// as long (253 us, 259 with eight).
 kda::LinCut cut_of(int32_t N, int32_t total_T, int32_t H, int32_t dz, int passes, bool tc) {
     return tc ? kda::lin_cut_tc(N, total_T, H, passes, sm_count())
               : kda::lin_cut(N, total_T, H, dz / 32, passes > 1 ? 3 : 8, sm_count());

@@ -17,9 +17,10 @@
 // outputs' pass, 62 % of the issue slots, 10 % of the memory's rate.  Chunks of 32
 // keep a quarter of X Y^T in 16 registers a thread (4 x 4 tiles: 16 multiply-adds
 // for two 16-byte reads), and slices of 32 columns leave room for two CTAs an SM.
-// Backward of 3,602 tokens in 5 sequences, 8 heads, 64 x 128 wide, fp32: 253 us
-// (57 the segments' states, 8 the scan, 189 the outputs); with one tile row a thread,
-// longer segments and a launch for each gradient it had taken 1,520.
+// Backward of 3,602 tokens in 5 sequences, 8 heads, 64 x 128 wide, fp32: 226 us
+// (45 the segments' states, 8 the scan, 183 the outputs, each brought on while the
+// one before ends); with one tile row a thread, longer segments and a launch for each
+// gradient it had taken 1,520.
 #include "kda_lin.h"
 
 #include <cuda_bf16.h>

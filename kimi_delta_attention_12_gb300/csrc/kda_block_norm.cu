@@ -27,6 +27,7 @@ constexpr int V = 8;             // channels per vector: 16 bytes of bf16
 constexpr int MAX_THREADS = 512;
 constexpr int MAX_ROWS = 4;      // rows that short-row blocks take at once
 constexpr int TILE = 2048;       // columns per block where rows do not couple them
+constexpr int SUMS = 2 * MAX_ROWS * 32 * 3;   // row_sum's buffer
 
 // A vector as it was loaded.
 template <typename T>
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(256) block_norm_heads_kernel(BlockNorm p, int6
 // vectors per thread, threadIdx.y over rows.
 template <typename T, int VPT>
 __global__ void __launch_bounds__(MAX_THREADS) block_norm_kernel(BlockNorm p) {
-    __shared__ float buf[2 * MAX_ROWS * 32 * 3];
+    __shared__ float buf[SUMS];
     const int warps = blockDim.x >> 5, vecs = p.D / V;
     const bool whole = p.group == p.D;
     const int lanes = whole ? 32 : p.group / V;
@@ -383,7 +384,7 @@ constexpr int KEEP_THREADS = 256, KEEP_ROWS = 2;   // of a block that keeps the 
 template <typename T, int VPT, int ACT, bool RING, bool FULL, bool KEEP = false>
 __global__ void __launch_bounds__(MAX_THREADS)
 block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
-    __shared__ float buf[2 * MAX_ROWS * 32 * 3];
+    __shared__ float buf[SUMS];
     // what the shape of a block that keeps the weights is
     const int width = KEEP ? KEEP_THREADS : (int)blockDim.x, rows = KEEP ? KEEP_ROWS : (int)blockDim.y;
     const int D = KEEP ? KEEP_THREADS * VPT * V : p.D, cols = KEEP ? D : tile;
@@ -788,7 +789,8 @@ cudaError_t backward(const BlockNorm& p, cudaStream_t stream) {
     const dim3 grid(parts, s.tiles);
     cudaError_t err = cudaSuccess;
     auto launch = [&](auto kernel) {
-        if (b.smem > 48 * 1024) {
+        // (without the attribute a block has 48 KB, the kernel's own buffer among them)
+        if (b.smem + SUMS * sizeof(float) > 48 * 1024) {
             err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)b.smem);
         }

@@ -203,10 +203,11 @@ __device__ __forceinline__ void pass(const LinPass& p, uint32_t block) {
         const float* X = stages + (ci % STAGES<T>) * STAGE_FLOATS<DX>;
         const float* Y = X + C * LD;
         float* Z = stages + (ci % STAGES<T>) * STAGE_FLOATS<DX> + 2 * C * LD;
-        // the thread's four values of Z, which it has copied, get their weight in the state
+        // the thread's four values of Z, which it has copied, get their weight in the state;
+        // rows past the end none (a growing decay's power there may be infinite)
         auto weigh = [&] {
             const int s = tid / 8;
-            const float w = lam[p.reverse ? s + 1 : (len - 1 - s) & (C - 1)] * p.kv_scale;
+            const float w = s < len ? lam[p.reverse ? s + 1 : len - 1 - s] * p.kv_scale : 0.0f;
             float4 v = load4(Z + s * SLICE + c4);
             v.x *= w; v.y *= w; v.z *= w; v.w *= w;
             store4(Z + s * SLICE + c4, v);

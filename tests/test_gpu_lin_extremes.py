@@ -1,0 +1,41 @@
+"""GPU parity of the decayed linear attention where decays are extreme, against the 64-bit
+recurrence with test_gpu_lin's bounds."""
+import pytest
+import torch
+
+import lin_reference as R
+import test_gpu_lin as L
+import kimi_delta_attention_12_gb300 as kda
+
+pytestmark = pytest.mark.gpu
+
+BF, F = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("dtype,d", [(F, 32), (F, 64), (BF, 64), (BF, 128)])
+def test_decays_that_grow_past_fp32_within_a_chunk(dtype, d):
+    """e^{20} a token: the powers up to the sequences' own lengths are finite, those up to a
+    whole chunk's are not, and count for nothing."""
+    x = R.make([1, 2, 4, 1], 2, d, d, dtype, seed=2, state=True, g=[3.0, 20.0])
+    v = R.dev(x)
+    args = (v["q"], v["k"], v["v"], v["log_decay"])
+    o, S = kda.kda_lin_prefill(*args, v["S0"], v["cu"], x["cu"])
+    L.check_forward(x, o, S, 1.0, d, dtype, L.tensor_core(d, d, dtype))
+    g = kda.kda_lin_backward(*args, v["dO"], v["S0"], v["cu"], x["cu"], v["dS"])
+    check_backward(x, g, 1.0, L.tensor_core(d, d, dtype))
+
+
+def check_backward(x, g, scale, tc):
+    """Every gradient within the roundings counted, as test_gpu_lin.test_backward has them."""
+    a = {n: R.f64(t) for n, t in x.items() if isinstance(t, torch.Tensor)}
+    inputs = [a[n] for n in ("q", "k", "v")]
+    want = R.lin_backward(*inputs, a["log_decay"], x["lens"], a["dO"], a.get("S0"), a.get("dS"),
+                          scale)
+    mag = R.lin_backward(*R.absolute(*inputs), a["log_decay"], x["lens"],
+                         *R.absolute(a["dO"], a.get("S0"), a.get("dS")), abs(scale))
+    terms = R.fp32_terms(x["lens"], max(inputs[0].shape[2], inputs[2].shape[2]))
+    for n in want:
+        assert bool(torch.isfinite(g[n]).all()), n
+        rows = n != "dS0"
+        R.check(n, g[n], want[n], mag[n], terms, rows and g[n].dtype == BF,
+                1 if rows and tc else 0)

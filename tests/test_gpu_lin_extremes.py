@@ -39,3 +39,36 @@ def check_backward(x, g, scale, tc):
         rows = n != "dS0"
         R.check(n, g[n], want[n], mag[n], terms, rows and g[n].dtype == BF,
                 1 if rows and tc else 0)
+
+
+def one_sign(T, H, d=128):
+    gen = torch.Generator(device="cuda").manual_seed(T + H)
+    q, k, v = (torch.rand(T, H, d, generator=gen, device="cuda").add(0.5).to(BF)
+               for _ in range(3))
+    g = torch.zeros(H, device="cuda")
+    g[1::3], g[2::3] = -1e-6, -2e-5
+    return q, k, v, g
+
+
+@pytest.mark.parametrize("T,H", [(65536, 64), (65536, 96), (20000, 4)],
+                         ids=["segments", "cut_in_two", "short_segments"])
+def test_long_sums_of_one_sign(T, H):
+    """States of slow decays whose terms all have one sign: what the tensor core cuts off the
+    sums is cut off the same side each time.  It adds up four chunks at most, 96 additions that
+    each lose less than 2^-23; everything after them is rounded, an addition a chunk."""
+    q, k, v, g = one_sign(T, H)
+    o, S = kda.kda_lin_prefill(q, k, v, g, scale=1.0 / T)
+    bound = (2 * 96 + T / 128 + 64) * R.U32
+    t = torch.arange(T, device="cuda", dtype=torch.float64)
+    for h in range(3):
+        w = torch.exp(g[h].double() * (T - 1 - t))[:, None]
+        want = (k[:, h].double() * w).T @ v[:, h].double()
+        assert float(((S[0, h].double() - want) / want).abs().max()) <= bound, h
+    H = max(1, H // 3)
+    g = g[:H].contiguous()
+    q, k, v = (a[:, :H].contiguous() for a in (q, k, v))
+    dS0 = kda.kda_lin_backward(q, k, v, g, v, scale=1.0 / T)["dS0"]
+    for h in range(min(H, 3)):
+        w = torch.exp(g[h].double() * (t + 1))[:, None] / T
+        want = (q[:, h].double() * w).T @ v[:, h].double()
+        assert float(((dS0[0, h].double() - want) / want).abs().max()) <= bound, h

@@ -15,6 +15,7 @@ Entry points (same names as the C ABI):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -731,6 +732,23 @@ def _host_seqlens(cu_seqlens_host, N: int):
     return cu_seqlens_host.to(torch.int32).contiguous()
 
 
+def _packed_rows(batch, stream: Optional[torch.cuda.Stream], **ts):
+    """[B, T, H, d] tensors as rows [B T, H, d].  A strided one is copied, on the stream
+    that the call runs on."""
+    for name, t in ts.items():
+        if t.dim() != 4 or t.shape[:2] != batch:
+            raise ValueError(f"{name} must have shape {(*batch, 'H', 'd')}, got {tuple(t.shape)}")
+    with _on(stream, _batch_device(*ts.values())) or contextlib.nullcontext():
+        return [t.reshape(-1, *t.shape[2:]) for t in ts.values()]
+
+
+def _batch_device(*ts) -> int:
+    dev = ts[0].get_device()
+    if dev < 0 or any(t.get_device() != dev for t in ts):
+        raise ValueError("KDA tensors must live on one CUDA device")
+    return dev
+
+
 def _scratch(nbytes: int, device) -> torch.Tensor:
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
@@ -753,7 +771,7 @@ def kda_lin_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay
     batch = None
     if q.dim() == 4:
         batch = q.shape[:2]
-        q, k, v = (t.reshape(-1, *t.shape[2:]) for t in (q, k, v))
+        q, k, v = _packed_rows(batch, stream, q=q, k=k, v=v)
     dev = _one_device(q, k, v, log_decay, initial_state, cu_seqlens, o, final_state, workspace)
     N, total_T, H, d_k, d_v = _lin_sizes(q, k, v, log_decay, cu_seqlens)
     if batch is not None:

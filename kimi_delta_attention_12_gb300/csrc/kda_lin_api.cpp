@@ -116,7 +116,7 @@ int kda_lin_prefill(const void* q, const void* k, const void* v, const float* lo
         if (overlaps(o, nv, ins[i], nin[i]) || overlaps(workspace, used, ins[i], nin[i])) {
             return KDA_ERR_INVALID_ARG;
         }
-        if (overlaps(final_state, nst, ins[i], nin[i]) && final_state != initial_state) {
+        if (overlaps(final_state, nst, ins[i], nin[i]) && !(i == 3 && ins[i] == final_state)) {
             return KDA_ERR_INVALID_ARG;
         }
     }

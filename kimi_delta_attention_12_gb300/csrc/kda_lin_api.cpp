@@ -54,6 +54,9 @@ size_t state_bytes(int32_t N, int32_t H, int32_t d_k, int32_t d_v) {
     return (size_t)N * H * d_k * d_v * sizeof(float);
 }
 
+size_t decay_bytes(int32_t H) { return (size_t)H * sizeof(float); }
+size_t seqlens_bytes(int32_t N) { return ((size_t)N + 1) * sizeof(int32_t); }
+
 // Room for the segments' states of `passes` passes that run at once, whichever
 // form a call's flags choose.
 size_t segment_room(int32_t N, int32_t total_T, int32_t H, int32_t d_k, int32_t d_v, kda_dtype dt,
@@ -109,10 +112,10 @@ int kda_lin_prefill(const void* q, const void* k, const void* v, const float* lo
         return KDA_ERR_ALIGNMENT;
     }
     // o may not overlap an input; final_state only the initial one, whole
-    const void* ins[4] = {q, k, v, initial_state};
-    const size_t nin[4] = {nqk, nqk, nv, nst};
+    const void* ins[6] = {q, k, v, initial_state, log_decay, cu_seqlens};
+    const size_t nin[6] = {nqk, nqk, nv, nst, decay_bytes(H), seqlens_bytes(N)};
     const size_t used = need;
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 6; ++i) {
         if (overlaps(o, nv, ins[i], nin[i]) || overlaps(workspace, used, ins[i], nin[i])) {
             return KDA_ERR_INVALID_ARG;
         }
@@ -173,9 +176,9 @@ int kda_lin_decode_step(const void* q, const void* k, const void* v, const float
     }
     const size_t eb = elem_bytes(dt), nqk = (size_t)B * H * d_k * eb,
                  nv = (size_t)B * H * d_v * eb, nst = state_bytes(pool_size, H, d_k, d_v);
-    const void* ins[3] = {q, k, v};
-    const size_t nin[3] = {nqk, nqk, nv};
-    for (int i = 0; i < 3; ++i) {
+    const void* ins[5] = {q, k, v, log_decay, slots};
+    const size_t nin[5] = {nqk, nqk, nv, decay_bytes(H), (size_t)B * sizeof(int32_t)};
+    for (int i = 0; i < 5; ++i) {
         if (overlaps(o, nv, ins[i], nin[i]) || overlaps(state, nst, ins[i], nin[i])) {
             return KDA_ERR_INVALID_ARG;
         }
@@ -217,9 +220,9 @@ int kda_lin_backward(const void* q, const void* k, const void* v, const float* l
     }
     const size_t need = kda_lin_backward_workspace_bytes(N, total_T, H, d_k, d_v, dt);
     if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;
-    const void* bufs[12] = {q, k, v, dO, initial_state, dS_final, dq, dk, dv, dS0, workspace,
-                            nullptr};
-    for (int i = 0; i < 10; ++i) {
+    const void* bufs[13] = {log_decay, cu_seqlens, q, k, v, dO, initial_state, dS_final,
+                            dq, dk, dv, dS0, workspace};
+    for (int i = 2; i < 12; ++i) {
         if (!aligned(bufs[i], 16)) return KDA_ERR_ALIGNMENT;
     }
     if (!aligned(log_decay, 4) || !aligned(cu_seqlens, 4) || !aligned(workspace, 256)) {
@@ -227,8 +230,9 @@ int kda_lin_backward(const void* q, const void* k, const void* v, const float* l
     }
     const size_t eb = elem_bytes(dt), nst = state_bytes(N, H, d_k, d_v);
     const size_t nqk = (size_t)total_T * H * d_k * eb, nv = (size_t)total_T * H * d_v * eb;
-    const size_t size[11] = {nqk, nqk, nv, nv, nst, nst, nqk, nqk, nv, nst, need};
-    for (int i = 6; i < 11; ++i) {      // no output, nor the workspace, on another buffer
+    const size_t size[13] = {decay_bytes(H), seqlens_bytes(N), nqk, nqk, nv, nv, nst, nst,
+                             nqk, nqk, nv, nst, need};
+    for (int i = 8; i < 13; ++i) {      // no output, nor the workspace, on another buffer
         for (int j = 0; j < i; ++j) {
             if (overlaps(bufs[i], size[i], bufs[j], size[j])) return KDA_ERR_INVALID_ARG;
         }

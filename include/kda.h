@@ -200,8 +200,8 @@ KDA_API int64_t kda_checkpoint_count(const int32_t* cu_seqlens_host, int32_t N,
                                      int32_t total_T, int32_t ckpt_interval);
 
 /*
- * kda_workspace_status -- wait for `stream`, then read the status word a
- * kda_prefill launch left in `workspace`.  Returns KDA_OK, KDA_ERR_TIMEOUT
+ * kda_workspace_status -- wait for `stream`, then read the status word the last
+ * kda_prefill, kda_lin_prefill or kda_lin_backward launch left in `workspace`.  Returns KDA_OK, KDA_ERR_TIMEOUT
  * (a bounded wait inside the kernel ran out; its outputs are invalid) or
  * KDA_ERR_CUDA.  Synchronising; meant for tests and diagnostics.
  */
@@ -500,7 +500,10 @@ KDA_API int kda_prefill_noalloc_status(void* stream);
  *  workspace      kda_lin_prefill_workspace_bytes(...) bytes, 256-byte
  *                 aligned, no initialisation needed; it begins with a status
  *                 word that kda_workspace_status reads
- * A sequence of length zero hands its initial state (or zeros) on.
+ * A sequence of length zero hands its initial state (or zeros) on.  A call that
+ * has nothing to write (no tokens and no final_state; for the backward, no tokens
+ * and no dS0) launches nothing and leaves the workspace, its status word too, as
+ * it is.
  *
  * bf16 with d_k = d_v = 128 runs on the tensor cores in chunks of 128 tokens;
  * o carries the rounding to bf16 of the products q.k and of the carried state

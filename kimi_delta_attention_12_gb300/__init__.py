@@ -803,6 +803,8 @@ def kda_lin_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay
             _addr(cu_seqlens), _addr(host_cu), N, total_T, H, d_k, d_v, code, scale,
             KDA_FLAG_RECURRENT if recurrent else 0, o.data_ptr(), _addr(final_state),
             workspace.data_ptr(), workspace.nbytes, _raw_stream(dev))
+        if total_T == 0 and final_state is None and st == KDA_OK:
+            workspace.view(-1)[:4].zero_()   # nothing was launched that would clear the status word
     finally:
         if on is not None:
             on.__exit__(None, None, None)

@@ -48,3 +48,21 @@ def test_host_batches_are_refused():
     x = [torch.zeros(2, 4, 1, 32) for _ in range(3)]
     with pytest.raises(ValueError):
         kda.kda_lin_prefill(*x, torch.zeros(1))
+
+
+@pytest.mark.parametrize("dtype,d", [(torch.float32, 32), (torch.bfloat16, 128)])
+def test_status_after_calls_of_no_tokens(dtype, d):
+    """A workspace with leftovers of another use reports no timeout."""
+    q = torch.empty(0, 2, d, dtype=dtype, device="cuda")
+    g = torch.zeros(2, device="cuda")
+    cu = torch.zeros(4, dtype=torch.int32)
+    need = max(kda.lin_prefill_workspace_bytes(3, 0, 2, d, d, dtype),
+               kda.lin_backward_workspace_bytes(3, 0, 2, d, d, dtype))
+    for final in (False, True):
+        w = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+        kda.kda_lin_prefill(q, q, q, g, None, cu.cuda(), cu, output_final_state=final,
+                            workspace=w)
+        assert kda.workspace_status(w) == kda.KDA_OK
+    w = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    kda.kda_lin_backward(q, q, q, g, q, None, cu.cuda(), cu, workspace=w)
+    assert kda.workspace_status(w) == kda.KDA_OK

@@ -674,6 +674,8 @@ def _on(stream: Optional[torch.cuda.Stream], dev: int):
     given stream (memory allocated for the call then belongs to it, so that its
     reuse waits for the call's kernels).  None where that is the present one."""
     if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"stream is of {stream.device}, the tensors of cuda:{dev}")
         return torch.cuda.stream(stream)
     if dev != torch.cuda.current_device():
         return torch.cuda.device(dev)

@@ -512,7 +512,8 @@ KDA_API int kda_prefill_noalloc_status(void* stream);
  * value that is not finite may reach the outputs of all tokens of its own chunk,
  * earlier ones among them; it never reaches another sequence.
  * Errors (nothing is launched): as kda_prefill, and KDA_ERR_INVALID_ARG for an
- * output or the workspace on top of another buffer.
+ * output or the workspace on top of another buffer, and for a cu_seqlens_host of
+ * unequal lengths without cu_seqlens.
  */
 KDA_API int kda_lin_prefill(const void* q, const void* k, const void* v,
                             const float* log_decay, const float* initial_state,

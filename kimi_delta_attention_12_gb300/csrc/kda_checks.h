@@ -25,11 +25,12 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
-// A host mirror of cu_seqlens starts at 0, does not decrease and ends at total_T.
-inline bool valid_host_seqlens(const int32_t* cu, int32_t N, int32_t total_T) {
+// A host mirror of cu_seqlens starts at 0, does not decrease and ends at total_T; without
+// cu_seqlens itself (`equal`) the sequences are N of equal length, and it says so too.
+inline bool valid_host_seqlens(const int32_t* cu, int32_t N, int32_t total_T, bool equal) {
     if (cu[0] != 0 || cu[N] != total_T) return false;
     for (int32_t n = 0; n < N; ++n) {
-        if (cu[n + 1] < cu[n]) return false;
+        if (cu[n + 1] < cu[n] || (equal && cu[n + 1] - cu[n] != total_T / N)) return false;
     }
     return true;
 }

@@ -99,7 +99,8 @@ int kda_lin_prefill(const void* q, const void* k, const void* v, const float* lo
     if ((flags & ~kLinFlags) != 0 || !isfinite(scale) || !log_decay) return KDA_ERR_INVALID_ARG;
     if (total_T > 0 && (!q || !k || !v || !o)) return KDA_ERR_INVALID_ARG;
     if (!cu_seqlens && total_T % N != 0) return KDA_ERR_INVALID_ARG;
-    if (cu_seqlens_host && !kda::valid_host_seqlens(cu_seqlens_host, N, total_T)) {
+    if (cu_seqlens_host &&
+        !kda::valid_host_seqlens(cu_seqlens_host, N, total_T, cu_seqlens == nullptr)) {
         return KDA_ERR_INVALID_ARG;
     }
     const size_t need = kda_lin_prefill_workspace_bytes(N, total_T, H, d_k, d_v, dt);
@@ -215,7 +216,8 @@ int kda_lin_backward(const void* q, const void* k, const void* v, const float* l
     if ((flags & ~kLinFlags) != 0 || !isfinite(scale) || !log_decay) return KDA_ERR_INVALID_ARG;
     if (total_T > 0 && (!q || !k || !v || !dO || !dq || !dk || !dv)) return KDA_ERR_INVALID_ARG;
     if (!cu_seqlens && total_T % N != 0) return KDA_ERR_INVALID_ARG;
-    if (cu_seqlens_host && !kda::valid_host_seqlens(cu_seqlens_host, N, total_T)) {
+    if (cu_seqlens_host &&
+        !kda::valid_host_seqlens(cu_seqlens_host, N, total_T, cu_seqlens == nullptr)) {
         return KDA_ERR_INVALID_ARG;
     }
     const size_t need = kda_lin_backward_workspace_bytes(N, total_T, H, d_k, d_v, dt);

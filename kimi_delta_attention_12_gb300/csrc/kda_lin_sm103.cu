@@ -82,7 +82,12 @@ constexpr uint32_t TC_W = 384;           // w Y of 32 tokens: two buffers of thr
 constexpr uint32_t TS_U = 0;
 constexpr uint32_t TS_W = 128;           // two buffers of three parts of 64 columns
 
-static_assert((132 + 132 + 128) * 4 + 320 <= 2048, "tables and barriers");
+// The tables: weights of a whole chunk's tokens in the state, then the powers of the
+// decay, then the barriers.  split_w reads a short chunk's weights from the middle of
+// the first on, up to C - 1 entries past its end: into the second, never past it.
+constexpr int POWERS = C + 4;
+static_assert(C - 1 <= POWERS, "reads past the weights stay in the tables");
+static_assert((C + POWERS) * 4 + 320 <= 2048, "tables and barriers");
 
 struct Args {
     CUtensorMap x, y, z, out;
@@ -270,7 +275,7 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t* r) {
 // to the fp32 product within 2^-24.  The tile is read transposed, 8 x 8 values
 // at a time, into the layout that TMEM takes 16 lanes at a time.  w: the weight
 // of token 0 of the chunk; rows past its end (another sequence's, maybe not
-// finite) count as zero, and their weights are read from the tables behind.
+// finite) count as zero, and their weights are read from the table behind.
 __device__ __forceinline__ void split_w(uint32_t y, int quad, int tok0, const float* w, float f,
                                         int len, uint32_t hi, uint32_t mid, uint32_t lo) {
     const int lane = threadIdx.x & 31, row = lane & 7, mat = lane >> 3;
@@ -334,9 +339,8 @@ __device__ __forceinline__ void load_tile(const CUtensorMap* map, uint8_t* dst, 
 struct Cta {
     uint8_t* sm;
     Bars* b;
-    float* lam;     // a^0 .. a^128
-    float* lamk;    // the same times kv_scale
     float* wtab;    // weights of a whole chunk's tokens in the state
+    float* lam;     // a^0 .. a^128
     lin::Segment sg;
     int h, chunks;
     bool rev;
@@ -356,10 +360,9 @@ __device__ __forceinline__ const Args* start(const Jobs& jobs, Cta& c) {
     const LinPass& p = args->p;
     c.sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                       ~(uintptr_t)1023);
-    c.lam = reinterpret_cast<float*>(c.sm + SM_TAB);
-    c.lamk = c.lam + 132;
-    c.wtab = c.lamk + 132;
-    c.b = reinterpret_cast<Bars*>(c.wtab + 128);
+    c.wtab = reinterpret_cast<float*>(c.sm + SM_TAB);
+    c.lam = c.wtab + C;
+    c.b = reinterpret_cast<Bars*>(c.lam + POWERS);
     c.h = blockIdx.x % H;
     c.rev = p.reverse != 0;
     int index = unit / jobs.n;
@@ -422,7 +425,6 @@ __device__ __forceinline__ void set_up(const Args& args, Cta& c, int issue, int 
     if (tid <= C) {
         const float a = lin::decay_pow(c.g, tid);
         c.lam[tid] = a;
-        c.lamk[tid] = a * p.kv_scale;
         if (p.reverse ? tid > 0 : tid < C) c.wtab[p.reverse ? tid - 1 : C - 1 - tid] = a * p.kv_scale;
     }
     __syncwarp();

@@ -15,6 +15,7 @@
 #include <cuda_bf16.h>
 #include <limits.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "kda_follow.cuh"
@@ -353,13 +354,14 @@ __global__ void __launch_bounds__(MAX_THREADS) block_norm_kernel(BlockNorm p) {
 // sums.  Rows too wide for that (stages = 0) are read into registers.
 // FULL: a row's threads cover the columns exactly, so that nothing needs a guard.
 // KEEP: every part is there (the norm over the row, both upstream gradients, dx), and
-// the three weights are in shared memory too, for the block's rows.  Beside
-// two blocks' rings of wide rows L1 is too small for them, and each row would
-// wait for L2: 4,096 rows of 4,096 in bf16 took 69 us without it, 59 with it, and 55
-// (4.9 TB/s, 72 % of a plain copy's) without the branches that absent parts need.
-// What is left is the chain of a row: two sums over it, each a barrier, with 16 warps
-// on an SM (128 registers a thread); the instructions alone would take 20 us.  64
-// registers and twice the warps spill, and take 74.
+// the three weights are in shared memory too, for the block's rows: no branches for absent
+// parts, and no row waits for weights that L1, beside the rings, is too small for.  Without
+// and with it, sigmoid gate, 4,096 rows (8,192 below 2,048 columns), us, bf16: 256 columns 30,
+// 30; 1,000 46, 40; 2,048 44, 37; 2,304 66, 46; 4,096 84, 60; 5,120 117, 78; 7,168 150, 100
+// (4.7 TB/s, 69 % of a plain copy's); 8,192, for which it has no room, 166.  fp32: 1,000 94,
+// 66; 2,304 100, 71; 4,096 161, 111.  What is left is the chain of a row: two sums over it,
+// each a barrier, with 16 warps at most on an SM (128 registers a thread); the instructions
+// alone would take 20 us at 4,096 columns.  64 registers and twice the warps spill.
 enum { Y = 0, GATE = 1, DXO = 2, X = 3, DH = 4, TENSORS = 5 };
 
 __device__ __forceinline__ void copy16(void* smem, const void* src) {
@@ -379,16 +381,13 @@ __device__ __forceinline__ void copies_done(int behind) {   // all but the last 
 }
 
 enum { NO_GATE = 0, SIGMOID = 1, SILU = 2 };
-constexpr int KEEP_THREADS = 256, KEEP_ROWS = 2;   // of a block that keeps the weights
 
 template <typename T, int VPT, int ACT, bool RING, bool FULL, bool KEEP = false>
 __global__ void __launch_bounds__(MAX_THREADS)
 block_norm_backward_kernel(BlockNorm p, int tile, int stages) {
     __shared__ float buf[SUMS];
-    // what the shape of a block that keeps the weights is
-    const int width = KEEP ? KEEP_THREADS : (int)blockDim.x, rows = KEEP ? KEEP_ROWS : (int)blockDim.y;
-    const int D = KEEP ? KEEP_THREADS * VPT * V : p.D, cols = KEEP ? D : tile;
-    const int depth = KEEP ? 2 : stages, warps = width >> 5;
+    const int width = blockDim.x, rows = blockDim.y, D = p.D, cols = KEEP ? D : tile;
+    const int depth = stages, warps = width >> 5;
     const int vec0 = KEEP ? (int)threadIdx.x : (int)(blockIdx.y * cols / V + threadIdx.x);
     const int vecs = KEEP ? D / V : min(D, ((int)blockIdx.y + 1) * cols) / V;
     const bool whole = KEEP || p.group == D, pre = KEEP || p.w_pre, pass_on = KEEP || p.dx;
@@ -720,10 +719,14 @@ Shape shape_of(int32_t D, bool coupled, int most) {
 
 constexpr int BACKWARD_THREADS = 256;
 constexpr size_t RING_HALF = 110 * 1024, RING_ALL = 220 * 1024;
+// What a block may have beside `buf`, alone on its SM and as one of two.
+constexpr size_t ROOM_ALL = 232448 - SUMS * sizeof(float), ROOM_HALF = 110 * 1024;
 
 // The backward's shape.  A ring of up to 3 rows in half of an SM's shared memory,
-// of 2 in all of it.  Two rows of 256 threads, each with its ring of 2, share a
-// block where that lets the weights stay beside them (4,096 columns of bf16).
+// of 2 in all of it.  With every part there the weights stay beside a ring of 2
+// wherever that has room (up to 7,168 columns of bf16, 4,096 of fp32), and two rows share a
+// block, and the weights, where an SM would hold one block of one row: bf16, 3,584 columns
+// 60 -> 55 us, 4,096 64 -> 60; not where it holds two, 2,048 37 -> 43.
 struct BackwardShape {
     Shape s;
     int stages;
@@ -735,16 +738,19 @@ BackwardShape backward_shape(int32_t D, bool coupled, bool all, int bytes) {
     BackwardShape b;
     b.s = shape_of(D, coupled, BACKWARD_THREADS);
     Shape& s = b.s;
-    const size_t row = (size_t)TENSORS * s.vpt * s.block.x * s.block.y * V * bytes;
+    const size_t one = (size_t)TENSORS * s.vpt * s.block.x * V * bytes, row = one * s.block.y;
     const size_t sums = (size_t)s.tile * sizeof(float);
     b.stages = 3 * row <= RING_HALF ? 3 : 2 * row <= RING_ALL ? 2 : 0;
     b.full = s.tiles * s.tile == D && s.tile == (int)s.block.x * s.vpt * V;
-    b.keep = all && bytes == 2 && b.full && s.tiles == 1 && s.vpt == 2 && s.block.x == KEEP_THREADS && b.stages == 2 &&
-             4 * row + 3 * sums <= RING_ALL;
     b.smem = b.stages * row > sums ? b.stages * row : sums;
+    b.keep = all && s.vpt <= 2 && 2 * row + 3 * sums <= ROOM_ALL;
     if (b.keep) {
-        s.block.y = KEEP_ROWS;
-        b.smem = 4 * row + 3 * sums;
+        b.stages = 2;
+        if (2 * row + 3 * sums > ROOM_HALF && s.block.y == 1 && 2 * s.block.x <= MAX_THREADS &&
+            4 * one + 3 * sums <= ROOM_ALL) {
+            s.block.y = 2;
+        }
+        b.smem = 2 * one * s.block.y + 3 * sums;
     }
     return b;
 }
@@ -773,9 +779,9 @@ cudaError_t forward(const BlockNorm& p, cudaStream_t stream) {
 
 // The backward's blocks along the rows: what keeps 152 SMs busy, fewer where
 // there are fewer rows.
-int parts_of(const Shape& s, int64_t rows) {
+int parts_of(const Shape& s, int64_t rows, size_t smem = 0) {
     const int threads = s.block.x * s.block.y;
-    const int most = 152 * (threads <= 128 ? 4 : threads <= 256 ? 2 : 1);
+    const int most = 152 * (smem > ROOM_HALF ? 1 : threads <= 128 ? 4 : threads <= 256 ? 2 : 1);
     const int64_t blocks = (rows + s.block.y - 1) / s.block.y;
     return (int)(blocks < most ? (blocks < 1 ? 1 : blocks) : most);
 }
@@ -785,7 +791,8 @@ cudaError_t backward(const BlockNorm& p, cudaStream_t stream) {
     const BackwardShape b = backward_shape(
         p.D, coupled(p), p.group == p.D && p.w_pre && p.dx_out && p.dx, sizeof(T));
     const Shape& s = b.s;
-    const int parts = b.keep ? parts_of(s, p.rows) : block_norm_parts(p.rows, p.D);
+    int parts = block_norm_parts(p.rows, p.D);
+    if (b.keep) parts = std::min(parts, parts_of(s, p.rows, b.smem));
     const dim3 grid(parts, s.tiles);
     cudaError_t err = cudaSuccess;
     auto launch = [&](auto kernel) {
@@ -798,10 +805,13 @@ cudaError_t backward(const BlockNorm& p, cudaStream_t stream) {
     };
     auto with_gate = [&](auto act) {
         constexpr int ACT = decltype(act)::value;
-        if constexpr (sizeof(T) == 2) {   // (fp32 rows that wide fill shared memory)
-            if (b.keep) return launch(block_norm_backward_kernel<T, 2, ACT, true, true, true>);
-        }
-        if (b.stages == 0) {
+        if (b.keep && s.vpt == 1) {
+            if (b.full) launch(block_norm_backward_kernel<T, 1, ACT, true, true, true>);
+            else launch(block_norm_backward_kernel<T, 1, ACT, true, false, true>);
+        } else if (b.keep) {
+            if (b.full) launch(block_norm_backward_kernel<T, 2, ACT, true, true, true>);
+            else launch(block_norm_backward_kernel<T, 2, ACT, true, false, true>);
+        } else if (b.stages == 0) {
             launch(block_norm_backward_kernel<T, 4, ACT, false, false>);
         } else if (s.vpt == 1) {
             if (b.full) launch(block_norm_backward_kernel<T, 1, ACT, true, true>);

@@ -1,6 +1,6 @@
-"""GPU parity of the block norm's backward over the widths at which its launch changes: rows
-past what a ring in shared memory holds, whose only dynamic shared memory is the room of the
-sums.  Bounds and references are test_gpu_block_norm's."""
+"""GPU parity of the block norms over the widths at which a launch changes: what a block keeps
+in shared memory, rows too wide for it, and the room of the sums.  Bounds and references are
+test_gpu_block_norm's."""
 import pytest
 import torch
 
@@ -24,4 +24,24 @@ AROUND_48K += [(2, 12288, 128, "sigmoid", True, True, True, dtype) for dtype in 
 
 @pytest.mark.parametrize("case", AROUND_48K, ids=case_id)
 def test_backward_of_rows_whose_sums_fill_48_kb(case):
+    B.test_backward(case)
+
+
+# Every part there: the weights stay in shared memory beside the ring while that has room, one
+# row a block or two (an SM would hold one block: 3,584 and 4,096 columns of bf16), with and
+# without columns to spare in the last vectors; past that they do not.  Some with more rows
+# than blocks, so that the ring goes round.
+KEPT = [(rows, D, 0, gate, True, True, True, BF)
+        for rows, D in ((9, 264), (1300, 1000), (700, 1024), (650, 2048), (5, 2304), (633, 2560),
+                        (5, 3584), (333, 4096), (4, 4096), (5, 4104), (161, 5000), (7, 5120),
+                        (313, 7168), (3, 7176), (3, 8192)) for gate in GATES]
+KEPT += [(rows, D, 0, gate, True, True, True, F)
+         for rows, D in ((9, 264), (650, 1024), (633, 1000), (311, 2304), (5, 2560), (155, 4096),
+                         (5, 4408), (5, 4416)) for gate in GATES]
+KEPT += [(160, 4096, 0, "silu", True, False, True, BF), (5, 7168, 0, "sigmoid", True, False, True, BF),
+         (333, 2304, 0, "none", True, False, True, F)]
+
+
+@pytest.mark.parametrize("case", KEPT, ids=case_id)
+def test_backward_with_every_part(case):
     B.test_backward(case)

@@ -45,3 +45,38 @@ KEPT += [(160, 4096, 0, "silu", True, False, True, BF), (5, 7168, 0, "sigmoid", 
 @pytest.mark.parametrize("case", KEPT, ids=case_id)
 def test_backward_with_every_part(case):
     B.test_backward(case)
+
+
+# Rows too wide for a ring, which are read into registers, and those whose two vectors a thread
+# take the form for four (fp32, 5,640 to 8,192 columns).
+WIDE = [(3, D, 0, gate, True, True, True, BF) for D in (11264, 11272, 16384) for gate in GATES]
+WIDE += [(3, D, 0, gate, True, True, True, F) for D in (5632, 5640, 7168, 8192, 8200, 16384)
+         for gate in GATES]
+WIDE += [(155, 7168, 0, "sigmoid", False, True, True, F), (155, 12288, 64, "silu", True, True, True, BF)]
+
+
+@pytest.mark.parametrize("case", WIDE, ids=case_id)
+def test_backward_of_wide_rows(case):
+    B.test_backward(case)
+
+
+# Parts left out: the same widths without the weights kept.
+PARTS = [(313, D, group, gate, residual, scale, pre, dtype)
+         for D, group in ((4096, 0), (7168, 0), (2048, 128))
+         for gate, residual, scale, pre in (("silu", False, True, True), ("none", True, True, False),
+                                            ("sigmoid", True, False, False))
+         for dtype in (F, BF)]
+
+
+@pytest.mark.parametrize("case", PARTS, ids=case_id)
+def test_backward_with_parts_left_out(case):
+    B.test_backward(case)
+
+
+FORWARD = [(3, D, 0, gate, True, True, True, dtype) for D in (7168, 8200, 16384)
+           for gate in GATES for dtype in (F, BF)]
+
+
+@pytest.mark.parametrize("case", FORWARD, ids=case_id)
+def test_forward_of_wide_rows(case):
+    B.test_forward(case)

@@ -485,7 +485,8 @@ KDA_API int kda_prefill_noalloc_status(void* stream);
  * [n][H][d_k][d_v] (the same pools, slots and kda_state_io serve them), d_k and
  * d_v in {32, 64, 128}, fp32 or bf16.  log_decay [H] is fp32 and a constant
  * of the layer (no gradient); it is normally negative, 0 keeps everything and
- * -infinity drops the state at every token.  q and k are taken as they are.
+ * -infinity is the factor 0, which drops a finite state at every token (0 times
+ * infinity or NaN is NaN).  q and k are taken as they are.
  *
  * kda_lin_prefill -- the recurrence over N packed sequences, in chunks.
  *
@@ -506,11 +507,12 @@ KDA_API int kda_prefill_noalloc_status(void* stream);
  * it is.
  *
  * bf16 with d_k = d_v = 128 runs on the tensor cores in chunks of 128 tokens;
- * o carries the rounding to bf16 of the products q.k and of the carried state
- * where they are multiplied (2^-9 each), the states keep fp32 sums.  Every other
- * size and type runs in fp32 arithmetic on the CUDA cores, in chunks of 32.  A
- * value that is not finite may reach the outputs of all tokens of its own chunk,
- * earlier ones among them; it never reaches another sequence.
+ * o carries the rounding to bf16 of the weighted products q.k and of the carried
+ * state where they are multiplied (up to 2^-8 of each), the states keep fp32 sums.
+ * Every other size and type runs in fp32 arithmetic on the CUDA cores, in chunks of
+ * 32.  A value that is not finite may reach the outputs of all tokens of its own
+ * chunk, earlier ones among them, and through the state those of later chunks, whatever
+ * the decay; it never reaches another sequence.
  * Errors (nothing is launched): as kda_prefill, and KDA_ERR_INVALID_ARG for an
  * output or the workspace on top of another buffer, and for a cu_seqlens_host of
  * unequal lengths without cu_seqlens.

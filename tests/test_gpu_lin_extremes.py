@@ -41,6 +41,33 @@ def check_backward(x, g, scale, tc):
                 1 if rows and tc else 0)
 
 
+@pytest.mark.parametrize("dtype,d", [(F, 64), (BF, 64), (BF, 128)])
+@pytest.mark.parametrize("decay", [0.0, -1e-9, -3.0, -40.0, -87.0, -1e30, float("-inf")])
+@pytest.mark.parametrize("lens", [[300, 17], [641, 0, 1]], ids=["two", "cut"])
+def test_gradients_at_extreme_decays(dtype, d, decay, lens):
+    x = R.make(lens, 2, d, d, dtype, seed=3, state=True, g=[decay, -0.1])
+    v = R.dev(x)
+    g = kda.kda_lin_backward(v["q"], v["k"], v["v"], v["log_decay"], v["dO"], v["S0"], v["cu"],
+                             x["cu"], v["dS"], scale=0.75)
+    check_backward(x, g, 0.75, L.tensor_core(d, d, dtype))
+
+
+@pytest.mark.parametrize("dtype,d", [(F, 64), (BF, 128)])
+def test_a_factor_of_zero_on_states_that_are_not_finite(dtype, d):
+    """log_decay of -infinity is the factor 0: finite states are dropped, and 0 times infinity is
+    NaN, as in the formula."""
+    x = R.make([1, 1], 1, d, d, dtype, seed=4, state=True, g=[float("-inf")])
+    x["S0"][1, 0, 3, 5] = float("inf")
+    v = R.dev(x)
+    args = (v["q"], v["k"], v["v"], v["log_decay"])
+    o, S = kda.kda_lin_prefill(*args, v["S0"], v["cu"], x["cu"])
+    pool = v["S0"].clone()
+    od = kda.kda_lin_decode_step(*args, pool)
+    for out, state in ((o, S), (od, pool)):
+        assert bool(torch.isfinite(state[0]).all()) and bool(torch.isnan(state[1, 0, 3, 5]))
+        assert bool(torch.isfinite(out[0]).all()) and bool(torch.isnan(out[1, 0, 5]))
+
+
 def one_sign(T, H, d=128):
     gen = torch.Generator(device="cuda").manual_seed(T + H)
     q, k, v = (torch.rand(T, H, d, generator=gen, device="cuda").add(0.5).to(BF)

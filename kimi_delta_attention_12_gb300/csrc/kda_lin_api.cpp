@@ -37,10 +37,14 @@ bool on_tensor_cores(int32_t d_k, int32_t d_v, kda_dtype dt, uint32_t flags, int
 
 // The tensor-core form works on a (sequence, head) pair of each of the `passes` it
 // runs at once with one CTA an SM; the CUDA-core form with one CTA for each 32
-// columns of dz, of which an SM takes two, and a few rounds of them even out
-// ragged lengths (with one round and a half a ragged fp32 backward took 368 us for
-// 329).  The three passes of a backward make three rounds of segments three times
-// as long (253 us, 259 with eight).
+// columns of dz, of which an SM takes two.  Its passes get segments for 8 CTAs an SM,
+// the three of a backward for 3 each.  With 1, 2, 3, 4, 8, 16 CTAs, us, prefill: 5
+// ragged sequences of 3,602 tokens, 8 heads, 64 x 128, fp32 186, 186, 122, 114, 106, 107;
+// 4,096 tokens, 8 heads, 128 x 128, fp32 293, 169, 197, 173, 167, 167; 16,384, 4 heads 537,
+// 285, 320, 326, 307, 325; 4,096, 32 heads, 64 x 64, bf16 430, 236, 243, 235, 221, 230.
+// Backward of the same: 386, 419, 231, 243, 235, 235; 453, 460, 422, 437, 443, 443; 1,025,
+// 812, 827, 842, 846, 868; 639, 605, 577, 590, 589, 617; 16 ragged sequences of 20,563
+// tokens, 16 heads, 64 x 64, bf16 885, 886, 885, 885, 1,005, 1,058.
 kda::LinCut cut_of(int32_t N, int32_t total_T, int32_t H, int32_t dz, int passes, bool tc) {
     return tc ? kda::lin_cut_tc(N, total_T, H, passes, sm_count())
               : kda::lin_cut(N, total_T, H, dz / 32, passes > 1 ? 3 : 8, sm_count());

@@ -631,10 +631,11 @@ __device__ __forceinline__ void issue_products(const LinPass& p, const Cta& c) {
 }
 
 // 32 columns of P, as bf16 pairs, column s weighted by 2^{g2 |t - s| + c}.  The
-// weights are formed on the spot, as 2^{base + slope s}: their error (2^-22 and
-// that of the exponent, at most 31 |g2| 2^-24) is far below the rounding to bf16
-// that follows, and a table in shared memory would wait for the products' own
-// reads of it.  MASKED: only columns first .. last of the block count.
+// weights are formed on the spot, as 2^{base + slope s}: a table in shared memory
+// would wait for the products' own reads of it.  Their error, 2^-22 and that of the
+// exponent (at most 31 |g2| 2^-24: 2^-20 for decays down to e^-0.35 a token, up to 2.4e-4, a
+// sixteenth of the bf16 rounding that follows, at the strongest that counts, g2 = -128), comes
+// before the rounding to bf16.  MASKED: only columns first .. last of the block count.
 template <bool MASKED>
 __device__ __forceinline__ void weigh(uint32_t col, float base, float slope, int first, int last) {
     uint32_t r[2][16], w[16];

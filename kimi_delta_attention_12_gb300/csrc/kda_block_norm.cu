@@ -819,7 +819,7 @@ cudaError_t backward(const BlockNorm& p, cudaStream_t stream) {
         } else if (s.vpt == 2) {
             if (b.full) launch(block_norm_backward_kernel<T, 2, ACT, true, true>);
             else launch(block_norm_backward_kernel<T, 2, ACT, true, false>);
-        } else {
+        } else if constexpr (sizeof(T) == 2) {   // (fp32 rows that wide have no ring)
             launch(block_norm_backward_kernel<T, 4, ACT, true, false>);
         }
     };

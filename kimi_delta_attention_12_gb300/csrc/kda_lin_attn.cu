@@ -13,12 +13,12 @@
 // starts from the state that a scan over the segments left for it.
 //
 // The products keep fp32 operands, so they are the CUDA cores'; what bounds them
-// is shared memory, which each multiply-add reads: 74 % of its cycles in the
-// outputs' pass, 62 % of the issue slots, 10 % of the memory's rate.  Chunks of 32
+// is shared memory, which each multiply-add reads: 78 % of its cycles in the
+// outputs' passes, 55 % of the issue slots, 7 % of the memory's rate.  Chunks of 32
 // keep a quarter of X Y^T in 16 registers a thread (4 x 4 tiles: 16 multiply-adds
 // for two 16-byte reads), and slices of 32 columns leave room for two CTAs an SM.
 // Backward of 3,602 tokens in 5 sequences, 8 heads, 64 x 128 wide, fp32: 226 us
-// (45 the segments' states, 8 the scan, 183 the outputs, each brought on while the
+// (45 the segments' states, 8 the scan, 178 the outputs, each brought on while the
 // one before ends); with one tile row a thread, longer segments and a launch for each
 // gradient it had taken 1,520.
 #include "kda_lin.h"

@@ -13,8 +13,8 @@
 // on a tensor core that otherwise waits for memory.
 //
 // What bounds it: the rows are read and written once (131 KB a chunk), and with
-// all SMs at work a chunk of 128 tokens takes 3.2 - 3.6 us an SM, 82 % of a plain copy's
-// rate on a ragged batch of 109,824 tokens and 64 heads (1,311 us).  A CTA alone on
+// all SMs at work a chunk of 128 tokens takes 3.2 - 3.6 us an SM, 79 - 83 % of a plain copy's
+// rate on a ragged batch of 109,824 tokens and 64 heads (1,305 - 1,372 us).  A CTA alone on
 // its memory still takes 2.95 us: the chain S -> X S -> state, and about 480 KB of
 // shared memory that the products and the copies move a chunk (1.85 us at 128
 // bytes a cycle).  The tensor core itself is busy for 42 %.  A fixed 10 us a CTA
@@ -22,9 +22,9 @@
 //
 // Few pairs of sequence and head leave SMs idle.  Then sequences are cut into
 // segments: one kernel forms the state that each segment adds (Y and Z alone, the
-// sums in TMEM from the first token to the last: 1.6 us a chunk), a scan carries them
+// sums in TMEM over four chunks at a time: 1.6 us a chunk), a scan carries them
 // on, and the pass starts each segment from its state.  One sequence of 4,096 tokens,
-// 32 heads: 64 us (about 21 states, 6 scan, 35 pass; each kernel is brought on
+// 32 heads: 65 us (about 22 states, 6 scan, 37 pass, one after another; each kernel is brought on
 // while the one before ends) where whole sequences took 108.
 //
 // Roles (28 warps): 0-7 turn P into P' and write the outputs (thread = token;

@@ -635,6 +635,203 @@ KDA_API int kda_block_norm_backward(const void* y, const float* w_post, const vo
 
 KDA_API size_t kda_block_norm_backward_workspace_bytes(int64_t rows, int32_t D, int32_t group);
 
+/*
+ * Softmax attention over a paged cache: the layers of a hybrid stack that stand
+ * between the recurrent ones, in serving.  One step of such a layer is
+ *
+ *     kda_cache_plan       blocks and slots for the step's tokens (once a step)
+ *     kda_rotary           positions into q and k
+ *     kda_cache_write      k and v into the cache, in 8 bits
+ *     kda_cache_attention  the new tokens' q over the cached k and v
+ *
+ * Tokens are packed as everywhere in this library; N requests, request i with
+ * new tokens cu_seqlens[i] .. cu_seqlens[i + 1) - 1.  Tensors with a `stride`
+ * argument are [rows, heads, d] with dense heads and rows `stride` elements apart
+ * (at least heads * d, a multiple of 16 bytes): parts of one wider projection need
+ * no copy.
+ *
+ * The cache is a pool of num_blocks blocks of `block` tokens (16, 32, 64 or 128):
+ * k_cache, v_cache [num_blocks, Hkv, block, d] e4m3 (1 sign, 4 exponent, 3 mantissa
+ * bits; 448 the largest, no infinities), k_scale, v_scale [num_blocks, Hkv] fp32:
+ * a value is its e4m3 number times the scale of its block and head.  Token p of a
+ * request lies in block block_table[i][p / block] at place p % block; its slot is
+ * block_table[i][p / block] * block + p % block.
+ */
+
+enum {
+    KDA_FLAG_ROTARY_INTERLEAVED = 32, /* kda_rotary: pairs are neighbouring channels */
+    KDA_FLAG_ROTARY_INVERSE = 64      /* kda_rotary: turn back (the backward) */
+};
+
+typedef enum {
+    KDA_ROTARY_PLAIN = 0,   /* f_j = base^(-2 j / rot) */
+    KDA_ROTARY_LINEAR = 1,  /* f_j / factor */
+    KDA_ROTARY_BY_PARTS = 2 /* f_j w_j + (1 - w_j) f_j / factor, where w_j goes linearly from 0
+                               to 1 as the turns that pair j makes in original_length tokens go
+                               from `slow` to `fast`; magnitude 0.1 ln(factor) + 1 (the
+                               published YaRN method) */
+} kda_rotary_scaling;
+
+/*
+ * kda_rotary_frequencies -- the angle per position of each pair, for a rotary part
+ * of `rot` channels, and the factor on the turned pairs.  Host memory, fp64
+ * arithmetic, results rounded to fp32.
+ *
+ *  rot        even, 2 .. 65536;  base > 0;  factor > 0 (1 = as trained; unused with
+ *             KDA_ROTARY_PLAIN)
+ *  original_length, fast, slow   KDA_ROTARY_BY_PARTS only: > 0, fast > slow > 0
+ *  inv_freq   [rot / 2] fp32, written;  magnitude: one fp32, written
+ * KDA_ERR_INVALID_ARG for anything else.
+ */
+KDA_API int kda_rotary_frequencies(int32_t rot, double base, kda_rotary_scaling scaling,
+                                   double factor, double original_length, double fast,
+                                   double slow, float* inv_freq, float* magnitude);
+
+/*
+ * kda_rotary -- rotary positions: with the angle a = positions[t] * inv_freq[j],
+ * pair j (u, w) of the channels first .. first + rot - 1 of every head becomes
+ *
+ *     magnitude * (u cos a - w sin a,  u sin a + w cos a)
+ *
+ * The pair is (x[first + j], x[first + j + rot / 2]), or with
+ * KDA_FLAG_ROTARY_INTERLEAVED (x[first + 2 j], x[first + 2 j + 1]).  The other
+ * channels are copied.  With KDA_FLAG_ROTARY_INVERSE the angle is -a: given the
+ * gradients of the outputs in place of q and k, that is the backward.
+ *
+ *  q          [T, Hq, d] dt with q_stride;  k [T, Hk, d] dt with k_stride, or NULL
+ *             (Hk = 0)
+ *  positions  [T] int32;  inv_freq [rot / 2] fp32 (magnitudes below 2^20)
+ *  d          a multiple of 8, at most 512;  rot a multiple of 16;  first a multiple
+ *             of 8;  first + rot <= d
+ *  q_out, k_out  as q and k, with strides of their own; each may be q or k itself
+ *             with the same stride (in place) and overlap nothing otherwise.  Rows of
+ *             one wider buffer that share no byte do not overlap.
+ * All pointers 16-byte aligned (positions and inv_freq 4).  The angle is reduced
+ * exactly (positions times frequencies as 64-bit fractions of a turn), so that far
+ * positions are as exact as near ones; fp32 arithmetic, one rounding to dt.
+ * Errors (nothing is launched): KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED (dtype,
+ * d, rot, first), KDA_ERR_ALIGNMENT.
+ */
+KDA_API int kda_rotary(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                       const int32_t* positions, const float* inv_freq, int64_t T, int32_t Hq,
+                       int32_t Hk, int32_t d, int32_t rot, int32_t first, kda_dtype dt,
+                       uint32_t flags, float magnitude, void* q_out, int64_t q_out_stride,
+                       void* k_out, int64_t k_out_stride, void* stream);
+
+/* What kda_cache_plan says of a request. */
+enum {
+    KDA_PLAN_OK = 0,
+    KDA_PLAN_BAD_LENGTH = 1, /* past < 0 or new < -1 */
+    KDA_PLAN_TABLE = 2,      /* more blocks than the table is wide */
+    KDA_PLAN_BLOCKS = 3,     /* no free blocks left for it */
+    KDA_PLAN_ROWS = 4        /* its tokens end behind the last row */
+};
+
+/*
+ * kda_cache_plan -- a step's bookkeeping, from the requests' lengths: blocks are
+ * taken from a free list into the block table, and every new token gets its
+ * position and slot.  On the device throughout, so that a step can be captured.
+ *
+ *  past, new_tokens  [N] int32: tokens in the cache, and tokens to come.  new -1 ends
+ *             the request: its blocks go back to the free list, ahead of everything
+ *             the step takes.
+ *  block_table  [N, table_width] int32, in place: row i holds the blocks of its past
+ *             tokens; those for the new ones are written behind them
+ *  free_blocks  [free_capacity] int32, in place: a stack whose first n_free[0] entries
+ *             are free; blocks are taken from its end in the order of the requests,
+ *             returned ones put on it in that order (those beyond the capacity are lost)
+ *  n_free     [1] int32;  n_free_out [1] int32, may be n_free itself
+ *  block      16, 32, 64 or 128;  T: rows of the step's packed tensors (at least the
+ *             sum of the new tokens; a padded batch has more)
+ *  cu_seqlens [N + 1], context_lens [N] (tokens of request i after the step; 0 when it
+ *             ended or is not served), status [N] (KDA_PLAN_...): int32, written
+ *  positions, slots  [T] int32, written: a row behind the last token gets position 0 and
+ *             slot -1
+ * A request that is not served (status not 0) takes no blocks and its rows get slot -1;
+ * its row range stays.  When the free blocks do not suffice, the requests from the first
+ * that cannot be served on get none (one that needs no new block is still served).
+ * A value that free_blocks or block_table holds is passed on as it is; one that makes no
+ * slot in 32 bits gives slot -1.
+ * Errors (nothing is launched): KDA_ERR_INVALID_ARG for a missing buffer, N < 1, T < 0,
+ * table_width or free_capacity < 1, or an output on another buffer; KDA_ERR_UNSUPPORTED
+ * for another block; KDA_ERR_ALIGNMENT (4 bytes).
+ */
+KDA_API int kda_cache_plan(const int32_t* past, const int32_t* new_tokens, int32_t N,
+                           int32_t* block_table, int32_t table_width, int32_t* free_blocks,
+                           int32_t free_capacity, const int32_t* n_free, int32_t* n_free_out,
+                           int32_t block, int32_t T, int32_t* cu_seqlens, int32_t* context_lens,
+                           int32_t* positions, int32_t* slots, int32_t* status, void* stream);
+
+/*
+ * kda_cache_write -- new keys and values into their slots of the cache, in 8 bits.
+ *
+ *  k, v       [T, Hkv, d] dt with k_stride, v_stride;  slots [T] int32
+ *  k_cache, v_cache, k_scale, v_scale   the cache, updated in place; d 32, 64 or 128
+ *
+ * The tokens of one block that a call writes stand in consecutive rows with rising
+ * consecutive slots (a run; kda_cache_plan's slots do).  A run that begins at place 0
+ * opens its block: the scale becomes the smallest power of two, 2^-60 at least, under
+ * which the run's largest value is at most 448.  A run that begins further on finds
+ * earlier tokens ahead of it: the scale becomes the larger of that power and the old
+ * scale, and where it grows the earlier tokens are rounded again to the new one (exact
+ * for powers of two, but for values that fall below e4m3's 2^-6).  Places behind a run
+ * are left as they are.  Rounding is to the nearest, ties to even.  Infinities and NaN
+ * do not count for the scale; an infinity becomes the largest number, a NaN stays one.
+ * Rows whose slot is negative or behind the pool are left out.  Two runs in one block,
+ * or a slot that is given twice, leave that block's content and scale unspecified, and
+ * no other's.
+ * num_blocks * block is at most 2^31 - 1.  Pointers 16-byte aligned (slots, scales 4).
+ * Errors (nothing is launched): KDA_ERR_INVALID_ARG (missing or overlapping buffers,
+ * sizes, strides), KDA_ERR_UNSUPPORTED (dtype, d, block), KDA_ERR_ALIGNMENT.
+ */
+KDA_API int kda_cache_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                            const int32_t* slots, int32_t T, int32_t Hkv, int32_t d,
+                            kda_dtype dt, void* k_cache, void* v_cache, float* k_scale,
+                            float* v_scale, int32_t num_blocks, int32_t block, void* stream);
+
+/*
+ * kda_cache_attention -- softmax attention of each request's new tokens over its
+ * cached ones.  Request i has c = context_lens[i] cached tokens, the new ones (already
+ * written) its last; its new token j of n sees the keys 0 .. c - n + j:
+ *
+ *     o = sum_s e^{scale q.k_s} v_s / sum_s e^{scale q.k_s}
+ *
+ *  q          [T, Hq, d] dt with q_stride; Hq a multiple of Hkv, at most 64 of them to
+ *             one; head h reads the keys and values of head h / (Hq / Hkv);  d 32, 64, 128
+ *  k_cache, v_cache, k_scale, v_scale   the cache; scales positive, 2^-60 .. 2^60
+ *  block_table  [N, table_width] int32;  context_lens [N] int32
+ *  cu_seqlens  [N + 1] int32, or NULL: one new token for each request (T = N)
+ *  max_new    the most new tokens of a request, or more; it chooses the kernels, so one
+ *             that is too small costs time, not results
+ *  o          [T, Hq, d] dt, dense
+ *  workspace  kda_cache_attention_workspace_bytes(...) bytes, 256-byte aligned, no
+ *             initialisation needed
+ * A row that sees no key (c = 0, or more new tokens than c) becomes zero.  Rows behind
+ * the last request's are left as they were.  Entries of block_table outside the pool
+ * count as tokens that are not there; context_lens and cu_seqlens are clamped to the
+ * table and to T.  What the cache holds behind a request's last token is not read.  A
+ * NaN among the values of a request's new tokens may reach the rows of its other new
+ * tokens in the same call.
+ * fp32 q and o: products to 22 bits and more, sums in fp32.  bf16: the weights
+ * are rounded to 11 bits before they meet the values (e4m3 values are exact), sums in
+ * fp32, one rounding to bf16.  The same bits on every call on one kind of device.
+ * Errors (nothing is launched): as kda_cache_write, and KDA_ERR_WORKSPACE.
+ */
+KDA_API int kda_cache_attention(const void* q, int64_t q_stride, const void* k_cache,
+                                const void* v_cache, const float* k_scale, const float* v_scale,
+                                int32_t num_blocks, int32_t block, const int32_t* block_table,
+                                int32_t table_width, const int32_t* context_lens,
+                                const int32_t* cu_seqlens, int32_t N, int32_t T,
+                                int32_t max_new, int32_t Hq, int32_t Hkv, int32_t d, kda_dtype dt,
+                                float scale, void* o, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* kda_cache_attention_workspace_bytes -- the workspace kda_cache_attention needs on the
+ * current device: partial sums of the pieces into which the cached tokens are cut, a
+ * fixed size for given heads (0 for invalid sizes). */
+KDA_API size_t kda_cache_attention_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t d,
+                                                   kda_dtype dt);
+
 /* Human-readable name of a kda_status value (static storage). */
 KDA_API const char* kda_status_string(int status);
 

@@ -12,6 +12,9 @@ Entry points (same names as the C ABI):
   kda_lin_prefill, kda_lin_decode_step, kda_lin_backward
                                              linear attention with one decay per head
   kda_block_norm, kda_block_norm_backward    norms, gate and residual between two blocks
+  kda_rotary, kda_rotary_backward            rotary positions of q and k
+  kda_cache_plan, kda_cache_write, kda_cache_attention
+                                             softmax attention over a paged 8-bit cache
 """
 from __future__ import annotations
 
@@ -42,6 +45,8 @@ KDA_FLAG_RECURRENT = 2
 KDA_FLAG_SOFTPLUS_GATE = 4
 KDA_FLAG_CONV_SILU = 8
 KDA_FLAG_SHORT_PEER_WAITS = 16
+KDA_FLAG_ROTARY_INTERLEAVED = 32
+KDA_FLAG_ROTARY_INVERSE = 64
 
 KDA_STATE_ZERO = 0
 KDA_STATE_COPY = 1
@@ -59,11 +64,25 @@ EXPORTED_SYMBOLS = (
     "kda_lin_prefill", "kda_lin_prefill_workspace_bytes", "kda_lin_decode_step",
     "kda_lin_backward", "kda_lin_backward_workspace_bytes",
     "kda_block_norm", "kda_block_norm_backward", "kda_block_norm_backward_workspace_bytes",
+    "kda_rotary", "kda_rotary_frequencies", "kda_cache_plan", "kda_cache_write",
+    "kda_cache_attention", "kda_cache_attention_workspace_bytes",
 )
 
 KDA_GATE_SIGMOID = 0
 KDA_GATE_SILU = 1
 _GATE_ACTS = {"sigmoid": KDA_GATE_SIGMOID, "silu": KDA_GATE_SILU}
+
+KDA_ROTARY_PLAIN = 0
+KDA_ROTARY_LINEAR = 1
+KDA_ROTARY_BY_PARTS = 2
+_ROTARY_SCALINGS = {None: KDA_ROTARY_PLAIN, "linear": KDA_ROTARY_LINEAR,
+                    "by_parts": KDA_ROTARY_BY_PARTS}
+
+KDA_PLAN_OK = 0
+KDA_PLAN_BAD_LENGTH = 1
+KDA_PLAN_TABLE = 2
+KDA_PLAN_BLOCKS = 3
+KDA_PLAN_ROWS = 4
 
 _lock = threading.Lock()
 _lib = None
@@ -163,6 +182,23 @@ def lib() -> ctypes.CDLL:
                                                   vp]
             L.kda_block_norm_backward_workspace_bytes.restype = sz
             L.kda_block_norm_backward_workspace_bytes.argtypes = [i64, i32, i32]
+            f64 = ctypes.c_double
+            L.kda_rotary_frequencies.restype = ctypes.c_int
+            L.kda_rotary_frequencies.argtypes = [i32, f64, ctypes.c_int, f64, f64, f64, f64, vp, vp]
+            L.kda_rotary.restype = ctypes.c_int
+            L.kda_rotary.argtypes = [vp, i64, vp, i64, vp, vp, i64, i32, i32, i32, i32, i32, dt,
+                                     u32, f32, vp, i64, vp, i64, vp]
+            L.kda_cache_plan.restype = ctypes.c_int
+            L.kda_cache_plan.argtypes = [vp, vp, i32, vp, i32, vp, i32, vp, vp, i32, i32, vp, vp,
+                                         vp, vp, vp, vp]
+            L.kda_cache_write.restype = ctypes.c_int
+            L.kda_cache_write.argtypes = [vp, i64, vp, i64, vp, i32, i32, i32, dt, vp, vp, vp, vp,
+                                          i32, i32, vp]
+            L.kda_cache_attention.restype = ctypes.c_int
+            L.kda_cache_attention.argtypes = [vp, i64, vp, vp, vp, vp, i32, i32, vp, i32, vp, vp,
+                                              i32, i32, i32, i32, i32, i32, dt, f32, vp, vp, sz, vp]
+            L.kda_cache_attention_workspace_bytes.restype = sz
+            L.kda_cache_attention_workspace_bytes.argtypes = [i32, i32, i32, dt]
             _lib = L
     return _lib
 
@@ -1006,3 +1042,281 @@ def kda_block_norm_backward(y: torch.Tensor, w_post: torch.Tensor,
     if st != KDA_OK:
         raise KDAError(st, "kda_block_norm_backward")
     return dict(dy=dy, dgate=dgate, dx=dx, dw_post=dw_post, dres_scale=dres, dw_pre=dw_pre)
+
+
+# ------------------------------------------------- rotary positions, paged cache
+def rotary_frequencies(rot: int, base: float = 10000.0, scaling: Optional[str] = None,
+                       factor: float = 1.0, original_length: float = 4096.0, fast: float = 32.0,
+                       slow: float = 1.0, device=None) -> Tuple[torch.Tensor, float]:
+    """(inv_freq [rot / 2] fp32, magnitude) for kda_rotary (kda_rotary_frequencies in
+    include/kda.h).  scaling: None, "linear" or "by_parts" (for contexts `factor` times as
+    long as the original_length trained on).  Formed on the host; keep them."""
+    if scaling not in _ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be None, 'linear' or 'by_parts', got {scaling!r}")
+    f = torch.empty(max(0, rot // 2), dtype=torch.float32)
+    m = ctypes.c_float()
+    st = lib().kda_rotary_frequencies(int(rot), float(base), _ROTARY_SCALINGS[scaling],
+                                      float(factor), float(original_length), float(fast),
+                                      float(slow), f.data_ptr() or None, ctypes.addressof(m))
+    if st != KDA_OK:
+        raise KDAError(st, "kda_rotary_frequencies")
+    return f.to(device or "cuda"), m.value
+
+
+def _row_stride(t: torch.Tensor, name: str, dev: int) -> int:
+    """Elements between the rows of a [rows, heads, d] tensor whose heads are dense."""
+    if t.get_device() != dev:
+        raise ValueError("KDA tensors must live on one CUDA device")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have shape [T, heads, d], got {tuple(t.shape)}")
+    rows, heads, d = t.shape
+    if t.is_contiguous():
+        return heads * d
+    st = t.stride()
+    if (d > 1 and st[2] != 1) or (heads > 1 and st[1] != d) or (rows > 1 and st[0] < heads * d):
+        raise ValueError(f"{name} must have dense heads, its rows not on top of each other")
+    return st[0] if rows > 1 else heads * d
+
+
+def _rotary_call(name, q, k, positions, inv_freq, interleaved, first, magnitude, q_out, k_out,
+                 stream, inverse):
+    batch = None
+    if q.dim() == 4:
+        batch = q.shape[:2]
+        if positions.shape != batch or (k is not None and (k.dim() != 4 or k.shape[:2] != batch)):
+            raise ValueError(f"k and positions must have q's leading shape {tuple(batch)}")
+        if any(t is not None and not t.is_contiguous() for t in (q, k, positions, q_out, k_out)):
+            raise ValueError("a 4-D batch must be contiguous")
+        q, k, q_out, k_out = (t if t is None else t.reshape(-1, *t.shape[2:])
+                              for t in (q, k, q_out, k_out))
+        positions = positions.reshape(-1)
+    dev = _one_device(positions, inv_freq)
+    qs = _row_stride(q, "q", dev)
+    T, Hq, d = q.shape
+    dt = q.dtype
+    code = _dtype_code(dt)
+    if positions.shape != (T,) or positions.dtype != torch.int32:
+        _expect(positions, (T,), "positions", torch.int32)
+    if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32:
+        raise ValueError("inv_freq must be a 1-D float32 tensor")
+    Hk, ks, kos = 0, 0, 0
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+    else:
+        ks = _row_stride(k, "k", dev)
+        Hk = k.shape[1]
+        if k.shape != (T, Hk, d) or k.dtype != dt:
+            _expect(k, (T, Hk, d), "k", dt)
+        if k_out is not None:
+            kos = _row_stride(k_out, "k_out", dev)
+            _expect(k_out, (T, Hk, d), "k_out", dt)
+    if q_out is not None:
+        qos = _row_stride(q_out, "q_out", dev)
+        _expect(q_out, (T, Hq, d), "q_out", dt)
+    on = _on(stream, dev)
+    if on is not None:
+        on.__enter__()
+    try:
+        if q_out is None:
+            q_out, qos = torch.empty((T, Hq, d), dtype=dt, device=q.device), Hq * d
+        if k is not None and k_out is None:
+            k_out, kos = torch.empty((T, Hk, d), dtype=dt, device=q.device), Hk * d
+        flags = ((KDA_FLAG_ROTARY_INTERLEAVED if interleaved else 0)
+                 | (KDA_FLAG_ROTARY_INVERSE if inverse else 0))
+        st = lib().kda_rotary(q.data_ptr(), qs, _addr(k), ks, positions.data_ptr(),
+                              inv_freq.data_ptr(), T, Hq, Hk, d, 2 * inv_freq.shape[0], first,
+                              code, flags, magnitude, q_out.data_ptr(), qos, _addr(k_out), kos,
+                              _raw_stream(dev))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
+    if st != KDA_OK:
+        raise KDAError(st, name)
+    if batch is not None:
+        q_out, k_out = (t if t is None else t.view(*batch, *t.shape[1:]) for t in (q_out, k_out))
+    return q_out, k_out
+
+
+def kda_rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
+               inv_freq: torch.Tensor, interleaved: bool = False, first: int = 0,
+               magnitude: float = 1.0, q_out: Optional[torch.Tensor] = None,
+               k_out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
+               ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Rotary positions (kda_rotary in include/kda.h): in every head of q [T, Hq, d] and k
+    [T, Hk, d] (or None) the pairs of the channels first .. first + 2 len(inv_freq) - 1 are
+    turned by positions[t] * inv_freq[j] and multiplied by magnitude.  Pairs lie half the
+    turned part apart, or side by side (interleaved=True).  q and k may be parts of a wider
+    projection (dense heads, rows any stride); q_out=q, k_out=k turns in place.  A contiguous
+    4-D batch [B, T, H, d] with positions [B, T] is accepted.  Returns (q_out, k_out)."""
+    return _rotary_call("kda_rotary", q, k, positions, inv_freq, interleaved, first, magnitude,
+                        q_out, k_out, stream, False)
+
+
+def kda_rotary_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], positions: torch.Tensor,
+                        inv_freq: torch.Tensor, interleaved: bool = False, first: int = 0,
+                        magnitude: float = 1.0, q_out: Optional[torch.Tensor] = None,
+                        k_out: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None
+                        ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Gradients of kda_rotary's q and k from those of its outputs: the pairs turned back.
+    Arguments as kda_rotary; q_out=dq, k_out=dk works in place.  Returns (dq, dk)."""
+    return _rotary_call("kda_rotary_backward", dq, dk, positions, inv_freq, interleaved, first,
+                        magnitude, q_out, k_out, stream, True)
+
+
+def _expect_i32(**ts):
+    for name, t in ts.items():
+        if t.dtype != torch.int32:
+            raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+
+
+def kda_cache_plan(past: torch.Tensor, new_tokens: torch.Tensor, block_table: torch.Tensor,
+                   free_blocks: torch.Tensor, n_free: torch.Tensor, block: int, rows: int,
+                   n_free_out: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """A step's bookkeeping on the GPU (kda_cache_plan in include/kda.h): past, new_tokens [N]
+    int32 (new -1 ends a request), block_table [N, W] and free_blocks [F] int32 updated in
+    place, n_free [1] int32 the free blocks in it, `rows` the rows of the step's packed tensors.
+    Returns a dict of int32 tensors: cu_seqlens [N + 1], context_lens, status [N], positions,
+    slots [rows], n_free [1] (n_free_out when given, which may be n_free itself)."""
+    dev = _one_device(past, new_tokens, block_table, free_blocks, n_free, n_free_out)
+    if past.dim() != 1 or past.shape[0] < 1 or block_table.dim() != 2 or free_blocks.dim() != 1:
+        raise ValueError("past must have shape [N], block_table [N, W] and free_blocks [F]")
+    N = past.shape[0]
+    _expect_i32(past=past, new_tokens=new_tokens, block_table=block_table,
+                free_blocks=free_blocks, n_free=n_free)
+    _expect(new_tokens, (N,), "new_tokens")
+    _expect(block_table, (N, block_table.shape[1]), "block_table")
+    _expect(n_free, (1,), "n_free")
+    _expect(n_free_out, (1,), "n_free_out", torch.int32)
+    rows = int(rows)
+    if rows < 0:
+        raise ValueError(f"rows must not be negative, got {rows}")
+    on = _on(stream, dev)
+    if on is not None:
+        on.__enter__()
+    try:
+        # one allocation: the parts of a step's plan live and die together
+        sizes = (N + 1, N, N, rows, rows) + (() if n_free_out is not None else (1,))
+        parts = torch.empty(sum(sizes), dtype=torch.int32, device=past.device).split(sizes)
+        cu, context, status, positions, slots = parts[:5]
+        left = parts[5] if n_free_out is None else n_free_out
+        st = lib().kda_cache_plan(
+            past.data_ptr(), new_tokens.data_ptr(), N, block_table.data_ptr(),
+            block_table.shape[1], free_blocks.data_ptr(), free_blocks.shape[0], n_free.data_ptr(),
+            left.data_ptr(), int(block), rows, cu.data_ptr(), context.data_ptr(),
+            positions.data_ptr(), slots.data_ptr(), status.data_ptr(), _raw_stream(dev))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
+    if st != KDA_OK:
+        raise KDAError(st, "kda_cache_plan")
+    return dict(cu_seqlens=cu, context_lens=context, positions=positions, slots=slots,
+                status=status, n_free=left)
+
+
+def _cache_sizes(k_cache, v_cache, k_scale, v_scale):
+    """(num_blocks, Hkv, block, d) of a cache, its shapes and types checked."""
+    if k_cache.dim() != 4 or k_cache.dtype != torch.float8_e4m3fn:
+        raise ValueError("k_cache must be a float8_e4m3fn [num_blocks, Hkv, block, d] tensor")
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        _expect(v_cache, k_cache.shape, "v_cache", torch.float8_e4m3fn)
+    nb, H, block, d = k_cache.shape
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t.shape != (nb, H) or t.dtype != torch.float32:
+            _expect(t, (nb, H), name, torch.float32)
+    return nb, H, block, d
+
+
+def kda_cache_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
+                    v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                    stream: Optional[torch.cuda.Stream] = None) -> None:
+    """New keys and values k, v [T, Hkv, d] (dense heads, rows any stride) into the slots [T]
+    int32 of a paged cache in 8 bits (kda_cache_write in include/kda.h): k_cache, v_cache
+    [num_blocks, Hkv, block, d] float8_e4m3fn, k_scale, v_scale [num_blocks, Hkv] fp32, all in
+    place."""
+    dev = _one_device(slots, k_cache, v_cache, k_scale, v_scale)
+    nb, H, block, d = _cache_sizes(k_cache, v_cache, k_scale, v_scale)
+    ks, vs = _row_stride(k, "k", dev), _row_stride(v, "v", dev)
+    T = k.shape[0]
+    code = _dtype_code(k.dtype)
+    for name, t in (("k", k), ("v", v)):
+        if t.shape != (T, H, d) or t.dtype != k.dtype:
+            _expect(t, (T, H, d), name, k.dtype)
+    _expect(slots, (T,), "slots", torch.int32)
+    on = _on(stream, dev)
+    if on is not None:
+        on.__enter__()
+    try:
+        st = lib().kda_cache_write(k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), T, H, d,
+                                   code, k_cache.data_ptr(), v_cache.data_ptr(),
+                                   k_scale.data_ptr(), v_scale.data_ptr(), nb, block,
+                                   _raw_stream(dev))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
+    if st != KDA_OK:
+        raise KDAError(st, "kda_cache_write")
+
+
+def cache_attention_workspace_bytes(Hq: int, Hkv: int, d: int, dtype: torch.dtype) -> int:
+    return int(lib().kda_cache_attention_workspace_bytes(Hq, Hkv, d, _dtype_code(dtype)))
+
+
+def kda_cache_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                        k_scale: torch.Tensor, v_scale: torch.Tensor, block_table: torch.Tensor,
+                        context_lens: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+                        max_new: Optional[int] = None, scale: Optional[float] = None,
+                        o: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Softmax attention of new tokens over a paged 8-bit cache (kda_cache_attention in
+    include/kda.h): q [T, Hq, d] (dense heads, rows any stride), the cache as kda_cache_write
+    fills it, block_table [N, W], context_lens [N] and cu_seqlens [N + 1] int32.  Without
+    cu_seqlens every request has one new token.  max_new: the most new tokens of a request
+    (default: T, or 1 without cu_seqlens); scale: d ** -0.5 by default.  Rows behind the last
+    request's are left as they were in o.  Returns o [T, Hq, d]."""
+    dev = _one_device(k_cache, v_cache, k_scale, v_scale, block_table, context_lens, cu_seqlens,
+                      o, workspace)
+    nb, H, block, d = _cache_sizes(k_cache, v_cache, k_scale, v_scale)
+    qs = _row_stride(q, "q", dev)
+    T, Hq = q.shape[:2]
+    if q.shape[2] != d:
+        _expect(q, (T, Hq, d), "q")
+    dt = q.dtype
+    code = _dtype_code(dt)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must have shape [N, W]")
+    N, W = block_table.shape
+    _expect_i32(block_table=block_table, context_lens=context_lens)
+    if context_lens.shape != (N,):
+        _expect(context_lens, (N,), "context_lens")
+    if cu_seqlens is None:
+        if T != N:
+            raise ValueError(f"without cu_seqlens q must have one row for each of {N} requests")
+        most = 1
+    else:
+        _expect(cu_seqlens, (N + 1,), "cu_seqlens", torch.int32)
+        most = T
+    _expect(o, (T, Hq, d), "o", dt)
+    on = _on(stream, dev)
+    if on is not None:
+        on.__enter__()
+    try:
+        if o is None:
+            o = torch.empty((T, Hq, d), dtype=dt, device=q.device)
+        if workspace is None:
+            workspace = _scratch(cache_attention_workspace_bytes(Hq, H, d, dt), q.device)
+        st = lib().kda_cache_attention(
+            q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), nb, block, block_table.data_ptr(), W, context_lens.data_ptr(),
+            _addr(cu_seqlens), N, T, most if max_new is None else int(max_new), Hq, H, d, code,
+            d ** -0.5 if scale is None else scale, o.data_ptr(), workspace.data_ptr(),
+            workspace.nbytes, _raw_stream(dev))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
+    if st != KDA_OK:
+        raise KDAError(st, "kda_cache_attention")
+    return o

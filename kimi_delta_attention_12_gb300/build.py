@@ -25,7 +25,9 @@ SOURCES = ["kda_api.cpp", "kda_recurrent.cu", "kda_state_io.cu", "kda_prefill_sm
            "kda_noalloc.cu", "kda_short_conv.cu",
            "kda_backward.cu", "kda_bwd_chunked.cu",
            "kda_lin_api.cpp", "kda_lin_attn.cu", "kda_lin_sm103.cu",
-           "kda_norm_api.cpp", "kda_block_norm.cu"]
+           "kda_norm_api.cpp", "kda_block_norm.cu",
+           "kda_cache_api.cpp", "kda_rotary.cu", "kda_cache_plan.cu", "kda_cache_write.cu",
+           "kda_cache_attn.cu"]
 
 
 def _nvcc() -> str:

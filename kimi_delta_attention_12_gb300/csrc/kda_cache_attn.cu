@@ -1,0 +1,653 @@
+// kda_cache_attn.cu -- softmax attention over the paged 8-bit cache (kda_cache_attention in
+// include/kda.h).
+//
+// Few rows meet many keys: a decode step reads every cached byte once, so HBM bounds it.  The
+// rows of one key and value head (its query heads times the new tokens) are tiles of 8 NT
+// columns, and the products stand with the cached tokens as the tensor core's 16 rows:
+//
+//     S^T = K Q^T        [16 tokens x 8 NT]      A = K, B = Q^T
+//     O^T += V^T P^T     [d x 8 NT]              A = V^T, B = P^T
+//
+// so that eight query rows fill an instruction.  The channels of a product may come in any
+// order as long as both sides agree, and the order taken makes every lane's part of a K row 16
+// neighbouring bytes: keys and values go from HBM into the registers they are multiplied
+// from, no shared memory between.  e4m3 numbers become fp16 exactly; q is scaled to [1, 2) by a power
+// of two per row (its exponent range is wider than fp16's), for fp32 split into two fp16
+// halves, and so are the weights P.  P^T needs the 8 x 8 transposes of S^T's tiles, one
+// instruction each (movmatrix).
+//
+// The value scale of a block goes into the exponent: with p' = 2^(s - m + 15) v_scale, m the
+// running maximum of s + log2 v_scale, P' is at most 2^15 whatever the scales, and the sum of
+// weights takes p' / v_scale.  The 2^15 is for fp16's range: weights down to 2^-29 of the largest
+// keep all their bits, and nothing above 2^-40 is lost, however many keys share it.
+//
+// Work is cut by tokens, not by requests: all (request, head, row tile) items in a row, each
+// ceil(tokens / 64) units, and every block takes the same stretch of units.  An item that lies
+// across blocks leaves partial sums, which a second kernel joins.  The 4 warps of a block take
+// 16 tokens of a unit each, with sums of their own that meet at the item's end.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kda_cache.h"
+#include "kda_e4m3.cuh"
+#include "kda_follow.cuh"
+#include "kda_seqlens.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kUnit = 16 * kWarps;       // tokens of a unit
+constexpr int kJoinThreads = 256;
+constexpr float kNone = -INFINITY;
+constexpr float kRaise = 15.0f;
+
+// Blocks that an SM holds at once, by the rows of a tile.
+__host__ __device__ constexpr int blocks_per_sm(int NT) { return NT == 1 ? 3 : 2; }
+
+struct Item {
+    int request, head, tile;
+    int64_t begin;            // where its units begin among all
+    int units, tiles;         // of the item; of its request and head
+    int tokens, fresh;        // cached, and new ones among them
+    int64_t row0;             // of the packed q
+};
+
+struct Span {
+    int64_t row0;
+    int tokens, fresh, tiles, units;
+    int64_t all;              // units of the request
+};
+
+__device__ __forceinline__ Span span_of(const CacheAttention& p, int i, int R) {
+    Span s;
+    int64_t bos, eos;
+    if (p.cu) {
+        clamped_seq(p.cu, i, p.N, p.T, bos, eos);
+    } else {
+        bos = i;
+        eos = i + 1;
+    }
+    // whole units of tokens stay within 32 bits
+    const int64_t table = (int64_t)p.width << p.block_log2;
+    const int64_t most = table < 0x7fff0000 ? table : 0x7fff0000;
+    const int64_t c = p.context[i];
+    s.row0 = bos;
+    s.fresh = (int)(eos - bos);
+    s.tokens = (int)(c < 0 ? 0 : (c < most ? c : most));
+    s.tiles = (int)(((int64_t)s.fresh * p.group + R - 1) / R);
+    s.units = s.tokens > 0 ? (int)(((int64_t)s.tokens + kUnit - 1) / kUnit) : 1;
+    s.all = (int64_t)s.tiles * p.heads * s.units;
+    return s;
+}
+
+// What each block takes: the units begin .. end - 1 of all, and the request that unit `begin`
+// belongs to.  All threads of the block; every thread gets the result.
+struct Stretch {
+    int64_t begin, end, per, first;     // first: where the request's units begin
+    int request;
+};
+
+template <int THREADS>
+__device__ __forceinline__ Stretch stretch_of(const CacheAttention& p, int R, int block,
+                                              int blocks) {
+    __shared__ int64_t sums[THREADS / 32 + 1];
+    __shared__ int64_t found_first;
+    __shared__ int found;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int k = (p.N + THREADS - 1) / THREADS;      // requests of a thread, neighbours
+    const int i0 = threadIdx.x * k, i1 = i0 + k < p.N ? i0 + k : p.N;
+    int64_t mine = 0;
+    for (int i = i0; i < i1; ++i) mine += span_of(p, i, R).all;
+    int64_t x = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) sums[w] = x;
+    if (threadIdx.x == 0) found = -1;
+    __syncthreads();
+    int64_t total = 0, before = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+        before += i < w ? sums[i] : 0;
+        total += sums[i];
+    }
+    Stretch s;
+    s.per = (total + blocks - 1) / blocks;
+    if (s.per < 1) s.per = 1;
+    s.begin = s.per * block;
+    s.end = s.begin + s.per < total ? s.begin + s.per : total;
+    int64_t at = before + x - mine;
+    if (s.begin < total && at <= s.begin && s.begin < at + mine) {
+        for (int i = i0; i < i1; ++i) {
+            const int64_t all = span_of(p, i, R).all;
+            if (s.begin < at + all) {
+                found = i;
+                found_first = at;
+                break;
+            }
+            at += all;
+        }
+    }
+    __syncthreads();
+    s.request = found;
+    s.first = found_first;
+    return s;
+}
+
+// The item of unit `at`, from request i on, whose units begin at `first`.
+__device__ __forceinline__ Item item_at(const CacheAttention& p, int R, int64_t at, int& i,
+                                        int64_t& first) {
+    Span s = span_of(p, i, R);
+    while (at >= first + s.all && i + 1 < p.N) {
+        first += s.all;
+        s = span_of(p, ++i, R);
+    }
+    Item t;
+    const int64_t n = (at - first) / s.units;
+    t.request = i;
+    t.head = (int)(n / s.tiles);
+    t.tile = (int)(n - (int64_t)t.head * s.tiles);
+    t.begin = first + n * s.units;
+    t.units = s.units;
+    t.tiles = s.tiles;
+    t.tokens = s.tokens;
+    t.fresh = s.fresh;
+    t.row0 = s.row0;
+    return t;
+}
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// What is left of lo and hi beside the fp16 pair h.
+__device__ __forceinline__ uint32_t rest_of(float lo, float hi, uint32_t h) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return half2_of(lo - f.x, hi - f.y);
+}
+
+__device__ __forceinline__ float exp2_of(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// The 16 tokens that a warp multiplies at once, as they lie in the cache.
+template <int D>
+struct Tokens {
+    static constexpr int kWords = D >= 64 ? D / 16 : 2;    // of a K row in a lane
+    static constexpr int vWords = D / 32;                  // of a V row in a lane
+    uint32_t k[2][kWords];
+    uint32_t v[4][vWords];
+};
+
+// The first channel of word s in a lane's part of a K row; c: the lane's place among four.
+template <int D>
+__device__ __forceinline__ int k_channel(int s, int c) {
+    return D >= 64 ? (s >> 2) * 64 + 16 * c + 4 * (s & 3) : 8 * c + 4 * s;
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t* to, const uint8_t* from) {
+    if (N == 4) {
+        const uint4 x = __ldcs(reinterpret_cast<const uint4*>(from));
+        to[0] = x.x; to[1] = x.y; to[2] = x.z; to[3] = x.w;
+    } else if (N == 2) {
+        const uint2 x = __ldcs(reinterpret_cast<const uint2*>(from));
+        to[0] = x.x; to[1] = x.y;
+    } else {
+        to[0] = __ldcs(reinterpret_cast<const uint32_t*>(from));
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void load_tokens(const CacheAttention& p, Tokens<D>& x, int head,
+                                            int block, int base, int limit, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+    const bool there = block >= 0 && block < p.num_blocks && base < limit;
+    const int64_t tile = ((int64_t)block * p.heads + head) << p.block_log2;
+    const int place = base & ((1 << p.block_log2) - 1);
+    const uint8_t* k = p.k_cache + (tile + place) * D;
+    const uint8_t* v = p.v_cache + (tile + place) * D;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int t = g + 8 * r;
+        const bool in = there && base + t < limit;
+        if (D >= 64) {
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+                if (in) {
+                    load_words<4>(&x.k[r][4 * j], k + t * D + 64 * j + 16 * c);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x.k[r][4 * j + i] = 0;
+                }
+            }
+        } else if (in) {
+            load_words<2>(&x.k[r][0], k + t * D + 8 * c);
+        } else {
+            x.k[r][0] = x.k[r][1] = 0;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int t = 2 * c + (r & 1) + 8 * (r >> 1);
+        if (there && base + t < limit) {
+            load_words<D / 32>(&x.v[r][0], v + t * D + g * (D / 8));
+        } else {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) x.v[r][i] = 0;
+        }
+    }
+}
+
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) cache_attention_kernel(
+    CacheAttention p) {
+    constexpr int R = 8 * NT, kSteps = D / 16, Q = F32 ? 2 : 1;
+    extern __shared__ float sums[];          // [kWarps][R][D], then m and l [kWarps][R] each
+    float* sums_m = sums + kWarps * R * D;
+    float* sums_l = sums_m + kWarps * R;
+    let_follow();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    const Stretch s = stretch_of<kThreads>(p, R, blockIdx.x, gridDim.x);
+    if (s.request < 0) return;
+    int request = s.request;
+    int64_t first = s.first;
+    const int heads_q = p.heads * p.group;
+    for (int64_t at = s.begin; at < s.end;) {
+        const Item it = item_at(p, R, at, request, first);
+        const int unit0 = (int)(at - it.begin);
+        const int units = (int)(s.end - at < it.units - unit0 ? s.end - at : it.units - unit0);
+        const int rows = it.fresh * p.group - it.tile * R;      // of this tile, may be above R
+        const int hidden = it.tokens - it.fresh + 1;            // keys that new token 0 sees
+        // ---- q of this lane's column, scaled to [1, 2) and in fp16
+        uint32_t q[Q][NT][kSteps][2];
+        float factor[NT][2];                 // of a score, for the columns 2 c and 2 c + 1
+        int limit[NT][2], low = 0x7fffffff, high = 0;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int n = 8 * t + g, flat = it.tile * R + n, j = flat / p.group;
+            float x[kSteps][4], top = 0.0f;
+            const int64_t base = (it.row0 + j) * p.q_stride +
+                                 (int64_t)(it.head * p.group + flat - j * p.group) * D;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int d = k_channel<D>(i, c);
+                if (n >= rows) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[i][e] = 0.0f;
+                } else if (F32) {
+                    const float4 f = *reinterpret_cast<const float4*>(
+                        static_cast<const float*>(p.q) + base + d);
+                    x[i][0] = f.x; x[i][1] = f.y; x[i][2] = f.z; x[i][3] = f.w;
+                } else {
+                    const uint2 f = *reinterpret_cast<const uint2*>(
+                        static_cast<const __nv_bfloat16*>(p.q) + base + d);
+                    x[i][0] = __uint_as_float(f.x << 16);
+                    x[i][1] = __uint_as_float(f.x & 0xffff0000u);
+                    x[i][2] = __uint_as_float(f.y << 16);
+                    x[i][3] = __uint_as_float(f.y & 0xffff0000u);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(x[i][e]));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            int e = __float_as_int(top) >> 23;
+            e = e < 1 ? 1 : (e > 253 ? 253 : e);
+            const float down = __int_as_float((254 - e) << 23), up = __int_as_float(e << 23);
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const float lo = x[i][2 * b] * down, hi = x[i][2 * b + 1] * down;
+                    q[0][t][i][b] = half2_of(lo, hi);
+                    if (F32) q[Q - 1][t][i][b] = rest_of(lo, hi, q[0][t][i][b]);
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int col = 2 * c + b;
+                factor[t][b] = __shfl_sync(0xffffffffu, up, 4 * col) *
+                               (p.scale * 1.44269504088896340736f);
+                const int nb = 8 * t + col, fb = it.tile * R + nb;
+                limit[t][b] = nb < rows ? hidden + fb / p.group : 0x7fffffff;
+            }
+        }
+        {
+            const int last = rows < R ? rows : R;
+            low = hidden + it.tile * R / p.group;
+            high = hidden + (it.tile * R + last - 1) / p.group;
+        }
+        // ---- this warp's part of the units
+        float o[NT][kSteps][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            m[t][0] = m[t][1] = kNone;
+            l[t][0] = l[t][1] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.0f;
+            }
+        }
+        const int32_t* table = p.table + (int64_t)it.request * p.width;
+        int ids = -1;                        // of the blocks of 32 units, one in each lane
+        float k_scale = 0.0f, v_scale = 1.0f;
+        auto look_up = [&](int u) {
+            const int base = (unit0 + u + lane) * kUnit + 16 * w;
+            ids = u + lane < units && base < high ? table[base >> p.block_log2] : -1;
+            k_scale = 0.0f;
+            v_scale = 1.0f;
+            if (ids >= 0 && ids < p.num_blocks) {
+                k_scale = p.k_scale[(int64_t)ids * p.heads + it.head];
+                v_scale = p.v_scale[(int64_t)ids * p.heads + it.head];
+            }
+        };
+        auto multiply = [&](const Tokens<D>& x, int u, float ks, float vs, bool there) {
+            const int base = (unit0 + u) * kUnit + 16 * w;
+            if (base >= high || !there) return;
+            float sc[NT][4];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const uint32_t a0 = half2_of_e4m3(x.k[0][i]), a1 = half2_of_e4m3(x.k[1][i]);
+                const uint32_t a2 = half2_of_e4m3_high(x.k[0][i]);
+                const uint32_t a3 = half2_of_e4m3_high(x.k[1][i]);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                    for (int h = 0; h < Q; ++h) {
+                        mma(sc[t], a0, a1, a2, a3, q[h][t][i][0], q[h][t][i][1]);
+                    }
+                }
+            }
+            const float lv = __log2f(vs), iv = __frcp_rn(vs);
+            const bool partly = base + 16 > low;
+            uint32_t b[Q][NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float f = factor[t][n] * ks;
+                    float s0 = fmaf(sc[t][n], f, lv), s1 = fmaf(sc[t][n + 2], f, lv);
+                    if (partly) {
+                        s0 = base + g < limit[t][n] ? s0 : kNone;
+                        s1 = base + g + 8 < limit[t][n] ? s1 : kNone;
+                    }
+                    sc[t][n] = s0;
+                    sc[t][n + 2] = s1;
+                }
+            }
+            float up[NT][2];
+            bool more = false;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    float x = fmaxf(sc[t][n], sc[t][n + 2]);
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                    up[t][n] = fmaxf(m[t][n], x);
+                    more |= up[t][n] > m[t][n];
+                }
+            }
+            if (__any_sync(0xffffffffu, more)) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    float less[2];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        less[n] = up[t][n] > m[t][n] ? exp2_of(m[t][n] - up[t][n]) : 1.0f;
+                        m[t][n] = up[t][n];
+                        l[t][n] *= less[n];
+                    }
+#pragma unroll
+                    for (int i = 0; i < kSteps; ++i) {
+                        o[t][i][0] *= less[0];
+                        o[t][i][1] *= less[1];
+                        o[t][i][2] *= less[0];
+                        o[t][i][3] *= less[1];
+                    }
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float e[4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float top = (m[t][n] == kNone ? 0.0f : m[t][n]) - kRaise;
+                    e[n] = exp2_of(sc[t][n] - top);
+                    e[n + 2] = exp2_of(sc[t][n + 2] - top);
+                    l[t][n] = fmaf(e[n] + e[n + 2], iv, l[t][n]);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t pair = half2_of(e[2 * h], e[2 * h + 1]);
+                    b[0][t][h] = transposed(pair);
+                    if (F32) {
+                        b[Q - 1][t][h] = transposed(rest_of(e[2 * h], e[2 * h + 1], pair));
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                // channels 2 i and 2 i + 1 of this lane's D / 8, of four tokens
+                uint32_t pair[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    pair[h] = __byte_perm(x.v[2 * h][i / 2], x.v[2 * h + 1][i / 2],
+                                          i & 1 ? 0x7362 : 0x5140);
+                }
+                const uint32_t a0 = half2_of_e4m3(pair[0]), a1 = half2_of_e4m3_high(pair[0]);
+                const uint32_t a2 = half2_of_e4m3(pair[1]), a3 = half2_of_e4m3_high(pair[1]);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                    for (int h = 0; h < Q; ++h) mma(o[t][i], a0, a1, a2, a3, b[h][t][0], b[h][t][1]);
+                }
+            }
+        };
+        for (int u0 = 0; u0 < units; u0 += 32) {
+            look_up(u0);
+            const int n = units - u0 < 32 ? units - u0 : 32;
+            Tokens<D> x, y;
+            auto load = [&](Tokens<D>& to, int u) {
+                load_tokens<D>(p, to, it.head, __shfl_sync(0xffffffffu, ids, u & 31),
+                               (unit0 + u0 + u) * kUnit + 16 * w, u < n ? high : 0, lane);
+            };
+            auto take = [&](const Tokens<D>& from, int u) {
+                const int id = __shfl_sync(0xffffffffu, ids, u);
+                const float ks = __shfl_sync(0xffffffffu, k_scale, u);
+                const float vs = __shfl_sync(0xffffffffu, v_scale, u);
+                multiply(from, u0 + u, ks, vs, id >= 0 && id < p.num_blocks);
+            };
+            load(x, 0);
+            load(y, 1);
+            for (int u = 0; u < n; u += 2) {
+                take(x, u);
+                load(x, u + 2);
+                if (u + 1 < n) take(y, u + 1);
+                load(y, u + 3);
+            }
+        }
+        // ---- the four warps' sums meet
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) {
+                    l[t][n] += __shfl_xor_sync(0xffffffffu, l[t][n], d);
+                }
+                const int col = 8 * t + 2 * c + n;
+                if (g == 0) {
+                    sums_m[w * R + col] = m[t][n];
+                    sums_l[w * R + col] = l[t][n];
+                }
+                float* to = sums + (w * R + col) * D + g * (D / 8);
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    to[2 * i] = o[t][i][n];
+                    to[2 * i + 1] = o[t][i][n + 2];
+                }
+            }
+        }
+        __syncthreads();
+        const int valid = rows < R ? rows : R;
+        const bool whole = unit0 == 0 && units == it.units;
+        float* part = p.partial + (int64_t)(blockIdx.x * 2 + (at != s.begin)) * R * (D + 2);
+        for (int i = threadIdx.x; i < valid * D; i += kThreads) {
+            const int n = i / D, d = i - n * D;
+            float top = kNone;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) top = fmaxf(top, sums_m[k * R + n]);
+            const float ref = top == kNone ? 0.0f : top;
+            float total = 0.0f, weight = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                const float f = exp2_of(sums_m[k * R + n] - ref);
+                total = fmaf(f, sums[(k * R + n) * D + d], total);
+                weight = fmaf(f, sums_l[k * R + n], weight);
+            }
+            if (whole) {
+                const int flat = it.tile * R + n, j = flat / p.group;
+                const int64_t to = ((it.row0 + j) * heads_q + it.head * p.group + flat -
+                                    j * p.group) * D + d;
+                const float y = weight == 0.0f ? 0.0f : total / weight;
+                if (F32) {
+                    static_cast<float*>(p.o)[to] = y;
+                } else {
+                    static_cast<__nv_bfloat16*>(p.o)[to] = __float2bfloat16_rn(y);
+                }
+            } else {
+                part[i] = total;
+                if (d == 0) {
+                    part[R * D + n] = top;
+                    part[R * D + R + n] = weight;
+                }
+            }
+        }
+        __syncthreads();
+        at += units;
+    }
+}
+
+// Joins the parts of the item that ends among block blockIdx.x's units and began before them.
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(CacheAttention p) {
+    constexpr int R = 8 * NT, kStride = R * (D + 2);
+    extern __shared__ float weights[];       // [R][blocks of the item]
+    __shared__ float total[R];
+    const Stretch s = stretch_of<kJoinThreads>(p, R, blockIdx.x, gridDim.x);
+    wait_before();
+    if (s.request < 0) return;
+    int request = s.request;
+    int64_t first = s.first;
+    const Item it = item_at(p, R, s.begin, request, first);
+    if (it.begin == s.begin || it.begin + it.units > s.end) return;
+    const int rows = it.fresh * p.group - it.tile * R, valid = rows < R ? rows : R;
+    const int b0 = (int)(it.begin / s.per), parts = blockIdx.x - b0 + 1;
+    auto part_of = [&](int k) {
+        const bool second = k == 0 && it.begin != b0 * s.per;
+        return p.partial + (int64_t)((b0 + k) * 2 + second) * kStride;
+    };
+    const int lane = threadIdx.x & 31;
+    for (int n = threadIdx.x >> 5; n < valid; n += kJoinThreads / 32) {
+        float top = kNone;
+        for (int k = lane; k < parts; k += 32) top = fmaxf(top, part_of(k)[R * D + n]);
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float ref = top == kNone ? 0.0f : top;
+        float sum = 0.0f;
+        for (int k = lane; k < parts; k += 32) {
+            const float* part = part_of(k) + R * D + n;
+            const float f = exp2_of(part[0] - ref);
+            weights[n * parts + k] = f;
+            sum = fmaf(f, part[R], sum);
+        }
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane == 0) total[n] = sum;
+    }
+    __syncthreads();
+    const int heads_q = p.heads * p.group;
+    for (int i = threadIdx.x; i < valid * D; i += kJoinThreads) {
+        const int n = i / D, d = i - n * D;
+        float y = 0.0f;
+#pragma unroll 8
+        for (int k = 0; k < parts; ++k) y = fmaf(weights[n * parts + k], part_of(k)[i], y);
+        y = total[n] == 0.0f ? 0.0f : y / total[n];
+        const int flat = it.tile * R + n, j = flat / p.group;
+        const int64_t to =
+            ((it.row0 + j) * heads_q + it.head * p.group + flat - j * p.group) * D + d;
+        if (F32) {
+            static_cast<float*>(p.o)[to] = y;
+        } else {
+            static_cast<__nv_bfloat16*>(p.o)[to] = __float2bfloat16_rn(y);
+        }
+    }
+}
+
+template <int D, int NT, bool F32>
+cudaError_t launch_tiles(const CacheAttention& p, int sms, cudaStream_t stream) {
+    constexpr int R = 8 * NT;
+    const size_t smem = (size_t)kWarps * R * (D + 2) * sizeof(float);
+    const int blocks = sms * blocks_per_sm(NT);
+    cache_attention_kernel<D, NT, F32><<<blocks, kThreads, smem, stream>>>(p);
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    return launch_follower(cache_attention_join_kernel<D, NT, F32>, dim3(blocks),
+                           dim3(kJoinThreads), (size_t)R * blocks * sizeof(float), stream, p);
+}
+
+template <int D, bool F32>
+cudaError_t launch_dim(const CacheAttention& p, int sms, cudaStream_t stream) {
+    // one column tile where the rows of every request fit it, else two: half the reads of K and V
+    return (int64_t)p.group * p.max_new <= 8 ? launch_tiles<D, 1, F32>(p, sms, stream)
+                                             : launch_tiles<D, 2, F32>(p, sms, stream);
+}
+
+template <bool F32>
+cudaError_t launch_typed(const CacheAttention& p, int sms, cudaStream_t stream) {
+    switch (p.d) {
+        case 32: return launch_dim<32, F32>(p, sms, stream);
+        case 64: return launch_dim<64, F32>(p, sms, stream);
+        default: return launch_dim<128, F32>(p, sms, stream);
+    }
+}
+
+}  // namespace
+
+size_t cache_attention_room(int32_t, int32_t d, int sms) {
+    const int most = blocks_per_sm(1) * 8 > blocks_per_sm(2) * 16 ? blocks_per_sm(1) * 8
+                                                                  : blocks_per_sm(2) * 16;
+    return (size_t)sms * most * 2 * (d + 2) * sizeof(float);
+}
+
+cudaError_t launch_cache_attention(const CacheAttention& p, int dtype, int sms,
+                                   cudaStream_t stream) {
+    return dtype == 0 ? launch_typed<true>(p, sms, stream) : launch_typed<false>(p, sms, stream);
+}
+
+}  // namespace kda

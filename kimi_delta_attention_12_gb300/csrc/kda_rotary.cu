@@ -1,0 +1,221 @@
+// kda_rotary.cu -- rotary positions of q and k, forward and backward (kda_rotary in
+// include/kda.h): pair (u, w) becomes magnitude (u cos a - w sin a, u sin a + w cos a) with
+// a = position * inv_freq.
+//
+// The angle.  Only its fraction of a turn matters, so the frequency is held as a 64-bit
+// fraction F = f / (2 pi) mod 1 and the phase is the wrapping integer product p F: exact to
+// 2^-41 of a turn at a position of 2^23, where an fp32 product of the two would have lost
+// the angle altogether.  F comes from the 24 mantissa bits of f and the first 64 bits of
+// 1 / (2 pi) by one integer product and a shift, no 64-bit floating point.  The upper 32 bits
+// of the phase become half turns in [-1, 1) for sincospif.
+//
+// Bound by HBM: every value is read and written once, three operations each.  A block takes a
+// stretch of (token, head) rows, forms the cosines and sines of its few tokens once in shared
+// memory (all heads of a token share them) while its first rows are on their way, and turns
+// 16-byte vectors: a vector of neighbouring channels, or two that lie rot / 2 apart.
+#include <cuda_bf16.h>
+
+#include "kda_cache.h"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnits = 4;        // vectors (or pairs of them) of a thread that are in flight
+
+// f / (2 pi) as a 64-bit fraction of a turn, whole turns dropped.
+__device__ __forceinline__ uint64_t turns_of(float f) {
+    // 1 / (2 pi) = 0.28BE60DB 9391054A ... in base 16: the binary digits of 0.159154943...
+    constexpr uint64_t kInvTwoPi = 0x28BE60DB9391054Aull;
+    const uint32_t bits = __float_as_uint(f);
+    const int e = (bits >> 23) & 255;
+    const uint64_t m = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
+    // f = m 2^-s: the product m * kInvTwoPi (88 bits) shifted right by s
+    const int s = 150 - (e ? e : 1);
+    const uint64_t lo = m * kInvTwoPi, hi = __umul64hi(m, kInvTwoPi);
+    uint64_t F;
+    if (s <= -64) {
+        F = 0;
+    } else if (s < 0) {
+        F = lo << -s;
+    } else if (s == 0) {
+        F = lo;
+    } else if (s < 64) {
+        F = (hi << (64 - s)) | (lo >> s);
+    } else {
+        F = s < 128 ? hi >> (s - 64) : 0;
+    }
+    return (bits >> 31) ? 0 - F : F;
+}
+
+// cos and sin of the angle, times the magnitude.
+__device__ __forceinline__ float2 turn(int32_t position, float f, float magnitude, bool inverse) {
+    const uint64_t phase = (uint64_t)(int64_t)position * turns_of(f);
+    float sn, cs;
+    sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &sn, &cs);
+    return make_float2(cs * magnitude, (inverse ? -sn : sn) * magnitude);
+}
+
+template <bool BF16>
+struct Vec {
+    static constexpr int n = BF16 ? 8 : 4;
+    uint4 raw;
+    __device__ __forceinline__ void get(float* x) const {
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (BF16) {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            } else {
+                x[i] = __uint_as_float(w[i]);
+            }
+        }
+    }
+    __device__ __forceinline__ void put(const float* x) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (BF16) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&b);
+            } else {
+                w[i] = __float_as_uint(x[i]);
+            }
+        }
+        raw = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// Rows of a call in order: token, then the heads of q, then those of k.  A row is cut into
+// `units`: the turned vectors (or pairs of vectors), then the ones that are copied.
+template <bool BF16, bool INTER>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(Rotary p, int rows_per_block, int units,
+                                                          int turned) {
+    using V = Vec<BF16>;
+    constexpr int n = V::n;
+    extern __shared__ float2 table[];        // [tokens of this block][rot / 2]
+    const int heads = p.heads[0] + p.heads[1], half = p.rot / 2;
+    const int64_t total = p.T * heads, row0 = (int64_t)blockIdx.x * rows_per_block;
+    const int rows = (int)(total - row0 < rows_per_block ? total - row0 : rows_per_block);
+    const int64_t t0 = row0 / heads;
+    const int head0 = (int)(row0 - t0 * heads);
+    const int tokens = (head0 + rows - 1) / heads + 1;
+
+    struct Unit {
+        char* to;
+        const char* from;
+        const float2* angles;
+        int far;                             // bytes to the second vector of a pair; 0: copy
+        V a, b;
+    };
+    constexpr int size = BF16 ? 2 : 4;
+    auto load = [&](int u, Unit& x) {
+        const int row = u / units, in_row = u - row * units;
+        const int flat = head0 + row, dt = flat / heads;
+        int h = flat - dt * heads;
+        const int which = h >= p.heads[0];
+        h -= which ? p.heads[0] : 0;
+        int c;                               // the unit's first channel
+        if (in_row < turned) {
+            c = p.first + in_row * n;
+            x.far = INTER ? size : half * size;
+            x.angles = table + dt * half + (INTER ? in_row * n / 2 : in_row * n);
+        } else {
+            c = (in_row - turned) * n;
+            c += c >= p.first ? p.rot : 0;
+            x.far = 0;
+        }
+        const int64_t col = (int64_t)h * p.d + c;
+        const int64_t t = t0 + dt;
+        x.from = static_cast<const char*>(which ? p.x[1] : p.x[0]) +
+                 (t * (which ? p.stride[1] : p.stride[0]) + col) * size;
+        x.to = static_cast<char*>(which ? p.out[1] : p.out[0]) +
+               (t * (which ? p.out_stride[1] : p.out_stride[0]) + col) * size;
+        x.a.raw = __ldcs(reinterpret_cast<const uint4*>(x.from));
+        if (!INTER && x.far) x.b.raw = __ldcs(reinterpret_cast<const uint4*>(x.from + x.far));
+    };
+    auto finish = [&](Unit& x) {
+        if (x.far) {
+            float u[n], w[n];
+            x.a.get(u);
+            if (INTER) {
+#pragma unroll
+                for (int i = 0; i < n / 2; ++i) {
+                    const float2 cs = x.angles[i];
+                    w[2 * i] = u[2 * i] * cs.x - u[2 * i + 1] * cs.y;
+                    w[2 * i + 1] = u[2 * i] * cs.y + u[2 * i + 1] * cs.x;
+                }
+                x.a.put(w);
+            } else {
+                x.b.get(w);
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    const float2 cs = x.angles[i];
+                    const float y = u[i] * cs.x - w[i] * cs.y;
+                    w[i] = u[i] * cs.y + w[i] * cs.x;
+                    u[i] = y;
+                }
+                x.a.put(u);
+                x.b.put(w);
+                __stcs(reinterpret_cast<uint4*>(x.to + x.far), x.b.raw);
+            }
+        }
+        __stcs(reinterpret_cast<uint4*>(x.to), x.a.raw);
+    };
+
+    const int count = rows * units;
+    Unit x[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        const int u = threadIdx.x + i * kThreads;
+        if (u < count) load(u, x[i]);
+    }
+    for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
+        const int dt = i / half, j = i - dt * half;
+        table[i] = turn(p.positions[t0 + dt], p.inv_freq[j], p.magnitude, p.inverse);
+    }
+    __syncthreads();
+    for (int base = threadIdx.x; base < count; base += kUnits * kThreads) {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            if (base + i * kThreads < count) finish(x[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int u = base + (kUnits + i) * kThreads;
+            if (u < count) load(u, x[i]);
+        }
+    }
+}
+
+template <bool BF16>
+cudaError_t launch_typed(const Rotary& p, cudaStream_t stream) {
+    constexpr int n = BF16 ? 8 : 4;
+    // in place the channels that are not turned need no pass
+    bool copy = false;
+    for (int i = 0; i < 2; ++i) copy |= p.heads[i] > 0 && p.out[i] != p.x[i];
+    const int turned = p.rot / n / (p.interleaved ? 1 : 2);
+    const int units = turned + (copy ? (p.d - p.rot) / n : 0);
+    const int64_t heads = p.heads[0] + p.heads[1], total = p.T * heads;
+    int rows = (2 * kUnits * kThreads + units - 1) / units;
+    const int64_t half = p.rot / 2;
+    // the table of a block's tokens stays within 32 KB
+    const int64_t most = (32768 / (half * 8) - 1) * heads;
+    if (rows > most) rows = most < 1 ? 1 : (int)most;
+    const int64_t tokens = (rows + heads - 2) / heads + 1;
+    const int64_t blocks = (total + rows - 1) / rows;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    const size_t smem = (size_t)(tokens * half) * sizeof(float2);
+    auto kernel = p.interleaved ? rotary_kernel<BF16, true> : rotary_kernel<BF16, false>;
+    kernel<<<(unsigned)blocks, kThreads, smem, stream>>>(p, rows, units, turned);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(const Rotary& p, int dtype, cudaStream_t stream) {
+    return dtype == 0 ? launch_typed<false>(p, stream) : launch_typed<true>(p, stream);
+}
+
+}  // namespace kda

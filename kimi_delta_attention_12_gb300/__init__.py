@@ -1099,29 +1099,29 @@ def _rotary_call(name, q, k, positions, inv_freq, interleaved, first, magnitude,
         _expect(positions, (T,), "positions", torch.int32)
     if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32:
         raise ValueError("inv_freq must be a 1-D float32 tensor")
-    Hk, ks, kos = 0, 0, 0
-    if k is None:
-        if k_out is not None:
-            raise ValueError("k_out without k")
-    else:
+    Hk, ks, qos, kos = 0, 0, Hq * d, 0
+    if k is not None:
         ks = _row_stride(k, "k", dev)
         Hk = k.shape[1]
-        if k.shape != (T, Hk, d) or k.dtype != dt:
+        kos = Hk * d
+        if k.dtype != dt or k.shape != (T, Hk, d):
             _expect(k, (T, Hk, d), "k", dt)
-        if k_out is not None:
-            kos = _row_stride(k_out, "k_out", dev)
-            _expect(k_out, (T, Hk, d), "k_out", dt)
     if q_out is not None:
         qos = _row_stride(q_out, "q_out", dev)
         _expect(q_out, (T, Hq, d), "q_out", dt)
+    if k_out is not None:
+        if k is None:
+            raise ValueError("k_out without k")
+        kos = _row_stride(k_out, "k_out", dev)
+        _expect(k_out, (T, Hk, d), "k_out", dt)
     on = _on(stream, dev)
     if on is not None:
         on.__enter__()
     try:
         if q_out is None:
-            q_out, qos = torch.empty((T, Hq, d), dtype=dt, device=q.device), Hq * d
+            q_out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
         if k is not None and k_out is None:
-            k_out, kos = torch.empty((T, Hk, d), dtype=dt, device=q.device), Hk * d
+            k_out = torch.empty((T, Hk, d), dtype=dt, device=q.device)
         flags = ((KDA_FLAG_ROTARY_INTERLEAVED if interleaved else 0)
                  | (KDA_FLAG_ROTARY_INVERSE if inverse else 0))
         st = lib().kda_rotary(q.data_ptr(), qs, _addr(k), ks, positions.data_ptr(),
@@ -1165,12 +1165,6 @@ def kda_rotary_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], positions:
                         magnitude, q_out, k_out, stream, True)
 
 
-def _expect_i32(**ts):
-    for name, t in ts.items():
-        if t.dtype != torch.int32:
-            raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
-
-
 def kda_cache_plan(past: torch.Tensor, new_tokens: torch.Tensor, block_table: torch.Tensor,
                    free_blocks: torch.Tensor, n_free: torch.Tensor, block: int, rows: int,
                    n_free_out: Optional[torch.Tensor] = None,
@@ -1181,16 +1175,16 @@ def kda_cache_plan(past: torch.Tensor, new_tokens: torch.Tensor, block_table: to
     Returns a dict of int32 tensors: cu_seqlens [N + 1], context_lens, status [N], positions,
     slots [rows], n_free [1] (n_free_out when given, which may be n_free itself)."""
     dev = _one_device(past, new_tokens, block_table, free_blocks, n_free, n_free_out)
-    if past.dim() != 1 or past.shape[0] < 1 or block_table.dim() != 2 or free_blocks.dim() != 1:
-        raise ValueError("past must have shape [N], block_table [N, W] and free_blocks [F]")
-    N = past.shape[0]
-    _expect_i32(past=past, new_tokens=new_tokens, block_table=block_table,
-                free_blocks=free_blocks, n_free=n_free)
-    _expect(new_tokens, (N,), "new_tokens")
-    _expect(block_table, (N, block_table.shape[1]), "block_table")
-    _expect(n_free, (1,), "n_free")
-    _expect(n_free_out, (1,), "n_free_out", torch.int32)
-    rows = int(rows)
+    N = past.shape[0] if past.dim() == 1 else 0
+    i32 = torch.int32
+    if (N < 1 or block_table.dim() != 2 or free_blocks.dim() != 1 or past.dtype != i32
+            or new_tokens.dtype != i32 or block_table.dtype != i32 or free_blocks.dtype != i32
+            or n_free.dtype != i32 or new_tokens.shape != (N,) or block_table.shape[0] != N
+            or n_free.shape != (1,)):
+        raise ValueError("past and new_tokens must be int32 [N], block_table int32 [N, W], "
+                         "free_blocks int32 [F] and n_free int32 [1]")
+    if n_free_out is not None:
+        _expect(n_free_out, (1,), "n_free_out", i32)
     if rows < 0:
         raise ValueError(f"rows must not be negative, got {rows}")
     on = _on(stream, dev)
@@ -1198,14 +1192,14 @@ def kda_cache_plan(past: torch.Tensor, new_tokens: torch.Tensor, block_table: to
         on.__enter__()
     try:
         # one allocation: the parts of a step's plan live and die together
-        sizes = (N + 1, N, N, rows, rows) + (() if n_free_out is not None else (1,))
-        parts = torch.empty(sum(sizes), dtype=torch.int32, device=past.device).split(sizes)
+        parts = torch.empty(3 * N + 2 + 2 * rows, dtype=i32, device=past.device)
+        parts = parts.split_with_sizes((N + 1, N, N, rows, rows, 1))
         cu, context, status, positions, slots = parts[:5]
         left = parts[5] if n_free_out is None else n_free_out
         st = lib().kda_cache_plan(
             past.data_ptr(), new_tokens.data_ptr(), N, block_table.data_ptr(),
             block_table.shape[1], free_blocks.data_ptr(), free_blocks.shape[0], n_free.data_ptr(),
-            left.data_ptr(), int(block), rows, cu.data_ptr(), context.data_ptr(),
+            left.data_ptr(), block, rows, cu.data_ptr(), context.data_ptr(),
             positions.data_ptr(), slots.data_ptr(), status.data_ptr(), _raw_stream(dev))
     finally:
         if on is not None:
@@ -1244,7 +1238,8 @@ def kda_cache_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cac
     for name, t in (("k", k), ("v", v)):
         if t.shape != (T, H, d) or t.dtype != k.dtype:
             _expect(t, (T, H, d), name, k.dtype)
-    _expect(slots, (T,), "slots", torch.int32)
+    if slots.shape != (T,) or slots.dtype != torch.int32:
+        _expect(slots, (T,), "slots", torch.int32)
     on = _on(stream, dev)
     if on is not None:
         on.__enter__()
@@ -1281,25 +1276,28 @@ def kda_cache_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
                       o, workspace)
     nb, H, block, d = _cache_sizes(k_cache, v_cache, k_scale, v_scale)
     qs = _row_stride(q, "q", dev)
-    T, Hq = q.shape[:2]
-    if q.shape[2] != d:
+    T, Hq, dq = q.shape
+    if dq != d:
         _expect(q, (T, Hq, d), "q")
     dt = q.dtype
     code = _dtype_code(dt)
     if block_table.dim() != 2:
         raise ValueError("block_table must have shape [N, W]")
     N, W = block_table.shape
-    _expect_i32(block_table=block_table, context_lens=context_lens)
-    if context_lens.shape != (N,):
-        _expect(context_lens, (N,), "context_lens")
+    if block_table.dtype != torch.int32:
+        raise TypeError(f"block_table must be torch.int32, got {block_table.dtype}")
+    if context_lens.shape != (N,) or context_lens.dtype != torch.int32:
+        _expect(context_lens, (N,), "context_lens", torch.int32)
     if cu_seqlens is None:
         if T != N:
             raise ValueError(f"without cu_seqlens q must have one row for each of {N} requests")
         most = 1
     else:
-        _expect(cu_seqlens, (N + 1,), "cu_seqlens", torch.int32)
+        if cu_seqlens.shape != (N + 1,) or cu_seqlens.dtype != torch.int32:
+            _expect(cu_seqlens, (N + 1,), "cu_seqlens", torch.int32)
         most = T
-    _expect(o, (T, Hq, d), "o", dt)
+    if o is not None:
+        _expect(o, (T, Hq, d), "o", dt)
     on = _on(stream, dev)
     if on is not None:
         on.__enter__()
@@ -1307,7 +1305,8 @@ def kda_cache_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
         if o is None:
             o = torch.empty((T, Hq, d), dtype=dt, device=q.device)
         if workspace is None:
-            workspace = _scratch(cache_attention_workspace_bytes(Hq, H, d, dt), q.device)
+            workspace = _scratch(lib().kda_cache_attention_workspace_bytes(Hq, H, d, code),
+                                 q.device)
         st = lib().kda_cache_attention(
             q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
             v_scale.data_ptr(), nb, block, block_table.data_ptr(), W, context_lens.data_ptr(),

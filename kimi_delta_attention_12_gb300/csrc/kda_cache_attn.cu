@@ -561,6 +561,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(Cach
     constexpr int R = 8 * NT, kStride = R * (D + 2);
     extern __shared__ float weights[];       // [R][blocks of the item]
     __shared__ float total[R];
+    __shared__ float4 shares[kJoinThreads];
     const Stretch s = stretch_of<kJoinThreads>(p, R, blockIdx.x, gridDim.x);
     wait_before();
     if (s.request < 0) return;
@@ -591,20 +592,51 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(Cach
         if (lane == 0) total[n] = sum;
     }
     __syncthreads();
-    const int heads_q = p.heads * p.group;
-    for (int i = threadIdx.x; i < valid * D; i += kJoinThreads) {
-        const int n = i / D, d = i - n * D;
-        float y = 0.0f;
+    // four channels to a thread; the threads left over share the parts
+    const int heads_q = p.heads * p.group, outs = valid * D / 4;
+    const int sharers = outs >= kJoinThreads ? 1 : kJoinThreads / outs;
+    for (int i0 = 0; i0 < outs; i0 += kJoinThreads) {
+        const int share = i0 + kJoinThreads <= outs || sharers == 1 ? 0 : threadIdx.x / outs;
+        const int i = i0 + (sharers == 1 ? threadIdx.x : threadIdx.x - share * outs);
+        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int n = 4 * i / D, d = 4 * i - n * D;
+        if (i < outs && share < sharers) {
 #pragma unroll 8
-        for (int k = 0; k < parts; ++k) y = fmaf(weights[n * parts + k], part_of(k)[i], y);
-        y = total[n] == 0.0f ? 0.0f : y / total[n];
+            for (int k = share; k < parts; k += sharers) {
+                const float f = weights[n * parts + k];
+                const float4 x = *reinterpret_cast<const float4*>(part_of(k) + 4 * i);
+                y.x = fmaf(f, x.x, y.x);
+                y.y = fmaf(f, x.y, y.y);
+                y.z = fmaf(f, x.z, y.z);
+                y.w = fmaf(f, x.w, y.w);
+            }
+        }
+        if (sharers > 1) {
+            shares[threadIdx.x] = y;
+            __syncthreads();
+            if (share > 0 || i >= outs) return;
+            for (int k = 1; k < sharers; ++k) {
+                const float4 x = shares[k * outs + i];
+                y.x += x.x;
+                y.y += x.y;
+                y.z += x.z;
+                y.w += x.w;
+            }
+        }
+        if (i >= outs) return;
+        const float all = total[n], by = all == 0.0f ? 0.0f : 1.0f / all;
         const int flat = it.tile * R + n, j = flat / p.group;
         const int64_t to =
             ((it.row0 + j) * heads_q + it.head * p.group + flat - j * p.group) * D + d;
         if (F32) {
-            static_cast<float*>(p.o)[to] = y;
+            *reinterpret_cast<float4*>(static_cast<float*>(p.o) + to) =
+                make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
         } else {
-            static_cast<__nv_bfloat16*>(p.o)[to] = __float2bfloat16_rn(y);
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x * by, y.y * by);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(y.z * by, y.w * by);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + to) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                           *reinterpret_cast<const uint32_t*>(&hi));
         }
     }
 }

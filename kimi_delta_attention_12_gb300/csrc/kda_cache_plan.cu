@@ -14,6 +14,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kRowThreads = 256;
+constexpr int kFewRows = 4096;       // that the one block does itself
 
 struct Request {
     int64_t past, rows, have, want;
@@ -61,48 +62,80 @@ __device__ __forceinline__ int64_t clamped(int64_t x, int64_t hi) {
     return x < 0 ? 0 : (x > hi ? hi : x);
 }
 
-__global__ void __launch_bounds__(kThreads, 1) plan_requests_kernel(CachePlan p) {
+// Position and slot of row t; `starts`: the requests' first rows.
+__device__ __forceinline__ void plan_row(const CachePlan& p, const int32_t* starts, int64_t t) {
+    int32_t position = 0;
+    int64_t slot = -1;
+    if (t < starts[p.N]) {
+        int lo = 0, hi = p.N;               // the last request that starts at or before t
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (starts[mid] <= t) {
+                lo = mid;
+            } else {
+                hi = mid;
+            }
+        }
+        const int64_t at = (int64_t)p.past[lo] + t - starts[lo];
+        position = (int32_t)at;
+        if (p.status[lo] == KDA_PLAN_OK) {
+            const int32_t b = p.table[(int64_t)lo * p.width + (at >> p.block_log2)];
+            slot = ((int64_t)b << p.block_log2) + (at & ((1 << p.block_log2) - 1));
+            if (b < 0 || slot > 0x7fffffff) slot = -1;
+        }
+    }
+    p.positions[t] = position;
+    p.slots[t] = (int32_t)slot;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) plan_requests_kernel(CachePlan p, int rows_too) {
     __shared__ int64_t warp[33];
     __shared__ int64_t at[kThreads];
-    __shared__ int32_t from[kThreads], count[kThreads];
+    __shared__ int32_t from[kThreads], count[kThreads], starts[kThreads + 1];
     let_follow();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int64_t n_free = clamped(p.n_free[0], p.capacity);
     // rows, and the blocks of ended requests put back on the stack
-    int64_t rows_before = 0, gone_before = 0;
+    Request r = {};
+    int64_t rows_before = 0, gone_before = 0, end = 0;
     for (int i0 = 0; i0 < p.N; i0 += kThreads) {
         const int i = i0 + threadIdx.x;
-        Request r = {};
+        r = Request();
         if (i < p.N) r = request_of(p, i);
         int64_t sum;
-        const int64_t end = rows_before + running(r.rows, &sum, warp);
+        end = rows_before + running(r.rows, &sum, warp);
         rows_before += sum;
-        if (i < p.N) p.cu[i + 1] = (int32_t)clamped(end, p.T);
+        if (i < p.N) {
+            p.cu[i + 1] = (int32_t)clamped(end, p.T);
+            if (p.N <= kThreads) starts[i + 1] = (int32_t)clamped(end, p.T);
+        }
         const int64_t gone = r.ends ? r.have : 0;
+        if (!__syncthreads_or(gone > 0)) continue;
         at[threadIdx.x] = n_free + gone_before + running(gone, &sum, warp) - gone;
         count[threadIdx.x] = (int32_t)gone;
+        gone_before += sum;
         __syncthreads();
-        if (sum > 0) {
-            gone_before += sum;
-            for (int k = w; k < kThreads && i0 + k < p.N; k += kThreads / 32) {
-                const int32_t* row = p.table + (int64_t)(i0 + k) * p.width;
-                for (int j = lane; j < count[k]; j += 32) {
-                    if (at[k] + j < p.capacity) p.free_blocks[at[k] + j] = row[j];
-                }
+        for (int k = w; k < kThreads && i0 + k < p.N; k += kThreads / 32) {
+            const int32_t* row = p.table + (int64_t)(i0 + k) * p.width;
+            for (int j = lane; j < count[k]; j += 32) {
+                if (at[k] + j < p.capacity) p.free_blocks[at[k] + j] = row[j];
             }
         }
         __syncthreads();
     }
     const int64_t total = clamped(n_free + gone_before, p.capacity);
     // blocks taken from the stack's end, and what becomes of each request
-    int64_t need_before = 0, taken = 0, end_before = 0;
+    int64_t need_before = 0, taken = 0;
+    rows_before = 0;
     for (int i0 = 0; i0 < p.N; i0 += kThreads) {
         const int i = i0 + threadIdx.x;
-        Request r = {};
-        if (i < p.N) r = request_of(p, i);
         int64_t sum;
-        const int64_t end = end_before + running(r.rows, &sum, warp);
-        end_before += sum;
+        if (p.N > kThreads) {
+            r = Request();
+            if (i < p.N) r = request_of(p, i);
+            end = rows_before + running(r.rows, &sum, warp);
+            rows_before += sum;
+        }
         int status = KDA_PLAN_OK;
         if (r.bad) {
             status = KDA_PLAN_BAD_LENGTH;
@@ -113,10 +146,11 @@ __global__ void __launch_bounds__(kThreads, 1) plan_requests_kernel(CachePlan p)
         }
         const int64_t need = status == KDA_PLAN_OK && !r.ends ? r.want - r.have : 0;
         const int64_t upto = need_before + running(need, &sum, warp);
+        const bool enough = need_before + sum <= total;
         need_before += sum;
         if (need > 0 && upto > total) status = KDA_PLAN_BLOCKS;
         const bool served = status == KDA_PLAN_OK;
-        running(served ? need : 0, &sum, warp);
+        if (!enough) running(served ? need : 0, &sum, warp);
         taken += sum;
         at[threadIdx.x] = total - 1 - (upto - need);
         from[threadIdx.x] = (int32_t)r.have;
@@ -136,44 +170,29 @@ __global__ void __launch_bounds__(kThreads, 1) plan_requests_kernel(CachePlan p)
     }
     if (threadIdx.x == 0) {
         p.cu[0] = 0;
+        starts[0] = 0;
         p.n_free_out[0] = (int32_t)(total - taken);
+    }
+    if (!rows_too) return;
+    __syncthreads();
+    for (int t = threadIdx.x; t < p.T; t += kThreads) {
+        plan_row(p, p.N <= kThreads ? starts : p.cu, t);
     }
 }
 
 __global__ void __launch_bounds__(kRowThreads) plan_rows_kernel(CachePlan p) {
     wait_before();
     const int64_t t = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
-    if (t >= p.T) return;
-    int32_t position = 0;
-    int64_t slot = -1;
-    if (t < p.cu[p.N]) {
-        int lo = 0, hi = p.N;               // the last request that starts at or before t
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (p.cu[mid] <= t) {
-                lo = mid;
-            } else {
-                hi = mid;
-            }
-        }
-        const int64_t at = (int64_t)p.past[lo] + t - p.cu[lo];
-        position = (int32_t)at;
-        if (p.status[lo] == KDA_PLAN_OK) {
-            const int32_t b = p.table[(int64_t)lo * p.width + (at >> p.block_log2)];
-            slot = ((int64_t)b << p.block_log2) + (at & ((1 << p.block_log2) - 1));
-            if (b < 0 || slot > 0x7fffffff) slot = -1;
-        }
-    }
-    p.positions[t] = position;
-    p.slots[t] = (int32_t)slot;
+    if (t < p.T) plan_row(p, p.cu, t);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_plan(const CachePlan& p, cudaStream_t stream) {
-    plan_requests_kernel<<<1, kThreads, 0, stream>>>(p);
+    const bool rows_too = p.T <= kFewRows;
+    plan_requests_kernel<<<1, kThreads, 0, stream>>>(p, rows_too);
     cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess || p.T == 0) return err;
+    if (err != cudaSuccess || rows_too) return err;
     return launch_follower(plan_rows_kernel, dim3((p.T + kRowThreads - 1) / kRowThreads),
                            dim3(kRowThreads), 0, stream, p);
 }

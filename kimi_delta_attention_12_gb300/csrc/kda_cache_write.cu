@@ -6,9 +6,9 @@
 //
 // Bound by HBM: bf16 2 bytes read and 1 written a value.  A run's values stay in registers
 // between the maximum and the rounding, so they are read once.  A block of threads takes the
-// runs that begin among `tile` rows, for one head and one of k and v: runs of more than
-// kShort rows one after the other with all its threads, shorter ones one to a warp.  Which
-// rows begin a run shows from the slots alone.
+// runs that begin among `tile` rows, for some of the heads of k and v: a run of a head goes to
+// as many warps as can hold it, which wait for one another alone.  Which rows begin a run shows
+// from the slots alone.
 #include <cuda_bf16.h>
 
 #include "kda_cache.h"
@@ -20,7 +20,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMostTile = 64;
-constexpr int kShort = 8;        // rows of a run that one warp takes alone
+constexpr int kShort = 256;      // vectors of a run that one warp takes alone
+constexpr int kBlocks = 4096;      // of threads, that a call aims at
 
 // Rows of the run that begins at row t (slot s), at most `most` (what its block has left).
 __device__ __forceinline__ int run_length(const int32_t* slots, int T, int t, int s, int most,
@@ -50,43 +51,47 @@ __device__ __forceinline__ void values_of(const uint4& raw, float* x) {
     }
 }
 
-// The largest finite magnitude.
+// Magnitudes compare as whole numbers, bf16 ones two at a time; whether one of them is not
+// finite shows at the end, and only then each is looked at.
 template <bool BF16>
-__device__ __forceinline__ float largest_of(const uint4& raw, float best) {
-    float x[BF16 ? 8 : 4];
-    values_of<BF16>(raw, x);
+__device__ __forceinline__ uint32_t most_of(const uint4& raw, uint32_t best) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-    for (int i = 0; i < (BF16 ? 8 : 4); ++i) {
-        const float a = fabsf(x[i]);
-        best = a < __int_as_float(0x7f800000) ? fmaxf(best, a) : best;
+    for (int i = 0; i < 4; ++i) {
+        best = BF16 ? __vmaxu2(best, w[i] & 0x7fff7fffu) : max(best, w[i] & 0x7fffffffu);
     }
     return best;
 }
 
-__device__ __forceinline__ float quotient(float x, float scale, float inverse) {
-    return inverse != 0.0f ? x * inverse : __fdiv_rn(x, scale);
+template <bool BF16>
+__device__ __forceinline__ uint32_t most_finite_of(const uint4& raw, uint32_t best) {
+    float x[BF16 ? 8 : 4];
+    values_of<BF16>(raw, x);
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 8 : 4); ++i) {
+        const uint32_t a = __float_as_uint(x[i]) & 0x7fffffffu;
+        best = a < 0x7f800000u ? max(best, a) : best;
+    }
+    return best;
 }
 
-// x / scale is x times its inverse, exactly, for a power of two whose inverse is a normal
-// number; 0 says that it is to be divided.
+// 1 / scale for a power of two whose inverse is a normal number: the product with it is the
+// quotient, exactly.  0 says that it is to be divided.
 __device__ __forceinline__ float exact_inverse(float scale) {
     const uint32_t bits = __float_as_uint(scale), e = bits >> 23;
     return (bits & 0x7fffffu) == 0 && e >= 1 && e <= 253 ? __uint_as_float((254 - e) << 23) : 0.0f;
 }
 
-template <bool BF16>
-__device__ __forceinline__ void store_rounded(uint8_t* to, const uint4& raw, float scale,
-                                              float inverse) {
+template <bool BF16, bool DIVIDE>
+__device__ __forceinline__ void store_rounded(uint8_t* to, const uint4& raw, float by) {
     float x[BF16 ? 8 : 4];
     values_of<BF16>(raw, x);
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 8 : 4); ++i) x[i] = DIVIDE ? __fdiv_rn(x[i], by) : x[i] * by;
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < (BF16 ? 2 : 1); ++i) {
-        const uint32_t lo = e4m3_of(quotient(x[4 * i], scale, inverse),
-                                    quotient(x[4 * i + 1], scale, inverse));
-        const uint32_t hi = e4m3_of(quotient(x[4 * i + 2], scale, inverse),
-                                    quotient(x[4 * i + 3], scale, inverse));
-        w[i] = lo | (hi << 16);
+        w[i] = e4m3_of(x[4 * i], x[4 * i + 1]) | e4m3_of(x[4 * i + 2], x[4 * i + 3]) << 16;
     }
     if (BF16) {
         *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
@@ -117,73 +122,123 @@ __device__ __forceinline__ void rescale16(uint8_t* at, float ratio) {
     *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One run, by 32 * W threads (`tid` among them): rows t .. t + n of head h into block b from
-// place `off` on.  At most M vectors fall to a thread.
-template <bool BF16, int W, int M>
-__device__ __forceinline__ void write_run(const CacheWrite& p, int which, int h, int t, int n,
-                                          int b, int off, int tid, float* shared) {
-    constexpr int size = BF16 ? 2 : 4, per = 16 / size, threads = 32 * W;
-    const int vecs = p.d / per, count = n * vecs;
-    const int64_t stride = which ? p.stride[1] : p.stride[0];
-    const char* x = static_cast<const char*>(which ? p.x[1] : p.x[0]) +
-                    ((int64_t)t * stride + (int64_t)h * p.d) * size;
-    const int64_t tile = ((int64_t)b * p.heads + h) << p.block_log2;
-    uint8_t* cache = (which ? p.cache[1] : p.cache[0]) + tile * p.d;
-    float* scale_at = (which ? p.scale[1] : p.scale[0]) + (int64_t)b * p.heads + h;
-    const float before = off > 0 ? *scale_at : 0.0f;
-    uint4 raw[M];
-    float best = 0.0f;
+// The barrier of some warps of a block.
+template <int THREADS>
+__device__ __forceinline__ void meet(int barrier) {
+    asm volatile("bar.sync %0, %1;" ::"r"(barrier), "n"(THREADS) : "memory");
+}
+
+// One run for one head of k or v: rows t .. t + n into block b from place `off` on.
+struct Run {
+    const char* x;
+    int64_t stride;          // in bytes
+    uint8_t* cache;          // the block's first place
+    float* scale;
+    int count, off;          // vectors of 16 bytes; places ahead
+};
+
+template <bool BF16>
+__device__ __forceinline__ Run run_of(const CacheWrite& p, int unit, int t, int n, int32_t slot) {
+    constexpr int size = BF16 ? 2 : 4;
+    const bool second = unit >= p.heads;
+    const int h = second ? unit - p.heads : unit;
+    const int64_t at = (int64_t)(slot >> p.block_log2) * p.heads + h;
+    Run r;
+    r.stride = (second ? p.stride[1] : p.stride[0]) * size;
+    r.x = static_cast<const char*>(second ? p.x[1] : p.x[0]) + t * r.stride + (int64_t)h * p.d * size;
+    r.cache = (second ? p.cache[1] : p.cache[0]) + (at << p.block_log2) * p.d;
+    r.scale = (second ? p.scale[1] : p.scale[0]) + at;
+    r.count = n * p.d * size / 16;
+    r.off = slot & ((1 << p.block_log2) - 1);
+    return r;
+}
+
+// The run's vectors into registers, by 32 * W threads, at most M to each.
+template <int W, int M>
+__device__ __forceinline__ void load_run(const Run& r, int vecs_log2, int tid, uint4 (&raw)[M],
+                                         float* before) {
 #pragma unroll
     for (int i = 0; i < M; ++i) {
-        const int u = tid + i * threads;
-        if (u < count) {
-            const int row = u / vecs, col = u - row * vecs;
-            raw[i] = __ldcs(reinterpret_cast<const uint4*>(x + row * stride * size) + col);
+        const int u = tid + i * 32 * W;
+        if (u < r.count) {
+            const int row = u >> vecs_log2, col = u & ((1 << vecs_log2) - 1);
+            raw[i] = __ldcs(reinterpret_cast<const uint4*>(r.x + row * r.stride) + col);
         }
     }
+    *before = r.off > 0 ? *r.scale : 0.0f;
+}
+
+// Its scale, and its values into the cache.  shared: W words that no thread still reads;
+// barrier: the W warps' own.
+template <bool BF16, int W, int M>
+__device__ __forceinline__ void finish_run(const Run& r, int d, int vecs_log2, int tid,
+                                           const uint4 (&raw)[M], float before, uint32_t* shared,
+                                           int barrier) {
+    constexpr int per = BF16 ? 8 : 4;
+    // the largest over the run: a bf16 magnitude in the upper half, as fp32 has it
+    auto most = [&](uint32_t x) {
+        x = __reduce_max_sync(0xffffffffu, x);
+        if (W > 1) {
+            if ((tid & 31) == 0) shared[tid >> 5] = x;
+            meet<32 * W>(barrier);
+            x = shared[0];
+#pragma unroll
+            for (int i = 1; i < W; ++i) x = max(x, shared[i]);
+        }
+        return x;
+    };
+    uint32_t best = 0;
 #pragma unroll
     for (int i = 0; i < M; ++i) {
-        if (tid + i * threads < count) best = largest_of<BF16>(raw[i], best);
+        if (tid + i * 32 * W < r.count) best = most_of<BF16>(raw[i], best);
     }
+    best = most(BF16 ? max(best << 16, best & 0xffff0000u) : best);
+    if (best >= 0x7f800000u) {
+        if (W > 1) meet<32 * W>(barrier);    // all have read `shared`
+        best = 0;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, d));
-    if (W > 1) {
-        if ((tid & 31) == 0) shared[tid >> 5] = best;
-        __syncthreads();
-        best = shared[0];
-#pragma unroll
-        for (int i = 1; i < W; ++i) best = fmaxf(best, shared[i]);
-        __syncthreads();
+        for (int i = 0; i < M; ++i) {
+            if (tid + i * 32 * W < r.count) best = most_finite_of<BF16>(raw[i], best);
+        }
+        best = most(best);
     }
-    const float fresh = e4m3_scale(best);
-    const float scale = off > 0 && before > fresh ? before : fresh;
+    const float fresh = e4m3_scale(__uint_as_float(best));
+    const float scale = r.off > 0 && before > fresh ? before : fresh;
     const float inverse = exact_inverse(scale);
 #pragma unroll
     for (int i = 0; i < M; ++i) {
-        const int u = tid + i * threads;
-        if (u < count) {
-            const int row = u / vecs, col = u - row * vecs;
-            store_rounded<BF16>(cache + (int64_t)(off + row) * p.d + col * per, raw[i], scale,
-                                inverse);
+        const int u = tid + i * 32 * W;
+        if (u < r.count) {
+            const int row = u >> vecs_log2, col = u & ((1 << vecs_log2) - 1);
+            uint8_t* to = r.cache + (r.off + row) * d + col * per;
+            if (inverse != 0.0f) {
+                store_rounded<BF16, false>(to, raw[i], inverse);
+            } else {
+                store_rounded<BF16, true>(to, raw[i], scale);
+            }
         }
     }
-    if (off > 0 && scale != before) {
+    if (r.off > 0 && scale != before) {
         const float ratio = __fdiv_rn(before, scale);
-        for (int u = tid; u < off * p.d / 16; u += threads) rescale16(cache + 16 * u, ratio);
+        for (int u = tid; u < r.off * d / 16; u += 32 * W) rescale16(r.cache + 16 * u, ratio);
     }
     if (W == 1) __syncwarp();
-    if (tid == 0) *scale_at = scale;       // this run's threads have all read it
+    // all threads of the run have read the old scale: the maximum brought them together
+    if (tid == 0) *r.scale = scale;
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheWrite p, int tile) {
+// G warps take a run together, M vectors of a whole block of tokens to a thread.
+template <bool BF16, int G, int M>
+__global__ void __launch_bounds__(kThreads, M > 8 ? 2 : (BF16 ? 4 : 3)) cache_write_kernel(CacheWrite p,
+                                                                               int tile,
+                                                                               int units) {
     __shared__ int32_t at[kMostTile];        // rows of the tile that begin a run
     __shared__ int32_t length[kMostTile];
-    __shared__ float shared[kWarps];
+    __shared__ uint32_t shared[2][kWarps];
     __shared__ int begins;
-    const int h = blockIdx.y, which = blockIdx.z;
     const int t0 = blockIdx.x * tile, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int size = 1 << p.block_log2;
+    const int vecs_log2 = 31 - __clz(p.d / (BF16 ? 8 : 4));
     const int64_t pool = (int64_t)p.num_blocks << p.block_log2;
     if (w == 0) {
         int n = 0;
@@ -192,8 +247,8 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheWrite p, int
             bool begin = false;
             if (i < tile && t < p.T) {
                 const int32_t s = p.slots[t];
-                begin = s >= 0 && s < pool &&
-                        (t == 0 || (s & (size - 1)) == 0 || p.slots[t - 1] != s - 1);
+                const int32_t ahead = t == 0 ? -1 : p.slots[t - 1];
+                begin = s >= 0 && s < pool && ((s & (size - 1)) == 0 || ahead != s - 1);
             }
             const uint32_t all = __ballot_sync(0xffffffffu, begin);
             if (begin) at[n + __popc(all & ((1u << lane) - 1))] = t;
@@ -203,32 +258,65 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheWrite p, int
     }
     __syncthreads();
     const int n = begins;
+    if (n == 0) return;
     for (int i = w; i < n; i += kWarps) {
         const int32_t s = p.slots[at[i]];
         const int len = run_length(p.slots, p.T, at[i], s, size - (s & (size - 1)), lane);
         if (lane == 0) length[i] = len;
-        if (len <= kShort) {
-            write_run<BF16, 1, BF16 ? 4 : 8>(p, which, h, at[i], len, s >> p.block_log2,
-                                             s & (size - 1), lane, nullptr);
-        }
     }
     __syncthreads();
-    for (int i = 0; i < n; ++i) {
-        if (length[i] <= kShort) continue;
-        const int32_t s = p.slots[at[i]];
-        write_run<BF16, kWarps, BF16 ? 8 : 16>(p, which, h, at[i], length[i], s >> p.block_log2,
-                                               s & (size - 1), threadIdx.x, shared);
+    // runs that one warp holds, run by run and head by head
+    const int first = blockIdx.y * units;
+    const int mine = 2 * p.heads - first < units ? 2 * p.heads - first : units;
+    for (int i = w; i < n * mine; i += kWarps) {
+        const int k = i / mine, len = length[k];
+        if (len << vecs_log2 > kShort) continue;
+        const Run r = run_of<BF16>(p, first + i - k * mine, at[k], len, p.slots[at[k]]);
+        uint4 raw[kShort / 32];
+        float before;
+        load_run<1>(r, vecs_log2, lane, raw, &before);
+        finish_run<BF16, 1>(r, p.d, vecs_log2, lane, raw, before, nullptr, 0);
     }
+    if (G == 1) return;
+    // the longer ones, G warps to each
+    const int group = w / G, tid = threadIdx.x - group * 32 * G;
+    int turn = 0;
+    for (int i = group; i < n * mine; i += kWarps / G) {
+        const int k = i / mine, len = length[k];
+        if (len << vecs_log2 <= kShort) continue;
+        const Run r = run_of<BF16>(p, first + i - k * mine, at[k], len, p.slots[at[k]]);
+        uint4 raw[M];
+        float before;
+        load_run<G>(r, vecs_log2, tid, raw, &before);
+        finish_run<BF16, G>(r, p.d, vecs_log2, tid, raw, before, shared[turn] + group * G,
+                            1 + group);
+        turn ^= 1;
+    }
+}
+
+template <bool BF16>
+cudaError_t launch_typed(const CacheWrite& p, cudaStream_t stream) {
+    const int tile = p.T <= 4096 ? 8 : kMostTile;
+    const int tiles = (p.T + tile - 1) / tile;
+    // heads of k and v are dealt to as many blocks as keep the SMs busy
+    int parts = (kBlocks + tiles - 1) / tiles;
+    if (parts > 2 * p.heads) parts = 2 * p.heads;
+    const int units = (2 * p.heads + parts - 1) / parts;
+    const dim3 grid(tiles, (2 * p.heads + units - 1) / units);
+    const int warps = (p.d << p.block_log2) / (BF16 ? 8 : 4) / kShort;   // a block of tokens fills
+    auto kernel = warps <= 1   ? cache_write_kernel<BF16, 1, 8>
+                  : warps <= 2 ? cache_write_kernel<BF16, 2, 8>
+                  : warps <= 4 ? cache_write_kernel<BF16, 4, 8>
+                  : warps <= 8 ? cache_write_kernel<BF16, 8, 8>
+                               : cache_write_kernel<BF16, 8, BF16 ? 8 : 16>;
+    kernel<<<grid, kThreads, 0, stream>>>(p, tile, units);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_cache_write(const CacheWrite& p, int dtype, cudaStream_t stream) {
-    const int tile = p.T <= 4096 ? 8 : kMostTile;
-    const dim3 grid((p.T + tile - 1) / tile, p.heads, 2);
-    auto kernel = dtype == 0 ? cache_write_kernel<false> : cache_write_kernel<true>;
-    kernel<<<grid, kThreads, 0, stream>>>(p, tile);
-    return cudaGetLastError();
+    return dtype == 0 ? launch_typed<false>(p, stream) : launch_typed<true>(p, stream);
 }
 
 }  // namespace kda

@@ -21,7 +21,9 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 4;        // vectors (or pairs of them) of a thread that are in flight
+// Vectors (or pairs of them) of a block.
+constexpr int kLeastUnits = 512, kMostUnits = 4096;
+constexpr int kBlocks = 1216;        // eight for each of 152 SMs
 
 // f / (2 pi) as a 64-bit fraction of a turn, whole turns dropped.
 __device__ __forceinline__ uint64_t turns_of(float f) {
@@ -87,13 +89,19 @@ struct Vec {
     }
 };
 
+// How a thread gets from one of its units to the next: kThreads units on.
+struct Steps {
+    int units, turned;       // of a row; of those, the turned ones
+    int in_row, tokens, heads;   // kThreads units as rows and a rest, the rows as tokens and a rest
+};
+
 // Rows of a call in order: token, then the heads of q, then those of k.  A row is cut into
 // `units`: the turned vectors (or pairs of vectors), then the ones that are copied.
 template <bool BF16, bool INTER>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(Rotary p, int rows_per_block, int units,
-                                                          int turned) {
+__global__ void __launch_bounds__(kThreads, 6) rotary_kernel(Rotary p, int rows_per_block,
+                                                          const Steps step) {
     using V = Vec<BF16>;
-    constexpr int n = V::n;
+    constexpr int n = V::n, size = BF16 ? 2 : 4;
     extern __shared__ float2 table[];        // [tokens of this block][rot / 2]
     const int heads = p.heads[0] + p.heads[1], half = p.rot / 2;
     const int64_t total = p.T * heads, row0 = (int64_t)blockIdx.x * rows_per_block;
@@ -104,39 +112,58 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(Rotary p, int rows_per
 
     struct Unit {
         char* to;
-        const char* from;
         const float2* angles;
-        int far;                             // bytes to the second vector of a pair; 0: copy
+        bool turned;
         V a, b;
     };
-    constexpr int size = BF16 ? 2 : 4;
-    auto load = [&](int u, Unit& x) {
-        const int row = u / units, in_row = u - row * units;
-        const int flat = head0 + row, dt = flat / heads;
-        int h = flat - dt * heads;
-        const int which = h >= p.heads[0];
-        h -= which ? p.heads[0] : 0;
-        int c;                               // the unit's first channel
-        if (in_row < turned) {
-            c = p.first + in_row * n;
-            x.far = INTER ? size : half * size;
-            x.angles = table + dt * half + (INTER ? in_row * n / 2 : in_row * n);
+    // where this thread is
+    int in_row = threadIdx.x % step.units, dt = (head0 + threadIdx.x / step.units) / heads;
+    int head = head0 + threadIdx.x / step.units - dt * heads, left = rows * step.units - threadIdx.x;
+    auto load = [&](Unit& x) {
+        if (left > 0) {
+            const bool second = head >= p.heads[0];
+            const int h = second ? head - p.heads[0] : head;
+            x.turned = in_row < step.turned;
+            int c;                           // the unit's first channel
+            if (x.turned) {
+                c = p.first + in_row * n;
+                x.angles = table + dt * half + (INTER ? in_row * n / 2 : in_row * n);
+            } else {
+                c = (in_row - step.turned) * n;
+                c += c >= p.first ? p.rot : 0;
+            }
+            const int64_t col = h * p.d + c, t = t0 + dt;
+            const char* from = static_cast<const char*>(second ? p.x[1] : p.x[0]) +
+                               (t * (second ? p.stride[1] : p.stride[0]) + col) * size;
+            x.to = static_cast<char*>(second ? p.out[1] : p.out[0]) +
+                   (t * (second ? p.out_stride[1] : p.out_stride[0]) + col) * size;
+            x.a.raw = __ldcs(reinterpret_cast<const uint4*>(from));
+            if (!INTER && x.turned) {
+                x.b.raw = __ldcs(reinterpret_cast<const uint4*>(from + half * size));
+            }
         } else {
-            c = (in_row - turned) * n;
-            c += c >= p.first ? p.rot : 0;
-            x.far = 0;
+            x.to = nullptr;
         }
-        const int64_t col = (int64_t)h * p.d + c;
-        const int64_t t = t0 + dt;
-        x.from = static_cast<const char*>(which ? p.x[1] : p.x[0]) +
-                 (t * (which ? p.stride[1] : p.stride[0]) + col) * size;
-        x.to = static_cast<char*>(which ? p.out[1] : p.out[0]) +
-               (t * (which ? p.out_stride[1] : p.out_stride[0]) + col) * size;
-        x.a.raw = __ldcs(reinterpret_cast<const uint4*>(x.from));
-        if (!INTER && x.far) x.b.raw = __ldcs(reinterpret_cast<const uint4*>(x.from + x.far));
+        left -= kThreads;
+        in_row += step.in_row;
+        head += step.heads;
+        dt += step.tokens;
+        if (in_row >= step.units) {
+            in_row -= step.units;
+            ++head;
+        }
+        if (head >= heads) {
+            head -= heads;
+            ++dt;
+        }
+        if (head >= heads) {                 // one head: the rest and the carry are a token each
+            head -= heads;
+            ++dt;
+        }
     };
     auto finish = [&](Unit& x) {
-        if (x.far) {
+        if (x.to == nullptr) return;
+        if (x.turned) {
             float u[n], w[n];
             x.a.get(u);
             if (INTER) {
@@ -158,34 +185,26 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(Rotary p, int rows_per
                 }
                 x.a.put(u);
                 x.b.put(w);
-                __stcs(reinterpret_cast<uint4*>(x.to + x.far), x.b.raw);
+                __stcs(reinterpret_cast<uint4*>(x.to + half * size), x.b.raw);
             }
         }
         __stcs(reinterpret_cast<uint4*>(x.to), x.a.raw);
     };
 
-    const int count = rows * units;
-    Unit x[kUnits];
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        const int u = threadIdx.x + i * kThreads;
-        if (u < count) load(u, x[i]);
-    }
+    // one unit ahead of the one that is stored
+    Unit x, y;
+    load(x);
     for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
-        const int dt = i / half, j = i - dt * half;
-        table[i] = turn(p.positions[t0 + dt], p.inv_freq[j], p.magnitude, p.inverse);
+        const int t = i / half, j = i - t * half;
+        table[i] = turn(p.positions[t0 + t], p.inv_freq[j], p.magnitude, p.inverse);
     }
     __syncthreads();
-    for (int base = threadIdx.x; base < count; base += kUnits * kThreads) {
-#pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            if (base + i * kThreads < count) finish(x[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            const int u = base + (kUnits + i) * kThreads;
-            if (u < count) load(u, x[i]);
-        }
+    while (x.to != nullptr) {
+        load(y);
+        finish(x);
+        if (y.to == nullptr) break;
+        load(x);
+        finish(y);
     }
 }
 
@@ -198,7 +217,11 @@ cudaError_t launch_typed(const Rotary& p, cudaStream_t stream) {
     const int turned = p.rot / n / (p.interleaved ? 1 : 2);
     const int units = turned + (copy ? (p.d - p.rot) / n : 0);
     const int64_t heads = p.heads[0] + p.heads[1], total = p.T * heads;
-    int rows = (2 * kUnits * kThreads + units - 1) / units;
+    // long stretches keep loads ahead of the stores, short ones keep all SMs busy
+    int64_t most_units = total * units / kBlocks;
+    most_units = most_units < kLeastUnits ? kLeastUnits
+                                          : (most_units > kMostUnits ? kMostUnits : most_units);
+    int rows = (int)((most_units + units - 1) / units);
     const int64_t half = p.rot / 2;
     // the table of a block's tokens stays within 32 KB
     const int64_t most = (32768 / (half * 8) - 1) * heads;
@@ -206,9 +229,15 @@ cudaError_t launch_typed(const Rotary& p, cudaStream_t stream) {
     const int64_t tokens = (rows + heads - 2) / heads + 1;
     const int64_t blocks = (total + rows - 1) / rows;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    Steps step;
+    step.units = units;
+    step.turned = turned;
+    step.in_row = kThreads % units;
+    step.tokens = (int)(kThreads / units / heads);
+    step.heads = (int)(kThreads / units % heads);
     const size_t smem = (size_t)(tokens * half) * sizeof(float2);
     auto kernel = p.interleaved ? rotary_kernel<BF16, true> : rotary_kernel<BF16, false>;
-    kernel<<<(unsigned)blocks, kThreads, smem, stream>>>(p, rows, units, turned);
+    kernel<<<(unsigned)blocks, kThreads, smem, stream>>>(p, rows, step);
     return cudaGetLastError();
 }
 

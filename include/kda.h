@@ -201,7 +201,7 @@ KDA_API int64_t kda_checkpoint_count(const int32_t* cu_seqlens_host, int32_t N,
 
 /*
  * kda_workspace_status -- wait for `stream`, then read the status word the last
- * kda_prefill, kda_lin_prefill or kda_lin_backward launch left in `workspace`.  Returns KDA_OK, KDA_ERR_TIMEOUT
+ * kda_prefill, kda_lin_prefill, kda_lin_backward or kda_cache_attention launch left in `workspace`.  Returns KDA_OK, KDA_ERR_TIMEOUT
  * (a bounded wait inside the kernel ran out; its outputs are invalid) or
  * KDA_ERR_CUDA.  Synchronising; meant for tests and diagnostics.
  */
@@ -805,7 +805,8 @@ KDA_API int kda_cache_write(const void* k, int64_t k_stride, const void* v, int6
  *             that is too small costs time, not results
  *  o          [T, Hq, d] dt, dense
  *  workspace  kda_cache_attention_workspace_bytes(...) bytes, 256-byte aligned, no
- *             initialisation needed
+ *             initialisation needed; it begins with a status word that
+ *             kda_workspace_status reads
  * A row that sees no key (c = 0, or more new tokens than c) becomes zero.  Rows behind
  * the last request's are left as they were.  Entries of block_table outside the pool
  * count as tokens that are not there; context_lens and cu_seqlens are clamped to the

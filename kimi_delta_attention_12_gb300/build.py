@@ -27,7 +27,7 @@ SOURCES = ["kda_api.cpp", "kda_recurrent.cu", "kda_state_io.cu", "kda_prefill_sm
            "kda_lin_api.cpp", "kda_lin_attn.cu", "kda_lin_sm103.cu",
            "kda_norm_api.cpp", "kda_block_norm.cu",
            "kda_cache_api.cpp", "kda_rotary.cu", "kda_cache_plan.cu", "kda_cache_write.cu",
-           "kda_cache_attn.cu"]
+           "kda_cache_attn.cu", "kda_cache_prompt_sm103.cu"]
 
 
 def _nvcc() -> str:

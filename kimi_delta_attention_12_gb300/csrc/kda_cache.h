@@ -75,11 +75,19 @@ struct CacheAttention {
     int32_t d;
     float scale;
     void* o;
-    float* partial;            // workspace
+    // workspace: a status word, which the call's first kernel clears, and partial sums
+    int32_t* status;
+    int32_t clears;
+    float* partial;
+    int64_t many_rows;         // rows (heads of a group times new tokens) of a request from which
+                               // on the prompts' kernel takes it, the other one below
 };
 
 // Bytes of partial sums, on a device of that many SMs.
 size_t cache_attention_room(int32_t group, int32_t d, int sms);
+// Whether the prompts' kernel has a form for these.
+bool cache_prompt_takes(int32_t d, int dtype);
+cudaError_t launch_cache_prompt(const CacheAttention& p, cudaStream_t stream);
 cudaError_t launch_cache_attention(const CacheAttention& p, int dtype, int sms,
                                    cudaStream_t stream);
 

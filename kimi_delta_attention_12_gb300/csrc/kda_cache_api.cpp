@@ -16,6 +16,7 @@ using kda::overlaps;
 using kda::round_up;
 using kda::supported_dim;
 
+constexpr size_t kHeader = 256;   // status word
 constexpr int32_t kMaxRotaryDim = 512;
 constexpr int32_t kMaxGroup = 64;
 constexpr uint32_t kRotaryFlags = KDA_FLAG_ROTARY_INTERLEAVED | KDA_FLAG_ROTARY_INVERSE;
@@ -252,7 +253,7 @@ size_t kda_cache_attention_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t d, k
         !good_type(dt)) {
         return 0;
     }
-    return round_up(kda::cache_attention_room(Hq / Hkv, d, sm_count()), 256) + 256;
+    return kHeader + round_up(kda::cache_attention_room(Hq / Hkv, d, sm_count()), 256);
 }
 
 int kda_cache_attention(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
@@ -305,7 +306,8 @@ int kda_cache_attention(const void* q, int64_t q_stride, const void* k_cache, co
     p.block_log2 = log2_of_block(block); p.table = block_table; p.width = table_width;
     p.context = context_lens; p.cu = cu_seqlens; p.N = N; p.T = T; p.max_new = max_new;
     p.heads = Hkv; p.group = group; p.d = d; p.scale = scale; p.o = o;
-    p.partial = static_cast<float*>(workspace);
+    p.status = static_cast<int32_t*>(workspace);
+    p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kHeader);
     return kda::launch_cache_attention(p, dt == KDA_F32 ? 0 : 1, sms,
                                        static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? KDA_OK

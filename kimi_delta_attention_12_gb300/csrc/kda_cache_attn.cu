@@ -42,6 +42,7 @@ constexpr int kUnit = 16 * kWarps;       // tokens of a unit
 constexpr int kJoinThreads = 256;
 constexpr float kNone = -INFINITY;
 constexpr float kRaise = 15.0f;
+constexpr int64_t kManyRows = 64, kManyWork = 4096;
 
 // Blocks that an SM holds at once, by the rows of a tile.
 __host__ __device__ constexpr int blocks_per_sm(int NT) { return NT == 1 ? 3 : 2; }
@@ -76,7 +77,8 @@ __device__ __forceinline__ Span span_of(const CacheAttention& p, int i, int R) {
     s.row0 = bos;
     s.fresh = (int)(eos - bos);
     s.tokens = (int)(c < 0 ? 0 : (c < most ? c : most));
-    s.tiles = (int)(((int64_t)s.fresh * p.group + R - 1) / R);
+    const int64_t rows = (int64_t)s.fresh * p.group;
+    s.tiles = rows < p.many_rows ? (int)((rows + R - 1) / R) : 0;
     s.units = s.tokens > 0 ? (int)(((int64_t)s.tokens + kUnit - 1) / kUnit) : 1;
     s.all = (int64_t)s.tiles * p.heads * s.units;
     return s;
@@ -269,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) cache_attention_k
     float* sums_m = sums + kWarps * R * D;
     float* sums_l = sums_m + kWarps * R;
     let_follow();
+    if (p.clears && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const Stretch s = stretch_of<kThreads>(p, R, blockIdx.x, gridDim.x);
     if (s.request < 0) return;
@@ -677,8 +680,18 @@ size_t cache_attention_room(int32_t, int32_t d, int sms) {
     return (size_t)sms * most * 2 * (d + 2) * sizeof(float);
 }
 
-cudaError_t launch_cache_attention(const CacheAttention& p, int dtype, int sms,
+cudaError_t launch_cache_attention(const CacheAttention& call, int dtype, int sms,
                                    cudaStream_t stream) {
+    CacheAttention p = call;
+    p.clears = 1;
+    p.many_rows = INT64_MAX;
+    const int64_t most = (int64_t)p.group * p.max_new, rows = (int64_t)p.group * p.T;
+    if (cache_prompt_takes(p.d, dtype) && most >= kManyRows && rows * p.heads >= kManyWork) {
+        p.many_rows = p.N == 1 ? 1 : kManyRows;
+        const cudaError_t err = launch_cache_prompt(p, stream);
+        if (err != cudaSuccess || p.N == 1) return err;
+        p.clears = 0;
+    }
     return dtype == 0 ? launch_typed<true>(p, sms, stream) : launch_typed<false>(p, sms, stream);
 }
 

@@ -139,44 +139,60 @@ def write(x, slots, cache, scale, block):
 
 
 def attention(q, k, v, k_scale, v_scale, table, context, cu, scale, block):
-    """(o, bound): o [T, Hq, d] in fp64, rows behind the last request's NaN, and per element
-    what the bound on the error is a multiple of, sum p |v| / sum p, and of each row the
-    largest scale sum |q| |k| over its keys.  k, v: the bytes [nb, H, block, d] as numpy."""
+    """(o, mass, size, least): o [T, Hq, d] in fp64, rows behind the last request's NaN, and what
+    bounds on the error are multiples of: per element sum p |v| / sum p and sum |v| / v_scale times
+    the scale of the heaviest key's block (heaviest by p v_scale), per row the largest scale
+    sum |q| |k| over its keys.  k, v: the bytes [nb, H, block, d] as numpy."""
     q = q.double().cpu().numpy()
     T, Hq, d = q.shape
     nb, H = k_scale.shape
     G = Hq // H
     o, mass = np.full((T, Hq, d), np.nan), np.zeros((T, Hq, d))
-    size = np.zeros((T, Hq, 1))
+    size, least = np.zeros((T, Hq, 1)), np.zeros((T, Hq, d))
     for i, c in enumerate(context):
         n = cu[i + 1] - cu[i]
-        for j in range(n):
-            seen = c - n + j + 1
-            p = [x for x in range(max(seen, 0)) if 0 <= table[i][x // block] < nb]
-            for hq in range(Hq):
-                t, h = cu[i] + j, hq // G
-                if not p:
-                    o[t, hq] = 0.0
+        there = [x for x in range(max(c, 0)) if 0 <= table[i][x // block] < nb]
+        b = np.array([table[i][x // block] for x in there], dtype=np.int64)
+        at = np.array([x % block for x in there], dtype=np.int64)
+        seen = np.array(there)[None] <= (c - n + np.arange(n))[:, None]       # [n, keys]
+        any_key = seen.any(axis=1)
+        for h in range(H):
+            K = e4m3_values(k[b, h, at]) * k_scale[b, h].astype(np.float64)[:, None]
+            V = e4m3_values(v[b, h, at]) * v_scale[b, h].astype(np.float64)[:, None]
+            for hq in range(h * G, (h + 1) * G):
+                x = q[cu[i]:cu[i + 1], hq]
+                o[cu[i]:cu[i + 1], hq] = 0.0
+                if not len(there):
                     continue
-                b = np.array([table[i][x // block] for x in p])
-                at = np.array([x % block for x in p])
-                K = e4m3_values(k[b, h, at]) * k_scale[b, h].astype(np.float64)[:, None]
-                V = e4m3_values(v[b, h, at]) * v_scale[b, h].astype(np.float64)[:, None]
-                s = scale * (K @ q[t, hq])
-                w = np.exp(s - s.max())
-                o[t, hq] = w @ V / w.sum()
-                mass[t, hq] = w @ np.abs(V) / w.sum()
-                size[t, hq] = abs(scale) * (np.abs(K) @ np.abs(q[t, hq])).max()
-    return o, mass, size
+                s = np.where(seen, scale * (x @ K.T), -np.inf)
+                top = np.where(any_key, np.max(s, axis=1, initial=-np.inf), 0.0)
+                w = np.where(seen, np.exp(s - top[:, None]), 0.0)
+                total = np.where(any_key, w.sum(axis=1), 1.0)[:, None]
+                clean = np.nan_to_num(V) if np.isnan(V).any() else V
+                vs = v_scale[b, h].astype(np.float64)
+                heavy = vs[np.argmax(s + np.log(vs)[None], axis=1)]
+                least[cu[i]:cu[i + 1], hq] = (seen @ np.abs(clean / vs[:, None])) * heavy[:, None]
+                y, y_abs = w @ clean / total, w @ np.abs(clean) / total
+                if np.isnan(V).any():
+                    y = np.where((w @ np.isnan(V)) > 0, np.nan, y)
+                rows = slice(cu[i], cu[i + 1])
+                o[rows, hq] = np.where(any_key[:, None], y, 0.0)
+                mass[rows, hq] = np.where(any_key[:, None], y_abs, 0.0)
+                size[rows, hq, 0] = np.where(
+                    any_key, abs(scale) * np.max(np.where(seen, np.abs(x) @ np.abs(K).T, 0.0),
+                                                 axis=1, initial=0.0), 0.0)
+    return o, mass, size, least
 
 
-def attention_bound(o, mass, size, d, longest, bf16):
+def attention_bound(o, mass, size, least, d, longest, bf16):
     """How far o may be off: a score's products carry 2^-22 of each (q in two halves of 11 bits)
     and d / 16 sums of two products rounded to 2^-22 of the whole; the weights' 2^-20 (exponent,
     its argument), the running sums 2^-24 for each 16 keys; for bf16 the weights' 11 bits and the
-    result's rounding, 2^-8."""
+    result's rounding, 2^-8.  And an fp16 weight is off by up to 2^-25 however small it is, where
+    the largest weight times its scale is 2^7 at least for bf16, 2^15 for fp32 (whose second half
+    is an fp16 number too): 2^-32 or 2^-40 of `least`."""
     ds = size * (1 + d / 8) * 2.0 ** -22
     rel = 2 * ds + 2.0 ** -20 + (longest / 16 + 8) * 2.0 ** -23
     if bf16:
-        return mass * (rel + 2.0 ** -11) + np.abs(o) * 2.0 ** -8
-    return mass * rel
+        return mass * (rel + 2.0 ** -11) + np.abs(o) * 2.0 ** -8 + least * 2.0 ** -32
+    return mass * rel + least * 2.0 ** -40

@@ -238,7 +238,7 @@ def test_reference_attention_of_one_key_is_its_value():
     k = np.zeros((1, 1, 16, 32), np.uint8)
     v = np.arange(16 * 32, dtype=np.uint8).reshape(1, 1, 16, 32) % 120
     one = np.ones((1, 1))
-    o, mass, _ = R.attention(torch.ones(1, 2, 32), k, v, one, one * 2.0, [[0]], [1], [0, 1], 1.0, 16)
+    o, *_ = R.attention(torch.ones(1, 2, 32), k, v, one, one * 2.0, [[0]], [1], [0, 1], 1.0, 16)
     assert np.array_equal(o[0, 0], 2.0 * R.e4m3_values(v[0, 0, 0]))
-    o, _, _ = R.attention(torch.ones(1, 2, 32), k, v, one, one, [[5]], [3], [0, 1], 1.0, 16)
+    o, *_ = R.attention(torch.ones(1, 2, 32), k, v, one, one, [[5]], [3], [0, 1], 1.0, 16)
     assert not o.any()

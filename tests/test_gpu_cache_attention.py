@@ -46,10 +46,10 @@ class Batch:
                 torch.tensor(self.cu, **i32))
 
     def check(self, got):
-        o, mass, size = R.attention(self.q, self.k.numpy(), self.v.numpy(), self.ks.numpy(),
-                                    self.vs.numpy(), self.table, self.context, self.cu, self.scale,
-                                    self.block)
-        bound = R.attention_bound(o, mass, size, self.d, max(self.context + [1]),
+        o, *sizes = R.attention(self.q, self.k.numpy(), self.v.numpy(), self.ks.numpy(),
+                                self.vs.numpy(), self.table, self.context, self.cu, self.scale,
+                                self.block)
+        bound = R.attention_bound(o, *sizes, self.d, max(self.context + [1]),
                                   self.q.dtype == torch.bfloat16)
         got, nan = got.double().cpu().numpy(), np.isnan(o)
         assert np.array_equal(np.isnan(got), nan)
@@ -80,6 +80,83 @@ def test_prompts_and_pieces(Hq, H, d, block, dtype):
     b.check(whole)
     for most in (1, 130):        # says which kernels, not what
         b.check(kda.kda_cache_attention(*args, max_new=most))
+
+
+def _tensor_cores(b, H):
+    """Whether the batch has the rows from which on prompts go to the tensor cores' kernel."""
+    return b.q.shape[0] * b.q.shape[1] >= 4096 and max(b.new) * b.q.shape[1] // H >= 64
+
+
+@pytest.mark.parametrize("past,new,block,Hq,H,d", [
+    ([0], [130], 16, 32, 8, 128),               # one request: nothing for the other kernel
+    ([0], [257], 64, 16, 16, 64),
+    ([1000], [90], 128, 64, 4, 128),
+    ([5, 300, 0, 77], [140, 1, 0, 129], 32, 32, 8, 128),      # prompts and single tokens
+    ([40, 0, 900], [333, 64, 15], 16, 20, 4, 64),
+    ([0, 0, 0], [1, 600, 2], 64, 7, 1, 128),
+    ([127, 128, 129], [128, 127, 129], 16, 12, 2, 64),
+])
+def test_prompts_on_the_tensor_cores(past, new, block, Hq, H, d):
+    b = Batch(past, new, block, Hq, H, d, torch.bfloat16, seed=sum(new))
+    assert _tensor_cores(b, H)
+    ws = torch.full((kda.cache_attention_workspace_bytes(Hq, H, d, torch.bfloat16),), 255,
+                    dtype=torch.uint8, device="cuda")
+    got = kda.kda_cache_attention(*b.args(), max_new=max(new), workspace=ws)
+    b.check(got)
+    assert kda.workspace_status(ws) == kda.KDA_OK
+    assert torch.equal(got, kda.kda_cache_attention(*b.args(), max_new=max(new)))
+    b.check(kda.kda_cache_attention(*b.args(), max_new=1))    # the other kernel, all rows
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_extremes_on_the_tensor_cores(d):
+    b = Batch([60, 0], [130, 100], 16, 32, 8, d, torch.bfloat16, seed=d)
+    assert _tensor_cores(b, 8)
+    b.vs = torch.exp2(torch.randint(-60, 61, b.vs.shape).float())
+    b.check(kda.kda_cache_attention(*b.args(), max_new=130))
+    b.vs.fill_(1.0)
+    b.q[::3] *= 1e30
+    b.q[1::3] *= 1e-30
+    b.q[2, 0] = 0.0
+    for scale in (1e-30, 0.0, -0.3, 3.0):
+        if scale in (-0.3, 3.0):
+            b.q = torch.randn(b.q.shape, generator=torch.Generator().manual_seed(1)).bfloat16()
+        b.scale = scale
+        b.check(kda.kda_cache_attention(*b.args(), max_new=130, scale=scale))
+
+
+def test_growing_scores_on_the_tensor_cores():
+    """Scores that rise along the keys: the running maximum moves at every step."""
+    b = Batch([900], [128], 64, 32, 8, 128, torch.bfloat16, seed=3)
+    for p in range(1028):
+        b.k[b.table[0][p // 64], :, p % 64, :8] = int(p / 1028 * 120)
+    b.q[:, :, :8] = b.q[:, :, :8].abs() + 1.0
+    b.scale = 0.5
+    b.check(kda.kda_cache_attention(*b.args(), max_new=128, scale=0.5))
+
+
+def test_rows_without_keys_on_the_tensor_cores():
+    b = Batch([0, 200, 0], [130, 140, 70], 16, 16, 4, 64, torch.bfloat16, seed=8)
+    args = list(b.args())
+    b.context = [0, 100, 30]           # fewer tokens than new ones
+    args[6] = torch.tensor(b.context, dtype=torch.int32).cuda()
+    b.table[1][2] = -1
+    args[5] = torch.tensor(b.table, dtype=torch.int32).cuda()
+    got = kda.kda_cache_attention(*args, max_new=140)
+    assert not got[:130].any()
+    b.check(got)
+
+
+def test_a_query_that_is_not_finite_on_the_tensor_cores():
+    b = Batch([70, 9], [140, 130], 16, 16, 8, 64, torch.bfloat16, seed=10)
+    args = b.args()
+    want = kda.kda_cache_attention(*args, max_new=140)
+    q = args[0].clone()
+    q[1, 2, 5], q[200, 0, 0] = float("nan"), float("inf")
+    got = kda.kda_cache_attention(q, *args[1:], max_new=140)
+    assert torch.isnan(got[1, 2]).all() and not torch.isfinite(got[200, 0]).any()
+    got[1, 2], got[200, 0] = want[1, 2], want[200, 0]
+    assert torch.equal(got, want)
 
 
 def test_long_context_and_many_requests():

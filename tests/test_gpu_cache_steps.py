@@ -39,12 +39,12 @@ def test_steps_of_a_layer():
         past = p["context_lens"]
         cu, context = p["cu_seqlens"].tolist(), past.tolist()
         # what the cache stands for, against the definition
-        want, mass, size = R.attention(
+        want, *sizes = R.attention(
             q, cache[0].view(torch.uint8).cpu().numpy(), cache[1].view(torch.uint8).cpu().numpy(),
             scales[0].cpu().numpy(), scales[1].cpu().numpy(), table.tolist(), context, cu,
             d ** -0.5, block)
         off = np.abs(o.double().cpu().numpy() - want)
-        assert (off <= R.attention_bound(want, mass, size, d, max(context), True)).all()
+        assert (off <= R.attention_bound(want, *sizes, d, max(context), True)).all()
         # and against the keys and values themselves: every cached number is within 2^-4 of its
         # own, or 2^-10 of its block's scale
         for i, n in enumerate(new):

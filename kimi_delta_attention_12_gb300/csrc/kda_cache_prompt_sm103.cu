@@ -12,7 +12,8 @@
 //
 // The tiles take turns: while one's softmax runs, the tensor core works for the other.  Roles:
 // warps 0-7 a row each (softmax, the output), warps 8-11 read e4m3 tiles of the cache and write
-// them as fp16 (exact) in the operands' layout, warp 12 issues the products.
+// them as fp16 (exact) in the operands' layout, warps 12 and 13 issue the products of a tile
+// each, warps 14 and 15 only give their registers away.
 //
 // fp16, not bf16: e4m3 numbers and, scaled to [1, 2) by a power of two per row, bf16 queries are
 // fp16 numbers, and P keeps 11 bits.  Scales of key blocks go into the exponent's factor, those
@@ -24,6 +25,7 @@
 
 #include "kda_cache.h"
 #include "kda_e4m3.cuh"
+#include "kda_packed.cuh"
 #include "kda_seqlens.cuh"
 #include "sm103_ptx.cuh"
 
@@ -36,7 +38,10 @@ constexpr int kRows = 128;               // of a tile
 constexpr int kTokens = 128;             // of a step
 constexpr int kSoftWarps = 8, kFillWarps = 4;
 constexpr int kIssueWarp = kSoftWarps + kFillWarps;
-constexpr int kThreads = 32 * (kIssueWarp + 1);
+constexpr int kThreads = 32 * (kIssueWarp + 4);   // whole groups of four warps share registers
+// Registers of a thread: at launch, and then of the softmax, filling and issuing groups.
+constexpr int kRegs = 128, kSoftRegs = 184, kFillRegs = 104, kIssueRegs = 40;
+static_assert(2 * kSoftRegs + kFillRegs + kIssueRegs <= 4 * kRegs, "register split");
 constexpr float kNone = -INFINITY;
 constexpr float kSlack = 8.0f, kRaise = 7.0f;
 constexpr uint32_t kHalf = 128 * 128;    // 64 columns of a tile: 128 rows of 128 bytes
@@ -52,17 +57,18 @@ struct Layout {
     static constexpr uint32_t bytes = scales + 1024 + 1024;  // scales, barriers; alignment
 };
 
-// Of a step's eight groups of 16 tokens: factor and offset of their scores, and what their
-// weights count in the sum.
-struct Scales {
-    float k[8], log_v[8], inv_v[8];
+// Of a group of 16 tokens: factor and offset of their scores, and what their weights count in
+// the sum.
+struct __align__(16) Scales {
+    float k, log_v, inv_v, unused;
 };
 
 struct Shared {
-    Scales scales[4];                    // of step i at i & 3
+    Scales scales[4][8];                 // of step i at i & 3
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t s_full[2], p_full[2], o_full[2];
-    uint64_t fin;
+    uint64_t fin[2];
+    uint64_t go;                         // the second tile sets out when the first has its weights
     uint32_t tmem;
     volatile int abort;
 };
@@ -137,6 +143,15 @@ __device__ __forceinline__ bool job_of(const CacheAttention& p, int index, int h
     __syncthreads();
     job = found;
     return any != 0;
+}
+
+template <int N>
+__device__ __forceinline__ void take_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void give_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // ------------------------------------------------------------------- waits
@@ -229,61 +244,60 @@ __device__ __forceinline__ float exp2_of(float x) {
 }
 
 // ------------------------------------------------------------------ issuing
+// All products of tile t.
 template <int D>
 __device__ __forceinline__ void issue(const CacheAttention& p, Shared* s, uint32_t base, int steps,
-                                      int tiles) {
+                                      int t) {
     using L = Layout<D>;
     constexpr uint32_t id_s = idesc_f16(128, kTokens, 0, 0), id_o = idesc_f16(128, D, 0, 1);
-    auto scores = [&](int t, int i) {
-        const uint32_t q = tile_k(base + L::q + t * L::tile);
-        const uint32_t k = tile_k(base + L::k + (i & 1) * L::tile);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            product(kS + 128 * t, q + step_k(kk), k + step_k(kk), id_s, kk > 0);
-        }
-        commit(&s->s_full[t]);
-    };
-    bool ok = wait_warp(p, s, &s->k_full[0], 0, 401);
-    if (ok) {
-        fence_proxy_async();
-        tc_fence_after();
-        for (int t = 0; t < tiles; ++t) scores(t, 0);
-        commit(&s->k_empty[0]);
-    }
-    for (int i = 0; ok && i < steps; ++i) {
-        const int stage = i & 1, phase = (i >> 1) & 1;
-        for (int t = 0; ok && t < tiles; ++t) {
-            ok = (t > 0 || wait_warp(p, s, &s->v_full[stage], phase, 402)) &&
-                 wait_warp(p, s, &s->p_full[t], i & 1, 403);
-            if (!ok) break;
+    const uint32_t q = tile_k(base + L::q + t * L::tile), cs = kS + 128 * t, co = kO + 128 * t;
+    for (int i = -1; i < steps; ++i) {
+        if (i >= 0) {
+            const uint32_t v = tile_mn(base + L::v + (i & 1) * L::tile);
+            if (!wait_warp(p, s, &s->v_full[i & 1], (i >> 1) & 1, 402)) break;
             fence_proxy_async();
+            if (!wait_warp(p, s, &s->p_full[t], i & 1, 403)) break;
             tc_fence_after();
-            const uint32_t v = tile_mn(base + L::v + stage * L::tile);
 #pragma unroll
             for (int kk = 0; kk < kTokens / 16; ++kk) {
-                product_ta(kO + 128 * t, kS + 128 * t + 8 * kk, v + step_mn(kk), id_o,
-                           i > 0 || kk > 0);
+                product_ta(co, cs + 8 * kk, v + step_mn(kk), id_o, i > 0 || kk > 0);
             }
             commit(&s->o_full[t]);
-            if (i + 1 < steps) {
-                // the next scores overwrite P: its products have to be done
-                ok = wait_warp(p, s, &s->o_full[t], i & 1, 404) &&
-                     (t > 0 || wait_warp(p, s, &s->k_full[stage ^ 1], ((i + 1) >> 1) & 1, 405));
-                if (!ok) break;
-                fence_proxy_async();
-                tc_fence_after();
-                scores(t, i + 1);
-            }
+            commit(&s->v_empty[i & 1]);
         }
-        if (!ok) break;
-        commit(&s->v_empty[stage]);
-        if (i + 1 < steps) commit(&s->k_empty[stage ^ 1]);
+        if (i + 1 < steps) {
+            // Half a step behind: one tile's softmax then runs beside the other's products.  Side
+            // by side they contend for the issue slots and then for the tensor core.
+            if (i < 0 && t == 1 && !wait_warp(p, s, &s->go, 0, 406)) break;
+            const int stage = (i + 1) & 1;
+            const uint32_t k = tile_k(base + L::k + stage * L::tile);
+            if (!wait_warp(p, s, &s->k_full[stage], ((i + 1) >> 1) & 1, 401)) break;
+            fence_proxy_async();
+            // the scores overwrite P: its products have to be done
+            if (i >= 0 && !wait_warp(p, s, &s->o_full[t], i & 1, 404)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                product(cs, q + step_k(kk), k + step_k(kk), id_s, kk > 0);
+            }
+            commit(&s->s_full[t]);
+            commit(&s->k_empty[stage]);
+        }
     }
-    commit(&s->fin);
-    mbar_wait(&s->fin, 0, nullptr);      // no product outlives the CTA
+    commit(&s->fin[t]);
+    mbar_wait(&s->fin[t], 0, nullptr);   // no product outlives the CTA
 }
 
 // ------------------------------------------------------------------ filling
+// A load that stays where it is written, ahead of the waits that it is to pass by.
+__device__ __forceinline__ uint4 load_early(const uint8_t* p) {
+    uint4 r;
+    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p));
+    return r;
+}
+
 // 16 channels of one token from e4m3 to two vectors of fp16 in a tile.
 __device__ __forceinline__ void spread(uint8_t* tile, int row, int part, const uint4& raw) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -314,94 +328,87 @@ __device__ __forceinline__ void fill(const CacheAttention& p, const Job& job, Sh
     const int tid = threadIdx.x - 32 * kSoftWarps, lane = tid & 31;
     const int part = tid % kParts, row0 = tid / kParts;
     const int32_t* table = p.table + (int64_t)job.request * p.width;
-    // lanes 0-7: the blocks of a step's groups of 16 tokens (-1: not there), and their scales
+    const int mask = (1 << p.block_log2) - 1;
+    const uint32_t block_bytes = (uint32_t)p.heads * D << p.block_log2;
+    const uint32_t in_block = ((uint32_t)job.head * D << p.block_log2) + 16 * part;
+    // lanes 0-7: the blocks of a step's groups of 16 tokens, -1 where there is none
     auto blocks_of = [&](int i) {
         const int token = i * kTokens + 16 * (lane & 7);
-        int b = -1;
-        if (i < steps && token < high) {
-            b = table[token >> p.block_log2];
-            if (b >= p.num_blocks) b = -1;
-        }
-        return b < 0 ? -1 : b;
+        const int b = i < steps && token < high ? table[token >> p.block_log2] : -1;
+        return b >= 0 && b < p.num_blocks ? b : -1;
     };
+    // Rows that are not there are read from block 0, so that no load waits for a branch, and
+    // zeroed.
     auto load = [&](const uint8_t* cache, int i, int blocks, uint4 (&raw)[kLoads]) {
 #pragma unroll
         for (int r = 0; r < kLoads; ++r) {
             const int row = row0 + r * kPass, token = i * kTokens + row;
-            const int b = __shfl_sync(0xffffffffu, blocks, row >> 4);
-            raw[r] = make_uint4(0, 0, 0, 0);
-            if (b >= 0 && token < high) {
-                const int64_t at = (((int64_t)b * p.heads + job.head) << p.block_log2) +
-                                   (token & ((1 << p.block_log2) - 1));
-                raw[r] = *reinterpret_cast<const uint4*>(cache + at * D + 16 * part);
-            }
+            const int b = max(__shfl_sync(0xffffffffu, blocks, row >> 4), 0);
+            raw[r] = load_early(cache + (uint64_t)(uint32_t)b * block_bytes +
+                                (in_block + (token & mask) * D));
         }
     };
-    auto store = [&](uint8_t* tile, const uint4 (&raw)[kLoads]) {
+    auto store = [&](uint8_t* tile, int i, int blocks, uint4 (&raw)[kLoads]) {
+        // (whole steps, but for a request's last)
+        if (__any_sync(0xffffffffu, blocks < 0) || (i + 1) * kTokens > high) {
+#pragma unroll
+            for (int r = 0; r < kLoads; ++r) {
+                const int row = row0 + r * kPass;
+                const int b = __shfl_sync(0xffffffffu, blocks, row >> 4);
+                if (b < 0 || i * kTokens + row >= high) raw[r] = make_uint4(0, 0, 0, 0);
+            }
+        }
 #pragma unroll
         for (int r = 0; r < kLoads; ++r) spread(tile, row0 + r * kPass, part, raw[r]);
     };
+    // of this lane's group: the scales of keys and values
+    auto scales_of = [&](int blocks, float& ks, float& vs) {
+        const int64_t at = (int64_t)max(blocks, 0) * p.heads + job.head;
+        ks = p.k_scale[at];
+        vs = p.v_scale[at];
+    };
     uint4 k[kLoads], v[kLoads];
     int blocks = blocks_of(0), next = blocks_of(1);
+    float ks, vs;
     load(p.k_cache, 0, blocks, k);
+    scales_of(blocks, ks, vs);
     for (int i = 0; i < steps; ++i) {
         const int stage = i & 1, phase = ((i >> 1) & 1) ^ 1;
         load(p.v_cache, i, blocks, v);
-        float ks = 0.0f, log_v = kNone, inv_v = 0.0f;
-        if (tid < 8 && blocks >= 0) {
-            const int64_t at = (int64_t)blocks * p.heads + job.head;
-            const float vs = p.v_scale[at];
-            ks = p.k_scale[at];
-            log_v = __log2f(vs);
-            inv_v = __frcp_rn(vs);
-        }
+        const int after = blocks_of(i + 2);
         if (i > 1 && !wait_warp(p, s, &s->k_empty[stage], phase, 411)) return;
-        store(sm + L::k + stage * L::tile, k);
+        store(sm + L::k + stage * L::tile, i, blocks, k);
         if (tid < 8) {
-            Scales& to = s->scales[i & 3];
-            to.k[tid] = ks;
-            to.log_v[tid] = log_v;
-            to.inv_v[tid] = inv_v;
+            // not there: no score of it counts
+            Scales& to = s->scales[i & 3][tid];
+            to.k = blocks < 0 ? 1.0f : ks;
+            to.log_v = blocks < 0 ? kNone : __log2f(vs);
+            to.inv_v = blocks < 0 ? 0.0f : __frcp_rn(vs);
         }
         arrive_warp(&s->k_full[stage]);
-        if (i + 1 < steps) load(p.k_cache, i + 1, next, k);
+        load(p.k_cache, i + 1, next, k);
+        scales_of(next, ks, vs);
         if (i > 1 && !wait_warp(p, s, &s->v_empty[stage], phase, 412)) return;
-        store(sm + L::v + stage * L::tile, v);
+        store(sm + L::v + stage * L::tile, i, blocks, v);
         arrive_warp(&s->v_full[stage]);
         blocks = next;
-        next = blocks_of(i + 2);
+        next = after;
     }
 }
 
 // ------------------------------------------------------------------ softmax
-template <bool MASKED>
-__device__ __forceinline__ float largest(const uint32_t (&r)[16], int seen) {
-    float top = kNone;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const float x = __uint_as_float(r[j]);
-        top = fmaxf(top, MASKED && j >= seen ? kNone : x);
-    }
-    return top;
-}
-
-// 16 scores to weights, as pairs; their sum.
-template <bool MASKED>
-__device__ __forceinline__ float weights(const uint32_t (&r)[16], float f, float offset, int seen,
-                                         uint32_t* pairs) {
-    float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-        float e[2];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            e[n] = exp2_of(fmaf(__uint_as_float(r[j + n]), f, offset));
-            if (MASKED && j + n >= seen) e[n] = 0.0f;
-            sum[n] += e[n];
-        }
-        pairs[j / 2] = half2_of(e[0], e[1]);
-    }
-    return sum[0] + sum[1];
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+        "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr));
 }
 
 template <int D>
@@ -416,28 +423,42 @@ __device__ __forceinline__ void soften(const CacheAttention& p, const Job& job, 
     float m = kNone, l = 0.0f;
     bool ok = true;
     for (int i = 0; i < steps; ++i) {
-        const int first = i * kTokens, seen = limit - first;
+        const int first = i * kTokens;
         const bool masked = first + kTokens > fewest;
         // (the scales were written before the keys that the scores are of)
+        const Scales* sc = s->scales[i & 3];
         ok = wait_warp(p, s, &s->s_full[t], i & 1, 422);
         if (!ok) break;
         tc_fence_after();
-        const Scales& sc = s->scales[i & 3];
+        uint32_t r[kTokens];
+#pragma unroll
+        for (int c = 0; c < kTokens; c += 32) tmem_ld32(cs + c, r + c);
+        tmem_wait_ld();
+        if (masked) {       // scores in full, and none where a row sees nothing
+            const int seen = limit - first;
+#pragma unroll
+            for (int j = 0; j < kTokens; ++j) {
+                const float x = fmaf(__uint_as_float(r[j]), factor * sc[j / 16].k, sc[j / 16].log_v);
+                r[j] = __float_as_uint(j < seen ? x : kNone);
+            }
+        }
+        // (the groups side by side, so that no maximum waits for the one before)
+        float tops[kTokens / 16];
+#pragma unroll
+        for (int g = 0; g < kTokens / 16; ++g) tops[g] = __uint_as_float(r[16 * g]);
+#pragma unroll
+        for (int j = 1; j < 15; j += 2) {
+#pragma unroll
+            for (int g = 0; g < kTokens / 16; ++g) {
+                tops[g] = fmaxf(fmaxf(tops[g], __uint_as_float(r[16 * g + j])),
+                                __uint_as_float(r[16 * g + j + 1]));
+            }
+        }
         float top = kNone;
 #pragma unroll
-        for (int g = 0; g < 8; g += 2) {
-            uint32_t r[2][16];
-            tmem_ld16(cs + 16 * g, r[0]);
-            tmem_ld16(cs + 16 * g + 16, r[1]);
-            tmem_wait_ld();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float x = masked ? largest<true>(r[h], seen - 16 * (g + h))
-                                       : largest<false>(r[h], 16);
-                // (the factor of a block that is not there is 0: no score of it counts)
-                const float y = fmaf(x, factor * sc.k[g + h], sc.log_v[g + h]);
-                top = fmaxf(top, x == kNone ? kNone : y);
-            }
+        for (int g = 0; g < kTokens / 16; ++g) {
+            tops[g] = fmaxf(tops[g], __uint_as_float(r[16 * g + 15]));
+            top = fmaxf(top, masked ? tops[g] : fmaf(tops[g], factor * sc[g].k, sc[g].log_v));
         }
         const bool raise = top > m + kSlack;
         if (__any_sync(0xffffffffu, raise)) {
@@ -449,41 +470,54 @@ __device__ __forceinline__ void soften(const CacheAttention& p, const Job& job, 
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t r[2][16];
-                    tmem_ld16(co + c, r[0]);
-                    tmem_ld16(co + c + 16, r[1]);
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t x[16];
+                    tmem_ld16(co + c, x);
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        r[0][j] = __float_as_uint(__uint_as_float(r[0][j]) * less);
-                        r[1][j] = __float_as_uint(__uint_as_float(r[1][j]) * less);
+                        x[j] = __float_as_uint(__uint_as_float(x[j]) * less);
                     }
-                    tmem_st16(co + c, r[0]);
-                    tmem_st16(co + c + 16, r[1]);
+                    tmem_st16(co + c, x);
                 }
             }
         }
         const float ref = (m == kNone ? 0.0f : m) - kRaise;
 #pragma unroll
-        for (int g = 0; g < 8; g += 2) {
-            uint32_t r[2][16], pairs[16];
-            tmem_ld16(cs + 16 * g, r[0]);
-            tmem_ld16(cs + 16 * g + 16, r[1]);
-            tmem_wait_ld();
+        for (int h = 0; h < kTokens / 32; ++h) {
+            uint64_t x[16];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float f = factor * sc.k[g + h], offset = sc.log_v[g + h] - ref;
-                const float sum = masked
-                    ? weights<true>(r[h], f, offset, seen - 16 * (g + h), pairs + 8 * h)
-                    : weights<false>(r[h], f, offset, 16, pairs + 8 * h);
-                l = fmaf(sum, sc.inv_v[g + h], l);
+            for (int g = 0; g < 2; ++g) {
+                const float f = masked ? 1.0f : factor * sc[2 * h + g].k;
+                const float off = (masked ? 0.0f : sc[2 * h + g].log_v) - ref;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int c = 32 * h + 16 * g + 2 * j;
+                    x[8 * g + j] = fma2(two(r[c], r[c + 1]), two(f, f), two(off, off));
+                }
             }
-            tmem_st16(cs + 8 * g, pairs);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                float lo, hi;
+                apart(x[j], lo, hi);
+                lo = exp2_of(lo);
+                hi = exp2_of(hi);
+                x[j] = two(lo, hi);
+                r[16 * h + j] = half2_of(lo, hi);
+            }
+            tmem_st16(cs + 16 * h, *reinterpret_cast<const uint32_t (*)[16]>(r + 16 * h));
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const uint64_t* y = x + 8 * g;
+                const uint64_t sum = add2(add2(add2(y[0], y[1]), add2(y[2], y[3])),
+                                          add2(add2(y[4], y[5]), add2(y[6], y[7])));
+                l = fmaf(sum2(sum), sc[2 * h + g].inv_v, l);
+            }
         }
         tmem_wait_st();
         tc_fence_before();
         arrive_warp(&s->p_full[t]);
+        if (i == 0 && t == 0) arrive_warp(&s->go);
     }
     if (ok && steps > 0) ok = wait_warp(p, s, &s->o_full[t], (steps - 1) & 1, 424);
     tc_fence_after();
@@ -573,17 +607,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_prompt_kernel(CacheAttentio
     if (p.clears && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
     Job job;
     if (!job_of(p, blockIdx.x / p.heads, blockIdx.x % p.heads, job)) return;
+    const int tiles = job.rows > kRows ? 2 : 1;
     if (threadIdx.x == 32 * kIssueWarp) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s->k_full[i], kFillWarps);
             mbar_init(&s->v_full[i], kFillWarps);
-            mbar_init(&s->k_empty[i], 1);
-            mbar_init(&s->v_empty[i], 1);
+            mbar_init(&s->k_empty[i], tiles);
+            mbar_init(&s->v_empty[i], tiles);
             mbar_init(&s->s_full[i], 1);
             mbar_init(&s->p_full[i], kSoftWarps / 2);
             mbar_init(&s->o_full[i], 1);
+            mbar_init(&s->fin[i], 1);
         }
-        mbar_init(&s->fin, 1);
+        mbar_init(&s->go, kSoftWarps / 2);
         s->abort = 0;
         fence_mbar_init();
     }
@@ -598,16 +634,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_prompt_kernel(CacheAttentio
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const int tiles = job.rows > kRows ? 2 : 1;
     const int high = job.hidden + (job.row0 + job.rows - 1) / p.group;
     const int steps = high > 0 ? (high + kTokens - 1) / kTokens : 0;
     if (w < kSoftWarps) {
+        take_registers<kSoftRegs>();
         const int t = threadIdx.x >> 7;
         if (t < tiles) soften<D>(p, job, s, sm, steps, t, factor);
     } else if (w < kIssueWarp) {
+        give_registers<kFillRegs>();
         fill<D>(p, job, s, sm, steps, high);
-    } else if (steps > 0) {
-        issue<D>(p, s, smem_u32(sm), steps, tiles);
+    } else {
+        give_registers<kIssueRegs>();
+        const int t = w - kIssueWarp;
+        if (t < tiles) issue<D>(p, s, smem_u32(sm), steps, t);
     }
     __syncwarp();
     tc_fence_before();

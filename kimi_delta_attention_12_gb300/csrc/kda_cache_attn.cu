@@ -25,6 +25,7 @@
 // ceil(tokens / 64) units, and every block takes the same stretch of units.  An item that lies
 // across blocks leaves partial sums, which a second kernel joins.  The 4 warps of a block take
 // 16 tokens of a unit each, with sums of their own that meet at the item's end.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -38,11 +39,11 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kUnit = 16 * kWarps;       // tokens of a unit
 constexpr int kJoinThreads = 256;
 constexpr float kNone = -INFINITY;
 constexpr float kRaise = 15.0f;
 constexpr int64_t kManyRows = 64, kManyWork = 4096;
+constexpr int kRounds = 24;          // of a warp in a cluster
 
 // Blocks that an SM holds at once, by the rows of a tile.
 __host__ __device__ constexpr int blocks_per_sm(int NT) { return NT == 1 ? 3 : 2; }
@@ -61,6 +62,8 @@ struct Span {
     int64_t all;              // units of the request
 };
 
+// UNIT: tokens of a unit, 16 for each warp.
+template <int UNIT>
 __device__ __forceinline__ Span span_of(const CacheAttention& p, int i, int R) {
     Span s;
     int64_t bos, eos;
@@ -79,7 +82,7 @@ __device__ __forceinline__ Span span_of(const CacheAttention& p, int i, int R) {
     s.tokens = (int)(c < 0 ? 0 : (c < most ? c : most));
     const int64_t rows = (int64_t)s.fresh * p.group;
     s.tiles = rows < p.many_rows ? (int)((rows + R - 1) / R) : 0;
-    s.units = s.tokens > 0 ? (int)(((int64_t)s.tokens + kUnit - 1) / kUnit) : 1;
+    s.units = s.tokens > 0 ? (int)(((int64_t)s.tokens + UNIT - 1) / UNIT) : 1;
     s.all = (int64_t)s.tiles * p.heads * s.units;
     return s;
 }
@@ -91,7 +94,7 @@ struct Stretch {
     int request;
 };
 
-template <int THREADS>
+template <int THREADS, int UNIT = 16 * kWarps>
 __device__ __forceinline__ Stretch stretch_of(const CacheAttention& p, int R, int block,
                                               int blocks) {
     __shared__ int64_t sums[THREADS / 32 + 1];
@@ -101,7 +104,7 @@ __device__ __forceinline__ Stretch stretch_of(const CacheAttention& p, int R, in
     const int k = (p.N + THREADS - 1) / THREADS;      // requests of a thread, neighbours
     const int i0 = threadIdx.x * k, i1 = i0 + k < p.N ? i0 + k : p.N;
     int64_t mine = 0;
-    for (int i = i0; i < i1; ++i) mine += span_of(p, i, R).all;
+    for (int i = i0; i < i1; ++i) mine += span_of<UNIT>(p, i, R).all;
     int64_t x = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -125,7 +128,7 @@ __device__ __forceinline__ Stretch stretch_of(const CacheAttention& p, int R, in
     int64_t at = before + x - mine;
     if (s.begin < total && at <= s.begin && s.begin < at + mine) {
         for (int i = i0; i < i1; ++i) {
-            const int64_t all = span_of(p, i, R).all;
+            const int64_t all = span_of<UNIT>(p, i, R).all;
             if (s.begin < at + all) {
                 found = i;
                 found_first = at;
@@ -143,10 +146,11 @@ __device__ __forceinline__ Stretch stretch_of(const CacheAttention& p, int R, in
 // The item of unit `at`, from request i on, whose units begin at `first`.
 __device__ __forceinline__ Item item_at(const CacheAttention& p, int R, int64_t at, int& i,
                                         int64_t& first) {
-    Span s = span_of(p, i, R);
+    constexpr int UNIT = 16 * kWarps;
+    Span s = span_of<UNIT>(p, i, R);
     while (at >= first + s.all && i + 1 < p.N) {
         first += s.all;
-        s = span_of(p, ++i, R);
+        s = span_of<UNIT>(p, ++i, R);
     }
     Item t;
     const int64_t n = (at - first) / s.units;
@@ -263,282 +267,310 @@ __device__ __forceinline__ void load_tokens(const CacheAttention& p, Tokens<D>& 
     }
 }
 
-template <int D, int NT, bool F32>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) cache_attention_kernel(
-    CacheAttention p) {
-    constexpr int R = 8 * NT, kSteps = D / 16, Q = F32 ? 2 : 1;
-    extern __shared__ float sums[];          // [kWarps][R][D], then m and l [kWarps][R] each
-    float* sums_m = sums + kWarps * R * D;
-    float* sums_l = sums_m + kWarps * R;
-    let_follow();
-    if (p.clears && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+// Units unit0 .. unit0 + units - 1 of an item by WARPS warps: every warp's sums [WARPS][R][D] in
+// `sums`, then their references and weights [WARPS][R] each.
+template <int D, int NT, bool F32, int WARPS>
+__device__ __forceinline__ void attend(const CacheAttention& p, const Item& it, int unit0,
+                                       int units, float* sums) {
+    constexpr int R = 8 * NT, kSteps = D / 16, Q = F32 ? 2 : 1, UNIT = 16 * WARPS;
+    float* sums_m = sums + WARPS * R * D;
+    float* sums_l = sums_m + WARPS * R;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    const Stretch s = stretch_of<kThreads>(p, R, blockIdx.x, gridDim.x);
-    if (s.request < 0) return;
-    int request = s.request;
-    int64_t first = s.first;
-    const int heads_q = p.heads * p.group;
-    for (int64_t at = s.begin; at < s.end;) {
-        const Item it = item_at(p, R, at, request, first);
-        const int unit0 = (int)(at - it.begin);
-        const int units = (int)(s.end - at < it.units - unit0 ? s.end - at : it.units - unit0);
-        const int rows = it.fresh * p.group - it.tile * R;      // of this tile, may be above R
-        const int hidden = it.tokens - it.fresh + 1;            // keys that new token 0 sees
-        // ---- q of this lane's column, scaled to [1, 2) and in fp16
-        uint32_t q[Q][NT][kSteps][2];
-        float factor[NT][2];                 // of a score, for the columns 2 c and 2 c + 1
-        int limit[NT][2], low = 0x7fffffff, high = 0;
+    const int rows = it.fresh * p.group - it.tile * R;      // of this tile, may be above R
+    const int hidden = it.tokens - it.fresh + 1;            // keys that new token 0 sees
+    const int last = rows < R ? rows : R;
+    const int low = hidden + it.tile * R / p.group;                  // what the tile's first row
+    const int high = hidden + (it.tile * R + last - 1) / p.group;    // and its last row see
+    // ---- the first tokens on their way
+    const int32_t* table = p.table + (int64_t)it.request * p.width;
+    int ids = -1;                        // of the blocks of 32 units, one in each lane
+    float k_scale = 0.0f, v_scale = 1.0f;
+    auto look_up = [&](int u) {
+        const int base = (unit0 + u + lane) * UNIT + 16 * w;
+        ids = u + lane < units && base < high ? table[base >> p.block_log2] : -1;
+        k_scale = 0.0f;
+        v_scale = 1.0f;
+        if (ids >= 0 && ids < p.num_blocks) {
+            k_scale = p.k_scale[(int64_t)ids * p.heads + it.head];
+            v_scale = p.v_scale[(int64_t)ids * p.heads + it.head];
+        }
+    };
+    int u0 = 0, n = units < 32 ? units : 32;     // units of which `ids` holds the blocks
+    Tokens<D> x, y;
+    auto load = [&](Tokens<D>& to, int u) {
+        load_tokens<D>(p, to, it.head, __shfl_sync(0xffffffffu, ids, u & 31),
+                       (unit0 + u0 + u) * UNIT + 16 * w, u < n ? high : 0, lane);
+    };
+    look_up(0);
+    load(x, 0);
+    load(y, 1);
+    // ---- q of this lane's column, scaled to [1, 2) and in fp16
+    uint32_t q[Q][NT][kSteps][2];
+    float factor[NT][2];                 // of a score, for the columns 2 c and 2 c + 1
+    int limit[NT][2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int n = 8 * t + g, flat = it.tile * R + n, j = flat / p.group;
-            float x[kSteps][4], top = 0.0f;
-            const int64_t base = (it.row0 + j) * p.q_stride +
-                                 (int64_t)(it.head * p.group + flat - j * p.group) * D;
+    for (int t = 0; t < NT; ++t) {
+        const int own = 8 * t + g, flat = it.tile * R + own, j = flat / p.group;
+        float v[kSteps][4], top = 0.0f;
+        const int64_t base = (it.row0 + j) * p.q_stride +
+                             (int64_t)(it.head * p.group + flat - j * p.group) * D;
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                const int d = k_channel<D>(i, c);
-                if (n >= rows) {
+        for (int i = 0; i < kSteps; ++i) {
+            const int d = k_channel<D>(i, c);
+            if (own >= rows) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[i][e] = 0.0f;
-                } else if (F32) {
-                    const float4 f = *reinterpret_cast<const float4*>(
-                        static_cast<const float*>(p.q) + base + d);
-                    x[i][0] = f.x; x[i][1] = f.y; x[i][2] = f.z; x[i][3] = f.w;
-                } else {
-                    const uint2 f = *reinterpret_cast<const uint2*>(
-                        static_cast<const __nv_bfloat16*>(p.q) + base + d);
-                    x[i][0] = __uint_as_float(f.x << 16);
-                    x[i][1] = __uint_as_float(f.x & 0xffff0000u);
-                    x[i][2] = __uint_as_float(f.y << 16);
-                    x[i][3] = __uint_as_float(f.y & 0xffff0000u);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(x[i][e]));
+                for (int e = 0; e < 4; ++e) v[i][e] = 0.0f;
+            } else if (F32) {
+                const float4 f = *reinterpret_cast<const float4*>(
+                    static_cast<const float*>(p.q) + base + d);
+                v[i][0] = f.x; v[i][1] = f.y; v[i][2] = f.z; v[i][3] = f.w;
+            } else {
+                const uint2 f = *reinterpret_cast<const uint2*>(
+                    static_cast<const __nv_bfloat16*>(p.q) + base + d);
+                v[i][0] = __uint_as_float(f.x << 16);
+                v[i][1] = __uint_as_float(f.x & 0xffff0000u);
+                v[i][2] = __uint_as_float(f.y << 16);
+                v[i][3] = __uint_as_float(f.y & 0xffff0000u);
             }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            int e = __float_as_int(top) >> 23;
-            e = e < 1 ? 1 : (e > 253 ? 253 : e);
-            const float down = __int_as_float((254 - e) << 23), up = __int_as_float(e << 23);
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(v[i][e]));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        int e = __float_as_int(top) >> 23;
+        e = e < 1 ? 1 : (e > 253 ? 253 : e);
+        const float down = __int_as_float((254 - e) << 23), up = __int_as_float(e << 23);
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const float lo = x[i][2 * b] * down, hi = x[i][2 * b + 1] * down;
-                    q[0][t][i][b] = half2_of(lo, hi);
-                    if (F32) q[Q - 1][t][i][b] = rest_of(lo, hi, q[0][t][i][b]);
-                }
-            }
+        for (int i = 0; i < kSteps; ++i) {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int col = 2 * c + b;
-                factor[t][b] = __shfl_sync(0xffffffffu, up, 4 * col) *
-                               (p.scale * 1.44269504088896340736f);
-                const int nb = 8 * t + col, fb = it.tile * R + nb;
-                limit[t][b] = nb < rows ? hidden + fb / p.group : 0x7fffffff;
+                const float lo = v[i][2 * b] * down, hi = v[i][2 * b + 1] * down;
+                q[0][t][i][b] = half2_of(lo, hi);
+                if (F32) q[Q - 1][t][i][b] = rest_of(lo, hi, q[0][t][i][b]);
             }
         }
-        {
-            const int last = rows < R ? rows : R;
-            low = hidden + it.tile * R / p.group;
-            high = hidden + (it.tile * R + last - 1) / p.group;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int col = 2 * c + b;
+            factor[t][b] = __shfl_sync(0xffffffffu, up, 4 * col) *
+                           (p.scale * 1.44269504088896340736f);
+            const int nb = 8 * t + col, fb = it.tile * R + nb;
+            limit[t][b] = nb < rows ? hidden + fb / p.group : 0x7fffffff;
         }
-        // ---- this warp's part of the units
-        float o[NT][kSteps][4], m[NT][2], l[NT][2];
+    }
+    // ---- this warp's part of the units
+    float o[NT][kSteps][4], m[NT][2], l[NT][2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            m[t][0] = m[t][1] = kNone;
-            l[t][0] = l[t][1] = 0.0f;
+    for (int t = 0; t < NT; ++t) {
+        m[t][0] = m[t][1] = kNone;
+        l[t][0] = l[t][1] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.0f;
-            }
+        for (int i = 0; i < kSteps; ++i) {
+            o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.0f;
         }
-        const int32_t* table = p.table + (int64_t)it.request * p.width;
-        int ids = -1;                        // of the blocks of 32 units, one in each lane
-        float k_scale = 0.0f, v_scale = 1.0f;
-        auto look_up = [&](int u) {
-            const int base = (unit0 + u + lane) * kUnit + 16 * w;
-            ids = u + lane < units && base < high ? table[base >> p.block_log2] : -1;
-            k_scale = 0.0f;
-            v_scale = 1.0f;
-            if (ids >= 0 && ids < p.num_blocks) {
-                k_scale = p.k_scale[(int64_t)ids * p.heads + it.head];
-                v_scale = p.v_scale[(int64_t)ids * p.heads + it.head];
-            }
-        };
-        auto multiply = [&](const Tokens<D>& x, int u, float ks, float vs, bool there) {
-            const int base = (unit0 + u) * kUnit + 16 * w;
-            if (base >= high || !there) return;
-            float sc[NT][4];
+    }
+    auto multiply = [&](const Tokens<D>& x, int u, float ks, float vs, bool there) {
+        const int base = (unit0 + u) * UNIT + 16 * w;
+        if (base >= high || !there) return;
+        float sc[NT][4];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.0f;
+        for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                const uint32_t a0 = half2_of_e4m3(x.k[0][i]), a1 = half2_of_e4m3(x.k[1][i]);
-                const uint32_t a2 = half2_of_e4m3_high(x.k[0][i]);
-                const uint32_t a3 = half2_of_e4m3_high(x.k[1][i]);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-#pragma unroll
-                    for (int h = 0; h < Q; ++h) {
-                        mma(sc[t], a0, a1, a2, a3, q[h][t][i][0], q[h][t][i][1]);
-                    }
-                }
-            }
-            const float lv = __log2f(vs), iv = __frcp_rn(vs);
-            const bool partly = base + 16 > low;
-            uint32_t b[Q][NT][2];
+        for (int i = 0; i < kSteps; ++i) {
+            const uint32_t a0 = half2_of_e4m3(x.k[0][i]), a1 = half2_of_e4m3(x.k[1][i]);
+            const uint32_t a2 = half2_of_e4m3_high(x.k[0][i]);
+            const uint32_t a3 = half2_of_e4m3_high(x.k[1][i]);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float f = factor[t][n] * ks;
-                    float s0 = fmaf(sc[t][n], f, lv), s1 = fmaf(sc[t][n + 2], f, lv);
-                    if (partly) {
-                        s0 = base + g < limit[t][n] ? s0 : kNone;
-                        s1 = base + g + 8 < limit[t][n] ? s1 : kNone;
-                    }
-                    sc[t][n] = s0;
-                    sc[t][n + 2] = s1;
+                for (int h = 0; h < Q; ++h) {
+                    mma(sc[t], a0, a1, a2, a3, q[h][t][i][0], q[h][t][i][1]);
                 }
-            }
-            float up[NT][2];
-            bool more = false;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    float x = fmaxf(sc[t][n], sc[t][n + 2]);
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                    up[t][n] = fmaxf(m[t][n], x);
-                    more |= up[t][n] > m[t][n];
-                }
-            }
-            if (__any_sync(0xffffffffu, more)) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    float less[2];
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        less[n] = up[t][n] > m[t][n] ? exp2_of(m[t][n] - up[t][n]) : 1.0f;
-                        m[t][n] = up[t][n];
-                        l[t][n] *= less[n];
-                    }
-#pragma unroll
-                    for (int i = 0; i < kSteps; ++i) {
-                        o[t][i][0] *= less[0];
-                        o[t][i][1] *= less[1];
-                        o[t][i][2] *= less[0];
-                        o[t][i][3] *= less[1];
-                    }
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                float e[4];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float top = (m[t][n] == kNone ? 0.0f : m[t][n]) - kRaise;
-                    e[n] = exp2_of(sc[t][n] - top);
-                    e[n + 2] = exp2_of(sc[t][n + 2] - top);
-                    l[t][n] = fmaf(e[n] + e[n + 2], iv, l[t][n]);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t pair = half2_of(e[2 * h], e[2 * h + 1]);
-                    b[0][t][h] = transposed(pair);
-                    if (F32) {
-                        b[Q - 1][t][h] = transposed(rest_of(e[2 * h], e[2 * h + 1], pair));
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                // channels 2 i and 2 i + 1 of this lane's D / 8, of four tokens
-                uint32_t pair[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    pair[h] = __byte_perm(x.v[2 * h][i / 2], x.v[2 * h + 1][i / 2],
-                                          i & 1 ? 0x7362 : 0x5140);
-                }
-                const uint32_t a0 = half2_of_e4m3(pair[0]), a1 = half2_of_e4m3_high(pair[0]);
-                const uint32_t a2 = half2_of_e4m3(pair[1]), a3 = half2_of_e4m3_high(pair[1]);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-#pragma unroll
-                    for (int h = 0; h < Q; ++h) mma(o[t][i], a0, a1, a2, a3, b[h][t][0], b[h][t][1]);
-                }
-            }
-        };
-        for (int u0 = 0; u0 < units; u0 += 32) {
-            look_up(u0);
-            const int n = units - u0 < 32 ? units - u0 : 32;
-            Tokens<D> x, y;
-            auto load = [&](Tokens<D>& to, int u) {
-                load_tokens<D>(p, to, it.head, __shfl_sync(0xffffffffu, ids, u & 31),
-                               (unit0 + u0 + u) * kUnit + 16 * w, u < n ? high : 0, lane);
-            };
-            auto take = [&](const Tokens<D>& from, int u) {
-                const int id = __shfl_sync(0xffffffffu, ids, u);
-                const float ks = __shfl_sync(0xffffffffu, k_scale, u);
-                const float vs = __shfl_sync(0xffffffffu, v_scale, u);
-                multiply(from, u0 + u, ks, vs, id >= 0 && id < p.num_blocks);
-            };
-            load(x, 0);
-            load(y, 1);
-            for (int u = 0; u < n; u += 2) {
-                take(x, u);
-                load(x, u + 2);
-                if (u + 1 < n) take(y, u + 1);
-                load(y, u + 3);
             }
         }
-        // ---- the four warps' sums meet
+        const float lv = __log2f(vs), iv = __frcp_rn(vs);
+        const bool partly = base + 16 > low;
+        uint32_t b[Q][NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
+                const float f = factor[t][n] * ks;
+                float s0 = fmaf(sc[t][n], f, lv), s1 = fmaf(sc[t][n + 2], f, lv);
+                if (partly) {
+                    s0 = base + g < limit[t][n] ? s0 : kNone;
+                    s1 = base + g + 8 < limit[t][n] ? s1 : kNone;
+                }
+                sc[t][n] = s0;
+                sc[t][n + 2] = s1;
+            }
+        }
+        float up[NT][2];
+        bool more = false;
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) {
-                    l[t][n] += __shfl_xor_sync(0xffffffffu, l[t][n], d);
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                float x = fmaxf(sc[t][n], sc[t][n + 2]);
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                up[t][n] = fmaxf(m[t][n], x);
+                more |= up[t][n] > m[t][n];
+            }
+        }
+        if (__any_sync(0xffffffffu, more)) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float less[2];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    less[n] = up[t][n] > m[t][n] ? exp2_of(m[t][n] - up[t][n]) : 1.0f;
+                    m[t][n] = up[t][n];
+                    l[t][n] *= less[n];
                 }
-                const int col = 8 * t + 2 * c + n;
-                if (g == 0) {
-                    sums_m[w * R + col] = m[t][n];
-                    sums_l[w * R + col] = l[t][n];
-                }
-                float* to = sums + (w * R + col) * D + g * (D / 8);
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) {
-                    to[2 * i] = o[t][i][n];
-                    to[2 * i + 1] = o[t][i][n + 2];
+                    o[t][i][0] *= less[0];
+                    o[t][i][1] *= less[1];
+                    o[t][i][2] *= less[0];
+                    o[t][i][3] *= less[1];
                 }
             }
         }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float e[4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const float top = (m[t][n] == kNone ? 0.0f : m[t][n]) - kRaise;
+                e[n] = exp2_of(sc[t][n] - top);
+                e[n + 2] = exp2_of(sc[t][n + 2] - top);
+                l[t][n] = fmaf(e[n] + e[n + 2], iv, l[t][n]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t pair = half2_of(e[2 * h], e[2 * h + 1]);
+                b[0][t][h] = transposed(pair);
+                if (F32) {
+                    b[Q - 1][t][h] = transposed(rest_of(e[2 * h], e[2 * h + 1], pair));
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            // channels 2 i and 2 i + 1 of this lane's D / 8, of four tokens
+            uint32_t pair[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                pair[h] = __byte_perm(x.v[2 * h][i / 2], x.v[2 * h + 1][i / 2],
+                                      i & 1 ? 0x7362 : 0x5140);
+            }
+            const uint32_t a0 = half2_of_e4m3(pair[0]), a1 = half2_of_e4m3_high(pair[0]);
+            const uint32_t a2 = half2_of_e4m3(pair[1]), a3 = half2_of_e4m3_high(pair[1]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int h = 0; h < Q; ++h) mma(o[t][i], a0, a1, a2, a3, b[h][t][0], b[h][t][1]);
+            }
+        }
+    };
+    auto take = [&](const Tokens<D>& from, int u) {
+        const int id = __shfl_sync(0xffffffffu, ids, u);
+        const float ks = __shfl_sync(0xffffffffu, k_scale, u);
+        const float vs = __shfl_sync(0xffffffffu, v_scale, u);
+        multiply(from, u0 + u, ks, vs, id >= 0 && id < p.num_blocks);
+    };
+    while (u0 < units) {
+        for (int u = 0; u < n; u += 2) {
+            take(x, u);
+            load(x, u + 2);
+            if (u + 1 < n) take(y, u + 1);
+            load(y, u + 3);
+        }
+        u0 += 32;
+        if (u0 >= units) break;
+        n = units - u0 < 32 ? units - u0 : 32;
+        look_up(u0);
+        load(x, 0);
+        load(y, 1);
+    }
+    // ---- the warps' sums, to where they meet
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+                l[t][n] += __shfl_xor_sync(0xffffffffu, l[t][n], d);
+            }
+            const int col = 8 * t + 2 * c + n;
+            if (g == 0) {
+                sums_m[w * R + col] = m[t][n];
+                sums_l[w * R + col] = l[t][n];
+            }
+            float* to = sums + (w * R + col) * D + g * (D / 8);
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                to[2 * i] = o[t][i][n];
+                to[2 * i + 1] = o[t][i][n + 2];
+            }
+        }
+    }
+}
+
+// Channel d of row n from the warps' sums, with the reference and weight of all of them.
+template <int D, int R, int WARPS>
+__device__ __forceinline__ void meet(const float* sums, int n, int d, float& total, float& weight,
+                                     float& top) {
+    const float* sums_m = sums + WARPS * R * D;
+    const float* sums_l = sums_m + WARPS * R;
+    top = kNone;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) top = fmaxf(top, sums_m[k * R + n]);
+    const float ref = top == kNone ? 0.0f : top;
+    total = weight = 0.0f;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) {
+        const float f = exp2_of(sums_m[k * R + n] - ref);
+        total = fmaf(f, sums[(k * R + n) * D + d], total);
+        weight = fmaf(f, sums_l[k * R + n], weight);
+    }
+}
+
+// Where row n of an item's tile goes in o.
+__device__ __forceinline__ int64_t place_of(const CacheAttention& p, const Item& it, int R, int n,
+                                            int D) {
+    const int flat = it.tile * R + n, j = flat / p.group;
+    return ((it.row0 + j) * (p.heads * p.group) + it.head * p.group + flat - j * p.group) * D;
+}
+
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) cache_attention_kernel(
+    CacheAttention p) {
+    constexpr int R = 8 * NT;
+    extern __shared__ float sums[];
+    let_follow();
+    if (p.clears && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+    const Stretch s = stretch_of<kThreads>(p, R, blockIdx.x, gridDim.x);
+    if (s.request < 0) return;
+    int request = s.request;
+    int64_t first = s.first;
+    for (int64_t at = s.begin; at < s.end;) {
+        const Item it = item_at(p, R, at, request, first);
+        const int unit0 = (int)(at - it.begin);
+        const int units = (int)(s.end - at < it.units - unit0 ? s.end - at : it.units - unit0);
+        attend<D, NT, F32, kWarps>(p, it, unit0, units, sums);
         __syncthreads();
-        const int valid = rows < R ? rows : R;
+        const int rows = it.fresh * p.group - it.tile * R, valid = rows < R ? rows : R;
         const bool whole = unit0 == 0 && units == it.units;
         float* part = p.partial + (int64_t)(blockIdx.x * 2 + (at != s.begin)) * R * (D + 2);
         for (int i = threadIdx.x; i < valid * D; i += kThreads) {
             const int n = i / D, d = i - n * D;
-            float top = kNone;
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) top = fmaxf(top, sums_m[k * R + n]);
-            const float ref = top == kNone ? 0.0f : top;
-            float total = 0.0f, weight = 0.0f;
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                const float f = exp2_of(sums_m[k * R + n] - ref);
-                total = fmaf(f, sums[(k * R + n) * D + d], total);
-                weight = fmaf(f, sums_l[k * R + n], weight);
-            }
+            float total, weight, top;
+            meet<D, R, kWarps>(sums, n, d, total, weight, top);
             if (whole) {
-                const int flat = it.tile * R + n, j = flat / p.group;
-                const int64_t to = ((it.row0 + j) * heads_q + it.head * p.group + flat -
-                                    j * p.group) * D + d;
+                const int64_t to = place_of(p, it, R, n, D) + d;
                 const float y = weight == 0.0f ? 0.0f : total / weight;
                 if (F32) {
                     static_cast<float*>(p.o)[to] = y;
@@ -555,6 +587,87 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) cache_attention_k
         }
         __syncthreads();
         at += units;
+    }
+}
+
+// Four neighbouring channels of the result.
+template <bool F32>
+__device__ __forceinline__ void store4(void* o, int64_t to, const float4& y, float by) {
+    if (F32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(o) + to) =
+            make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
+    } else {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x * by, y.y * by);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(y.z * by, y.w * by);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o) + to) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                       *reinterpret_cast<const uint32_t*>(&hi));
+    }
+}
+
+// Few requests and heads: a cluster of blocks for each, which share its tokens and join their sums
+// through one another's shared memory, all in one launch.
+__host__ __device__ constexpr int cluster_warps(int NT) { return NT == 1 ? 8 : 4; }
+
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(32 * cluster_warps(NT), 1) cache_attention_cluster_kernel(
+    CacheAttention p) {
+    namespace cg = cooperative_groups;
+    constexpr int R = 8 * NT, W = cluster_warps(NT), kAll = 32 * W;
+    extern __shared__ float sums[];          // the warps', then this block's: [R][D], m, l [R]
+    float* block_o = sums + W * R * (D + 2);
+    float* block_m = block_o + R * D;
+    float* block_l = block_m + R;
+    if (p.clears && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int item = blockIdx.x / blocks;
+    Item it;
+    it.request = item / p.heads;
+    it.head = item - it.request * p.heads;
+    const Span s = span_of<16 * W>(p, it.request, R);
+    it.units = s.units;
+    it.tokens = s.tokens;
+    it.fresh = s.fresh;
+    it.row0 = s.row0;
+    const int per = (s.units + blocks - 1) / blocks;
+    const int unit0 = rank * per < s.units ? rank * per : s.units;
+    const int units = s.units - unit0 < per ? s.units - unit0 : per;
+    for (it.tile = 0; it.tile < s.tiles; ++it.tile) {
+        attend<D, NT, F32, W>(p, it, unit0, units, sums);
+        __syncthreads();
+        const int rows = it.fresh * p.group - it.tile * R, valid = rows < R ? rows : R;
+        for (int i = threadIdx.x; i < valid * D; i += kAll) {
+            const int n = i / D, d = i - n * D;
+            float weight, top;
+            meet<D, R, W>(sums, n, d, block_o[i], weight, top);
+            if (d == 0) {
+                block_m[n] = top;
+                block_l[n] = weight;
+            }
+        }
+        cluster.sync();
+        for (int i = rank * kAll + threadIdx.x; i < valid * D / 4; i += blocks * kAll) {
+            const int n = 4 * i / D;
+            float top = kNone, all = 0.0f;
+            for (int k = 0; k < blocks; ++k) top = fmaxf(top, cluster.map_shared_rank(block_m, k)[n]);
+            const float ref = top == kNone ? 0.0f : top;
+            float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int k = 0; k < blocks; ++k) {
+                const float f = exp2_of(cluster.map_shared_rank(block_m, k)[n] - ref);
+                const float4 x =
+                    *reinterpret_cast<const float4*>(cluster.map_shared_rank(block_o, k) + 4 * i);
+                all = fmaf(f, cluster.map_shared_rank(block_l, k)[n], all);
+                y.x = fmaf(f, x.x, y.x);
+                y.y = fmaf(f, x.y, y.y);
+                y.z = fmaf(f, x.z, y.z);
+                y.w = fmaf(f, x.w, y.w);
+            }
+            store4<F32>(p.o, place_of(p, it, R, n, D) + 4 * i - n * D, y,
+                        all == 0.0f ? 0.0f : 1.0f / all);
+        }
+        cluster.sync();                      // the others may still read this block's sums
     }
 }
 
@@ -596,7 +709,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(Cach
     }
     __syncthreads();
     // four channels to a thread; the threads left over share the parts
-    const int heads_q = p.heads * p.group, outs = valid * D / 4;
+    const int outs = valid * D / 4;
     const int sharers = outs >= kJoinThreads ? 1 : kJoinThreads / outs;
     for (int i0 = 0; i0 < outs; i0 += kJoinThreads) {
         const int share = i0 + kJoinThreads <= outs || sharers == 1 ? 0 : threadIdx.x / outs;
@@ -627,26 +740,54 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(Cach
             }
         }
         if (i >= outs) return;
-        const float all = total[n], by = all == 0.0f ? 0.0f : 1.0f / all;
-        const int flat = it.tile * R + n, j = flat / p.group;
-        const int64_t to =
-            ((it.row0 + j) * heads_q + it.head * p.group + flat - j * p.group) * D + d;
-        if (F32) {
-            *reinterpret_cast<float4*>(static_cast<float*>(p.o) + to) =
-                make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
-        } else {
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x * by, y.y * by);
-            const __nv_bfloat162 hi = __floats2bfloat162_rn(y.z * by, y.w * by);
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + to) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                           *reinterpret_cast<const uint32_t*>(&hi));
-        }
+        const float all = total[n];
+        store4<F32>(p.o, place_of(p, it, R, n, D) + d, y, all == 0.0f ? 0.0f : 1.0f / all);
     }
+}
+
+// Blocks of a cluster for each item of the call, 1: none.  Every SM gets a block at most, with
+// clusters of 8 every other one (they lie within a group of SMs, and 16 of them did not fit at
+// once), and a warp at most kRounds times 16 tokens; beyond, the even stretches over all SMs are
+// faster although they take two launches.  8 heads of d = 128, 4 rows each, clusters against
+// stretches, us: 1 request of 1K, 8K, 32K, 128K tokens 6.3, 11.1, 28.6, 114 against 10.8, 18.5,
+// 26.6, 56.7 (8 a cluster); 4 of 8K, 32K 17.1, 61.2 against 21.1, 51.4 (4); 8 of 4K 17.2 against
+// 20.3, 9 of 1K 8.3 against 15.0 (2).  Clusters of 16 took 17.0 for 1 of 8K.
+int cluster_of(const CacheAttention& p, int sms, int NT) {
+    const int64_t items = (int64_t)p.N * p.heads, most = (int64_t)p.width << p.block_log2;
+    for (int c = 8; c > 1; c /= 2) {
+        const bool fits = items * c <= (c == 8 ? sms / 2 : sms);
+        if (fits && most <= (int64_t)kRounds * c * 16 * cluster_warps(NT)) return c;
+    }
+    return 1;
+}
+
+template <int D, int NT, bool F32>
+cudaError_t launch_clusters(const CacheAttention& p, int blocks, cudaStream_t stream) {
+    auto kernel = cache_attention_cluster_kernel<D, NT, F32>;
+    constexpr int R = 8 * NT, W = cluster_warps(NT);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = blocks;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(p.N * p.heads * blocks);
+    config.blockDim = dim3(32 * W);
+    config.dynamicSmemBytes = (size_t)(W + 1) * R * (D + 2) * sizeof(float);
+    config.stream = stream;
+    config.attrs = &attr;
+    config.numAttrs = 1;
+    return cudaLaunchKernelEx(&config, kernel, p);
 }
 
 template <int D, int NT, bool F32>
 cudaError_t launch_tiles(const CacheAttention& p, int sms, cudaStream_t stream) {
     constexpr int R = 8 * NT;
+    // (rows that fill one tile at most: the work is the tokens alone)
+    const int cluster = (int64_t)p.group * p.max_new <= R ? cluster_of(p, sms, NT) : 1;
+    if (cluster > 1) {
+        if (launch_clusters<D, NT, F32>(p, cluster, stream) == cudaSuccess) return cudaSuccess;
+        cudaGetLastError();                  // a device that cannot take them (a part of a GPU)
+    }
     const size_t smem = (size_t)kWarps * R * (D + 2) * sizeof(float);
     const int blocks = sms * blocks_per_sm(NT);
     cache_attention_kernel<D, NT, F32><<<blocks, kThreads, smem, stream>>>(p);

@@ -45,6 +45,12 @@ class Batch:
                 torch.tensor(self.table, **i32), torch.tensor(self.context, **i32),
                 torch.tensor(self.cu, **i32))
 
+    def wide(self):
+        """A table too wide for the clusters, which would leave a warp too many tokens."""
+        t = torch.full((len(self.table), (1 << 16) // self.block), -1, dtype=torch.int32)
+        t[:, :len(self.table[0])] = torch.tensor(self.table, dtype=torch.int32)
+        return t.cuda()
+
     def check(self, got):
         o, *sizes = R.attention(self.q, self.k.numpy(), self.v.numpy(), self.ks.numpy(),
                                 self.vs.numpy(), self.table, self.context, self.cu, self.scale,
@@ -66,8 +72,22 @@ def test_single_tokens(G, d, dtype):
     past = [0, 1, 14, 15, 16, 17, 63, 64, 200, 701]
     b = Batch(past, [1] * len(past), block, 2 * G, 2, d, dtype, seed=G)
     args = b.args()
-    b.check(kda.kda_cache_attention(*args[:-1]))
+    b.check(kda.kda_cache_attention(*args[:-1]))        # few items: clusters
     b.check(kda.kda_cache_attention(*args, max_new=1))
+    b.check(kda.kda_cache_attention(*args[:5], b.wide(), args[6]))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N,H,G,d,new", [(1, 1, 4, 128, 1), (1, 3, 8, 64, 2), (2, 8, 2, 128, 3),
+                                         (5, 7, 1, 32, 5), (3, 25, 16, 64, 1), (1, 9, 7, 128, 2),
+                                         (1, 1, 64, 32, 1)])
+def test_few_items(N, H, G, d, new, dtype):
+    """Clusters of every size, tiles of one and two columns of eight, and the even stretches."""
+    past = [random.Random(i).choice([0, 5, 300, 1500, 4000]) for i in range(N)]
+    b = Batch(past, [new] * N, 32, G * H, H, d, dtype, seed=N + H)
+    args = b.args()
+    b.check(kda.kda_cache_attention(*args, max_new=new))
+    b.check(kda.kda_cache_attention(*args[:5], b.wide(), *args[6:], max_new=new))
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])

@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional, Tuple
@@ -1078,6 +1079,10 @@ def _row_stride(t: torch.Tensor, name: str, dev: int) -> int:
     return st[0] if rows > 1 else heads * d
 
 
+def _dense_like(t: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _rotary_call(name, q, k, positions, inv_freq, interleaved, first, magnitude, q_out, k_out,
                  stream, inverse):
     batch = None
@@ -1119,9 +1124,9 @@ def _rotary_call(name, q, k, positions, inv_freq, interleaved, first, magnitude,
         on.__enter__()
     try:
         if q_out is None:
-            q_out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
+            q_out = _dense_like(q)
         if k is not None and k_out is None:
-            k_out = torch.empty((T, Hk, d), dtype=dt, device=q.device)
+            k_out = _dense_like(k)
         flags = ((KDA_FLAG_ROTARY_INTERLEAVED if interleaved else 0)
                  | (KDA_FLAG_ROTARY_INVERSE if inverse else 0))
         st = lib().kda_rotary(q.data_ptr(), qs, _addr(k), ks, positions.data_ptr(),
@@ -1255,6 +1260,12 @@ def kda_cache_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cac
         raise KDAError(st, "kda_cache_write")
 
 
+@functools.lru_cache(maxsize=64)
+def _cache_attention_room(dev: int, Hq: int, Hkv: int, d: int, code: int) -> int:
+    """The workspace on device `dev`, which is the current one: the same for every call."""
+    return int(lib().kda_cache_attention_workspace_bytes(Hq, Hkv, d, code))
+
+
 def cache_attention_workspace_bytes(Hq: int, Hkv: int, d: int, dtype: torch.dtype) -> int:
     return int(lib().kda_cache_attention_workspace_bytes(Hq, Hkv, d, _dtype_code(dtype)))
 
@@ -1303,10 +1314,9 @@ def kda_cache_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
         on.__enter__()
     try:
         if o is None:
-            o = torch.empty((T, Hq, d), dtype=dt, device=q.device)
+            o = _dense_like(q)
         if workspace is None:
-            workspace = _scratch(lib().kda_cache_attention_workspace_bytes(Hq, H, d, code),
-                                 q.device)
+            workspace = _scratch(_cache_attention_room(dev, Hq, H, d, code), q.device)
         st = lib().kda_cache_attention(
             q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
             v_scale.data_ptr(), nb, block, block_table.data_ptr(), W, context_lens.data_ptr(),

@@ -58,6 +58,10 @@ int log2_of_block(int32_t block) {
     return block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : block == 128 ? 7 : -1;
 }
 
+size_t attention_room(int32_t group, int32_t d, int sms) {
+    return kHeader + round_up(kda::cache_attention_room(group, d, sms), 256);
+}
+
 bool good_type(kda_dtype dt) { return dt == KDA_F32 || dt == KDA_BF16; }
 
 // What the cache's calls check alike; KDA_OK, or the error.
@@ -253,7 +257,7 @@ size_t kda_cache_attention_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t d, k
         !good_type(dt)) {
         return 0;
     }
-    return kHeader + round_up(kda::cache_attention_room(Hq / Hkv, d, sm_count()), 256);
+    return attention_room(Hq / Hkv, d, sm_count());
 }
 
 int kda_cache_attention(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
@@ -274,7 +278,8 @@ int kda_cache_attention(const void* q, int64_t q_stride, const void* k_cache, co
     if (!block_table || !context_lens || (T > 0 && (!q || !o))) return KDA_ERR_INVALID_ARG;
     const int64_t width = (int64_t)Hq * d;
     if (!good_stride(q_stride, width, dt)) return KDA_ERR_INVALID_ARG;
-    const size_t need = kda_cache_attention_workspace_bytes(Hq, Hkv, d, dt);
+    const int sms = sm_count();
+    const size_t need = attention_room(group, d, sms);
     if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;
     if (!aligned(q, 16) || !aligned(o, 16) || !aligned(block_table, 4) ||
         !aligned(context_lens, 4) || !aligned(cu_seqlens, 4) || !aligned(workspace, 256)) {
@@ -295,7 +300,6 @@ int kda_cache_attention(const void* q, int64_t q_stride, const void* k_cache, co
     }
     if (overlaps(o, out, workspace, need)) return KDA_ERR_INVALID_ARG;
     if (T == 0) return KDA_OK;
-    const int sms = sm_count();
     if (sms < 1) return KDA_ERR_CUDA;
     kda::CacheAttention p;
     memset(&p, 0, sizeof(p));

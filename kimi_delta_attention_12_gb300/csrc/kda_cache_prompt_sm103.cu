@@ -40,8 +40,10 @@ constexpr int kSoftWarps = 8, kFillWarps = 4;
 constexpr int kIssueWarp = kSoftWarps + kFillWarps;
 constexpr int kThreads = 32 * (kIssueWarp + 4);   // whole groups of four warps share registers
 // Registers of a thread: at launch, and then of the softmax, filling and issuing groups.
-constexpr int kRegs = 128, kSoftRegs = 184, kFillRegs = 104, kIssueRegs = 40;
+constexpr int kRegs = 128, kSoftRegs = 176, kFillRegs = 120, kIssueRegs = 40;
 static_assert(2 * kSoftRegs + kFillRegs + kIssueRegs <= 4 * kRegs, "register split");
+static_assert(kSoftRegs >= kRegs && kFillRegs <= kRegs && kIssueRegs <= kRegs,
+              "a group that gives registers away ends with no more than it had");
 constexpr float kNone = -INFINITY;
 constexpr float kSlack = 8.0f, kRaise = 7.0f;
 constexpr uint32_t kHalf = 128 * 128;    // 64 columns of a tile: 128 rows of 128 bytes
@@ -66,7 +68,7 @@ struct __align__(16) Scales {
 struct Shared {
     Scales scales[4][8];                 // of step i at i & 3
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], p_full[2][2], o_full[2];   // p_full: of each half of the weights
     uint64_t fin[2];
     uint64_t go;                         // the second tile sets out when the first has its weights
     uint32_t tmem;
@@ -256,12 +258,17 @@ __device__ __forceinline__ void issue(const CacheAttention& p, Shared* s, uint32
             const uint32_t v = tile_mn(base + L::v + (i & 1) * L::tile);
             if (!wait_warp(p, s, &s->v_full[i & 1], (i >> 1) & 1, 402)) break;
             fence_proxy_async();
-            if (!wait_warp(p, s, &s->p_full[t], i & 1, 403)) break;
-            tc_fence_after();
+            bool ok = true;
 #pragma unroll
-            for (int kk = 0; kk < kTokens / 16; ++kk) {
-                product_ta(co, cs + 8 * kk, v + step_mn(kk), id_o, i > 0 || kk > 0);
+            for (int h = 0; h < 2; ++h) {
+                if (!(ok = ok && wait_warp(p, s, &s->p_full[t][h], i & 1, 403))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 4 * h; kk < 4 * h + 4; ++kk) {
+                    product_ta(co, cs + 8 * kk, v + step_mn(kk), id_o, i > 0 || kk > 0);
+                }
             }
+            if (!ok) break;
             commit(&s->o_full[t]);
             commit(&s->v_empty[i & 1]);
         }
@@ -298,24 +305,14 @@ __device__ __forceinline__ uint4 load_early(const uint8_t* p) {
     return r;
 }
 
-// 16 channels of one token from e4m3 to two vectors of fp16 in a tile.
-__device__ __forceinline__ void spread(uint8_t* tile, int row, int part, const uint4& raw) {
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    uint4 h[2];
-    h[0] = make_uint4(half2_of_e4m3(w[0]), half2_of_e4m3_high(w[0]), half2_of_e4m3(w[1]),
-                      half2_of_e4m3_high(w[1]));
-    h[1] = make_uint4(half2_of_e4m3(w[2]), half2_of_e4m3_high(w[2]), half2_of_e4m3(w[3]),
-                      half2_of_e4m3_high(w[3]));
-    // parts 0-3 and 4-7 of a row lie in two halves of the same banks: they take their two
-    // vectors in opposite order
-    const int first = part >> 2;
-    uint8_t* half = tile + first * kHalf + row * 128;
-    const int chunk = 2 * (part & 3);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int j = i ^ first;
-        *reinterpret_cast<uint4*>(half + (((chunk + j) ^ (row & 7)) << 4)) = j ? h[1] : h[0];
-    }
+// 16 channels of one token from e4m3 to two neighbouring vectors of fp16.
+__device__ __forceinline__ void spread(uint8_t* tile, uint32_t at, const uint4& raw) {
+    *reinterpret_cast<uint4*>(tile + at) =
+        make_uint4(half2_of_e4m3(raw.x), half2_of_e4m3_high(raw.x), half2_of_e4m3(raw.y),
+                   half2_of_e4m3_high(raw.y));
+    *reinterpret_cast<uint4*>(tile + (at ^ 16)) =
+        make_uint4(half2_of_e4m3(raw.z), half2_of_e4m3_high(raw.z), half2_of_e4m3(raw.w),
+                   half2_of_e4m3_high(raw.w));
 }
 
 template <int D>
@@ -326,7 +323,11 @@ __device__ __forceinline__ void fill(const CacheAttention& p, const Job& job, Sh
     constexpr int kPass = 32 * kFillWarps / kParts;      // rows of all threads' loads
     constexpr int kLoads = kTokens / kPass;
     const int tid = threadIdx.x - 32 * kSoftWarps, lane = tid & 31;
-    const int part = tid % kParts, row0 = tid / kParts;
+    // Eight lanes, which store at once, have four parts of two rows each: their 16-byte vectors lie
+    // in eight different places of a row's 128 bytes.
+    const int part = D == 64 ? lane & 3 : (lane & 3) + ((lane >> 1) & 4);
+    const int row0 = D == 64 ? tid >> 2 : 4 * (tid >> 5) + 2 * (lane >> 4) + ((lane >> 2) & 1);
+    const uint32_t at0 = (part >> 2) * kHalf + row0 * 128 + (((2 * (part & 3)) ^ (row0 & 7)) << 4);
     const int32_t* table = p.table + (int64_t)job.request * p.width;
     const int mask = (1 << p.block_log2) - 1;
     const uint32_t block_bytes = (uint32_t)p.heads * D << p.block_log2;
@@ -359,7 +360,7 @@ __device__ __forceinline__ void fill(const CacheAttention& p, const Job& job, Sh
             }
         }
 #pragma unroll
-        for (int r = 0; r < kLoads; ++r) spread(tile, row0 + r * kPass, part, raw[r]);
+        for (int r = 0; r < kLoads; ++r) spread(tile, at0 + r * kPass * 128, raw[r]);
     };
     // of this lane's group: the scales of keys and values
     auto scales_of = [&](int blocks, float& ks, float& vs) {
@@ -397,6 +398,12 @@ __device__ __forceinline__ void fill(const CacheAttention& p, const Job& job, Sh
 }
 
 // ------------------------------------------------------------------ softmax
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -411,117 +418,136 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
         : "r"(taddr));
 }
 
-template <int D>
-__device__ __forceinline__ void soften(const CacheAttention& p, const Job& job, Shared* s,
-                                       uint8_t* sm, int steps, int t, float factor) {
-    const int row = threadIdx.x & 127, lanes_of = (threadIdx.x >> 5) & 3;
-    const uint32_t lane0 = (uint32_t)lanes_of << 21;     // TMEM lane 32 * (warp % 4)
-    const uint32_t cs = lane0 + kS + 128 * t, co = lane0 + kO + 128 * t;
-    const int flat = job.row0 + kRows * t + row, limit = job.hidden + flat / p.group;
-    // the first row of this warp sees the fewest keys
-    const int fewest = job.hidden + (flat - (threadIdx.x & 31)) / p.group;
-    float m = kNone, l = 0.0f;
-    bool ok = true;
-    for (int i = 0; i < steps; ++i) {
-        const int first = i * kTokens;
-        const bool masked = first + kTokens > fewest;
-        // (the scales were written before the keys that the scores are of)
-        const Scales* sc = s->scales[i & 3];
-        ok = wait_warp(p, s, &s->s_full[t], i & 1, 422);
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t r[kTokens];
+// What a thread keeps of its row from step to step.
+struct Row {
+    float factor;                        // of its scores
+    float m, l;                          // their reference, and the sum of weights
+    int limit;                           // keys that it sees
+};
+
+// One step of a tile: weights in place of the scores.  MASKED: some rows do not see every key.
+template <int D, bool MASKED>
+__device__ __forceinline__ bool soften_step(const CacheAttention& p, Shared* s, int i, int t,
+                                            uint32_t cs, uint32_t co, Row& row) {
+    // (the scales were written before the keys that the scores are of)
+    const Scales* sc = s->scales[i & 3];
+    if (!wait_warp(p, s, &s->s_full[t], i & 1, 422)) return false;
+    tc_fence_after();
+    uint32_t r[kTokens];
 #pragma unroll
-        for (int c = 0; c < kTokens; c += 32) tmem_ld32(cs + c, r + c);
-        tmem_wait_ld();
-        if (masked) {       // scores in full, and none where a row sees nothing
-            const int seen = limit - first;
+    for (int c = 0; c < kTokens; c += 32) tmem_ld32(cs + c, r + c);
+    tmem_wait_ld();
+    if (MASKED) {           // scores in full, and none where the row sees nothing
+        const int seen = row.limit - i * kTokens;
 #pragma unroll
-            for (int j = 0; j < kTokens; ++j) {
-                const float x = fmaf(__uint_as_float(r[j]), factor * sc[j / 16].k, sc[j / 16].log_v);
-                r[j] = __float_as_uint(j < seen ? x : kNone);
-            }
+        for (int j = 0; j < kTokens; ++j) {
+            const float x = fmaf(__uint_as_float(r[j]), row.factor * sc[j / 16].k, sc[j / 16].log_v);
+            r[j] = __float_as_uint(j < seen ? x : kNone);
         }
-        // (the groups side by side, so that no maximum waits for the one before)
-        float tops[kTokens / 16];
+    }
+    // (the groups side by side, so that no maximum waits for the one before)
+    float tops[kTokens / 16];
 #pragma unroll
-        for (int g = 0; g < kTokens / 16; ++g) tops[g] = __uint_as_float(r[16 * g]);
+    for (int g = 0; g < kTokens / 16; ++g) tops[g] = __uint_as_float(r[16 * g]);
 #pragma unroll
-        for (int j = 1; j < 15; j += 2) {
-#pragma unroll
-            for (int g = 0; g < kTokens / 16; ++g) {
-                tops[g] = fmaxf(fmaxf(tops[g], __uint_as_float(r[16 * g + j])),
-                                __uint_as_float(r[16 * g + j + 1]));
-            }
-        }
-        float top = kNone;
+    for (int j = 1; j < 15; j += 2) {
 #pragma unroll
         for (int g = 0; g < kTokens / 16; ++g) {
-            tops[g] = fmaxf(tops[g], __uint_as_float(r[16 * g + 15]));
-            top = fmaxf(top, masked ? tops[g] : fmaf(tops[g], factor * sc[g].k, sc[g].log_v));
+            tops[g] = max3(tops[g], __uint_as_float(r[16 * g + j]),
+                           __uint_as_float(r[16 * g + j + 1]));
         }
-        const bool raise = top > m + kSlack;
-        if (__any_sync(0xffffffffu, raise)) {
-            const float now = fmaxf(m, top), less = now > m ? exp2_of(m - now) : 1.0f;
-            m = now;
-            l *= less;
-            if (i > 0) {
-                ok = wait_warp(p, s, &s->o_full[t], (i - 1) & 1, 423);
-                if (!ok) break;
-                tc_fence_after();
+    }
+    float top = kNone;
 #pragma unroll
-                for (int c = 0; c < D; c += 16) {
-                    uint32_t x[16];
-                    tmem_ld16(co + c, x);
-                    tmem_wait_ld();
+    for (int g = 0; g < kTokens / 16; ++g) {
+        tops[g] = fmaxf(tops[g], __uint_as_float(r[16 * g + 15]));
+        top = fmaxf(top, MASKED ? tops[g] : fmaf(tops[g], row.factor * sc[g].k, sc[g].log_v));
+    }
+    if (__any_sync(0xffffffffu, top > row.m + kSlack)) {
+        const float now = fmaxf(row.m, top), less = now > row.m ? exp2_of(row.m - now) : 1.0f;
+        row.m = now;
+        row.l *= less;
+        if (i > 0) {
+            if (!wait_warp(p, s, &s->o_full[t], (i - 1) & 1, 423)) return false;
+            tc_fence_after();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        x[j] = __float_as_uint(__uint_as_float(x[j]) * less);
-                    }
-                    tmem_st16(co + c, x);
+            for (int c = 0; c < D; c += 16) {
+                uint32_t x[16];
+                tmem_ld16(co + c, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    x[j] = __float_as_uint(__uint_as_float(x[j]) * less);
                 }
+                tmem_st16(co + c, x);
             }
         }
-        const float ref = (m == kNone ? 0.0f : m) - kRaise;
+    }
+    const float ref = (row.m == kNone ? 0.0f : row.m) - kRaise;
 #pragma unroll
-        for (int h = 0; h < kTokens / 32; ++h) {
-            uint64_t x[16];
+    for (int h = 0; h < kTokens / 32; ++h) {
+        uint64_t x[16];
+        uint32_t pairs[16];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const float f = masked ? 1.0f : factor * sc[2 * h + g].k;
-                const float off = (masked ? 0.0f : sc[2 * h + g].log_v) - ref;
+        for (int g = 0; g < 2; ++g) {
+            const float f = MASKED ? 1.0f : row.factor * sc[2 * h + g].k;
+            const float off = (MASKED ? 0.0f : sc[2 * h + g].log_v) - ref;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int c = 32 * h + 16 * g + 2 * j;
-                    x[8 * g + j] = fma2(two(r[c], r[c + 1]), two(f, f), two(off, off));
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                float lo, hi;
-                apart(x[j], lo, hi);
-                lo = exp2_of(lo);
-                hi = exp2_of(hi);
-                x[j] = two(lo, hi);
-                r[16 * h + j] = half2_of(lo, hi);
-            }
-            tmem_st16(cs + 16 * h, *reinterpret_cast<const uint32_t (*)[16]>(r + 16 * h));
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const uint64_t* y = x + 8 * g;
-                const uint64_t sum = add2(add2(add2(y[0], y[1]), add2(y[2], y[3])),
-                                          add2(add2(y[4], y[5]), add2(y[6], y[7])));
-                l = fmaf(sum2(sum), sc[2 * h + g].inv_v, l);
+            for (int j = 0; j < 8; ++j) {
+                const int c = 32 * h + 16 * g + 2 * j;
+                x[8 * g + j] = fma2(two(r[c], r[c + 1]), two(f, f), two(off, off));
             }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        arrive_warp(&s->p_full[t]);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            float lo, hi;
+            apart(x[j], lo, hi);
+            lo = exp2_of(lo);
+            hi = exp2_of(hi);
+            x[j] = two(lo, hi);
+            pairs[j] = half2_of(lo, hi);
+        }
+        tmem_st16(cs + 16 * h, pairs);
+        if (h & 1) {                     // half of the weights: its products may begin
+            tmem_wait_st();
+            tc_fence_before();
+            arrive_warp(&s->p_full[t][h >> 1]);
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const uint64_t* y = x + 8 * g;
+            const uint64_t sum = add2(add2(add2(y[0], y[1]), add2(y[2], y[3])),
+                                      add2(add2(y[4], y[5]), add2(y[6], y[7])));
+            row.l = fmaf(sum2(sum), sc[2 * h + g].inv_v, row.l);
+        }
+    }
+    return true;
+}
+
+template <int D>
+__device__ __forceinline__ void soften(const CacheAttention& p, const Job& job, Shared* s,
+                                       int steps, int t, float factor) {
+    const int in_tile = threadIdx.x & 127;
+    const uint32_t lane0 = (uint32_t)(in_tile >> 5) << 21;       // TMEM lane 32 * (warp % 4)
+    const uint32_t cs = lane0 + kS + 128 * t, co = lane0 + kO + 128 * t;
+    const int flat = job.row0 + kRows * t + in_tile;
+    Row row = {factor, kNone, 0.0f, job.hidden + flat / p.group};
+    // the first row of this warp sees the fewest keys
+    const int fewest = job.hidden + (flat - (threadIdx.x & 31)) / p.group;
+    const int whole = fewest < 0 ? 0 : min(fewest / kTokens, steps);
+    bool ok = true;
+    for (int i = 0; ok && i < whole; ++i) {
+        ok = soften_step<D, false>(p, s, i, t, cs, co, row);
         if (i == 0 && t == 0) arrive_warp(&s->go);
     }
+    for (int i = whole; ok && i < steps; ++i) {
+        ok = soften_step<D, true>(p, s, i, t, cs, co, row);
+        if (i == 0 && t == 0) arrive_warp(&s->go);
+    }
+    const float l = row.l;
     if (ok && steps > 0) ok = wait_warp(p, s, &s->o_full[t], (steps - 1) & 1, 424);
     tc_fence_after();
-    const bool mine = ok && kRows * t + row < job.rows;
+    const bool mine = ok && kRows * t + in_tile < job.rows;
     const float by = l == 0.0f ? 0.0f : 1.0f / l;
     const int j = flat / p.group;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) +
@@ -615,7 +641,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_prompt_kernel(CacheAttentio
             mbar_init(&s->k_empty[i], tiles);
             mbar_init(&s->v_empty[i], tiles);
             mbar_init(&s->s_full[i], 1);
-            mbar_init(&s->p_full[i], kSoftWarps / 2);
+            mbar_init(&s->p_full[i][0], kSoftWarps / 2);
+            mbar_init(&s->p_full[i][1], kSoftWarps / 2);
             mbar_init(&s->o_full[i], 1);
             mbar_init(&s->fin[i], 1);
         }
@@ -639,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_prompt_kernel(CacheAttentio
     if (w < kSoftWarps) {
         take_registers<kSoftRegs>();
         const int t = threadIdx.x >> 7;
-        if (t < tiles) soften<D>(p, job, s, sm, steps, t, factor);
+        if (t < tiles) soften<D>(p, job, s, steps, t, factor);
     } else if (w < kIssueWarp) {
         give_registers<kFillRegs>();
         fill<D>(p, job, s, sm, steps, high);

@@ -199,7 +199,7 @@ def lib() -> ctypes.CDLL:
             L.kda_cache_attention.argtypes = [vp, i64, vp, vp, vp, vp, i32, i32, vp, i32, vp, vp,
                                               i32, i32, i32, i32, i32, i32, dt, f32, vp, vp, sz, vp]
             L.kda_cache_attention_workspace_bytes.restype = sz
-            L.kda_cache_attention_workspace_bytes.argtypes = [i32, i32, i32, dt]
+            L.kda_cache_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, dt]
             _lib = L
     return _lib
 
@@ -1260,14 +1260,17 @@ def kda_cache_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cac
         raise KDAError(st, "kda_cache_write")
 
 
-@functools.lru_cache(maxsize=64)
-def _cache_attention_room(dev: int, Hq: int, Hkv: int, d: int, code: int) -> int:
-    """The workspace on device `dev`, which is the current one: the same for every call."""
-    return int(lib().kda_cache_attention_workspace_bytes(Hq, Hkv, d, code))
+@functools.lru_cache(maxsize=256)
+def _cache_attention_room(dev: int, T: int, max_new: int, Hq: int, Hkv: int, d: int,
+                          code: int) -> int:
+    """The workspace on device `dev`, which is the current one: the same for every such call."""
+    return int(lib().kda_cache_attention_workspace_bytes(T, max_new, Hq, Hkv, d, code))
 
 
-def cache_attention_workspace_bytes(Hq: int, Hkv: int, d: int, dtype: torch.dtype) -> int:
-    return int(lib().kda_cache_attention_workspace_bytes(Hq, Hkv, d, _dtype_code(dtype)))
+def cache_attention_workspace_bytes(T: int, max_new: int, Hq: int, Hkv: int, d: int,
+                                    dtype: torch.dtype) -> int:
+    return int(lib().kda_cache_attention_workspace_bytes(T, max_new, Hq, Hkv, d,
+                                                         _dtype_code(dtype)))
 
 
 def kda_cache_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -1307,6 +1310,8 @@ def kda_cache_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
         if cu_seqlens.shape != (N + 1,) or cu_seqlens.dtype != torch.int32:
             _expect(cu_seqlens, (N + 1,), "cu_seqlens", torch.int32)
         most = T
+    if max_new is not None:
+        most = max_new
     if o is not None:
         _expect(o, (T, Hq, d), "o", dt)
     on = _on(stream, dev)
@@ -1316,11 +1321,11 @@ def kda_cache_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
         if o is None:
             o = _dense_like(q)
         if workspace is None:
-            workspace = _scratch(_cache_attention_room(dev, Hq, H, d, code), q.device)
+            workspace = _scratch(_cache_attention_room(dev, T, most, Hq, H, d, code), q.device)
         st = lib().kda_cache_attention(
             q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
             v_scale.data_ptr(), nb, block, block_table.data_ptr(), W, context_lens.data_ptr(),
-            _addr(cu_seqlens), N, T, most if max_new is None else int(max_new), Hq, H, d, code,
+            _addr(cu_seqlens), N, T, most, Hq, H, d, code,
             d ** -0.5 if scale is None else scale, o.data_ptr(), workspace.data_ptr(),
             workspace.nbytes, _raw_stream(dev))
     finally:

@@ -83,11 +83,16 @@ struct CacheAttention {
                                // on the prompts' kernel takes it, the other one below
 };
 
-// Bytes of partial sums, on a device of that many SMs.
-size_t cache_attention_room(int32_t group, int32_t d, int sms);
 // Whether the prompts' kernel has a form for these.
 bool cache_prompt_takes(int32_t d, int dtype);
-cudaError_t launch_cache_prompt(const CacheAttention& p, cudaStream_t stream);
+size_t cache_prompt_room(int32_t d, int sms);
+cudaError_t launch_cache_prompt(const CacheAttention& p, int sms, cudaStream_t stream);
+// Whether a call's prompts go to it: so many rows in all, and in the longest request.
+bool cache_prompt_used(int32_t heads, int32_t group, int32_t T, int32_t max_new, int32_t d,
+                       int dtype);
+// Bytes of partial sums, on a device of that many SMs.
+size_t cache_attention_room(int32_t heads, int32_t group, int32_t T, int32_t max_new, int32_t d,
+                            int dtype, int sms);
 cudaError_t launch_cache_attention(const CacheAttention& p, int dtype, int sms,
                                    cudaStream_t stream);
 

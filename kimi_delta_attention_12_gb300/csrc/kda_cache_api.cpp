@@ -58,8 +58,10 @@ int log2_of_block(int32_t block) {
     return block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : block == 128 ? 7 : -1;
 }
 
-size_t attention_room(int32_t group, int32_t d, int sms) {
-    return kHeader + round_up(kda::cache_attention_room(group, d, sms), 256);
+size_t attention_room(int32_t T, int32_t max_new, int32_t Hq, int32_t Hkv, int32_t d,
+                      kda_dtype dt, int sms) {
+    return kHeader + round_up(kda::cache_attention_room(Hkv, Hq / Hkv, T, max_new, d,
+                                                        dt == KDA_F32 ? 0 : 1, sms), 256);
 }
 
 bool good_type(kda_dtype dt) { return dt == KDA_F32 || dt == KDA_BF16; }
@@ -252,12 +254,13 @@ int kda_cache_write(const void* k, int64_t k_stride, const void* v, int64_t v_st
                : KDA_ERR_CUDA;
 }
 
-size_t kda_cache_attention_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t d, kda_dtype dt) {
-    if (Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > kMaxGroup || !supported_dim(d) ||
+size_t kda_cache_attention_workspace_bytes(int32_t T, int32_t max_new, int32_t Hq, int32_t Hkv,
+                                           int32_t d, kda_dtype dt) {
+    if (T < 0 || max_new < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > kMaxGroup || !supported_dim(d) ||
         !good_type(dt)) {
         return 0;
     }
-    return attention_room(Hq / Hkv, d, sm_count());
+    return attention_room(T, max_new, Hq, Hkv, d, dt, sm_count());
 }
 
 int kda_cache_attention(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
@@ -279,7 +282,7 @@ int kda_cache_attention(const void* q, int64_t q_stride, const void* k_cache, co
     const int64_t width = (int64_t)Hq * d;
     if (!good_stride(q_stride, width, dt)) return KDA_ERR_INVALID_ARG;
     const int sms = sm_count();
-    const size_t need = attention_room(group, d, sms);
+    const size_t need = attention_room(T, max_new, Hq, Hkv, d, dt, sms);
     if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;
     if (!aligned(q, 16) || !aligned(o, 16) || !aligned(block_table, 4) ||
         !aligned(context_lens, 4) || !aligned(cu_seqlens, 4) || !aligned(workspace, 256)) {

@@ -815,10 +815,20 @@ cudaError_t launch_typed(const CacheAttention& p, int sms, cudaStream_t stream) 
 
 }  // namespace
 
-size_t cache_attention_room(int32_t, int32_t d, int sms) {
+bool cache_prompt_used(int32_t heads, int32_t group, int32_t T, int32_t max_new, int32_t d,
+                       int dtype) {
+    return cache_prompt_takes(d, dtype) && (int64_t)group * max_new >= kManyRows &&
+           (int64_t)group * T * heads >= kManyWork;
+}
+
+size_t cache_attention_room(int32_t heads, int32_t group, int32_t T, int32_t max_new, int32_t d,
+                            int dtype, int sms) {
     const int most = blocks_per_sm(1) * 8 > blocks_per_sm(2) * 16 ? blocks_per_sm(1) * 8
                                                                   : blocks_per_sm(2) * 16;
-    return (size_t)sms * most * 2 * (d + 2) * sizeof(float);
+    const size_t room = (size_t)sms * most * 2 * (d + 2) * sizeof(float);
+    const size_t prompts = cache_prompt_used(heads, group, T, max_new, d, dtype)
+                               ? cache_prompt_room(d, sms) : 0;
+    return room > prompts ? room : prompts;
 }
 
 cudaError_t launch_cache_attention(const CacheAttention& call, int dtype, int sms,
@@ -826,10 +836,9 @@ cudaError_t launch_cache_attention(const CacheAttention& call, int dtype, int sm
     CacheAttention p = call;
     p.clears = 1;
     p.many_rows = INT64_MAX;
-    const int64_t most = (int64_t)p.group * p.max_new, rows = (int64_t)p.group * p.T;
-    if (cache_prompt_takes(p.d, dtype) && most >= kManyRows && rows * p.heads >= kManyWork) {
+    if (cache_prompt_used(p.heads, p.group, p.T, p.max_new, p.d, dtype)) {
         p.many_rows = p.N == 1 ? 1 : kManyRows;
-        const cudaError_t err = launch_cache_prompt(p, stream);
+        const cudaError_t err = launch_cache_prompt(p, sms, stream);
         if (err != cudaSuccess || p.N == 1) return err;
         p.clears = 0;
     }

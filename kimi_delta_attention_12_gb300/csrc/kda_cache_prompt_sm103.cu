@@ -10,6 +10,9 @@
 //     P = 2^(S f - m)    one thread a row, written back over S as fp16 pairs
 //     O += P V     P from TMEM, V from shared memory, O in TMEM
 //
+// A CTA stays on its SM and takes its share of all steps, a stretch that may begin and end inside
+// an item; such an item's sums are joined by a second kernel.
+//
 // The tiles take turns: while one's softmax runs, the tensor core works for the other.  Roles:
 // warps 0-7 a row each (softmax, the output), warps 8-11 read e4m3 tiles of the cache and write
 // them as fp16 (exact) in the operands' layout, warps 12 and 13 issue the products of a tile
@@ -25,6 +28,7 @@
 
 #include "kda_cache.h"
 #include "kda_e4m3.cuh"
+#include "kda_follow.cuh"
 #include "kda_packed.cuh"
 #include "kda_seqlens.cuh"
 #include "sm103_ptx.cuh"
@@ -46,6 +50,8 @@ static_assert(kSoftRegs >= kRegs && kFillRegs <= kRegs && kIssueRegs <= kRegs,
               "a group that gives registers away ends with no more than it had");
 constexpr float kNone = -INFINITY;
 constexpr float kSlack = 8.0f, kRaise = 7.0f;
+constexpr int kLeastSteps = 8;           // of a block, so that parts are worth their joining
+constexpr int kJoinThreads = 256, kJoinRows = 32;
 constexpr uint32_t kHalf = 128 * 128;    // 64 columns of a tile: 128 rows of 128 bytes
 // TMEM columns: S (and P over its first half) and O of the two tiles
 constexpr uint32_t kS = 0, kO = 256;
@@ -65,46 +71,76 @@ struct __align__(16) Scales {
     float k, log_v, inv_v, unused;
 };
 
-struct Shared {
-    Scales scales[4][8];                 // of step i at i & 3
+struct Bars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t s_full[2], p_full[2][2], o_full[2];   // p_full: of each half of the weights
     uint64_t fin[2];
     uint64_t go;                         // the second tile sets out when the first has its weights
+};
+
+struct Shared {
+    Scales scales[4][8];                 // of step i at i & 3
+    Bars bars[2];                        // of one piece of work and the next
     uint32_t tmem;
     volatile int abort;
 };
 static_assert(sizeof(Shared) <= 1024, "scales and barriers");
 
-struct Job {
+// 256 rows of a request and head, and the steps that they need.
+struct Item {
     int request, head;
     int tokens, row0, rows;              // cached; first row of the request's, and how many
     int hidden;                          // keys that the request's row 0 sees
     int64_t token0;                      // of the packed q
+    int64_t begin;                       // where its steps begin among all
+    int nominal, steps;                  // steps set aside, those that its last row needs
 };
 
-// The rows' tiles of the requests that this kernel takes, last ones first: later tokens see more
-// keys, and the long tiles start early.
-__device__ __forceinline__ bool job_of(const CacheAttention& p, int index, int head, Job& job) {
-    __shared__ int64_t sums[kThreads / 32];
-    __shared__ Job found;
-    __shared__ int any;
+// Every tile of a request counts as many steps as its last one needs, so that a step's place is
+// found without walking the tiles; a tile that sees fewer keys leaves the rest of its steps empty.
+struct Span {
+    int64_t bos, rows, tiles, all;
+    int tokens, nominal;
+};
+
+__device__ __forceinline__ Span span_of(const CacheAttention& p, int i) {
+    Span s;
+    int64_t eos;
+    if (p.cu) {
+        clamped_seq(p.cu, i, p.N, p.T, s.bos, eos);
+    } else {
+        s.bos = i;
+        eos = i + 1;
+    }
+    const int64_t table = (int64_t)p.width << p.block_log2;
+    const int64_t most = table < 0x7fff0000 ? table : 0x7fff0000;
+    const int64_t c = p.context[i];
+    s.tokens = (int)(c < 0 ? 0 : (c < most ? c : most));
+    s.rows = (eos - s.bos) * p.group;
+    if (s.rows < p.many_rows) s.rows = 0;
+    s.tiles = (s.rows + 2 * kRows - 1) / (2 * kRows);
+    s.nominal = s.tokens > 0 ? (int)(((int64_t)s.tokens + kTokens - 1) / kTokens) : 1;
+    s.all = s.tiles * p.heads * s.nominal;
+    return s;
+}
+
+// What each block takes: the steps begin .. end - 1 of all, from request `request` on, whose
+// steps begin at `first`.  All threads of the block call it.
+struct Stretch {
+    int64_t begin, end, per, first;
+    int request;
+};
+
+template <int THREADS>
+__device__ __forceinline__ Stretch stretch_of(const CacheAttention& p, int block, int blocks) {
+    __shared__ int64_t sums[THREADS / 32];
+    __shared__ int64_t found_first;
+    __shared__ int found;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int k = (p.N + kThreads - 1) / kThreads;
+    const int k = (p.N + THREADS - 1) / THREADS;
     const int i0 = threadIdx.x * k, i1 = i0 + k < p.N ? i0 + k : p.N;
-    auto rows_of = [&](int i, int64_t& bos) {
-        int64_t eos;
-        if (p.cu) {
-            clamped_seq(p.cu, i, p.N, p.T, bos, eos);
-        } else {
-            bos = i;
-            eos = i + 1;
-        }
-        const int64_t rows = (eos - bos) * p.group;
-        return rows >= p.many_rows ? rows : 0;
-    };
-    int64_t mine = 0, bos;
-    for (int i = i0; i < i1; ++i) mine += (rows_of(i, bos) + 2 * kRows - 1) / (2 * kRows);
+    int64_t mine = 0;
+    for (int i = i0; i < i1; ++i) mine += span_of(p, i).all;
     int64_t x = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -112,39 +148,69 @@ __device__ __forceinline__ bool job_of(const CacheAttention& p, int index, int h
         if (lane >= d) x += y;
     }
     if (lane == 31) sums[w] = x;
-    if (threadIdx.x == 0) any = 0;
+    if (threadIdx.x == 0) found = -1;
     __syncthreads();
     int64_t total = 0, before = 0;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
+    for (int i = 0; i < THREADS / 32; ++i) {
         before += i < w ? sums[i] : 0;
         total += sums[i];
     }
+    Stretch s;
+    s.per = (total + blocks - 1) / blocks;
+    if (s.per < kLeastSteps) s.per = kLeastSteps;
+    s.begin = s.per * block;
+    s.end = s.begin + s.per < total ? s.begin + s.per : total;
     int64_t at = before + x - mine;
-    const int64_t want = total - 1 - index;
-    if (want >= at && want < at + mine) {
+    if (s.begin < total && at <= s.begin && s.begin < at + mine) {
         for (int i = i0; i < i1; ++i) {
-            const int64_t rows = rows_of(i, bos), tiles = (rows + 2 * kRows - 1) / (2 * kRows);
-            if (want < at + tiles) {
-                const int64_t table = (int64_t)p.width << p.block_log2;
-                const int64_t most = table < 0x7fff0000 ? table : 0x7fff0000;
-                const int64_t c = p.context[i], r0 = (want - at) * 2 * kRows;
-                found.request = i;
-                found.head = head;
-                found.tokens = (int)(c < 0 ? 0 : (c < most ? c : most));
-                found.row0 = (int)r0;
-                found.rows = (int)(rows - r0 < 2 * kRows ? rows - r0 : 2 * kRows);
-                found.hidden = found.tokens - (int)(rows / p.group) + 1;
-                found.token0 = bos;
-                any = 1;
+            const int64_t all = span_of(p, i).all;
+            if (s.begin < at + all) {
+                found = i;
+                found_first = at;
                 break;
             }
-            at += tiles;
+            at += all;
         }
     }
     __syncthreads();
-    job = found;
-    return any != 0;
+    s.request = found;
+    s.first = found_first;
+    return s;
+}
+
+// The item of step `at`, from request i on, whose steps begin at `first`.  Tiles follow each other
+// first, last, second, last but one, ...: under a causal mask a tile and its neighbour together
+// take the same time wherever they stand.
+__device__ __forceinline__ Item item_at(const CacheAttention& p, int64_t at, int& i,
+                                        int64_t& first) {
+    Span s = span_of(p, i);
+    while (at >= first + s.all && i + 1 < p.N) {
+        first += s.all;
+        s = span_of(p, ++i);
+    }
+    const int64_t n = (at - first) / s.nominal, head = n / s.tiles, k = n - head * s.tiles;
+    const int64_t row0 = 2 * kRows * (k & 1 ? s.tiles - 1 - (k >> 1) : k >> 1);
+    Item t;
+    t.request = i;
+    t.head = (int)head;
+    t.tokens = s.tokens;
+    t.row0 = (int)row0;
+    t.rows = (int)(s.rows - row0 < 2 * kRows ? s.rows - row0 : 2 * kRows);
+    t.hidden = s.tokens - (int)(s.rows / p.group) + 1;
+    t.token0 = s.bos;
+    t.begin = first + n * s.nominal;
+    t.nominal = s.nominal;
+    const int high = t.hidden + (t.row0 + t.rows - 1) / p.group;
+    t.steps = high > kTokens ? (high + kTokens - 1) / kTokens : 1;
+    return t;
+}
+
+// Where block `block` leaves its sums of an item that it does not have whole: the one that it
+// begins with, or another.
+__device__ __forceinline__ float* part_of(const CacheAttention& p, int64_t block, bool begins_with,
+                                          int D) {
+    return p.partial + (block * 2 + !begins_with) * (2 * kRows) * (D + 2);
 }
 
 template <int N>
@@ -248,20 +314,20 @@ __device__ __forceinline__ float exp2_of(float x) {
 // ------------------------------------------------------------------ issuing
 // All products of tile t.
 template <int D>
-__device__ __forceinline__ void issue(const CacheAttention& p, Shared* s, uint32_t base, int steps,
-                                      int t) {
+__device__ __forceinline__ void issue(const CacheAttention& p, Shared* s, Bars* b, uint32_t base,
+                                      int steps, int t) {
     using L = Layout<D>;
     constexpr uint32_t id_s = idesc_f16(128, kTokens, 0, 0), id_o = idesc_f16(128, D, 0, 1);
     const uint32_t q = tile_k(base + L::q + t * L::tile), cs = kS + 128 * t, co = kO + 128 * t;
     for (int i = -1; i < steps; ++i) {
         if (i >= 0) {
             const uint32_t v = tile_mn(base + L::v + (i & 1) * L::tile);
-            if (!wait_warp(p, s, &s->v_full[i & 1], (i >> 1) & 1, 402)) break;
+            if (!wait_warp(p, s, &b->v_full[i & 1], (i >> 1) & 1, 402)) break;
             fence_proxy_async();
             bool ok = true;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if (!(ok = ok && wait_warp(p, s, &s->p_full[t][h], i & 1, 403))) break;
+                if (!(ok = ok && wait_warp(p, s, &b->p_full[t][h], i & 1, 403))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 4 * h; kk < 4 * h + 4; ++kk) {
@@ -269,30 +335,30 @@ __device__ __forceinline__ void issue(const CacheAttention& p, Shared* s, uint32
                 }
             }
             if (!ok) break;
-            commit(&s->o_full[t]);
-            commit(&s->v_empty[i & 1]);
+            commit(&b->o_full[t]);
+            commit(&b->v_empty[i & 1]);
         }
         if (i + 1 < steps) {
             // Half a step behind: one tile's softmax then runs beside the other's products.  Side
             // by side they contend for the issue slots and then for the tensor core.
-            if (i < 0 && t == 1 && !wait_warp(p, s, &s->go, 0, 406)) break;
+            if (i < 0 && t == 1 && !wait_warp(p, s, &b->go, 0, 406)) break;
             const int stage = (i + 1) & 1;
             const uint32_t k = tile_k(base + L::k + stage * L::tile);
-            if (!wait_warp(p, s, &s->k_full[stage], ((i + 1) >> 1) & 1, 401)) break;
+            if (!wait_warp(p, s, &b->k_full[stage], ((i + 1) >> 1) & 1, 401)) break;
             fence_proxy_async();
             // the scores overwrite P: its products have to be done
-            if (i >= 0 && !wait_warp(p, s, &s->o_full[t], i & 1, 404)) break;
+            if (i >= 0 && !wait_warp(p, s, &b->o_full[t], i & 1, 404)) break;
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 product(cs, q + step_k(kk), k + step_k(kk), id_s, kk > 0);
             }
-            commit(&s->s_full[t]);
-            commit(&s->k_empty[stage]);
+            commit(&b->s_full[t]);
+            commit(&b->k_empty[stage]);
         }
     }
-    commit(&s->fin[t]);
-    mbar_wait(&s->fin[t], 0, nullptr);   // no product outlives the CTA
+    commit(&b->fin[t]);
+    mbar_wait(&b->fin[t], 0, nullptr);   // no product outlives the CTA
 }
 
 // ------------------------------------------------------------------ filling
@@ -315,9 +381,10 @@ __device__ __forceinline__ void spread(uint8_t* tile, uint32_t at, const uint4& 
                    half2_of_e4m3_high(raw.w));
 }
 
+// Steps first .. first + steps - 1 of an item.
 template <int D>
-__device__ __forceinline__ void fill(const CacheAttention& p, const Job& job, Shared* s,
-                                     uint8_t* sm, int steps, int high) {
+__device__ __forceinline__ void fill(const CacheAttention& p, const Item& job, Shared* s, Bars* bars,
+                                     uint8_t* sm, int first, int steps, int high) {
     using L = Layout<D>;
     constexpr int kParts = D / 16;                       // vectors of 16 numbers in a row
     constexpr int kPass = 32 * kFillWarps / kParts;      // rows of all threads' loads
@@ -334,7 +401,7 @@ __device__ __forceinline__ void fill(const CacheAttention& p, const Job& job, Sh
     const uint32_t in_block = ((uint32_t)job.head * D << p.block_log2) + 16 * part;
     // lanes 0-7: the blocks of a step's groups of 16 tokens, -1 where there is none
     auto blocks_of = [&](int i) {
-        const int token = i * kTokens + 16 * (lane & 7);
+        const int token = (first + i) * kTokens + 16 * (lane & 7);
         const int b = i < steps && token < high ? table[token >> p.block_log2] : -1;
         return b >= 0 && b < p.num_blocks ? b : -1;
     };
@@ -343,7 +410,7 @@ __device__ __forceinline__ void fill(const CacheAttention& p, const Job& job, Sh
     auto load = [&](const uint8_t* cache, int i, int blocks, uint4 (&raw)[kLoads]) {
 #pragma unroll
         for (int r = 0; r < kLoads; ++r) {
-            const int row = row0 + r * kPass, token = i * kTokens + row;
+            const int row = row0 + r * kPass, token = (first + i) * kTokens + row;
             const int b = max(__shfl_sync(0xffffffffu, blocks, row >> 4), 0);
             raw[r] = load_early(cache + (uint64_t)(uint32_t)b * block_bytes +
                                 (in_block + (token & mask) * D));
@@ -351,12 +418,12 @@ __device__ __forceinline__ void fill(const CacheAttention& p, const Job& job, Sh
     };
     auto store = [&](uint8_t* tile, int i, int blocks, uint4 (&raw)[kLoads]) {
         // (whole steps, but for a request's last)
-        if (__any_sync(0xffffffffu, blocks < 0) || (i + 1) * kTokens > high) {
+        if (__any_sync(0xffffffffu, blocks < 0) || (first + i + 1) * kTokens > high) {
 #pragma unroll
             for (int r = 0; r < kLoads; ++r) {
                 const int row = row0 + r * kPass;
                 const int b = __shfl_sync(0xffffffffu, blocks, row >> 4);
-                if (b < 0 || i * kTokens + row >= high) raw[r] = make_uint4(0, 0, 0, 0);
+                if (b < 0 || (first + i) * kTokens + row >= high) raw[r] = make_uint4(0, 0, 0, 0);
             }
         }
 #pragma unroll
@@ -377,7 +444,7 @@ __device__ __forceinline__ void fill(const CacheAttention& p, const Job& job, Sh
         const int stage = i & 1, phase = ((i >> 1) & 1) ^ 1;
         load(p.v_cache, i, blocks, v);
         const int after = blocks_of(i + 2);
-        if (i > 1 && !wait_warp(p, s, &s->k_empty[stage], phase, 411)) return;
+        if (i > 1 && !wait_warp(p, s, &bars->k_empty[stage], phase, 411)) return;
         store(sm + L::k + stage * L::tile, i, blocks, k);
         if (tid < 8) {
             // not there: no score of it counts
@@ -386,12 +453,12 @@ __device__ __forceinline__ void fill(const CacheAttention& p, const Job& job, Sh
             to.log_v = blocks < 0 ? kNone : __log2f(vs);
             to.inv_v = blocks < 0 ? 0.0f : __frcp_rn(vs);
         }
-        arrive_warp(&s->k_full[stage]);
+        arrive_warp(&bars->k_full[stage]);
         load(p.k_cache, i + 1, next, k);
         scales_of(next, ks, vs);
-        if (i > 1 && !wait_warp(p, s, &s->v_empty[stage], phase, 412)) return;
+        if (i > 1 && !wait_warp(p, s, &bars->v_empty[stage], phase, 412)) return;
         store(sm + L::v + stage * L::tile, i, blocks, v);
-        arrive_warp(&s->v_full[stage]);
+        arrive_warp(&bars->v_full[stage]);
         blocks = next;
         next = after;
     }
@@ -427,11 +494,11 @@ struct Row {
 
 // One step of a tile: weights in place of the scores.  MASKED: some rows do not see every key.
 template <int D, bool MASKED>
-__device__ __forceinline__ bool soften_step(const CacheAttention& p, Shared* s, int i, int t,
-                                            uint32_t cs, uint32_t co, Row& row) {
+__device__ __forceinline__ bool soften_step(const CacheAttention& p, Shared* s, Bars* b, int i,
+                                            int t, uint32_t cs, uint32_t co, Row& row) {
     // (the scales were written before the keys that the scores are of)
     const Scales* sc = s->scales[i & 3];
-    if (!wait_warp(p, s, &s->s_full[t], i & 1, 422)) return false;
+    if (!wait_warp(p, s, &b->s_full[t], i & 1, 422)) return false;
     tc_fence_after();
     uint32_t r[kTokens];
 #pragma unroll
@@ -468,7 +535,7 @@ __device__ __forceinline__ bool soften_step(const CacheAttention& p, Shared* s, 
         row.m = now;
         row.l *= less;
         if (i > 0) {
-            if (!wait_warp(p, s, &s->o_full[t], (i - 1) & 1, 423)) return false;
+            if (!wait_warp(p, s, &b->o_full[t], (i - 1) & 1, 423)) return false;
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < D; c += 16) {
@@ -511,7 +578,7 @@ __device__ __forceinline__ bool soften_step(const CacheAttention& p, Shared* s, 
         if (h & 1) {                     // half of the weights: its products may begin
             tmem_wait_st();
             tc_fence_before();
-            arrive_warp(&s->p_full[t][h >> 1]);
+            arrive_warp(&b->p_full[t][h >> 1]);
         }
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
@@ -524,65 +591,76 @@ __device__ __forceinline__ bool soften_step(const CacheAttention& p, Shared* s, 
     return true;
 }
 
+// Steps first .. first + steps - 1 of tile t; `part`: where to leave the sums of an item of which
+// this is not all.
 template <int D>
-__device__ __forceinline__ void soften(const CacheAttention& p, const Job& job, Shared* s,
-                                       int steps, int t, float factor) {
-    const int in_tile = threadIdx.x & 127;
+__device__ __forceinline__ void soften(const CacheAttention& p, const Item& job, Shared* s, Bars* b,
+                                       int first, int steps, int t, float factor, float* part) {
+    const int in_tile = threadIdx.x & 127, n = kRows * t + in_tile;
     const uint32_t lane0 = (uint32_t)(in_tile >> 5) << 21;       // TMEM lane 32 * (warp % 4)
     const uint32_t cs = lane0 + kS + 128 * t, co = lane0 + kO + 128 * t;
-    const int flat = job.row0 + kRows * t + in_tile;
-    Row row = {factor, kNone, 0.0f, job.hidden + flat / p.group};
+    const int flat = job.row0 + n, before = first * kTokens;
+    Row row = {factor, kNone, 0.0f, job.hidden + flat / p.group - before};
     // the first row of this warp sees the fewest keys
-    const int fewest = job.hidden + (flat - (threadIdx.x & 31)) / p.group;
+    const int fewest = job.hidden + (flat - (threadIdx.x & 31)) / p.group - before;
     const int whole = fewest < 0 ? 0 : min(fewest / kTokens, steps);
     bool ok = true;
     for (int i = 0; ok && i < whole; ++i) {
-        ok = soften_step<D, false>(p, s, i, t, cs, co, row);
-        if (i == 0 && t == 0) arrive_warp(&s->go);
+        ok = soften_step<D, false>(p, s, b, i, t, cs, co, row);
+        if (i == 0 && t == 0) arrive_warp(&b->go);
     }
     for (int i = whole; ok && i < steps; ++i) {
-        ok = soften_step<D, true>(p, s, i, t, cs, co, row);
-        if (i == 0 && t == 0) arrive_warp(&s->go);
+        ok = soften_step<D, true>(p, s, b, i, t, cs, co, row);
+        if (i == 0 && t == 0) arrive_warp(&b->go);
     }
-    const float l = row.l;
-    if (ok && steps > 0) ok = wait_warp(p, s, &s->o_full[t], (steps - 1) & 1, 424);
+    ok = ok && wait_warp(p, s, &b->o_full[t], (steps - 1) & 1, 424);
     tc_fence_after();
-    const bool mine = ok && kRows * t + in_tile < job.rows;
-    const float by = l == 0.0f ? 0.0f : 1.0f / l;
+    const bool mine = ok && n < job.rows;
+    if (part) {
+        if (mine) {
+            part[2 * kRows * D + n] = row.m;
+            part[2 * kRows * (D + 1) + n] = row.l;
+        }
+#pragma unroll
+        for (int c = 0; c < D; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(co + c, r);
+            tmem_wait_ld();
+            uint4* to = reinterpret_cast<uint4*>(part + n * D + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (mine) to[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+            }
+        }
+        return;
+    }
+    const float by = row.l == 0.0f ? 0.0f : 1.0f / row.l;
     const int j = flat / p.group;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) +
                          ((job.token0 + j) * (p.heads * p.group) + job.head * p.group + flat -
                           j * p.group) * D;
 #pragma unroll
-    for (int c = 0; c < D; c += 32) {
-        uint32_t r[2][16];
-        if (steps > 0) {
-            tmem_ld16(co + c, r[0]);
-            tmem_ld16(co + c + 16, r[1]);
-            tmem_wait_ld();
+    for (int c = 0; c < D; c += 16) {
+        uint32_t r[16], w[8];
+        tmem_ld16(co + c, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[2 * i]) * by,
+                                                           __uint_as_float(r[2 * i + 1]) * by);
+            w[i] = *reinterpret_cast<const uint32_t*>(&v);
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float lo = l == 0.0f ? 0.0f : __uint_as_float(r[h][2 * i]) * by;
-                const float hi = l == 0.0f ? 0.0f : __uint_as_float(r[h][2 * i + 1]) * by;
-                const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-                w[i] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-            if (mine) {
-                uint4* to = reinterpret_cast<uint4*>(out + c + 16 * h);
-                to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                to[1] = make_uint4(w[4], w[5], w[6], w[7]);
-            }
+        if (mine) {
+            uint4* to = reinterpret_cast<uint4*>(out + c);
+            to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            to[1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
     }
 }
 
 // This thread's row of q, scaled to [1, 2) and in fp16, into its tile; the factor of its scores.
 template <int D>
-__device__ __forceinline__ float stage_query(const CacheAttention& p, const Job& job, uint8_t* sm) {
+__device__ __forceinline__ float stage_query(const CacheAttention& p, const Item& job, uint8_t* sm) {
     const int row = threadIdx.x & 127, t = threadIdx.x >> 7, n = kRows * t + row;
     const int flat = job.row0 + n, j = flat / p.group;
     const bool there = n < job.rows;
@@ -622,6 +700,52 @@ __device__ __forceinline__ float stage_query(const CacheAttention& p, const Job&
     return __int_as_float(e << 23) * (fabsf(p.scale) * 1.44269504088896340736f);
 }
 
+__device__ __forceinline__ void set_up(Bars* b, int tiles) {
+    for (int i = 0; i < 2; ++i) {
+        mbar_init(&b->k_full[i], kFillWarps);
+        mbar_init(&b->v_full[i], kFillWarps);
+        mbar_init(&b->k_empty[i], tiles);
+        mbar_init(&b->v_empty[i], tiles);
+        mbar_init(&b->s_full[i], 1);
+        mbar_init(&b->p_full[i][0], kSoftWarps / 2);
+        mbar_init(&b->p_full[i][1], kSoftWarps / 2);
+        mbar_init(&b->o_full[i], 1);
+        mbar_init(&b->fin[i], 1);
+    }
+    mbar_init(&b->go, kSoftWarps / 2);
+    fence_mbar_init();
+}
+
+__device__ __forceinline__ void tear_down(Bars* b) {
+    uint64_t* bar = reinterpret_cast<uint64_t*>(b);
+    for (int i = 0; i < (int)(sizeof(Bars) / sizeof(uint64_t)); ++i) {
+        asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar + i)) : "memory");
+    }
+}
+
+// All roles of the block, each in code of its own: what was written before is there for all.
+__device__ __forceinline__ void meet() {
+    __syncwarp();
+    tc_fence_before();
+    asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+    tc_fence_after();
+}
+
+// The pieces of a block's stretch: steps u0 .. u1 - 1 of an item, and the piece's number.
+template <typename Work>
+__device__ __forceinline__ void walk(const CacheAttention& p, const Stretch& all, Work work) {
+    int request = all.request, turn = 0;
+    int64_t first = all.first;
+    for (int64_t at = all.begin; at < all.end;) {
+        const Item it = item_at(p, at, request, first);
+        const int64_t last = it.begin + it.nominal < all.end ? it.begin + it.nominal : all.end;
+        const int u0 = (int)min(at - it.begin, (int64_t)it.steps);
+        const int u1 = (int)min(last - it.begin, (int64_t)it.steps);
+        at = last;
+        if (u0 < u1) work(it, u0, u1, turn++);   // (else steps that the tile does not need)
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) cache_prompt_kernel(CacheAttention p) {
     extern __shared__ uint8_t raw[];
@@ -629,78 +753,136 @@ __global__ void __launch_bounds__(kThreads, 1) cache_prompt_kernel(CacheAttentio
                                              ~(uintptr_t)1023);
     Shared* s = reinterpret_cast<Shared*>(sm + Layout<D>::scales);
     const int w = threadIdx.x >> 5;
+    let_follow();
     // (the earliest any CTA can report a wait is seconds away)
     if (p.clears && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
-    Job job;
-    if (!job_of(p, blockIdx.x / p.heads, blockIdx.x % p.heads, job)) return;
-    const int tiles = job.rows > kRows ? 2 : 1;
-    if (threadIdx.x == 32 * kIssueWarp) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s->k_full[i], kFillWarps);
-            mbar_init(&s->v_full[i], kFillWarps);
-            mbar_init(&s->k_empty[i], tiles);
-            mbar_init(&s->v_empty[i], tiles);
-            mbar_init(&s->s_full[i], 1);
-            mbar_init(&s->p_full[i][0], kSoftWarps / 2);
-            mbar_init(&s->p_full[i][1], kSoftWarps / 2);
-            mbar_init(&s->o_full[i], 1);
-            mbar_init(&s->fin[i], 1);
-        }
-        mbar_init(&s->go, kSoftWarps / 2);
-        s->abort = 0;
-        fence_mbar_init();
-    }
+    const Stretch all = stretch_of<kThreads>(p, blockIdx.x, gridDim.x);
+    if (all.request < 0) return;
     if (w == kIssueWarp) {
+        if ((threadIdx.x & 31) == 0) s->abort = 0;
         __syncwarp();
         tmem_alloc(&s->tmem, 512);
         tmem_relinquish();
     }
-    float factor = 0.0f;
-    if (w < kSoftWarps) factor = stage_query<D>(p, job, sm);
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const int high = job.hidden + (job.row0 + job.rows - 1) / p.group;
-    const int steps = high > 0 ? (high + kTokens - 1) / kTokens : 0;
+    // Every role walks the block's pieces by itself, and all meet before and after each.  (One
+    // walk for all would leave every role with the registers of the launch.)
     if (w < kSoftWarps) {
         take_registers<kSoftRegs>();
-        const int t = threadIdx.x >> 7;
-        if (t < tiles) soften<D>(p, job, s, steps, t, factor);
+        walk(p, all, [&](const Item& it, int u0, int u1, int turn) {
+            const float factor = stage_query<D>(p, it, sm);
+            meet();
+            const int t = threadIdx.x >> 7;
+            float* part = u0 == 0 && u1 == it.steps
+                              ? nullptr
+                              : part_of(p, blockIdx.x, it.begin <= all.begin, D);
+            if (t == 0 || it.rows > kRows) {
+                soften<D>(p, it, s, &s->bars[turn & 1], u0, u1 - u0, t, factor, part);
+            }
+            meet();
+        });
     } else if (w < kIssueWarp) {
         give_registers<kFillRegs>();
-        fill<D>(p, job, s, sm, steps, high);
+        walk(p, all, [&](const Item& it, int u0, int u1, int turn) {
+            meet();
+            const int high = it.hidden + (it.row0 + it.rows - 1) / p.group;
+            fill<D>(p, it, s, &s->bars[turn & 1], sm, u0, u1 - u0, high);
+            meet();
+        });
     } else {
         give_registers<kIssueRegs>();
-        const int t = w - kIssueWarp;
-        if (t < tiles) issue<D>(p, s, smem_u32(sm), steps, t);
+        walk(p, all, [&](const Item& it, int u0, int u1, int turn) {
+            const int tiles = it.rows > kRows ? 2 : 1;
+            Bars* b = &s->bars[turn & 1];
+            if (threadIdx.x == 32 * kIssueWarp) {
+                if (turn > 1) tear_down(b);  // (of the piece before the last: long over)
+                set_up(b, tiles);
+            }
+            meet();
+            if (w - kIssueWarp < tiles) {
+                issue<D>(p, s, b, smem_u32(sm), u1 - u0, w - kIssueWarp);
+            }
+            meet();
+        });
     }
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     if (w == kIssueWarp) tmem_dealloc(s->tmem, 512);
 }
 
+// Joins the parts of the item that ends among block blockIdx.x's steps and began before them;
+// kJoinRows of its rows.
 template <int D>
-cudaError_t launch_dim(const CacheAttention& p, cudaStream_t stream) {
-    const cudaError_t err = cudaFuncSetAttribute(
+__global__ void __launch_bounds__(kJoinThreads) cache_prompt_join_kernel(CacheAttention p) {
+    __shared__ float tops[kJoinRows], by[kJoinRows];
+    const Stretch all = stretch_of<kJoinThreads>(p, blockIdx.x, gridDim.x);
+    wait_before();
+    if (all.request < 0) return;
+    int request = all.request;
+    int64_t first = all.first;
+    const Item it = item_at(p, all.begin, request, first);
+    const int64_t b0 = it.begin / all.per, b1 = (it.begin + it.steps - 1) / all.per;
+    // (an item whose steps all lie in one block is whole there)
+    if (it.begin >= all.begin || it.begin + it.nominal > all.end || b0 == b1) return;
+    const int r0 = blockIdx.y * kJoinRows;
+    const int rows = it.rows - r0 < kJoinRows ? it.rows - r0 : kJoinRows;
+    auto part = [&](int64_t b) { return part_of(p, b, it.begin <= b * all.per, D); };
+    const int n = threadIdx.x;
+    if (n < rows) {
+        float top = kNone, l = 0.0f;
+        for (int64_t b = b0; b <= b1; ++b) top = fmaxf(top, part(b)[2 * kRows * D + r0 + n]);
+        const float ref = top == kNone ? 0.0f : top;
+        for (int64_t b = b0; b <= b1; ++b) {
+            const float* x = part(b) + 2 * kRows * D + r0 + n;
+            l = fmaf(exp2_of(x[0] - ref), x[2 * kRows], l);
+        }
+        tops[n] = ref;
+        by[n] = l == 0.0f ? 0.0f : 1.0f / l;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * D / 4; i += kJoinThreads) {
+        const int r = 4 * i / D, c = 4 * i - r * D;
+        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int64_t b = b0; b <= b1; ++b) {
+            const float* x = part(b);
+            const float f = exp2_of(x[2 * kRows * D + r0 + r] - tops[r]);
+            const float4 v = *reinterpret_cast<const float4*>(x + (r0 + r) * D + c);
+            y.x = fmaf(f, v.x, y.x);
+            y.y = fmaf(f, v.y, y.y);
+            y.z = fmaf(f, v.z, y.z);
+            y.w = fmaf(f, v.w, y.w);
+        }
+        const int flat = it.row0 + r0 + r, j = flat / p.group;
+        const int64_t to = ((it.token0 + j) * (p.heads * p.group) + it.head * p.group + flat -
+                            j * p.group) * D + c;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x * by[r], y.y * by[r]);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(y.z * by[r], y.w * by[r]);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + to) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                       *reinterpret_cast<const uint32_t*>(&hi));
+    }
+}
+
+template <int D>
+cudaError_t launch_dim(const CacheAttention& p, int sms, cudaStream_t stream) {
+    cudaError_t err = cudaFuncSetAttribute(
         cache_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::bytes);
     if (err != cudaSuccess) return err;
-    // every request may leave a tile partly filled
-    const int64_t rows = (int64_t)p.T * p.group;
-    const int64_t tiles = rows / (2 * kRows) + (p.N < p.T ? p.N : p.T);
-    if (tiles * p.heads > 0x7fffffff) return cudaErrorInvalidValue;
-    cache_prompt_kernel<D><<<(unsigned)(tiles * p.heads), kThreads, Layout<D>::bytes, stream>>>(p);
-    return cudaGetLastError();
+    cache_prompt_kernel<D><<<sms, kThreads, Layout<D>::bytes, stream>>>(p);
+    err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    return launch_follower(cache_prompt_join_kernel<D>, dim3(sms, 2 * kRows / kJoinRows),
+                           dim3(kJoinThreads), 0, stream, p);
 }
 
 }  // namespace
 
 bool cache_prompt_takes(int32_t d, int dtype) { return dtype == 1 && (d == 64 || d == 128); }
 
-cudaError_t launch_cache_prompt(const CacheAttention& p, cudaStream_t stream) {
-    return p.d == 64 ? launch_dim<64>(p, stream) : launch_dim<128>(p, stream);
+size_t cache_prompt_room(int32_t d, int sms) {
+    return (size_t)sms * 2 * (2 * kRows) * (d + 2) * sizeof(float);
+}
+
+cudaError_t launch_cache_prompt(const CacheAttention& p, int sms, cudaStream_t stream) {
+    return p.d == 64 ? launch_dim<64>(p, sms, stream) : launch_dim<128>(p, sms, stream);
 }
 
 }  // namespace kda

@@ -150,9 +150,10 @@ def test_attention_refusals(L, over, expect):
 
 def test_workspace_size_is_zero_for_bad_sizes(L):
     size = L.kda_cache_attention_workspace_bytes
-    assert size(8, 2, 64, kda.KDA_BF16) > 0
-    for a in ((8, 3, 64, 1), (1, 2, 64, 1), (8, 0, 64, 1), (8, 2, 48, 1), (8, 2, 64, 2),
-              (130, 2, 64, 1)):
+    assert size(4, 1, 8, 2, 64, kda.KDA_BF16) > 0
+    for a in ((4, 1, 8, 3, 64, 1), (4, 1, 1, 2, 64, 1), (4, 1, 8, 0, 64, 1), (4, 1, 8, 2, 48, 1),
+              (4, 1, 8, 2, 64, 2), (4, 1, 130, 2, 64, 1), (-1, 1, 8, 2, 64, 1),
+              (4, -1, 8, 2, 64, 1)):
         assert size(*a) == 0
 
 

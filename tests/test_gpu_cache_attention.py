@@ -119,7 +119,7 @@ def _tensor_cores(b, H):
 def test_prompts_on_the_tensor_cores(past, new, block, Hq, H, d):
     b = Batch(past, new, block, Hq, H, d, torch.bfloat16, seed=sum(new))
     assert _tensor_cores(b, H)
-    ws = torch.full((kda.cache_attention_workspace_bytes(Hq, H, d, torch.bfloat16),), 255,
+    ws = torch.full((kda.cache_attention_workspace_bytes(b.q.shape[0], max(new), Hq, H, d, torch.bfloat16),), 255,
                     dtype=torch.uint8, device="cuda")
     got = kda.kda_cache_attention(*b.args(), max_new=max(new), workspace=ws)
     b.check(got)
@@ -284,7 +284,7 @@ def test_a_strided_query_and_the_same_bits_each_time():
 def test_streams_and_graphs_with_one_workspace():
     a = Batch([300, 20, 77], [1, 1, 1], 16, 8, 2, 64, torch.bfloat16, seed=12)
     b = Batch([10, 200, 400], [1, 3, 9], 16, 8, 2, 64, torch.bfloat16, seed=13)
-    ws = torch.empty(kda.cache_attention_workspace_bytes(8, 2, 64, torch.bfloat16),
+    ws = torch.empty(kda.cache_attention_workspace_bytes(13, 13, 8, 2, 64, torch.bfloat16),
                      dtype=torch.uint8, device="cuda")
     xs = [a.args(), b.args()]
     want = [kda.kda_cache_attention(*x) for x in xs]

@@ -142,13 +142,13 @@ def attention(q, k, v, k_scale, v_scale, table, context, cu, scale, block):
     """(o, mass, size, least): o [T, Hq, d] in fp64, rows behind the last request's NaN, and what
     bounds on the error are multiples of: per element sum p |v| / sum p and sum |v| / v_scale times
     the scale of the heaviest key's block (heaviest by p v_scale), per row the largest scale
-    sum |q| |k| over its keys.  k, v: the bytes [nb, H, block, d] as numpy."""
+    sum |q| |k| and |log2 v_scale| over its keys.  k, v: the bytes [nb, H, block, d] as numpy."""
     q = q.double().cpu().numpy()
     T, Hq, d = q.shape
     nb, H = k_scale.shape
     G = Hq // H
     o, mass = np.full((T, Hq, d), np.nan), np.zeros((T, Hq, d))
-    size, least = np.zeros((T, Hq, 1)), np.zeros((T, Hq, d))
+    size, least = np.zeros((T, Hq, 2)), np.zeros((T, Hq, d))
     for i, c in enumerate(context):
         n = cu[i + 1] - cu[i]
         there = [x for x in range(max(c, 0)) if 0 <= table[i][x // block] < nb]
@@ -181,18 +181,21 @@ def attention(q, k, v, k_scale, v_scale, table, context, cu, scale, block):
                 size[rows, hq, 0] = np.where(
                     any_key, abs(scale) * np.max(np.where(seen, np.abs(x) @ np.abs(K).T, 0.0),
                                                  axis=1, initial=0.0), 0.0)
+                size[rows, hq, 1] = np.max(np.where(seen, np.abs(np.log2(vs))[None], 0.0), axis=1,
+                                           initial=0.0)
     return o, mass, size, least
 
 
 def attention_bound(o, mass, size, least, d, longest, bf16):
     """How far o may be off: a score's products carry 2^-22 of each (q in two halves of 11 bits)
     and d / 16 sums of two products rounded to 2^-22 of the whole; the weights' 2^-20 (exponent,
-    its argument), the running sums 2^-24 for each 16 keys; for bf16 the weights' 11 bits and the
+    its argument up to 16); the logarithm of a value scale in the argument, rounded itself, in the
+    sum and in the reference, 3 ln 2 2^-24 < 2^-22 of its size; the running sums 2^-24 for each 16 keys; for bf16 the weights' 11 bits and the
     result's rounding, 2^-8.  And an fp16 weight is off by up to 2^-25 however small it is, where
     the largest weight times its scale is 2^7 at least for bf16, 2^15 for fp32 (whose second half
     is an fp16 number too): 2^-32 or 2^-40 of `least`."""
-    ds = size * (1 + d / 8) * 2.0 ** -22
-    rel = 2 * ds + 2.0 ** -20 + (longest / 16 + 8) * 2.0 ** -23
+    ds, log_scale = size[..., :1] * (1 + d / 8) * 2.0 ** -22, size[..., 1:]
+    rel = 2 * ds + 2.0 ** -20 + 2 * log_scale * 2.0 ** -22 + (longest / 16 + 8) * 2.0 ** -23
     if bf16:
         return mass * (rel + 2.0 ** -11) + np.abs(o) * 2.0 ** -8 + least * 2.0 ** -32
     return mass * rel + least * 2.0 ** -40

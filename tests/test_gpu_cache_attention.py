@@ -132,7 +132,8 @@ def test_prompts_on_the_tensor_cores(past, new, block, Hq, H, d):
 def test_extremes_on_the_tensor_cores(d):
     b = Batch([60, 0], [130, 100], 16, 32, 8, d, torch.bfloat16, seed=d)
     assert _tensor_cores(b, 8)
-    b.vs = torch.exp2(torch.randint(-60, 61, b.vs.shape).float())
+    b.vs = torch.exp2(torch.randint(-60, 61, b.vs.shape,
+                                    generator=torch.Generator().manual_seed(7)).float())
     b.check(kda.kda_cache_attention(*b.args(), max_new=130))
     b.vs.fill_(1.0)
     b.q[::3] *= 1e30
@@ -193,7 +194,7 @@ def test_rows_without_keys_and_rows_behind():
     b.context[0], b.context[1] = 0, 2         # fewer tokens than new ones: two see none
     args[6] = torch.tensor(b.context, dtype=torch.int32).cuda()
     o = torch.full((9, 4, 64), 7.0, device="cuda")
-    b.q = torch.cat((b.q, torch.randn(3, 4, 64)))
+    b.q = torch.cat((b.q, torch.zeros(3, 4, 64)))
     args[0] = b.q.cuda()
     got = kda.kda_cache_attention(*args, o=o)
     assert got.data_ptr() == o.data_ptr()
@@ -229,7 +230,8 @@ def test_lengths_beyond_the_table_and_the_rows():
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_scales_far_apart(dtype):
     b = Batch([200, 90], [1, 3], 16, 4, 1, 64, dtype, seed=7)
-    b.vs = torch.exp2(torch.randint(-60, 61, b.vs.shape).float())
+    b.vs = torch.exp2(torch.randint(-60, 61, b.vs.shape,
+                                    generator=torch.Generator().manual_seed(7)).float())
     b.check(kda.kda_cache_attention(*b.args()))
     b.vs.fill_(1.7)
     b.ks.fill_(2.0 ** -60)
@@ -246,7 +248,7 @@ def test_large_and_small_queries(dtype):
     b.check(kda.kda_cache_attention(*b.args(), scale=b.scale))
     b.scale = 0.0
     b.check(kda.kda_cache_attention(*b.args(), scale=0.0))
-    b.q = torch.randn(3, 4, 64).to(dtype)
+    b.q = torch.randn(3, 4, 64, generator=torch.Generator().manual_seed(8)).to(dtype)
     b.scale = -0.3
     b.check(kda.kda_cache_attention(*b.args(), scale=-0.3))
 

@@ -37,7 +37,8 @@ def _data(T, H, d, dtype, seed=0):
 ])
 def test_sizes(inter, dtype, T, Hq, Hk, d, rot, first):
     q, k = _data(T, Hq, d, dtype), _data(T, Hk, d, dtype, 1) if Hk else None
-    pos = torch.randint(0, 1 << 20, (T,), dtype=torch.int32)
+    pos = torch.randint(0, 1 << 20, (T,), dtype=torch.int32,
+                        generator=torch.Generator().manual_seed(T))
     f, _ = kda.rotary_frequencies(rot)
     for call, inverse in ((kda.kda_rotary, False), (kda.kda_rotary_backward, True)):
         qo, ko = call(q, k, pos.cuda(), f, interleaved=inter, first=first, magnitude=1.25)
@@ -118,7 +119,8 @@ def test_copied_channels_keep_their_bits():
 def test_the_backward_is_the_gradient():
     """Against differences of the 64-bit forward along random directions."""
     x, w = _data(9, 2, 64, torch.float32), _data(9, 2, 64, torch.float32, 5)
-    pos = torch.randint(0, 5000, (9,), dtype=torch.int32)
+    pos = torch.randint(0, 5000, (9,), dtype=torch.int32,
+                        generator=torch.Generator().manual_seed(2))
     f, m = kda.rotary_frequencies(32, scaling="by_parts", factor=4.0)
     dx, _ = kda.kda_rotary_backward(w, None, pos.cuda(), f, first=16, magnitude=m)
     for seed in range(3):

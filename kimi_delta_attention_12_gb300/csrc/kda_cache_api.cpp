@@ -130,14 +130,13 @@ int kda_rotary(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
         (flags & ~kRotaryFlags) != 0 || !isfinite(magnitude) || !inv_freq) {
         return KDA_ERR_INVALID_ARG;
     }
-    if ((k == nullptr) != (k_out == nullptr) || (k == nullptr && Hk != 0) ||
-        (k != nullptr && Hk == 0 && T > 0)) {
+    if (T > 0 && (!q || !q_out || !positions || (Hk > 0) != (k != nullptr) ||
+                  (Hk > 0) != (k_out != nullptr))) {
         return KDA_ERR_INVALID_ARG;
     }
-    if (T > 0 && (!q || !q_out || !positions)) return KDA_ERR_INVALID_ARG;
     const int64_t nq = (int64_t)Hq * d, nk = (int64_t)Hk * d;
     if (!good_stride(q_stride, nq, dt) || !good_stride(q_out_stride, nq, dt) ||
-        (k && (!good_stride(k_stride, nk, dt) || !good_stride(k_out_stride, nk, dt)))) {
+        (Hk > 0 && (!good_stride(k_stride, nk, dt) || !good_stride(k_out_stride, nk, dt)))) {
         return KDA_ERR_INVALID_ARG;
     }
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) ||
@@ -146,9 +145,9 @@ int kda_rotary(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
     }
     const size_t eb = elem_bytes(dt);
     const Rows in[2] = {{q, T, (size_t)q_stride * eb, (size_t)nq * eb},
-                        {k, k ? T : 0, (size_t)k_stride * eb, (size_t)nk * eb}};
+                        {k, Hk > 0 ? T : 0, (size_t)k_stride * eb, (size_t)nk * eb}};
     const Rows out[2] = {{q_out, T, (size_t)q_out_stride * eb, (size_t)nq * eb},
-                         {k_out, k ? T : 0, (size_t)k_out_stride * eb, (size_t)nk * eb}};
+                         {k_out, Hk > 0 ? T : 0, (size_t)k_out_stride * eb, (size_t)nk * eb}};
     for (int o = 0; o < 2; ++o) {
         for (int i = 0; i < 2; ++i) {
             const bool itself = i == o && out[o].p == in[i].p &&

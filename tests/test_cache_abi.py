@@ -60,6 +60,7 @@ def test_rotary_refusals(L, over, expect):
 def test_rotary_without_rows_launches_nothing(L):
     assert _rotary(L, T=0) == kda.KDA_OK
     assert _rotary(L, T=0, q=None, qo=None, pos=None) == kda.KDA_OK
+    assert _rotary(L, T=0, q=None, qo=None, pos=None, k=None, ko=None) == kda.KDA_OK
 
 
 def _plan(L, **over):

@@ -63,3 +63,26 @@ def test_steps_of_a_layer():
     assert int(n_free) == nb - held
     assert sorted(free[:int(n_free)].tolist() + [int(table[i, j]) for i, c in enumerate(past.tolist())
                                                  for j in range(-(-c // block))]) == list(range(nb))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_step_without_tokens(dtype):
+    """Requests end or wait, and no row comes: every call takes empty tensors."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table, free, n_free = torch.tensor([[0, 1], [2, 0]], **i32), torch.zeros(4, **i32), \
+        torch.tensor([0], **i32)
+    p = kda.kda_cache_plan(torch.tensor([20, 3], **i32), torch.tensor([-1, 0], **i32), table, free,
+                           n_free, 16, 0, n_free_out=n_free)
+    assert p["context_lens"].tolist() == [0, 3] and n_free.tolist() == [2]
+    assert p["slots"].shape == p["positions"].shape == (0,)
+    wide = torch.empty(0, 6, 32, dtype=dtype, device="cuda")
+    q, k, v = wide[:, :4], wide[:, 4:5], wide[:, 5:]
+    f, _ = kda.rotary_frequencies(32)
+    assert kda.kda_rotary(q, k, p["positions"], f, q_out=q, k_out=k)[0].shape == (0, 4, 32)
+    assert kda.kda_rotary_backward(q, None, p["positions"], f)[0].shape == (0, 4, 32)
+    cache = [torch.zeros(4, 1, 16, 32, device="cuda").to(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.ones(4, 1, device="cuda") for _ in range(2)]
+    kda.kda_cache_write(k, v, p["slots"], *cache, *scales)
+    o = kda.kda_cache_attention(q, *cache, *scales, table, p["context_lens"], p["cu_seqlens"])
+    assert o.shape == (0, 4, 32)
+    torch.cuda.synchronize()

@@ -87,7 +87,7 @@ struct CacheAttention {
 bool cache_prompt_takes(int32_t d, int dtype);
 size_t cache_prompt_room(int32_t d, int sms);
 cudaError_t launch_cache_prompt(const CacheAttention& p, int sms, cudaStream_t stream);
-// Whether a call's prompts go to it: so many rows in all, and in the longest request.
+// Whether a call's prompts may go to it: so many rows in all, and in the longest request.
 bool cache_prompt_used(int32_t heads, int32_t group, int32_t T, int32_t max_new, int32_t d,
                        int dtype);
 // Bytes of partial sums, on a device of that many SMs.

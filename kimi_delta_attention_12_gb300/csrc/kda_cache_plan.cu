@@ -3,8 +3,10 @@
 // each row.
 //
 // Bound by latency: one block of 1,024 threads does the requests, the sums in two passes
-// because what is taken depends on how much all ended requests have returned; many blocks do
-// the rows, each row finding its request by bisection of the row starts.
+// because what is taken depends on how much all ended requests have returned; the rows, each of
+// which finds its request by bisection of the row starts, are done by the same block up to 4,096
+// of them, by many blocks in a second launch beyond.  256 requests of one token 5.4 us (two launches
+// 8.4), 16 prompts of 109,824 tokens 13 us.
 #include "../../include/kda.h"
 #include "kda_cache.h"
 #include "kda_follow.cuh"

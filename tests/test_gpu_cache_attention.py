@@ -102,9 +102,13 @@ def test_prompts_and_pieces(Hq, H, d, block, dtype):
         b.check(kda.kda_cache_attention(*args, max_new=most))
 
 
-def _tensor_cores(b, H):
-    """Whether the batch has the rows from which on prompts go to the tensor cores' kernel."""
-    return b.q.shape[0] * b.q.shape[1] >= 4096 and max(b.new) * b.q.shape[1] // H >= 64
+def _tensor_cores(b):
+    """The batch's arguments with a table that can hold so much that its prompts go to the tensor
+    cores' kernel, and the most new tokens."""
+    rows, H = b.q.shape[0] * b.q.shape[1], b.ks.shape[1]
+    assert rows >= 1024 and max(b.new) * b.q.shape[1] // H >= 64 and rows << 16 >= 1 << 23
+    args = b.args()
+    return (*args[:5], b.wide(), *args[6:]), max(b.new)
 
 
 @pytest.mark.parametrize("past,new,block,Hq,H,d", [
@@ -118,23 +122,23 @@ def _tensor_cores(b, H):
 ])
 def test_prompts_on_the_tensor_cores(past, new, block, Hq, H, d):
     b = Batch(past, new, block, Hq, H, d, torch.bfloat16, seed=sum(new))
-    assert _tensor_cores(b, H)
+    args, most = _tensor_cores(b)
     ws = torch.full((kda.cache_attention_workspace_bytes(b.q.shape[0], max(new), Hq, H, d, torch.bfloat16),), 255,
                     dtype=torch.uint8, device="cuda")
-    got = kda.kda_cache_attention(*b.args(), max_new=max(new), workspace=ws)
+    got = kda.kda_cache_attention(*args, max_new=most, workspace=ws)
     b.check(got)
     assert kda.workspace_status(ws) == kda.KDA_OK
-    assert torch.equal(got, kda.kda_cache_attention(*b.args(), max_new=max(new)))
-    b.check(kda.kda_cache_attention(*b.args(), max_new=1))    # the other kernel, all rows
+    assert torch.equal(got, kda.kda_cache_attention(*args, max_new=most))
+    b.check(kda.kda_cache_attention(*args, max_new=1))    # the other kernel, all rows
 
 
 @pytest.mark.parametrize("d", [64, 128])
 def test_extremes_on_the_tensor_cores(d):
     b = Batch([60, 0], [130, 100], 16, 32, 8, d, torch.bfloat16, seed=d)
-    assert _tensor_cores(b, 8)
     b.vs = torch.exp2(torch.randint(-60, 61, b.vs.shape,
                                     generator=torch.Generator().manual_seed(7)).float())
-    b.check(kda.kda_cache_attention(*b.args(), max_new=130))
+    args, most = _tensor_cores(b)
+    b.check(kda.kda_cache_attention(*args, max_new=most))
     b.vs.fill_(1.0)
     b.q[::3] *= 1e30
     b.q[1::3] *= 1e-30
@@ -143,7 +147,7 @@ def test_extremes_on_the_tensor_cores(d):
         if scale in (-0.3, 3.0):
             b.q = torch.randn(b.q.shape, generator=torch.Generator().manual_seed(1)).bfloat16()
         b.scale = scale
-        b.check(kda.kda_cache_attention(*b.args(), max_new=130, scale=scale))
+        b.check(kda.kda_cache_attention(*_tensor_cores(b)[0], max_new=most, scale=scale))
 
 
 def test_growing_scores_on_the_tensor_cores():
@@ -153,24 +157,21 @@ def test_growing_scores_on_the_tensor_cores():
         b.k[b.table[0][p // 64], :, p % 64, :8] = int(p / 1028 * 120)
     b.q[:, :, :8] = b.q[:, :, :8].abs() + 1.0
     b.scale = 0.5
-    b.check(kda.kda_cache_attention(*b.args(), max_new=128, scale=0.5))
+    b.check(kda.kda_cache_attention(*_tensor_cores(b)[0], max_new=128, scale=0.5))
 
 
 def test_rows_without_keys_on_the_tensor_cores():
     b = Batch([0, 200, 0], [130, 140, 70], 16, 16, 4, 64, torch.bfloat16, seed=8)
-    args = list(b.args())
     b.context = [0, 100, 30]           # fewer tokens than new ones
-    args[6] = torch.tensor(b.context, dtype=torch.int32).cuda()
     b.table[1][2] = -1
-    args[5] = torch.tensor(b.table, dtype=torch.int32).cuda()
-    got = kda.kda_cache_attention(*args, max_new=140)
+    got = kda.kda_cache_attention(*_tensor_cores(b)[0], max_new=140)
     assert not got[:130].any()
     b.check(got)
 
 
 def test_a_query_that_is_not_finite_on_the_tensor_cores():
     b = Batch([70, 9], [140, 130], 16, 16, 8, 64, torch.bfloat16, seed=10)
-    args = b.args()
+    args, _ = _tensor_cores(b)
     want = kda.kda_cache_attention(*args, max_new=140)
     q = args[0].clone()
     q[1, 2, 5], q[200, 0, 0] = float("nan"), float("inf")

@@ -46,8 +46,8 @@ def test_blocks_beyond_four_gigabytes():
         want, *sizes = R.attention(q, *small, *scales, [[0, 1, 2], [3, 4, 5]], past, cu, d ** -0.5,
                                    block)
         bound = R.attention_bound(want, *sizes, d, max(past), True)
-        for most, t in ((max(new), table), (1, table),
-                        (1, torch.cat((table, table.expand(2, 3).repeat(1, 200)), 1))):
+        wide = torch.cat((table, table.expand(2, 3).repeat(1, 200)), 1)    # other kernels' share
+        for most, t in ((max(new), table), (1, table), (max(new), wide), (1, wide)):
             o = kda.kda_cache_attention(q, k_cache, v_cache, k_scale, v_scale, t.contiguous(),
                                         torch.tensor(past, **i32), torch.tensor(cu, **i32),
                                         max_new=most)
@@ -56,7 +56,7 @@ def test_blocks_beyond_four_gigabytes():
 
 
 def test_prompts_in_graphs_that_share_a_workspace():
-    from test_gpu_cache_attention import Batch
+    from test_gpu_cache_attention import Batch, _tensor_cores
     a = Batch([0, 70], [150, 90], 16, 32, 8, 64, torch.bfloat16, seed=1)
     b = Batch([300], [130], 32, 32, 8, 64, torch.bfloat16, seed=2)
     ws = torch.empty(max(kda.cache_attention_workspace_bytes(x.q.shape[0], max(x.new), 32, 8, 64,
@@ -64,7 +64,7 @@ def test_prompts_in_graphs_that_share_a_workspace():
                      dtype=torch.uint8, device="cuda")
     graphs = []
     for x in (a, b):
-        args = x.args()
+        args, _ = _tensor_cores(x)
         kda.kda_cache_attention(*args, max_new=max(x.new), workspace=ws)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
@@ -84,8 +84,8 @@ def test_prompts_in_graphs_that_share_a_workspace():
 
 def test_many_pieces_of_prompts():
     """More items than blocks, items across blocks, and tiles that do not need all of their steps."""
-    from test_gpu_cache_attention import Batch
+    from test_gpu_cache_attention import Batch, _tensor_cores
     b = Batch([0, 600], [700, 40], 64, 64, 16, 64, torch.bfloat16, seed=3)
-    b.check(kda.kda_cache_attention(*b.args(), max_new=700))
+    b.check(kda.kda_cache_attention(*_tensor_cores(b)[0], max_new=700))
     b = Batch([2000], [260], 128, 32, 2, 128, torch.bfloat16, seed=4)
-    b.check(kda.kda_cache_attention(*b.args(), max_new=260))
+    b.check(kda.kda_cache_attention(*_tensor_cores(b)[0], max_new=260))

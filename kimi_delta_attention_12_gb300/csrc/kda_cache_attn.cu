@@ -97,6 +97,11 @@ __device__ __forceinline__ Span span_of(const CacheAttention& p, int i, int R) {
     return s;
 }
 
+// a / b, both not negative; 64-bit quotients only where they must be.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // What each block takes: the units begin .. end - 1 of all, and the request that unit `begin`
 // belongs to.  All threads of the block; every thread gets the result.
 struct Stretch {
@@ -131,7 +136,7 @@ __device__ __forceinline__ Stretch stretch_of(const CacheAttention& p, int R, in
         total += sums[i];
     }
     Stretch s;
-    s.per = (total + blocks - 1) / blocks;
+    s.per = quotient(total + blocks - 1, blocks);
     if (s.per < 1) s.per = 1;
     s.begin = s.per * block;
     s.end = s.begin + s.per < total ? s.begin + s.per : total;
@@ -163,9 +168,9 @@ __device__ __forceinline__ Item item_at(const CacheAttention& p, int R, int64_t 
         s = span_of<UNIT>(p, ++i, R);
     }
     Item t;
-    const int64_t n = (at - first) / s.units;
+    const int64_t n = quotient(at - first, s.units);
     t.request = i;
-    t.head = (int)(n / s.tiles);
+    t.head = (int)quotient(n, s.tiles);
     // first, last, second, last but one, ...: under a causal mask a tile and its neighbour together
     // have the same work wherever they stand
     const int k = (int)(n - (int64_t)t.head * s.tiles);
@@ -280,13 +285,22 @@ __device__ __forceinline__ void load_tokens(const CacheAttention& p, Tokens<D>& 
     }
 }
 
-// Units unit0 .. unit0 + units - 1 of an item by WARPS warps: every warp's sums [WARPS][R][D] in
-// `sums`, then their references and weights [WARPS][R] each.
+// The warps' sums in shared memory: [WARPS][R] rows of sum_stride(D), then their references and
+// weights [WARPS][R] each.  Column 2 c + n of an 8-column tile has place 4 n + c there: with the
+// rows' 4 floats of padding a half-warp's pairs lie in different banks, or two to a bank.
+__host__ __device__ constexpr int sum_stride(int D) { return D + 4; }
+__host__ __device__ constexpr int sums_of(int D, int R, int warps) {
+    return warps * R * (sum_stride(D) + 2);
+}
+__device__ __forceinline__ int sum_place(int n) { return (n & ~7) + 4 * (n & 1) + ((n & 7) >> 1); }
+
+// Units unit0 .. unit0 + units - 1 of an item by WARPS warps: every warp's sums into `sums`.
 template <int D, int NT, bool F32, int WARPS>
 __device__ __forceinline__ void attend(const CacheAttention& p, const Item& it, int unit0,
                                        int units, float* sums) {
     constexpr int R = 8 * NT, kSteps = D / 16, Q = F32 ? 2 : 1, UNIT = 16 * WARPS;
-    float* sums_m = sums + WARPS * R * D;
+    constexpr int S = sum_stride(D);
+    float* sums_m = sums + WARPS * R * S;
     float* sums_l = sums_m + WARPS * R;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const int rows = it.fresh * p.group - it.tile * R;      // of this tile, may be above R
@@ -517,38 +531,44 @@ __device__ __forceinline__ void attend(const CacheAttention& p, const Item& it, 
             for (int d = 4; d < 32; d <<= 1) {
                 l[t][n] += __shfl_xor_sync(0xffffffffu, l[t][n], d);
             }
-            const int col = 8 * t + 2 * c + n;
+            const int col = 8 * t + 4 * n + c;
             if (g == 0) {
                 sums_m[w * R + col] = m[t][n];
                 sums_l[w * R + col] = l[t][n];
             }
-            float* to = sums + (w * R + col) * D + g * (D / 8);
+            float* to = sums + (w * R + col) * S + g * (D / 8);
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
-                to[2 * i] = o[t][i][n];
-                to[2 * i + 1] = o[t][i][n + 2];
+                *reinterpret_cast<float2*>(to + 2 * i) = make_float2(o[t][i][n], o[t][i][n + 2]);
             }
         }
     }
 }
 
-// Channel d of row n from the warps' sums, with the reference and weight of all of them.
+// Channels d .. d + 3 of row n from the warps' sums, with the reference and weight of all of them.
 template <int D, int R, int WARPS>
-__device__ __forceinline__ void meet(const float* sums, int n, int d, float& total, float& weight,
-                                     float& top) {
-    const float* sums_m = sums + WARPS * R * D;
+__device__ __forceinline__ float4 meet(const float* sums, int n, int d, float& weight, float& top) {
+    constexpr int S = sum_stride(D);
+    const int place = sum_place(n);
+    const float* sums_m = sums + WARPS * R * S + place;
     const float* sums_l = sums_m + WARPS * R;
     top = kNone;
 #pragma unroll
-    for (int k = 0; k < WARPS; ++k) top = fmaxf(top, sums_m[k * R + n]);
+    for (int k = 0; k < WARPS; ++k) top = fmaxf(top, sums_m[k * R]);
     const float ref = top == kNone ? 0.0f : top;
-    total = weight = 0.0f;
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    weight = 0.0f;
 #pragma unroll
     for (int k = 0; k < WARPS; ++k) {
-        const float f = exp2_of(sums_m[k * R + n] - ref);
-        total = fmaf(f, sums[(k * R + n) * D + d], total);
-        weight = fmaf(f, sums_l[k * R + n], weight);
+        const float f = exp2_of(sums_m[k * R] - ref);
+        const float4 x = *reinterpret_cast<const float4*>(sums + (k * R + place) * S + d);
+        y.x = fmaf(f, x.x, y.x);
+        y.y = fmaf(f, x.y, y.y);
+        y.z = fmaf(f, x.z, y.z);
+        y.w = fmaf(f, x.w, y.w);
+        weight = fmaf(f, sums_l[k * R], weight);
     }
+    return y;
 }
 
 // Where row n of an item's tile goes in o.
@@ -556,51 +576,6 @@ __device__ __forceinline__ int64_t place_of(const CacheAttention& p, const Item&
                                             int D) {
     const int flat = it.tile * R + n, j = flat / p.group;
     return ((it.row0 + j) * (p.heads * p.group) + it.head * p.group + flat - j * p.group) * D;
-}
-
-template <int D, int NT, bool F32>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(NT, D)) cache_attention_kernel(
-    CacheAttention p) {
-    constexpr int R = 8 * NT;
-    extern __shared__ float sums[];
-    let_follow();
-    if (p.clears && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
-    const Stretch s = stretch_of<kThreads>(p, R, blockIdx.x, gridDim.x);
-    if (s.request < 0) return;
-    int request = s.request;
-    int64_t first = s.first;
-    for (int64_t at = s.begin; at < s.end;) {
-        const Item it = item_at(p, R, at, request, first);
-        const int unit0 = (int)(at - it.begin);
-        const int units = (int)(s.end - at < it.units - unit0 ? s.end - at : it.units - unit0);
-        attend<D, NT, F32, kWarps>(p, it, unit0, units, sums);
-        __syncthreads();
-        const int rows = it.fresh * p.group - it.tile * R, valid = rows < R ? rows : R;
-        const bool whole = unit0 == 0 && units == it.units;
-        float* part = p.partial + (int64_t)(blockIdx.x * 2 + (at != s.begin)) * R * (D + 2);
-        for (int i = threadIdx.x; i < valid * D; i += kThreads) {
-            const int n = i / D, d = i - n * D;
-            float total, weight, top;
-            meet<D, R, kWarps>(sums, n, d, total, weight, top);
-            if (whole) {
-                const int64_t to = place_of(p, it, R, n, D) + d;
-                const float y = weight == 0.0f ? 0.0f : total / weight;
-                if (F32) {
-                    static_cast<float*>(p.o)[to] = y;
-                } else {
-                    static_cast<__nv_bfloat16*>(p.o)[to] = __float2bfloat16_rn(y);
-                }
-            } else {
-                part[i] = total;
-                if (d == 0) {
-                    part[R * D + n] = top;
-                    part[R * D + R + n] = weight;
-                }
-            }
-        }
-        __syncthreads();
-        at += units;
-    }
 }
 
 // Four neighbouring channels of the result.
@@ -618,6 +593,46 @@ __device__ __forceinline__ void store4(void* o, int64_t to, const float4& y, flo
     }
 }
 
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(NT, D)) cache_attention_kernel(
+    CacheAttention p) {
+    constexpr int R = 8 * NT;
+    extern __shared__ __align__(16) float sums[];
+    let_follow();
+    if (p.clears && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+    const Stretch s = stretch_of<kThreads>(p, R, blockIdx.x, gridDim.x);
+    if (s.request < 0) return;
+    int request = s.request;
+    int64_t first = s.first;
+    for (int64_t at = s.begin; at < s.end;) {
+        const Item it = item_at(p, R, at, request, first);
+        const int unit0 = (int)(at - it.begin);
+        const int units = (int)(s.end - at < it.units - unit0 ? s.end - at : it.units - unit0);
+        attend<D, NT, F32, kWarps>(p, it, unit0, units, sums);
+        __syncthreads();
+        const int rows = it.fresh * p.group - it.tile * R, valid = rows < R ? rows : R;
+        const bool whole = unit0 == 0 && units == it.units;
+        float* part = p.partial + (int64_t)(blockIdx.x * 2 + (at != s.begin)) * R * (D + 2);
+        for (int i = 4 * threadIdx.x; i < valid * D; i += 4 * kThreads) {
+            const int n = i / D, d = i - n * D;
+            float weight, top;
+            const float4 y = meet<D, R, kWarps>(sums, n, d, weight, top);
+            if (whole) {
+                store4<F32>(p.o, place_of(p, it, R, n, D) + d, y,
+                            weight == 0.0f ? 0.0f : 1.0f / weight);
+            } else {
+                *reinterpret_cast<float4*>(part + i) = y;
+                if (d == 0) {
+                    part[R * D + n] = top;
+                    part[R * D + R + n] = weight;
+                }
+            }
+        }
+        __syncthreads();
+        at += units;
+    }
+}
+
 // Few requests and heads: a cluster of blocks for each, which share its tokens and join their sums
 // through one another's shared memory, all in one launch.
 __host__ __device__ constexpr int cluster_warps(int NT) { return NT == 1 ? 8 : 4; }
@@ -627,8 +642,8 @@ __global__ void __launch_bounds__(32 * cluster_warps(NT), 1) cache_attention_clu
     CacheAttention p) {
     namespace cg = cooperative_groups;
     constexpr int R = 8 * NT, W = cluster_warps(NT), kAll = 32 * W;
-    extern __shared__ float sums[];          // the warps', then this block's: [R][D], m, l [R]
-    float* block_o = sums + W * R * (D + 2);
+    extern __shared__ __align__(16) float sums[];          // the warps', then this block's: [R][D], m, l [R]
+    float* block_o = sums + sums_of(D, R, W);
     float* block_m = block_o + R * D;
     float* block_l = block_m + R;
     if (p.clears && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
@@ -650,10 +665,10 @@ __global__ void __launch_bounds__(32 * cluster_warps(NT), 1) cache_attention_clu
         attend<D, NT, F32, W>(p, it, unit0, units, sums);
         __syncthreads();
         const int rows = it.fresh * p.group - it.tile * R, valid = rows < R ? rows : R;
-        for (int i = threadIdx.x; i < valid * D; i += kAll) {
+        for (int i = 4 * threadIdx.x; i < valid * D; i += 4 * kAll) {
             const int n = i / D, d = i - n * D;
             float weight, top;
-            meet<D, R, W>(sums, n, d, block_o[i], weight, top);
+            *reinterpret_cast<float4*>(block_o + i) = meet<D, R, W>(sums, n, d, weight, top);
             if (d == 0) {
                 block_m[n] = top;
                 block_l[n] = weight;
@@ -699,7 +714,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(Cach
     const Item it = item_at(p, R, s.begin, request, first);
     if (it.begin == s.begin || it.begin + it.units > s.end) return;
     const int rows = it.fresh * p.group - it.tile * R, valid = rows < R ? rows : R;
-    const int b0 = (int)(it.begin / s.per), parts = blockIdx.x - b0 + 1;
+    const int b0 = (int)quotient(it.begin, s.per), parts = blockIdx.x - b0 + 1;
     auto part_of = [&](int k) {
         const bool second = k == 0 && it.begin != b0 * s.per;
         return p.partial + (int64_t)((b0 + k) * 2 + second) * kStride;
@@ -785,7 +800,7 @@ cudaError_t launch_clusters(const CacheAttention& p, int blocks, cudaStream_t st
     cudaLaunchConfig_t config = {};
     config.gridDim = dim3(p.N * p.heads * blocks);
     config.blockDim = dim3(32 * W);
-    config.dynamicSmemBytes = (size_t)(W + 1) * R * (D + 2) * sizeof(float);
+    config.dynamicSmemBytes = (size_t)(sums_of(D, R, W) + R * (D + 2)) * sizeof(float);
     config.stream = stream;
     config.attrs = &attr;
     config.numAttrs = 1;
@@ -801,7 +816,7 @@ cudaError_t launch_tiles(const CacheAttention& p, int sms, cudaStream_t stream) 
         if (launch_clusters<D, NT, F32>(p, cluster, stream) == cudaSuccess) return cudaSuccess;
         cudaGetLastError();                  // a device that cannot take them (a part of a GPU)
     }
-    const size_t smem = (size_t)kWarps * R * (D + 2) * sizeof(float);
+    const size_t smem = (size_t)sums_of(D, R, kWarps) * sizeof(float);
     const int blocks = sms * blocks_per_sm(NT, D);
     cache_attention_kernel<D, NT, F32><<<blocks, kThreads, smem, stream>>>(p);
     cudaError_t err = cudaGetLastError();

@@ -28,8 +28,9 @@
 // tokens of two units on their way, 8 KB; 12 warps an SM keep HBM busy.  128 requests over 1.1 M
 // cached tokens, 32 heads over 8, d = 128, bf16: 385 us, 6.3 TB/s, 93 % of the measured copy.
 // Prompts in fp32 or of d = 32, which the tensor-core form does not take, come here too, 16 rows a
-// tile: 6 requests of 824 new tokens, 15 heads over 3, d = 64, fp32 35 us (tiles of 32 rows, which
-// spill, 43).
+// tile: 6 requests of 824 new tokens, 15 heads over 3, d = 64, fp32 30 us (35 when each channel of the
+// warps' sums was added up for itself; tiles of 32 rows, which spill, took 8 more; 64 rows an item, 16
+// for each warp over all its tokens, 39: four times the partial sums).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -308,6 +309,10 @@ __device__ __forceinline__ void attend(const CacheAttention& p, const Item& it, 
     const int last = rows < R ? rows : R;
     const int low = hidden + it.tile * R / p.group;                  // what the tile's first row
     const int high = hidden + (it.tile * R + last - 1) / p.group;    // and its last row see
+    if (R == 16) {                       // a prompt's tiles end before its tokens do
+        const int past = high > 0 ? (high - 1) / UNIT + 1 - unit0 : 0;
+        if (units > past) units = past;
+    }
     // ---- the first tokens on their way
     const int32_t* table = p.table + (int64_t)it.request * p.width;
     int ids = -1;                        // of the blocks of 32 units, one in each lane
@@ -827,9 +832,14 @@ cudaError_t launch_tiles(const CacheAttention& p, int sms, cudaStream_t stream) 
 
 template <int D, bool F32>
 cudaError_t launch_dim(const CacheAttention& p, int sms, cudaStream_t stream) {
-    // one column tile where the rows of every request fit it, else two: half the reads of K and V
-    return (int64_t)p.group * p.max_new <= 8 ? launch_tiles<D, 1, F32>(p, sms, stream)
-                                             : launch_tiles<D, 2, F32>(p, sms, stream);
+    // one column tile where the rows of every request fit it, else two: half the reads of K and V.
+    // Beside the tensor cores' kernel the other requests' rows count, at their average: 63 single
+    // tokens, 200 new ones, 32 heads over 8, d = 128, behind 2,000 each 122 -> 105 us; 64 times 4
+    // and 500 behind 4,000, which stay with two, 169 against 213.
+    const int64_t rows = p.many_rows == INT64_MAX ? (int64_t)p.group * p.max_new
+                         : (int64_t)p.group * (p.T - p.max_new) / (p.N - 1);
+    return rows <= 8 ? launch_tiles<D, 1, F32>(p, sms, stream)
+                     : launch_tiles<D, 2, F32>(p, sms, stream);
 }
 
 template <bool F32>

@@ -19,16 +19,19 @@
 // The value scale of a block goes into the exponent: with p' = 2^(s - m + 15) v_scale, m the
 // running maximum of s + log2 v_scale, P' is at most 2^15 whatever the scales, and the sum of
 // weights takes p' / v_scale.  The 2^15 is for fp16's range: weights down to 2^-29 of the largest
-// keep all their bits, and nothing above 2^-40 is lost, however many keys share it.
+// keep all their bits, and nothing above 2^-40 is lost, however many keys share it.  For bf16 m may
+// stay up to 4 below the maximum, at 2^11 instead: a unit whose scores do not pass that, which each
+// lane sees for its own, needs no maxima across lanes and no rescaling (256 requests of 4,000 tokens,
+// 32 heads over 8, d = 64: 237 -> 214 us; fp32, which keeps the range, 257 -> 235).
 //
 // Work is cut by tokens, not by requests: all (request, head, row tile) items in a row, each
 // ceil(tokens / 64) units, and every block takes the same stretch of units.  An item that lies
 // across blocks leaves partial sums, which a second kernel joins.  The 4 warps of a block take
 // 16 tokens of a unit each, with sums of their own that meet at the item's end.  A warp has the
-// tokens of two units on their way, 8 KB; 12 warps an SM keep HBM busy.  128 requests over 1.1 M
-// cached tokens, 32 heads over 8, d = 128, bf16: 385 us, 6.3 TB/s, 93 % of the measured copy.
+// tokens of two units on their way, 8 KB; 12 warps an SM keep HBM busy (d = 128).  128 requests over 1.1 M
+// cached tokens, 32 heads over 8, d = 128, bf16: 380 us, 6.4 TB/s, 94 % of the measured copy.
 // Prompts in fp32 or of d = 32, which the tensor-core form does not take, come here too, 16 rows a
-// tile: 6 requests of 824 new tokens, 15 heads over 3, d = 64, fp32 30 us (35 when each channel of the
+// tile: 6 requests of 824 new tokens, 15 heads over 3, d = 64, fp32 31 us (35 when each channel of the
 // warps' sums was added up for itself; tiles of 32 rows, which spill, took 8 more; 64 rows an item, 16
 // for each warp over all its tokens, 39: four times the partial sums).
 #include <cooperative_groups.h>
@@ -47,7 +50,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kJoinThreads = 256;
 constexpr float kNone = -INFINITY;
-constexpr float kRaise = 15.0f;
+// In powers of two: how far a weight may pass its reference, and what the reference stands for.
+__host__ __device__ constexpr float slack_of(bool F32) { return F32 ? 0.0f : 4.0f; }
+__host__ __device__ constexpr float raise_of(bool F32) { return 15.0f - slack_of(F32); }
 // From where on prompts go to the tensor cores: rows of the longest request, rows of all heads, and
 // those times the tokens that the table can hold.  32 heads over 8, d = 128, one request, us, this
 // kernel against that one: 128 / 256 new tokens of 1K 32 against 36 / 48 against 37; 32 / 64 of 8K
@@ -55,9 +60,13 @@ constexpr float kRaise = 15.0f;
 constexpr int64_t kManyRows = 64, kManyHeadRows = 1024, kManyWork = (int64_t)1 << 23;
 constexpr int kRounds = 24;          // of a warp in a cluster
 
-// Blocks that an SM holds at once, by what a tile needs in registers (fp32 prompts at d = 64 with 3
-// instead of 2, some registers spilled: 38.1 -> 35.4 us).
-__host__ __device__ constexpr int blocks_per_sm(int NT, int D) { return NT == 1 || D <= 64 ? 3 : 2; }
+// Blocks that an SM holds at once, by what a tile needs in registers.  More warps, a few registers
+// spilled, beat fewer: single tokens as above, d = 64 with 4 instead of 3 blocks 214 -> 187 us,
+// d = 32 with 5 instead of 3 175 -> 140 us, 16 rows there with 4 instead of 3 197 -> 175 us; fp32
+// prompts at d = 64 with 3 instead of 2 38.1 -> 35.4 us.
+__host__ __device__ constexpr int blocks_per_sm(int NT, int D) {
+    return (D == 32 ? 6 : D == 64 ? 5 : 4) - NT;
+}
 
 struct Item {
     int request, head, tile;
@@ -316,15 +325,18 @@ __device__ __forceinline__ void attend(const CacheAttention& p, const Item& it, 
     // ---- the first tokens on their way
     const int32_t* table = p.table + (int64_t)it.request * p.width;
     int ids = -1;                        // of the blocks of 32 units, one in each lane
-    float k_scale = 0.0f, v_scale = 1.0f;
+    float k_scale = 0.0f, v_log = 0.0f, v_inverse = 1.0f;
     auto look_up = [&](int u) {
         const int base = (unit0 + u + lane) * UNIT + 16 * w;
         ids = u + lane < units && base < high ? table[base >> p.block_log2] : -1;
         k_scale = 0.0f;
-        v_scale = 1.0f;
+        v_log = 0.0f;
+        v_inverse = 1.0f;
         if (ids >= 0 && ids < p.num_blocks) {
             k_scale = p.k_scale[(int64_t)ids * p.heads + it.head];
-            v_scale = p.v_scale[(int64_t)ids * p.heads + it.head];
+            const float v_scale = p.v_scale[(int64_t)ids * p.heads + it.head];
+            v_log = __log2f(v_scale);
+            v_inverse = __frcp_rn(v_scale);
         }
     };
     int u0 = 0, n = units < 32 ? units : 32;     // units of which `ids` holds the blocks
@@ -401,7 +413,7 @@ __device__ __forceinline__ void attend(const CacheAttention& p, const Item& it, 
             o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.0f;
         }
     }
-    auto multiply = [&](const Tokens<D>& x, int u, float ks, float vs, bool there) {
+    auto multiply = [&](const Tokens<D>& x, int u, float ks, float lv, float iv, bool there) {
         const int base = (unit0 + u) * UNIT + 16 * w;
         if (base >= high || !there) return;
         float sc[NT][4];
@@ -420,7 +432,6 @@ __device__ __forceinline__ void attend(const CacheAttention& p, const Item& it, 
                 }
             }
         }
-        const float lv = __log2f(vs), iv = __frcp_rn(vs);
         const bool partly = base + 16 > low;
         uint32_t b[Q][NT][2];
 #pragma unroll
@@ -437,21 +448,27 @@ __device__ __forceinline__ void attend(const CacheAttention& p, const Item& it, 
                 sc[t][n + 2] = s1;
             }
         }
-        float up[NT][2];
         bool more = false;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                float x = fmaxf(sc[t][n], sc[t][n + 2]);
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                up[t][n] = fmaxf(m[t][n], x);
-                more |= up[t][n] > m[t][n];
+                more |= fmaxf(sc[t][n], sc[t][n + 2]) > m[t][n] + slack_of(F32);
             }
         }
         if (__any_sync(0xffffffffu, more)) {
+            float up[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    float x = fmaxf(sc[t][n], sc[t][n + 2]);
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                    up[t][n] = fmaxf(m[t][n], x);
+                }
+            }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 float less[2];
@@ -475,7 +492,7 @@ __device__ __forceinline__ void attend(const CacheAttention& p, const Item& it, 
             float e[4];
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                const float top = (m[t][n] == kNone ? 0.0f : m[t][n]) - kRaise;
+                const float top = (m[t][n] == kNone ? 0.0f : m[t][n]) - raise_of(F32);
                 e[n] = exp2_of(sc[t][n] - top);
                 e[n + 2] = exp2_of(sc[t][n + 2] - top);
                 l[t][n] = fmaf(e[n] + e[n + 2], iv, l[t][n]);
@@ -510,8 +527,9 @@ __device__ __forceinline__ void attend(const CacheAttention& p, const Item& it, 
     auto take = [&](const Tokens<D>& from, int u) {
         const int id = __shfl_sync(0xffffffffu, ids, u);
         const float ks = __shfl_sync(0xffffffffu, k_scale, u);
-        const float vs = __shfl_sync(0xffffffffu, v_scale, u);
-        multiply(from, u0 + u, ks, vs, id >= 0 && id < p.num_blocks);
+        const float lv = __shfl_sync(0xffffffffu, v_log, u);
+        const float iv = __shfl_sync(0xffffffffu, v_inverse, u);
+        multiply(from, u0 + u, ks, lv, iv, id >= 0 && id < p.num_blocks);
     };
     while (u0 < units) {
         for (int u = 0; u < n; u += 2) {

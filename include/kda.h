@@ -815,7 +815,7 @@ KDA_API int kda_cache_write(const void* k, int64_t k_stride, const void* v, int6
  * tokens in the same call.
  * fp32 q and o: products to 22 bits and more, sums in fp32.  bf16: the weights
  * are rounded to 11 bits before they meet the values (e4m3 values are exact), sums in
- * fp32, one rounding to bf16.  Weights below 2^-36 of a row's heaviest (by weight times
+ * fp32, one rounding to bf16.  Weights below 2^-32 of a row's heaviest (by weight times
  * value scale; fp32: 2^-40) count in the sum of weights alone.  The same bits on every call on
  * one kind of device.  T = 0 launches nothing and leaves the workspace as it is.
  * Errors (nothing is launched): as kda_cache_write, and KDA_ERR_WORKSPACE.

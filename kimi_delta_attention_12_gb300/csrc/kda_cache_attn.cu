@@ -28,12 +28,12 @@
 // ceil(tokens / 64) units, and every block takes the same stretch of units.  An item that lies
 // across blocks leaves partial sums, which a second kernel joins.  The 4 warps of a block take
 // 16 tokens of a unit each, with sums of their own that meet at the item's end.  A warp has the
-// tokens of two units on their way, 8 KB; 12 warps an SM keep HBM busy (d = 128).  128 requests over 1.1 M
-// cached tokens, 32 heads over 8, d = 128, bf16: 380 us, 6.4 TB/s, 94 % of the measured copy.
+// tokens of two units on their way, 8 KB; 12 warps an SM keep HBM busy (d = 128).  128 requests over
+// 1.1 M cached tokens, 32 heads over 8, d = 128, bf16: 380 us, 6.4 TB/s, 94 % of the measured copy.
 // Prompts in fp32 or of d = 32, which the tensor-core form does not take, come here too, 16 rows a
-// tile: 6 requests of 824 new tokens, 15 heads over 3, d = 64, fp32 31 us (35 when each channel of the
-// warps' sums was added up for itself; tiles of 32 rows, which spill, took 8 more; 64 rows an item, 16
-// for each warp over all its tokens, 39: four times the partial sums).
+// tile: 6 requests of 824 new tokens, 15 heads over 3, d = 64, fp32 31 us (35 when each channel of
+// the warps' sums was added up for itself; tiles of 32 rows, which spill, took 8 more; 64 rows an
+// item, 16 for each warp over all its tokens, 39: four times the partial sums).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -192,10 +192,10 @@ def attention_bound(o, mass, size, least, d, longest, bf16):
     its argument up to 16); the logarithm of a value scale in the argument, rounded itself, in the
     sum and in the reference, 3 ln 2 2^-24 < 2^-22 of its size; the running sums 2^-24 for each 16 keys; for bf16 the weights' 11 bits and the
     result's rounding, 2^-8.  And an fp16 weight is off by up to 2^-25 however small it is, where
-    the largest weight times its scale is 2^11 at least for bf16, 2^15 for fp32 (whose second half
-    is an fp16 number too): 2^-36 or 2^-40 of `least`."""
+    the largest weight times its scale is 2^7 at least for bf16, 2^15 for fp32 (whose second half
+    is an fp16 number too): 2^-32 or 2^-40 of `least`."""
     ds, log_scale = size[..., :1] * (1 + d / 8) * 2.0 ** -22, size[..., 1:]
     rel = 2 * ds + 2.0 ** -20 + 2 * log_scale * 2.0 ** -22 + (longest / 16 + 8) * 2.0 ** -23
     if bf16:
-        return mass * (rel + 2.0 ** -11) + np.abs(o) * 2.0 ** -8 + least * 2.0 ** -36
+        return mass * (rel + 2.0 ** -11) + np.abs(o) * 2.0 ** -8 + least * 2.0 ** -32
     return mass * rel + least * 2.0 ** -40

@@ -816,8 +816,8 @@ KDA_API int kda_cache_write(const void* k, int64_t k_stride, const void* v, int6
  * fp32 q and o: products to 22 bits and more, sums in fp32.  bf16: the weights
  * are rounded to 11 bits before they meet the values (e4m3 values are exact), sums in
  * fp32, one rounding to bf16.  Weights below 2^-32 of a row's heaviest (by weight times
- * value scale; fp32: 2^-40) count in the sum of weights alone.  The same bits on every call on
- * one kind of device.  T = 0 launches nothing and leaves the workspace as it is.
+ * value scale; fp32: 2^-40) count in the sum of weights alone.  The same bits on every
+ * call on one kind of device.  T = 0 launches nothing and leaves the workspace as it is.
  * Errors (nothing is launched): as kda_cache_write, and KDA_ERR_WORKSPACE.
  */
 KDA_API int kda_cache_attention(const void* q, int64_t q_stride, const void* k_cache,
@@ -830,7 +830,7 @@ KDA_API int kda_cache_attention(const void* q, int64_t q_stride, const void* k_c
                                 void* stream);
 
 /* kda_cache_attention_workspace_bytes -- the workspace kda_cache_attention needs on the
- * current device: partial sums of the pieces into which the cached tokens are cut (about 10 MB,
+ * current device: partial sums of the pieces into which the cached tokens are cut (up to 5 MB,
  * 40 MB where prompts of many rows go to the tensor cores; 0 for invalid sizes). */
 KDA_API size_t kda_cache_attention_workspace_bytes(int32_t T, int32_t max_new, int32_t Hq,
                                                    int32_t Hkv, int32_t d, kda_dtype dt);

@@ -79,7 +79,7 @@ __device__ __forceinline__ void plan_row(const CachePlan& p, const int32_t* star
             }
         }
         const int64_t at = (int64_t)p.past[lo] + t - starts[lo];
-        position = (int32_t)at;
+        position = (int32_t)(at < 0x7fffffff ? at : 0x7fffffff);
         if (p.status[lo] == KDA_PLAN_OK) {
             const int32_t b = p.table[(int64_t)lo * p.width + (at >> p.block_log2)];
             slot = ((int64_t)b << p.block_log2) + (at & ((1 << p.block_log2) - 1));
@@ -141,9 +141,9 @@ __global__ void __launch_bounds__(kThreads, 1) plan_requests_kernel(CachePlan p,
         int status = KDA_PLAN_OK;
         if (r.bad) {
             status = KDA_PLAN_BAD_LENGTH;
-        } else if (r.want > p.width) {
+        } else if (r.want > p.width || r.past + r.rows > 0x7fffffff) {
             status = KDA_PLAN_TABLE;
-        } else if (end > p.T) {
+        } else if (r.rows > 0 && end > p.T) {
             status = KDA_PLAN_ROWS;
         }
         const int64_t need = status == KDA_PLAN_OK && !r.ends ? r.want - r.have : 0;

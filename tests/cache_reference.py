@@ -58,9 +58,9 @@ def plan(past, new, table, free, n_free, block, rows):
         st = 0
         if past[i] < 0 or new[i] < -1:
             st = 1
-        elif want > W:
+        elif want > W or past[i] + n > 0x7fffffff:
             st = 2
-        elif end > rows:
+        elif n > 0 and end > rows:
             st = 4
         elif new[i] != -1 and want > have:
             if starved or want - have > top:
@@ -75,7 +75,7 @@ def plan(past, new, table, free, n_free, block, rows):
     for i in range(N):
         for j in range(cu[i + 1] - cu[i]):
             p = past[i] + j
-            positions[cu[i] + j] = p
+            positions[cu[i] + j] = min(p, 0x7fffffff)
             b = table[i][p // block] if status[i] == 0 else -1
             if 0 <= b and b * block + p % block < 1 << 31:
                 slots[cu[i] + j] = b * block + p % block

@@ -67,6 +67,22 @@ def test_requests_that_are_not_served():
     assert want["status"][4:] == [4, 4, 4, 4] and want["cu_seqlens"][-1] == 20
 
 
+def test_requests_without_tokens_behind_the_last_row():
+    past, new = [0, 40, 7, 0], [30, -1, 0, 5]
+    table, free, spare = _setup(past, 16, 4, 6, 8)
+    want = _check(past, new, table, free, spare, 16, 20)
+    assert want["status"] == [4, 0, 0, 4] and want["context_lens"] == [0, 0, 7, 0]
+    assert want["n_free"] == [9]
+
+
+def test_lengths_near_the_largest_whole_number():
+    most = 0x7fffffff
+    past, new = [most, most - 3, most, 2], [most, 3, -1, most]
+    table, free, spare = _setup([0, 0, 0, 2], 128, 3, 2, 9)
+    want = _check(past, new, table, free, spare, 128, 4)
+    assert want["status"] == [2, 2, 2, 2]
+
+
 def test_returned_blocks_are_taken_in_the_same_step():
     past, new = [40, 0, 33], [-1, 48, -1]
     table, free, spare = _setup(past, 16, 4, 0, 3)

@@ -831,7 +831,7 @@ KDA_API int kda_cache_attention(const void* q, int64_t q_stride, const void* k_c
 
 /* kda_cache_attention_workspace_bytes -- the workspace kda_cache_attention needs on the
  * current device: partial sums of the pieces into which the cached tokens are cut (up to 5 MB,
- * 40 MB where prompts of many rows go to the tensor cores; 0 for invalid sizes). */
+ * 45 MB where prompts of many rows go to the tensor cores; 0 for invalid sizes). */
 KDA_API size_t kda_cache_attention_workspace_bytes(int32_t T, int32_t max_new, int32_t Hq,
                                                    int32_t Hkv, int32_t d, kda_dtype dt);
 

@@ -79,6 +79,7 @@ struct CacheAttention {
     int32_t* status;
     int32_t clears;
     float* partial;
+    float* prompt_partial;     // of the prompts' kernel
     int64_t many_rows;         // rows (heads of a group times new tokens) of a request from which
                                // on the prompts' kernel takes it, the other one below
 };
@@ -86,7 +87,9 @@ struct CacheAttention {
 // Whether the prompts' kernel has a form for these.
 bool cache_prompt_takes(int32_t d, int dtype);
 size_t cache_prompt_room(int32_t d, int sms);
+// The kernel, and what joins its parts: launched behind it, or behind one that waits for it.
 cudaError_t launch_cache_prompt(const CacheAttention& p, int sms, cudaStream_t stream);
+cudaError_t launch_cache_prompt_join(const CacheAttention& p, int sms, cudaStream_t stream);
 // Whether a call's prompts may go to it: so many rows in all, and in the longest request.
 bool cache_prompt_used(int32_t heads, int32_t group, int32_t T, int32_t max_new, int32_t d,
                        int dtype);

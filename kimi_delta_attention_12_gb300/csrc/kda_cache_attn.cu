@@ -624,10 +624,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT, D)) cache_attentio
     let_follow();
     if (p.clears && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
     const Stretch s = stretch_of<kThreads>(p, R, blockIdx.x, gridDim.x);
-    if (s.request < 0) return;
     int request = s.request;
     int64_t first = s.first;
-    for (int64_t at = s.begin; at < s.end;) {
+    for (int64_t at = s.begin; request >= 0 && at < s.end;) {
         const Item it = item_at(p, R, at, request, first);
         const int unit0 = (int)(at - it.begin);
         const int units = (int)(s.end - at < it.units - unit0 ? s.end - at : it.units - unit0);
@@ -654,6 +653,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT, D)) cache_attentio
         __syncthreads();
         at += units;
     }
+    // behind the prompts' kernel, whose sums this one does not need: its end follows that one's
+    if (blockIdx.x == gridDim.x - 1) wait_before();
 }
 
 // Few requests and heads: a cluster of blocks for each, which share its tokens and join their sums
@@ -841,8 +842,17 @@ cudaError_t launch_tiles(const CacheAttention& p, int sms, cudaStream_t stream) 
     }
     const size_t smem = (size_t)sums_of(D, R, kWarps) * sizeof(float);
     const int blocks = sms * blocks_per_sm(NT, D);
-    cache_attention_kernel<D, NT, F32><<<blocks, kThreads, smem, stream>>>(p);
-    cudaError_t err = cudaGetLastError();
+    cudaError_t err;
+    if (p.many_rows == INT64_MAX) {
+        cache_attention_kernel<D, NT, F32><<<blocks, kThreads, smem, stream>>>(p);
+        err = cudaGetLastError();
+    } else {
+        // on SMs that the prompts leave idle, or are done with; what joins their parts waits for both
+        // (63 single tokens and a prompt of 200 as above 105 -> 86 us)
+        err = launch_follower(cache_attention_kernel<D, NT, F32>, dim3(blocks), dim3(kThreads), smem,
+                              stream, p);
+        if (err == cudaSuccess) err = launch_cache_prompt_join(p, sms, stream);
+    }
     if (err != cudaSuccess) return err;
     return launch_follower(cache_attention_join_kernel<D, NT, F32>, dim3(blocks),
                            dim3(kJoinThreads), (size_t)R * blocks * sizeof(float), stream, p);
@@ -883,7 +893,7 @@ size_t cache_attention_room(int32_t heads, int32_t group, int32_t T, int32_t max
     const size_t room = (size_t)sms * most * 2 * (d + 2) * sizeof(float);
     const size_t prompts = cache_prompt_used(heads, group, T, max_new, d, dtype)
                                ? cache_prompt_room(d, sms) : 0;
-    return room > prompts ? room : prompts;
+    return prompts + room;
 }
 
 cudaError_t launch_cache_attention(const CacheAttention& call, int dtype, int sms,
@@ -894,8 +904,11 @@ cudaError_t launch_cache_attention(const CacheAttention& call, int dtype, int sm
     const double work = (double)p.group * p.T * p.heads * ((int64_t)p.width << p.block_log2);
     if (cache_prompt_used(p.heads, p.group, p.T, p.max_new, p.d, dtype) && work >= kManyWork) {
         p.many_rows = p.N == 1 ? 1 : kManyRows;
+        p.prompt_partial = p.partial;
+        p.partial += cache_prompt_room(p.d, sms) / sizeof(float);
         const cudaError_t err = launch_cache_prompt(p, sms, stream);
-        if (err != cudaSuccess || p.N == 1) return err;
+        if (err != cudaSuccess) return err;
+        if (p.N == 1) return launch_cache_prompt_join(p, sms, stream);
         p.clears = 0;
     }
     return dtype == 0 ? launch_typed<true>(p, sms, stream) : launch_typed<false>(p, sms, stream);

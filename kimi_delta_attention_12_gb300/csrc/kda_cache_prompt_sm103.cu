@@ -220,7 +220,7 @@ __device__ __forceinline__ Item item_at(const CacheAttention& p, int64_t at, int
 // begins with, or another.
 __device__ __forceinline__ float* part_of(const CacheAttention& p, int64_t block, bool begins_with,
                                           int D) {
-    return p.partial + (block * 2 + !begins_with) * (2 * kRows) * (D + 2);
+    return p.prompt_partial + (block * 2 + !begins_with) * (2 * kRows) * (D + 2);
 }
 
 template <int N>
@@ -806,6 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_prompt_kernel(CacheAttentio
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) cache_prompt_join_kernel(CacheAttention p) {
     __shared__ float tops[kJoinRows], by[kJoinRows];
+    let_follow();
     const Stretch all = stretch_of<kJoinThreads>(p, blockIdx.x, gridDim.x);
     wait_before();
     if (all.request < 0) return;
@@ -861,10 +862,7 @@ cudaError_t launch_dim(const CacheAttention& p, int sms, cudaStream_t stream) {
         cache_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::bytes);
     if (err != cudaSuccess) return err;
     cache_prompt_kernel<D><<<sms, kThreads, Layout<D>::bytes, stream>>>(p);
-    err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-    return launch_follower(cache_prompt_join_kernel<D>, dim3(sms, 2 * kRows / kJoinRows),
-                           dim3(kJoinThreads), 0, stream, p);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -877,6 +875,11 @@ size_t cache_prompt_room(int32_t d, int sms) {
 
 cudaError_t launch_cache_prompt(const CacheAttention& p, int sms, cudaStream_t stream) {
     return p.d == 64 ? launch_dim<64>(p, sms, stream) : launch_dim<128>(p, sms, stream);
+}
+
+cudaError_t launch_cache_prompt_join(const CacheAttention& p, int sms, cudaStream_t stream) {
+    return launch_follower(p.d == 64 ? cache_prompt_join_kernel<64> : cache_prompt_join_kernel<128>,
+                           dim3(sms, 2 * kRows / kJoinRows), dim3(kJoinThreads), 0, stream, p);
 }
 
 }  // namespace kda

@@ -150,6 +150,40 @@ def test_extremes_on_the_tensor_cores(d):
         b.check(kda.kda_cache_attention(*_tensor_cores(b)[0], max_new=most, scale=scale))
 
 
+@pytest.mark.parametrize("past,new,Hq,H,d", [
+    ([900] * 30 + [0], [1] * 30 + [150], 32, 8, 128),           # singles beside a short prompt
+    ([0, 300, 5, 70, 1200], [400, 1, 7, 0, 1], 16, 2, 64),      # the prompt first
+    ([100, 200, 300], [90, 200, 130], 8, 4, 128),               # prompts alone
+    ([0] * 4 + [40], [3, 15, 2, 1, 200], 16, 1, 64),
+])
+def test_both_kernels_of_a_batch_back_to_back(past, new, Hq, H, d):
+    """The kernels of a call overlap; calls that share a workspace, eager and in a graph, do not."""
+    b = Batch(past, new, 32, Hq, H, d, torch.bfloat16, seed=sum(new))
+    c = Batch(past[::-1], new[::-1], 32, Hq, H, d, torch.bfloat16, seed=1 + sum(new))
+    (x, most), (y, _) = _tensor_cores(b), _tensor_cores(c)
+    ws = torch.full((kda.cache_attention_workspace_bytes(b.q.shape[0], most, Hq, H, d, torch.bfloat16),), 255,
+                    dtype=torch.uint8, device="cuda")
+    outs = [[torch.full_like(x[0], 7) for _ in range(2)] for _ in range(6)]
+
+    def calls(pair):
+        kda.kda_cache_attention(*x, max_new=most, workspace=ws, o=pair[0])
+        kda.kda_cache_attention(*y, max_new=most, workspace=ws, o=pair[1])
+
+    for pair in outs[:5]:
+        calls(pair)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls(outs[5])
+        calls(outs[5])
+    graph.replay()
+    graph.replay()
+    b.check(outs[0][0])
+    c.check(outs[0][1])
+    for pair in outs[1:]:
+        assert torch.equal(pair[0], outs[0][0]) and torch.equal(pair[1], outs[0][1])
+    assert kda.workspace_status(ws) == kda.KDA_OK
+
+
 def test_growing_scores_on_the_tensor_cores():
     """Scores that rise along the keys: the running maximum moves at every step."""
     b = Batch([900], [128], 64, 32, 8, 128, torch.bfloat16, seed=3)

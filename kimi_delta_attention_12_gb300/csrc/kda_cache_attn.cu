@@ -55,10 +55,11 @@ __host__ __device__ constexpr float slack_of(bool F32) { return F32 ? 0.0f : 4.0
 __host__ __device__ constexpr float raise_of(bool F32) { return 15.0f - slack_of(F32); }
 // From where on prompts go to the tensor cores: rows of the longest request, rows of all heads, and
 // those times the tokens that the table can hold.  32 heads over 8, d = 128, one request, us, this
-// kernel against that one: 128 / 256 new tokens of 1K 32 against 36 / 48 against 37; 32 / 64 of 8K
-// 44 against 41 / 66 against 49; 16 / 32 of 32K 69 against 68 / 114 against 73.
-constexpr int64_t kManyRows = 64, kManyHeadRows = 1024, kManyWork = (int64_t)1 << 23;
-constexpr int kRounds = 24;          // of a warp in a cluster
+// kernel against that one: 128 / 256 new tokens of 1K 27 against 36 / 38 against 37; 32 / 64 of 8K
+// 37 against 43 / 56 against 52; 16 / 32 of 32K 61 against 72 / 99 against 77; 16 heads over 1,
+// d = 64: 64 of 8K 26 against 35, 32 of 32K 40 against 47.
+constexpr int64_t kManyRows = 64, kManyHeadRows = 1024, kManyWork = (int64_t)1 << 24;
+constexpr int kRounds = 32;          // of a warp in a cluster
 
 // Blocks that an SM holds at once, by what a tile needs in registers.  More warps, a few registers
 // spilled, beat fewer: single tokens as above, d = 64 with 4 instead of 3 blocks 214 -> 187 us,
@@ -801,9 +802,10 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(Cach
 // clusters of 8 every other one (they lie within a group of SMs, and 16 of them did not fit at
 // once), and a warp at most kRounds times 16 tokens; beyond, the even stretches over all SMs are
 // faster although they take two launches.  8 heads of d = 128, 4 rows each, clusters against
-// stretches, us: 1 request of 1K, 8K, 32K, 128K tokens 6.3, 11.1, 28.6, 114 against 10.8, 18.5,
-// 26.6, 56.7 (8 a cluster); 4 of 8K, 32K 17.1, 61.2 against 21.1, 51.4 (4); 8 of 4K 17.2 against
-// 20.3, 9 of 1K 8.3 against 15.0 (2).  Clusters of 16 took 17.0 for 1 of 8K.
+// stretches, us: 1 request of 1K, 8K, 32K, 128K tokens 6.1, 10.4, 24.2, 106 against 11.1, 19.2,
+// 26.4, 58.8 (8 a cluster); 4 of 8K, 16K, 32K 15.2, 32.1, 58.9 against 21.5, 34.2, 53.9 (4); 8 of
+// 8K 32.0 against 33.7, 9 of 1K 8.1 against 15.9 (2).  Clusters of 16 took 17.0 for 1 of 8K, when
+// 8 took 11.4.
 int cluster_of(const CacheAttention& p, int sms, int NT) {
     const int64_t items = (int64_t)p.N * p.heads, most = (int64_t)p.width << p.block_log2;
     for (int c = 8; c > 1; c /= 2) {

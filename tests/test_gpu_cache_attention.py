@@ -106,7 +106,7 @@ def _tensor_cores(b):
     """The batch's arguments with a table that can hold so much that its prompts go to the tensor
     cores' kernel, and the most new tokens."""
     rows, H = b.q.shape[0] * b.q.shape[1], b.ks.shape[1]
-    assert rows >= 1024 and max(b.new) * b.q.shape[1] // H >= 64 and rows << 16 >= 1 << 23
+    assert rows >= 1024 and max(b.new) * b.q.shape[1] // H >= 64 and rows << 16 >= 1 << 24
     args = b.args()
     return (*args[:5], b.wide(), *args[6:]), max(b.new)
 

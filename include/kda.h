@@ -645,7 +645,8 @@ KDA_API size_t kda_block_norm_backward_workspace_bytes(int64_t rows, int32_t D, 
  *     kda_cache_attention  the new tokens' q over the cached k and v
  *
  * Tokens are packed as everywhere in this library; N requests, request i with
- * new tokens cu_seqlens[i] .. cu_seqlens[i + 1) - 1.  Tensors with a `stride`
+ * new tokens cu_seqlens[i] .. cu_seqlens[i + 1] - 1.  N, T and, for attention, T
+ * times the query heads to a key head are at most 2^31 - 2^16.  Tensors with a `stride`
  * argument are [rows, heads, d] with dense heads and rows `stride` elements apart
  * (at least heads * d, a multiple of 16 bytes): parts of one wider projection need
  * no copy.
@@ -748,8 +749,9 @@ enum {
  *  positions, slots  [T] int32, written: a row behind the last token gets position 0 and
  *             slot -1
  * A request that is not served (status not 0) takes no blocks and its rows get slot -1;
- * its row range stays.  One without new tokens needs no rows.  When the free blocks do not suffice, the requests from the first
- * that cannot be served on get none (one that needs no new block is still served).
+ * its row range stays.  One without new tokens needs no rows.  When the free blocks do
+ * not suffice, the requests from the first that cannot be served on get none (one that
+ * needs no new block is still served).
  * A value that free_blocks or block_table holds is passed on as it is; one that makes no
  * slot in 32 bits gives slot -1.
  * Errors (nothing is launched): KDA_ERR_INVALID_ARG for a missing buffer, N < 1, T < 0,

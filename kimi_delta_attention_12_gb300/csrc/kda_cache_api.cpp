@@ -19,6 +19,7 @@ using kda::supported_dim;
 constexpr size_t kHeader = 256;   // status word
 constexpr int32_t kMaxRotaryDim = 512;
 constexpr int32_t kMaxGroup = 64;
+constexpr int32_t kMostRows = 0x7fff0000;   // whole tiles of rows stay within 32 bits
 constexpr uint32_t kRotaryFlags = KDA_FLAG_ROTARY_INTERLEAVED | KDA_FLAG_ROTARY_INVERSE;
 
 int sm_count() {
@@ -123,7 +124,7 @@ int kda_rotary(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                int64_t k_out_stride, void* stream) {
     if (!good_type(dt)) return KDA_ERR_UNSUPPORTED;
     if (d < 8 || d > kMaxRotaryDim || d % 8 != 0 || rot < 16 || rot % 16 != 0 || first < 0 ||
-        first % 8 != 0 || first + rot > d) {
+        first % 8 != 0 || rot > d || first > d - rot) {
         return KDA_ERR_UNSUPPORTED;
     }
     if (T < 0 || T > ((int64_t)1 << 31) || Hq < 1 || Hk < 0 || Hq > 65535 || Hk > 65535 ||
@@ -183,7 +184,7 @@ int kda_cache_plan(const int32_t* past, const int32_t* new_tokens, int32_t N, in
                    const int32_t* n_free, int32_t* n_free_out, int32_t block, int32_t T,
                    int32_t* cu_seqlens, int32_t* context_lens, int32_t* positions, int32_t* slots,
                    int32_t* status, void* stream) {
-    if (log2_of_block(block) < 0) return KDA_ERR_UNSUPPORTED;
+    if (log2_of_block(block) < 0 || N > kMostRows || T > kMostRows) return KDA_ERR_UNSUPPORTED;
     if (N < 1 || T < 0 || table_width < 1 || free_capacity < 1 || !past || !new_tokens ||
         !block_table || !free_blocks || !n_free || !n_free_out || !cu_seqlens || !context_lens ||
         !status || (T > 0 && (!positions || !slots))) {
@@ -223,6 +224,7 @@ int kda_cache_write(const void* k, int64_t k_stride, const void* v, int64_t v_st
     const int bad = check_cache(k_cache, v_cache, k_scale, v_scale, num_blocks, block, Hkv, d, dt);
     if (bad != KDA_OK) return bad;
     if (T < 0 || (T > 0 && (!k || !v || !slots))) return KDA_ERR_INVALID_ARG;
+    if (T > kMostRows) return KDA_ERR_UNSUPPORTED;
     const int64_t width = (int64_t)Hkv * d;
     if (!good_stride(k_stride, width, dt) || !good_stride(v_stride, width, dt)) {
         return KDA_ERR_INVALID_ARG;
@@ -255,8 +257,8 @@ int kda_cache_write(const void* k, int64_t k_stride, const void* v, int64_t v_st
 
 size_t kda_cache_attention_workspace_bytes(int32_t T, int32_t max_new, int32_t Hq, int32_t Hkv,
                                            int32_t d, kda_dtype dt) {
-    if (T < 0 || max_new < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > kMaxGroup || !supported_dim(d) ||
-        !good_type(dt)) {
+    if (T < 0 || max_new < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > kMaxGroup ||
+        !supported_dim(d) || !good_type(dt)) {
         return 0;
     }
     return attention_room(T, max_new, Hq, Hkv, d, dt, sm_count());
@@ -276,7 +278,9 @@ int kda_cache_attention(const void* q, int64_t q_stride, const void* k_cache, co
         return KDA_ERR_INVALID_ARG;
     }
     const int32_t group = Hq / Hkv;
-    if (group > kMaxGroup || (int64_t)T * group > 0x7fff0000) return KDA_ERR_UNSUPPORTED;
+    if (group > kMaxGroup || (int64_t)T * group > kMostRows || N > kMostRows) {
+        return KDA_ERR_UNSUPPORTED;
+    }
     if (!block_table || !context_lens || (T > 0 && (!q || !o))) return KDA_ERR_INVALID_ARG;
     const int64_t width = (int64_t)Hq * d;
     if (!good_stride(q_stride, width, dt)) return KDA_ERR_INVALID_ARG;

@@ -72,7 +72,7 @@ __host__ __device__ constexpr int blocks_per_sm(int NT, int D) {
 struct Item {
     int request, head, tile;
     int64_t begin;            // where its units begin among all
-    int units, tiles;         // of the item; of its request and head
+    int units;
     int tokens, fresh;        // cached, and new ones among them
     int64_t row0;             // of the packed q
 };
@@ -188,7 +188,6 @@ __device__ __forceinline__ Item item_at(const CacheAttention& p, int R, int64_t 
     t.tile = k & 1 ? s.tiles - 1 - (k >> 1) : k >> 1;
     t.begin = first + n * s.units;
     t.units = s.units;
-    t.tiles = s.tiles;
     t.tokens = s.tokens;
     t.fresh = s.fresh;
     t.row0 = s.row0;
@@ -667,7 +666,8 @@ __global__ void __launch_bounds__(32 * cluster_warps(NT), 1) cache_attention_clu
     CacheAttention p) {
     namespace cg = cooperative_groups;
     constexpr int R = 8 * NT, W = cluster_warps(NT), kAll = 32 * W;
-    extern __shared__ __align__(16) float sums[];          // the warps', then this block's: [R][D], m, l [R]
+    // the warps' sums, then this block's: [R][D], m, l [R]
+    extern __shared__ __align__(16) float sums[];
     float* block_o = sums + sums_of(D, R, W);
     float* block_m = block_o + R * D;
     float* block_l = block_m + R;
@@ -703,7 +703,9 @@ __global__ void __launch_bounds__(32 * cluster_warps(NT), 1) cache_attention_clu
         for (int i = rank * kAll + threadIdx.x; i < valid * D / 4; i += blocks * kAll) {
             const int n = 4 * i / D;
             float top = kNone, all = 0.0f;
-            for (int k = 0; k < blocks; ++k) top = fmaxf(top, cluster.map_shared_rank(block_m, k)[n]);
+            for (int k = 0; k < blocks; ++k) {
+                top = fmaxf(top, cluster.map_shared_rank(block_m, k)[n]);
+            }
             const float ref = top == kNone ? 0.0f : top;
             float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
@@ -849,10 +851,10 @@ cudaError_t launch_tiles(const CacheAttention& p, int sms, cudaStream_t stream) 
         cache_attention_kernel<D, NT, F32><<<blocks, kThreads, smem, stream>>>(p);
         err = cudaGetLastError();
     } else {
-        // on SMs that the prompts leave idle, or are done with; what joins their parts waits for both
-        // (63 single tokens and a prompt of 200 as above 105 -> 86 us)
-        err = launch_follower(cache_attention_kernel<D, NT, F32>, dim3(blocks), dim3(kThreads), smem,
-                              stream, p);
+        // on SMs that the prompts leave idle or are done with; what joins their parts waits for
+        // both (63 single tokens and a prompt of 200 as above 105 -> 86 us)
+        err = launch_follower(cache_attention_kernel<D, NT, F32>, dim3(blocks), dim3(kThreads),
+                              smem, stream, p);
         if (err == cudaSuccess) err = launch_cache_prompt_join(p, sms, stream);
     }
     if (err != cudaSuccess) return err;

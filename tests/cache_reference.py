@@ -190,8 +190,8 @@ def attention_bound(o, mass, size, least, d, longest, bf16):
     """How far o may be off: a score's products carry 2^-22 of each (q in two halves of 11 bits)
     and d / 16 sums of two products rounded to 2^-22 of the whole; the weights' 2^-20 (exponent,
     its argument up to 16); the logarithm of a value scale in the argument, rounded itself, in the
-    sum and in the reference, 3 ln 2 2^-24 < 2^-22 of its size; the running sums 2^-24 for each 16 keys; for bf16 the weights' 11 bits and the
-    result's rounding, 2^-8.  And an fp16 weight is off by up to 2^-25 however small it is, where
+    sum and in the reference, 3 ln 2 2^-24 < 2^-22 of its size; the running sums 2^-24 for each
+    16 keys; for bf16 the weights' 11 bits and the result's rounding, 2^-8.  And an fp16 weight is off by up to 2^-25 however small it is, where
     the largest weight times its scale is 2^7 at least for bf16, 2^15 for fp32 (whose second half
     is an fp16 number too): 2^-32 or 2^-40 of `least`."""
     ds, log_scale = size[..., :1] * (1 + d / 8) * 2.0 ** -22, size[..., 1:]

@@ -38,6 +38,7 @@ def _rotary(L, **over):
     (dict(dt=2), UNS), (dict(d=60), UNS), (dict(d=520), UNS), (dict(d=0), UNS),
     (dict(rot=8), UNS), (dict(rot=24), UNS), (dict(rot=64), UNS), (dict(first=4), UNS),
     (dict(first=-8), UNS), (dict(first=40), UNS),
+    (dict(first=0x7ffffff8, rot=16), UNS), (dict(first=16, rot=0x7ffffff0), UNS),
     (dict(T=-1), INV), (dict(Hq=0), INV), (dict(Hk=-1), INV), (dict(flags=1), INV),
     (dict(flags=128), INV), (dict(mag=float("nan")), INV), (dict(mag=float("inf")), INV),
     (dict(f=None), INV), (dict(pos=None), INV), (dict(q=None), INV), (dict(qo=None), INV),
@@ -76,6 +77,7 @@ def _plan(L, **over):
 @pytest.mark.parametrize("over,expect", [
     (dict(block=8), UNS), (dict(block=48), UNS), (dict(block=256), UNS),
     (dict(N=0), INV), (dict(T=-1), INV), (dict(W=0), INV), (dict(F=0), INV),
+    (dict(N=0x7fff0001), UNS), (dict(T=0x7fff0001), UNS),
     (dict(past=None), INV), (dict(new=None), INV), (dict(table=None), INV), (dict(free=None), INV),
     (dict(nf=None), INV), (dict(nfo=None), INV), (dict(cu=None), INV), (dict(ctx=None), INV),
     (dict(pos=None), INV), (dict(slots=None), INV), (dict(st=None), INV),
@@ -101,6 +103,7 @@ def _write(L, **over):
 @pytest.mark.parametrize("over,expect", [
     (dict(dt=3), UNS), (dict(d=48), UNS), (dict(d=256), UNS), (dict(block=24), UNS),
     (dict(H=0), INV), (dict(nb=0), INV), (dict(T=-1), INV), (dict(nb=1 << 27), INV),
+    (dict(T=0x7fff0001), UNS),
     (dict(k=None), INV), (dict(v=None), INV), (dict(slots=None), INV), (dict(kc=None), INV),
     (dict(vc=None), INV), (dict(ksc=None), INV), (dict(vsc=None), INV),
     (dict(ks=124), INV), (dict(vs=130), INV),
@@ -131,7 +134,8 @@ def _attention(L, **over):
 
 @pytest.mark.parametrize("over,expect", [
     (dict(dt=2), UNS), (dict(d=96), UNS), (dict(block=8), UNS),
-    (dict(Hq=130, qs=130 * 64), UNS),
+    (dict(Hq=130, qs=130 * 64), UNS), (dict(N=0x7fff0001, T=0x7fff0001), UNS),
+    (dict(N=0x7fff0001, cu=BASE + 9 * M), UNS),
     (dict(H=0), INV), (dict(Hq=5, qs=320), INV), (dict(Hq=1, qs=64), INV), (dict(N=0), INV),
     (dict(T=-1), INV), (dict(T=5), INV), (dict(most=-1), INV), (dict(W=0), INV),
     (dict(nb=0), INV), (dict(nb=1 << 28), INV), (dict(scale=float("nan")), INV),

@@ -123,8 +123,8 @@ def _tensor_cores(b):
 def test_prompts_on_the_tensor_cores(past, new, block, Hq, H, d):
     b = Batch(past, new, block, Hq, H, d, torch.bfloat16, seed=sum(new))
     args, most = _tensor_cores(b)
-    ws = torch.full((kda.cache_attention_workspace_bytes(b.q.shape[0], max(new), Hq, H, d, torch.bfloat16),), 255,
-                    dtype=torch.uint8, device="cuda")
+    room = kda.cache_attention_workspace_bytes(b.q.shape[0], max(new), Hq, H, d, torch.bfloat16)
+    ws = torch.full((room,), 255, dtype=torch.uint8, device="cuda")
     got = kda.kda_cache_attention(*args, max_new=most, workspace=ws)
     b.check(got)
     assert kda.workspace_status(ws) == kda.KDA_OK
@@ -161,8 +161,8 @@ def test_both_kernels_of_a_batch_back_to_back(past, new, Hq, H, d):
     b = Batch(past, new, 32, Hq, H, d, torch.bfloat16, seed=sum(new))
     c = Batch(past[::-1], new[::-1], 32, Hq, H, d, torch.bfloat16, seed=1 + sum(new))
     (x, most), (y, _) = _tensor_cores(b), _tensor_cores(c)
-    ws = torch.full((kda.cache_attention_workspace_bytes(b.q.shape[0], most, Hq, H, d, torch.bfloat16),), 255,
-                    dtype=torch.uint8, device="cuda")
+    room = kda.cache_attention_workspace_bytes(b.q.shape[0], most, Hq, H, d, torch.bfloat16)
+    ws = torch.full((room,), 255, dtype=torch.uint8, device="cuda")
     outs = [[torch.full_like(x[0], 7) for _ in range(2)] for _ in range(6)]
 
     def calls(pair):

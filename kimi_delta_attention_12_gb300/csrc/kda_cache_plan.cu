@@ -10,6 +10,7 @@
 #include "../../include/kda.h"
 #include "kda_cache.h"
 #include "kda_follow.cuh"
+#include "kda_seqlens.cuh"
 
 namespace kda {
 namespace {
@@ -69,15 +70,7 @@ __device__ __forceinline__ void plan_row(const CachePlan& p, const int32_t* star
     int32_t position = 0;
     int64_t slot = -1;
     if (t < starts[p.N]) {
-        int lo = 0, hi = p.N;               // the last request that starts at or before t
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (starts[mid] <= t) {
-                lo = mid;
-            } else {
-                hi = mid;
-            }
-        }
+        const int lo = last_start(starts, p.N, t);
         const int64_t at = (int64_t)p.past[lo] + t - starts[lo];
         position = (int32_t)(at < 0x7fffffff ? at : 0x7fffffff);
         if (p.status[lo] == KDA_PLAN_OK) {

@@ -43,4 +43,21 @@ __device__ __forceinline__ int64_t clamped_len(const int32_t* cu_seqlens, int n,
     return eos - bos;
 }
 
+// The last of n sequences that starts at or before token t (0 where none does), by bisection of
+// their starts, which do not decrease.  The middle is taken from the distance: lo + hi passes 2^31
+// from 1.43 thousand million sequences on.
+template <typename Starts>
+__device__ __forceinline__ int last_start(const Starts& starts, int n, int64_t t) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = lo + ((hi - lo) >> 1);
+        if (starts[mid] <= t) {
+            lo = mid;
+        } else {
+            hi = mid;
+        }
+    }
+    return lo;
+}
+
 }  // namespace kda

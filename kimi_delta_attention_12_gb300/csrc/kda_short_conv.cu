@@ -145,16 +145,7 @@ __device__ __forceinline__ int seq_of(const ShortConvParams& p, int64_t t) {
     if (!p.cu_seqlens) {
         return (int)(t / (p.total_T / p.N));
     }
-    int lo = 0, hi = p.N - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.cu_seqlens[mid] <= t) {
-            lo = mid;
-        } else {
-            hi = mid - 1;
-        }
-    }
-    return lo;
+    return last_start(p.cu_seqlens, p.N, t);
 }
 
 // One token of one channel vector: y = sum_j wt[j] x_{t-R+j} (x_t the raw row

@@ -800,7 +800,8 @@ KDA_API int kda_cache_write(const void* k, int64_t k_stride, const void* v, int6
  *
  *  q          [T, Hq, d] dt with q_stride; Hq a multiple of Hkv, at most 64 of them to
  *             one; head h reads the keys and values of head h / (Hq / Hkv);  d 32, 64, 128
- *  k_cache, v_cache, k_scale, v_scale   the cache; scales positive, 2^-60 .. 2^60
+ *  k_cache, v_cache, k_scale, v_scale   the cache; scales positive, 2^-60 .. 2^60; a row's
+ *             largest |q| times |scale| times a key scale below 2^127
  *  block_table  [N, table_width] int32;  context_lens [N] int32
  *  cu_seqlens  [N + 1] int32, or NULL: one new token for each request (T = N)
  *  max_new    the most new tokens of a request, or more; it chooses the kernels, so one
@@ -815,11 +816,14 @@ KDA_API int kda_cache_write(const void* k, int64_t k_stride, const void* v, int6
  * table and to T.  What the cache holds behind a request's last token is not read.  A
  * NaN among the values of a request's new tokens may reach the rows of its other new
  * tokens in the same call.
- * fp32 q and o: products to 22 bits and more, sums in fp32.  bf16: the weights
- * are rounded to 11 bits before they meet the values (e4m3 values are exact), sums in
- * fp32, one rounding to bf16.  Weights below 2^-32 of a row's heaviest (by weight times
- * value scale; fp32: 2^-40) count in the sum of weights alone.  The same bits on every
- * call on one kind of device.  T = 0 launches nothing and leaves the workspace as it is.
+ * fp32 q and o: products to 22 bits and more, but that a channel of q is off by up to
+ * 2^-39 of its row's largest however small it is; sums in fp32.  bf16: products are exact
+ * for the channels of q down to 2^-31 of their row's largest; the weights are rounded to
+ * 11 bits before they meet the values (e4m3 values are exact), sums in fp32, one rounding
+ * to bf16.  Weights below 2^-32 of a row's heaviest (by weight times value scale; fp32:
+ * 2^-40) count in the sum of weights alone, below 2^-118 not at all.  The same bits on
+ * every call on one kind of device.  T = 0 launches nothing and leaves the workspace as
+ * it is.
  * Errors (nothing is launched): as kda_cache_write, and KDA_ERR_WORKSPACE.
  */
 KDA_API int kda_cache_attention(const void* q, int64_t q_stride, const void* k_cache,

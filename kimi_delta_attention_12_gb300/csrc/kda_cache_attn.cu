@@ -11,10 +11,12 @@
 // so that eight query rows fill an instruction.  The channels of a product may come in any
 // order as long as both sides agree, and the order taken makes every lane's part of a K row 16
 // neighbouring bytes: keys and values go from HBM into the registers they are multiplied
-// from, no shared memory between.  e4m3 numbers become fp16 exactly; q is scaled to [1, 2) by a power
-// of two per row (its exponent range is wider than fp16's), for fp32 split into two fp16
-// halves, and so are the weights P.  P^T needs the 8 x 8 transposes of S^T's tiles, one
-// instruction each (movmatrix).
+// from, no shared memory between.  e4m3 numbers become fp16 exactly; q is scaled by a power of two
+// per row (its exponent range is wider than fp16's), for fp32 split into two fp16 halves, and so are
+// the weights P.  A row's largest channel comes to [2^14, 2^15), the top of fp16's range: bf16 channels
+// are exact down to 2^-31 of it, fp32 ones hold 22 bits down to 2^-17 of it and are off by 2^-39 of it
+// below (at [1, 2) a channel 2^-12 of the largest had 13 bits); products with e4m3's 448 at most stay
+// far inside fp32.  P^T needs the 8 x 8 transposes of S^T's tiles, one instruction each (movmatrix).
 //
 // The value scale of a block goes into the exponent: with p' = 2^(s - m + 15) v_scale, m the
 // running maximum of s + log2 v_scale, P' is at most 2^15 whatever the scales, and the sum of
@@ -348,7 +350,7 @@ __device__ __forceinline__ void attend(const CacheAttention& p, const Item& it, 
     look_up(0);
     load(x, 0);
     load(y, 1);
-    // ---- q of this lane's column, scaled to [1, 2) and in fp16
+    // ---- q of this lane's column, its largest channel scaled to [2^14, 2^15), in fp16
     uint32_t q[Q][NT][kSteps][2];
     float factor[NT][2];                 // of a score, for the columns 2 c and 2 c + 1
     int limit[NT][2];
@@ -382,8 +384,8 @@ __device__ __forceinline__ void attend(const CacheAttention& p, const Item& it, 
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         int e = __float_as_int(top) >> 23;
-        e = e < 1 ? 1 : (e > 253 ? 253 : e);
-        const float down = __int_as_float((254 - e) << 23), up = __int_as_float(e << 23);
+        e = e < 15 ? 15 : (e > 254 ? 254 : e);
+        const float down = __int_as_float((268 - e) << 23), up = __int_as_float((e - 14) << 23);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
 #pragma unroll

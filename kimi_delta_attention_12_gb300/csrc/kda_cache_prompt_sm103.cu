@@ -18,8 +18,8 @@
 // them as fp16 (exact) in the operands' layout, warps 12 and 13 issue the products of a tile
 // each, warps 14 and 15 only give their registers away.
 //
-// fp16, not bf16: e4m3 numbers and, scaled to [1, 2) by a power of two per row, bf16 queries are
-// fp16 numbers, and P keeps 11 bits.  Scales of key blocks go into the exponent's factor, those
+// fp16, not bf16: e4m3 numbers are fp16 numbers, and so are the channels of a bf16 query, down to 2^-31
+// of its largest, which a power of two per row brings to [2^14, 2^15); and P keeps 11 bits.  Scales of key blocks go into the exponent's factor, those
 // of value blocks into its offset, as in the kernel for few rows: p' = 2^(s - m + 7) v_scale with
 // m at most 8 below the running maximum of s + log2 v_scale.  That slack is what spares most tiles
 // the rescaling of O: it is done where the maximum has grown by more, and P stays below 2^15 (a
@@ -678,7 +678,8 @@ __device__ __forceinline__ void soften(const CacheAttention& p, const Item& job,
     }
 }
 
-// This thread's row of q, scaled to [1, 2) and in fp16, into its tile; the factor of its scores.
+// This thread's row of q, its largest channel scaled to [2^14, 2^15), in fp16, into its tile; the
+// factor of its scores.
 template <int D>
 __device__ __forceinline__ float stage_query(const CacheAttention& p, const Item& job, uint8_t* sm) {
     const int row = threadIdx.x & 127, t = threadIdx.x >> 7, n = kRows * t + row;
@@ -700,9 +701,9 @@ __device__ __forceinline__ float stage_query(const CacheAttention& p, const Item
         }
     }
     int e = __float_as_int(top) >> 23;
-    e = e < 1 ? 1 : (e > 253 ? 253 : e);
+    e = e < 15 ? 15 : (e > 254 ? 254 : e);
     // a negative scale turns q around, so that the largest score is the largest product
-    const float down = copysignf(__int_as_float((254 - e) << 23), p.scale);
+    const float down = copysignf(__int_as_float((268 - e) << 23), p.scale);
     uint8_t* tile = sm + Layout<D>::q + t * Layout<D>::tile;
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) {
@@ -717,7 +718,7 @@ __device__ __forceinline__ float stage_query(const CacheAttention& p, const Item
                                   (((i & 7) ^ (row & 7)) << 4)) =
             make_uint4(h[0], h[1], h[2], h[3]);
     }
-    return __int_as_float(e << 23) * (fabsf(p.scale) * 1.44269504088896340736f);
+    return __int_as_float((e - 14) << 23) * (fabsf(p.scale) * 1.44269504088896340736f);
 }
 
 __device__ __forceinline__ void set_up(Bars* b, int tiles) {

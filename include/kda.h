@@ -815,7 +815,7 @@ KDA_API int kda_cache_write(const void* k, int64_t k_stride, const void* v, int6
  * count as tokens that are not there; context_lens and cu_seqlens are clamped to the
  * table and to T.  What the cache holds behind a request's last token is not read.  A
  * NaN among the values of a request's new tokens may reach the rows of its other new
- * tokens in the same call.
+ * tokens in the same call, but for those that see no key.
  * fp32 q and o: products to 22 bits and more, but that a channel of q is off by up to
  * 2^-39 of its row's largest however small it is; sums in fp32.  bf16: products are exact
  * for the channels of q down to 2^-31 of their row's largest; the weights are rounded to

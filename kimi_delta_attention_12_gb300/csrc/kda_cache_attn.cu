@@ -603,15 +603,19 @@ __device__ __forceinline__ int64_t place_of(const CacheAttention& p, const Item&
     return ((it.row0 + j) * (p.heads * p.group) + it.head * p.group + flat - j * p.group) * D;
 }
 
-// Four neighbouring channels of the result.
+// Four neighbouring channels of the result: the sums over `weight`, 0 where nothing was seen (whose
+// sums are weights of 0 times values that may be NaN).
 template <bool F32>
-__device__ __forceinline__ void store4(void* o, int64_t to, const float4& y, float by) {
+__device__ __forceinline__ void store4(void* o, int64_t to, const float4& sums, float weight) {
+    const bool none = weight == 0.0f;
+    const float by = none ? 0.0f : 1.0f / weight;
+    const float4 y = make_float4(none ? 0.0f : sums.x * by, none ? 0.0f : sums.y * by,
+                                 none ? 0.0f : sums.z * by, none ? 0.0f : sums.w * by);
     if (F32) {
-        *reinterpret_cast<float4*>(static_cast<float*>(o) + to) =
-            make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
+        *reinterpret_cast<float4*>(static_cast<float*>(o) + to) = y;
     } else {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x * by, y.y * by);
-        const __nv_bfloat162 hi = __floats2bfloat162_rn(y.z * by, y.w * by);
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(y.z, y.w);
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o) + to) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
                        *reinterpret_cast<const uint32_t*>(&hi));
@@ -642,8 +646,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT, D)) cache_attentio
             float weight, top;
             const float4 y = meet<D, R, kWarps>(sums, n, d, weight, top);
             if (whole) {
-                store4<F32>(p.o, place_of(p, it, R, n, D) + d, y,
-                            weight == 0.0f ? 0.0f : 1.0f / weight);
+                store4<F32>(p.o, place_of(p, it, R, n, D) + d, y, weight);
             } else {
                 *reinterpret_cast<float4*>(part + i) = y;
                 if (d == 0) {
@@ -721,8 +724,7 @@ __global__ void __launch_bounds__(32 * cluster_warps(NT), 1) cache_attention_clu
                 y.z = fmaf(f, x.z, y.z);
                 y.w = fmaf(f, x.w, y.w);
             }
-            store4<F32>(p.o, place_of(p, it, R, n, D) + 4 * i - n * D, y,
-                        all == 0.0f ? 0.0f : 1.0f / all);
+            store4<F32>(p.o, place_of(p, it, R, n, D) + 4 * i - n * D, y, all);
         }
         cluster.sync();                      // the others may still read this block's sums
     }
@@ -797,8 +799,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(Cach
             }
         }
         if (i >= outs) return;
-        const float all = total[n];
-        store4<F32>(p.o, place_of(p, it, R, n, D) + d, y, all == 0.0f ? 0.0f : 1.0f / all);
+        store4<F32>(p.o, place_of(p, it, R, n, D) + d, y, total[n]);
     }
 }
 

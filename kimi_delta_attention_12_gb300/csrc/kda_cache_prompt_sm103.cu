@@ -654,7 +654,8 @@ __device__ __forceinline__ void soften(const CacheAttention& p, const Item& job,
         }
         return;
     }
-    const float by = row.l == 0.0f ? 0.0f : 1.0f / row.l;
+    const bool none = row.l == 0.0f;         // nothing seen: O is 0 times values that may be NaN
+    const float by = none ? 0.0f : 1.0f / row.l;
     const int j = flat / p.group;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) +
                          ((job.token0 + j) * (p.heads * p.group) + job.head * p.group + flat -
@@ -668,7 +669,7 @@ __device__ __forceinline__ void soften(const CacheAttention& p, const Item& job,
         for (int i = 0; i < 8; ++i) {
             const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[2 * i]) * by,
                                                            __uint_as_float(r[2 * i + 1]) * by);
-            w[i] = *reinterpret_cast<const uint32_t*>(&v);
+            w[i] = none ? 0u : *reinterpret_cast<const uint32_t*>(&v);
         }
         if (mine) {
             uint4* to = reinterpret_cast<uint4*>(out + c);
@@ -877,9 +878,10 @@ __global__ void __launch_bounds__(kJoinThreads) cache_prompt_join_kernel(CacheAt
                             j * p.group) * D + c;
         const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x * by[r], y.y * by[r]);
         const __nv_bfloat162 hi = __floats2bfloat162_rn(y.z * by[r], y.w * by[r]);
+        const bool none = by[r] == 0.0f;
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + to) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                       *reinterpret_cast<const uint32_t*>(&hi));
+            make_uint2(none ? 0u : *reinterpret_cast<const uint32_t*>(&lo),
+                       none ? 0u : *reinterpret_cast<const uint32_t*>(&hi));
     }
 }
 

@@ -45,10 +45,13 @@ class SoftmaxLayer:
 
     def step(self, h, new, max_new):
         """h [rows, width] of the requests' new tokens, new [requests] how many each has (-1: the
-        request ends).  Returns y [rows, width] and the plan."""
+        request ends).  Returns y [rows, width] and the plan; the rows of a request whose status in
+        it is not 0 are zero and to be given again."""
         plan = kda.kda_cache_plan(self.past, new, self.table, self.free, self.n_free, self.block,
                                   h.shape[0], n_free_out=self.n_free)
-        self.past.copy_(plan["context_lens"])
+        # a request that is not served this time (no free block, say) waits where it is
+        served = plan["status"] == kda.KDA_PLAN_OK
+        self.past.copy_(torch.where(served, plan["context_lens"], self.past))
         qkv = (h @ self.w_in).view(h.shape[0], self.heads + 2 * self.kv_heads, self.dim)
         q, k = qkv[:, :self.heads], qkv[:, self.heads:self.heads + self.kv_heads]
         v = qkv[:, self.heads + self.kv_heads:]

@@ -1178,7 +1178,8 @@ def kda_cache_plan(past: torch.Tensor, new_tokens: torch.Tensor, block_table: to
     int32 (new -1 ends a request), block_table [N, W] and free_blocks [F] int32 updated in
     place, n_free [1] int32 the free blocks in it, `rows` the rows of the step's packed tensors.
     Returns a dict of int32 tensors: cu_seqlens [N + 1], context_lens, status [N], positions,
-    slots [rows], n_free [1] (n_free_out when given, which may be n_free itself)."""
+    slots [rows], n_free [1] (n_free_out when given, which may be n_free itself).  The next step's
+    past is context_lens where status is 0; a request with another status keeps its past."""
     dev = _one_device(past, new_tokens, block_table, free_blocks, n_free, n_free_out)
     N = past.shape[0] if past.dim() == 1 else 0
     i32 = torch.int32

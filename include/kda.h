@@ -750,9 +750,9 @@ enum {
  *             slot -1
  * A request that is not served (status not 0) takes no blocks and its rows get slot -1;
  * its row range stays, and its blocks remain its own: its past tokens of the next step are
- * those of this one, not its context_lens, which is 0 so that attention leaves it out.  One without new tokens needs no rows.  When the free blocks do
- * not suffice, the requests from the first that cannot be served on get none (one that
- * needs no new block is still served).
+ * those of this one, not its context_lens, which is 0 so that attention leaves it out.  One
+ * without new tokens needs no rows.  When the free blocks do not suffice, the requests from
+ * the first that cannot be served on get none (one that needs no new block is still served).
  * A value that free_blocks or block_table holds is passed on as it is; one that makes no
  * slot in 32 bits gives slot -1.
  * Errors (nothing is launched): KDA_ERR_INVALID_ARG for a missing buffer, N < 1, T < 0,

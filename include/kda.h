@@ -669,8 +669,10 @@ typedef enum {
     KDA_ROTARY_LINEAR = 1,  /* f_j / factor */
     KDA_ROTARY_BY_PARTS = 2 /* f_j w_j + (1 - w_j) f_j / factor, where w_j goes linearly from 0
                                to 1 as the turns that pair j makes in original_length tokens go
-                               from `slow` to `fast`; magnitude 0.1 ln(factor) + 1 (the
-                               published YaRN method) */
+                               from `slow` to `fast`; magnitude 0.1 ln(factor) + 1, and 1 for
+                               factors below 1.  The ramp is that of the YaRN paper, linear in
+                               the turns; programs whose ramp is linear in j between rounded
+                               bounds have other frequencies, to be given as inv_freq */
 } kda_rotary_scaling;
 
 /*

@@ -113,7 +113,8 @@ int kda_rotary_frequencies(int32_t rot, double base, kda_rotary_scaling scaling,
         }
         inv_freq[j] = (float)f;
     }
-    *magnitude = parts ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
+    // (a factor below 1 lengthens nothing, and far below it the logarithm would turn pairs around)
+    *magnitude = parts && factor > 1.0 ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
     return KDA_OK;
 }
 

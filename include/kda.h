@@ -684,7 +684,8 @@ typedef enum {
  *             KDA_ROTARY_PLAIN)
  *  original_length, fast, slow   KDA_ROTARY_BY_PARTS only: > 0, fast > slow > 0
  *  inv_freq   [rot / 2] fp32, written;  magnitude: one fp32, written
- * KDA_ERR_INVALID_ARG for anything else.
+ * KDA_ERR_INVALID_ARG for anything else, and where a frequency comes to 2^20 or more, which
+ * kda_rotary does not take (a base or a factor far below 1); nothing is written then.
  */
 KDA_API int kda_rotary_frequencies(int32_t rot, double base, kda_rotary_scaling scaling,
                                    double factor, double original_length, double fast,

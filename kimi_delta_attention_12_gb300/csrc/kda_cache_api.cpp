@@ -18,6 +18,7 @@ using kda::supported_dim;
 
 constexpr size_t kHeader = 256;   // status word
 constexpr int32_t kMaxRotaryDim = 512;
+constexpr float kMostFrequency = 0x1p20f;   // that kda_rotary is made for
 constexpr int32_t kMaxGroup = 64;
 constexpr int32_t kMostRows = 0x7fff0000;   // whole tiles of rows stay within 32 bits
 constexpr uint32_t kRotaryFlags = KDA_FLAG_ROTARY_INTERLEAVED | KDA_FLAG_ROTARY_INVERSE;
@@ -101,7 +102,7 @@ int kda_rotary_frequencies(int32_t rot, double base, kda_rotary_scaling scaling,
         return KDA_ERR_INVALID_ARG;
     }
     constexpr double kTwoPi = 6.283185307179586476925286766559;
-    for (int32_t j = 0; j < rot / 2; ++j) {
+    auto frequency = [&](int32_t j) {
         double f = pow(base, -2.0 * j / rot);
         if (linear) {
             f /= factor;
@@ -111,8 +112,12 @@ int kda_rotary_frequencies(int32_t rot, double base, kda_rotary_scaling scaling,
             w = w < 0.0 ? 0.0 : (w > 1.0 ? 1.0 : w);
             f = f * w + f / factor * (1.0 - w);
         }
-        inv_freq[j] = (float)f;
+        return f;
+    };
+    for (int32_t j = 0; j < rot / 2; ++j) {
+        if (!((float)frequency(j) < kMostFrequency)) return KDA_ERR_INVALID_ARG;
     }
+    for (int32_t j = 0; j < rot / 2; ++j) inv_freq[j] = (float)frequency(j);
     // (a factor below 1 lengthens nothing, and far below it the logarithm would turn pairs around)
     *magnitude = parts && factor > 1.0 ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
     return KDA_OK;

@@ -155,11 +155,7 @@ __global__ void __launch_bounds__(kThreads, 6) rotary_kernel(Rotary p, int rows_
             in_row -= step.units;
             ++head;
         }
-        if (head >= heads) {
-            head -= heads;
-            ++dt;
-        }
-        if (head >= heads) {                 // one head: the rest and the carry are a token each
+        if (head >= heads) {                 // (below 2 heads: step.heads is below heads)
             head -= heads;
             ++dt;
         }

@@ -1061,7 +1061,7 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: Optional[str] =
                                       float(slow), f.data_ptr() or None, ctypes.addressof(m))
     if st != KDA_OK:
         raise KDAError(st, "kda_rotary_frequencies")
-    return f.to(device or "cuda"), m.value
+    return f.to("cuda" if device is None else device), m.value
 
 
 def _row_stride(t: torch.Tensor, name: str, dev: int) -> int:

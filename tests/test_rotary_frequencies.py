@@ -3,6 +3,7 @@ import ctypes
 import math
 
 import pytest
+import torch
 
 import kimi_delta_attention_12_gb300 as kda
 
@@ -42,3 +43,13 @@ def test_frequencies_that_the_rotary_call_does_not_take_are_refused(base, scalin
         assert st == kda.KDA_OK and max(f) < 2.0 ** 20 and m.value == 1.0
     else:
         assert st == kda.KDA_ERR_INVALID_ARG and list(f) == [7.0] * 32 and m.value == 7.0
+
+
+@pytest.mark.parametrize("device,to", [(None, "cuda"), (0, 0), (1, 1), ("cpu", "cpu"),
+                                       (torch.device("cpu"), torch.device("cpu"))])
+def test_frequencies_go_to_the_device_that_is_named(monkeypatch, device, to):
+    """Device 0 is device 0, whichever is the current one."""
+    seen = []
+    monkeypatch.setattr(torch.Tensor, "to", lambda self, where: seen.append(where) or self)
+    kda.rotary_frequencies(64, device=device)
+    assert seen == [to]

@@ -259,7 +259,7 @@ def prefill_workspace_bytes(N: int, total_T: int, H: int, d_k: int, d_v: int,
 def alloc_workspace(N: int, total_T: int, H: int, d_k: int, d_v: int, dtype: torch.dtype,
                     device=None) -> torch.Tensor:
     nbytes = prefill_workspace_bytes(N, total_T, H, d_k, d_v, dtype)
-    return torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(nbytes, dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def kda_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, z: torch.Tensor,

@@ -6,7 +6,8 @@
 // because what is taken depends on how much all ended requests have returned; the rows, each of
 // which finds its request by bisection of the row starts, are done by the same block up to 4,096
 // of them, by many blocks in a second launch beyond.  256 requests of one token 5.4 us (two launches
-// 8.4), 16 prompts of 109,824 tokens 13 us.
+// 8.4), 16 prompts of 109,824 tokens 13 us: the second launch, and one warp to each request's blocks,
+// 32 of them at a time, each trip behind the one before (1,001 blocks of the longest prompt: 32 trips).
 #include "../../include/kda.h"
 #include "kda_cache.h"
 #include "kda_follow.cuh"

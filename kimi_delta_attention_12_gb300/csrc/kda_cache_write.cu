@@ -24,7 +24,7 @@ constexpr int kMostTile = 64;
 constexpr int kShort = 256;      // vectors of a run that one warp takes alone
 constexpr int kBlocks = 4096;    // of threads, that a call aims at
 constexpr int kFewRows = 4096;
-constexpr int kWave = 640;       // blocks at once, about
+constexpr int kWave = 640;       // blocks at once, about: four (bf16) or three for each of GB300's 152 SMs
 
 // Rows of the run that begins at row t (slot s), at most `most` (what its block has left).
 __device__ __forceinline__ int run_length(const int32_t* slots, int T, int t, int s, int most,

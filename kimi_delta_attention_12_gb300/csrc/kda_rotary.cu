@@ -26,7 +26,8 @@ namespace {
 constexpr int kThreads = 256;
 // Vectors (or pairs of them) of a block.
 constexpr int kLeastUnits = 512, kMostUnits = 4096;
-constexpr int kBlocks = 1216;        // eight for each of 152 SMs
+constexpr int kBlocks = 1216;        // that a large call aims at: eight for each of GB300's 152 SMs, which
+                                     // hold six at once
 
 // f / (2 pi) as a 64-bit fraction of a turn, whole turns dropped.
 __device__ __forceinline__ uint64_t turns_of(float f) {

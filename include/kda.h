@@ -783,6 +783,7 @@ KDA_API int kda_cache_plan(const int32_t* past, const int32_t* new_tokens, int32
  * for powers of two, but for values that fall below e4m3's 2^-6).  Places behind a run
  * are left as they are.  Rounding is to the nearest, ties to even.  Infinities and NaN
  * do not count for the scale; an infinity becomes the largest number, a NaN stays one.
+ * (Values beyond 448 * 2^60 take a scale that kda_cache_attention is not made for.)
  * Rows whose slot is negative or behind the pool are left out.  Two runs in one block,
  * or a slot that is given twice, leave that block's content and scale unspecified, and
  * no other's.

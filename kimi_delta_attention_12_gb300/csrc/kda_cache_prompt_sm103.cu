@@ -18,13 +18,13 @@
 // them as fp16 (exact) in the operands' layout, warps 12 and 13 issue the products of a tile
 // each, warps 14 and 15 only give their registers away.
 //
-// fp16, not bf16: e4m3 numbers are fp16 numbers, and so are the channels of a bf16 query, down to 2^-31
-// of its largest, which a power of two per row brings to [2^14, 2^15); and P keeps 11 bits.  Scales of key blocks go into the exponent's factor, those
-// of value blocks into its offset, as in the kernel for few rows: p' = 2^(s - m + 7) v_scale with
-// m at most 8 below the running maximum of s + log2 v_scale.  That slack is what spares most tiles
-// the rescaling of O: it is done where the maximum has grown by more, and P stays below 2^15 (a
-// slack of 4 took 850 us where this one takes 836).  What is 2^-21 of the heaviest or more keeps all
-// its bits.
+// fp16, not bf16: e4m3 numbers are fp16 numbers, and so are the channels of a bf16 query, down to
+// 2^-31 of its largest, which a power of two per row brings to [2^14, 2^15); and P keeps 11 bits.
+// Scales of key blocks go into the exponent's factor, those of value blocks into its offset, as in
+// the kernel for few rows: p' = 2^(s - m + 7) v_scale with m at most 8 below the running maximum of
+// s + log2 v_scale.  That slack is what spares most tiles the rescaling of O: it is done where the
+// maximum has grown by more, and P stays below 2^15 (a slack of 4 took 850 us where this one takes
+// 836).  What is 2^-21 of the heaviest or more keeps all its bits.
 //
 // Measured: 4,096 new tokens behind 12,288, 32 heads over 8, d = 128: 836 us, 1.15 PFLOP/s, 60 % of
 // the measured bf16 rate.  The tensor pipe is busy for 46 % of the cycles and so are the issue
